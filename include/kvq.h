@@ -118,6 +118,9 @@ typedef enum {
 #define KVQ_FLAG_NONFINITE    0x8u /* group held inf/NaN, stored as zeros      */
 #define KVQ_FLAG_OOB          0x10u /* debug builds: an access outside its array
                                        was skipped (see kvq_debug_checks)      */
+#define KVQ_FLAG_POOL_EMPTY   0x20u /* too few free pages: nothing was reserved */
+#define KVQ_FLAG_PAGE_LIST    0x40u /* a copy list names a page twice as target,
+                                       or one page as source and target       */
 
 typedef enum { KVQ_DENSE = 0, KVQ_PAGED = 1 } kvq_layout;
 
@@ -326,6 +329,235 @@ KVQ_API kvq_status kvq_append_decode_attn(const kvq_cache_desc* desc, const kvq_
                                   float softmax_scale, uint16_t* out,
                                   void* workspace, size_t workspace_bytes,
                                   uint32_t* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Prompts: several new tokens per sequence.  The calls below take a padded
+ * batch: num_new token rows per sequence, of which sequence b uses the first
+ * new_lens[b] (device int32 [batch]; NULL = all num_new).  The rows behind
+ * are neither read nor written.  A new_lens[b] outside [0, num_new] or a
+ * negative length flags KVQ_FLAG_SEQ_LEN and the sequence is skipped.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Rotary positions.  Channels [0, rotary_dim) of a head form rotary_dim / 2
+ * pairs, (2i, 2i+1) when interleaved, else (i, i + rotary_dim/2); pair i of
+ * the token at position p turns by p * w_i radians and is scaled by the
+ * amplitude:  y0 = a (x0 cos - x1 sin),  y1 = a (x1 cos + x0 sin).
+ * The other channels pass unchanged.  w_i = base^(-2i / rotary_dim), changed
+ * for contexts beyond the trained one by
+ *   LINEAR  w_i / factor (position interpolation);
+ *   NTK     base * factor^(rotary_dim / (rotary_dim - 2)) in place of base;
+ *   BANDS   by turns in the original context, n = original_context w_i / 2pi:
+ *           w_i where n >= high_turns, w_i / factor where n <= low_turns, and
+ *           between them the mix with weight (n - low) / (high - low) on w_i;
+ *   YARN    by pair index: w_i below lo = max(floor(at(high_turns)), 0),
+ *           w_i / factor above hi = min(ceil(at(low_turns)), rotary_dim - 1),
+ *           a linear ramp between, at(n) = rotary_dim ln(original_context /
+ *           (2 pi n)) / (2 ln base); the amplitude is 0.1 ln(factor) + 1.
+ * (LINEAR, NTK, YARN: the published methods of those names.)
+ */
+typedef enum {
+  KVQ_ROPE_NONE = 0,
+  KVQ_ROPE_LINEAR = 1,
+  KVQ_ROPE_NTK = 2,
+  KVQ_ROPE_BANDS = 3,
+  KVQ_ROPE_YARN = 4
+} kvq_rope_scaling;
+
+#define KVQ_ROPE_MAX_PAIRS 128
+
+typedef struct {
+  int32_t rotary_dim;       /* even, 2 .. 256                                  */
+  int32_t interleaved;      /* 1: pairs (2i, 2i+1); 0: (i, i + rotary_dim/2)   */
+  int32_t scaling;          /* kvq_rope_scaling                                */
+  int32_t original_context; /* BANDS, YARN: positions the model was trained on */
+  double base;              /* > 1                                             */
+  double factor;            /* >= 1; 1 when scaling is NONE                    */
+  double low_turns;         /* BANDS: default 1; YARN: default 1  (0 = default)*/
+  double high_turns;        /* BANDS: default 4; YARN: default 32 (0 = default)*/
+  double amplitude;         /* 0 = as above (1, or YARN's); in (0, 4)          */
+} kvq_rope_desc;
+
+/* A filled rotation (host memory, passed by value to the kernels): turns[i]
+ * is w_i / 2pi rounded to units of 2^-64 turns, so that position * turns[i]
+ * modulo 2^64 is the angle without any further rounding, at any position. */
+typedef struct {
+  int32_t rotary_dim;
+  int32_t interleaved;
+  uint64_t amplitude;       /* units of 2^-61                                  */
+  uint64_t turns[KVQ_ROPE_MAX_PAIRS];
+} kvq_rope;
+
+/* Fills *rope from *desc.  Host arithmetic only. */
+KVQ_API kvq_status kvq_rope_init(const kvq_rope_desc* desc, kvq_rope* rope);
+
+/*
+ * Rotates q and / or k.
+ *   q, q_out   device fp16 [batch][num_new][num_q_heads][head_dim]
+ *   k, k_out   device fp16 [batch][num_new][num_k_heads][head_dim]
+ *              (num_q_heads or num_k_heads 0: that tensor is not touched)
+ *   positions        device int32 [batch][num_new], any value; or NULL:
+ *   seq_lens_before  device int32 [batch]: token t of sequence b is at
+ *                    position seq_lens_before[b] + t.
+ * head_dim is a multiple of 8, rotary_dim <= head_dim <= 256.  x_out is x
+ * itself (in place) or does not overlap it.  The angle is that of turns[]
+ * exactly; cos, sin and the products carry 2^-44, and y is rounded once, so
+ * it is the nearest fp16 to the formula's value unless that lies within
+ * 2^-44 (|x0| + |x1|) of a tie.  An infinity or NaN in x gives one in y.
+ */
+KVQ_API kvq_status kvq_rope_apply(const kvq_rope* rope, int32_t head_dim, int32_t batch,
+                          int32_t num_new, int32_t num_q_heads, const uint16_t* q,
+                          uint16_t* q_out, int32_t num_k_heads, const uint16_t* k,
+                          uint16_t* k_out, const int32_t* positions,
+                          const int32_t* seq_lens_before, const int32_t* new_lens,
+                          uint32_t* dev_status, void* stream);
+
+/*
+ * kvq_append of rotated keys, and the rotation of q, in one launch: the cache
+ * and q_out are bit for bit those of kvq_rope_apply on q and k_new followed
+ * by kvq_append of the result and v_new (num_q_heads 0: no q).  Unlike
+ * kvq_append it takes new_lens.  Axis-aware caches: KVQ_ERR_UNSUPPORTED (call
+ * kvq_rope_apply, then kvq_append).
+ */
+KVQ_API kvq_status kvq_rope_append(const kvq_cache_desc* desc, const kvq_cache* cache,
+                           const kvq_rope* rope, int32_t batch, int32_t num_new,
+                           const uint16_t* k_new, const uint16_t* v_new,
+                           int32_t num_q_heads, const uint16_t* q, uint16_t* q_out,
+                           const int32_t* seq_lens_before, const int32_t* new_lens,
+                           uint32_t* dev_status, void* stream);
+
+/*
+ * Reads cached rows back: row t of sequence b is position start[b] + t, for
+ * the t < num_rows with start[b] + t < seq_lens[b]; rows behind are left as
+ * they were.
+ *   seq_lens      device int32 [batch]: tokens cached
+ *   start         device int32 [batch]
+ *   k_out, v_out  device fp16 [batch][num_rows][num_kv_heads][head_dim]
+ *                 (either may be NULL)
+ * The value is x_hat = (q - z) s (fp32), rounded to fp16 and held at the
+ * largest finite fp16; fp16 rows are copied.  A negative start, a length
+ * outside the cache or an unmapped page is flagged and its rows are left.
+ */
+KVQ_API kvq_status kvq_cache_read(const kvq_cache_desc* desc, const kvq_cache* cache,
+                          int32_t batch, int32_t num_rows, const int32_t* seq_lens,
+                          const int32_t* start, uint16_t* k_out, uint16_t* v_out,
+                          uint32_t* dev_status, void* stream);
+
+/* Splits and workspace of kvq_extend_attn; the conventions of
+ * kvq_decode_num_splits and kvq_decode_workspace_size. */
+KVQ_API int32_t kvq_extend_num_splits(const kvq_cache_desc* desc, int32_t batch, int32_t num_new,
+                              int32_t num_q_heads, int32_t max_seq_len, int32_t num_splits);
+KVQ_API size_t kvq_extend_workspace_size(const kvq_cache_desc* desc, int32_t batch,
+                                 int32_t num_new, int32_t num_q_heads, int32_t max_seq_len,
+                                 int32_t num_splits);
+
+/*
+ * Causal attention of several new tokens per sequence over the cache, their
+ * own rows included (kvq_append or kvq_rope_append has written them): a
+ * prompt, a chunk of one, the suffix behind shared pages, drafted tokens.
+ *   q                device fp16 [batch][num_new][num_q_heads][head_dim]
+ *   seq_lens_before  device int32 [batch]: tokens cached before the new ones;
+ *                    token t attends to positions [0, seq_lens_before[b] + t].
+ *   max_seq_len      host upper bound on seq_lens_before[b] + new_lens[b]
+ *   out              device fp16 like q; may not overlap it
+ * num_splits, softmax_scale and workspace as for kvq_decode_attn, but any
+ * number of query heads per KV head.  Scores and softmax in fp32; K and V
+ * enter the products as the fp16 values that kvq_cache_read returns, the
+ * probabilities as fp16 (relative to their row's maximum).  A sequence whose
+ * length exceeds min(max_seq_len, cache capacity) flags KVQ_FLAG_SEQ_LEN and
+ * yields zero rows; a token whose page is unmapped flags KVQ_FLAG_BLOCK_TABLE
+ * and is left out; a row with nothing to attend to is zero.
+ */
+KVQ_API kvq_status kvq_extend_attn(const kvq_cache_desc* desc, const kvq_cache* cache,
+                           int32_t batch, int32_t num_new, int32_t num_q_heads,
+                           const uint16_t* q, const int32_t* seq_lens_before,
+                           const int32_t* new_lens, int32_t max_seq_len, int32_t num_splits,
+                           float softmax_scale, uint16_t* out, void* workspace,
+                           size_t workspace_bytes, uint32_t* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Page pool: which pages the sequences of a paged cache hold.  One pool
+ * serves every layer (the layers' caches share the block table).  Its state
+ * is the block table and a reference count per page; a page with count 0 is
+ * free, and pages are always taken lowest first, so the same calls give the
+ * same tables.  All of it runs on the device, in stream order.
+ * For an axis-aware cache the pool's positions are those after the sinks, and
+ * the fp16 windows, which are per sequence, are the caller's to copy.
+ * ------------------------------------------------------------------------ */
+
+/* Largest batch of a pool (kvq_pages_reserve holds the batch on chip). */
+#define KVQ_MAX_POOL_BATCH 16384
+
+typedef struct {
+  int32_t num_pages;
+  int32_t page_size;          /* tokens per page                               */
+  int32_t batch;              /* rows of the block table                       */
+  int32_t max_blocks_per_seq;
+  int32_t* ref_count;         /* device [num_pages]: block-table entries on it */
+  int32_t* block_table;       /* device [batch][max_blocks_per_seq]; -1: none  */
+} kvq_page_pool;
+
+/* Device scratch of kvq_pages_reserve and kvq_pages_compact. */
+KVQ_API size_t kvq_pages_workspace_size(const kvq_page_pool* pool);
+
+/*
+ * Fork, trim, permute and free: every row of the table becomes the first
+ * ceil(keep_lens[b] / page_size) entries of the row parent[b] had before the
+ * call, -1 behind; reference counts follow, so pages nobody holds any more
+ * are free.  parent[b] = b keeps a sequence, -1 frees it, a parent named by
+ * several rows is forked (its pages are shared, no data moves).
+ *   parent     device int32 [batch], -1 .. batch-1 (others flag
+ *              KVQ_FLAG_BLOCK_TABLE and count as -1)
+ *   keep_lens  device int32 [batch], or NULL for whole rows; outside
+ *              [0, page_size * max_blocks_per_seq]: KVQ_FLAG_SEQ_LEN, as -1
+ */
+KVQ_API kvq_status kvq_pages_reorder(const kvq_page_pool* pool, const int32_t* parent,
+                             const int32_t* keep_lens, uint32_t* dev_status, void* stream);
+
+/*
+ * Makes positions [seq_lens_before[b], seq_lens_before[b] + new_lens[b])
+ * writable for every sequence: blocks without a page get one, and a page
+ * shared with another sequence is replaced by a fresh one (where all holders
+ * of a shared page ask for it, the last of them keeps it).  A replaced page
+ * that holds tokens before seq_lens_before[b] has to be copied:
+ *   copy_src, copy_dst  device int32 [batch]: the pair of sequence b, or -1;
+ *                       pass them to kvq_pages_copy for every layer, before
+ *                       the new tokens are appended
+ *   granted             device int32 [batch] or NULL: new_lens[b] (num_new
+ *                       when new_lens is NULL); 0 for a skipped sequence
+ * With too few free pages nothing changes for any sequence: KVQ_FLAG_POOL_EMPTY,
+ * no copies, granted 0 throughout (pass granted as new_lens to the calls that
+ * write and nothing is written).
+ */
+KVQ_API kvq_status kvq_pages_reserve(const kvq_page_pool* pool, const int32_t* seq_lens_before,
+                             const int32_t* new_lens, int32_t num_new, int32_t* copy_src,
+                             int32_t* copy_dst, int32_t* granted, void* workspace,
+                             size_t workspace_bytes, uint32_t* dev_status, void* stream);
+
+/*
+ * Compacts the pool: with n pages in use, the k-th page at or behind n moves
+ * to the k-th free page before n; table and counts follow.
+ *   move_src, move_dst  device int32 [num_pages / 2]: the moves, -1 behind;
+ *                       pass them to kvq_pages_copy for every layer
+ *   num_live            device int32 [1]: n
+ * An entry of the table that names a page of count 0 becomes -1
+ * (KVQ_FLAG_BLOCK_TABLE).
+ */
+KVQ_API kvq_status kvq_pages_compact(const kvq_page_pool* pool, int32_t* move_src,
+                             int32_t* move_dst, int32_t* num_live, void* workspace,
+                             size_t workspace_bytes, uint32_t* dev_status, void* stream);
+
+/*
+ * Copies pages in num_layers caches of one descriptor (caches: host array):
+ * page copy_dst[i] takes the bytes of page copy_src[i], i < num_pairs (device
+ * arrays; pairs with a -1 are skipped).  No page may be the target of two
+ * pairs, or source and target; then KVQ_FLAG_PAGE_LIST is set and the
+ * contents of the targets concerned are unspecified.  An index outside the
+ * pool flags KVQ_FLAG_BLOCK_TABLE and its pair is skipped.
+ */
+KVQ_API kvq_status kvq_pages_copy(const kvq_cache_desc* desc, const kvq_cache* caches,
+                          int32_t num_layers, const int32_t* copy_src, const int32_t* copy_dst,
+                          int32_t num_pairs, uint32_t* dev_status, void* stream);
 
 /* Size of the library's own split scratch used by kvq_decode_attn_static_ws. */
 #define KVQ_STATIC_WORKSPACE_BYTES ((size_t)8 << 20)

@@ -8,7 +8,8 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, Structure, byref, c_float, c_int32, c_int64, c_size_t, c_uint32, c_void_p
+from ctypes import (POINTER, Structure, byref, c_double, c_float, c_int32, c_int64, c_size_t, c_uint32,  # noqa: F401
+                    c_uint64, c_void_p)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libkvq.so")
@@ -26,6 +27,13 @@ KVQ_FLAG_BLOCK_TABLE = 0x2
 KVQ_FLAG_ZERO_CLAMPED = 0x4
 KVQ_FLAG_NONFINITE = 0x8
 KVQ_FLAG_OOB = 0x10  # debug builds only: an access outside its array was skipped
+KVQ_FLAG_POOL_EMPTY = 0x20
+KVQ_FLAG_PAGE_LIST = 0x40
+
+# kvq_rope_scaling
+ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "bands": 3, "yarn": 4}
+KVQ_ROPE_MAX_PAIRS = 128
+KVQ_MAX_POOL_BATCH = 16384
 
 # kvq_array: the caller arrays a debug build checks
 (KVQ_ARRAY_K_CODES, KVQ_ARRAY_V_CODES, KVQ_ARRAY_K_SCALE, KVQ_ARRAY_K_ZERO, KVQ_ARRAY_V_SCALE,
@@ -68,6 +76,40 @@ class kvq_cache(Structure):
     ]
 
 
+class kvq_rope_desc(Structure):
+    _fields_ = [
+        ("rotary_dim", c_int32),
+        ("interleaved", c_int32),
+        ("scaling", c_int32),
+        ("original_context", c_int32),
+        ("base", c_double),
+        ("factor", c_double),
+        ("low_turns", c_double),
+        ("high_turns", c_double),
+        ("amplitude", c_double),
+    ]
+
+
+class kvq_rope(Structure):
+    _fields_ = [
+        ("rotary_dim", c_int32),
+        ("interleaved", c_int32),
+        ("amplitude", c_uint64),
+        ("turns", c_uint64 * KVQ_ROPE_MAX_PAIRS),
+    ]
+
+
+class kvq_page_pool(Structure):
+    _fields_ = [
+        ("num_pages", c_int32),
+        ("page_size", c_int32),
+        ("batch", c_int32),
+        ("max_blocks_per_seq", c_int32),
+        ("ref_count", c_void_p),
+        ("block_table", c_void_p),
+    ]
+
+
 class KVQError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -98,6 +140,31 @@ SIGNATURES = {
     "kvq_decode_attn_static_ws": (c_int32, [POINTER(kvq_cache_desc), POINTER(kvq_cache), c_int32,
                                             c_int32, c_void_p, c_void_p, c_int32, c_int32,
                                             c_float, c_void_p, c_void_p, c_void_p]),
+    "kvq_rope_init": (c_int32, [POINTER(kvq_rope_desc), POINTER(kvq_rope)]),
+    "kvq_rope_apply": (c_int32, [POINTER(kvq_rope), c_int32, c_int32, c_int32, c_int32, c_void_p,
+                                 c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_void_p,
+                                 c_void_p, c_void_p, c_void_p]),
+    "kvq_rope_append": (c_int32, [POINTER(kvq_cache_desc), POINTER(kvq_cache), POINTER(kvq_rope),
+                                  c_int32, c_int32, c_void_p, c_void_p, c_int32, c_void_p,
+                                  c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+    "kvq_cache_read": (c_int32, [POINTER(kvq_cache_desc), POINTER(kvq_cache), c_int32, c_int32,
+                                 c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+    "kvq_extend_num_splits": (c_int32, [POINTER(kvq_cache_desc), c_int32, c_int32, c_int32,
+                                        c_int32, c_int32]),
+    "kvq_extend_workspace_size": (c_size_t, [POINTER(kvq_cache_desc), c_int32, c_int32, c_int32,
+                                             c_int32, c_int32]),
+    "kvq_extend_attn": (c_int32, [POINTER(kvq_cache_desc), POINTER(kvq_cache), c_int32, c_int32,
+                                  c_int32, c_void_p, c_void_p, c_void_p, c_int32, c_int32,
+                                  c_float, c_void_p, c_void_p, c_size_t, c_void_p, c_void_p]),
+    "kvq_pages_workspace_size": (c_size_t, [POINTER(kvq_page_pool)]),
+    "kvq_pages_reorder": (c_int32, [POINTER(kvq_page_pool), c_void_p, c_void_p, c_void_p,
+                                    c_void_p]),
+    "kvq_pages_reserve": (c_int32, [POINTER(kvq_page_pool), c_void_p, c_void_p, c_int32, c_void_p,
+                                    c_void_p, c_void_p, c_void_p, c_size_t, c_void_p, c_void_p]),
+    "kvq_pages_compact": (c_int32, [POINTER(kvq_page_pool), c_void_p, c_void_p, c_void_p,
+                                    c_void_p, c_size_t, c_void_p, c_void_p]),
+    "kvq_pages_copy": (c_int32, [POINTER(kvq_cache_desc), POINTER(kvq_cache), c_int32, c_void_p,
+                                 c_void_p, c_int32, c_void_p, c_void_p]),
     "kvq_debug_checks": (c_int32, []),
     "kvq_debug_shrink_extent": (c_int32, [c_int32, c_int64]),
     "kvq_status_string": (ctypes.c_char_p, [c_int32]),

@@ -10,7 +10,7 @@
 #include <algorithm>
 #include <mutex>
 
-#include "kvq_internal.cuh"
+#include "kvq_host.cuh"
 
 namespace kvq {
 
@@ -39,14 +39,6 @@ unsigned long long current_context_id() {
   if (get_id(c, &id) != CUDA_SUCCESS) return 0;
   return id + 1;  // 0 stays "unknown"
 }
-
-namespace {
-
-constexpr size_t kAlign = 16;
-
-bool aligned(const void* p) { return ((uintptr_t)p % kAlign) == 0; }
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Validates a cache descriptor; fills `g` on success.
 kvq_status check_desc(const kvq_cache_desc* d, CacheGeom* g) {
@@ -194,11 +186,6 @@ int32_t choose_splits(int64_t units, int64_t max_len, int32_t requested, int cta
 // at the quantiles of a normal distribution).  Each quantile solves
 // Phi(x) = p, Phi(x) = erfc(-x / sqrt 2) / 2, by bisection to double
 // precision.  Computed once.
-struct Nf4Table {
-  float level[16];
-  float mid[16];
-  bool symmetric;  // level[15 - i] == -level[i]: the tensor-core kernel's sign-magnitude lookup
-};
 
 const Nf4Table& nf4_table() {
   static const Nf4Table t = [] {
@@ -341,8 +328,6 @@ void dbg_fill(CacheGeom& g, const kvq_cache_desc* desc, const kvq_cache* cache, 
   (void)k_new, (void)v_new, (void)lens, (void)out, (void)ws, (void)ws_bytes, (void)status;
 #endif
 }
-
-}  // namespace
 
 size_t workspace_bytes(int64_t batch, int64_t Hq, int64_t D, int64_t splits) {
   if (splits <= 1) return 0;

@@ -1,0 +1,301 @@
+// Causal attention of several new tokens per sequence over the cache
+// (kvq_extend_attn), and the merge of its split partials.
+//
+// Rows.  The G query heads of a KV head and the new tokens share K and V, so
+// a tile's rows are (token, head) pairs, row r = token r / G, head r % G;
+// row r attends to positions up to seq_lens_before + r / G.
+//
+// One pass over the keys with a running maximum and sum per row, in log2
+// units: m' = max(m, max_j s_j), l' = 2^(m - m') l + sum_j 2^(s_j - m'),
+// o' = 2^(m - m') o + sum_j 2^(s_j - m') v_j; splits over the context write
+// (m, l, o) and a merge joins them.
+#include "kvq_decode_fast.cuh"
+#include "kvq_load.cuh"
+#include "kvq_rope.cuh"
+
+namespace kvq {
+namespace {
+
+using fast::ex2;
+using fast::ldsm_x4;
+using fast::ldsm_x4_t;
+using fast::mma16816;
+using fast::smem_u32;
+
+constexpr int kRows = 64;  // 4 warps of 16 rows
+constexpr int kThreads = 128;
+
+// Keys per tile: K and V rows as fp16 in shared memory
+__host__ __device__ constexpr int tile_keys(int D) { return D == 256 ? 32 : 64; }
+__host__ __device__ constexpr size_t extend_smem(int D) {
+  return (size_t)(kRows + 2 * tile_keys(D)) * D * 2 + tile_keys(D) * sizeof(int);
+}
+
+// Byte offset of 16-byte chunk c of row r in a [rows][D] fp16 tile; the
+// chunk index is XORed with the row so that ldmatrix's 8 rows fall into
+// different banks.
+template <int D>
+__device__ __forceinline__ uint32_t at(int r, int c) {
+  return (uint32_t)(r * (2 * D) + ((c ^ (r & 7)) << 4));
+}
+
+// One sequence's share of the call: its rows and lengths.
+struct Span {
+  int before, n, L;
+};
+__device__ __forceinline__ Span span_of(const ExtendParams& p, int b, bool report) {
+  Span s;
+  s.before = checked_len(p.v.geom, p.lens_before, b, -1);
+  s.n = new_rows_of(p.new_lens, b, p.num_new);
+  const long long L = (long long)s.before + s.n;
+  const bool bad = s.before < 0 || s.n < 0 || L > p.len_limit;
+  if (bad && report && p.status) atomicOr(p.status, KVQ_FLAG_SEQ_LEN);
+  s.L = bad ? 0 : (int)L;  // no keys: the rows come out zero
+  s.n = max(s.n, 0);
+  return s;
+}
+
+template <int BITS, int D>
+__global__ void __launch_bounds__(kThreads) extend_kernel(const __grid_constant__ ExtendParams p) {
+  constexpr int KEYS = tile_keys(D), CH = D / 8, KB = D / 16, NT = KEYS / 8;
+  pdl_launch_dependents();
+  pdl_wait();
+  extern __shared__ __align__(128) uint8_t smem[];
+  const CacheGeom& c = p.v.geom;
+  const int kvh = blockIdx.y, b = blockIdx.z;
+  const int split = blockIdx.x % p.splits, tile = blockIdx.x / p.splits;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const Span sp = span_of(p, b, threadIdx.x == 0 && blockIdx.x == 0 && kvh == 0);
+  const long long r0 = (long long)tile * kRows;
+  const long long live_rows = (long long)sp.n * p.G;
+  if (r0 >= live_rows) return;
+
+  const uint32_t q_s = smem_u32(smem), k_s = q_s + kRows * D * 2, v_s = k_s + KEYS * D * 2;
+  int* ok_s = reinterpret_cast<int*>(smem + (kRows + 2 * KEYS) * D * 2);
+
+  // q rows of the tile (zero behind the last)
+  for (int i = threadIdx.x; i < kRows * CH; i += kThreads) {
+    const int r = i / CH, ch = i % CH;
+    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+    if (r0 + r < live_rows) {
+      const int t = (int)((r0 + r) / p.G), h = (int)((r0 + r) % p.G);
+      const uint4* src = reinterpret_cast<const uint4*>(
+          p.q + (((long long)b * p.num_new + t) * p.Hq + (long long)kvh * p.G + h) * D) + ch;
+      if (KVQ_IN(c, KVQ_ARRAY_Q, src, 16)) x = *src;
+    }
+    *reinterpret_cast<uint4*>(smem + at<D>(r, ch)) = x;
+  }
+
+  // the tile's last row sees positions below `end`
+  const int t_last = (int)((min(r0 + kRows, live_rows) - 1) / p.G);
+  const int end = sp.L ? min(sp.L, sp.before + t_last + 1) : 0;
+  const int k0 = split * p.chunk, k1 = min(end, k0 + p.chunk);
+
+  float o[D / 8][4];
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  // this lane's two rows: last position seen
+  int last[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const long long r = r0 + warp * 16 + (lane >> 2) + 8 * e;
+    last[e] = r < live_rows ? sp.before + (int)(r / p.G) : -1;
+  }
+
+  for (int ks = k0; ks < k1; ks += KEYS) {
+    __syncthreads();  // the tile before is used up (and q is in place)
+    for (int i = threadIdx.x; i < KEYS * CH; i += kThreads) {
+      const int j = i / CH, ch = i % CH, pos = ks + j;
+      uint4 kx = make_uint4(0u, 0u, 0u, 0u), vx = kx;
+      bool ok = pos < k1;
+      if (ok) {
+        const long long row = view_row(c, b, kvh, sp.L, pos);
+        if (row < 0) {
+          ok = false;
+          if (ch == 0 && p.status) atomicOr(p.status, KVQ_FLAG_BLOCK_TABLE);
+        } else {
+          kx = load8<BITS>(p.v, 0, b, kvh, sp.L, pos, row, ch);
+          vx = load8<BITS>(p.v, 1, b, kvh, sp.L, pos, row, ch);
+        }
+      }
+      *reinterpret_cast<uint4*>(smem + kRows * D * 2 + at<D>(j, ch)) = kx;
+      *reinterpret_cast<uint4*>(smem + (kRows + KEYS) * D * 2 + at<D>(j, ch)) = vx;
+      if (ch == 0) ok_s[j] = ok;
+    }
+    __syncthreads();
+
+    float s[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      uint32_t a[4];
+      ldsm_x4(q_s + at<D>(warp * 16 + (lane & 15), kb * 2 + (lane >> 4)), a[0], a[1], a[2], a[3]);
+#pragma unroll
+      for (int n = 0; n < NT; n += 2) {
+        uint32_t b0, b1, b2, b3;  // keys n*8 .. n*8+15, channels 16 kb .. +15
+        ldsm_x4(k_s + at<D>(n * 8 + (lane & 7) + ((lane >> 4) << 3), kb * 2 + ((lane >> 3) & 1)), b0, b1, b2, b3);
+        mma16816(s[n], a[0], a[1], a[2], a[3], b0, b1);
+        mma16816(s[n + 1], a[0], a[1], a[2], a[3], b2, b3);
+      }
+    }
+
+    float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = n * 8 + (lane & 3) * 2 + (e & 1);
+        const bool see = ok_s[j] && ks + j <= last[e >> 1];
+        s[n][e] = see ? s[n][e] * p.scale_log2 : -INFINITY;
+        mx[e >> 1] = fmaxf(mx[e >> 1], s[n][e]);
+      }
+    }
+    float alpha[2], base[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
+      mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
+      const float mn = fmaxf(m[e], mx[e]);
+      base[e] = mn == -INFINITY ? 0.f : mn;  // nothing seen yet: every weight is 2^-inf = 0
+      alpha[e] = ex2(m[e] - base[e]);
+      m[e] = mn;
+      l[e] *= alpha[e];
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[n][e] = ex2(s[n][e] - base[e >> 1]);
+        l[e >> 1] += s[n][e];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+      o[i][0] *= alpha[0];
+      o[i][1] *= alpha[0];
+      o[i][2] *= alpha[1];
+      o[i][3] *= alpha[1];
+    }
+#pragma unroll
+    for (int kb = 0; kb < KEYS / 16; ++kb) {
+      const uint32_t a0 = fast::pack_h2(s[2 * kb][0], s[2 * kb][1]);
+      const uint32_t a1 = fast::pack_h2(s[2 * kb][2], s[2 * kb][3]);
+      const uint32_t a2 = fast::pack_h2(s[2 * kb + 1][0], s[2 * kb + 1][1]);
+      const uint32_t a3 = fast::pack_h2(s[2 * kb + 1][2], s[2 * kb + 1][3]);
+#pragma unroll
+      for (int n = 0; n < D / 8; n += 2) {
+        uint32_t b0, b1, b2, b3;  // keys 16 kb .. +15, channels n*8 .. +15
+        ldsm_x4_t(v_s + at<D>(kb * 16 + (lane & 15), n + (lane >> 4)), b0, b1, b2, b3);
+        mma16816(o[n], a0, a1, a2, a3, b0, b1);
+        mma16816(o[n + 1], a0, a1, a2, a3, b2, b3);
+      }
+    }
+  }
+
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+    l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+    const long long r = r0 + warp * 16 + (lane >> 2) + 8 * e;
+    if (r >= live_rows) continue;
+    const int t = (int)(r / p.G), h = (int)(r % p.G);
+    const long long orow = ((long long)b * p.num_new + t) * p.Hq + (long long)kvh * p.G + h;
+    if (p.splits == 1) {
+      const float inv = l[e] > 0.f ? 1.f / l[e] : 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        __half2* d = reinterpret_cast<__half2*>(p.out + orow * D + i * 8 + (lane & 3) * 2);
+        if (KVQ_IN(c, KVQ_ARRAY_OUT, d, 4)) *d = __floats2half2_rn(o[i][2 * e] * inv, o[i][2 * e + 1] * inv);
+      }
+    } else {
+      const long long w = orow * p.splits + split;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        float2* d = reinterpret_cast<float2*>(p.ws_o + w * D + i * 8 + (lane & 3) * 2);
+        if (KVQ_IN(c, KVQ_ARRAY_WORKSPACE, d, 8)) *d = make_float2(o[i][2 * e], o[i][2 * e + 1]);
+      }
+      float2* ml = reinterpret_cast<float2*>(p.ws_ml) + w;
+      if ((lane & 3) == 0 && KVQ_IN(c, KVQ_ARRAY_WORKSPACE, ml, 8)) *ml = make_float2(m[e], l[e]);
+    }
+  }
+}
+
+// out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s of each live row; one
+// CTA of D threads per (sequence, new token, head).
+__global__ void __launch_bounds__(256) extend_merge_kernel(const __grid_constant__ ExtendParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const CacheGeom& c = p.v.geom;
+  const long long row = blockIdx.x;
+  const int b = (int)(row / p.Hq / p.num_new);
+  const int t = (int)(row / p.Hq - (long long)b * p.num_new);
+  if (t >= new_rows_of(p.new_lens, b, p.num_new)) return;
+  const int D = c.D, d = threadIdx.x;
+  const float2* ml = reinterpret_cast<const float2*>(p.ws_ml) + row * p.splits;
+  const float* o = p.ws_o + row * p.splits * D + d;
+  float M = -INFINITY, num = 0.f, den = 0.f;
+  for (int s = 0; s < p.splits; ++s) {
+    if (!KVQ_IN(c, KVQ_ARRAY_WORKSPACE, ml + s, 8) || !KVQ_IN(c, KVQ_ARRAY_WORKSPACE, o + (long long)s * D, 4))
+      continue;
+    const float2 v = ml[s];
+    if (v.x == -INFINITY) continue;  // nothing seen: o is zero, m no reference
+    const float Mn = fmaxf(M, v.x), a = ex2(M - Mn), f = ex2(v.x - Mn);
+    num = num * a + f * o[(long long)s * D];
+    den = den * a + f * v.y;
+    M = Mn;
+  }
+  if (KVQ_IN(c, KVQ_ARRAY_OUT, p.out + row * D + d, 2))
+    p.out[row * D + d] = __float2half_rn(den > 0.f ? num / den : 0.f);
+}
+
+template <int BITS, int D>
+cudaError_t run(const ExtendParams* p, ExtendPlan* plan, cudaStream_t stream) {
+  static KernelSetup setup;
+  int occ = 0;
+  cudaError_t e = setup_kernel(extend_kernel<BITS, D>, setup, kThreads, extend_smem(D), &occ);
+  if (e != cudaSuccess) return e;
+  if (plan) {
+    plan->tile_rows = kRows;
+    plan->occ = occ;
+    return cudaSuccess;
+  }
+  const long long tiles = ((long long)p->num_new * p->G + kRows - 1) / kRows;
+  const dim3 grid((unsigned)(tiles * p->splits), p->v.geom.Hkv, p->batch);
+  return launch_pdl(extend_kernel<BITS, D>, grid, dim3(kThreads), extend_smem(D), stream, *p);
+}
+
+template <int BITS>
+cudaError_t run_d(int D, const ExtendParams* p, ExtendPlan* plan, cudaStream_t stream) {
+  if (D == 64) return run<BITS, 64>(p, plan, stream);
+  if (D == 128) return run<BITS, 128>(p, plan, stream);
+  return run<BITS, 256>(p, plan, stream);
+}
+
+cudaError_t run_any(const CacheGeom& c, const ExtendParams* p, ExtendPlan* plan, cudaStream_t stream) {
+  switch (c.bits) {
+    case 2: return run_d<2>(c.D, p, plan, stream);
+    case 4: return run_d<4>(c.D, p, plan, stream);
+    case 8: return run_d<8>(c.D, p, plan, stream);
+    default: return run_d<16>(c.D, p, plan, stream);
+  }
+}
+
+}  // namespace
+
+cudaError_t extend_plan(const CacheGeom& c, int num_new, int G, int max_len, ExtendPlan* plan) {
+  (void)num_new, (void)G, (void)max_len;
+  return run_any(c, nullptr, plan, nullptr);
+}
+
+cudaError_t launch_extend(const ExtendParams& p, const ExtendPlan&, cudaStream_t stream) {
+  cudaError_t e = run_any(p.v.geom, &p, nullptr, stream);
+  if (e == cudaSuccess && p.splits > 1) {
+    const long long rows = (long long)p.batch * p.num_new * p.Hq;
+    e = launch_pdl(extend_merge_kernel, dim3((unsigned)rows), dim3(p.v.geom.D), 0, stream, p);
+  }
+  return e;
+}
+
+}  // namespace kvq

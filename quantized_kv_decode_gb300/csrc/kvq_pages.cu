@@ -1,0 +1,374 @@
+// Page pool kernels: reorder (fork, trim, permute, free), reserve, compact,
+// and the copy of pages in the layers' caches.
+//
+// Reference counts change by integer atomics only, whose sums do not depend
+// on the order, and pages are handed out by prefix sums over the page index,
+// so every result is determined by the inputs.
+#include "kvq_pages.cuh"
+
+namespace kvq {
+namespace {
+
+constexpr int kOne = 1024;  // threads of the single-CTA kernels
+
+__device__ __forceinline__ void flag(uint32_t* status, uint32_t f) {
+  if (f && status) atomicOr(status, f);
+}
+
+// Exclusive prefix sum of x over the CTA's threads (kOne of them), and the
+// total.  `scratch`: 33 ints of shared memory, free again on return.
+__device__ __forceinline__ int block_scan(int x, int* scratch, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int inc = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  if (lane == 31) scratch[warp] = inc;
+  __syncthreads();
+  if (warp == 0) {
+    const int w = lane < kOne / 32 ? scratch[lane] : 0;
+    int s = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += y;
+    }
+    scratch[lane] = s - w;
+    if (lane == 31) scratch[32] = s;
+  }
+  __syncthreads();
+  const int r = scratch[warp] + inc - x;
+  *total = scratch[32];
+  __syncthreads();
+  return r;
+}
+
+// ---- reorder ----------------------------------------------------------
+
+// One CTA per group of `cols` table columns: the columns of every row are
+// read to shared memory, then written through parent[], so the table changes
+// in place.  Counts: -1 for every old entry, +1 for every new one.
+__global__ void __launch_bounds__(256) reorder_kernel(const __grid_constant__ PoolParams p, int cols) {
+  pdl_launch_dependents();
+  pdl_wait();
+  extern __shared__ int32_t old[];  // [batch][cols]
+  const kvq_page_pool& pl = p.pool;
+  const int M = pl.max_blocks_per_seq;
+  const int c0 = blockIdx.x * cols;
+  uint32_t flags = 0;
+  for (int i = threadIdx.x; i < pl.batch * cols; i += blockDim.x) {
+    const int b = i / cols, c = c0 + i % cols;
+    int e = -1;
+    if (c < M) {
+      e = pl.block_table[(long long)b * M + c];
+      if (e >= pl.num_pages) flags |= KVQ_FLAG_BLOCK_TABLE;
+      if (e < 0 || e >= pl.num_pages) e = -1;
+    }
+    old[i] = e;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < pl.batch * cols; i += blockDim.x) {
+    const int b = i / cols, k = i % cols, c = c0 + k;
+    if (c >= M) continue;
+    int par = __ldg(p.parent + b);
+    if (par < -1 || par >= pl.batch) {
+      flags |= KVQ_FLAG_BLOCK_TABLE;
+      par = -1;
+    }
+    int blocks = M;
+    if (p.keep_lens) {
+      const int keep = __ldg(p.keep_lens + b);
+      if (keep < 0 || (long long)keep > (long long)M * pl.page_size) {
+        if (par >= 0) flags |= KVQ_FLAG_SEQ_LEN;
+        blocks = 0;
+      } else {
+        blocks = (int)(((long long)keep + pl.page_size - 1) / pl.page_size);
+      }
+    }
+    const int e = (par >= 0 && c < blocks) ? old[par * cols + k] : -1;
+    const int was = old[i];
+    pl.block_table[(long long)b * M + c] = e;
+    if (e != was) {
+      if (e >= 0) atomicAdd(pl.ref_count + e, 1);
+      if (was >= 0) atomicSub(pl.ref_count + was, 1);
+    }
+  }
+  flag(p.status, flags);
+}
+
+// ---- reserve ----------------------------------------------------------
+
+// What sequence b asks for: the touched blocks [first, last), and whether
+// the first holds tokens from before (partial).
+struct Ask {
+  int first, last, n;
+  bool partial;
+  uint32_t flags;
+};
+__device__ __forceinline__ Ask ask_of(const PoolParams& p, int b) {
+  const kvq_page_pool& pl = p.pool;
+  Ask a{0, 0, 0, false, 0u};
+  const int before = __ldg(p.seq_lens_before + b);
+  const int n = p.new_lens ? __ldg(p.new_lens + b) : p.num_new;
+  if (n == 0 && before >= 0) return a;
+  if (n < 0 || n > p.num_new || before < 0 ||
+      (long long)before + n > (long long)pl.max_blocks_per_seq * pl.page_size) {
+    a.flags = KVQ_FLAG_SEQ_LEN;
+    return a;
+  }
+  a.n = n;
+  a.first = before / pl.page_size;
+  a.last = (int)(((long long)before + n + pl.page_size - 1) / pl.page_size);
+  a.partial = before % pl.page_size != 0;
+  return a;
+}
+
+__device__ __forceinline__ int entry(const PoolParams& p, int b, int j) {
+  const int e = p.pool.block_table[(long long)b * p.pool.max_blocks_per_seq + j];
+  return (e < 0 || e >= p.pool.num_pages) ? -1 : e;
+}
+
+// One CTA.  Shared: mine[b] = the mapped partial page of b (-1: none), later
+// whether it is replaced; at[b] = exclusive prefix of the pages needed.
+__global__ void __launch_bounds__(kOne) reserve_kernel(const __grid_constant__ PoolParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  extern __shared__ int32_t sh[];
+  __shared__ int scratch[33];
+  const kvq_page_pool& pl = p.pool;
+  const int B = pl.batch, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long M = pl.max_blocks_per_seq;
+  int32_t* mine = sh;
+  int32_t* at = sh + B;
+  uint32_t flags = 0;
+
+  for (int b = threadIdx.x; b < B; b += kOne) {
+    const Ask a = ask_of(p, b);
+    flags |= a.flags;
+    mine[b] = (a.n && a.partial) ? entry(p, b, a.first) : -1;
+  }
+  __syncthreads();
+  // a shared partial page is replaced for all its askers but the last, who
+  // keeps it when every holder asks: rank k of the askers leaves refs - k
+  for (int b = threadIdx.x; b < B; b += kOne) {
+    const int e = mine[b];
+    int replaced = 0;
+    if (e >= 0) {
+      const int refs = pl.ref_count[e];
+      if (refs > 1) {
+        int k = 0;
+        for (int i = 0; i < b; ++i) k += mine[i] == e;
+        replaced = refs - k > 1;
+      }
+    }
+    at[b] = replaced;
+  }
+  __syncthreads();
+  for (int b = threadIdx.x; b < B; b += kOne) mine[b] = at[b];
+  __syncthreads();
+  // pages needed per sequence: a warp each
+  for (int b = warp; b < B; b += kOne / 32) {
+    const Ask a = ask_of(p, b);
+    int need = 0;
+    for (int j = a.first + lane; j < a.last; j += 32) {
+      const int e = entry(p, b, j);
+      const bool part = j == a.first && a.partial;
+      need += e < 0 ? 1 : (part ? mine[b] : pl.ref_count[e] > 1);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) need += __shfl_xor_sync(0xffffffffu, need, o);
+    if (lane == 0) at[b] = need;
+  }
+  __syncthreads();
+  int total = 0;
+  for (int b0 = 0; b0 < B; b0 += kOne) {
+    const int b = b0 + threadIdx.x;
+    int sum;
+    const int ex = block_scan(b < B ? at[b] : 0, scratch, &sum);
+    if (b < B) at[b] = total + ex;
+    total += sum;
+  }
+  // the lowest free pages, in order
+  int found = 0;
+  for (int i0 = 0; i0 < pl.num_pages && found < total; i0 += kOne) {
+    const int i = i0 + threadIdx.x;
+    const int is_free = i < pl.num_pages && pl.ref_count[i] == 0;
+    int sum;
+    const int ex = block_scan(is_free, scratch, &sum);
+    if (is_free && found + ex < total) p.ws[found + ex] = i;
+    found += sum;
+  }
+  __syncthreads();
+  const bool ok = found >= total;
+  if (!ok && threadIdx.x == 0) flags |= KVQ_FLAG_POOL_EMPTY;
+  for (int b = warp; b < B; b += kOne / 32) {
+    const Ask a = ask_of(p, b);
+    int src = -1, dst = -1, next = at[b];
+    if (ok) {
+      for (int j0 = a.first; j0 < a.last; j0 += 32) {
+        const int j = j0 + lane;
+        const int e = j < a.last ? entry(p, b, j) : 0;
+        const bool part = j == a.first && a.partial;
+        const bool take = j < a.last && (e < 0 || (part ? mine[b] != 0 : pl.ref_count[e] > 1));
+        const unsigned who = __ballot_sync(0xffffffffu, take);
+        if (take) {
+          const int rank = next + __popc(who & ((1u << lane) - 1));
+          const int page = p.ws[rank];
+          pl.block_table[(long long)b * M + j] = page;
+          pl.ref_count[page] = 1;
+          p.ws[pl.num_pages + rank] = e;
+          if (e >= 0 && part) {
+            src = e;
+            dst = page;
+          }
+        }
+        next += __popc(who);
+      }
+    }
+    if (lane == 0) {  // the partial block is the first one: lane 0 of the first pass
+      p.copy_src[b] = src;
+      p.copy_dst[b] = dst;
+      if (p.granted) p.granted[b] = ok ? a.n : 0;
+    }
+  }
+  // the replaced pages' holders are counted off last, so that every decision
+  // above went by the counts before the call
+  __syncthreads();
+  if (ok)
+    for (int k = threadIdx.x; k < total; k += kOne) {
+      const int e = p.ws[pl.num_pages + k];
+      if (e >= 0) atomicSub(pl.ref_count + e, 1);
+    }
+  flag(p.status, flags);
+}
+
+// ---- compact ----------------------------------------------------------
+
+// One CTA.  ws[page]: for a live page at or behind n, its rank among them.
+__global__ void __launch_bounds__(kOne) compact_kernel(const __grid_constant__ PoolParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  __shared__ int scratch[33];
+  const kvq_page_pool& pl = p.pool;
+  const int N = pl.num_pages, half = N / 2;
+  int n = 0;
+  for (int i0 = 0; i0 < N; i0 += kOne) {
+    const int i = i0 + threadIdx.x;
+    n += __syncthreads_count(i < N && pl.ref_count[i] > 0);
+  }
+  int movers = 0, holes = 0;
+  for (int i0 = 0; i0 < N; i0 += kOne) {
+    const int i = i0 + threadIdx.x;
+    const bool live = i < N && pl.ref_count[i] > 0;
+    const int mover = live && i >= n, hole = i < n && !live;
+    int sum;
+    const int ex = block_scan(mover | (hole << 16), scratch, &sum);
+    const int km = movers + (ex & 0xffff), kh = holes + (ex >> 16);
+    if (mover) {
+      p.copy_src[km] = i;
+      p.ws[i] = km;
+    }
+    if (hole) p.copy_dst[kh] = i;
+    movers += sum & 0xffff;
+    holes += sum >> 16;
+  }
+  for (int k = movers + threadIdx.x; k < half; k += kOne) p.copy_src[k] = p.copy_dst[k] = -1;
+  if (threadIdx.x == 0) *p.num_live = n;
+  __syncthreads();
+  uint32_t flags = 0;
+  const long long entries = (long long)pl.batch * pl.max_blocks_per_seq;
+  for (long long i = threadIdx.x; i < entries; i += kOne) {
+    const int e = pl.block_table[i];
+    if (e < 0) continue;
+    if (e >= N || pl.ref_count[e] <= 0) {
+      pl.block_table[i] = -1;
+      flags |= KVQ_FLAG_BLOCK_TABLE;
+    } else if (e >= n) {
+      pl.block_table[i] = p.copy_dst[p.ws[e]];
+    }
+  }
+  __syncthreads();
+  for (int k = threadIdx.x; k < movers; k += kOne) {
+    const int s = p.copy_src[k], d = p.copy_dst[k];
+    pl.ref_count[d] = pl.ref_count[s];
+    pl.ref_count[s] = 0;
+  }
+  flag(p.status, flags);
+}
+
+// ---- copy -------------------------------------------------------------
+
+// Grid: x = pairs, y = layers.
+__global__ void __launch_bounds__(128) copy_kernel(const __grid_constant__ PageCopyParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int i = blockIdx.x, layer = blockIdx.y;
+  const int s = __ldg(p.src + i), d = __ldg(p.dst + i);
+  if (s < 0 || d < 0) return;
+  const bool report = p.report && layer == 0;
+  if (s >= p.num_pages || d >= p.num_pages) {
+    if (report && threadIdx.x == 0) flag(p.status, KVQ_FLAG_BLOCK_TABLE);
+    return;
+  }
+#pragma unroll
+  for (int a = 0; a < 6; ++a) {
+    const uint32_t n = p.bytes[a] / 16;
+    if (!n) continue;
+    const uint4* from = reinterpret_cast<const uint4*>(p.base[layer][a] + (size_t)s * p.bytes[a]);
+    uint4* to = reinterpret_cast<uint4*>(p.base[layer][a] + (size_t)d * p.bytes[a]);
+    for (uint32_t k = threadIdx.x; k < n; k += blockDim.x) to[k] = from[k];
+  }
+  if (report) {
+    uint32_t flags = d == s ? KVQ_FLAG_PAGE_LIST : 0u;
+    for (int j = threadIdx.x; j < p.num_pairs; j += blockDim.x) {
+      if (j == i) continue;
+      const int sj = __ldg(p.src + j), dj = __ldg(p.dst + j);
+      if (sj >= 0 && dj >= 0 && (sj == d || dj == d)) flags = KVQ_FLAG_PAGE_LIST;
+    }
+    flag(p.status, flags);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_pages_reorder(const PoolParams& p, cudaStream_t stream) {
+  // a CTA holds its columns of every row: as many as fit 128 KB, at most 32
+  int cols = 32;
+  while (cols > 1 && (size_t)p.pool.batch * cols * 4 > 128 * 1024) cols >>= 1;
+  const size_t smem = (size_t)p.pool.batch * cols * 4;
+  cudaError_t e = cudaFuncSetAttribute(reorder_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       128 * 1024);
+  if (e != cudaSuccess) return e;
+  const unsigned grid = (unsigned)((p.pool.max_blocks_per_seq + cols - 1) / cols);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, reorder_kernel, p, cols);
+}
+
+cudaError_t launch_pages_reserve(const PoolParams& p, cudaStream_t stream) {
+  const size_t smem = (size_t)p.pool.batch * 8;
+  cudaError_t e = cudaFuncSetAttribute(reserve_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       KVQ_MAX_POOL_BATCH * 8);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(reserve_kernel, dim3(1), dim3(kOne), smem, stream, p);
+}
+
+cudaError_t launch_pages_compact(const PoolParams& p, cudaStream_t stream) {
+  return launch_pdl(compact_kernel, dim3(1), dim3(kOne), 0, stream, p);
+}
+
+cudaError_t launch_pages_copy(const PageCopyParams& p, cudaStream_t stream) {
+  return launch_pdl(copy_kernel, dim3(p.num_pairs, p.layers), dim3(128), 0, stream, p);
+}
+
+}  // namespace kvq

@@ -1,0 +1,274 @@
+"""GPU tests of kvq_extend_attn against the fp64 oracle on the cache's own
+rows (read back through kvq_cache_read, itself tested bit for bit), with the
+error bound of tests/_prompt.py; refusals and flags; splits, streams, graphs; and equality with the decode call for one new token."""
+import numpy as np
+import pytest
+
+from tests._cases import Guarded, check_guards
+from tests._prompt import FORMATS, check_extend, new_cache, read_rows
+
+pytestmark = pytest.mark.gpu
+
+
+def _fill(K, cache, rng, lens, Hkv, D, most):
+    """`most` random rows of every sequence appended (keys with large channels)."""
+    import torch
+    B = len(lens)
+    k = rng.standard_normal((B, most, Hkv, D)).astype(np.float16)
+    k[..., 1:3] *= 4
+    v = rng.standard_normal((B, most, Hkv, D)).astype(np.float16)
+    z = torch.zeros(B, dtype=torch.int32, device="cuda")
+    K.kvq_append(cache, torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda(), z)
+
+
+def _case(fmt, D, Hq, Hkv, T, before, new=None, page=0, splits=0, seed=0, scale=0.0, extra=2):
+    """One call on guarded buffers, every sequence checked."""
+    import torch
+    import quantized_kv_decode_gb300 as K
+    rng = np.random.default_rng(seed)
+    B = len(before)
+    new = [T] * B if new is None else new
+    lens = [a + n for a, n in zip(before, new)]
+    most = max(max(lens), 1)
+    kch = FORMATS[fmt][2].get("k_per_channel", False)
+    cache = new_cache(fmt, Hkv, D, B, most + extra, page, seed)
+    if kch:  # a sequence's window holds its own newest tokens: append to its length
+        k = rng.standard_normal((B, most, Hkv, D)).astype(np.float16)
+        v = rng.standard_normal((B, most, Hkv, D)).astype(np.float16)
+        at = np.zeros(B, dtype=np.int32)
+        assert len(set(lens)) == 1, "axis-aware cases use one length"
+        K.kvq_append(cache, torch.from_numpy(k[:, :lens[0]].copy()).cuda(),
+                     torch.from_numpy(v[:, :lens[0]].copy()).cuda(), torch.from_numpy(at).cuda())
+    else:
+        _fill(K, cache, rng, lens, Hkv, D, most)
+    k16, v16 = read_rows(cache, lens, most)
+    q = rng.standard_normal((B, T, Hq, D)).astype(np.float16)
+    dev = "cuda"
+    tq = torch.from_numpy(q).to(dev)
+    tb = torch.tensor(before, dtype=torch.int32, device=dev)
+    tn = torch.tensor(new, dtype=torch.int32, device=dev)
+    out = Guarded(q.shape, torch.float16, dev)
+    out.tensor.fill_(9)
+    need = K.kvq_extend_workspace_size(cache.desc, B, T, Hq, most, splits)
+    ws = Guarded((need,), torch.uint8, dev) if need else None
+    if ws is not None:
+        ws.tensor.fill_(0xFF)          # NaN in every float
+    st = torch.zeros(1, dtype=torch.int32, device=dev)
+    for _ in range(2):                 # twice on one workspace
+        K.kvq_extend_attn(cache, tq, tb, most, new_lens=tn, out=out.tensor, workspace=None if ws is None else ws.tensor,
+                          dev_status=st, num_splits=splits, softmax_scale=scale)
+        assert int(st.item()) == 0
+        check_guards({"out": out, **({"ws": ws} if ws else {})}, "extend")
+        got = out.tensor.cpu().numpy()
+        for b in range(B):
+            assert (got[b, new[b]:] == 9).all(), "rows behind the sequence"
+            if new[b]:
+                check_extend(got[b], q[b], k16[b], v16[b], before[b], new[b], scale or D ** -0.5)
+    return got
+
+
+@pytest.mark.parametrize("fmt", list(FORMATS))
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_every_format(fmt, D):
+    _case(fmt, D, 4, 2, 37, [60, 60])
+
+
+@pytest.mark.parametrize("fmt", ["int4", "int8", "fp16", "kch4", "nf4"])
+@pytest.mark.parametrize("page", [8, 16, 64])
+def test_paged(fmt, page):
+    kch = fmt == "kch4"
+    _case(fmt, 128, 4, 2, 21, [100, 100] if kch else [100, 3], page=page)
+
+
+@pytest.mark.parametrize("T", [1, 2, 5, 16, 17, 64, 129, 300])
+@pytest.mark.parametrize("before", [0, 1, 63, 64, 700])
+def test_lengths(T, before):
+    _case("int4", 128, 8, 2, T, [before])
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (3, 1), (7, 1), (8, 1), (14, 2), (17, 1), (5, 5), (40, 2)])
+def test_head_groups(Hq, Hkv):
+    _case("int8", 64, Hq, Hkv, 19, [33, 150], new=[19, 6])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("fmt", ["fp16", "int4", "int8", "sym4", "int2"])
+def test_long_prompts(fmt, D):
+    """Several row tiles and key tiles, lengths that are no multiple of them."""
+    _case(fmt, D, 4, 2, 391, [0, 517], new=[391, 200], seed=2)
+
+
+@pytest.mark.parametrize("splits", [1, 2, 3, 7, 50])
+@pytest.mark.parametrize("fmt", ["int4", "fp16"])
+def test_splits(splits, fmt):
+    """Splits past a sequence's end and past a tile's last visible key."""
+    _case(fmt, 64, 4, 1, 40, [0, 300, 10], new=[40, 1, 0], splits=splits)
+
+
+def test_ragged_batch_and_scale():
+    _case("int4", 128, 8, 2, 33, [0, 5, 200, 64, 31], new=[33, 1, 0, 17, 32], page=16, scale=0.3)
+
+
+def test_split_counts_follow_the_request():
+    import quantized_kv_decode_gb300 as K
+    d = K.make_desc(4, 32, 2, 64, K.KVQ_DENSE, 4096)
+    assert K.kvq_extend_num_splits(d, 1, 4, 8, 4096, 5) == 5
+    assert K.kvq_extend_num_splits(d, 1, 4, 8, 64, 5) == 1
+    assert K.kvq_extend_workspace_size(d, 1, 4, 8, 64, 5) == 0
+    s = K.kvq_extend_num_splits(d, 1, 4, 8, 4096)
+    assert s > 1 and K.kvq_extend_workspace_size(d, 1, 4, 8, 4096) >= 4 * 8 * s * (64 + 2) * 4
+
+
+def test_one_new_token_is_the_decode_call():
+    """T = 1 and kvq_decode_attn agree within both calls' tolerances."""
+    import torch
+    import quantized_kv_decode_gb300 as K
+    rng = np.random.default_rng(1)
+    lens = [700, 64, 1]
+    cache = new_cache("int4", 2, 128, 3, 701)
+    _fill(K, cache, rng, lens, 2, 128, 700)
+    q = torch.from_numpy(rng.standard_normal((3, 8, 128)).astype(np.float16)).cuda()
+    t = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    a = K.kvq_decode_attn(cache, q, t, 700)
+    b = K.kvq_extend_attn(cache, q[:, None].contiguous(), t - 1, 700)[:, 0]
+    # the decode tolerance, and K, V and p rounded to fp16 (2^-11 each of |v| <= 5)
+    assert float((a - b).abs().max()) <= 2e-3 + 3 * 5 * 2.0 ** -11
+
+
+def test_flags_and_left_out_tokens():
+    import torch
+    import quantized_kv_decode_gb300 as K
+    rng = np.random.default_rng(9)
+    B, T, Hkv, Hq, D, L = 4, 5, 1, 3, 64, 40
+    cache = new_cache("int8", Hkv, D, B, L, 8)
+    _fill(K, cache, rng, [L] * B, Hkv, D, L)
+    k16, v16 = read_rows(cache, [L] * B, L)
+    q = rng.standard_normal((B, T, Hq, D)).astype(np.float16)
+    before = [20, 39, -1, 10]
+    cache.block_table[0, 1] = -1            # positions 8..15 of sequence 0
+    cache.block_table[3, :2] = 1 << 20      # everything of sequence 3: 0..14
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for splits in (1, 3):
+        st.zero_()
+        out = torch.full(q.shape, 9.0, dtype=torch.float16, device="cuda")
+        K.kvq_extend_attn(cache, torch.from_numpy(q).cuda(), torch.tensor(before, dtype=torch.int32, device="cuda"),
+                          L, out=out, dev_status=st, num_splits=splits)
+        assert int(st.item()) == K._lib.KVQ_FLAG_SEQ_LEN | K._lib.KVQ_FLAG_BLOCK_TABLE
+        got = out.cpu().numpy()
+        mapped = np.ones(25, dtype=bool)
+        mapped[8:16] = False
+        check_extend(got[0], q[0], k16[0], v16[0], 20, T, D ** -0.5, mapped)
+        assert (got[1:] == 0).all()         # too long, negative, nothing mapped: zero rows
+    # an unusable new_lens: that sequence is skipped
+    out.fill_(9)
+    st.zero_()
+    K.kvq_extend_attn(cache, torch.from_numpy(q).cuda(), torch.tensor([0, 0, 0, 0], dtype=torch.int32, device="cuda"),
+                      L, new_lens=torch.tensor([T + 1, -1, 1, 0], dtype=torch.int32, device="cuda"), out=out,
+                      dev_status=st)
+    got = out.cpu().numpy()
+    assert int(st.item()) & K._lib.KVQ_FLAG_SEQ_LEN
+    assert (got[0] == 9).all() and (got[1] == 9).all() and (got[2, 1:] == 9).all() and (got[3] == 9).all()
+    check_extend(got[2], q[2], k16[2], v16[2], 0, 1, D ** -0.5)
+
+
+@pytest.mark.parametrize("T", [3, 200])
+@pytest.mark.parametrize("fmt,value", [("fp16", float("nan")), ("fp16", float("inf")), ("int8", None)])
+def test_rows_behind_the_sequence_do_not_count(fmt, value, T):
+    """NaN and infinities in cached rows that no token may see: behind the
+    sequence, and in the causal mask's reach only later tokens'."""
+    import torch
+    import quantized_kv_decode_gb300 as K
+    rng = np.random.default_rng(4)
+    Hkv, D, L = 2, 64, 150 + T
+    cache = new_cache(fmt, Hkv, D, 1, L + 100)
+    _fill(K, cache, rng, [L], Hkv, D, L)
+    k16, v16 = read_rows(cache, [L], L)
+    if fmt == "fp16":
+        for t in (cache.k_codes, cache.v_codes):
+            t.view(torch.float16)[:, :, L:] = value
+    else:
+        for t in (cache.k_scale, cache.v_scale, cache.k_zero, cache.v_zero):
+            t[:, :, L:] = float("nan")
+    q = rng.standard_normal((1, T, 4, D)).astype(np.float16)
+    got = K.kvq_extend_attn(cache, torch.from_numpy(q).cuda(), torch.tensor([150], dtype=torch.int32, device="cuda"),
+                            L + 100).cpu().numpy()
+    check_extend(got[0], q[0], k16[0], v16[0], 150, T, D ** -0.5)
+
+
+def test_large_scores_keep_the_softmax_exact():
+    """Scores of several thousand: one key takes all the weight, whichever
+    tile it is in, and earlier tiles' sums vanish without overflow."""
+    import torch
+    import quantized_kv_decode_gb300 as K
+    D, L, T = 64, 600, 130
+    cache = new_cache("fp16", 1, D, 1, L)
+    k = np.zeros((1, L, 1, D), dtype=np.float16)
+    k[0, :, 0, 0] = np.arange(L) % 97 * 8
+    v = np.random.default_rng(0).standard_normal((1, L, 1, D)).astype(np.float16)
+    z = torch.zeros(1, dtype=torch.int32, device="cuda")
+    K.kvq_append(cache, torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda(), z)
+    q = np.zeros((1, T, 2, D), dtype=np.float16)
+    q[0, :, 0, 0] = 64.0
+    q[0, :, 1, 0] = -64.0
+    got = K.kvq_extend_attn(cache, torch.from_numpy(q).cuda(), torch.tensor([L - T], dtype=torch.int32, device="cuda"),
+                            L, softmax_scale=1.0).cpu().numpy().astype(np.float64)
+    for t in range(T):
+        see = np.arange(L - T + t + 1)
+        top = see[see % 97 == (see % 97).max()]
+        low = see[see % 97 == 0]
+        for h, w in ((0, top), (1, low)):
+            want = v[0, w, 0].astype(np.float64).mean(0)
+            # weights are exactly 1 / len(w): the mean's sum in fp32 and one rounding
+            assert np.abs(got[0, t, h] - want).max() <= 2.0 ** -11 * 5 + 2.0 ** -18
+
+
+def test_streams_and_graph_replay():
+    """Two calls on two streams with their own workspaces, and a captured call
+    replayed on new inputs, give the eager results bit for bit."""
+    import torch
+    import quantized_kv_decode_gb300 as K
+    rng = np.random.default_rng(6)
+    B, T, Hq, Hkv, D, L = 2, 9, 8, 2, 128, 900
+    cache = new_cache("int4", Hkv, D, B, L)
+    _fill(K, cache, rng, [L] * B, Hkv, D, L)
+    before = torch.tensor([L - T, 100], dtype=torch.int32, device="cuda")
+    qs = [torch.from_numpy(rng.standard_normal((B, T, Hq, D)).astype(np.float16)).cuda() for _ in range(3)]
+    need = K.kvq_extend_workspace_size(cache.desc, B, T, Hq, L)
+    ws = [torch.empty(max(need, 16), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    eager = [K.kvq_extend_attn(cache, q, before, L) for q in qs]
+    outs = [torch.empty_like(q) for q in qs]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for i, s in enumerate(streams):
+        K.kvq_extend_attn(cache, qs[i], before, L, out=outs[i], workspace=ws[i], stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], eager[0]) and torch.equal(outs[1], eager[1])
+    q, out = qs[0].clone(), torch.empty_like(qs[0])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        K.kvq_extend_attn(cache, q, before, L, out=out, workspace=ws[0])
+    for i in (2, 1):
+        q.copy_(qs[i])
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager[i])
+
+
+def test_workspace_refusal_and_device_checks():
+    import torch
+    import quantized_kv_decode_gb300 as K
+    cache = new_cache("int4", 2, 64, 2, 512)
+    q = torch.zeros((2, 3, 4, 64), dtype=torch.float16, device="cuda")
+    b = torch.zeros(2, dtype=torch.int32, device="cuda")
+    small = torch.empty(16, dtype=torch.uint8, device="cuda")
+    with pytest.raises(K.KVQError) as e:
+        K.kvq_extend_attn(cache, q, b, 512, workspace=small, num_splits=4)
+    assert e.value.status == K.KVQ_ERR_WORKSPACE
+    for bad in (dict(seq_lens_before=b.cpu()), dict(seq_lens_before=b.long()), dict(new_lens=b[:1]),
+                dict(out=q.float()), dict(dev_status=torch.zeros(1, device="cuda"))):
+        with pytest.raises((TypeError, ValueError)):
+            K.kvq_extend_attn(cache, **{"q": q, "seq_lens_before": b, "max_seq_len": 512, **bad})
+    with pytest.raises(ValueError):
+        K.kvq_extend_attn(cache, q.transpose(1, 2), b, 512)
+    with pytest.raises(ValueError):
+        K.kvq_extend_attn(cache, torch.cat([q, q]), torch.cat([b, b]), 512)
