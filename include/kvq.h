@@ -34,7 +34,8 @@
  *     block-table entry, a group the format cannot store) are OR-ed as
  *     KVQ_FLAG_* bits into *dev_status (a device uint32_t, may be NULL) and
  *     the offending unit is skipped as documented per call; read the word
- *     after the stream has synchronized.  No kernel traps or waits.
+ *     after the stream has synchronized.  No kernel traps, and waits
+ *     between the warps of one thread block end after two seconds.
  *
  * Cache layouts (one instance for K, one for V; the same shapes for both):
  *   row_bytes = head_dim * bits / 8;  groups = head_dim / group_size
@@ -121,6 +122,8 @@ typedef enum {
 #define KVQ_FLAG_POOL_EMPTY   0x20u /* too few free pages: nothing was reserved */
 #define KVQ_FLAG_PAGE_LIST    0x40u /* a copy list names a page twice as target,
                                        or one page as source and target       */
+#define KVQ_FLAG_TIMEOUT      0x80u /* a kernel's internal wait ran out (2 s):
+                                       the call's output is unusable          */
 
 typedef enum { KVQ_DENSE = 0, KVQ_PAGED = 1 } kvq_layout;
 

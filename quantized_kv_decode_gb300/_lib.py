@@ -29,6 +29,7 @@ KVQ_FLAG_NONFINITE = 0x8
 KVQ_FLAG_OOB = 0x10  # debug builds only: an access outside its array was skipped
 KVQ_FLAG_POOL_EMPTY = 0x20
 KVQ_FLAG_PAGE_LIST = 0x40
+KVQ_FLAG_TIMEOUT = 0x80  # a bounded wait inside a kernel ran out
 
 # kvq_rope_scaling
 ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "bands": 3, "yarn": 4}

@@ -82,11 +82,12 @@ kvq_status choose_extend(const kvq_cache_desc* desc, const CacheGeom& g, int32_t
                          int32_t num_new, int32_t num_q_heads, int32_t max_seq_len,
                          int32_t requested, ExtendChoice* out) {
   const int G = num_q_heads / desc->num_kv_heads;
-  const cudaError_t e = extend_plan(g, num_new, G, max_seq_len, &out->plan);
+  const cudaError_t e = extend_plan(g, num_new, G, &out->plan);
   if (e != cudaSuccess) return from_cuda(e);
   const int64_t tiles = ceil_div((int64_t)num_new * G, out->plan.tile_rows);
   const int64_t units = tiles * desc->num_kv_heads * std::max(batch, 1);
   out->splits = choose_splits(units, max_seq_len, requested, out->plan.occ);
+  if (tiles * out->splits > INT32_MAX) return KVQ_ERR_UNSUPPORTED;
   return out->splits > 0 ? KVQ_OK : KVQ_ERR_CUDA;
 }
 

@@ -9,7 +9,8 @@
 // units: m' = max(m, max_j s_j), l' = 2^(m - m') l + sum_j 2^(s_j - m'),
 // o' = 2^(m - m') o + sum_j 2^(s_j - m') v_j; splits over the context write
 // (m, l, o) and a merge joins them.
-#include "kvq_decode_fast.cuh"
+#include "kvq_extend_tc.cuh"
+#include "kvq_host.cuh"
 #include "kvq_load.cuh"
 #include "kvq_rope.cuh"
 
@@ -240,7 +241,7 @@ __global__ void __launch_bounds__(256) extend_merge_kernel(const __grid_constant
     if (!KVQ_IN(c, KVQ_ARRAY_WORKSPACE, ml + s, 8) || !KVQ_IN(c, KVQ_ARRAY_WORKSPACE, o + (long long)s * D, 4))
       continue;
     const float2 v = ml[s];
-    if (v.x == -INFINITY) continue;  // nothing seen: o is zero, m no reference
+    if (v.x == -INFINITY && v.y == 0.f) continue;  // nothing seen: o is zero, m no reference
     const float Mn = fmaxf(M, v.x), a = ex2(M - Mn), f = ex2(v.x - Mn);
     num = num * a + f * o[(long long)s * D];
     den = den * a + f * v.y;
@@ -284,13 +285,30 @@ cudaError_t run_any(const CacheGeom& c, const ExtendParams* p, ExtendPlan* plan,
 
 }  // namespace
 
-cudaError_t extend_plan(const CacheGeom& c, int num_new, int G, int max_len, ExtendPlan* plan) {
-  (void)num_new, (void)G, (void)max_len;
-  return run_any(c, nullptr, plan, nullptr);
+// The tensor-core kernel takes every per-token format at head_dim 64 and 128.
+static bool takes_tc(const CacheGeom& c) {
+  return !c.kch && (c.D == 64 || c.D == 128) && (!c.nf4 || nf4_table().symmetric);
 }
 
-cudaError_t launch_extend(const ExtendParams& p, const ExtendPlan&, cudaStream_t stream) {
-  cudaError_t e = run_any(p.v.geom, &p, nullptr, stream);
+static cudaError_t run_tc_any(const CacheGeom& c, int nq, const ExtendParams* p, ExtendPlan* plan, cudaStream_t s) {
+  if (c.nf4) return run_extend_tc_nf4(c.D, nq, p, plan, s);
+  switch (c.bits) {
+    case 2: return run_extend_tc_int2(c.D, nq, p, plan, s);
+    case 4: return run_extend_tc_int4(c.D, nq, p, plan, s);
+    case 8: return run_extend_tc_int8(c.D, nq, p, plan, s);
+    default: return run_extend_tc_fp16(c.D, nq, p, plan, s);
+  }
+}
+
+cudaError_t extend_plan(const CacheGeom& c, int num_new, int G, ExtendPlan* plan) {
+  plan->kind = !takes_tc(c) ? 0 : (long long)num_new * G <= 128 ? 1 : 2;
+  if (plan->kind == 0) return run_any(c, nullptr, plan, nullptr);
+  return run_tc_any(c, plan->kind, nullptr, plan, nullptr);
+}
+
+cudaError_t launch_extend(const ExtendParams& p, const ExtendPlan& plan, cudaStream_t stream) {
+  cudaError_t e = plan.kind == 0 ? run_any(p.v.geom, &p, nullptr, stream)
+                                 : run_tc_any(p.v.geom, plan.kind, &p, nullptr, stream);
   if (e == cudaSuccess && p.splits > 1) {
     const long long rows = (long long)p.batch * p.num_new * p.Hq;
     e = launch_pdl(extend_merge_kernel, dim3((unsigned)rows), dim3(p.v.geom.D), 0, stream, p);

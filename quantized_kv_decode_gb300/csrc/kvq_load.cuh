@@ -145,9 +145,9 @@ struct ExtendParams {
 struct ExtendPlan {
   int tile_rows = 0;
   int occ = 0;
-  int kind = 0;
+  int kind = 0;  // 0: mma.sync kernel, 1 / 2: tensor-core kernel with that many 128-row tiles a CTA
 };
-cudaError_t extend_plan(const CacheGeom& c, int num_new, int G, int max_len, ExtendPlan* plan);
+cudaError_t extend_plan(const CacheGeom& c, int num_new, int G, ExtendPlan* plan);
 cudaError_t launch_extend(const ExtendParams& p, const ExtendPlan& plan, cudaStream_t stream);
 
 }  // namespace kvq
