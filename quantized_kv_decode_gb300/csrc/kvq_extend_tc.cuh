@@ -50,6 +50,10 @@ namespace ext {
 using fast::ex2;
 
 constexpr int kKeys = 64;
+template <int N>
+struct Int {
+  static constexpr int value = N;
+};
 constexpr float kLazy = 8.f;  // log2 units the maximum may lead the reference
 
 // KIND: 0 uniform codes (asymmetric or symmetric), 1 NF4, 2 fp16
@@ -58,17 +62,32 @@ struct Cfg {
   static constexpr bool LO = KIND != 2;
   static constexpr int SOFT = 4 * NQ;             // softmax warps
   static constexpr int PROD = NQ == 1 ? 8 : 4;    // producer warps
-  static constexpr int WARPS = SOFT + PROD + 1;
+  static constexpr int LOAD = LO ? 2 : 1;         // loader warps (fp16: the warp that passes stages on)
+  static constexpr int WARPS = SOFT + PROD + 1 + LOAD;
   static constexpr int THREADS = WARPS * 32;
   static constexpr int MAT = kKeys * D * 2;       // one fp16 tile
   static constexpr int STAGE = (LO ? 3 : 2) * MAT;
-  static constexpr int STAGES = D == 128 ? 4 : 6;
+  static constexpr int STAGES = LO ? 3 : 4;
   static constexpr int SEGS = D / 32;             // 32-channel segments of a row
-  static constexpr int UNITS = 2 * SEGS * kKeys / (PROD * 32);  // segments per producer thread and tile
+  // A producer warp works on items: the whole rows of KPI keys of K or V, a
+  // segment per lane.
+  static constexpr int KPI = 32 / SEGS;
+  static constexpr int ITEMS = 2 * kKeys / KPI;   // of a tile
+  static constexpr int MINE = ITEMS / PROD;       // of a warp and tile
+  // Codes and headers arrive in a ring of DEPTH tiles by asynchronous copies
+  // (one to three tiles of latency covered); fp16 rows go to their stage.
+  static constexpr int DEPTH = !LO ? 0 : D == 128 ? (BITS == 8 ? 3 : 4) : 6;
+  static constexpr int HDR = 512;                 // an item's scales, and its zeros 256 bytes on
+  static constexpr int RAW = LO ? 32 * 4 * BITS + HDR : 0;  // bytes of an item
+  // arrivals that fill a ring slot: the loaders' copies (fp16: the
+  // producers', straight into a stage) and the key masks; and a stage
+  static constexpr int RAW_FULL = (LO ? LOAD : PROD) * 32 + 1, FULL = LO ? PROD : 1;
+  static constexpr int SLOTS = LO ? DEPTH : STAGES;
   // tensor memory columns: per tile S (64, P in its place), O (D), Q (D / 2)
   static constexpr uint32_t COL_S = 0, COL_O = NQ * kKeys, COL_Q = COL_O + NQ * D;
   static constexpr uint32_t COLS = NQ == 2 ? 512 : 256;
-  static constexpr size_t SMEM = (size_t)STAGES * STAGE + 1024 + 512;
+  static constexpr size_t SMEM = (size_t)STAGES * STAGE + (size_t)DEPTH * ITEMS * RAW + 1024 + 1024;
+  static_assert(SMEM <= 227 * 1024, "shared memory");
   static_assert(COL_Q + NQ * D / 2 <= COLS, "tensor memory");
   // channel held at place i of an eight-channel chunk (the unpacking leaves
   // 4-bit and 2-bit codes as pairs (i, i + 4))
@@ -77,8 +96,11 @@ struct Cfg {
 };
 
 // Barriers and flags behind the stages
+constexpr int kMaxDepth = 6;
 template <int STAGES>
 struct Shared {
+  unsigned long long raw_full[kMaxDepth], raw_empty[kMaxDepth];
+  uint32_t raw_ok[kMaxDepth][2];
   unsigned long long full[STAGES], empty[STAGES];
   unsigned long long q_full[2], s_full[2], p_full[2], o_full[2];
   uint32_t ok[STAGES][2];   // per key: mapped and before the end
@@ -89,57 +111,107 @@ struct Shared {
 
 // ---- producers --------------------------------------------------------
 
-// The codes and headers of 32 channels of one key, as loaded.
+// The codes and headers of 32 channels of one key.
 template <int BITS>
 struct Seg {
   uint32_t w[BITS == 16 ? 1 : BITS];  // 32 * BITS / 32 words
   uint32_t s[2], z[2];                // up to four fp16 scales and zeros
 };
 
-template <int BITS, int KIND>
-__device__ __forceinline__ void load_seg(const ExtendParams& p, int which, long long row, int seg,
-                                         Seg<BITS>& x) {
+// Starts the copy of an item's codes and headers: this lane's segment of its
+// key's row (`row`, -1: none), and, spread over the lanes, the keys' headers
+// (2 * ngroups bytes each; row_k: the row of key lane % KPI).
+template <int BITS, int KIND, int D, int HB>
+__device__ __forceinline__ void copy_item(const ExtendParams& p, int which, long long row, long long row_k, int seg,
+                                          int lane, uint32_t dst) {
+  constexpr int KPI = 32 / (D / 32), SB = 4 * BITS;
   const CacheGeom& c = p.v.geom;
-#pragma unroll
-  for (int i = 0; i < BITS; ++i) x.w[i] = 0;
-  x.s[0] = x.s[1] = x.z[0] = x.z[1] = 0;
-  if (row < 0) return;
-  const uint8_t* src = p.v.codes[which] + row * c.row_bytes + seg * 4 * BITS;
   const int a_codes = which ? KVQ_ARRAY_V_CODES : KVQ_ARRAY_K_CODES;
-  if (KVQ_IN(c, a_codes, src, 4 * BITS)) {
-    if constexpr (BITS == 2) {
-      const uint2 t = __ldg(reinterpret_cast<const uint2*>(src));
-      x.w[0] = t.x, x.w[1] = t.y;
-    } else {
+  const uint8_t* src = p.v.codes[which] + max(row, 0ll) * (D * BITS / 8) + seg * SB;
+  const bool live = row >= 0 && KVQ_IN(c, a_codes, src, SB);
+  if constexpr (SB == 8) {
+    fast::cp_async_small<8>(dst + lane * 8, src, live);
+  } else {
 #pragma unroll
-      for (int i = 0; i < BITS / 4; ++i) {
-        const uint4 t = __ldg(reinterpret_cast<const uint4*>(src) + i);
-        x.w[4 * i] = t.x, x.w[4 * i + 1] = t.y, x.w[4 * i + 2] = t.z, x.w[4 * i + 3] = t.w;
+    for (int i = 0; i < SB / 16; ++i) fast::cp_async16(dst + lane * SB + i * 16, src + i * 16, live);
+  }
+  const bool zeros = lane >= KPI;
+  const int k = lane & (KPI - 1);
+  const int arr = zeros ? (which ? KVQ_ARRAY_V_ZERO : KVQ_ARRAY_K_ZERO)
+                        : (which ? KVQ_ARRAY_V_SCALE : KVQ_ARRAY_K_SCALE);
+  const __half* h = (zeros ? p.v.zero[which] : p.v.scale[which]) + max(row_k, 0ll) * (HB / 2);
+  const uint32_t to = dst + 32 * SB + (zeros ? 256 : 0);
+  const bool mine = lane < ((KIND == 0 && !c.sym) ? 2 * KPI : KPI);
+  const bool on = row_k >= 0 && mine && KVQ_IN(c, arr, h, HB);
+  if constexpr (HB >= 4) {
+    if (mine) {
+      if constexpr (HB == 4 || HB == 8) {
+        fast::cp_async_small<HB>(to + k * HB, h, on);
+      } else {
+        fast::cp_async16(to + k * HB, h, on);
+        if constexpr (HB == 32) fast::cp_async16(to + k * HB + 16, h + 8, on);
       }
     }
-  }
-  const int n = c.g >= 32 ? 1 : 32 / c.g;  // groups in the segment: 1, 2 or 4
-  const long long h = row * c.ngroups + seg * 32 / c.g;
-  const int a_scale = which ? KVQ_ARRAY_V_SCALE : KVQ_ARRAY_K_SCALE;
-  const int a_zero = which ? KVQ_ARRAY_V_ZERO : KVQ_ARRAY_K_ZERO;
-  const __half* sp = p.v.scale[which] + h;
-  if (KVQ_IN(c, a_scale, sp, 2 * n)) {
-    if (n == 1) x.s[0] = __ldg(reinterpret_cast<const unsigned short*>(sp));
-    else if (n == 2) x.s[0] = __ldg(reinterpret_cast<const uint32_t*>(sp));
-    else {
-      const uint2 t = __ldg(reinterpret_cast<const uint2*>(sp));
-      x.s[0] = t.x, x.s[1] = t.y;
+  } else {
+    // One header of two bytes per key: copied by aligned words, which two
+    // consecutive rows share; a word whose other row is not this item's (or
+    // not in the cache) is taken in part.  Key k lies (row of key 0) & 1
+    // halves further on, and the key in a word's first half takes the word.
+    const int odd = (int)(__shfl_sync(0xffffffffu, max(row_k, 0ll), 0, KPI) & 1);
+    const long long next = __shfl_down_sync(0xffffffffu, row_k, 1, KPI);
+    const bool pair = k + 1 < KPI && next == row_k + 1;
+    if (mine && (((k + odd) & 1) == 0 || k == 0)) {
+      const __half* word = h - (row_k >= 0 ? (row_k & 1) : 0);
+      const int bytes = !on ? 0 : ((row_k & 1) || pair) ? 4 : 2;
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(to + ((k + odd) >> 1) * 4), "l"(word),
+                   "r"(bytes)
+                   : "memory");
     }
   }
-  if (KIND == 0 && !c.sym) {
-    const __half* zp = p.v.zero[which] + h;
-    if (KVQ_IN(c, a_zero, zp, 2 * n)) {
-      if (n == 1) x.z[0] = __ldg(reinterpret_cast<const unsigned short*>(zp));
-      else if (n == 2) x.z[0] = __ldg(reinterpret_cast<const uint32_t*>(zp));
-      else {
-        const uint2 t = __ldg(reinterpret_cast<const uint2*>(zp));
-        x.z[0] = t.x, x.z[1] = t.y;
-      }
+}
+
+// Reads one lane's segment back from the ring.  Lanes of the upper 64
+// channels take their chunks in the order 2, 3, 0, 1 (swap), so that the
+// stores of a warp fall into different banks.
+template <int BITS, int KIND, int D, int NG>
+__device__ __forceinline__ void take_item(const CacheGeom& c, const uint8_t* item, int lane, int odd, bool swap,
+                                          Seg<BITS>& x) {
+  constexpr int SEGS = D / 32, SB = 4 * BITS;
+  const int key = lane / SEGS, seg = lane % SEGS;
+  if constexpr (SB == 8) {
+    const uint2 t = *reinterpret_cast<const uint2*>(item + lane * 8);
+    x.w[0] = swap ? t.y : t.x;
+    x.w[1] = swap ? t.x : t.y;
+  } else {
+    uint32_t w[BITS];
+#pragma unroll
+    for (int i = 0; i < SB / 16; ++i) {
+      const uint4 t = *reinterpret_cast<const uint4*>(item + lane * SB + i * 16);
+      w[4 * i] = t.x, w[4 * i + 1] = t.y, w[4 * i + 2] = t.z, w[4 * i + 3] = t.w;
+    }
+#pragma unroll
+    for (int i = 0; i < BITS; ++i) x.w[i] = swap ? w[(i + BITS / 2) % BITS] : w[i];
+  }
+  const uint8_t* h = item + 32 * SB;
+  x.s[0] = x.s[1] = x.z[0] = x.z[1] = 0;
+  const bool zeros = KIND == 0 && !c.sym;
+  if constexpr (NG == 1) {
+    const int n = c.ngroups;  // the row's groups; this segment's is seg * 32 / g
+    const int at = n == 1 ? 2 * (key + odd) : key * 2 * n + 2 * (seg * 32 / c.g);
+    x.s[0] = *reinterpret_cast<const unsigned short*>(h + at);
+    if (zeros) x.z[0] = *reinterpret_cast<const unsigned short*>(h + 256 + at);
+  } else if constexpr (NG == 2) {
+    const int at = lane * 4;
+    x.s[0] = *reinterpret_cast<const uint32_t*>(h + at);
+    if (zeros) x.z[0] = *reinterpret_cast<const uint32_t*>(h + 256 + at);
+    if (swap) x.s[0] = fast::prmt_b32(x.s[0], 0u, 0x1032u), x.z[0] = fast::prmt_b32(x.z[0], 0u, 0x1032u);
+  } else {
+    const int at = lane * 8;
+    uint2 t = *reinterpret_cast<const uint2*>(h + at);
+    x.s[0] = swap ? t.y : t.x, x.s[1] = swap ? t.x : t.y;
+    if (zeros) {
+      t = *reinterpret_cast<const uint2*>(h + 256 + at);
+      x.z[0] = swap ? t.y : t.x, x.z[1] = swap ? t.x : t.y;
     }
   }
 }
@@ -147,74 +219,114 @@ __device__ __forceinline__ void load_seg(const ExtendParams& p, int which, long 
 __device__ __forceinline__ __half2 as_h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
 __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 
-// The eight codes of chunk ch of a segment as fp16 1024 + q (NF4: as levels)
+// A group's conversion: d = q - z from the unpacked codes, hi = fp16(d s).
+struct Group {
+  __half2 s, off, off16;  // scale; -(1024 + z); -(64 + z)
+  float sf, zf;
+  bool plain;             // 1024 + z a number that fp16 holds, no product beyond fp16
+};
 template <int BITS, int KIND>
-__device__ __forceinline__ void biased8(const Seg<BITS>& x, int ch, const uint32_t (&lut)[4], uint32_t (&o)[4]) {
+__device__ __forceinline__ Group group_of(uint32_t sw, uint32_t zw, int sym) {
+  Group g;
+  const __half s = __ushort_as_half((unsigned short)(sw & 0xFFFFu));
+  g.s = __half2half2(s);
+  g.sf = __half2float(s);
+  g.zf = 0.f;
+  g.plain = true;
+  g.off = g.off16 = g.s;
+  if constexpr (KIND == 0) {
+    g.zf = sym ? (float)(1 << (BITS - 1)) : __half2float(__ushort_as_half((unsigned short)(zw & 0xFFFFu)));
+    g.plain = fabsf(g.zf) <= 1024.f && g.sf * (fabsf(g.zf) + (float)((1 << BITS) - 1)) < 65504.f;
+    g.off = __half2half2(__float2half_rn(-1024.f - g.zf));
+    g.off16 = __half2half2(__float2half_rn(-64.f - g.zf));
+  }
+  return g;
+}
+
+// d of the eight codes of chunk ch of a segment, in fp16 pairs
+template <int BITS, int KIND>
+__device__ __forceinline__ void codes8(const Seg<BITS>& x, int ch, const Group& g, const uint32_t (&lut)[4],
+                                       __half2 (&d)[4]) {
   if constexpr (KIND == 1) {
+    uint32_t o[4];
     fast::nib8_to_h2_nf4(x.w[ch], o, lut);
-  } else if constexpr (BITS == 4) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = fast::and_or(x.w[ch] >> (4 * i), 0x000F000Fu, fast::kH1024);
+    for (int i = 0; i < 4; ++i) d[i] = as_h2(o[i]);
+  } else if constexpr (BITS == 4) {
+    // low nibbles as 1024 + q; high ones, left in place, as 1024 + 16 q
+    const __half2 k16 = as_h2(fast::kH1_16);
+    const uint32_t w = x.w[ch], v = w >> 8;
+    d[0] = __hadd2(as_h2(fast::and_or(w, 0x000F000Fu, fast::kH1024)), g.off);
+    d[1] = __hfma2(as_h2(fast::and_or(w, 0x00F000F0u, fast::kH1024)), k16, g.off16);
+    d[2] = __hadd2(as_h2(fast::and_or(v, 0x000F000Fu, fast::kH1024)), g.off);
+    d[3] = __hfma2(as_h2(fast::and_or(v, 0x00F000F0u, fast::kH1024)), k16, g.off16);
   } else if constexpr (BITS == 2) {
     const uint32_t w = (x.w[ch >> 1] >> (16 * (ch & 1))) & 0xFFFFu;
     const uint32_t v = (w & 0xFFu) | ((w & 0xFF00u) << 8);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = fast::and_or(v >> (2 * i), 0x00030003u, fast::kH1024);
+    for (int i = 0; i < 4; ++i) d[i] = __hadd2(as_h2(fast::and_or(v >> (2 * i), 0x00030003u, fast::kH1024)), g.off);
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      o[i] = fast::prmt_b32(x.w[2 * ch + (i >> 1)], 0x64646464u, (i & 1) ? 0x4342u : 0x4140u);
+      d[i] = __hadd2(as_h2(fast::prmt_b32(x.w[2 * ch + (i >> 1)], 0x64646464u, (i & 1) ? 0x4342u : 0x4140u)), g.off);
   }
 }
 
-// One segment to fp16 (hi, and lo for K) at its places in the tile:
-// blocks of 64 channels, [key][128 bytes], chunks XORed with the key.
-template <int BITS, int KIND, int D>
-__device__ __forceinline__ void store_seg(const ExtendParams& p, const Seg<BITS>& x, bool is_k, int key, int seg,
+// One segment to fp16 (hi, and lo for K) at its places in the tile: blocks
+// of 64 channels, [key][128 bytes], 16-byte chunks XORed with the key.
+// NG: groups in the segment.  swap (0 or 2): x holds its chunks in that order.
+template <int BITS, int KIND, int NG>
+__device__ __forceinline__ void store_seg(const Seg<BITS>& x, bool is_k, int key, int seg, int sym, int swap,
                                           uint8_t* hi, uint8_t* lo, const uint32_t (&lut)[4]) {
-  const CacheGeom& c = p.v.geom;
   const uint32_t base = (uint32_t)((seg >> 1) * (kKeys * 128) + key * 128);
-  const int per = c.g >= 32 ? 4 : c.g / 8;  // chunks per group
+  const uint32_t turn = (uint32_t)(((seg & 1) * 4) ^ swap ^ (key & 7));
+  Group g[NG];
+  bool plain = true;
 #pragma unroll
-  for (int ch = 0; ch < 4; ++ch) {
-    const int grp = ch / per;
-    const uint32_t sw = (grp & 2 ? x.s[1] : x.s[0]) >> (16 * (grp & 1));
-    const __half s = __ushort_as_half((unsigned short)(sw & 0xFFFFu));
-    __half z = __ushort_as_half(0);
-    uint32_t b[4], h[4], l[4];
-    biased8<BITS, KIND>(x, ch, lut, b);
-    const __half2 s2 = __half2half2(s);
-    bool plain = true;  // no product beyond fp16, and 1024 + z a whole number that fp16 holds
-    __half2 off = __half2half2(z);
-    if constexpr (KIND == 0) {
-      const uint32_t zw = (grp & 2 ? x.z[1] : x.z[0]) >> (16 * (grp & 1));
-      z = c.sym ? __int2half_rn(1 << (BITS - 1)) : __ushort_as_half((unsigned short)(zw & 0xFFFFu));
-      const float zf = __half2float(z), sf = __half2float(s);
-      plain = fabsf(zf) <= 1024.f && sf * (fabsf(zf) + (float)((1 << BITS) - 1)) < 65504.f;
-      off = __half2half2(__float2half_rn(-1024.f - zf));
-    }
-    if (plain) {
+  for (int n = 0; n < NG; ++n) {
+    g[n] = group_of<BITS, KIND>(x.s[n >> 1] >> (16 * (n & 1)), x.z[n >> 1] >> (16 * (n & 1)), sym);
+    plain = plain && g[n].plain;
+  }
+  if (plain) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __half2 d = KIND == 1 ? as_h2(b[i]) : __hadd2(as_h2(b[i]), off);
-        const __half2 v = __hmul2_rn(d, s2);
-        h[i] = as_u32(v);
-        l[i] = as_u32(__hfma2(d, s2, __hneg2(v)));  // the product is exact in the fma: what hi left
+    for (int ch = 0; ch < 4; ++ch) {
+      const Group& gc = g[ch / (4 / NG)];
+      __half2 d[4], v[4];
+      codes8<BITS, KIND>(x, ch, gc, lut, d);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = __hmul2_rn(d[i], gc.s);
+      const uint32_t at = base + ((turn ^ ch) << 4);
+      *reinterpret_cast<uint4*>(hi + at) = make_uint4(as_u32(v[0]), as_u32(v[1]), as_u32(v[2]), as_u32(v[3]));
+      if (is_k) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = __hfma2(d[i], gc.s, __hneg2(v[i]));  // exact inside: what hi left
+        *reinterpret_cast<uint4*>(lo + at) = make_uint4(as_u32(v[0]), as_u32(v[1]), as_u32(v[2]), as_u32(v[3]));
       }
-    } else {  // far zero-points and scales near fp16's end, in fp32
+    }
+  } else {  // far zero-points and scales near fp16's end, in fp32
+#pragma unroll
+    for (int ch = 0; ch < 4; ++ch) {
+      const Group& gc = g[ch / (4 / NG)];
+      uint32_t h[4], l[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 q = __half22float2(__hsub2(as_h2(b[i]), as_h2(fast::kH1024)));
-        const float zf = __half2float(z), sf = __half2float(s);
-        const float a = (q.x - zf) * sf, e = (q.y - zf) * sf;
-        h[i] = pack_sat(a, e);
+        float a[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int q = BITS <= 4 ? i + 4 * e : 2 * i + e;  // the code at this place
+          const uint32_t c = BITS == 8   ? x.w[2 * ch + (q >> 2)] >> (8 * (q & 3))
+                             : BITS == 4 ? x.w[ch] >> (4 * q)
+                                         : x.w[ch >> 1] >> (16 * (ch & 1) + 2 * q);
+          a[e] = ((float)(c & ((1u << BITS) - 1u)) - gc.zf) * gc.sf;
+        }
+        h[i] = pack_sat(a[0], a[1]);
         const float2 v = __half22float2(as_h2(h[i]));
-        l[i] = pack_sat(fabsf(a) > 65504.f ? 0.f : a - v.x, fabsf(e) > 65504.f ? 0.f : e - v.y);
+        l[i] = pack_sat(fabsf(a[0]) > 65504.f ? 0.f : a[0] - v.x, fabsf(a[1]) > 65504.f ? 0.f : a[1] - v.y);
       }
+      const uint32_t at = base + ((turn ^ ch) << 4);
+      *reinterpret_cast<uint4*>(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
+      if (is_k) *reinterpret_cast<uint4*>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
     }
-    const uint32_t at = base + ((((uint32_t)(seg & 1) * 4 + ch) ^ (key & 7)) << 4);
-    *reinterpret_cast<uint4*>(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
-    if (is_k) *reinterpret_cast<uint4*>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
   }
 }
 
@@ -232,7 +344,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
   pdl_launch_dependents();
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + ((1024 - (tc::smem_addr(raw) & 1023)) & 1023);
-  auto& sh = *reinterpret_cast<Shared<C::STAGES>*>(smem + C::STAGES * C::STAGE);
+  auto& sh = *reinterpret_cast<Shared<C::STAGES>*>(smem + C::STAGES * C::STAGE + C::DEPTH * C::ITEMS * C::RAW);
   const CacheGeom& c = p.v.geom;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int kvh = blockIdx.y, b = blockIdx.z;
@@ -258,10 +370,12 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
   const int all_see = L ? before + t_first : -1;  // every row sees the positions up to here
   const int nq = (NQ == 2 && live_rows - r0 <= 128) ? 1 : NQ;  // tiles with rows
 
-  static_assert(sizeof(Shared<C::STAGES>) <= 512, "room behind the stages");
+  static_assert(sizeof(Shared<C::STAGES>) <= 1024, "room behind the stages");
   const uint32_t bars = tc::smem_addr(&sh);
   auto full = [&](int s) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, full) + 8 * s; };
   auto empty = [&](int s) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, empty) + 8 * s; };
+  auto raw_full = [&](int s) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, raw_full) + 8 * s; };
+  auto raw_empty = [&](int s) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, raw_empty) + 8 * s; };
   auto q_full = [&](int i) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, q_full) + 8 * i; };
   auto s_full = [&](int i) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, s_full) + 8 * i; };
   auto p_full = [&](int i) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, p_full) + 8 * i; };
@@ -270,8 +384,12 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
-      tc::mbar_init(full(s), C::PROD);
+      tc::mbar_init(full(s), C::FULL);
       tc::mbar_init(empty(s), 1);
+    }
+    for (int s = 0; s < C::SLOTS; ++s) {
+      tc::mbar_init(raw_full(s), C::RAW_FULL);
+      tc::mbar_init(raw_empty(s), C::PROD);
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(q_full(i), 128);
@@ -287,6 +405,20 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = sh.tmem;
+
+  // row of a position of this split: -1 behind its end, -2 unmapped
+  auto row_of = [&](int pos) -> long long {
+    if (pos >= k1) return -1;
+    const long long row = token_row(c, b, kvh, pos);
+    return row < 0 ? -2 : row;
+  };
+  auto note_keys = [&](uint32_t* to, int j) {  // which keys of tile j count; one warp
+    const int pos = k0 + j * kKeys + lane;
+    const long long r0k = row_of(pos), r1k = row_of(pos + 32);
+    const uint32_t a = __ballot_sync(0xffffffffu, r0k >= 0), d = __ballot_sync(0xffffffffu, r1k >= 0);
+    if (lane == 0) to[0] = a, to[1] = d;
+    if ((r0k == -2 || r1k == -2) && p.status) atomicOr(p.status, KVQ_FLAG_BLOCK_TABLE);
+  };
 
   if (warp < C::SOFT) {
     // ------------------------------------------------------ softmax rows
@@ -347,7 +479,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
         const bool whole = (ok0 & ok1) == 0xFFFFFFFFu && ks + kKeys - 1 <= last;
         if (!__all_sync(0xffffffffu, whole)) {
           uint32_t bad0 = 0, bad1 = 0;
-          if constexpr (KIND == 2)
+          if (KIND == 2 && ks + kKeys - 1 > all_see)  // (checked in these tiles alone)
 #pragma unroll
             for (int g = 0; g < C::SEGS; ++g) bad0 |= sh.bad[st][g][0], bad1 |= sh.bad[st][g][1];
           const int seen = last - ks;  // keys 0 .. seen of the tile
@@ -359,10 +491,10 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
             else if (KIND == 2 && (bad & 1u)) u[e >> 5][e & 31] = 0x7FFFFFFFu;    // NaN: its V is not finite
           }
         }
-        float mx = -INFINITY;
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int e = 0; e < 64; ++e) mx = fmaxf(mx, __uint_as_float(u[e >> 5][e & 31]));
-        mx *= p.scale_log2;
+        for (int e = 0; e < 64; ++e) top[e & 3] = fmaxf(top[e & 3], __uint_as_float(u[e >> 5][e & 31]));
+        const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale_log2;
         const bool moves = mx > m + kLazy;  // m = -inf: any finite maximum
         if (__any_sync(0xffffffffu, moves)) {
           const float mn = moves ? mx : m;
@@ -382,17 +514,20 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
           }
         }
         const float base = m == -INFINITY ? 0.f : m;
+        const float2 sl2 = make_float2(p.scale_log2, p.scale_log2), nb2 = make_float2(-base, -base);
         uint32_t w[32];
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int e = 0; e < 64; e += 2) {
-          const float a = ex2(fmaf(__uint_as_float(u[e >> 5][e & 31]), p.scale_log2, -base));
-          const float d = ex2(fmaf(__uint_as_float(u[e >> 5][(e & 31) + 1]), p.scale_log2, -base));
-          sum[e & 2] += a;
-          sum[(e & 2) + 1] += d;
-          w[e >> 1] = fast::pack_h2(a, d);
+          float2 x = make_float2(__uint_as_float(u[e >> 5][e & 31]), __uint_as_float(u[e >> 5][(e & 31) + 1]));
+          x = tc::fma2(x, sl2, nb2);
+          x.x = ex2(x.x);
+          x.y = ex2(x.y);
+          sum[(e >> 1) & 1] = tc::add2(sum[(e >> 1) & 1], x);
+          w[e >> 1] = fast::pack_h2(x.x, x.y);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        sum[0] = tc::add2(sum[0], sum[1]);
+        l += sum[0].x + sum[0].y;
         tc::st32(ts, w);
         tc::wait_st();
       }
@@ -442,24 +577,8 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
     }
   } else if (warp < C::SOFT + C::PROD) {
     // ------------------------------------------------------ producers
-    const int tid = threadIdx.x - C::SOFT * 32;
-    constexpr int PT = C::PROD * 32;
-    // this thread's key, and segment and K / V of its unit u; the keys of a
-    // warp are consecutive, so its 16-byte stores hit all banks
-    const int key = tid & (kKeys - 1);
-    auto seg_of = [&](int u) { return ((u * PT + tid) / kKeys) % C::SEGS; };
-    auto which_of = [&](int u) { return (u * PT + tid) / (kKeys * C::SEGS); };
-    auto row_at = [&](int j) -> long long {
-      const int pos = k0 + j * kKeys + key;
-      if (pos >= k1) return -1;
-      const long long row = token_row(c, b, kvh, pos);
-      return row < 0 ? -2 : row;
-    };
-    auto note_keys = [&](int st, long long row) {  // the first two warps hold key = lane, 32 + lane
-      const uint32_t ok = __ballot_sync(0xffffffffu, row >= 0);
-      if (lane == 0) sh.ok[st][tid >> 5] = ok;
-      if (row == -2 && p.status) atomicOr(p.status, KVQ_FLAG_BLOCK_TABLE);
-    };
+    const int tid = threadIdx.x - C::SOFT * 32, pw = tid >> 5;
+    bool ok = true;  // after a wait that ran out the loops go on without waiting
     if constexpr (KIND != 2) {
       uint32_t lut[4] = {0u, 0u, 0u, 0u};
       if constexpr (KIND == 1) {
@@ -470,132 +589,208 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
           lut[2 + (i >> 2)] |= (h >> 8) << (8 * (i & 3));
         }
       }
-      Seg<BITS> x[C::UNITS];
-      long long row = -1;
-      auto load_all = [&](int j) {
-        row = row_at(j);
-#pragma unroll
-        for (int u = 0; u < C::UNITS; ++u) load_seg<BITS, KIND>(p, which_of(u), row, seg_of(u), x[u]);
-      };
-      if (tiles) load_all(0);
-      for (int j = 0; j < tiles; ++j) {
-        const int st = j % C::STAGES;
-        if (!__all_sync(0xffffffffu, tc::mbar_wait(empty(st), ((j / C::STAGES) & 1) ^ 1, stop))) break;
-        uint8_t* base = smem + st * C::STAGE;
-        Seg<BITS> y[C::UNITS];
-#pragma unroll
-        for (int u = 0; u < C::UNITS; ++u) y[u] = x[u];
-        const long long key_row = row;
-        if (j + 1 < tiles) load_all(j + 1);
-        if (tid < 64) note_keys(st, key_row);
-#pragma unroll
-        for (int u = 0; u < C::UNITS; ++u) {
-          const bool is_k = which_of(u) == 0;
-          store_seg<BITS, KIND, D>(p, y[u], is_k, key, seg_of(u), base + (is_k ? 0 : 2 * C::MAT),
-                                   base + C::MAT, lut);
-        }
-        tc::fence_async_shared();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(full(st));
-      }
-    } else {
-      // fp16 rows: straight to their places, one tile ahead of the arrival
-      for (int j = 0; j <= tiles; ++j) {
-        if (j < tiles) {
-          const int st = j % C::STAGES;
-          if (!__all_sync(0xffffffffu, tc::mbar_wait(empty(st), ((j / C::STAGES) & 1) ^ 1, stop))) break;
-          const uint32_t base = tc::smem_addr(smem + st * C::STAGE);
-          const long long row = row_at(j);
-          if (tid < 64) note_keys(st, row);
-#pragma unroll
-          for (int u = 0; u < C::UNITS; ++u) {
-            const int seg = seg_of(u), which = which_of(u);
-            const uint8_t* src = p.v.codes[which] + max(row, 0ll) * c.row_bytes + seg * 64;
-            const uint32_t dst = base + which * C::MAT + (seg >> 1) * (kKeys * 128) + key * 128;
-#pragma unroll
-            for (int ch = 0; ch < 4; ++ch) {
-              const uint8_t* sp = src + ch * 16;
-              fast::cp_async16(dst + ((((seg & 1) * 4 + ch) ^ (key & 7)) << 4), sp,
-                               row >= 0 && KVQ_IN(c, which ? KVQ_ARRAY_V_CODES : KVQ_ARRAY_K_CODES, sp, 16));
-            }
-          }
-        }
-        fast::cp_async_commit();
-        fast::cp_async_wait<1>();
-        if (j > 0) {
-          const int st = (j - 1) % C::STAGES;
-          // in a tile that some row sees in part, an infinite or NaN V must
-          // not meet the zero weights of the rows that do not see it
-          const bool partly = k0 + j * kKeys - 1 > all_see;
-#pragma unroll
-          for (int u = 0; u < C::UNITS; ++u) {
-            if (which_of(u) == 0) continue;  // (a warp's units are all K or all V)
-            const int seg = seg_of(u);
-            bool bad = false;
-            if (partly) {
-              uint8_t* row = smem + st * C::STAGE + C::MAT + (seg >> 1) * (kKeys * 128) + key * 128;
-#pragma unroll
-              for (int ch = 0; ch < 4; ++ch) {
-                uint4* v = reinterpret_cast<uint4*>(row + ((((seg & 1) * 4 + ch) ^ (key & 7)) << 4));
-                const uint4 q = *v;
-                if (nonfinite2(q.x) || nonfinite2(q.y) || nonfinite2(q.z) || nonfinite2(q.w)) {
-                  bad = true;
-                  *v = make_uint4(0u, 0u, 0u, 0u);
-                }
-              }
-            }
-            const uint32_t keys = __ballot_sync(0xffffffffu, bad);
-            if (lane == 0) sh.bad[st][seg][(tid >> 5) & 1] = keys;
+      constexpr int KI = kKeys / C::KPI;  // items of K (and of V)
+      const int seg = lane % C::SEGS, key_l = lane / C::SEGS;
+      const int swap = seg >= 2 ? 2 : 0;
+      // (NG, groups per segment, is fixed for the call: one small loop runs)
+      auto convert = [&](auto ng) {
+        constexpr int NG = decltype(ng)::value;
+        int st = 0, ph = 1, slot = 0, rph = 0;
+#pragma unroll 1
+        for (int j = 0; j < tiles; ++j) {
+          if (ok) ok = tc::mbar_wait(raw_full(slot), rph, stop) && tc::mbar_wait(empty(st), ph, stop);
+          ok = __all_sync(0xffffffffu, ok);
+          uint8_t* base = smem + st * C::STAGE;
+          if (pw == 0 && lane < 2) sh.ok[st][lane] = sh.raw_ok[slot][lane];
+#pragma unroll(C::MINE < 2 ? 1 : 2)
+          for (int u = 0; u < C::MINE; ++u) {
+            const int item = u * C::PROD + pw, key0 = (item % KI) * C::KPI;
+            const bool is_k = item < KI;
+            const uint8_t* raw_item = smem + C::STAGES * C::STAGE + (slot * C::ITEMS + item) * C::RAW;
+            const int pos0 = k0 + j * kKeys + key0;
+            const int odd = c.layout == KVQ_DENSE && pos0 < k1 ? (((b * c.Hkv + kvh) & c.slots) ^ pos0) & 1 : 0;
+            Seg<BITS> x;
+            take_item<BITS, KIND, D, NG>(c, raw_item, lane, odd, swap, x);
+            store_seg<BITS, KIND, NG>(x, is_k, key0 + key_l, seg, c.sym, swap, base + (is_k ? 0 : 2 * C::MAT),
+                                      base + C::MAT, lut);
           }
           tc::fence_async_shared();
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(full(st));
+          if (lane == 0) {
+            tc::mbar_arrive(full(st));
+            tc::mbar_arrive(raw_empty(slot));
+          }
+          if (++st == C::STAGES) st = 0, ph ^= 1;
+          if (++slot == C::DEPTH) slot = 0, rph ^= 1;
         }
+      };
+      if (c.g >= 32) convert(Int<1>{});
+      else if (c.g == 16) convert(Int<2>{});
+      else convert(Int<4>{});
+    } else {
+      // fp16 rows: straight to their places.  This thread's key, and segment
+      // and K / V of its unit u: the keys of a warp are consecutive, so its
+      // 16-byte copies hit all banks.
+      constexpr int PT = C::PROD * 32, UNITS = 2 * C::SEGS * kKeys / PT;
+      const int key = tid & (kKeys - 1);
+      auto seg_of = [&](int u) { return ((u * PT + tid) / kKeys) % C::SEGS; };
+      auto which_of = [&](int u) { return (u * PT + tid) / (kKeys * C::SEGS); };
+      for (int j = 0; j < tiles; ++j) {
+        const int st = j % C::STAGES;
+        if (ok) ok = tc::mbar_wait(empty(st), ((j / C::STAGES) & 1) ^ 1, stop);
+        ok = __all_sync(0xffffffffu, ok);
+        const uint32_t base = tc::smem_addr(smem + st * C::STAGE);
+        const long long row = row_of(k0 + j * kKeys + key);
+#pragma unroll 1
+        for (int u = 0; u < UNITS; ++u) {
+          const int seg = seg_of(u), which = which_of(u);
+          const uint8_t* src = p.v.codes[which] + max(row, 0ll) * c.row_bytes + seg * 64;
+          const uint32_t dst = base + which * C::MAT + (seg >> 1) * (kKeys * 128) + key * 128;
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) {
+            const uint8_t* sp = src + ch * 16;
+            fast::cp_async16(dst + ((((seg & 1) * 4 + ch) ^ (key & 7)) << 4), sp,
+                             row >= 0 && KVQ_IN(c, which ? KVQ_ARRAY_V_CODES : KVQ_ARRAY_K_CODES, sp, 16));
+          }
+        }
+        if (pw == 0) {
+          note_keys(sh.ok[st], j);
+          if (lane == 0) tc::mbar_arrive(raw_full(st));
+        }
+        if (k0 + (j + 1) * kKeys - 1 <= all_see) {
+          tc::mbar_arrive_copies(raw_full(st));
+          continue;
+        }
+        // in a tile that some row sees in part, an infinite or NaN V must not
+        // meet the zero weights of the rows that do not see it
+        fast::cp_async_commit();
+        fast::cp_async_wait<0>();
+#pragma unroll 1
+        for (int u = 0; u < UNITS; ++u) {
+          if (which_of(u) == 0) continue;  // (a warp's units are all K or all V)
+          const int seg = seg_of(u);
+          bool bad = false;
+          uint8_t* vrow = smem + st * C::STAGE + C::MAT + (seg >> 1) * (kKeys * 128) + key * 128;
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) {
+            uint4* v = reinterpret_cast<uint4*>(vrow + ((((seg & 1) * 4 + ch) ^ (key & 7)) << 4));
+            const uint4 q = *v;
+            if (nonfinite2(q.x) || nonfinite2(q.y) || nonfinite2(q.z) || nonfinite2(q.w)) {
+              bad = true;
+              *v = make_uint4(0u, 0u, 0u, 0u);
+            }
+          }
+          const uint32_t keys = __ballot_sync(0xffffffffu, bad);
+          if (lane == 0) sh.bad[st][seg][pw & 1] = keys;
+        }
+        tc::mbar_arrive(raw_full(st));
+      }
+      fast::cp_async_commit();
+      fast::cp_async_wait<0>();  // nothing in flight when the block ends
+    }
+  } else if (warp < C::SOFT + C::PROD + C::LOAD) {
+    // ------------------------------------------------------ loaders
+    bool ok = true;
+    if constexpr (KIND != 2) {
+      constexpr int KI = kKeys / C::KPI;  // items of K (and of V)
+      const int lw = warp - C::SOFT - C::PROD;
+      const int seg = lane % C::SEGS, key_l = lane / C::SEGS;
+      auto load = [&](auto hb) {  // (the headers' size is fixed for the call)
+        int slot = 0, ph = 1;
+#pragma unroll 1
+        for (int j = 0; j < tiles; ++j) {
+          long long row_k[KI / C::LOAD];  // this lane's header row of each item
+#pragma unroll
+          for (int u = 0; u < KI / C::LOAD; ++u)
+            row_k[u] = row_of(k0 + j * kKeys + (u * C::LOAD + lw) * C::KPI + (lane & (C::KPI - 1)));
+          if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(raw_empty(slot), ph, stop));
+          const uint32_t dst = tc::smem_addr(smem + C::STAGES * C::STAGE + slot * C::ITEMS * C::RAW);
+#pragma unroll
+          for (int u = 0; u < KI / C::LOAD; ++u) {
+            const int i = u * C::LOAD + lw;
+            const long long row = __shfl_sync(0xffffffffu, row_k[u], key_l);
+            copy_item<BITS, KIND, D, decltype(hb)::value>(p, 0, row, row_k[u], seg, lane, dst + i * C::RAW);
+            copy_item<BITS, KIND, D, decltype(hb)::value>(p, 1, row, row_k[u], seg, lane, dst + (KI + i) * C::RAW);
+          }
+          tc::mbar_arrive_copies(raw_full(slot));
+          if (lw == 0) {
+            note_keys(sh.raw_ok[slot], j);
+            if (lane == 0) tc::mbar_arrive(raw_full(slot));
+          }
+          if (++slot == C::DEPTH) slot = 0, ph ^= 1;
+        }
+      };
+      switch (c.ngroups) {
+        case 1: load(Int<2>{}); break;
+        case 2: load(Int<4>{}); break;
+        case 4: load(Int<8>{}); break;
+        case 8: load(Int<16>{}); break;
+        default: load(Int<32>{}); break;
+      }
+      fast::cp_async_commit();
+      fast::cp_async_wait<0>();  // nothing in flight when the block ends
+    } else {
+      // The rows of a stage have landed: make them visible to the tensor core
+      // and pass the stage on.  (Not the producers' job: the fence would wait
+      // for their later copies; nor the MMA warp's: for its products.)
+#pragma unroll 1
+      for (int j = 0; j < tiles && ok; ++j) {
+        const int st = j % C::STAGES;
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(raw_full(st), (j / C::STAGES) & 1, stop));
+        tc::fence_async_shared();
+        if (ok && lane == 0) tc::mbar_arrive(full(st));
+        __syncwarp();
       }
     }
-  } else if (lane == 0 && tiles) {
+  } else if (tiles) {
     // ------------------------------------------------------ MMA issue
+    // (the whole warp walks the loop, one lane issues: operands stay uniform)
     constexpr uint32_t id_qk = tc::idesc_f16(kKeys, false), id_pv = tc::idesc_f16(D, true);
+    const uint32_t t0 = __shfl_sync(0xffffffffu, tmem, 0);
     const uint32_t data = tc::smem_addr(smem);
-    auto qk = [&](int i, int j) {
-      const uint32_t base = data + (j % C::STAGES) * C::STAGE;
-      const uint32_t d = tmem + C::COL_S + i * kKeys, a = tmem + C::COL_Q + i * (D / 2);
+    const uint64_t k_desc = tc::smem_desc(data, 16, 1024);
+    const uint64_t v_desc = tc::smem_desc(data + (C::LO ? 2 : 1) * C::MAT, kKeys * 128, 1024);
+    auto qk = [&](int i, int st) {  // descriptors count 16 bytes
+      const uint64_t kd = k_desc + (uint32_t)(st * (C::STAGE / 16));
+      const uint32_t d = t0 + C::COL_S + i * kKeys, a = t0 + C::COL_Q + i * (D / 2);
+      // hi, then lo: the tiles follow one another in 64-channel blocks
 #pragma unroll
-      for (int part = 0; part < (C::LO ? 2 : 1); ++part)
+      for (int n = 0; n < (C::LO ? 2 : 1) * (D / 64); ++n)
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          tc::mma_ts(d, a + kk * 8,
-                     tc::smem_desc(base + part * C::MAT + (kk >> 2) * (kKeys * 128) + (kk & 3) * 32, 16, 1024), id_qk,
-                     part || kk);
+        for (int kk = 0; kk < 4; ++kk)
+          tc::mma_ts(d, a + ((n * 4) & (D / 16 - 1)) * 8 + kk * 8, kd + (uint32_t)(n * (kKeys * 128 / 16) + kk * 2),
+                     id_qk, n || kk);
       tc::commit(s_full(i));
     };
-    auto pv = [&](int i, int j) {
-      const uint32_t base = data + (j % C::STAGES) * C::STAGE + (C::LO ? 2 : 1) * C::MAT;
-      const uint32_t d = tmem + C::COL_O + i * D, a = tmem + C::COL_S + i * kKeys;
+    auto pv = [&](int i, int st, bool first, uint32_t then) {
+      const uint64_t vd = v_desc + (uint32_t)(st * (C::STAGE / 16));
+      const uint32_t d = t0 + C::COL_O + i * D, a = t0 + C::COL_S + i * kKeys;
 #pragma unroll
-      for (int kk = 0; kk < kKeys / 16; ++kk)
-        tc::mma_ts(d, a + kk * 8, tc::smem_desc(base + kk * 2048, kKeys * 128, 1024), id_pv, j || kk);
+      for (int kk = 0; kk < kKeys / 16; ++kk) tc::mma_ts(d, a + kk * 8, vd + kk * (2048 / 16), id_pv, !first || kk);
+      if (then) tc::commit(then);
     };
-    bool ok = tc::mbar_wait(full(0), 0, stop);
+    bool ok = __all_sync(0xffffffffu, tc::mbar_wait(full(0), 0, stop));
     for (int i = 0; ok && i < nq; ++i) {
-      ok = tc::mbar_wait(q_full(i), 0, stop);
+      ok = __all_sync(0xffffffffu, tc::mbar_wait(q_full(i), 0, stop));
       tc::fence_after();
       if (ok) qk(i, 0);
     }
+    int st = 0, ph = 0;  // stage of key tile j and its phase
     for (int j = 0; ok && j < tiles; ++j) {
-      for (int i = 0; ok && i < nq; ++i) {
-        ok = tc::mbar_wait(p_full(i), j & 1, stop);
+      const int st1 = st + 1 == C::STAGES ? 0 : st + 1, ph1 = st1 ? ph : ph ^ 1;
+      for (int i = 0; i < nq; ++i) {
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(p_full(i), j & 1, stop));
         tc::fence_after();
         if (!ok) break;
-        pv(i, j);
-        if (i == nq - 1) tc::commit(empty(j % C::STAGES));
-        if (j + 1 < tiles) {
-          if (i == 0) ok = tc::mbar_wait(full((j + 1) % C::STAGES), ((j + 1) / C::STAGES) & 1, stop);
-          if (ok) qk(i, j + 1);
-        } else {
-          tc::commit(o_full(i));
-        }
+        const bool end_tile = i == nq - 1, end_key = j + 1 == tiles;
+        pv(i, st, j == 0, end_key ? o_full(i) : end_tile ? empty(st) : 0u);
+        if (end_key) continue;
+        if (i == 0) ok = __all_sync(0xffffffffu, tc::mbar_wait(full(st1), ph1, stop));
+        if (!ok) break;
+        qk(i, st1);
       }
+      st = st1;
+      ph = ph1;
     }
   }
   __syncwarp();
