@@ -14,11 +14,11 @@
 // bytes a cycle from shared memory, half its bandwidth or less; with Q in
 // shared memory a 64-key step would be bound by fetching Q again.
 //
-// Warps.  0-3 (and 4-7 with two tiles): softmax, a row per thread.  Then the
-// producers, which read the codes, turn them into fp16 and store them in the
-// tensor core's swizzled layout (four warps, or eight with one tile).  The
-// last warp issues the MMAs.  With two tiles one's softmax runs under the
-// other's products.
+// Warps.  0 and 3 issue the MMAs, a tile each; 1 and 2 copy codes and headers to a ring in
+// shared memory; from 4 on softmax, a row per thread (four warps a tile); the
+// producers behind turn the ring's codes into fp16 in the tensor core's
+// swizzled layout (four warps, or eight with one tile).  With two tiles one's
+// softmax runs under the other's products.
 //
 // Precision.  q - z is a whole number (exact in fp16 up to 2048) and s has
 // 11 bits, so x_hat = (q - z) s has up to 23: K enters as the sum of two fp16
@@ -33,7 +33,7 @@
 // Reference maximum.  m moves only when a tile's maximum exceeds it by 2^8
 // (P is at most 256 then), so O in tensor memory is rescaled rarely.
 //
-// Order of the MMAs.  One thread issues PV(j) and then QK(j + 1) of a tile,
+// Order of the MMAs.  One lane issues PV(j) and then QK(j + 1) of a tile,
 // and MMAs run in the order issued: S may be overwritten as soon as QK(j + 1)
 // is issued, and when its completion is seen PV(j) is complete too, so the
 // softmax may rescale O until it hands over P(j + 1).
@@ -61,9 +61,11 @@ template <int BITS, int KIND, int D, int NQ>
 struct Cfg {
   static constexpr bool LO = KIND != 2;
   static constexpr int SOFT = 4 * NQ;             // softmax warps
-  static constexpr int PROD = NQ == 1 ? 8 : 4;    // producer warps
+  static constexpr int PROD = NQ == 1 || LO ? 8 : 4;  // producer warps
   static constexpr int LOAD = LO ? 2 : 1;         // loader warps (fp16: the warp that passes stages on)
-  static constexpr int WARPS = SOFT + PROD + 1 + LOAD;
+  // warps 0 and 3 issue the MMAs, 1 .. LOAD load; softmax from 4 on (a warp reads
+  // the tensor memory lanes of its number modulo 4), producers behind
+  static constexpr int SOFT0 = 4, PROD0 = SOFT0 + SOFT, WARPS = PROD0 + PROD;
   static constexpr int THREADS = WARPS * 32;
   static constexpr int MAT = kKeys * D * 2;       // one fp16 tile
   static constexpr int STAGE = (LO ? 3 : 2) * MAT;
@@ -102,7 +104,7 @@ struct Shared {
   unsigned long long raw_full[kMaxDepth], raw_empty[kMaxDepth];
   uint32_t raw_ok[kMaxDepth][2];
   unsigned long long full[STAGES], empty[STAGES];
-  unsigned long long q_full[2], s_full[2], p_full[2], o_full[2];
+  unsigned long long q_full[2], s_full[2], p_full[2], o_full[2], turn[2];
   uint32_t ok[STAGES][2];   // per key: mapped and before the end
   uint32_t bad[STAGES][4][2];  // per segment and key: V held an infinity or NaN (set to zero)
   uint32_t tmem;
@@ -346,15 +348,15 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
   uint8_t* smem = raw + ((1024 - (tc::smem_addr(raw) & 1023)) & 1023);
   auto& sh = *reinterpret_cast<Shared<C::STAGES>*>(smem + C::STAGES * C::STAGE + C::DEPTH * C::ITEMS * C::RAW);
   const CacheGeom& c = p.v.geom;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = tc::uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int kvh = blockIdx.y, b = blockIdx.z;
   const int split = blockIdx.x % p.splits;
   // row tiles last first: with a causal mask they see the most keys
   const int tile = gridDim.x / p.splits - 1 - blockIdx.x / p.splits;
   pdl_wait();
 
-  const int before = checked_len(c, p.lens_before, b, -1);
-  const int n_raw = new_rows_of(p.new_lens, b, p.num_new);
+  const int before = tc::uniform(checked_len(c, p.lens_before, b, -1));
+  const int n_raw = tc::uniform(new_rows_of(p.new_lens, b, p.num_new));
   const int n = max(n_raw, 0);
   const bool fits = before >= 0 && n_raw >= 0 && (long long)before + n <= p.len_limit;
   if (!fits && threadIdx.x == 0 && blockIdx.x == 0 && kvh == 0 && p.status) atomicOr(p.status, KVQ_FLAG_SEQ_LEN);
@@ -379,13 +381,14 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
   auto q_full = [&](int i) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, q_full) + 8 * i; };
   auto s_full = [&](int i) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, s_full) + 8 * i; };
   auto p_full = [&](int i) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, p_full) + 8 * i; };
+  auto turn = [&](int i) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, turn) + 8 * i; };
   auto o_full = [&](int i) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, o_full) + 8 * i; };
   volatile int* stop = &sh.stop;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
       tc::mbar_init(full(s), C::FULL);
-      tc::mbar_init(empty(s), 1);
+      tc::mbar_init(empty(s), nq);
     }
     for (int s = 0; s < C::SLOTS; ++s) {
       tc::mbar_init(raw_full(s), C::RAW_FULL);
@@ -394,17 +397,18 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(q_full(i), 128);
       tc::mbar_init(s_full(i), 1);
-      tc::mbar_init(p_full(i), 128);
+      tc::mbar_init(p_full(i), 4);
       tc::mbar_init(o_full(i), 1);
+      tc::mbar_init(turn(i), 1);
     }
     sh.stop = 0;
     tc::mbar_init_fence();
   }
-  if (warp == C::WARPS - 1) tc::tmem_alloc(tc::smem_addr(&sh.tmem), C::COLS);
+  if (warp == 0) tc::tmem_alloc(tc::smem_addr(&sh.tmem), C::COLS);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  const uint32_t tmem = sh.tmem;
+  const uint32_t tmem = tc::uniform(sh.tmem);
 
   // row of a position of this split: -1 behind its end, -2 unmapped
   auto row_of = [&](int pos) -> long long {
@@ -420,9 +424,9 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
     if ((r0k == -2 || r1k == -2) && p.status) atomicOr(p.status, KVQ_FLAG_BLOCK_TABLE);
   };
 
-  if (warp < C::SOFT) {
+  if (warp >= C::SOFT0 && warp < C::PROD0) {
     // ------------------------------------------------------ softmax rows
-    const int i = warp >> 2;
+    const int i = (warp - C::SOFT0) >> 2;
     const long long r = r0 + i * 128 + (warp & 3) * 32 + lane;
     const bool live = r < live_rows;
     const bool any_live = r - lane < live_rows;
@@ -462,38 +466,45 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
     }
     float m = -INFINITY, l = 0.f;  // reference maximum (log2 units) and sum
     bool going = i < nq;
+#pragma unroll 1
     for (int j = 0; going && j < tiles; ++j) {
       const int st = j % C::STAGES;
-      // (the tile's key masks come with its stage, which stays until P is handed over)
-      going = tc::mbar_wait(full(st), (j / C::STAGES) & 1, stop) && tc::mbar_wait(s_full(i), j & 1, stop);
-      going = __all_sync(0xffffffffu, going);
+      // (S follows the stage's arrival, so its key masks are there too; they
+      // stay until P is handed over)
+      going = __all_sync(0xffffffffu, tc::mbar_wait(s_full(i), j & 1, stop));
       if (!going) break;
       tc::fence_after();
       if (any_live) {
         uint32_t u[2][32];
         tc::ld32(ts, u[0]);
         tc::ld32(ts + 32, u[1]);
-        tc::wait_ld();
         const int ks = k0 + j * kKeys;
         const uint32_t ok0 = sh.ok[st][0], ok1 = sh.ok[st][1];
-        const bool whole = (ok0 & ok1) == 0xFFFFFFFFu && ks + kKeys - 1 <= last;
-        if (!__all_sync(0xffffffffu, whole)) {
-          uint32_t bad0 = 0, bad1 = 0;
-          if (KIND == 2 && ks + kKeys - 1 > all_see)  // (checked in these tiles alone)
+        const bool whole = __all_sync(0xffffffffu, (ok0 & ok1) == 0xFFFFFFFFu && ks + kKeys - 1 <= last);
+        tc::wait_ld();
+        if (!whole) {
 #pragma unroll
-            for (int g = 0; g < C::SEGS; ++g) bad0 |= sh.bad[st][g][0], bad1 |= sh.bad[st][g][1];
-          const int seen = last - ks;  // keys 0 .. seen of the tile
+          for (int h = 0; h < 2; ++h) {
+            uint32_t bad = 0;
+            if (KIND == 2 && ks + kKeys - 1 > all_see)  // (checked in these tiles alone)
 #pragma unroll
-          for (int e = 0; e < 64; ++e) {
-            const uint32_t ok = (e < 32 ? ok0 : ok1) >> (e & 31), bad = (e < 32 ? bad0 : bad1) >> (e & 31);
-            const bool see = e <= seen && (ok & 1u);
-            if (!see) u[e >> 5][e & 31] = 0xFF800000u;             // -inf
-            else if (KIND == 2 && (bad & 1u)) u[e >> 5][e & 31] = 0x7FFFFFFFu;    // NaN: its V is not finite
+              for (int g = 0; g < C::SEGS; ++g) bad |= sh.bad[st][g][h];
+            const int seen = last - ks - 32 * h;  // keys 0 .. seen of these
+            const uint32_t see = (h ? ok1 : ok0) & (seen >= 31 ? 0xFFFFFFFFu : seen < 0 ? 0u : (2u << seen) - 1u);
+            bad &= see;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              if (!(see >> e & 1u)) u[h][e] = 0xFF800000u;                   // -inf
+              else if (KIND == 2 && (bad >> e & 1u)) u[h][e] = 0x7FFFFFFFu;  // NaN: its V is not finite
+            }
           }
+          __syncwarp();
         }
         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int e = 0; e < 64; ++e) top[e & 3] = fmaxf(top[e & 3], __uint_as_float(u[e >> 5][e & 31]));
+        for (int e = 0; e < 64; e += 2)
+          top[(e >> 1) & 3] = tc::max3(top[(e >> 1) & 3], __uint_as_float(u[e >> 5][e & 31]),
+                                       __uint_as_float(u[e >> 5][(e & 31) + 1]));
         const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale_log2;
         const bool moves = mx > m + kLazy;  // m = -inf: any finite maximum
         if (__any_sync(0xffffffffu, moves)) {
@@ -515,24 +526,29 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
         }
         const float base = m == -INFINITY ? 0.f : m;
         const float2 sl2 = make_float2(p.scale_log2, p.scale_log2), nb2 = make_float2(-base, -base);
-        uint32_t w[32];
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int e = 0; e < 64; e += 2) {
-          float2 x = make_float2(__uint_as_float(u[e >> 5][e & 31]), __uint_as_float(u[e >> 5][(e & 31) + 1]));
-          x = tc::fma2(x, sl2, nb2);
-          x.x = ex2(x.x);
-          x.y = ex2(x.y);
-          sum[(e >> 1) & 1] = tc::add2(sum[(e >> 1) & 1], x);
-          w[e >> 1] = fast::pack_h2(x.x, x.y);
+        for (int h = 0; h < 4; ++h) {  // (P overwrites scores already in registers)
+          uint32_t w[8];
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            const int k = 16 * h + e;
+            float2 x = make_float2(__uint_as_float(u[k >> 5][k & 31]), __uint_as_float(u[k >> 5][(k & 31) + 1]));
+            x = tc::fma2(x, sl2, nb2);
+            x.x = ex2(x.x);
+            x.y = ex2(x.y);
+            sum[(e >> 1) & 1] = tc::add2(sum[(e >> 1) & 1], x);
+            w[e >> 1] = fast::pack_h2(x.x, x.y);
+          }
+          tc::st8(ts + 8 * h, w);
         }
+        tc::wait_st();
         sum[0] = tc::add2(sum[0], sum[1]);
         l += sum[0].x + sum[0].y;
-        tc::st32(ts, w);
-        tc::wait_st();
       }
       tc::fence_before();
-      tc::mbar_arrive(p_full(i));
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(p_full(i));
     }
     if (going && tiles) going = __all_sync(0xffffffffu, tc::mbar_wait(o_full(i), 0, stop));
     tc::fence_after();
@@ -575,9 +591,9 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
         if (KVQ_IN(c, KVQ_ARRAY_WORKSPACE, ml, 8)) *ml = make_float2(m, l);
       }
     }
-  } else if (warp < C::SOFT + C::PROD) {
+  } else if (warp >= C::PROD0) {
     // ------------------------------------------------------ producers
-    const int tid = threadIdx.x - C::SOFT * 32, pw = tid >> 5;
+    const int tid = threadIdx.x - C::PROD0 * 32, pw = tid >> 5;
     bool ok = true;  // after a wait that ran out the loops go on without waiting
     if constexpr (KIND != 2) {
       uint32_t lut[4] = {0u, 0u, 0u, 0u};
@@ -602,7 +618,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
           ok = __all_sync(0xffffffffu, ok);
           uint8_t* base = smem + st * C::STAGE;
           if (pw == 0 && lane < 2) sh.ok[st][lane] = sh.raw_ok[slot][lane];
-#pragma unroll(C::MINE < 2 ? 1 : 2)
+#pragma unroll 1
           for (int u = 0; u < C::MINE; ++u) {
             const int item = u * C::PROD + pw, key0 = (item % KI) * C::KPI;
             const bool is_k = item < KI;
@@ -688,12 +704,12 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
       fast::cp_async_commit();
       fast::cp_async_wait<0>();  // nothing in flight when the block ends
     }
-  } else if (warp < C::SOFT + C::PROD + C::LOAD) {
+  } else if (warp >= 1 && warp <= C::LOAD) {
     // ------------------------------------------------------ loaders
     bool ok = true;
     if constexpr (KIND != 2) {
       constexpr int KI = kKeys / C::KPI;  // items of K (and of V)
-      const int lw = warp - C::SOFT - C::PROD;
+      const int lw = warp - 1;
       const int seg = lane % C::SEGS, key_l = lane / C::SEGS;
       auto load = [&](auto hb) {  // (the headers' size is fixed for the call)
         int slot = 0, ph = 1;
@@ -742,61 +758,71 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
         __syncwarp();
       }
     }
-  } else if (tiles) {
+  } else if ((warp == 0 || warp == 3) && tiles) {
     // ------------------------------------------------------ MMA issue
-    // (the whole warp walks the loop, one lane issues: operands stay uniform)
+    // A warp per tile of rows: what one does between its products (waiting,
+    // descriptors) runs under the other's.
+    const int i = warp == 0 ? 0 : 1;
     constexpr uint32_t id_qk = tc::idesc_f16(kKeys, false), id_pv = tc::idesc_f16(D, true);
-    const uint32_t t0 = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint32_t t0 = tmem;
     const uint32_t data = tc::smem_addr(smem);
-    const uint64_t k_desc = tc::smem_desc(data, 16, 1024);
-    const uint64_t v_desc = tc::smem_desc(data + (C::LO ? 2 : 1) * C::MAT, kKeys * 128, 1024);
-    auto qk = [&](int i, int st) {  // descriptors count 16 bytes
-      const uint64_t kd = k_desc + (uint32_t)(st * (C::STAGE / 16));
-      const uint32_t d = t0 + C::COL_S + i * kKeys, a = t0 + C::COL_Q + i * (D / 2);
+    constexpr uint32_t hi = tc::desc_hi(1024);
+    const uint32_t k_lo = tc::desc_lo(data, 16);
+    const uint32_t v_lo = tc::desc_lo(data + (C::LO ? 2 : 1) * C::MAT, kKeys * 128);
+    const uint32_t d_s = t0 + C::COL_S + i * kKeys, d_o = t0 + C::COL_O + i * D, a_q = t0 + C::COL_Q + i * (D / 2);
+    auto qk = [&](int st) {
+      const uint32_t kd = k_lo + st * (C::STAGE / 16);
       // hi, then lo: the tiles follow one another in 64-channel blocks
 #pragma unroll
       for (int n = 0; n < (C::LO ? 2 : 1) * (D / 64); ++n)
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          tc::mma_ts(d, a + ((n * 4) & (D / 16 - 1)) * 8 + kk * 8, kd + (uint32_t)(n * (kKeys * 128 / 16) + kk * 2),
-                     id_qk, n || kk);
+          tc::mma_ts(d_s, a_q + ((n * 4) & (D / 16 - 1)) * 8 + kk * 8, kd + n * (kKeys * 128 / 16) + kk * 2, hi, id_qk,
+                     n || kk);
       tc::commit(s_full(i));
     };
-    auto pv = [&](int i, int st, bool first, uint32_t then) {
-      const uint64_t vd = v_desc + (uint32_t)(st * (C::STAGE / 16));
-      const uint32_t d = t0 + C::COL_O + i * D, a = t0 + C::COL_S + i * kKeys;
-#pragma unroll
-      for (int kk = 0; kk < kKeys / 16; ++kk) tc::mma_ts(d, a + kk * 8, vd + kk * (2048 / 16), id_pv, !first || kk);
-      if (then) tc::commit(then);
+    auto wait = [&](uint32_t bar, int parity) { return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, stop)); };
+    // the warps take turns, so that one tile's softmax runs under the other
+    // tile's products and not beside its softmax
+    auto pass = [&] {
+      if (nq == 2 && lane == 0) tc::mbar_arrive(turn(1 - i));
+      __syncwarp();
     };
-    bool ok = __all_sync(0xffffffffu, tc::mbar_wait(full(0), 0, stop));
-    for (int i = 0; ok && i < nq; ++i) {
-      ok = __all_sync(0xffffffffu, tc::mbar_wait(q_full(i), 0, stop));
+    if (i < nq && wait(full(0), 0) && wait(q_full(i), 0) && (i == 0 || wait(turn(1), 0))) {
       tc::fence_after();
-      if (ok) qk(i, 0);
-    }
-    int st = 0, ph = 0;  // stage of key tile j and its phase
-    for (int j = 0; ok && j < tiles; ++j) {
-      const int st1 = st + 1 == C::STAGES ? 0 : st + 1, ph1 = st1 ? ph : ph ^ 1;
-      for (int i = 0; i < nq; ++i) {
-        ok = __all_sync(0xffffffffu, tc::mbar_wait(p_full(i), j & 1, stop));
+      qk(0);
+      pass();
+      int st = 0, ph = 0, tp = i;  // stage of key tile j and its phase; phase of the turn
+#pragma unroll 1
+      for (int j = 0;; ++j) {
+        const bool more = j + 1 < tiles;
+        const int st1 = st + 1 == C::STAGES ? 0 : st + 1, ph1 = st1 ? ph : ph ^ 1;
+        if (more && !wait(full(st1), ph1)) break;
+        if (!wait(p_full(i), j & 1)) break;
+        if (nq == 2 && !wait(turn(i), tp)) break;
+        tp ^= 1;
         tc::fence_after();
-        if (!ok) break;
-        const bool end_tile = i == nq - 1, end_key = j + 1 == tiles;
-        pv(i, st, j == 0, end_key ? o_full(i) : end_tile ? empty(st) : 0u);
-        if (end_key) continue;
-        if (i == 0) ok = __all_sync(0xffffffffu, tc::mbar_wait(full(st1), ph1, stop));
-        if (!ok) break;
-        qk(i, st1);
+        const uint32_t vd = v_lo + st * (C::STAGE / 16);
+#pragma unroll
+        for (int kk = 0; kk < kKeys / 16; ++kk)
+          tc::mma_ts(d_o, d_s + kk * 8, vd + kk * (2048 / 16), hi, id_pv, j || kk);
+        if (!more) {
+          tc::commit(o_full(i));
+          pass();
+          break;
+        }
+        qk(st1);
+        tc::commit(empty(st));
+        pass();
+        st = st1;
+        ph = ph1;
       }
-      st = st1;
-      ph = ph1;
     }
   }
   __syncwarp();
   tc::fence_before();
   __syncthreads();
-  if (warp == C::WARPS - 1) {
+  if (warp == 0) {
     tc::fence_after();
     tc::tmem_dealloc(tmem, C::COLS);
   }
