@@ -62,7 +62,7 @@ struct Cfg {
   static constexpr bool LO = KIND != 2;
   static constexpr int SOFT = 4 * NQ;             // softmax warps
   static constexpr int PROD = NQ == 1 || LO ? 8 : 4;  // producer warps
-  static constexpr int LOAD = LO ? 2 : 1;         // loader warps (fp16: the warp that passes stages on)
+  static constexpr int LOAD = 1;                  // loader warp (fp16: the warp that passes stages on)
   // warps 0 and 3 issue the MMAs, 1 .. LOAD load; softmax from 4 on (a warp reads
   // the tensor memory lanes of its number modulo 4), producers behind
   static constexpr int SOFT0 = 4, PROD0 = SOFT0 + SOFT, WARPS = PROD0 + PROD;
@@ -76,19 +76,19 @@ struct Cfg {
   static constexpr int KPI = 32 / SEGS;
   static constexpr int ITEMS = 2 * kKeys / KPI;   // of a tile
   static constexpr int MINE = ITEMS / PROD;       // of a warp and tile
-  // Codes and headers arrive in a ring of DEPTH tiles by asynchronous copies
-  // (one to three tiles of latency covered); fp16 rows go to their stage.
+  // Codes and headers arrive in a ring of DEPTH tiles by bulk copies (one to
+  // three tiles of latency covered); fp16 rows go to their stage.
   static constexpr int DEPTH = !LO ? 0 : D == 128 ? (BITS == 8 ? 3 : 4) : 6;
-  static constexpr int HDR = 512;                 // an item's scales, and its zeros 256 bytes on
-  static constexpr int RAW = LO ? 32 * 4 * BITS + HDR : 0;  // bytes of an item
-  // arrivals that fill a ring slot: the loaders' copies (fp16: the
-  // producers', straight into a stage) and the key masks; and a stage
-  static constexpr int RAW_FULL = (LO ? LOAD : PROD) * 32 + 1, FULL = LO ? PROD : 1;
+  static constexpr int CODES = LO ? kKeys * D * BITS / 8 : 0;  // bytes of a tile's K (or V) codes
+  static constexpr int HDR = kKeys * D / 4 + 16;  // most bytes of one header array, from a 16-byte boundary on
+  static constexpr int RAW = LO ? 2 * CODES + 4 * HDR : 0;     // K codes, V codes, K scale, K zero, V scale, V zero
+  // arrivals that fill a ring slot (fp16: a stage's copies and key masks), and a stage
+  static constexpr int RAW_FULL = LO ? 1 : PROD * 32 + 1, FULL = LO ? PROD : 1;
   static constexpr int SLOTS = LO ? DEPTH : STAGES;
   // tensor memory columns: per tile S (64, P in its place), O (D), Q (D / 2)
   static constexpr uint32_t COL_S = 0, COL_O = NQ * kKeys, COL_Q = COL_O + NQ * D;
   static constexpr uint32_t COLS = NQ == 2 ? 512 : 256;
-  static constexpr size_t SMEM = (size_t)STAGES * STAGE + (size_t)DEPTH * ITEMS * RAW + 1024 + 1024;
+  static constexpr size_t SMEM = (size_t)STAGES * STAGE + (size_t)DEPTH * RAW + 1024 + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory");
   static_assert(COL_Q + NQ * D / 2 <= COLS, "tensor memory");
   // channel held at place i of an eight-channel chunk (the unpacking leaves
@@ -120,99 +120,41 @@ struct Seg {
   uint32_t s[2], z[2];                // up to four fp16 scales and zeros
 };
 
-// Starts the copy of an item's codes and headers: this lane's segment of its
-// key's row (`row`, -1: none), and, spread over the lanes, the keys' headers
-// (2 * ngroups bytes each; row_k: the row of key lane % KPI).
-template <int BITS, int KIND, int D, int HB>
-__device__ __forceinline__ void copy_item(const ExtendParams& p, int which, long long row, long long row_k, int seg,
-                                          int lane, uint32_t dst) {
-  constexpr int KPI = 32 / (D / 32), SB = 4 * BITS;
-  const CacheGeom& c = p.v.geom;
-  const int a_codes = which ? KVQ_ARRAY_V_CODES : KVQ_ARRAY_K_CODES;
-  const uint8_t* src = p.v.codes[which] + max(row, 0ll) * (D * BITS / 8) + seg * SB;
-  const bool live = row >= 0 && KVQ_IN(c, a_codes, src, SB);
+// Reads one lane's segment from the ring: `codes` of the item's first key,
+// scales and zeros of its key.  Lanes of the upper 64 channels take their
+// chunks in the order 2, 3, 0, 1 (swap), so that the stores of a warp fall
+// into different banks.
+template <int BITS, int KIND, int NG>
+__device__ __forceinline__ void take_item(const uint8_t* codes, const uint8_t* s, const uint8_t* z, bool zeros,
+                                          int lane, bool swap, Seg<BITS>& x) {
+  constexpr int SB = 4 * BITS;
   if constexpr (SB == 8) {
-    fast::cp_async_small<8>(dst + lane * 8, src, live);
-  } else {
-#pragma unroll
-    for (int i = 0; i < SB / 16; ++i) fast::cp_async16(dst + lane * SB + i * 16, src + i * 16, live);
-  }
-  const bool zeros = lane >= KPI;
-  const int k = lane & (KPI - 1);
-  const int arr = zeros ? (which ? KVQ_ARRAY_V_ZERO : KVQ_ARRAY_K_ZERO)
-                        : (which ? KVQ_ARRAY_V_SCALE : KVQ_ARRAY_K_SCALE);
-  const __half* h = (zeros ? p.v.zero[which] : p.v.scale[which]) + max(row_k, 0ll) * (HB / 2);
-  const uint32_t to = dst + 32 * SB + (zeros ? 256 : 0);
-  const bool mine = lane < ((KIND == 0 && !c.sym) ? 2 * KPI : KPI);
-  const bool on = row_k >= 0 && mine && KVQ_IN(c, arr, h, HB);
-  if constexpr (HB >= 4) {
-    if (mine) {
-      if constexpr (HB == 4 || HB == 8) {
-        fast::cp_async_small<HB>(to + k * HB, h, on);
-      } else {
-        fast::cp_async16(to + k * HB, h, on);
-        if constexpr (HB == 32) fast::cp_async16(to + k * HB + 16, h + 8, on);
-      }
-    }
-  } else {
-    // One header of two bytes per key: copied by aligned words, which two
-    // consecutive rows share; a word whose other row is not this item's (or
-    // not in the cache) is taken in part.  Key k lies (row of key 0) & 1
-    // halves further on, and the key in a word's first half takes the word.
-    const int odd = (int)(__shfl_sync(0xffffffffu, max(row_k, 0ll), 0, KPI) & 1);
-    const long long next = __shfl_down_sync(0xffffffffu, row_k, 1, KPI);
-    const bool pair = k + 1 < KPI && next == row_k + 1;
-    if (mine && (((k + odd) & 1) == 0 || k == 0)) {
-      const __half* word = h - (row_k >= 0 ? (row_k & 1) : 0);
-      const int bytes = !on ? 0 : ((row_k & 1) || pair) ? 4 : 2;
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(to + ((k + odd) >> 1) * 4), "l"(word),
-                   "r"(bytes)
-                   : "memory");
-    }
-  }
-}
-
-// Reads one lane's segment back from the ring.  Lanes of the upper 64
-// channels take their chunks in the order 2, 3, 0, 1 (swap), so that the
-// stores of a warp fall into different banks.
-template <int BITS, int KIND, int D, int NG>
-__device__ __forceinline__ void take_item(const CacheGeom& c, const uint8_t* item, int lane, int odd, bool swap,
-                                          Seg<BITS>& x) {
-  constexpr int SEGS = D / 32, SB = 4 * BITS;
-  const int key = lane / SEGS, seg = lane % SEGS;
-  if constexpr (SB == 8) {
-    const uint2 t = *reinterpret_cast<const uint2*>(item + lane * 8);
+    const uint2 t = *reinterpret_cast<const uint2*>(codes + lane * 8);
     x.w[0] = swap ? t.y : t.x;
     x.w[1] = swap ? t.x : t.y;
   } else {
     uint32_t w[BITS];
 #pragma unroll
     for (int i = 0; i < SB / 16; ++i) {
-      const uint4 t = *reinterpret_cast<const uint4*>(item + lane * SB + i * 16);
+      const uint4 t = *reinterpret_cast<const uint4*>(codes + lane * SB + i * 16);
       w[4 * i] = t.x, w[4 * i + 1] = t.y, w[4 * i + 2] = t.z, w[4 * i + 3] = t.w;
     }
 #pragma unroll
     for (int i = 0; i < BITS; ++i) x.w[i] = swap ? w[(i + BITS / 2) % BITS] : w[i];
   }
-  const uint8_t* h = item + 32 * SB;
   x.s[0] = x.s[1] = x.z[0] = x.z[1] = 0;
-  const bool zeros = KIND == 0 && !c.sym;
   if constexpr (NG == 1) {
-    const int n = c.ngroups;  // the row's groups; this segment's is seg * 32 / g
-    const int at = n == 1 ? 2 * (key + odd) : key * 2 * n + 2 * (seg * 32 / c.g);
-    x.s[0] = *reinterpret_cast<const unsigned short*>(h + at);
-    if (zeros) x.z[0] = *reinterpret_cast<const unsigned short*>(h + 256 + at);
+    x.s[0] = *reinterpret_cast<const unsigned short*>(s);
+    if (zeros) x.z[0] = *reinterpret_cast<const unsigned short*>(z);
   } else if constexpr (NG == 2) {
-    const int at = lane * 4;
-    x.s[0] = *reinterpret_cast<const uint32_t*>(h + at);
-    if (zeros) x.z[0] = *reinterpret_cast<const uint32_t*>(h + 256 + at);
+    x.s[0] = *reinterpret_cast<const uint32_t*>(s);
+    if (zeros) x.z[0] = *reinterpret_cast<const uint32_t*>(z);
     if (swap) x.s[0] = fast::prmt_b32(x.s[0], 0u, 0x1032u), x.z[0] = fast::prmt_b32(x.z[0], 0u, 0x1032u);
   } else {
-    const int at = lane * 8;
-    uint2 t = *reinterpret_cast<const uint2*>(h + at);
+    uint2 t = *reinterpret_cast<const uint2*>(s);
     x.s[0] = swap ? t.y : t.x, x.s[1] = swap ? t.x : t.y;
     if (zeros) {
-      t = *reinterpret_cast<const uint2*>(h + 256 + at);
+      t = *reinterpret_cast<const uint2*>(z);
       x.z[0] = swap ? t.y : t.x, x.z[1] = swap ? t.x : t.y;
     }
   }
@@ -224,23 +166,26 @@ __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast
 // A group's conversion: d = q - z from the unpacked codes, hi = fp16(d s).
 struct Group {
   __half2 s, off, off16;  // scale; -(1024 + z); -(64 + z)
-  float sf, zf;
+  __half z;
   bool plain;             // 1024 + z a number that fp16 holds, no product beyond fp16
 };
 template <int BITS, int KIND>
 __device__ __forceinline__ Group group_of(uint32_t sw, uint32_t zw, int sym) {
   Group g;
-  const __half s = __ushort_as_half((unsigned short)(sw & 0xFFFFu));
-  g.s = __half2half2(s);
-  g.sf = __half2float(s);
-  g.zf = 0.f;
+  g.s = as_h2(fast::prmt_b32(sw, 0u, 0x1010u));
+  g.z = __ushort_as_half(0);
   g.plain = true;
   g.off = g.off16 = g.s;
   if constexpr (KIND == 0) {
-    g.zf = sym ? (float)(1 << (BITS - 1)) : __half2float(__ushort_as_half((unsigned short)(zw & 0xFFFFu)));
-    g.plain = fabsf(g.zf) <= 1024.f && g.sf * (fabsf(g.zf) + (float)((1 << BITS) - 1)) < 65504.f;
-    g.off = __half2half2(__float2half_rn(-1024.f - g.zf));
-    g.off16 = __half2half2(__float2half_rn(-64.f - g.zf));
+    // (symmetric codes: z = 2^(bits-1), as fp16)
+    constexpr uint32_t half_range = BITS == 2 ? 0x40004000u : BITS == 4 ? 0x48004800u : 0x58005800u;
+    const __half2 z = as_h2(sym ? half_range : fast::prmt_b32(zw, 0u, 0x1010u));
+    g.z = __low2half(z);
+    g.off = __hneg2(__hadd2(z, as_h2(fast::kH1024)));
+    g.off16 = __hneg2(__hadd2(z, as_h2(0x54005400u)));
+    const __half2 az = __habs2(z);
+    const __half2 most = __hmul2(__hadd2(az, as_h2(BITS == 8 ? 0x5BF85BF8u : BITS == 4 ? 0x4B804B80u : 0x42004200u)), g.s);
+    g.plain = __hle(__low2half(az), __ushort_as_half(0x6400)) && __hlt(__low2half(most), __ushort_as_half(0x7BD0));
   }
   return g;
 }
@@ -319,7 +264,7 @@ __device__ __forceinline__ void store_seg(const Seg<BITS>& x, bool is_k, int key
           const uint32_t c = BITS == 8   ? x.w[2 * ch + (q >> 2)] >> (8 * (q & 3))
                              : BITS == 4 ? x.w[ch] >> (4 * q)
                                          : x.w[ch >> 1] >> (16 * (ch & 1) + 2 * q);
-          a[e] = ((float)(c & ((1u << BITS) - 1u)) - gc.zf) * gc.sf;
+          a[e] = ((float)(c & ((1u << BITS) - 1u)) - __half2float(gc.z)) * __low2float(gc.s);
         }
         h[i] = pack_sat(a[0], a[1]);
         const float2 v = __half22float2(as_h2(h[i]));
@@ -346,7 +291,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
   pdl_launch_dependents();
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + ((1024 - (tc::smem_addr(raw) & 1023)) & 1023);
-  auto& sh = *reinterpret_cast<Shared<C::STAGES>*>(smem + C::STAGES * C::STAGE + C::DEPTH * C::ITEMS * C::RAW);
+  auto& sh = *reinterpret_cast<Shared<C::STAGES>*>(smem + C::STAGES * C::STAGE + C::DEPTH * C::RAW);
   const CacheGeom& c = p.v.geom;
   const int warp = tc::uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int kvh = blockIdx.y, b = blockIdx.z;
@@ -410,6 +355,9 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
   tc::fence_after();
   const uint32_t tmem = tc::uniform(sh.tmem);
 
+  // where a dense header array's rows begin in their first 16 bytes (the same for every tile)
+  const int mis = c.layout == KVQ_DENSE
+                      ? (int)((((long long)b * c.Hkv + kvh) * c.slots + k0) * (2 * c.ngroups) & 15) : 0;
   // row of a position of this split: -1 behind its end, -2 unmapped
   auto row_of = [&](int pos) -> long long {
     if (pos >= k1) return -1;
@@ -608,6 +556,8 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
       constexpr int KI = kKeys / C::KPI;  // items of K (and of V)
       const int seg = lane % C::SEGS, key_l = lane / C::SEGS;
       const int swap = seg >= 2 ? 2 : 0;
+      const bool zeros = KIND == 0 && !c.sym;
+      const int hb = 2 * c.ngroups, hseg = 2 * (seg * 32 / c.g);
       // (NG, groups per segment, is fixed for the call: one small loop runs)
       auto convert = [&](auto ng) {
         constexpr int NG = decltype(ng)::value;
@@ -617,18 +567,22 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
           if (ok) ok = tc::mbar_wait(raw_full(slot), rph, stop) && tc::mbar_wait(empty(st), ph, stop);
           ok = __all_sync(0xffffffffu, ok);
           uint8_t* base = smem + st * C::STAGE;
-          if (pw == 0 && lane < 2) sh.ok[st][lane] = sh.raw_ok[slot][lane];
+          const uint8_t* ring = smem + C::STAGES * C::STAGE + slot * C::RAW;
+          const uint32_t ok0 = sh.raw_ok[slot][0], ok1 = sh.raw_ok[slot][1];
+          if (pw == 0 && lane == 0) sh.ok[st][0] = ok0, sh.ok[st][1] = ok1;
+          const bool all = (ok0 & ok1) == 0xFFFFFFFFu;
 #pragma unroll 1
           for (int u = 0; u < C::MINE; ++u) {
-            const int item = u * C::PROD + pw, key0 = (item % KI) * C::KPI;
+            const int item = u * C::PROD + pw, key0 = (item % KI) * C::KPI, key = key0 + key_l;
             const bool is_k = item < KI;
-            const uint8_t* raw_item = smem + C::STAGES * C::STAGE + (slot * C::ITEMS + item) * C::RAW;
-            const int pos0 = k0 + j * kKeys + key0;
-            const int odd = c.layout == KVQ_DENSE && pos0 < k1 ? (((b * c.Hkv + kvh) & c.slots) ^ pos0) & 1 : 0;
+            const uint8_t* h = ring + 2 * C::CODES + (is_k ? 0 : 2 * C::HDR) + mis + key * hb + hseg;
             Seg<BITS> x;
-            take_item<BITS, KIND, D, NG>(c, raw_item, lane, odd, swap, x);
-            store_seg<BITS, KIND, NG>(x, is_k, key0 + key_l, seg, c.sym, swap, base + (is_k ? 0 : 2 * C::MAT),
-                                      base + C::MAT, lut);
+            take_item<BITS, KIND, NG>(ring + (is_k ? 0 : C::CODES) + key0 * (D * BITS / 8), h, h + C::HDR, zeros, lane,
+                                      swap, x);
+            if (!all && !((key < 32 ? ok0 : ok1) >> (key & 31) & 1u))  // not a key: zeros, whatever the ring held
+              x.s[0] = x.s[1] = x.z[0] = x.z[1] = 0;
+            store_seg<BITS, KIND, NG>(x, is_k, key, seg, c.sym, swap, base + (is_k ? 0 : 2 * C::MAT), base + C::MAT,
+                                      lut);
           }
           tc::fence_async_shared();
           __syncwarp();
@@ -708,43 +662,95 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
     // ------------------------------------------------------ loaders
     bool ok = true;
     if constexpr (KIND != 2) {
-      constexpr int KI = kKeys / C::KPI;  // items of K (and of V)
-      const int lw = warp - 1;
-      const int seg = lane % C::SEGS, key_l = lane / C::SEGS;
-      auto load = [&](auto hb) {  // (the headers' size is fixed for the call)
-        int slot = 0, ph = 1;
+      // A tile's rows come in runs of consecutive rows: one in a dense cache,
+      // one per page in a paged one.  Lane: array a of run r, r + 4, ...
+      const int a = lane & 7;  // K codes, V codes, K scale, K zero, V scale, V zero
+      const int hb = 2 * c.ngroups;
+      const bool have = a < 2 || a == 2 || a == 4 || (a < 6 && KIND == 0 && !c.sym);
+      const int which = a < 2 ? a : min((a - 2) >> 1, 1);
+      const uint8_t* array = a < 2 ? p.v.codes[which]
+                                   : reinterpret_cast<const uint8_t*>((a & 1) ? p.v.zero[which] : p.v.scale[which]);
+      const int size = a < 2 ? D * BITS / 8 : hb;  // bytes of a row
+      const int kind = a < 2 ? KVQ_ARRAY_K_CODES + which
+                             : (which ? KVQ_ARRAY_V_SCALE : KVQ_ARRAY_K_SCALE) + (a & 1);
+      const uint32_t place = a < 2 ? which * C::CODES : 2 * C::CODES + (a - 2) * C::HDR + mis;
+      int slot = 0, ph = 1, j = 0;
 #pragma unroll 1
-        for (int j = 0; j < tiles; ++j) {
-          long long row_k[KI / C::LOAD];  // this lane's header row of each item
+      for (; j < tiles; ++j) {
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(raw_empty(slot), ph, stop));
+        if (!ok) break;
+        const int p0 = k0 + j * kKeys, p1 = min(p0 + kKeys, k1);
+        const uint32_t dst = tc::smem_addr(smem + C::STAGES * C::STAGE + slot * C::RAW);
+        uint8_t* const at = smem + C::STAGES * C::STAGE + slot * C::RAW;
+        const uint8_t* src[3];
+        uint32_t to[3], bytes[3], total = 0;
+        uint32_t dead0 = 0, dead1 = 0;  // keys without a row
 #pragma unroll
-          for (int u = 0; u < KI / C::LOAD; ++u)
-            row_k[u] = row_of(k0 + j * kKeys + (u * C::LOAD + lw) * C::KPI + (lane & (C::KPI - 1)));
-          if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(raw_empty(slot), ph, stop));
-          const uint32_t dst = tc::smem_addr(smem + C::STAGES * C::STAGE + slot * C::ITEMS * C::RAW);
-#pragma unroll
-          for (int u = 0; u < KI / C::LOAD; ++u) {
-            const int i = u * C::LOAD + lw;
-            const long long row = __shfl_sync(0xffffffffu, row_k[u], key_l);
-            copy_item<BITS, KIND, D, decltype(hb)::value>(p, 0, row, row_k[u], seg, lane, dst + i * C::RAW);
-            copy_item<BITS, KIND, D, decltype(hb)::value>(p, 1, row, row_k[u], seg, lane, dst + (KI + i) * C::RAW);
+        for (int u = 0; u < 3; ++u) {
+          const int r = u * 4 + (lane >> 3);
+          int start = p0, end = p1;
+          if (c.layout == KVQ_PAGED) {
+            const int blk = p0 / c.slots + r;
+            start = max(p0, blk * c.slots);
+            end = min(p1, (blk + 1) * c.slots);
+          } else if (r) {
+            start = p1;
           }
-          tc::mbar_arrive_copies(raw_full(slot));
-          if (lw == 0) {
-            note_keys(sh.raw_ok[slot], j);
-            if (lane == 0) tc::mbar_arrive(raw_full(slot));
+          bytes[u] = 0;
+          if (start >= end) continue;
+          const long long row = token_row(c, b, kvh, start);
+          int rows = end - start;
+          const uint8_t* from = array + max(row, 0ll) * size;
+          bool live = row >= 0;
+          if (live && have && !KVQ_IN(c, kind, from, (long long)rows * size)) live = false;
+          if (!live) {
+            const int k = start - p0, n = end - p0;  // keys k .. n - 1
+            dead0 |= (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u) & ~(k >= 32 ? 0xFFFFFFFFu : (1u << k) - 1u);
+            dead1 |= (n > 32 ? (n >= 64 ? 0xFFFFFFFFu : (1u << (n - 32)) - 1u) : 0u) &
+                     ~(k > 32 ? (1u << (k - 32)) - 1u : 0u);
+            if (row < 0 && p.status) atomicOr(p.status, KVQ_FLAG_BLOCK_TABLE);
+            continue;
           }
-          if (++slot == C::DEPTH) slot = 0, ph ^= 1;
+          if (!have) continue;
+          // Whole 16-byte pieces.  In a page that is rows rounded up to 8 (the
+          // page has them); a dense header array starts mis bytes into one,
+          // and what its last piece holds is copied by hand.
+          src[u] = from;
+          to[u] = dst + place + (start - p0) * size;
+          if (c.layout == KVQ_PAGED) {
+            bytes[u] = ((rows + 7) & ~7) * size;
+          } else if (a < 2) {
+            bytes[u] = rows * size;
+          } else {
+            const int n = mis + rows * size;
+            src[u] -= mis;
+            to[u] -= mis;
+            bytes[u] = n & ~15;
+            for (int x = max(n & ~15, mis); x < n; x += 2)
+              *reinterpret_cast<unsigned short*>(at + place - mis + x) =
+                  *reinterpret_cast<const unsigned short*>(src[u] + x);
+          }
+          total += bytes[u];
         }
-      };
-      switch (c.ngroups) {
-        case 1: load(Int<2>{}); break;
-        case 2: load(Int<4>{}); break;
-        case 4: load(Int<8>{}); break;
-        case 8: load(Int<16>{}); break;
-        default: load(Int<32>{}); break;
+        total = __reduce_add_sync(0xffffffffu, total);
+        dead0 = __reduce_or_sync(0xffffffffu, dead0);
+        dead1 = __reduce_or_sync(0xffffffffu, dead1);
+        const int n = p1 - p0;
+        if (lane == 0) {
+          sh.raw_ok[slot][0] = (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u) & ~dead0;
+          sh.raw_ok[slot][1] = (n > 32 ? (n >= 64 ? 0xFFFFFFFFu : (1u << (n - 32)) - 1u) : 0u) & ~dead1;
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive_expect(raw_full(slot), total);
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < 3; ++u)
+          if (bytes[u]) tc::bulk_load(to[u], src[u], bytes[u], raw_full(slot));
+        if (++slot == C::DEPTH) slot = 0, ph ^= 1;
       }
-      fast::cp_async_commit();
-      fast::cp_async_wait<0>();  // nothing in flight when the block ends
+      // after a wait that ran out: nothing in flight when the block ends
+      if (!ok)
+        for (int t = max(j - C::DEPTH, 0); t < j; ++t) tc::mbar_drain(raw_full(t % C::DEPTH), (t / C::DEPTH) & 1);
     } else {
       // The rows of a stage have landed: make them visible to the tensor core
       // and pass the stage on.  (Not the producers' job: the fence would wait
@@ -811,8 +817,8 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
           pass();
           break;
         }
-        qk(st1);
         tc::commit(empty(st));
+        qk(st1);
         pass();
         st = st1;
         ph = ph1;
