@@ -404,9 +404,9 @@ KVQ_API kvq_status kvq_rope_init(const kvq_rope_desc* desc, kvq_rope* rope);
  *                    position seq_lens_before[b] + t.
  * head_dim is a multiple of 8, rotary_dim <= head_dim <= 256.  x_out is x
  * itself (in place) or does not overlap it.  The angle is that of turns[]
- * exactly; cos, sin and the products carry 2^-44, and y is rounded once, so
+ * exactly; cos, sin and the products carry 2^-42, and y is rounded once, so
  * it is the nearest fp16 to the formula's value unless that lies within
- * 2^-44 (|x0| + |x1|) of a tie.  An infinity or NaN in x gives one in y.
+ * 2^-42 (|x0| + |x1|) of a tie.  An infinity or NaN in x gives one in y.
  */
 KVQ_API kvq_status kvq_rope_apply(const kvq_rope* rope, int32_t head_dim, int32_t batch,
                           int32_t num_new, int32_t num_q_heads, const uint16_t* q,

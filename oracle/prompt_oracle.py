@@ -55,12 +55,13 @@ def rope_rotate(x16, positions, ws, amp, rd, interleaved):
     x16 fp16 [..., H, D], positions integer [...]; one position per H rows.
     The angle position * w carries the roundings of w and of the product, up
     to 2^-50 of itself; the library's w is a whole number of 2^-64 turns, so
-    its angle may differ by position * pi 2^-64 more."""
+    its angle may differ by position * pi 2^-64 more, and it works the turn out
+    to 2^-42."""
     x = np.asarray(x16, dtype=np.float64)
     pos = np.asarray(positions, dtype=np.float64)[..., None]
     angle = pos * ws
     c, s = (amp * np.cos(angle))[..., None, :], (amp * np.sin(angle))[..., None, :]
-    own = (np.abs(angle) * 2.0 ** -50 + np.abs(pos) * math.pi * 2.0 ** -64 + 2.0 ** -44)[..., None, :] * amp
+    own = (np.abs(angle) * 2.0 ** -50 + np.abs(pos) * math.pi * 2.0 ** -64 + 2.0 ** -42)[..., None, :] * amp
     y, err = x.copy(), np.zeros_like(x)
     if interleaved:
         a, b = x[..., 0:rd:2], x[..., 1:rd:2]

@@ -258,7 +258,7 @@ kvq_status kvq_cache_read(const kvq_cache_desc* desc, const kvq_cache* cache, in
   if ((st = check_cache(desc, cache)) != KVQ_OK) return st;
   if (batch < 0 || num_rows < 0) return KVQ_ERR_INVALID_ARG;
   if (batch == 0 || num_rows == 0 || (!k_out && !v_out)) return KVQ_OK;
-  if ((int64_t)batch * num_rows * desc->num_kv_heads * (desc->head_dim / 8) > (int64_t)INT32_MAX * 128)
+  if (too_many_rows(batch, num_rows, desc->num_kv_heads))
     return KVQ_ERR_UNSUPPORTED;
   if (!seq_lens || !start) return KVQ_ERR_INVALID_ARG;
   if (!aligned(seq_lens) || !aligned(start) || !aligned(k_out) || !aligned(v_out))

@@ -74,12 +74,12 @@ __device__ __forceinline__ uint4 load8(const CacheView& v, int which, int b, int
         w1 = t.y;
       }
     }
-    float x[8];
+    float x[8];  // the code as the last bits of 2^23 + code
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const uint32_t q = BITS == 8 ? ((e < 4 ? w0 >> (8 * e) : w1 >> (8 * (e - 4))) & 255u)
+      const uint32_t q = BITS == 8 ? __byte_perm(e < 4 ? w0 : w1, 0u, 0x4440 + (e & 3))
                                    : ((w0 >> (BITS * e)) & ((1u << BITS) - 1u));
-      x[e] = (float)q;
+      x[e] = __uint_as_float(q | 0x4B000000u) - 8388608.f;
     }
     const int a_scale = which ? KVQ_ARRAY_V_SCALE : KVQ_ARRAY_K_SCALE;
     const int a_zero = which ? KVQ_ARRAY_V_ZERO : KVQ_ARRAY_K_ZERO;

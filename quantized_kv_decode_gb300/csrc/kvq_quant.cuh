@@ -7,10 +7,10 @@
 // codes per byte with the even channel in the low nibble.
 //
 // Arithmetic (fixed so that codes are reproducible bit for bit):
-//   range = max - min            fp64 (exact for two fp16 values)
+//   range = max - min            in whole units of 2^-24 (exact)
 //   s     = the smallest fp16 with s * (2^b - 1) >= range (range / (2^b - 1)
-//           rounded toward +inf): an fp32 estimate, then exact fp64 checks
-//   z     = rint(-min / s)       fp32 IEEE division, round half to even,
+//           rounded toward +inf): an fp32 estimate, then exact integer checks
+//   z     = rint(-min / s)       quotient rounded to fp32, round half to even,
 //                                clamped to +-2048 (flagged) and stored as an
 //                                integer (+0, never -0)
 //   q     = clamp(rint(x / s) + z, 0, 2^b - 1)
@@ -25,21 +25,40 @@ namespace kvq {
 
 namespace quant_detail {
 
-__device__ __forceinline__ double half_bits_value(unsigned short h) {
-  return (double)__half2float(__ushort_as_half(h));
+// A non-negative fp16 value, by its bits, in units of 2^-24 (below 2^41).
+__device__ __forceinline__ long long half_units(unsigned short h) {
+  const int e = h >> 10, m = h & 0x3ff;
+  return e ? (long long)(m | 0x400) << (e - 1) : m;
+}
+// An fp16 value held as fp32, in units of 2^-24 (exact).
+__device__ __forceinline__ long long value_units(float f) {
+  const unsigned short h = __half_as_ushort(__float2half_rn(f));
+  const long long u = half_units(h & 0x7fff);
+  return (h & 0x8000) ? -u : u;
 }
 
-// smallest fp16 s > 0 with s * qmax >= range, for 0 < range <= 2 * 65504
-__device__ __forceinline__ __half scale_round_up(double range, int qmax) {
+// smallest fp16 s > 0 with s * qmax >= range, for 0 < range <= 2 * 65504 in
+// units of 2^-24 (whole numbers: every fp16 value is one, and so the
+// comparisons are exact)
+__device__ __forceinline__ __half scale_round_up(long long range, float range_f, int qmax) {
   unsigned short h;
-  const float est = (float)range / (float)qmax;
+  const float est = range_f / (float)qmax;
   asm("cvt.rp.f16.f32 %0, %1;" : "=h"(h) : "f"(est));
   // the estimate is within one fp16 step of the answer; settle it exactly
-  // (h * qmax is exact in fp64: 11-bit significand times an 8-bit integer)
-  if (half_bits_value(h) * qmax < range) h = (unsigned short)(h + 1);
-  if (h > 1 && half_bits_value((unsigned short)(h - 1)) * qmax >= range)
+  if (half_units(h) * qmax < range) h = (unsigned short)(h + 1);
+  if (h > 1 && half_units((unsigned short)(h - 1)) * qmax >= range)
     h = (unsigned short)(h - 1);
   return __ushort_as_half(h);
+}
+
+// x / s correctly rounded to fp32, for fp16 values x and s > 0 and r = 1/s
+// rounded: q0 = x r is off by 2^-23 at most, the remainder x - q0 s is exact
+// in the fma (12 bits are left of 35), and q0 + rem r is within 2^-47 of the
+// quotient before its one rounding.  A quotient of two 11-bit numbers is at
+// least 2^-36 away from a tie of fp32 roundings, so it rounds as the quotient.
+__device__ __forceinline__ float div_by(float x, float s, float r) {
+  const float q0 = __fmul_rn(x, r);
+  return __fmaf_rn(__fmaf_rn(-q0, s, x), r, q0);
 }
 
 }  // namespace quant_detail
@@ -49,6 +68,7 @@ __device__ __forceinline__ __half scale_round_up(double range, int qmax) {
 struct GroupParams {
   __half s, z;     // stored scale and zero-point
   float sf, zf;    // the same as fp32 (zf an integer)
+  float rs;        // 1 / sf
   uint32_t flags;  // KVQ_FLAG_ZERO_CLAMPED / KVQ_FLAG_NONFINITE
   bool finite;
 };
@@ -61,20 +81,22 @@ __device__ __forceinline__ GroupParams group_params(float mn, float mx, bool fin
   r.z = __ushort_as_half(0);
   r.sf = 0.f;
   r.zf = 0.f;
+  r.rs = 0.f;
   r.flags = 0;
   r.finite = finite;
   if (!finite) {
     r.flags = KVQ_FLAG_NONFINITE;
     return r;
   }
-  const double range = (double)mx - (double)mn;
-  if (range == 0.0) {
+  if (mx == mn) {
     r.s = __float2half_rn(mn == 0.f ? 1.f : fabsf(mn));
   } else {
-    r.s = quant_detail::scale_round_up(range, QMAX);
+    const long long range = quant_detail::value_units(mx) - quant_detail::value_units(mn);
+    r.s = quant_detail::scale_round_up(range, __fadd_rn(mx, -mn), QMAX);
   }
   r.sf = __half2float(r.s);
-  float zf = rintf(__fdiv_rn(-mn, r.sf));
+  r.rs = __frcp_rn(r.sf);
+  float zf = rintf(quant_detail::div_by(-mn, r.sf, r.rs));
   if (fabsf(zf) > 2048.f) {
     r.flags |= KVQ_FLAG_ZERO_CLAMPED;
     zf = fminf(fmaxf(zf, -2048.f), 2048.f);
@@ -90,7 +112,7 @@ template <int BITS>
 __device__ __forceinline__ uint32_t group_encode(float x, const GroupParams& gp) {
   constexpr int QMAX = (1 << BITS) - 1;
   if (!gp.finite) return 0u;
-  const float tq = rintf(__fdiv_rn(x, gp.sf)) + gp.zf;
+  const float tq = rintf(quant_detail::div_by(x, gp.sf, gp.rs)) + gp.zf;
   return (uint32_t)fminf(fmaxf(tq, 0.f), (float)QMAX);
 }
 
@@ -139,18 +161,20 @@ __device__ __forceinline__ Quant8 quantize8(const uint4 v, int tpg) {
   r.w1 = 0;
   if constexpr (SYM) {
     r.z = __int2half_rn(HALF);
-    float sf = 0.f;
+    float sf = 0.f, rs = 0.f;
     if (!finite) {
       r.flags |= KVQ_FLAG_NONFINITE;
     } else {
       const float a = fmaxf(fabsf(mn), fabsf(mx));
-      r.s = (a == 0.f) ? __float2half_rn(1.f) : quant_detail::scale_round_up((double)a, HALF - 1);
+      r.s = (a == 0.f) ? __float2half_rn(1.f)
+                       : quant_detail::scale_round_up(quant_detail::value_units(a), a, HALF - 1);
       sf = __half2float(r.s);
+      rs = __frcp_rn(sf);
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       float t = 0.f;
-      if (finite) t = fminf(fmaxf(rintf(__fdiv_rn(__half2float(h[k]), sf)), (float)-HALF), (float)(HALF - 1));
+      if (finite) t = fminf(fmaxf(rintf(quant_detail::div_by(__half2float(h[k]), sf, rs)), (float)-HALF), (float)(HALF - 1));
       const uint32_t q = (uint32_t)(int)(t + (float)HALF);
       if constexpr (BITS == 2) {
         r.w0 |= q << (2 * k);
@@ -210,9 +234,10 @@ __device__ __forceinline__ Quant8 quantize8_nf4(const uint4 v, int tpg, const fl
   r.w0 = 0;
   r.w1 = 0;
   if (live) {
+    const float ra = __frcp_rn(a);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const float t = __fdiv_rn(__half2float(h[k]), a);
+      const float t = quant_detail::div_by(__half2float(h[k]), a, ra);
       uint32_t q = 0;
 #pragma unroll
       for (int i = 0; i < 15; ++i) q += (mid[i] < t) ? 1u : 0u;

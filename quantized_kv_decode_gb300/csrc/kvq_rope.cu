@@ -54,68 +54,33 @@ __device__ __forceinline__ void fill_turns(const RopeParams& p, long long first,
   __syncthreads();
 }
 
+// ---- the general form: any even rotary_dim -------------------------------
+
 // Rotates rows r0, r0 + step, ... of one token's [heads][D] block: each row
-// is cut into items, VEC: pairs of 8-channel chunks (or one chunk of 4
-// interleaved pairs), else single pairs; then the channels behind the
-// rotated ones, copied unless in place.  An item's inputs are read before
-// its outputs are written and no other item touches them, so src may be dst.
-template <bool VEC>
-__device__ __forceinline__ void rotate_rows(const RopeParams& p, const Turn* turns,
-                                            const __half* src, __half* dst, int heads, int item,
-                                            int items, int r0, int step) {
+// is cut into items, the pairs and then the channels behind them, copied
+// unless in place.  An item's inputs are read before its outputs are written
+// and no other item touches them, so src may be dst.
+__device__ __forceinline__ void rotate_rows(const RopeParams& p, const Turn* turns, const __half* src, __half* dst,
+                                            int heads, int item, int r0, int step) {
   const int rd = p.rope.rotary_dim, pairs = rd >> 1;
   const bool inter = p.rope.interleaved != 0;
-  const int per = VEC ? 8 : 1;  // channels of a pass-through item
-  const int rot = VEC ? (inter ? rd / 8 : rd / 16) : pairs;
   for (int row = r0; row < heads; row += step) {
     const __half* s = src + (long long)row * p.D;
     __half* d = dst + (long long)row * p.D;
-    if (item < rot) {
-      if constexpr (VEC) {
-        uint4 v[2], o[2];
-        const int c0 = inter ? item * 8 : item * 8, c1 = c0 + pairs;
-        v[0] = *reinterpret_cast<const uint4*>(s + c0);
-        const __half* x = reinterpret_cast<const __half*>(v);
-        __half* y = reinterpret_cast<__half*>(o);
-        if (inter) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            rope::rotate_exact(turns[item * 4 + e], x[2 * e], x[2 * e + 1], y[2 * e], y[2 * e + 1]);
-          *reinterpret_cast<uint4*>(d + c0) = o[0];
-        } else {
-          v[1] = *reinterpret_cast<const uint4*>(s + c1);
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            rope::rotate_exact(turns[c0 + e], x[e], x[8 + e], y[e], y[8 + e]);
-          *reinterpret_cast<uint4*>(d + c0) = o[0];
-          *reinterpret_cast<uint4*>(d + c1) = o[1];
-        }
-      } else {
-        const int c0 = inter ? 2 * item : item, c1 = inter ? c0 + 1 : c0 + pairs;
-        __half y0, y1;
-        rope::rotate_exact(turns[item], s[c0], s[c1], y0, y1);
-        d[c0] = y0;
-        d[c1] = y1;
-      }
+    if (item < pairs) {
+      const int c0 = inter ? 2 * item : item, c1 = inter ? c0 + 1 : c0 + pairs;
+      __half y0, y1;
+      rope::rotate_exact(turns[item], s[c0], s[c1], y0, y1);
+      d[c0] = y0;
+      d[c1] = y1;
     } else if (s != d) {
-      const int c = rd + (item - rot) * per;
-      if constexpr (VEC) *reinterpret_cast<uint4*>(d + c) = *reinterpret_cast<const uint4*>(s + c);
-      else d[c] = s[c];
+      d[pairs + item] = s[pairs + item];
     }
   }
 }
-
-// items of a row, and whether the vector form applies (rotated part a whole
-// number of chunks on both sides)
-__device__ __host__ __forceinline__ bool rope_vec(int rd, bool inter) {
-  return inter ? rd % 8 == 0 : rd % 16 == 0;
-}
-__device__ __forceinline__ int rope_items(int rd, bool inter, int D, bool vec) {
-  return vec ? (inter ? rd / 8 : rd / 16) + (D - rd) / 8 : (rd >> 1) + (D - rd);
-}
+__device__ __forceinline__ int rope_items(const RopeParams& p) { return p.D - (p.rope.rotary_dim >> 1); }
 
 // Grid: x = groups of `tokens` tokens, y = slices of the rows of a token.
-template <bool VEC>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p, int tokens) {
   pdl_launch_dependents();
   pdl_wait();
@@ -126,7 +91,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   const int count = (int)min((long long)tokens, total - first);
   fill_turns(p, first, count, turns, toks);
   const int pairs = p.rope.rotary_dim >> 1;
-  const int items = rope_items(p.rope.rotary_dim, p.rope.interleaved != 0, p.D, VEC);
+  const int items = rope_items(p);  // at most 255
   const int rows = kThreads / items;  // rows per pass
   const int r = threadIdx.x / items;
   if (r >= rows) return;
@@ -135,57 +100,36 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     if (!toks[k].live) continue;
     const long long at = first + k;
     if (p.Hq)
-      rotate_rows<VEC>(p, turns + k * pairs, p.q + at * p.Hq * p.D, p.q_out + at * p.Hq * p.D, p.Hq,
-                       item, items, r + rows * blockIdx.y, rows * gridDim.y);
+      rotate_rows(p, turns + k * pairs, p.q + at * p.Hq * p.D, p.q_out + at * p.Hq * p.D, p.Hq, item,
+                  r + rows * blockIdx.y, rows * gridDim.y);
     if (p.Hk)
-      rotate_rows<VEC>(p, turns + k * pairs, p.k + at * p.Hk * p.D, p.k_out + at * p.Hk * p.D, p.Hk,
-                       item, items, r + rows * blockIdx.y, rows * gridDim.y);
+      rotate_rows(p, turns + k * pairs, p.k + at * p.Hk * p.D, p.k_out + at * p.Hk * p.D, p.Hk, item,
+                  r + rows * blockIdx.y, rows * gridDim.y);
   }
 }
 
 // The 8 channels of chunk `ch` of a rotated row.
-template <bool VEC>
-__device__ __forceinline__ uint4 rotated_chunk(const RopeParams& p, const CacheGeom& c,
-                                               const Turn* turns, const __half* row, int ch) {
+__device__ __forceinline__ uint4 rotated_chunk(const RopeParams& p, const CacheGeom& c, const Turn* turns,
+                                               const __half* row, int ch) {
   const int rd = p.rope.rotary_dim, pairs = rd >> 1;
   const bool inter = p.rope.interleaved != 0;
-  uint4 v[2];
-  v[0] = make_uint4(0u, 0u, 0u, 0u);
-  v[1] = v[0];
+  uint4 v = make_uint4(0u, 0u, 0u, 0u);
   const uint4* own = reinterpret_cast<const uint4*>(row) + ch;
-  if (KVQ_IN(c, KVQ_ARRAY_K_NEW, own, 16)) v[0] = __ldg(own);
-  if (ch * 8 >= rd) return v[0];
-  uint4 o;
+  if (KVQ_IN(c, KVQ_ARRAY_K_NEW, own, 16)) v = __ldg(own);
+  uint4 o = v;
   __half* y = reinterpret_cast<__half*>(&o);
-  const __half* x = reinterpret_cast<const __half*>(v);
+  const __half* x = reinterpret_cast<const __half*>(&v);
   __half skip;
-  if constexpr (VEC) {
-    if (inter) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        rope::rotate_exact(turns[ch * 4 + e], x[2 * e], x[2 * e + 1], y[2 * e], y[2 * e + 1]);
-    } else {
-      const bool upper = ch * 8 >= pairs;
-      const uint4* oth = reinterpret_cast<const uint4*>(row + ch * 8 + (upper ? -pairs : pairs));
-      if (KVQ_IN(c, KVQ_ARRAY_K_NEW, oth, 16)) v[1] = __ldg(oth);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (upper) rope::rotate_exact(turns[ch * 8 - pairs + e], x[8 + e], x[e], skip, y[e]);
-        else rope::rotate_exact(turns[ch * 8 + e], x[e], x[8 + e], y[e], skip);
-      }
-    }
-  } else {
-    for (int e = 0; e < 8; ++e) {
-      const int d = ch * 8 + e;
-      y[e] = x[e];
-      if (d >= rd) continue;
-      const bool second = inter ? (d & 1) : d >= pairs;
-      const int i = inter ? d >> 1 : (second ? d - pairs : d);
-      const __half* op = row + (inter ? (d ^ 1) : (second ? i : d + pairs));
-      const __half other = KVQ_IN(c, KVQ_ARRAY_K_NEW, op, 2) ? *op : __ushort_as_half(0);
-      if (second) rope::rotate_exact(turns[i], other, x[e], skip, y[e]);
-      else rope::rotate_exact(turns[i], x[e], other, y[e], skip);
-    }
+  for (int e = 0; e < 8; ++e) {
+    const int d = ch * 8 + e;
+    if (d >= rd) continue;
+    const bool second = inter ? (d & 1) : d >= pairs;
+    const int i = inter ? d >> 1 : (second ? d - pairs : d);
+    const __half* op = row + (inter ? (d ^ 1) : (second ? i : d + pairs));
+    const __half other = KVQ_IN(c, KVQ_ARRAY_K_NEW, op, 2) ? *op : __ushort_as_half(0);
+    if (second) rope::rotate_exact(turns[i], other, x[e], skip, y[e]);
+    else rope::rotate_exact(turns[i], x[e], other, y[e], skip);
   }
   return o;
 }
@@ -193,7 +137,7 @@ __device__ __forceinline__ uint4 rotated_chunk(const RopeParams& p, const CacheG
 // Grid as rope_kernel.  K rows are rotated and quantized, V rows quantized
 // (quantize8, as in append_kernel: a thread per 8 channels, a group's lanes
 // adjacent), q rows rotated.  KIND: 0 asymmetric, 1 symmetric, 2 NF4.
-template <int BITS, int KIND, bool VEC>
+template <int BITS, int KIND>
 __global__ void __launch_bounds__(kThreads)
     rope_append_kernel(const __grid_constant__ RopeAppendParams pp, int tokens) {
   pdl_launch_dependents();
@@ -239,7 +183,7 @@ __global__ void __launch_bounds__(kThreads)
         const uint4* sp = reinterpret_cast<const uint4*>(src) + ch;
         if (KVQ_IN(c, KVQ_ARRAY_V_NEW, sp, 16)) v = __ldg(sp);
       } else {
-        v = rotated_chunk<VEC>(p, c, turns + k * pairs, src, ch);
+        v = rotated_chunk(p, c, turns + k * pairs, src, ch);
       }
     }
     const int a_codes = which ? KVQ_ARRAY_V_CODES : KVQ_ARRAY_K_CODES;
@@ -270,15 +214,235 @@ __global__ void __launch_bounds__(kThreads)
   if (flags && p.status) atomicOr(p.status, flags);
 
   if (p.Hq) {
-    const int items = rope_items(p.rope.rotary_dim, p.rope.interleaved != 0, p.D, VEC);
+    const int items = rope_items(p);
     const int qrows = kThreads / items, r = threadIdx.x / items;
     if (r >= qrows) return;
     for (int k = 0; k < count; ++k)
       if (toks[k].live)
-        rotate_rows<VEC>(p, turns + k * pairs, p.q + (first + k) * p.Hq * p.D,
-                         p.q_out + (first + k) * p.Hq * p.D, p.Hq, threadIdx.x - r * items, items,
-                         r + qrows * blockIdx.y, qrows * gridDim.y);
+        rotate_rows(p, turns + k * pairs, p.q + (first + k) * p.Hq * p.D, p.q_out + (first + k) * p.Hq * p.D, p.Hq,
+                    threadIdx.x - r * items, r + qrows * blockIdx.y, qrows * gridDim.y);
   }
+}
+
+template <typename Params>
+cudaError_t launch2(void (*kernel)(Params, int), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                    const Params& p, int tokens) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p, tokens);
+}
+
+// ---- the vector form: a warp per token ----------------------------------
+//
+// A warp computes its token's turns once (two pairs a lane) and then walks
+// the token's rows: K rows (rotated and quantized), V rows (quantized), q
+// rows and, without a cache, k rows (rotated).  A lane keeps the same
+// channels in every row of a kind, so their turns stay in its registers, and
+// it has several rows' loads in flight.  With few tokens a token's rows are
+// spread over `slices` warps.  BITS 0: no append.
+constexpr int kWarps = 4;
+
+template <int BITS, int KIND, bool INTER>
+__global__ void __launch_bounds__(kWarps * 32)
+    rope_warp_kernel(const __grid_constant__ RopeAppendParams pp, int slices) {
+  pdl_launch_dependents();
+  pdl_wait();
+  __shared__ __align__(16) float2 hi_s[kWarps][KVQ_ROPE_MAX_PAIRS], lo_s[kWarps][KVQ_ROPE_MAX_PAIRS];
+  const RopeParams& p = pp.r;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long w = (long long)blockIdx.x * kWarps + warp;
+  const long long at = w / slices;  // token
+  const int slice = (int)(w - at * slices);
+  if (at >= (long long)p.batch * p.num_new) return;
+  const Token tok = token_of(p, at);
+  if (!tok.live) return;
+  float2* hi = hi_s[warp];
+  float2* lo = lo_s[warp];
+  const int rd = p.rope.rotary_dim, pairs = rd >> 1;
+  for (int i = lane; i < pairs; i += 32) {
+    const Turn t = rope::turn_of((unsigned long long)tok.pos * p.rope.turns[i], p.rope.amplitude);
+    hi[i] = make_float2(t.ch, t.sh);
+    lo[i] = make_float2(t.cl, t.sl);
+  }
+  __syncwarp();
+  const float e = fmaxf((float)p.rope.amplitude * 0x1p-61f, 1.f) * 0x1p-22f;
+  int next = slice;  // this warp's next pass, counted over all kinds
+
+  if constexpr (BITS != 0) {
+    const AppendParams& a = pp.a;
+    const CacheGeom& c = a.geom;
+    const int chunks = c.D / 8, rpp = 32 / chunks;  // whole rows per pass
+    const int ch = lane % chunks, sub = lane / chunks;
+    const int passes = (c.Hkv + rpp - 1) / rpp;
+    const long long limit = c.layout == KVQ_DENSE ? c.slots : (long long)c.max_blocks * c.slots;
+    uint32_t flags = tok.pos >= limit ? KVQ_FLAG_SEQ_LEN : 0u;
+    // this lane's chunk: turned with its partner chunk (half layout), or by
+    // itself (interleaved)
+    const bool turned = ch * 8 < rd, upper = !INTER && ch * 8 >= pairs;
+    const int first = INTER ? ch * 4 : (upper ? ch * 8 - pairs : ch * 8);
+    float2 tr[8];
+#pragma unroll
+    for (int i = 0; i < (INTER ? 4 : 8); ++i) tr[i] = turned ? hi[first + i] : make_float2(1.f, 0.f);
+#pragma unroll 1
+    for (int pass = next; pass < 2 * passes; pass += slices) {
+      next = pass + slices;
+      const int which = pass >= passes;
+      const int kvh = (which ? pass - passes : pass) * rpp + sub;
+      long long row = -1;
+      if (kvh < c.Hkv && tok.pos < limit) {
+        row = token_row(c, tok.b, kvh, (int)tok.pos);
+        if (row < 0) flags |= KVQ_FLAG_BLOCK_TABLE;
+      }
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (row >= 0) {
+        const __half* src = a.src[which] + (at * c.Hkv + kvh) * c.D;
+        const uint4* own = reinterpret_cast<const uint4*>(src) + ch;
+        if (KVQ_IN(c, which ? KVQ_ARRAY_V_NEW : KVQ_ARRAY_K_NEW, own, 16)) v = __ldg(own);
+        if (!which && turned) {
+          const __half2* x = reinterpret_cast<const __half2*>(&v);
+          uint4 o;
+          uint32_t* y = reinterpret_cast<uint32_t*>(&o);
+          if constexpr (INTER) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 f = __half22float2(x[i]);
+              y[i] = rope::rotate_pair(tr[i], lo + first + i, e, f.x, f.y);
+            }
+          } else {
+            uint4 u = make_uint4(0u, 0u, 0u, 0u);
+            const uint4* oth = reinterpret_cast<const uint4*>(src + ch * 8 + (upper ? -pairs : pairs));
+            if (KVQ_IN(c, KVQ_ARRAY_K_NEW, oth, 16)) u = __ldg(oth);
+            const __half2* z = reinterpret_cast<const __half2*>(&u);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 f = __half22float2(x[i]), g = __half22float2(z[i]);
+              const uint32_t r0 = rope::rotate_pair(tr[2 * i], lo + first + 2 * i, e, upper ? g.x : f.x, upper ? f.x : g.x);
+              const uint32_t r1 =
+                  rope::rotate_pair(tr[2 * i + 1], lo + first + 2 * i + 1, e, upper ? g.y : f.y, upper ? f.y : g.y);
+              y[i] = __byte_perm(r0, r1, upper ? 0x7632 : 0x5410);
+            }
+          }
+          v = o;
+        }
+      }
+      const int a_codes = which ? KVQ_ARRAY_V_CODES : KVQ_ARRAY_K_CODES;
+      uint8_t* dst = a.codes[which] + row * c.row_bytes + ch * BITS;
+      if constexpr (BITS == 16) {
+        if (row >= 0 && KVQ_IN(c, a_codes, dst, 16)) *reinterpret_cast<uint4*>(dst) = v;
+      } else {
+        const int tpg = c.g / 8;
+        __syncwarp();
+        // every lane: the group uses shuffles
+        const Quant8 qz = KIND == 2 ? quantize8_nf4(v, tpg, a.nf4_mid) : quantize8<BITS, KIND == 1>(v, tpg);
+        if (row < 0) continue;
+        flags |= qz.flags;
+        if (KVQ_IN(c, a_codes, dst, BITS)) {
+          if constexpr (BITS == 2) *reinterpret_cast<uint16_t*>(dst) = (uint16_t)qz.w0;
+          else if constexpr (BITS == 4) *reinterpret_cast<uint32_t*>(dst) = qz.w0;
+          else *reinterpret_cast<uint2*>(dst) = make_uint2(qz.w0, qz.w1);
+        }
+        if (ch % tpg == 0) {
+          const long long h = row * c.ngroups + ch / tpg;
+          if (KVQ_IN(c, which ? KVQ_ARRAY_V_SCALE : KVQ_ARRAY_K_SCALE, a.scale[which] + h, 2))
+            a.scale[which][h] = qz.s;
+          if constexpr (KIND == 0)
+            if (KVQ_IN(c, which ? KVQ_ARRAY_V_ZERO : KVQ_ARRAY_K_ZERO, a.zero[which] + h, 2))
+              a.zero[which][h] = qz.z;
+        }
+      }
+    }
+    if (flags && p.status) atomicOr(p.status, flags);
+    next = next >= 2 * passes ? next - 2 * passes : next;
+  }
+
+  // q and k rows: items of two partner chunks (half layout) or of one chunk,
+  // then the chunks behind the turned channels, copied unless in place
+  const int rot = INTER ? rd / 8 : rd / 16, items = rot + (p.D - rd) / 8;
+  const int rpp = 32 / items, sub = lane / items, item = lane - sub * items;
+  const bool turns = item < rot;
+  float2 tr[8];
+#pragma unroll
+  for (int i = 0; i < (INTER ? 4 : 8); ++i) tr[i] = turns ? hi[item * (INTER ? 4 : 8) + i] : make_float2(1.f, 0.f);
+  const int c0 = turns ? item * 8 : rd + (item - rot) * 8;
+  constexpr int UN = INTER ? 4 : 2;  // rows in flight
+  const int rows = p.Hq + p.Hk;
+  if (sub >= rpp) return;
+  for (int r0 = next * rpp + sub; r0 < rows; r0 += UN * slices * rpp) {
+    uint4 v[UN], z[UN];
+    const __half* src[UN];
+    __half* dst[UN];
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+      const int r = r0 + u * slices * rpp;
+      const bool is_k = r >= p.Hq;
+      const long long o = is_k ? (at * p.Hk + (r - p.Hq)) * p.D : (at * p.Hq + r) * p.D;
+      src[u] = r < rows ? (is_k ? p.k : p.q) + o + c0 : nullptr;
+      dst[u] = (is_k ? p.k_out : p.q_out) + o + c0;
+      if (!src[u]) continue;
+      v[u] = *reinterpret_cast<const uint4*>(src[u]);
+      if (!INTER && turns) z[u] = *reinterpret_cast<const uint4*>(src[u] + pairs);
+    }
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+      if (!src[u]) continue;
+      if (!turns) {
+        if (src[u] != dst[u]) *reinterpret_cast<uint4*>(dst[u]) = v[u];
+        continue;
+      }
+      const __half2* x = reinterpret_cast<const __half2*>(&v[u]);
+      uint4 o, q;
+      uint32_t* y = reinterpret_cast<uint32_t*>(&o);
+      if constexpr (INTER) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = __half22float2(x[i]);
+          y[i] = rope::rotate_pair(tr[i], lo + item * 4 + i, e, f.x, f.y);
+        }
+      } else {
+        const __half2* s = reinterpret_cast<const __half2*>(&z[u]);
+        uint32_t* t = reinterpret_cast<uint32_t*>(&q);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = __half22float2(x[i]), g = __half22float2(s[i]);
+          const uint32_t a0 = rope::rotate_pair(tr[2 * i], lo + item * 8 + 2 * i, e, f.x, g.x);
+          const uint32_t a1 = rope::rotate_pair(tr[2 * i + 1], lo + item * 8 + 2 * i + 1, e, f.y, g.y);
+          y[i] = __byte_perm(a0, a1, 0x5410);
+          t[i] = __byte_perm(a0, a1, 0x7632);
+        }
+        *reinterpret_cast<uint4*>(dst[u] + pairs) = q;
+      }
+      *reinterpret_cast<uint4*>(dst[u]) = o;
+    }
+  }
+}
+
+template <int BITS, int KIND>
+cudaError_t launch_warp(const RopeAppendParams& p, cudaStream_t stream) {
+  const long long total = (long long)p.r.batch * p.r.num_new;
+  // passes of a token's rows, and warps sharing them while the grid is small
+  // (eight warps an SM already cover a memory latency)
+  const int rd = p.r.rope.rotary_dim;
+  const bool inter = p.r.rope.interleaved != 0;
+  const int items = (inter ? rd / 8 : rd / 16) + (p.r.D - rd) / 8, rpp = 32 / items;
+  long long passes = (p.r.Hq + p.r.Hk + rpp - 1) / rpp;
+  if (BITS) {
+    const int k = 32 / (p.r.D / 8);
+    passes += 2 * ((p.a.geom.Hkv + k - 1) / k);
+  }
+  long long slices = 1;
+  while (slices < passes && total * slices < 1216) slices *= 2;
+  const long long warps = total * slices;
+  const dim3 grid((unsigned)((warps + kWarps - 1) / kWarps));
+  return inter ? launch2(rope_warp_kernel<BITS, KIND, true>, grid, kWarps * 32, 0, stream, p, (int)slices)
+               : launch2(rope_warp_kernel<BITS, KIND, false>, grid, kWarps * 32, 0, stream, p, (int)slices);
 }
 
 // Tokens per CTA and slices of a token's rows: up to kMaxTokens tokens share
@@ -294,32 +458,20 @@ void rope_grid(long long total, int rows_per_token, int rows_per_pass, int* toke
   *grid = dim3((unsigned)((total + n - 1) / n), (unsigned)slices);
 }
 
-template <typename Params>
-cudaError_t launch2(void (*kernel)(Params, int), dim3 grid, size_t smem, cudaStream_t stream,
-                    const Params& p, int tokens) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p, tokens);
-}
-
 size_t turn_bytes(const kvq_rope& r, int tokens) {
   return (size_t)tokens * (r.rotary_dim / 2) * sizeof(Turn);  // at most 16 KB
 }
 
+// Whether the vector form applies: pairs in whole 16-byte chunks
+bool rope_vec(const kvq_rope& r) { return r.interleaved ? r.rotary_dim % 8 == 0 : r.rotary_dim % 16 == 0; }
+
 template <int BITS, int KIND>
-cudaError_t launch_append_bits(const RopeAppendParams& p, cudaStream_t s, dim3 grid, int tokens) {
-  const size_t smem = turn_bytes(p.r.rope, tokens);
-  return rope_vec(p.r.rope.rotary_dim, p.r.rope.interleaved != 0)
-             ? launch2(rope_append_kernel<BITS, KIND, true>, grid, smem, s, p, tokens)
-             : launch2(rope_append_kernel<BITS, KIND, false>, grid, smem, s, p, tokens);
+cudaError_t launch_append_bits(const RopeAppendParams& p, cudaStream_t s) {
+  if (rope_vec(p.r.rope)) return launch_warp<BITS, KIND>(p, s);
+  int tokens;
+  dim3 grid;
+  rope_grid((long long)p.a.batch * p.a.num_new, p.r.Hq + 2 * p.a.geom.Hkv, 16, &tokens, &grid);
+  return launch2(rope_append_kernel<BITS, KIND>, grid, kThreads, turn_bytes(p.r.rope, tokens), s, p, tokens);
 }
 
 }  // namespace
@@ -327,31 +479,29 @@ cudaError_t launch_append_bits(const RopeAppendParams& p, cudaStream_t s, dim3 g
 cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream) {
   const long long total = (long long)p.batch * p.num_new;
   if (total == 0 || p.Hq + p.Hk == 0) return cudaSuccess;
-  const bool vec = rope_vec(p.rope.rotary_dim, p.rope.interleaved != 0) && p.D % 8 == 0;
+  if (rope_vec(p.rope)) {
+    RopeAppendParams q{};
+    q.r = p;
+    return launch_warp<0, 0>(q, stream);
+  }
   int tokens;
   dim3 grid;
-  rope_grid(total, p.Hq + p.Hk, 32, &tokens, &grid);
-  const size_t smem = turn_bytes(p.rope, tokens);
-  return vec ? launch2(rope_kernel<true>, grid, smem, stream, p, tokens)
-             : launch2(rope_kernel<false>, grid, smem, stream, p, tokens);
+  rope_grid(total, p.Hq + p.Hk, 1, &tokens, &grid);
+  return launch2(rope_kernel, grid, kThreads, turn_bytes(p.rope, tokens), stream, p, tokens);
 }
 
 cudaError_t launch_rope_append(const RopeAppendParams& p, cudaStream_t stream) {
   const CacheGeom& c = p.a.geom;
-  const long long total = (long long)p.a.batch * p.a.num_new;
-  if (total == 0) return cudaSuccess;
-  int tokens;
-  dim3 grid;
-  rope_grid(total, p.r.Hq + 2 * c.Hkv, 16, &tokens, &grid);
+  if ((long long)p.a.batch * p.a.num_new == 0) return cudaSuccess;
   switch (c.bits * 4 + (c.nf4 ? 2 : (c.sym ? 1 : 0))) {
-    case 8:  return launch_append_bits<2, 0>(p, stream, grid, tokens);
-    case 9:  return launch_append_bits<2, 1>(p, stream, grid, tokens);
-    case 16: return launch_append_bits<4, 0>(p, stream, grid, tokens);
-    case 17: return launch_append_bits<4, 1>(p, stream, grid, tokens);
-    case 18: return launch_append_bits<4, 2>(p, stream, grid, tokens);
-    case 32: return launch_append_bits<8, 0>(p, stream, grid, tokens);
-    case 33: return launch_append_bits<8, 1>(p, stream, grid, tokens);
-    default: return launch_append_bits<16, 0>(p, stream, grid, tokens);
+    case 8:  return launch_append_bits<2, 0>(p, stream);
+    case 9:  return launch_append_bits<2, 1>(p, stream);
+    case 16: return launch_append_bits<4, 0>(p, stream);
+    case 17: return launch_append_bits<4, 1>(p, stream);
+    case 18: return launch_append_bits<4, 2>(p, stream);
+    case 32: return launch_append_bits<8, 0>(p, stream);
+    case 33: return launch_append_bits<8, 1>(p, stream);
+    default: return launch_append_bits<16, 0>(p, stream);
   }
 }
 

@@ -8,17 +8,22 @@
 // turn count.  With u = |r| / (1/8 turn) and w = u^2 (both in units of 2^-64),
 //   sin = u * sum_k (-1)^k (pi/4)^(2k+1) / (2k+1)! w^k,
 //   cos =     sum_k (-1)^k (pi/4)^(2k)   / (2k)!   w^k,
-// the Taylor series, by Horner's rule in units of 2^-62 (each term is smaller
-// than the one before, so no intermediate leaves [0, 1]).  Eight and nine
-// terms: the first term left out is below 2^-54, and so is the error seen
-// over random angles.
+// the Taylor series, by Horner's rule: the first three coefficients in units
+// of 2^-62 and 64-bit products, the rest, below 2^-11, in 32 bits (units of
+// 2^-46 and 2^-53, of 2^-43 and 2^-49).  Eight terms each: the first one left
+// out is below 2^-49, and with the 32-bit products' truncation the error seen
+// over random angles is below 2^-43.
 //
 // Product.  c and s are split into two floats each (48 bits), the products
 // with the fp16 values (11 bits) and their sum carry their rounding errors
 // along, and the last rounding to fp16 sees the exact side of a tie.  So the
 // result is the nearest fp16 to the formula's value, whatever order the
 // multiplications are done in; keys quantized from it have the same codes as
-// those of any other implementation that rounds correctly.
+// those of any other implementation that rounds correctly.  Almost always a
+// plain fp32 product settles that: its error is below E = 2^-22 max(a, 1)
+// (|x0| + |x1|) (two roundings of 2^-24 and the coefficients' 2^-24), so
+// where value - E and value + E round alike the long way is not taken (one
+// pair in about 500 takes it).
 #pragma once
 
 #include "kvq_internal.cuh"
@@ -31,11 +36,11 @@ struct Turn {
   float ch, cl, sh, sl;
 };
 
+// v in units of 2^-59, |v| < 2^61: the nearest multiple of 2^-23 and the rest
 __device__ __forceinline__ void split_q59(long long v, float& hi, float& lo) {
-  const float f = __ll2float_rn(v);
-  const long long rest = v - (long long)f;  // |f| <= 2^61: the cast is exact
-  hi = f * 0x1p-59f;
-  lo = (float)rest * 0x1p-59f;
+  const long long top = (v + (1ll << 35)) >> 36;  // below 2^25
+  hi = (float)(int)top * 0x1p-23f;
+  lo = (float)(int)((v - (top << 36)) >> 5) * 0x1p-54f;
 }
 
 // amplitude (units of 2^-61, below 2^63) times cos and sin of `frac` turns
@@ -47,34 +52,38 @@ __device__ __forceinline__ Turn turn_of(unsigned long long frac, unsigned long l
   a = a < (1ull << 61) ? a : (1ull << 61) - 1;
   const unsigned long long u = a << 3;
   const unsigned long long w = __umul64hi(u, u);
-  unsigned long long s = 0x16faeull;
-  s = 0x1e8f435ull - __umul64hi(s, w);
-  s = 0x1e3074fdfull - __umul64hi(s, w);
-  s = 0x150783487eeull - __umul64hi(s, w);
-  s = 0x9969667315ecull - __umul64hi(s, w);
-  s = 0x28cd78ceeb55c4ull - __umul64hi(s, w);
+  const uint32_t w32 = (uint32_t)(w >> 32);
+  uint32_t t = 0xf47au - __umulhi(0xb8u, w32);
+  t = 0xf183a8u - __umulhi(t, w32);
+  t = 0xa83c1a44u - __umulhi(t, w32);
+  t = 0x99696673u - (__umulhi(t, w32) >> 7);
+  unsigned long long s = 0x28cd78ceeb55c4ull - ((unsigned long long)t * w32 >> 16);
   s = 0x52aef39896f94b0ull - __umul64hi(s, w);
   s = 0x3243f6a8885a308dull - __umul64hi(s, w);
   s = __umul64hi(s, u);
-  unsigned long long c = 0x120cull;
-  c = 0x1b6e25ull - __umul64hi(c, w);
-  c = 0x1f9d38a3ull - __umul64hi(c, w);
-  c = 0x1a6d1f2a20ull - __umul64hi(c, w);
-  c = 0xf0fa83448ddull - __umul64hi(c, w);
-  c = 0x5574f1f8f2ffeull - __umul64hi(c, w);
-  c = 0x103c1f081b5ac3bull - __umul64hi(c, w);
+  t = 0xfceau - __umulhi(0xdbu, w32);
+  t = 0xd368f9u - __umulhi(t, w32);
+  t = 0x787d41a2u - __umulhi(t, w32);
+  t = 0xaae9e3f2u - (__umulhi(t, w32) >> 6);
+  unsigned long long c = 0x103c1f081b5ac3bull - ((unsigned long long)t * w32 >> 13);
   c = 0x13bd3cc9be45de5aull - __umul64hi(c, w);
   c = 0x4000000000000000ull - __umul64hi(c, w);
   // units of 2^-62 times units of 2^-61, high halves: units of 2^-59
-  long long sv = (long long)__umul64hi(s, amplitude);
-  const long long cv = (long long)__umul64hi(c, amplitude);
+  long long sv, cv;
+  if (amplitude == 1ull << 61) {
+    sv = (long long)(s >> 3);
+    cv = (long long)(c >> 3);
+  } else {
+    sv = (long long)__umul64hi(s, amplitude);
+    cv = (long long)__umul64hi(c, amplitude);
+  }
   if (r < 0) sv = -sv;
   const long long x = (quarter & 1) ? -sv : cv;
   const long long y = (quarter & 1) ? cv : sv;
-  Turn t;
-  split_q59((quarter & 2) ? -x : x, t.ch, t.cl);
-  split_q59((quarter & 2) ? -y : y, t.sh, t.sl);
-  return t;
+  Turn o;
+  split_q59((quarter & 2) ? -x : x, o.ch, o.cl);
+  split_q59((quarter & 2) ? -y : y, o.sh, o.sl);
+  return o;
 }
 
 // fp16 nearest to a * (bh + bl) + c * (dh + dl), a and c fp16 values
@@ -102,6 +111,32 @@ __device__ __forceinline__ void rotate_exact(const Turn& t, __half x0, __half x1
   const float a = __half2float(x0), b = __half2float(x1);
   y0 = dot2_round(a, t.ch, t.cl, -b, t.sh, t.sl);
   y1 = dot2_round(b, t.ch, t.cl, a, t.sh, t.sl);
+}
+
+// The same for a pair, plainly where that settles the rounding.  hi: (c, s);
+// lo is read only if need be.  e: 2^-22 max(amplitude, 1).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n"
+      : "=l"(*reinterpret_cast<unsigned long long*>(&d))
+      : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)),
+        "l"(*reinterpret_cast<unsigned long long*>(&c)));
+  return d;
+}
+__device__ __forceinline__ uint32_t half2_bits(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// y0 in the low half, y1 in the high one
+__device__ __forceinline__ uint32_t rotate_pair(float2 hi, const float2* lo, float e, float x0, float x1) {
+  const float2 r = fma2(make_float2(x0, x1), make_float2(hi.x, hi.x), make_float2(__fmul_rn(-x1, hi.y), __fmul_rn(x0, hi.y)));
+  const float d = __fmul_rn(fabsf(x0) + fabsf(x1), e);
+  const uint32_t up = half2_bits(r.x + d, r.y + d);
+  if (up == half2_bits(r.x - d, r.y - d)) return up;
+  const float2 l = *lo;
+  const __half y0 = dot2_round(x0, hi.x, l.x, -x1, hi.y, l.y);
+  const __half y1 = dot2_round(x1, hi.x, l.x, x0, hi.y, l.y);
+  return (uint32_t)__half_as_ushort(y0) | (uint32_t)__half_as_ushort(y1) << 16;
 }
 
 }  // namespace rope
