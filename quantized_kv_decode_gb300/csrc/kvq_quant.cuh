@@ -61,6 +61,15 @@ __device__ __forceinline__ float div_by(float x, float s, float r) {
   return __fmaf_rn(__fmaf_rn(-q0, s, x), r, q0);
 }
 
+// Nearest integer (ties to even) for |x| < 2^22.  x / s stays below 2^20: a
+// group's range is at least one fp16 step of its largest value, so |x| is at
+// most 2^11 ranges, and s is a range over at most 255 (a constant group: 1).
+__device__ __forceinline__ float rint_small(float x) { return __fadd_rn(__fadd_rn(x, 12582912.f), -12582912.f); }
+// A whole number held to [low, high] as a code.
+__device__ __forceinline__ uint32_t code_of(float t, float low, int high) {
+  return __float_as_uint(__fadd_rn(fminf(fmaxf(t, low), (float)high), 8388608.f)) & 0xFFu;
+}
+
 }  // namespace quant_detail
 
 // Parameters of one asymmetric group from its min and max (fp16 values as
@@ -112,8 +121,7 @@ template <int BITS>
 __device__ __forceinline__ uint32_t group_encode(float x, const GroupParams& gp) {
   constexpr int QMAX = (1 << BITS) - 1;
   if (!gp.finite) return 0u;
-  const float tq = rintf(quant_detail::div_by(x, gp.sf, gp.rs)) + gp.zf;
-  return (uint32_t)fminf(fmaxf(tq, 0.f), (float)QMAX);
+  return quant_detail::code_of(quant_detail::rint_small(quant_detail::div_by(x, gp.sf, gp.rs)) + gp.zf, 0.f, QMAX);
 }
 
 // One lane's share of a group: 8 channels.
@@ -138,20 +146,15 @@ template <int BITS, bool SYM = false>
 __device__ __forceinline__ Quant8 quantize8(const uint4 v, int tpg) {
   constexpr int HALF = 1 << (BITS - 1);  // symmetric code offset
   const __half* h = reinterpret_cast<const __half*>(&v);
-  float mn = INFINITY, mx = -INFINITY;
-  bool finite = true;
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const float f = __half2float(h[k]);
-    finite = finite && isfinite(f);
-    mn = fminf(mn, f);
-    mx = fmaxf(mx, f);
-  }
-  for (int o = 1; o < tpg; o <<= 1) {
-    mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    finite = (__shfl_xor_sync(0xffffffffu, (int)finite, o) != 0) && finite;
-  }
+  // the largest x and -x of the group in one pair (fp16 maxima are exact; a
+  // NaN stays, so the group is finite if both are)
+  const __half2* h2 = reinterpret_cast<const __half2*>(&v);
+  const __half2 hi = __hmax2_nan(__hmax2_nan(h2[0], h2[1]), __hmax2_nan(h2[2], h2[3]));
+  const __half2 lo = __hmax2_nan(__hmax2_nan(__hneg2(h2[0]), __hneg2(h2[1])), __hmax2_nan(__hneg2(h2[2]), __hneg2(h2[3])));
+  __half2 top = __hmax2_nan(__lows2half2(hi, lo), __highs2half2(hi, lo));
+  for (int o = 1; o < tpg; o <<= 1) top = __hmax2_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const float mx = __low2float(top), mn = -__high2float(top);
+  const bool finite = isfinite(mx) && isfinite(mn);
 
   Quant8 r;
   r.s = __ushort_as_half(0);
@@ -173,9 +176,10 @@ __device__ __forceinline__ Quant8 quantize8(const uint4 v, int tpg) {
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      float t = 0.f;
-      if (finite) t = fminf(fmaxf(rintf(quant_detail::div_by(__half2float(h[k]), sf, rs)), (float)-HALF), (float)(HALF - 1));
-      const uint32_t q = (uint32_t)(int)(t + (float)HALF);
+      uint32_t q = HALF;
+      if (finite)
+        q = quant_detail::code_of(quant_detail::rint_small(quant_detail::div_by(__half2float(h[k]), sf, rs)) + (float)HALF,
+                                  0.f, 2 * HALF - 1);
       if constexpr (BITS == 2) {
         r.w0 |= q << (2 * k);
       } else if constexpr (BITS == 4) {

@@ -250,12 +250,17 @@ cudaError_t launch2(void (*kernel)(Params, int), dim3 grid, int threads, size_t 
 // spread over `slices` warps.  BITS 0: no append.
 constexpr int kWarps = 4;
 
+// Lanes a row of q or k takes: a lane handles two chunks (half layout) or one.
+__host__ __device__ __forceinline__ int row_items(int rd, bool inter, int D) {
+  return inter ? D / 8 : rd / 16 + ((D - rd) / 8 + 1) / 2;
+}
+
 template <int BITS, int KIND, bool INTER>
 __global__ void __launch_bounds__(kWarps * 32)
     rope_warp_kernel(const __grid_constant__ RopeAppendParams pp, int slices) {
   pdl_launch_dependents();
   pdl_wait();
-  __shared__ __align__(16) float2 hi_s[kWarps][KVQ_ROPE_MAX_PAIRS], lo_s[kWarps][KVQ_ROPE_MAX_PAIRS];
+  __shared__ Turn turn_s[kWarps][KVQ_ROPE_MAX_PAIRS];
   const RopeParams& p = pp.r;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long w = (long long)blockIdx.x * kWarps + warp;
@@ -264,16 +269,16 @@ __global__ void __launch_bounds__(kWarps * 32)
   if (at >= (long long)p.batch * p.num_new) return;
   const Token tok = token_of(p, at);
   if (!tok.live) return;
-  float2* hi = hi_s[warp];
-  float2* lo = lo_s[warp];
+  Turn* turn = turn_s[warp];
   const int rd = p.rope.rotary_dim, pairs = rd >> 1;
-  for (int i = lane; i < pairs; i += 32) {
-    const Turn t = rope::turn_of((unsigned long long)tok.pos * p.rope.turns[i], p.rope.amplitude);
-    hi[i] = make_float2(t.ch, t.sh);
-    lo[i] = make_float2(t.cl, t.sl);
-  }
+  // Pair i of the P pairs of item k at i * items + k: the lanes of a row read
+  // consecutive turns.
+  constexpr int P = INTER ? 4 : 8;
+  const int rot = pairs / P;
+  for (int i = lane; i < pairs; i += 32)
+    turn[(i & (P - 1)) * rot + i / P] = rope::turn_of((unsigned long long)tok.pos * p.rope.turns[i], p.rope.amplitude);
   __syncwarp();
-  const float e = fmaxf((float)p.rope.amplitude * 0x1p-61f, 1.f) * 0x1p-22f;
+  const float e = fmaxf((float)p.rope.amplitude * 0x1p-61f, 1.f) * (1.0625f * 0x1p-24f);
   int next = slice;  // this warp's next pass, counted over all kinds
 
   if constexpr (BITS != 0) {
@@ -287,10 +292,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     // this lane's chunk: turned with its partner chunk (half layout), or by
     // itself (interleaved)
     const bool turned = ch * 8 < rd, upper = !INTER && ch * 8 >= pairs;
-    const int first = INTER ? ch * 4 : (upper ? ch * 8 - pairs : ch * 8);
-    float2 tr[8];
-#pragma unroll
-    for (int i = 0; i < (INTER ? 4 : 8); ++i) tr[i] = turned ? hi[first + i] : make_float2(1.f, 0.f);
+    const int item = INTER ? ch : (upper ? ch - rot : ch);
 #pragma unroll 1
     for (int pass = next; pass < 2 * passes; pass += slices) {
       next = pass + slices;
@@ -307,30 +309,14 @@ __global__ void __launch_bounds__(kWarps * 32)
         const uint4* own = reinterpret_cast<const uint4*>(src) + ch;
         if (KVQ_IN(c, which ? KVQ_ARRAY_V_NEW : KVQ_ARRAY_K_NEW, own, 16)) v = __ldg(own);
         if (!which && turned) {
-          const __half2* x = reinterpret_cast<const __half2*>(&v);
-          uint4 o;
-          uint32_t* y = reinterpret_cast<uint32_t*>(&o);
-          if constexpr (INTER) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 f = __half22float2(x[i]);
-              y[i] = rope::rotate_pair(tr[i], lo + first + i, e, f.x, f.y);
-            }
-          } else {
-            uint4 u = make_uint4(0u, 0u, 0u, 0u);
+          uint4 u = make_uint4(0u, 0u, 0u, 0u), o0, o1;
+          if constexpr (!INTER) {
             const uint4* oth = reinterpret_cast<const uint4*>(src + ch * 8 + (upper ? -pairs : pairs));
             if (KVQ_IN(c, KVQ_ARRAY_K_NEW, oth, 16)) u = __ldg(oth);
-            const __half2* z = reinterpret_cast<const __half2*>(&u);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 f = __half22float2(x[i]), g = __half22float2(z[i]);
-              const uint32_t r0 = rope::rotate_pair(tr[2 * i], lo + first + 2 * i, e, upper ? g.x : f.x, upper ? f.x : g.x);
-              const uint32_t r1 =
-                  rope::rotate_pair(tr[2 * i + 1], lo + first + 2 * i + 1, e, upper ? g.y : f.y, upper ? f.y : g.y);
-              y[i] = __byte_perm(r0, r1, upper ? 0x7632 : 0x5410);
-            }
           }
-          v = o;
+          const uint4 x0 = upper ? u : v, x1 = upper ? v : u;
+          rope::rotate_chunk<P, INTER>(turn + item, rot, e, x0, x1, o0, o1);
+          v = upper ? o1 : o0;
         }
       }
       const int a_codes = which ? KVQ_ARRAY_V_CODES : KVQ_ARRAY_K_CODES;
@@ -364,62 +350,47 @@ __global__ void __launch_bounds__(kWarps * 32)
   }
 
   // q and k rows: items of two partner chunks (half layout) or of one chunk,
-  // then the chunks behind the turned channels, copied unless in place
-  const int rot = INTER ? rd / 8 : rd / 16, items = rot + (p.D - rd) / 8;
+  // then the chunks behind the turned channels by twos (or one), copied
+  // unless in place
+  const int items = row_items(rd, INTER, p.D);
   const int rpp = 32 / items, sub = lane / items, item = lane - sub * items;
   const bool turns = item < rot;
-  float2 tr[8];
-#pragma unroll
-  for (int i = 0; i < (INTER ? 4 : 8); ++i) tr[i] = turns ? hi[item * (INTER ? 4 : 8) + i] : make_float2(1.f, 0.f);
-  const int c0 = turns ? item * 8 : rd + (item - rot) * 8;
-  constexpr int UN = INTER ? 4 : 2;  // rows in flight
-  const int rows = p.Hq + p.Hk;
+  const int c0 = turns ? item * 8 : rd + (item - rot) * (INTER ? 8 : 16);
+  const int c1 = turns ? pairs : 8;  // the second chunk, half layout
+  const bool two = !INTER && (turns || c0 + 8 < p.D);
+  constexpr int UN = 2;  // rows in flight
+  const int rows = p.Hq + p.Hk, step = slices * rpp;
   if (sub >= rpp) return;
-  for (int r0 = next * rpp + sub; r0 < rows; r0 += UN * slices * rpp) {
-    uint4 v[UN], z[UN];
-    const __half* src[UN];
-    __half* dst[UN];
+#pragma unroll 1
+  for (int r0 = next * rpp + sub; r0 < rows; r0 += UN * step) {
+    uint4 x0[UN], x1[UN];
+    long long at_row[UN];
 #pragma unroll
     for (int u = 0; u < UN; ++u) {
-      const int r = r0 + u * slices * rpp;
+      const int r = r0 + u * step;
+      if (r >= rows) continue;
       const bool is_k = r >= p.Hq;
-      const long long o = is_k ? (at * p.Hk + (r - p.Hq)) * p.D : (at * p.Hq + r) * p.D;
-      src[u] = r < rows ? (is_k ? p.k : p.q) + o + c0 : nullptr;
-      dst[u] = (is_k ? p.k_out : p.q_out) + o + c0;
-      if (!src[u]) continue;
-      v[u] = *reinterpret_cast<const uint4*>(src[u]);
-      if (!INTER && turns) z[u] = *reinterpret_cast<const uint4*>(src[u] + pairs);
+      at_row[u] = (is_k ? at * p.Hk + (r - p.Hq) : at * p.Hq + r) * p.D + c0;
+      const __half* src = (is_k ? p.k : p.q) + at_row[u];
+      x0[u] = *reinterpret_cast<const uint4*>(src);
+      if (two) x1[u] = *reinterpret_cast<const uint4*>(src + c1);
     }
 #pragma unroll
     for (int u = 0; u < UN; ++u) {
-      if (!src[u]) continue;
+      const int r = r0 + u * step;
+      if (r >= rows) continue;
+      __half* dst = (r >= p.Hq ? p.k_out : p.q_out) + at_row[u];
       if (!turns) {
-        if (src[u] != dst[u]) *reinterpret_cast<uint4*>(dst[u]) = v[u];
+        if (dst != (r >= p.Hq ? p.k : p.q) + at_row[u]) {
+          *reinterpret_cast<uint4*>(dst) = x0[u];
+          if (two) *reinterpret_cast<uint4*>(dst + c1) = x1[u];
+        }
         continue;
       }
-      const __half2* x = reinterpret_cast<const __half2*>(&v[u]);
-      uint4 o, q;
-      uint32_t* y = reinterpret_cast<uint32_t*>(&o);
-      if constexpr (INTER) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = __half22float2(x[i]);
-          y[i] = rope::rotate_pair(tr[i], lo + item * 4 + i, e, f.x, f.y);
-        }
-      } else {
-        const __half2* s = reinterpret_cast<const __half2*>(&z[u]);
-        uint32_t* t = reinterpret_cast<uint32_t*>(&q);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = __half22float2(x[i]), g = __half22float2(s[i]);
-          const uint32_t a0 = rope::rotate_pair(tr[2 * i], lo + item * 8 + 2 * i, e, f.x, g.x);
-          const uint32_t a1 = rope::rotate_pair(tr[2 * i + 1], lo + item * 8 + 2 * i + 1, e, f.y, g.y);
-          y[i] = __byte_perm(a0, a1, 0x5410);
-          t[i] = __byte_perm(a0, a1, 0x7632);
-        }
-        *reinterpret_cast<uint4*>(dst[u] + pairs) = q;
-      }
-      *reinterpret_cast<uint4*>(dst[u]) = o;
+      uint4 y0, y1;
+      rope::rotate_chunk<P, INTER>(turn + item, rot, e, x0[u], x1[u], y0, y1);
+      *reinterpret_cast<uint4*>(dst) = y0;
+      if (!INTER) *reinterpret_cast<uint4*>(dst + pairs) = y1;
     }
   }
 }
@@ -431,7 +402,7 @@ cudaError_t launch_warp(const RopeAppendParams& p, cudaStream_t stream) {
   // (eight warps an SM already cover a memory latency)
   const int rd = p.r.rope.rotary_dim;
   const bool inter = p.r.rope.interleaved != 0;
-  const int items = (inter ? rd / 8 : rd / 16) + (p.r.D - rd) / 8, rpp = 32 / items;
+  const int rpp = 32 / row_items(rd, inter, p.r.D);
   long long passes = (p.r.Hq + p.r.Hk + rpp - 1) / rpp;
   if (BITS) {
     const int k = 32 / (p.r.D / 8);

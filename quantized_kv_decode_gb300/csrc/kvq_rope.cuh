@@ -19,11 +19,12 @@
 // along, and the last rounding to fp16 sees the exact side of a tie.  So the
 // result is the nearest fp16 to the formula's value, whatever order the
 // multiplications are done in; keys quantized from it have the same codes as
-// those of any other implementation that rounds correctly.  Almost always a
-// plain fp32 product settles that: its error is below E = 2^-22 max(a, 1)
-// (|x0| + |x1|) (two roundings of 2^-24 and the coefficients' 2^-24), so
-// where value - E and value + E round alike the long way is not taken (one
-// pair in about 500 takes it).
+// those of any other implementation that rounds correctly.  Almost always
+// plain fp32 arithmetic settles that: with x lo added up first, the value is
+// off by the roundings of the last two sums only, 2^-24 of |x1| a + |y|
+// (y0's; a the amplitude) and terms below 2^-46, so where value - E and value
+// + E round alike, E = 1.0625 2^-24 max(a, 1) (|x1| + |y|), the long way is
+// not taken.
 #pragma once
 
 #include "kvq_internal.cuh"
@@ -113,8 +114,7 @@ __device__ __forceinline__ void rotate_exact(const Turn& t, __half x0, __half x1
   y1 = dot2_round(b, t.ch, t.cl, a, t.sh, t.sl);
 }
 
-// The same for a pair, plainly where that settles the rounding.  hi: (c, s);
-// lo is read only if need be.  e: 2^-22 max(amplitude, 1).
+// The same for a pair, plainly where that settles the rounding.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
   asm("fma.rn.f32x2 %0, %1, %2, %3;\n"
@@ -127,16 +127,85 @@ __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// y0 in the low half, y1 in the high one
-__device__ __forceinline__ uint32_t rotate_pair(float2 hi, const float2* lo, float e, float x0, float x1) {
-  const float2 r = fma2(make_float2(x0, x1), make_float2(hi.x, hi.x), make_float2(__fmul_rn(-x1, hi.y), __fmul_rn(x0, hi.y)));
-  const float d = __fmul_rn(fabsf(x0) + fabsf(x1), e);
-  const uint32_t up = half2_bits(r.x + d, r.y + d);
-  if (up == half2_bits(r.x - d, r.y - d)) return up;
-  const float2 l = *lo;
-  const __half y0 = dot2_round(x0, hi.x, l.x, -x1, hi.y, l.y);
-  const __half y1 = dot2_round(x1, hi.x, l.x, x0, hi.y, l.y);
+// y0 in the low half, y1 in the high one.  e: 1.0625 2^-24 max(amplitude, 1).
+// sure: whether the rounding is settled; if not, rotate_long tells.
+__device__ __forceinline__ uint32_t rotate_pair(const Turn& t, float e, float x0, float x1, bool& sure) {
+  const float2 x = make_float2(x0, x1), o = make_float2(-x1, x0);
+  float2 r = make_float2(__fmul_rn(x0, t.cl), __fmul_rn(x1, t.cl));
+  r = fma2(o, make_float2(t.sl, t.sl), r);
+  r = fma2(o, make_float2(t.sh, t.sh), r);
+  r = fma2(x, make_float2(t.ch, t.ch), r);
+  const float d0 = __fmul_rn(fabsf(x1) + fabsf(r.x), e), d1 = __fmul_rn(fabsf(x0) + fabsf(r.y), e);
+  const uint32_t up = half2_bits(r.x + d0, r.y + d1);
+  // (an infinity among the inputs makes a NaN of x lo: the long way tells)
+  const __half2 u = *reinterpret_cast<const __half2*>(&up);
+  sure = up == half2_bits(r.x - d0, r.y - d1) && __hbeq2(u, u);
+  return up;
+}
+__device__ __forceinline__ uint32_t rotate_long(const Turn& t, float x0, float x1) {
+  const __half y0 = dot2_round(x0, t.ch, t.cl, -x1, t.sh, t.sl);
+  const __half y1 = dot2_round(x1, t.ch, t.cl, x0, t.sh, t.sl);
   return (uint32_t)__half_as_ushort(y0) | (uint32_t)__half_as_ushort(y1) << 16;
+}
+
+__device__ __forceinline__ uint32_t pick(const uint4& v, int i) {
+  const uint32_t a = (i & 1) ? v.y : v.x, b = (i & 1) ? v.w : v.z;
+  return (i & 2) ? b : a;
+}
+
+// N pairs (x0 of pair i in x0[i/2], half i & 1, as fp16 pairs; INTER: pair i
+// is x0[i]) turned by t[i * stride]: y0 and y1 laid out as x0 and x1.  The
+// pairs that plain arithmetic leaves open are gone over one at a time, so
+// that the long way is there once.
+template <int N, bool INTER>
+__device__ __forceinline__ void rotate_chunk(const Turn* t, int stride, float e, const uint4& x0v, const uint4& x1v,
+                                             uint4& y0v, uint4& y1v) {
+  const uint32_t x0[4] = {x0v.x, x0v.y, x0v.z, x0v.w}, x1[4] = {x1v.x, x1v.y, x1v.z, x1v.w};
+  uint32_t y0[4], y1[4];
+  uint32_t open = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint32_t a = INTER ? x0[i] : x0[i >> 1], b = INTER ? 0u : x1[i >> 1];
+    const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&a));
+    const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&b));
+    bool sure;
+    const uint32_t r = rotate_pair(t[i * stride], e, (!INTER && (i & 1)) ? fa.y : fa.x,
+                                   INTER ? fa.y : (i & 1) ? fb.y : fb.x, sure);
+    if (!sure) open |= 1u << i;
+    if (INTER) {
+      y0[i] = r;
+    } else if (i & 1) {
+      const uint32_t q = y0[i >> 1];
+      y0[i >> 1] = __byte_perm(q, r, 0x5410);
+      y1[i >> 1] = __byte_perm(q, r, 0x7632);
+    } else {
+      y0[i >> 1] = r;
+    }
+  }
+  while (open) {
+    const int k = __ffs(open) - 1;
+    open &= open - 1;
+    const int w = INTER ? k : k >> 1;
+    uint32_t a = pick(x0v, w), b = INTER ? 0u : pick(x1v, w);
+    if (!INTER && (k & 1)) a >>= 16, b >>= 16;
+    const float f0 = __half2float(__ushort_as_half((unsigned short)a));
+    const float f1 = __half2float(__ushort_as_half((unsigned short)(INTER ? a >> 16 : b)));
+    const uint32_t r = rotate_long(t[k * stride], f0, f1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool here = i == w;
+      if (INTER) {
+        y0[i] = here ? r : y0[i];
+      } else {
+        const uint32_t p0 = __byte_perm(y0[i], r, (k & 1) ? 0x5410 : 0x3254);
+        const uint32_t p1 = __byte_perm(y1[i], r, (k & 1) ? 0x7610 : 0x3276);
+        y0[i] = here ? p0 : y0[i];
+        y1[i] = here ? p1 : y1[i];
+      }
+    }
+  }
+  y0v = make_uint4(y0[0], y0[1], y0[2], y0[3]);
+  if (!INTER) y1v = make_uint4(y1[0], y1[1], y1[2], y1[3]);
 }
 
 }  // namespace rope

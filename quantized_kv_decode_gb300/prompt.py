@@ -7,7 +7,7 @@ device, on its current stream unless `stream` is given.
 """
 from __future__ import annotations
 
-from ctypes import byref
+from ctypes import POINTER, byref, c_uint64, cast
 from dataclasses import dataclass
 
 import torch
@@ -18,16 +18,19 @@ from .api import KVCache, _ptr
 
 
 def _check(t, dtype, name, shape, device):
-    """A contiguous CUDA tensor of this dtype and shape (None: any size), on `device`."""
+    """A contiguous CUDA tensor of this dtype and shape (None in it: any size),
+    on `device` (an index; None: any)."""
     if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor of dtype {dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
+    got = t.shape
+    if got != shape and (len(got) != len(shape)
+                         or any(w is not None and w != n for w, n in zip(shape, got))):
         raise ValueError(f"{name} must have shape {tuple('*' if w is None else w for w in shape)}, "
-                         f"not {tuple(t.shape)}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
+                         f"not {tuple(got)}")
+    if device is not None and t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{device}")
 
 
 def _optional(t, dtype, name, shape, device):
@@ -36,18 +39,19 @@ def _optional(t, dtype, name, shape, device):
 
 
 def _status(t, device):
-    if t is not None and (not isinstance(t, torch.Tensor) or t.device != device
+    if t is not None and (not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != device
                           or t.dtype not in (torch.int32, torch.uint32) or t.numel() < 1):
-        raise TypeError(f"dev_status must be an int32 tensor on {device}")
+        raise TypeError(f"dev_status must be an int32 tensor on cuda:{device}")
 
 
 def _bytes(t, device, need, name):
     """(tensor, its bytes) of a workspace; allocated when missing or too small."""
-    if t is not None and (not isinstance(t, torch.Tensor) or t.device != device or not t.is_contiguous()):
-        raise TypeError(f"{name} must be a contiguous tensor on {device}")
+    if t is not None and (not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != device
+                          or not t.is_contiguous()):
+        raise TypeError(f"{name} must be a contiguous tensor on cuda:{device}")
     size = 0 if t is None else t.numel() * t.element_size()
     if need > size:
-        t, size = torch.empty(need, dtype=torch.uint8, device=device), need
+        t, size = torch.empty(need, dtype=torch.uint8, device=f"cuda:{device}"), need
     return t, size
 
 
@@ -56,7 +60,7 @@ class _on:
     __slots__ = ("guard",)
 
     def __init__(self, device):
-        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        self.guard = None if device == torch.cuda.current_device() else torch.cuda.device(device)
 
     def __enter__(self):
         if self.guard is not None:
@@ -74,8 +78,8 @@ def _stream_on(stream, device):
 
 
 def _same_cache_device(cache: KVCache, device):
-    if cache.k_codes.device != device:
-        raise ValueError(f"the cache is on {cache.k_codes.device}, not on {device}")
+    if not cache.k_codes.is_cuda or cache.k_codes.get_device() != device:
+        raise ValueError(f"the cache is on {cache.k_codes.device}, not on cuda:{device}")
 
 
 def _batch(cache: KVCache, B):
@@ -116,7 +120,7 @@ def kvq_rope_apply(rope: kvq_rope, q: torch.Tensor | None = None, k: torch.Tenso
         raise ValueError("q or k must be given")
     _check(x, torch.float16, "q" if q is not None else "k", (None,) * 4, None)
     B, T, _, D = x.shape
-    dev = x.device
+    dev = x.get_device()
     if positions is None and seq_lens_before is None:
         raise ValueError("positions or seq_lens_before must be given")
     _optional(positions, torch.int32, "positions", (B, T), dev)
@@ -133,7 +137,7 @@ def kvq_rope_apply(rope: kvq_rope, q: torch.Tensor | None = None, k: torch.Tenso
         _check(t, torch.float16, name, (B, T, None, D), dev)
         if o is None:
             o = torch.zeros_like(t) if new_lens is not None else torch.empty_like(t)
-        _check(o, torch.float16, name + "_out", tuple(t.shape), dev)
+        _check(o, torch.float16, name + "_out", t.shape, dev)
         outs.append(o)
     with _on(dev):
         st = _lib.lib().kvq_rope_apply(
@@ -154,8 +158,8 @@ def kvq_rope_append(cache: KVCache, rope: kvq_rope, k_new: torch.Tensor, v_new: 
     d = cache.desc
     _check(k_new, torch.float16, "k_new", (None, None, d.num_kv_heads, d.head_dim), None)
     B, T, _, D = k_new.shape
-    dev = k_new.device
-    _check(v_new, torch.float16, "v_new", tuple(k_new.shape), dev)
+    dev = k_new.get_device()
+    _check(v_new, torch.float16, "v_new", k_new.shape, dev)
     _check(seq_lens_before, torch.int32, "seq_lens_before", (B,), dev)
     _optional(new_lens, torch.int32, "new_lens", (B,), dev)
     _same_cache_device(cache, dev)
@@ -165,7 +169,7 @@ def kvq_rope_append(cache: KVCache, rope: kvq_rope, k_new: torch.Tensor, v_new: 
         _check(q, torch.float16, "q", (B, T, None, D), dev)
         if q_out is None:
             q_out = torch.zeros_like(q) if new_lens is not None else torch.empty_like(q)
-        _check(q_out, torch.float16, "q_out", tuple(q.shape), dev)
+        _check(q_out, torch.float16, "q_out", q.shape, dev)
     elif q_out is not None:
         raise ValueError("q_out without q")
     with _on(dev):
@@ -189,9 +193,9 @@ def kvq_cache_read(cache: KVCache, seq_lens: torch.Tensor, start: torch.Tensor,
         raise ValueError("k_out or v_out must be given")
     _check(x, torch.float16, "k_out" if k_out is not None else "v_out",
            (None, None, d.num_kv_heads, d.head_dim), None)
-    B, T, dev = x.shape[0], x.shape[1], x.device
-    _optional(k_out, torch.float16, "k_out", tuple(x.shape), dev)
-    _optional(v_out, torch.float16, "v_out", tuple(x.shape), dev)
+    B, T, dev = x.shape[0], x.shape[1], x.get_device()
+    _optional(k_out, torch.float16, "k_out", x.shape, dev)
+    _optional(v_out, torch.float16, "v_out", x.shape, dev)
     _check(seq_lens, torch.int32, "seq_lens", (B,), dev)
     _check(start, torch.int32, "start", (B,), dev)
     _same_cache_device(cache, dev)
@@ -227,7 +231,7 @@ def kvq_extend_attn(cache: KVCache, q: torch.Tensor, seq_lens_before: torch.Tens
     d = cache.desc
     _check(q, torch.float16, "q", (None, None, None, d.head_dim), None)
     B, T, Hq, _ = q.shape
-    dev = q.device
+    dev = q.get_device()
     _check(seq_lens_before, torch.int32, "seq_lens_before", (B,), dev)
     _optional(new_lens, torch.int32, "new_lens", (B,), dev)
     _same_cache_device(cache, dev)
@@ -235,7 +239,7 @@ def kvq_extend_attn(cache: KVCache, q: torch.Tensor, seq_lens_before: torch.Tens
     _status(dev_status, dev)
     if out is None:
         out = torch.zeros_like(q) if new_lens is not None else torch.empty_like(q)
-    _check(out, torch.float16, "out", tuple(q.shape), dev)
+    _check(out, torch.float16, "out", q.shape, dev)
     with _on(dev):
         need = 0 if workspace is not None else \
             kvq_extend_workspace_size(d, B, T, Hq, max_seq_len, num_splits)
@@ -258,7 +262,7 @@ class PagePool:
 
     def __post_init__(self):
         _check(self.ref_count, torch.int32, "ref_count", (None,), None)
-        _check(self.block_table, torch.int32, "block_table", (None, None), self.ref_count.device)
+        _check(self.block_table, torch.int32, "block_table", (None, None), self.ref_count.get_device())
 
     @classmethod
     def allocate(cls, num_pages: int, page_size: int, batch: int, max_blocks_per_seq: int,
@@ -283,7 +287,7 @@ def kvq_pages_reorder(pool: PagePool, parent: torch.Tensor, keep_lens: torch.Ten
                       dev_status: torch.Tensor | None = None, stream=None) -> None:
     """Row b of the block table becomes the first ceil(keep_lens[b] /
     page_size) entries of row parent[b] (-1: freed); reference counts follow."""
-    B, dev = pool.block_table.shape[0], pool.ref_count.device
+    B, dev = pool.block_table.shape[0], pool.ref_count.get_device()
     _check(parent, torch.int32, "parent", (B,), dev)
     _optional(keep_lens, torch.int32, "keep_lens", (B,), dev)
     _status(dev_status, dev)
@@ -301,7 +305,7 @@ def kvq_pages_reserve(pool: PagePool, seq_lens_before: torch.Tensor,
     """Make positions [seq_lens_before[b], seq_lens_before[b] + new_lens[b])
     writable (new_lens None: max_new each); the pages to copy first are left
     in copy_src / copy_dst [B], the tokens granted in granted [B]."""
-    B, dev = pool.block_table.shape[0], pool.ref_count.device
+    B, dev = pool.block_table.shape[0], pool.ref_count.get_device()
     _check(seq_lens_before, torch.int32, "seq_lens_before", (B,), dev)
     _optional(new_lens, torch.int32, "new_lens", (B,), dev)
     _check(copy_src, torch.int32, "copy_src", (B,), dev)
@@ -324,7 +328,7 @@ def kvq_pages_compact(pool: PagePool, move_src: torch.Tensor, move_dst: torch.Te
                       dev_status: torch.Tensor | None = None, stream=None) -> None:
     """Move the pages in use to the low end of the pool: table and counts
     change here, the moves [num_pages // 2] go to kvq_pages_copy."""
-    n, dev = pool.ref_count.numel(), pool.ref_count.device
+    n, dev = pool.ref_count.numel(), pool.ref_count.get_device()
     _check(move_src, torch.int32, "move_src", (n // 2,), dev)
     _check(move_dst, torch.int32, "move_dst", (n // 2,), dev)
     _check(num_live, torch.int32, "num_live", (1,), dev)
@@ -346,16 +350,23 @@ def kvq_pages_copy(caches, copy_src: torch.Tensor, copy_dst: torch.Tensor,
     caches = list(caches)
     if not caches:
         return
-    dev = caches[0].k_codes.device
+    dev = caches[0].k_codes.get_device()
     _check(copy_src, torch.int32, "copy_src", (None,), dev)
-    _check(copy_dst, torch.int32, "copy_dst", tuple(copy_src.shape), dev)
+    _check(copy_dst, torch.int32, "copy_dst", copy_src.shape, dev)
     _status(dev_status, dev)
-    first = bytes(caches[0].desc)
+    desc = caches[0].desc
+    first = bytes(desc)
+    flat = []
     for c in caches:
-        _same_cache_device(c, dev)
-        if bytes(c.desc) != first:
+        if c.k_codes.get_device() != dev:
+            _same_cache_device(c, dev)
+        if c.desc is not desc and bytes(c.desc) != first:
             raise ValueError("the caches must have one descriptor")
-    arrays = (kvq_cache * len(caches))(*[c.ptrs for c in caches])
+        flat += [0 if t is None else t.data_ptr() for t in
+                 (c.k_codes, c.v_codes, c.k_scale, c.k_zero, c.v_scale, c.v_zero, c.block_table, c.k_window,
+                  c.v_window)]
+    # (the pointers of the kvq_cache structures one after the other)
+    arrays = cast((c_uint64 * len(flat))(*flat), POINTER(kvq_cache))
     with _on(dev):
         st = _lib.lib().kvq_pages_copy(byref(caches[0].desc), arrays, len(caches), _ptr(copy_src),
                                        _ptr(copy_dst), copy_src.numel(), _ptr(dev_status),
