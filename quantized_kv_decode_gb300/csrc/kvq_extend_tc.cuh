@@ -2,8 +2,10 @@
 // tensor cores (head_dim 64 and 128, every per-token format).
 //
 // Rows.  As in kvq_extend.cu the rows of a tile are (new token, head of the
-// KV head's group) pairs.  A CTA takes NQ tiles of 128 rows of one KV head
-// and one split of the keys, in steps of 64 keys:
+// KV head's group) pairs.  A CTA takes two tiles of 128 rows of one KV head
+// and one split of the keys, in steps of 64 keys; a call of at most 128 rows
+// takes one tile in two streams that share the key tiles out between them and
+// are joined at the end (NQ = 1):
 //   S = Q K^T     A = Q, resident in tensor memory for the whole call; B = K
 //                 from shared memory
 //   P = 2^(S - m) one thread per row: 64 scores from tensor memory to
@@ -17,7 +19,7 @@
 // Warps.  0 and 3 issue the MMAs, a tile each; 1 and 2 copy codes and headers to a ring in
 // shared memory; from 4 on softmax, a row per thread (four warps a tile); the
 // producers behind turn the ring's codes into fp16 in the tensor core's
-// swizzled layout (four warps, or eight with one tile).  With two tiles one's
+// swizzled layout (eight warps; four for fp16).  One tile's (or stream's)
 // softmax runs under the other's products.
 //
 // Precision.  q - z is a whole number (exact in fp16 up to 2048) and s has
@@ -60,9 +62,11 @@ constexpr float kLazy = 8.f;  // log2 units the maximum may lead the reference
 template <int BITS, int KIND, int D, int NQ>
 struct Cfg {
   static constexpr bool LO = KIND != 2;
-  static constexpr int SOFT = 4 * NQ;             // softmax warps
-  static constexpr int PROD = NQ == 1 || LO ? 8 : 4;  // producer warps
-  static constexpr int LOAD = 1;                  // loader warp (fp16: the warp that passes stages on)
+  static constexpr bool DUAL = NQ == 1;           // one tile of rows, the key tiles shared between two streams
+  static constexpr int ROWS = 128 * NQ;
+  static constexpr int SOFT = 8;                  // softmax warps
+  static constexpr int PROD = LO ? 8 : 4;         // producer warps
+  static constexpr int LOAD = LO ? 2 : 1;         // loader warps, K and V (fp16: the warp that passes stages on)
   // warps 0 and 3 issue the MMAs, 1 .. LOAD load; softmax from 4 on (a warp reads
   // the tensor memory lanes of its number modulo 4), producers behind
   static constexpr int SOFT0 = 4, PROD0 = SOFT0 + SOFT, WARPS = PROD0 + PROD;
@@ -83,14 +87,14 @@ struct Cfg {
   static constexpr int HDR = kKeys * D / 4 + 16;  // most bytes of one header array, from a 16-byte boundary on
   static constexpr int RAW = LO ? 2 * CODES + 4 * HDR : 0;     // K codes, V codes, K scale, K zero, V scale, V zero
   // arrivals that fill a ring slot (fp16: a stage's copies and key masks), and a stage
-  static constexpr int RAW_FULL = LO ? 1 : PROD * 32 + 1, FULL = LO ? PROD : 1;
+  static constexpr int RAW_FULL = LO ? LOAD : PROD * 32 + 1, FULL = LO ? PROD : 1;
   static constexpr int SLOTS = LO ? DEPTH : STAGES;
   // tensor memory columns: per tile S (64, P in its place), O (D), Q (D / 2)
-  static constexpr uint32_t COL_S = 0, COL_O = NQ * kKeys, COL_Q = COL_O + NQ * D;
-  static constexpr uint32_t COLS = NQ == 2 ? 512 : 256;
-  static constexpr size_t SMEM = (size_t)STAGES * STAGE + (size_t)DEPTH * RAW + 1024 + 1024;
+  static constexpr uint32_t COL_S = 0, COL_O = 2 * kKeys, COL_Q = COL_O + 2 * D, COLS = 512;
+  static constexpr size_t SMEM = (size_t)STAGES * STAGE + (size_t)DEPTH * RAW + 1024 + 2048;
   static_assert(SMEM <= 227 * 1024, "shared memory");
-  static_assert(COL_Q + NQ * D / 2 <= COLS, "tensor memory");
+  static_assert(COL_Q + 2 * D / 2 <= COLS, "tensor memory");
+  static_assert(!DUAL || (size_t)STAGES * STAGE >= (size_t)128 * D * 4, "the second stream's result");
   // channel held at place i of an eight-channel chunk (the unpacking leaves
   // 4-bit and 2-bit codes as pairs (i, i + 4))
   static constexpr bool PAIRED = BITS <= 4;
@@ -104,7 +108,8 @@ struct Shared {
   unsigned long long raw_full[kMaxDepth], raw_empty[kMaxDepth];
   uint32_t raw_ok[kMaxDepth][2];
   unsigned long long full[STAGES], empty[STAGES];
-  unsigned long long q_full[2], s_full[2], p_full[2], o_full[2], turn[2];
+  unsigned long long q_full[2], s_full[2], p_full[2], o_full[2], turn[2], merge;
+  float2 ml[128];           // the second stream's maximum and sum per row
   uint32_t ok[STAGES][2];   // per key: mapped and before the end
   uint32_t bad[STAGES][4][2];  // per segment and key: V held an infinity or NaN (set to zero)
   uint32_t tmem;
@@ -287,7 +292,7 @@ template <int BITS, int KIND, int D, int NQ>
 __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
     extend_tc_kernel(const __grid_constant__ ExtendParams p) {
   using C = Cfg<BITS, KIND, D, NQ>;
-  constexpr int ROWS = 128 * NQ;
+  constexpr int ROWS = C::ROWS, STEP = C::DUAL ? 2 : 1;  // key tiles from one of a stream's to its next
   pdl_launch_dependents();
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + ((1024 - (tc::smem_addr(raw) & 1023)) & 1023);
@@ -315,9 +320,9 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
   const int k0 = split * p.chunk, k1 = min(end, k0 + p.chunk);
   const int tiles = k1 > k0 ? (k1 - k0 + kKeys - 1) / kKeys : 0;
   const int all_see = L ? before + t_first : -1;  // every row sees the positions up to here
-  const int nq = (NQ == 2 && live_rows - r0 <= 128) ? 1 : NQ;  // tiles with rows
+  const int nq = (!C::DUAL && live_rows - r0 <= 128) ? 1 : 2;  // tiles of rows, or streams
 
-  static_assert(sizeof(Shared<C::STAGES>) <= 1024, "room behind the stages");
+  static_assert(sizeof(Shared<C::STAGES>) <= 2048, "room behind the stages");
   const uint32_t bars = tc::smem_addr(&sh);
   auto full = [&](int s) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, full) + 8 * s; };
   auto empty = [&](int s) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, empty) + 8 * s; };
@@ -327,13 +332,14 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
   auto s_full = [&](int i) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, s_full) + 8 * i; };
   auto p_full = [&](int i) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, p_full) + 8 * i; };
   auto turn = [&](int i) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, turn) + 8 * i; };
+  const uint32_t merge = bars + (uint32_t)offsetof(Shared<C::STAGES>, merge);
   auto o_full = [&](int i) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, o_full) + 8 * i; };
   volatile int* stop = &sh.stop;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
       tc::mbar_init(full(s), C::FULL);
-      tc::mbar_init(empty(s), nq);
+      tc::mbar_init(empty(s), C::DUAL ? 1 : nq);
     }
     for (int s = 0; s < C::SLOTS; ++s) {
       tc::mbar_init(raw_full(s), C::RAW_FULL);
@@ -346,6 +352,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
       tc::mbar_init(o_full(i), 1);
       tc::mbar_init(turn(i), 1);
     }
+    tc::mbar_init(merge, 4);
     sh.stop = 0;
     tc::mbar_init_fence();
   }
@@ -375,7 +382,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
   if (warp >= C::SOFT0 && warp < C::PROD0) {
     // ------------------------------------------------------ softmax rows
     const int i = (warp - C::SOFT0) >> 2;
-    const long long r = r0 + i * 128 + (warp & 3) * 32 + lane;
+    const long long r = r0 + (C::DUAL ? 0 : i * 128) + (warp & 3) * 32 + lane;
     const bool live = r < live_rows;
     const bool any_live = r - lane < live_rows;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -386,7 +393,8 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
     const long long orow = ((long long)b * p.num_new + t) * p.Hq + (long long)kvh * p.G + (live ? (int)(r % p.G) : 0);
     // (rows behind the last take part with q = 0 and are not written)
     const int last = live ? before + t : 0x7fffffff;
-    if (i < nq && tiles) {
+    const int mine = C::DUAL ? (tiles + 1 - i) / 2 : tiles;  // this stream's key tiles
+    if (i < nq && mine) {
       // q to tensor memory, channels in the order the keys are unpacked in
       const uint4* src = reinterpret_cast<const uint4*>(p.q + orow * D);
 #pragma unroll
@@ -415,11 +423,11 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
     float m = -INFINITY, l = 0.f;  // reference maximum (log2 units) and sum
     bool going = i < nq;
 #pragma unroll 1
-    for (int j = 0; going && j < tiles; ++j) {
-      const int st = j % C::STAGES;
+    for (int n = 0; going && n < mine; ++n) {
+      const int j = C::DUAL ? 2 * n + i : n, st = j % C::STAGES;
       // (S follows the stage's arrival, so its key masks are there too; they
       // stay until P is handed over)
-      going = __all_sync(0xffffffffu, tc::mbar_wait(s_full(i), j & 1, stop));
+      going = __all_sync(0xffffffffu, tc::mbar_wait(s_full(i), n & 1, stop));
       if (!going) break;
       tc::fence_after();
       if (any_live) {
@@ -460,7 +468,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
           const float alpha = moves ? ex2(m - mn) : 1.f;
           m = mn;
           l *= alpha;
-          if (j) {
+          if (n) {
 #pragma unroll 1
             for (int h = 0; h < D / 16; ++h) {  // rare: few registers
               uint32_t o[16];
@@ -498,20 +506,65 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(p_full(i));
     }
-    if (going && tiles) going = __all_sync(0xffffffffu, tc::mbar_wait(o_full(i), 0, stop));
+    if (going && mine) going = __all_sync(0xffffffffu, tc::mbar_wait(o_full(i), 0, stop));
     tc::fence_after();
-    if (going && any_live) {
+    // The second stream hands its sum over in the stages' memory, once both
+    // streams' products are done with it: chunk c of row r at r, c ^ (r & 7).
+    const int rr = (warp & 3) * 32 + lane;
+    uint8_t* const other = smem + rr * (D * 4);
+    float a0 = 1.f, a1 = 0.f;  // the streams' factors
+    if (C::DUAL && going && tiles > 1) {
+      if (i == 1) {
+        going = __all_sync(0xffffffffu, tc::mbar_wait(o_full(0), 0, stop));
+        if (going && any_live) {
+#pragma unroll
+          for (int h = 0; h < D / 16; ++h) {
+            uint32_t o[16];
+            tc::ld16(to + h * 16, o);
+            tc::wait_ld();
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              *reinterpret_cast<uint4*>(other + (((h * 4 + e) ^ (rr & 7)) << 4)) =
+                  make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          }
+          sh.ml[rr] = make_float2(m, l);
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(merge);
+      } else {
+        going = __all_sync(0xffffffffu, tc::mbar_wait(merge, 0, stop));
+        if (going && any_live) {
+          const float2 x = sh.ml[rr];
+          const float mn = fmaxf(m, x.x), base = mn == -INFINITY ? 0.f : mn;
+          a0 = ex2(m - base);
+          a1 = ex2(x.x - base);
+          l = l * a0 + x.y * a1;
+          m = mn;
+        }
+      }
+    }
+    if (going && any_live && !(C::DUAL && i)) {
       const float inv = l != 0.f ? 1.f / l : 0.f;
       const long long w = orow * p.splits + split;
 #pragma unroll
       for (int h = 0; h < D / 32; ++h) {
         uint32_t o[32];
-        if (tiles) {
+        if (mine) {
           tc::ld32(to + h * 32, o);
           tc::wait_ld();
         } else {
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0;
+        }
+        if (C::DUAL && tiles > 1) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float4 y = *reinterpret_cast<const float4*>(other + (((h * 8 + e) ^ (rr & 7)) << 4));
+            const float z[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+              o[4 * e + g] = __float_as_uint(__uint_as_float(o[4 * e + g]) * a0 + z[g] * a1);
+          }
         }
         float x[32];  // place i of a chunk holds channel(i)
 #pragma unroll
@@ -663,89 +716,87 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
     bool ok = true;
     if constexpr (KIND != 2) {
       // A tile's rows come in runs of consecutive rows: one in a dense cache,
-      // one per page in a paged one.  Lane: array a of run r, r + 4, ...
-      const int a = lane & 7;  // K codes, V codes, K scale, K zero, V scale, V zero
-      const int hb = 2 * c.ngroups;
-      const bool have = a < 2 || a == 2 || a == 4 || (a < 6 && KIND == 0 && !c.sym);
-      const int which = a < 2 ? a : min((a - 2) >> 1, 1);
-      const uint8_t* array = a < 2 ? p.v.codes[which]
-                                   : reinterpret_cast<const uint8_t*>((a & 1) ? p.v.zero[which] : p.v.scale[which]);
-      const int size = a < 2 ? D * BITS / 8 : hb;  // bytes of a row
-      const int kind = a < 2 ? KVQ_ARRAY_K_CODES + which
-                             : (which ? KVQ_ARRAY_V_SCALE : KVQ_ARRAY_K_SCALE) + (a & 1);
-      const uint32_t place = a < 2 ? which * C::CODES : 2 * C::CODES + (a - 2) * C::HDR + mis;
+      // one per page (or part of one) in a paged one; lane r finds run r.
+      const int which = warp - 1;
+      const bool zeros = KIND == 0 && !c.sym, paged = c.layout == KVQ_PAGED;
+      const uint32_t hb = 2 * c.ngroups;
+      constexpr uint32_t RB = D * BITS / 8;
+      const uint8_t* const codes = p.v.codes[which];
+      const uint8_t* const scale = reinterpret_cast<const uint8_t*>(p.v.scale[which]);
+      const uint8_t* const zero = reinterpret_cast<const uint8_t*>(p.v.zero[which]);
       int slot = 0, ph = 1, j = 0;
 #pragma unroll 1
       for (; j < tiles; ++j) {
+        const int p0 = k0 + j * kKeys, p1 = min(p0 + kKeys, k1);
+        int start = p0, end = p1;
+        if (paged) {
+          const int blk = p0 / c.slots + lane;
+          start = min(max(p0, blk * c.slots), p1);  // (at most nine runs)
+          end = min(p1, (blk + 1) * c.slots);
+          if (lane > 8) start = end = p1;
+        } else if (lane) {
+          start = p1;
+        }
+        const int rows = end - start;
+        const long long row = rows > 0 ? token_row(c, b, kvh, start) : -1;
+        bool live = row >= 0;
+        live = live && KVQ_IN(c, KVQ_ARRAY_K_CODES + which, codes + row * RB, (long long)rows * RB) &&
+               KVQ_IN(c, which ? KVQ_ARRAY_V_SCALE : KVQ_ARRAY_K_SCALE, scale + row * hb, (long long)rows * hb) &&
+               (!zeros || KVQ_IN(c, which ? KVQ_ARRAY_V_ZERO : KVQ_ARRAY_K_ZERO, zero + row * hb, (long long)rows * hb));
+        // Whole 16-byte pieces: in a page, rows rounded up to 8 (the page has
+        // them); a dense header array starts mis bytes into one, and what its
+        // last piece holds is copied by hand.
+        const uint32_t up = paged ? (rows + 7) & ~7 : rows;
+        const uint32_t hdr = paged ? up * hb : (mis + rows * hb) & ~15u;
+        const uint32_t total = __reduce_add_sync(0xffffffffu, live ? up * RB + (zeros ? 2 : 1) * hdr : 0u);
         ok = __all_sync(0xffffffffu, tc::mbar_wait(raw_empty(slot), ph, stop));
         if (!ok) break;
-        const int p0 = k0 + j * kKeys, p1 = min(p0 + kKeys, k1);
-        const uint32_t dst = tc::smem_addr(smem + C::STAGES * C::STAGE + slot * C::RAW);
         uint8_t* const at = smem + C::STAGES * C::STAGE + slot * C::RAW;
-        const uint8_t* src[3];
-        uint32_t to[3], bytes[3], total = 0;
-        uint32_t dead0 = 0, dead1 = 0;  // keys without a row
-#pragma unroll
-        for (int u = 0; u < 3; ++u) {
-          const int r = u * 4 + (lane >> 3);
-          int start = p0, end = p1;
-          if (c.layout == KVQ_PAGED) {
-            const int blk = p0 / c.slots + r;
-            start = max(p0, blk * c.slots);
-            end = min(p1, (blk + 1) * c.slots);
-          } else if (r) {
-            start = p1;
-          }
-          bytes[u] = 0;
-          if (start >= end) continue;
-          const long long row = token_row(c, b, kvh, start);
-          int rows = end - start;
-          const uint8_t* from = array + max(row, 0ll) * size;
-          bool live = row >= 0;
-          if (live && have && !KVQ_IN(c, kind, from, (long long)rows * size)) live = false;
-          if (!live) {
-            const int k = start - p0, n = end - p0;  // keys k .. n - 1
-            dead0 |= (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u) & ~(k >= 32 ? 0xFFFFFFFFu : (1u << k) - 1u);
-            dead1 |= (n > 32 ? (n >= 64 ? 0xFFFFFFFFu : (1u << (n - 32)) - 1u) : 0u) &
-                     ~(k > 32 ? (1u << (k - 32)) - 1u : 0u);
+        uint8_t* const at_h = at + 2 * C::CODES + 2 * which * C::HDR;
+        if (which == 0) {  // which keys there are
+          uint32_t d0 = 0, d1 = 0;
+          if (rows > 0 && !live) {
+            const int k = start - p0, n = end - p0;  // keys k .. n - 1 have no row
+            d0 = (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u) & ~(k >= 32 ? 0xFFFFFFFFu : (1u << k) - 1u);
+            d1 = (n > 32 ? (n >= 64 ? 0xFFFFFFFFu : (1u << (n - 32)) - 1u) : 0u) &
+                 ~(k > 32 ? (1u << (k - 32)) - 1u : 0u);
             if (row < 0 && p.status) atomicOr(p.status, KVQ_FLAG_BLOCK_TABLE);
-            continue;
           }
-          if (!have) continue;
-          // Whole 16-byte pieces.  In a page that is rows rounded up to 8 (the
-          // page has them); a dense header array starts mis bytes into one,
-          // and what its last piece holds is copied by hand.
-          src[u] = from;
-          to[u] = dst + place + (start - p0) * size;
-          if (c.layout == KVQ_PAGED) {
-            bytes[u] = ((rows + 7) & ~7) * size;
-          } else if (a < 2) {
-            bytes[u] = rows * size;
-          } else {
-            const int n = mis + rows * size;
-            src[u] -= mis;
-            to[u] -= mis;
-            bytes[u] = n & ~15;
-            for (int x = max(n & ~15, mis); x < n; x += 2)
-              *reinterpret_cast<unsigned short*>(at + place - mis + x) =
-                  *reinterpret_cast<const unsigned short*>(src[u] + x);
+          const int n = p1 - p0;
+          d0 = __reduce_or_sync(0xffffffffu, d0);
+          d1 = __reduce_or_sync(0xffffffffu, d1);
+          if (lane == 0) {
+            sh.raw_ok[slot][0] = (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u) & ~d0;
+            sh.raw_ok[slot][1] = (n > 32 ? (n >= 64 ? 0xFFFFFFFFu : (1u << (n - 32)) - 1u) : 0u) & ~d1;
           }
-          total += bytes[u];
         }
-        total = __reduce_add_sync(0xffffffffu, total);
-        dead0 = __reduce_or_sync(0xffffffffu, dead0);
-        dead1 = __reduce_or_sync(0xffffffffu, dead1);
-        const int n = p1 - p0;
-        if (lane == 0) {
-          sh.raw_ok[slot][0] = (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u) & ~dead0;
-          sh.raw_ok[slot][1] = (n > 32 ? (n >= 64 ? 0xFFFFFFFFu : (1u << (n - 32)) - 1u) : 0u) & ~dead1;
+        uint32_t todo = __ballot_sync(0xffffffffu, live);
+        const int n = mis + (p1 - p0) * (int)hb;
+        if (!paged && (n & 15) && todo) {
+          const int x = (n & ~15) + 2 * lane;
+          const long long from = (((long long)b * c.Hkv + kvh) * c.slots + p0) * hb - mis + x;
+          if (x >= mis && x < n) {
+            *reinterpret_cast<unsigned short*>(at_h + x) = *reinterpret_cast<const unsigned short*>(scale + from);
+            if (zeros)
+              *reinterpret_cast<unsigned short*>(at_h + C::HDR + x) = *reinterpret_cast<const unsigned short*>(zero + from);
+          }
         }
         __syncwarp();
         if (lane == 0) tc::mbar_arrive_expect(raw_full(slot), total);
         __syncwarp();
-#pragma unroll
-        for (int u = 0; u < 3; ++u)
-          if (bytes[u]) tc::bulk_load(to[u], src[u], bytes[u], raw_full(slot));
+        const uint32_t dst = tc::smem_addr(at) + which * C::CODES, dst_h = tc::smem_addr(at_h);
+        while (todo) {
+          const int r = __ffs(todo) - 1;
+          todo &= todo - 1;
+          const long long row_r = __shfl_sync(0xffffffffu, row, r);
+          const uint32_t key = __shfl_sync(0xffffffffu, start, r) - p0;
+          const uint32_t up_r = __shfl_sync(0xffffffffu, up, r), hdr_r = __shfl_sync(0xffffffffu, hdr, r);
+          tc::bulk_load(dst + key * RB, codes + row_r * RB, up_r * RB, raw_full(slot));
+          if (hdr_r) {
+            tc::bulk_load(dst_h + key * hb, scale + row_r * hb - mis, hdr_r, raw_full(slot));
+            if (zeros) tc::bulk_load(dst_h + C::HDR + key * hb, zero + row_r * hb - mis, hdr_r, raw_full(slot));
+          }
+        }
         if (++slot == C::DEPTH) slot = 0, ph ^= 1;
       }
       // after a wait that ran out: nothing in flight when the block ends
@@ -791,37 +842,39 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
     // the warps take turns, so that one tile's softmax runs under the other
     // tile's products and not beside its softmax
     auto pass = [&] {
-      if (nq == 2 && lane == 0) tc::mbar_arrive(turn(1 - i));
+      if (!C::DUAL && nq == 2 && lane == 0) tc::mbar_arrive(turn(1 - i));
       __syncwarp();
     };
-    if (i < nq && wait(full(0), 0) && wait(q_full(i), 0) && (i == 0 || wait(turn(1), 0))) {
+    const int j0 = C::DUAL ? i : 0;  // this stream's first key tile
+    if (i < nq && j0 < tiles && wait(full(j0), 0) && wait(q_full(i), 0) && (C::DUAL || i == 0 || wait(turn(1), 0))) {
       tc::fence_after();
-      qk(0);
+      qk(j0);
       pass();
-      int st = 0, ph = 0, tp = i;  // stage of key tile j and its phase; phase of the turn
+      int st = j0, tp = i;  // stage of key tile j; phase of the turn
 #pragma unroll 1
-      for (int j = 0;; ++j) {
-        const bool more = j + 1 < tiles;
-        const int st1 = st + 1 == C::STAGES ? 0 : st + 1, ph1 = st1 ? ph : ph ^ 1;
-        if (more && !wait(full(st1), ph1)) break;
-        if (!wait(p_full(i), j & 1)) break;
-        if (nq == 2 && !wait(turn(i), tp)) break;
+      for (int j = j0, n = 0;; j += STEP, ++n) {
+        const int next = j + STEP;
+        const bool more = next < tiles;
+        const int st1 = next % C::STAGES;
+        if (!C::DUAL && more && !wait(full(st1), (next / C::STAGES) & 1)) break;
+        if (!wait(p_full(i), n & 1)) break;
+        if (!C::DUAL && nq == 2 && !wait(turn(i), tp)) break;
         tp ^= 1;
         tc::fence_after();
         const uint32_t vd = v_lo + st * (C::STAGE / 16);
 #pragma unroll
         for (int kk = 0; kk < kKeys / 16; ++kk)
-          tc::mma_ts(d_o, d_s + kk * 8, vd + kk * (2048 / 16), hi, id_pv, j || kk);
+          tc::mma_ts(d_o, d_s + kk * 8, vd + kk * (2048 / 16), hi, id_pv, n || kk);
         if (!more) {
           tc::commit(o_full(i));
           pass();
           break;
         }
         tc::commit(empty(st));
+        if (C::DUAL && !wait(full(st1), (next / C::STAGES) & 1)) break;
         qk(st1);
         pass();
         st = st1;
-        ph = ph1;
       }
     }
   }
