@@ -164,7 +164,7 @@ SIGNATURES = {
                                     c_void_p, c_void_p, c_void_p, c_size_t, c_void_p, c_void_p]),
     "kvq_pages_compact": (c_int32, [POINTER(kvq_page_pool), c_void_p, c_void_p, c_void_p,
                                     c_void_p, c_size_t, c_void_p, c_void_p]),
-    "kvq_pages_copy": (c_int32, [POINTER(kvq_cache_desc), POINTER(kvq_cache), c_int32, c_void_p,
+    "kvq_pages_copy": (c_int32, [POINTER(kvq_cache_desc), c_void_p, c_int32, c_void_p,
                                  c_void_p, c_int32, c_void_p, c_void_p]),
     "kvq_debug_checks": (c_int32, []),
     "kvq_debug_shrink_extent": (c_int32, [c_int32, c_int64]),

@@ -45,6 +45,22 @@ __device__ __forceinline__ int block_scan(int x, int* scratch, int* total) {
   return r;
 }
 
+// Which of pages i .. i + 3 (i a multiple of 4) exist and have count 0, and
+// count > 0, as bits.
+__device__ __forceinline__ void states4(const kvq_page_pool& pl, int i, int* free4, int* live4) {
+  int c[4] = {-1, -1, -1, -1};
+  if (i + 4 <= pl.num_pages) {
+    const int4 v = *reinterpret_cast<const int4*>(pl.ref_count + i);
+    c[0] = v.x, c[1] = v.y, c[2] = v.z, c[3] = v.w;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (i + e < pl.num_pages) c[e] = pl.ref_count[i + e];
+  }
+  *free4 = (c[0] == 0) | (c[1] == 0) << 1 | (c[2] == 0) << 2 | (c[3] == 0) << 3;
+  *live4 = (c[0] > 0) | (c[1] > 0) << 1 | (c[2] > 0) << 2 | (c[3] > 0) << 3;
+}
+
 // ---- reorder ----------------------------------------------------------
 
 // One CTA per group of `cols` table columns: the columns of every row are
@@ -132,13 +148,16 @@ __device__ __forceinline__ int entry(const PoolParams& p, int b, int j) {
 
 // One CTA.  Shared: mine[b] = the mapped partial page of b (-1: none), later
 // whether it is replaced; at[b] = exclusive prefix of the pages needed.
-__global__ void __launch_bounds__(kOne) reserve_kernel(const __grid_constant__ PoolParams p) {
+__global__ void __launch_bounds__(kOne) reserve_kernel(const __grid_constant__ PoolParams p, int lps) {
   pdl_launch_dependents();
   pdl_wait();
   extern __shared__ int32_t sh[];
   __shared__ int scratch[33];
   const kvq_page_pool& pl = p.pool;
-  const int B = pl.batch, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // a group of lps lanes (4 .. 32) per sequence: as many as it touches blocks
+  const int B = pl.batch, groups = kOne / lps, group = threadIdx.x / lps, gl = threadIdx.x % lps;
+  const int shift = threadIdx.x & 31 & ~(lps - 1);  // the group's first lane
+  const unsigned all = lps == 32 ? 0xffffffffu : (1u << lps) - 1u;
   const long long M = pl.max_blocks_per_seq;
   int32_t* mine = sh;
   int32_t* at = sh + B;
@@ -168,18 +187,20 @@ __global__ void __launch_bounds__(kOne) reserve_kernel(const __grid_constant__ P
   __syncthreads();
   for (int b = threadIdx.x; b < B; b += kOne) mine[b] = at[b];
   __syncthreads();
-  // pages needed per sequence: a warp each
-  for (int b = warp; b < B; b += kOne / 32) {
-    const Ask a = ask_of(p, b);
+  // pages needed per sequence
+  for (int b0 = 0; b0 < B; b0 += groups) {
+    const int b = b0 + group;
     int need = 0;
-    for (int j = a.first + lane; j < a.last; j += 32) {
-      const int e = entry(p, b, j);
-      const bool part = j == a.first && a.partial;
-      need += e < 0 ? 1 : (part ? mine[b] : pl.ref_count[e] > 1);
+    if (b < B) {
+      const Ask a = ask_of(p, b);
+      for (int j = a.first + gl; j < a.last; j += lps) {
+        const int e = entry(p, b, j);
+        const bool part = j == a.first && a.partial;
+        need += e < 0 ? 1 : (part ? mine[b] : pl.ref_count[e] > 1);
+      }
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) need += __shfl_xor_sync(0xffffffffu, need, o);
-    if (lane == 0) at[b] = need;
+    for (int o = lps >> 1; o; o >>= 1) need += __shfl_xor_sync(0xffffffffu, need, o);
+    if (gl == 0 && b < B) at[b] = need;
   }
   __syncthreads();
   int total = 0;
@@ -192,42 +213,46 @@ __global__ void __launch_bounds__(kOne) reserve_kernel(const __grid_constant__ P
   }
   // the lowest free pages, in order
   int found = 0;
-  for (int i0 = 0; i0 < pl.num_pages && found < total; i0 += kOne) {
-    const int i = i0 + threadIdx.x;
-    const int is_free = i < pl.num_pages && pl.ref_count[i] == 0;
-    int sum;
-    const int ex = block_scan(is_free, scratch, &sum);
-    if (is_free && found + ex < total) p.ws[found + ex] = i;
+  for (int i0 = 0; i0 < pl.num_pages && found < total; i0 += 4 * kOne) {
+    const int i = i0 + 4 * threadIdx.x;
+    int free4 = 0, live4 = 0, sum;
+    if (i < pl.num_pages) states4(pl, i, &free4, &live4);
+    int at_free = found + block_scan(__popc(free4), scratch, &sum);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if ((free4 >> e & 1) && at_free < total) p.ws[at_free] = i + e, ++at_free;
     found += sum;
   }
   __syncthreads();
   const bool ok = found >= total;
   if (!ok && threadIdx.x == 0) flags |= KVQ_FLAG_POOL_EMPTY;
-  for (int b = warp; b < B; b += kOne / 32) {
-    const Ask a = ask_of(p, b);
-    int src = -1, dst = -1, next = at[b];
-    if (ok) {
-      for (int j0 = a.first; j0 < a.last; j0 += 32) {
-        const int j = j0 + lane;
-        const int e = j < a.last ? entry(p, b, j) : 0;
-        const bool part = j == a.first && a.partial;
-        const bool take = j < a.last && (e < 0 || (part ? mine[b] != 0 : pl.ref_count[e] > 1));
-        const unsigned who = __ballot_sync(0xffffffffu, take);
-        if (take) {
-          const int rank = next + __popc(who & ((1u << lane) - 1));
-          const int page = p.ws[rank];
-          pl.block_table[(long long)b * M + j] = page;
-          pl.ref_count[page] = 1;
-          p.ws[pl.num_pages + rank] = e;
-          if (e >= 0 && part) {
-            src = e;
-            dst = page;
-          }
+  for (int b0 = 0; b0 < B; b0 += groups) {
+    const int b = b0 + group;
+    Ask a{0, 0, 0, false, 0u};
+    if (b < B) a = ask_of(p, b);
+    int src = -1, dst = -1, next = b < B ? at[b] : 0;
+    // (as many rounds as the warp's longest group: the ballot needs all lanes)
+    for (int j0 = a.first; __any_sync(0xffffffffu, ok && j0 < a.last); j0 += lps) {
+      const int j = j0 + gl;
+      const bool mine_j = ok && j < a.last;
+      const int e = mine_j ? entry(p, b, j) : 0;
+      const bool part = j == a.first && a.partial;
+      const bool take = mine_j && (e < 0 || (part ? mine[b] != 0 : pl.ref_count[e] > 1));
+      const unsigned who = (__ballot_sync(0xffffffffu, take) >> shift) & all;
+      if (take) {
+        const int rank = next + __popc(who & ((1u << gl) - 1));
+        const int page = p.ws[rank];
+        pl.block_table[(long long)b * M + j] = page;
+        pl.ref_count[page] = 1;
+        p.ws[pl.num_pages + rank] = e;
+        if (e >= 0 && part) {
+          src = e;
+          dst = page;
         }
-        next += __popc(who);
       }
+      next += __popc(who);
     }
-    if (lane == 0) {  // the partial block is the first one: lane 0 of the first pass
+    if (gl == 0 && b < B) {  // the partial block is the first one: lane 0 of the first round
       p.copy_src[b] = src;
       p.copy_dst[b] = dst;
       if (p.granted) p.granted[b] = ok ? a.n : 0;
@@ -254,23 +279,34 @@ __global__ void __launch_bounds__(kOne) compact_kernel(const __grid_constant__ P
   const kvq_page_pool& pl = p.pool;
   const int N = pl.num_pages, half = N / 2;
   int n = 0;
-  for (int i0 = 0; i0 < N; i0 += kOne) {
-    const int i = i0 + threadIdx.x;
-    n += __syncthreads_count(i < N && pl.ref_count[i] > 0);
+  {
+    int mine = 0, sum;
+    for (int i = 4 * threadIdx.x; i < N; i += 4 * kOne) {
+      int free4, live4;
+      states4(pl, i, &free4, &live4);
+      mine += __popc(live4);
+    }
+    block_scan(mine, scratch, &sum);
+    n = sum;
   }
   int movers = 0, holes = 0;
-  for (int i0 = 0; i0 < N; i0 += kOne) {
-    const int i = i0 + threadIdx.x;
-    const bool live = i < N && pl.ref_count[i] > 0;
-    const int mover = live && i >= n, hole = i < n && !live;
-    int sum;
-    const int ex = block_scan(mover | (hole << 16), scratch, &sum);
-    const int km = movers + (ex & 0xffff), kh = holes + (ex >> 16);
-    if (mover) {
-      p.copy_src[km] = i;
-      p.ws[i] = km;
+  for (int i0 = 0; i0 < N; i0 += 4 * kOne) {
+    const int i = i0 + 4 * threadIdx.x;
+    int free4 = 0, live4 = 0, sum;
+    if (i < N) states4(pl, i, &free4, &live4);
+    const int exist = i >= N ? 0 : i + 4 <= N ? 15 : (1 << (N - i)) - 1;
+    const int before = n <= i ? 0 : n >= i + 4 ? 15 : (1 << (n - i)) - 1;  // of them, in front of the border
+    const int mover = live4 & ~before, hole = exist & before & ~live4;
+    const int ex = block_scan(__popc(mover) | (__popc(hole) << 16), scratch, &sum);
+    int km = movers + (ex & 0xffff), kh = holes + (ex >> 16);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (mover >> e & 1) {
+        p.copy_src[km] = i + e;
+        p.ws[i + e] = km++;
+      }
+      if (hole >> e & 1) p.copy_dst[kh++] = i + e;
     }
-    if (hole) p.copy_dst[kh] = i;
     movers += sum & 0xffff;
     holes += sum >> 16;
   }
@@ -301,7 +337,8 @@ __global__ void __launch_bounds__(kOne) compact_kernel(const __grid_constant__ P
 // ---- copy -------------------------------------------------------------
 
 // Grid: x = pairs, y = layers.
-__global__ void __launch_bounds__(128) copy_kernel(const __grid_constant__ PageCopyParams p) {
+constexpr int kCopyThreads = 128, kCopyLoads = 8;
+__global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ PageCopyParams p) {
   pdl_launch_dependents();
   pdl_wait();
   const int i = blockIdx.x, layer = blockIdx.y;
@@ -312,13 +349,29 @@ __global__ void __launch_bounds__(128) copy_kernel(const __grid_constant__ PageC
     if (report && threadIdx.x == 0) flag(p.status, KVQ_FLAG_BLOCK_TABLE);
     return;
   }
+  // the arrays' pieces of 16 bytes in one row, eight loads of a thread in flight
+  uint32_t ends[6], total = 0;
 #pragma unroll
-  for (int a = 0; a < 6; ++a) {
-    const uint32_t n = p.bytes[a] / 16;
-    if (!n) continue;
-    const uint4* from = reinterpret_cast<const uint4*>(p.base[layer][a] + (size_t)s * p.bytes[a]);
-    uint4* to = reinterpret_cast<uint4*>(p.base[layer][a] + (size_t)d * p.bytes[a]);
-    for (uint32_t k = threadIdx.x; k < n; k += blockDim.x) to[k] = from[k];
+  for (int a = 0; a < 6; ++a) ends[a] = total += p.bytes[a] / 16;
+  for (uint32_t k0 = threadIdx.x; k0 < total; k0 += kCopyThreads * kCopyLoads) {
+    uint4 v[kCopyLoads];
+    uint4* to[kCopyLoads];
+#pragma unroll
+    for (int u = 0; u < kCopyLoads; ++u) {
+      const uint32_t k = k0 + u * kCopyThreads;
+      to[u] = nullptr;
+      if (k >= total) continue;
+      uint8_t* base = p.base[layer][0];
+      uint32_t bytes = p.bytes[0], first = 0;
+#pragma unroll
+      for (int a = 1; a < 6; ++a)
+        if (k >= ends[a - 1]) base = p.base[layer][a], bytes = p.bytes[a], first = ends[a - 1];
+      v[u] = *(reinterpret_cast<const uint4*>(base + (size_t)s * bytes) + (k - first));
+      to[u] = reinterpret_cast<uint4*>(base + (size_t)d * bytes) + (k - first);
+    }
+#pragma unroll
+    for (int u = 0; u < kCopyLoads; ++u)
+      if (to[u]) *to[u] = v[u];
   }
   if (report) {
     uint32_t flags = d == s ? KVQ_FLAG_PAGE_LIST : 0u;
@@ -333,6 +386,22 @@ __global__ void __launch_bounds__(128) copy_kernel(const __grid_constant__ PageC
 
 }  // namespace
 
+// launch_pdl for a kernel with one more integer
+static cudaError_t launch_int(void (*kernel)(PoolParams, int), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                              const PoolParams& p, int x) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p, x);
+}
+
 cudaError_t launch_pages_reorder(const PoolParams& p, cudaStream_t stream) {
   // a CTA holds its columns of every row: as many as fit 128 KB, at most 32
   int cols = 32;
@@ -342,17 +411,7 @@ cudaError_t launch_pages_reorder(const PoolParams& p, cudaStream_t stream) {
                                        128 * 1024);
   if (e != cudaSuccess) return e;
   const unsigned grid = (unsigned)((p.pool.max_blocks_per_seq + cols - 1) / cols);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, reorder_kernel, p, cols);
+  return launch_int(reorder_kernel, dim3(grid), dim3(256), smem, stream, p, cols);
 }
 
 cudaError_t launch_pages_reserve(const PoolParams& p, cudaStream_t stream) {
@@ -360,7 +419,9 @@ cudaError_t launch_pages_reserve(const PoolParams& p, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(reserve_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        KVQ_MAX_POOL_BATCH * 8);
   if (e != cudaSuccess) return e;
-  return launch_pdl(reserve_kernel, dim3(1), dim3(kOne), smem, stream, p);
+  int lps = 4;
+  while (lps < 32 && lps < p.num_new / p.pool.page_size + 2) lps *= 2;
+  return launch_int(reserve_kernel, dim3(1), dim3(kOne), smem, stream, p, lps);
 }
 
 cudaError_t launch_pages_compact(const PoolParams& p, cudaStream_t stream) {
@@ -368,7 +429,7 @@ cudaError_t launch_pages_compact(const PoolParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_pages_copy(const PageCopyParams& p, cudaStream_t stream) {
-  return launch_pdl(copy_kernel, dim3(p.num_pairs, p.layers), dim3(128), 0, stream, p);
+  return launch_pdl(copy_kernel, dim3(p.num_pairs, p.layers), dim3(kCopyThreads), 0, stream, p);
 }
 
 }  // namespace kvq

@@ -7,13 +7,15 @@ device, on its current stream unless `stream` is given.
 """
 from __future__ import annotations
 
-from ctypes import POINTER, byref, c_uint64, cast
+from array import array
+from ctypes import byref
 from dataclasses import dataclass
+from operator import attrgetter
 
 import torch
 
 from . import _lib
-from ._lib import ROPE_SCALING, kvq_cache, kvq_page_pool, kvq_rope, kvq_rope_desc
+from ._lib import ROPE_SCALING, kvq_page_pool, kvq_rope, kvq_rope_desc
 from .api import KVCache, _ptr
 
 
@@ -343,6 +345,9 @@ def kvq_pages_compact(pool: PagePool, move_src: torch.Tensor, move_dst: torch.Te
     _lib.check(st, "kvq_pages_compact")
 
 
+_PAGED_ARRAYS = attrgetter("k_codes", "v_codes", "k_scale", "k_zero", "v_scale", "v_zero")
+
+
 def kvq_pages_copy(caches, copy_src: torch.Tensor, copy_dst: torch.Tensor,
                    dev_status: torch.Tensor | None = None, stream=None) -> None:
     """Page copy_dst[i] takes the bytes of page copy_src[i] in every cache of
@@ -356,17 +361,22 @@ def kvq_pages_copy(caches, copy_src: torch.Tensor, copy_dst: torch.Tensor,
     _status(dev_status, dev)
     desc = caches[0].desc
     first = bytes(desc)
+    tail = [0 if t is None else t.data_ptr() for t in
+            (caches[0].block_table, caches[0].k_window, caches[0].v_window)]
     flat = []
     for c in caches:
-        if c.k_codes.get_device() != dev:
+        kc, vc, ks, kz, vs, vz = _PAGED_ARRAYS(c)
+        if kc.get_device() != dev:
             _same_cache_device(c, dev)
         if c.desc is not desc and bytes(c.desc) != first:
             raise ValueError("the caches must have one descriptor")
-        flat += [0 if t is None else t.data_ptr() for t in
-                 (c.k_codes, c.v_codes, c.k_scale, c.k_zero, c.v_scale, c.v_zero, c.block_table, c.k_window,
-                  c.v_window)]
-    # (the pointers of the kvq_cache structures one after the other)
-    arrays = cast((c_uint64 * len(flat))(*flat), POINTER(kvq_cache))
+        flat += (kc.data_ptr(), vc.data_ptr(), 0 if ks is None else ks.data_ptr(),
+                 0 if kz is None else kz.data_ptr(), 0 if vs is None else vs.data_ptr(),
+                 0 if vz is None else vz.data_ptr())
+        flat += tail  # (not touched by the copy)
+    # the kvq_cache structures: their pointers one after the other
+    structs = array("Q", flat)
+    arrays = structs.buffer_info()[0]
     with _on(dev):
         st = _lib.lib().kvq_pages_copy(byref(caches[0].desc), arrays, len(caches), _ptr(copy_src),
                                        _ptr(copy_dst), copy_src.numel(), _ptr(dev_status),
