@@ -77,7 +77,39 @@ struct ExtendChoice {
   int32_t splits = 0;
 };
 
-// Splits spread a call with few row tiles over the device.
+// Splits spread a call with few row tiles over the device, and even out
+// sequences of different lengths.  The automatic choice weighs, in positions
+// of a CTA's work: equal sequences, whose CTAs run in whole waves; and (with
+// several sequences) lengths spread over the range up to max_seq_len, where
+// about 0.6 of the CTAs have keys and the last ones half overlap.  A CTA
+// costs kFixed positions beside its own (set-up, filling the pipeline,
+// writing out), the partials their bytes written and read: 13 ns a position
+// with one tile of rows, 20 with two, 6800 bytes a ns.
+constexpr int64_t kFixed = 384;
+int32_t choose_extend_splits(int64_t units, int64_t max_len, int64_t rows, int64_t D, bool several, int requested,
+                             const ExtendPlan& plan) {
+  const int64_t L = std::max<int64_t>(max_len, 1);
+  if (requested > 0) return choose_splits(units, max_len, requested, 0);
+  const int sms = sm_count();
+  if (sms <= 0 || plan.occ <= 0) return 0;
+  const double slots = (double)sms * plan.occ, ns = plan.kind == 2 ? 20.0 : 13.0;
+  const int64_t cap = std::max<int64_t>(1, std::min<int64_t>(ceil_div(L, 256), 64));
+  int64_t best = 1;
+  double best_cost = 1e300;
+  for (int64_t c = 1; c <= cap; ++c) {
+    const int64_t chunk = split_chunk(L, (int32_t)c), eff = ceil_div(L, chunk);
+    const double waves = (double)std::max<int64_t>(units, 1) * eff / slots, each = (double)(chunk + kFixed);
+    const double equal = ceil(waves) * each, spread = std::max(1.0, 0.6 * waves + 0.5) * each;
+    const double join = eff > 1 ? (double)rows * D * 8.0 * eff / 6800.0 / ns : 0.0;
+    const double cost = (several ? 0.5 * (equal + spread) : equal) + join;
+    if (cost < best_cost * 0.999) {
+      best_cost = cost;
+      best = eff;
+    }
+  }
+  return (int32_t)best;
+}
+
 kvq_status choose_extend(const kvq_cache_desc* desc, const CacheGeom& g, int32_t batch,
                          int32_t num_new, int32_t num_q_heads, int32_t max_seq_len,
                          int32_t requested, ExtendChoice* out) {
@@ -86,7 +118,8 @@ kvq_status choose_extend(const kvq_cache_desc* desc, const CacheGeom& g, int32_t
   if (e != cudaSuccess) return from_cuda(e);
   const int64_t tiles = ceil_div((int64_t)num_new * G, out->plan.tile_rows);
   const int64_t units = tiles * desc->num_kv_heads * std::max(batch, 1);
-  out->splits = choose_splits(units, max_seq_len, requested, out->plan.occ);
+  out->splits = choose_extend_splits(units, max_seq_len, (int64_t)batch * num_new * num_q_heads, desc->head_dim,
+                                     batch > 1, requested, out->plan);
   if (tiles * out->splits > INT32_MAX) return KVQ_ERR_UNSUPPORTED;
   return out->splits > 0 ? KVQ_OK : KVQ_ERR_CUDA;
 }

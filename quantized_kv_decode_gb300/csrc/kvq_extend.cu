@@ -223,32 +223,62 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const __grid_constant_
   }
 }
 
-// out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s of each live row; one
-// CTA of D threads per (sequence, new token, head).
+// out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s of each live row
+// (sequence, new token, head): D / 4 threads a row, four channels each, the
+// partials of kMergeSplits splits in flight.  Bound by memory once rows are
+// many (a CTA of D threads per row took 135 us for 131072 rows of two splits,
+// 134 MB).
+constexpr int kMergeSplits = 4;
 __global__ void __launch_bounds__(256) extend_merge_kernel(const __grid_constant__ ExtendParams p) {
   pdl_launch_dependents();
   pdl_wait();
   const CacheGeom& c = p.v.geom;
-  const long long row = blockIdx.x;
-  const int b = (int)(row / p.Hq / p.num_new);
-  const int t = (int)(row / p.Hq - (long long)b * p.num_new);
+  const int per = c.D / 4;  // 16, 32 or 64
+  const long long row = (long long)blockIdx.x * (256 / per) + threadIdx.x / per;
+  if (row >= (long long)p.batch * p.num_new * p.Hq) return;
+  const long long tok = row / p.Hq;
+  const int b = (int)(tok / p.num_new), t = (int)(tok - (long long)b * p.num_new);
   if (t >= new_rows_of(p.new_lens, b, p.num_new)) return;
-  const int D = c.D, d = threadIdx.x;
+  const int D = c.D, d = threadIdx.x % per * 4;
   const float2* ml = reinterpret_cast<const float2*>(p.ws_ml) + row * p.splits;
   const float* o = p.ws_o + row * p.splits * D + d;
-  float M = -INFINITY, num = 0.f, den = 0.f;
-  for (int s = 0; s < p.splits; ++s) {
-    if (!KVQ_IN(c, KVQ_ARRAY_WORKSPACE, ml + s, 8) || !KVQ_IN(c, KVQ_ARRAY_WORKSPACE, o + (long long)s * D, 4))
-      continue;
-    const float2 v = ml[s];
-    if (v.x == -INFINITY && v.y == 0.f) continue;  // nothing seen: o is zero, m no reference
-    const float Mn = fmaxf(M, v.x), a = ex2(M - Mn), f = ex2(v.x - Mn);
-    num = num * a + f * o[(long long)s * D];
-    den = den * a + f * v.y;
+  float M = -INFINITY, den = 0.f;
+  float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = 0; s0 < p.splits; s0 += kMergeSplits) {
+    float2 v[kMergeSplits];
+    float4 x[kMergeSplits];
+    float Mn = M;
+#pragma unroll
+    for (int u = 0; u < kMergeSplits; ++u) {
+      const int s = s0 + u;
+      v[u] = make_float2(-INFINITY, 0.f);
+      x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (s < p.splits && KVQ_IN(c, KVQ_ARRAY_WORKSPACE, ml + s, 8) &&
+          KVQ_IN(c, KVQ_ARRAY_WORKSPACE, o + (long long)s * D, 16)) {
+        v[u] = ml[s];
+        x[u] = *reinterpret_cast<const float4*>(o + (long long)s * D);
+      }
+      Mn = fmaxf(Mn, v[u].x);
+    }
+    const float base = Mn == -INFINITY ? 0.f : Mn, a = ex2(M - base);
+    num = make_float4(num.x * a, num.y * a, num.z * a, num.w * a);
+    den *= a;
+#pragma unroll
+    for (int u = 0; u < kMergeSplits; ++u) {
+      if (v[u].x == -INFINITY && v[u].y == 0.f) continue;  // nothing seen there
+      const float f = ex2(v[u].x - base);
+      num.x = fmaf(f, x[u].x, num.x);
+      num.y = fmaf(f, x[u].y, num.y);
+      num.z = fmaf(f, x[u].z, num.z);
+      num.w = fmaf(f, x[u].w, num.w);
+      den = fmaf(f, v[u].y, den);
+    }
     M = Mn;
   }
-  if (KVQ_IN(c, KVQ_ARRAY_OUT, p.out + row * D + d, 2))
-    p.out[row * D + d] = __float2half_rn(den > 0.f ? num / den : 0.f);
+  const float inv = den != 0.f ? 1.f / den : 0.f;
+  uint2* to = reinterpret_cast<uint2*>(p.out + row * D + d);
+  if (KVQ_IN(c, KVQ_ARRAY_OUT, to, 8))
+    *to = make_uint2(fast::pack_h2(num.x * inv, num.y * inv), fast::pack_h2(num.z * inv, num.w * inv));
 }
 
 template <int BITS, int D>
@@ -311,7 +341,8 @@ cudaError_t launch_extend(const ExtendParams& p, const ExtendPlan& plan, cudaStr
                                  : run_tc_any(p.v.geom, plan.kind, &p, nullptr, stream);
   if (e == cudaSuccess && p.splits > 1) {
     const long long rows = (long long)p.batch * p.num_new * p.Hq;
-    e = launch_pdl(extend_merge_kernel, dim3((unsigned)rows), dim3(p.v.geom.D), 0, stream, p);
+    const int per = 256 / (p.v.geom.D / 4);
+    e = launch_pdl(extend_merge_kernel, dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0, stream, p);
   }
   return e;
 }

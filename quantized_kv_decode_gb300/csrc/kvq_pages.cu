@@ -66,7 +66,7 @@ __device__ __forceinline__ void states4(const kvq_page_pool& pl, int i, int* fre
 // One CTA per group of `cols` table columns: the columns of every row are
 // read to shared memory, then written through parent[], so the table changes
 // in place.  Counts: -1 for every old entry, +1 for every new one.
-__global__ void __launch_bounds__(256) reorder_kernel(const __grid_constant__ PoolParams p, int cols) {
+__global__ void __launch_bounds__(1024) reorder_kernel(const __grid_constant__ PoolParams p, int cols) {
   pdl_launch_dependents();
   pdl_wait();
   extern __shared__ int32_t old[];  // [batch][cols]
@@ -403,15 +403,19 @@ static cudaError_t launch_int(void (*kernel)(PoolParams, int), dim3 grid, dim3 b
 }
 
 cudaError_t launch_pages_reorder(const PoolParams& p, cudaStream_t stream) {
-  // a CTA holds its columns of every row: as many as fit 128 KB, at most 32
+  // A CTA holds its columns of every row: as many as fit 128 KB, at most 32,
+  // and down to 4 (half a sector a row) while there are fewer CTAs than SMs
+  // (256 rows of 190 blocks: 43 us with 32 columns a CTA and 256 threads).
   int cols = 32;
-  while (cols > 1 && (size_t)p.pool.batch * cols * 4 > 128 * 1024) cols >>= 1;
+  while (cols > 1 && ((size_t)p.pool.batch * cols * 4 > 128 * 1024 ||
+                      (cols > 4 && p.pool.max_blocks_per_seq < 152 * cols)))
+    cols >>= 1;
   const size_t smem = (size_t)p.pool.batch * cols * 4;
   cudaError_t e = cudaFuncSetAttribute(reorder_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        128 * 1024);
   if (e != cudaSuccess) return e;
   const unsigned grid = (unsigned)((p.pool.max_blocks_per_seq + cols - 1) / cols);
-  return launch_int(reorder_kernel, dim3(grid), dim3(256), smem, stream, p, cols);
+  return launch_int(reorder_kernel, dim3(grid), dim3(1024), smem, stream, p, cols);
 }
 
 cudaError_t launch_pages_reserve(const PoolParams& p, cudaStream_t stream) {
