@@ -617,8 +617,14 @@ KVQ_API kvq_status kvq_decode_attn_static_ws(const kvq_cache_desc* desc, const k
  *   seq_lens / seq_lens_before   batch int32;
  *   workspace      workspace_bytes (the static array for the
  *                  _static_ws call).
- * Every global load and store of the kernels first checks that its bytes lie
- * inside the extent of the array it addresses.  An access that does not is
+ *   kvq_cache_read: k_out and v_out as k_new and v_new with num_rows tokens;
+ *   kvq_extend_attn: q and out batch * num_new rows; kvq_rope_append: k_new
+ *   and v_new.  The other arrays of the prompt and pool calls (q of the
+ *   rotations, positions, new_lens, start, the pool's and the copy lists) are
+ *   read and written at indexes the kernels have checked against the sizes
+ *   given, in every build, and carry no extents.
+ * Every global load and store of the arrays above first checks that its bytes
+ * lie inside the extent of the array it addresses.  An access that does not is
  * skipped (a load yields zeros), and KVQ_FLAG_OOB is OR-ed into *dev_status
  * (when dev_status is not NULL).  The checks cost time; results are otherwise
  * those of the release library, which never sets KVQ_FLAG_OOB.

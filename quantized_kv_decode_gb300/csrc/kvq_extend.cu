@@ -29,7 +29,7 @@ constexpr int kThreads = 128;
 // Keys per tile: K and V rows as fp16 in shared memory
 __host__ __device__ constexpr int tile_keys(int D) { return D == 256 ? 32 : 64; }
 __host__ __device__ constexpr size_t extend_smem(int D) {
-  return (size_t)(kRows + 2 * tile_keys(D)) * D * 2 + tile_keys(D) * sizeof(int);
+  return (size_t)(kRows + 2 * tile_keys(D)) * D * 2 + 3 * tile_keys(D) * sizeof(int);
 }
 
 // Byte offset of 16-byte chunk c of row r in a [rows][D] fp16 tile; the
@@ -73,6 +73,8 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const __grid_constant_
 
   const uint32_t q_s = smem_u32(smem), k_s = q_s + kRows * D * 2, v_s = k_s + KEYS * D * 2;
   int* ok_s = reinterpret_cast<int*>(smem + (kRows + 2 * KEYS) * D * 2);
+  int* bad_s = ok_s + KEYS;  // [2][KEYS], the tiles in turn: V held an infinity or NaN (set to zero)
+  for (int i = threadIdx.x; i < 2 * KEYS; i += kThreads) bad_s[i] = 0;
 
   // q rows of the tile (zero behind the last)
   for (int i = threadIdx.x; i < kRows * CH; i += kThreads) {
@@ -88,6 +90,7 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const __grid_constant_
   }
 
   // the tile's last row sees positions below `end`
+  const int all_see = sp.L ? sp.before + (int)(r0 / p.G) : -1;  // every row sees the positions up to here
   const int t_last = (int)((min(r0 + kRows, live_rows) - 1) / p.G);
   const int end = sp.L ? min(sp.L, sp.before + t_last + 1) : 0;
   const int k0 = split * p.chunk, k1 = min(end, k0 + p.chunk);
@@ -104,7 +107,8 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const __grid_constant_
     last[e] = r < live_rows ? sp.before + (int)(r / p.G) : -1;
   }
 
-  for (int ks = k0; ks < k1; ks += KEYS) {
+  int turn = 0;
+  for (int ks = k0; ks < k1; ks += KEYS, turn ^= 1) {
     __syncthreads();  // the tile before is used up (and q is in place)
     for (int i = threadIdx.x; i < KEYS * CH; i += kThreads) {
       const int j = i / CH, ch = i % CH, pos = ks + j;
@@ -118,6 +122,13 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const __grid_constant_
         } else {
           kx = load8<BITS>(p.v, 0, b, kvh, sp.L, pos, row, ch);
           vx = load8<BITS>(p.v, 1, b, kvh, sp.L, pos, row, ch);
+          // In a tile that some row sees in part an infinite or NaN V must
+          // not meet the zero weights of the rows that do not see it.
+          if (ks + KEYS - 1 > all_see && (ext::nonfinite2(vx.x) || ext::nonfinite2(vx.y) || ext::nonfinite2(vx.z) ||
+                                          ext::nonfinite2(vx.w))) {
+            vx = make_uint4(0u, 0u, 0u, 0u);
+            bad_s[turn * KEYS + j] = 1;
+          }
         }
       }
       *reinterpret_cast<uint4*>(smem + kRows * D * 2 + at<D>(j, ch)) = kx;
@@ -125,6 +136,7 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const __grid_constant_
       if (ch == 0) ok_s[j] = ok;
     }
     __syncthreads();
+    for (int i = threadIdx.x; i < KEYS; i += kThreads) bad_s[(turn ^ 1) * KEYS + i] = 0;
 
     float s[NT][4];
 #pragma unroll
@@ -149,7 +161,7 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const __grid_constant_
       for (int e = 0; e < 4; ++e) {
         const int j = n * 8 + (lane & 3) * 2 + (e & 1);
         const bool see = ok_s[j] && ks + j <= last[e >> 1];
-        s[n][e] = see ? s[n][e] * p.scale_log2 : -INFINITY;
+        s[n][e] = !see ? -INFINITY : bad_s[turn * KEYS + j] ? __int_as_float(0x7FFFFFFF) : s[n][e] * p.scale_log2;
         mx[e >> 1] = fmaxf(mx[e >> 1], s[n][e]);
       }
     }
@@ -204,7 +216,7 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const __grid_constant_
     const int t = (int)(r / p.G), h = (int)(r % p.G);
     const long long orow = ((long long)b * p.num_new + t) * p.Hq + (long long)kvh * p.G + h;
     if (p.splits == 1) {
-      const float inv = l[e] > 0.f ? 1.f / l[e] : 0.f;
+      const float inv = l[e] != 0.f ? 1.f / l[e] : 0.f;
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) {
         __half2* d = reinterpret_cast<__half2*>(p.out + orow * D + i * 8 + (lane & 3) * 2);

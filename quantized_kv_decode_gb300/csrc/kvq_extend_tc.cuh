@@ -94,7 +94,7 @@ struct Cfg {
   static constexpr size_t SMEM = (size_t)STAGES * STAGE + (size_t)DEPTH * RAW + 1024 + 2048;
   static_assert(SMEM <= 227 * 1024, "shared memory");
   static_assert(COL_Q + 2 * D / 2 <= COLS, "tensor memory");
-  static_assert(!DUAL || (size_t)STAGES * STAGE >= (size_t)128 * D * 4, "the second stream's result");
+  static_assert((size_t)STAGES * STAGE >= (DUAL ? (size_t)128 * D * 4 : 0) + SOFT * 4096, "scratch in the stages");
   // channel held at place i of an eight-channel chunk (the unpacking leaves
   // 4-bit and 2-bit codes as pairs (i, i + 4))
   static constexpr bool PAIRED = BITS <= 4;
@@ -111,7 +111,7 @@ struct Shared {
   unsigned long long q_full[2], s_full[2], p_full[2], o_full[2], turn[2], merge;
   float2 ml[128];           // the second stream's maximum and sum per row
   uint32_t ok[STAGES][2];   // per key: mapped and before the end
-  uint32_t bad[STAGES][4][2];  // per segment and key: V held an infinity or NaN (set to zero)
+  alignas(4) uint8_t bad[STAGES][kKeys];  // per key: V held an infinity or NaN (set to zero)
   uint32_t tmem;
   int stop;
 };
@@ -382,39 +382,62 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
   if (warp >= C::SOFT0 && warp < C::PROD0) {
     // ------------------------------------------------------ softmax rows
     const int i = (warp - C::SOFT0) >> 2;
-    const long long r = r0 + (C::DUAL ? 0 : i * 128) + (warp & 3) * 32 + lane;
+    const int row0 = (int)r0 + (C::DUAL ? 0 : i * 128) + (warp & 3) * 32;  // the warp's first row
+    const int r = row0 + lane;
     const bool live = r < live_rows;
-    const bool any_live = r - lane < live_rows;
+    const bool any_live = row0 < live_rows;
+    // 32 rows of 128 bytes in the stages' memory, before they are first
+    // filled and after the last product
+    uint8_t* scratch = smem + (warp - C::SOFT0) * 4096;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + C::COL_S + i * kKeys;
     const uint32_t to = tmem + lanes + C::COL_O + i * D;
     const uint32_t tq = tmem + lanes + C::COL_Q + i * (D / 2);
-    const int t = live ? (int)(r / p.G) : 0;
-    const long long orow = ((long long)b * p.num_new + t) * p.Hq + (long long)kvh * p.G + (live ? (int)(r % p.G) : 0);
+    const int t = live ? r / p.G : 0;
+    const long long orow = ((long long)b * p.num_new + t) * p.Hq + (long long)kvh * p.G + (live ? r % p.G : 0);
     // (rows behind the last take part with q = 0 and are not written)
     const int last = live ? before + t : 0x7fffffff;
     const int mine = C::DUAL ? (tiles + 1 - i) / 2 : tiles;  // this stream's key tiles
     if (i < nq && mine) {
-      // q to tensor memory, channels in the order the keys are unpacked in
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + orow * D);
-#pragma unroll
+      // q to tensor memory, channels in the order the keys are unpacked in: 64
+      // channels at a time through the warp's scratch, whole lines from global
+      // memory (a lane reading its own row takes a line's tag per lane and
+      // load: 7000 cycles for the tile)
+      // (Set-up and writing out run once a block, their instructions fetched
+      // anew: rolled loops.)
+#pragma unroll 1
       for (int h = 0; h < D / 64; ++h) {
+        uint4 x[8];
+#pragma unroll
+        for (int it = 0; it < 8; ++it) {  // (all loads, then the stores)
+          const int row = min(row0 + it * 4 + (lane >> 3), (int)live_rows - 1), t2 = row / p.G;
+          const uint4* src = reinterpret_cast<const uint4*>(
+              p.q + (((long long)b * p.num_new + t2) * p.Hq + (long long)kvh * p.G + (row - t2 * p.G)) * D) + h * 8 +
+              (lane & 7);
+          x[it] = KVQ_IN(c, KVQ_ARRAY_Q, src, 16) ? __ldg(src) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int it = 0; it < 8; ++it) {
+          const int rr = it * 4 + (lane >> 3);
+          if (row0 + rr >= live_rows) x[it] = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(scratch + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4)) = x[it];
+        }
+        __syncwarp();
         uint32_t w[32];
 #pragma unroll
         for (int ch = 0; ch < 8; ++ch) {
-          uint4 x = make_uint4(0u, 0u, 0u, 0u);
-          if (live && KVQ_IN(c, KVQ_ARRAY_Q, src + h * 8 + ch, 16)) x = src[h * 8 + ch];
+          const uint4 y = *reinterpret_cast<const uint4*>(scratch + lane * 128 + ((ch ^ (lane & 7)) << 4));
           if constexpr (C::PAIRED) {  // (0, 4), (1, 5), (2, 6), (3, 7)
-            w[4 * ch] = fast::prmt_b32(x.x, x.z, 0x5410u);
-            w[4 * ch + 1] = fast::prmt_b32(x.x, x.z, 0x7632u);
-            w[4 * ch + 2] = fast::prmt_b32(x.y, x.w, 0x5410u);
-            w[4 * ch + 3] = fast::prmt_b32(x.y, x.w, 0x7632u);
+            w[4 * ch] = fast::prmt_b32(y.x, y.z, 0x5410u);
+            w[4 * ch + 1] = fast::prmt_b32(y.x, y.z, 0x7632u);
+            w[4 * ch + 2] = fast::prmt_b32(y.y, y.w, 0x5410u);
+            w[4 * ch + 3] = fast::prmt_b32(y.y, y.w, 0x7632u);
           } else {
-            w[4 * ch] = x.x, w[4 * ch + 1] = x.y, w[4 * ch + 2] = x.z, w[4 * ch + 3] = x.w;
+            w[4 * ch] = y.x, w[4 * ch + 1] = y.y, w[4 * ch + 2] = y.z, w[4 * ch + 3] = y.w;
           }
         }
-        __syncwarp();
         tc::st32(tq + h * 32, w);
+        __syncwarp();
       }
       tc::wait_st();
       tc::fence_before();
@@ -442,9 +465,13 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t bad = 0;
-            if (KIND == 2 && ks + kKeys - 1 > all_see)  // (checked in these tiles alone)
+            if (KIND == 2 && ks + kKeys - 1 > all_see) {  // (checked in these tiles alone)
 #pragma unroll
-              for (int g = 0; g < C::SEGS; ++g) bad |= sh.bad[st][g][h];
+              for (int g = 0; g < 8; ++g) {
+                const uint32_t v = reinterpret_cast<const uint32_t*>(sh.bad[st])[h * 8 + g];
+                bad |= ((v & 1u) | (v >> 7 & 2u) | (v >> 14 & 4u) | (v >> 21 & 8u)) << (4 * g);
+              }
+            }
             const int seen = last - ks - 32 * h;  // keys 0 .. seen of these
             const uint32_t see = (h ? ok1 : ok0) & (seen >= 31 ? 0xFFFFFFFFu : seen < 0 ? 0u : (2u << seen) - 1u);
             bad &= see;
@@ -506,18 +533,19 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(p_full(i));
     }
-    if (going && mine) going = __all_sync(0xffffffffu, tc::mbar_wait(o_full(i), 0, stop));
+    // both tiles' (streams') products are done with the stages
+    for (int k = 0; k < nq && going; ++k)
+      if (C::DUAL ? k < tiles : tiles > 0) going = __all_sync(0xffffffffu, tc::mbar_wait(o_full(k), 0, stop));
     tc::fence_after();
-    // The second stream hands its sum over in the stages' memory, once both
-    // streams' products are done with it: chunk c of row r at r, c ^ (r & 7).
+    // The second stream hands its sum over in the stages' memory: chunk c of
+    // row r at r, c ^ (r & 7).
     const int rr = (warp & 3) * 32 + lane;
     uint8_t* const other = smem + rr * (D * 4);
     float a0 = 1.f, a1 = 0.f;  // the streams' factors
     if (C::DUAL && going && tiles > 1) {
       if (i == 1) {
-        going = __all_sync(0xffffffffu, tc::mbar_wait(o_full(0), 0, stop));
-        if (going && any_live) {
-#pragma unroll
+        if (any_live) {
+#pragma unroll 1
           for (int h = 0; h < D / 16; ++h) {
             uint32_t o[16];
             tc::ld16(to + h * 16, o);
@@ -545,8 +573,8 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
     }
     if (going && any_live && !(C::DUAL && i)) {
       const float inv = l != 0.f ? 1.f / l : 0.f;
-      const long long w = orow * p.splits + split;
-#pragma unroll
+      scratch += C::DUAL ? 128 * D * 4 : 0;
+#pragma unroll 1
       for (int h = 0; h < D / 32; ++h) {
         uint32_t o[32];
         if (mine) {
@@ -569,26 +597,41 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
         float x[32];  // place i of a chunk holds channel(i)
 #pragma unroll
         for (int e = 0; e < 32; ++e) x[(e & ~7) + C::channel(e & 7)] = __uint_as_float(o[e]);
-        if (live && p.splits == 1) {
-          uint4* d = reinterpret_cast<uint4*>(p.out + orow * D + h * 32);
+        // through the scratch, so that lanes write whole lines of a row
+        const bool halves = p.splits == 1;
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (KVQ_IN(c, KVQ_ARRAY_OUT, d + e, 16))
-              d[e] = make_uint4(fast::pack_h2(x[8 * e] * inv, x[8 * e + 1] * inv),
-                                fast::pack_h2(x[8 * e + 2] * inv, x[8 * e + 3] * inv),
-                                fast::pack_h2(x[8 * e + 4] * inv, x[8 * e + 5] * inv),
-                                fast::pack_h2(x[8 * e + 6] * inv, x[8 * e + 7] * inv));
-        } else if (live) {
-          float4* d = reinterpret_cast<float4*>(p.ws_o + w * D + h * 32);
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (KVQ_IN(c, KVQ_ARRAY_WORKSPACE, d + e, 16))
-              d[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+        for (int e = 0; e < 8; ++e) {
+          if (halves && e >= 4) continue;
+          uint4 y;
+          if (halves)
+            y = make_uint4(fast::pack_h2(x[8 * (e & 3)] * inv, x[8 * (e & 3) + 1] * inv),
+                           fast::pack_h2(x[8 * (e & 3) + 2] * inv, x[8 * (e & 3) + 3] * inv),
+                           fast::pack_h2(x[8 * (e & 3) + 4] * inv, x[8 * (e & 3) + 5] * inv),
+                           fast::pack_h2(x[8 * (e & 3) + 6] * inv, x[8 * (e & 3) + 7] * inv));
+          else
+            y = make_uint4(__float_as_uint(x[4 * e]), __float_as_uint(x[4 * e + 1]), __float_as_uint(x[4 * e + 2]),
+                           __float_as_uint(x[4 * e + 3]));
+          *reinterpret_cast<uint4*>(scratch + lane * 128 + ((e ^ (lane & 7)) << 4)) = y;
+        }
+        __syncwarp();
+        const int per = halves ? 4 : 8, ch = lane & (per - 1);  // lanes a row takes
+#pragma unroll 4
+        for (int rr = lane / per; rr < 32; rr += 32 / per) {
+          const long long row = __shfl_sync(0xffffffffu, orow, rr);
+          if (row0 + rr >= live_rows) continue;
+          const uint4 y = *reinterpret_cast<const uint4*>(scratch + rr * 128 + ((ch ^ (rr & 7)) << 4));
+          if (halves) {
+            uint4* d = reinterpret_cast<uint4*>(p.out + row * D + h * 32) + ch;
+            if (KVQ_IN(c, KVQ_ARRAY_OUT, d, 16)) *d = y;
+          } else {
+            uint4* d = reinterpret_cast<uint4*>(p.ws_o + (row * p.splits + split) * D + h * 32) + ch;
+            if (KVQ_IN(c, KVQ_ARRAY_WORKSPACE, d, 16)) *d = y;
+          }
         }
         __syncwarp();
       }
       if (p.splits > 1 && live) {
-        float2* ml = reinterpret_cast<float2*>(p.ws_ml) + w;
+        float2* ml = reinterpret_cast<float2*>(p.ws_ml) + orow * p.splits + split;
         if (KVQ_IN(c, KVQ_ARRAY_WORKSPACE, ml, 8)) *ml = make_float2(m, l);
       }
     }
@@ -596,6 +639,9 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
     // ------------------------------------------------------ producers
     const int tid = threadIdx.x - C::PROD0 * 32, pw = tid >> 5;
     bool ok = true;  // after a wait that ran out the loops go on without waiting
+    for (int k = 0; k < nq; ++k)  // (q passes through the stages' memory first)
+      if (C::DUAL ? k < tiles : tiles > 0) ok = ok && tc::mbar_wait(q_full(k), 0, stop);
+    ok = __all_sync(0xffffffffu, ok);
     if constexpr (KIND != 2) {
       uint32_t lut[4] = {0u, 0u, 0u, 0u};
       if constexpr (KIND == 1) {
@@ -651,30 +697,25 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
       else if (c.g == 16) convert(Int<2>{});
       else convert(Int<4>{});
     } else {
-      // fp16 rows: straight to their places.  This thread's key, and segment
-      // and K / V of its unit u: the keys of a warp are consecutive, so its
-      // 16-byte copies hit all banks.
-      constexpr int PT = C::PROD * 32, UNITS = 2 * C::SEGS * kKeys / PT;
-      const int key = tid & (kKeys - 1);
-      auto seg_of = [&](int u) { return ((u * PT + tid) / kKeys) % C::SEGS; };
-      auto which_of = [&](int u) { return (u * PT + tid) / (kKeys * C::SEGS); };
+      // fp16 rows: straight to their places, a row by consecutive lanes (a row
+      // per lane took a tag per lane and copy: 2050 cycles of issue a tile).
+      constexpr int CH = D / 8, RPP = C::PROD * 32 / CH;  // chunks of a row, rows a pass
+      const int ch = tid % CH, sub = tid / CH;
+#pragma unroll 1
       for (int j = 0; j < tiles; ++j) {
         const int st = j % C::STAGES;
         if (ok) ok = tc::mbar_wait(empty(st), ((j / C::STAGES) & 1) ^ 1, stop);
         ok = __all_sync(0xffffffffu, ok);
-        const uint32_t base = tc::smem_addr(smem + st * C::STAGE);
-        const long long row = row_of(k0 + j * kKeys + key);
-#pragma unroll 1
-        for (int u = 0; u < UNITS; ++u) {
-          const int seg = seg_of(u), which = which_of(u);
-          const uint8_t* src = p.v.codes[which] + max(row, 0ll) * c.row_bytes + seg * 64;
-          const uint32_t dst = base + which * C::MAT + (seg >> 1) * (kKeys * 128) + key * 128;
-#pragma unroll
-          for (int ch = 0; ch < 4; ++ch) {
-            const uint8_t* sp = src + ch * 16;
-            fast::cp_async16(dst + ((((seg & 1) * 4 + ch) ^ (key & 7)) << 4), sp,
-                             row >= 0 && KVQ_IN(c, which ? KVQ_ARRAY_V_CODES : KVQ_ARRAY_K_CODES, sp, 16));
-          }
+        uint8_t* const stage = smem + st * C::STAGE;
+        const uint32_t base = tc::smem_addr(stage) + (ch >> 3) * (kKeys * 128);
+#pragma unroll 4
+        for (int pass = 0; pass < kKeys / RPP; ++pass) {
+          const int key = pass * RPP + sub;
+          const long long row = row_of(k0 + j * kKeys + key);
+          const uint32_t dst = base + key * 128 + (((ch & 7) ^ (key & 7)) << 4);
+          const long long o = max(row, 0ll) * (2 * D) + ch * 16;
+          fast::cp_async16(dst, p.v.codes[0] + o, row >= 0 && KVQ_IN(c, KVQ_ARRAY_K_CODES, p.v.codes[0] + o, 16));
+          fast::cp_async16(dst + C::MAT, p.v.codes[1] + o, row >= 0 && KVQ_IN(c, KVQ_ARRAY_V_CODES, p.v.codes[1] + o, 16));
         }
         if (pw == 0) {
           note_keys(sh.ok[st], j);
@@ -688,23 +729,16 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
         // meet the zero weights of the rows that do not see it
         fast::cp_async_commit();
         fast::cp_async_wait<0>();
-#pragma unroll 1
-        for (int u = 0; u < UNITS; ++u) {
-          if (which_of(u) == 0) continue;  // (a warp's units are all K or all V)
-          const int seg = seg_of(u);
-          bool bad = false;
-          uint8_t* vrow = smem + st * C::STAGE + C::MAT + (seg >> 1) * (kKeys * 128) + key * 128;
-#pragma unroll
-          for (int ch = 0; ch < 4; ++ch) {
-            uint4* v = reinterpret_cast<uint4*>(vrow + ((((seg & 1) * 4 + ch) ^ (key & 7)) << 4));
-            const uint4 q = *v;
-            if (nonfinite2(q.x) || nonfinite2(q.y) || nonfinite2(q.z) || nonfinite2(q.w)) {
-              bad = true;
-              *v = make_uint4(0u, 0u, 0u, 0u);
-            }
-          }
-          const uint32_t keys = __ballot_sync(0xffffffffu, bad);
-          if (lane == 0) sh.bad[st][seg][pw & 1] = keys;
+#pragma unroll 2
+        for (int pass = 0; pass < kKeys / RPP; ++pass) {
+          const int key = pass * RPP + sub;
+          uint4* v = reinterpret_cast<uint4*>(stage + C::MAT + (ch >> 3) * (kKeys * 128) + key * 128 +
+                                              (((ch & 7) ^ (key & 7)) << 4));
+          const uint4 q = *v;
+          const bool bad = nonfinite2(q.x) || nonfinite2(q.y) || nonfinite2(q.z) || nonfinite2(q.w);
+          if (bad) *v = make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t row_bad = __ballot_sync(0xffffffffu, bad) >> (lane & ~(CH - 1)) & ((1u << CH) - 1u);
+          if (ch == 0) sh.bad[st][key] = row_bad != 0;
         }
         tc::mbar_arrive(raw_full(st));
       }

@@ -195,6 +195,82 @@ def test_rows_behind_the_sequence_do_not_count(fmt, value, T):
     check_extend(got[0], q[0], k16[0], v16[0], 150, T, D ** -0.5)
 
 
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("T,D", [(5, 64), (200, 128), (150, 256)])
+def test_a_later_token_does_not_reach_earlier_ones(T, D, value):
+    """An infinity or NaN in K and V of one new token: the tokens before it
+    come out as without it, its own and later ones are not finite."""
+    import torch
+    import quantized_kv_decode_gb300 as K
+    rng = np.random.default_rng(8)
+    before, at = 70, T // 2
+    L = before + T
+    cache = new_cache("fp16", 1, D, 1, L)
+    _fill(K, cache, rng, [L], 1, D, L)
+    k16, v16 = read_rows(cache, [L], L)
+    for t in (cache.k_codes, cache.v_codes):
+        t.view(torch.float16)[:, :, before + at, 3] = value
+    q = rng.standard_normal((1, T, 4, D)).astype(np.float16)
+    got = K.kvq_extend_attn(cache, torch.from_numpy(q).cuda(), torch.tensor([before], dtype=torch.int32, device="cuda"),
+                            L).cpu().numpy()
+    check_extend(got[0], q[0], k16[0], v16[0], before, at, D ** -0.5)
+    assert not np.isfinite(got[0, at:]).all(axis=-1).any()
+
+
+@pytest.mark.parametrize("fmt", ["int4", "int8", "sym4", "nf4"])
+@pytest.mark.parametrize("g_is_D", [False, True])
+@pytest.mark.parametrize("extra", [0, 1, 2, 5])
+def test_header_arrays_of_any_alignment(fmt, g_is_D, extra):
+    """Dense capacities that leave a head's scales and zeros at any two-byte
+    boundary, down to one header per row; the last head's end the array."""
+    import torch
+    import quantized_kv_decode_gb300 as K
+    rng = np.random.default_rng(12)
+    bits, g, kw = FORMATS[fmt]
+    D, Hkv, B, T, L = 64, 3, 2, 6, 131 + extra
+    desc = K.make_desc(bits, D if g_is_D else g, Hkv, D, K.KVQ_DENSE, L, **kw)
+    cache = K.KVCache.allocate(desc, B, "cuda")
+    _fill(K, cache, rng, [L] * B, Hkv, D, L)
+    k16, v16 = read_rows(cache, [L] * B, L)
+    q = rng.standard_normal((B, T, 6, D)).astype(np.float16)
+    before = [L - T, 57]
+    for splits in (1, 2):
+        got = K.kvq_extend_attn(cache, torch.from_numpy(q).cuda(), torch.tensor(before, dtype=torch.int32, device="cuda"),
+                                L, num_splits=splits).cpu().numpy()
+        for b in range(B):
+            check_extend(got[b], q[b], k16[b], v16[b], before[b], T, D ** -0.5)
+
+
+def test_far_zero_points_and_large_scales():
+    """Groups whose zero-point lies beyond +-1024 and groups that reach fp16's
+    end: products that leave the fast fp16 conversion."""
+    import torch
+    import quantized_kv_decode_gb300 as K
+    rng = np.random.default_rng(13)
+    D, L, T = 64, 90, 7
+    cache = new_cache("int8", 1, D, 1, L)
+    k = (rng.standard_normal((1, L, 1, D)) * 0.01).astype(np.float16)
+    k[0, ::3] += np.float16(0.5)           # range 0.06 around 0.5: z about -2000
+    v = rng.standard_normal((1, L, 1, D)).astype(np.float16)
+    z = torch.zeros(1, dtype=torch.int32, device="cuda")
+    K.kvq_append(cache, torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda(), z)
+    assert float(cache.k_zero.float().abs().max()) > 1024
+    k16, v16 = read_rows(cache, [L], L)
+    q = rng.standard_normal((1, T, 2, D)).astype(np.float16)
+    b = torch.tensor([L - T], dtype=torch.int32, device="cuda")
+    got = K.kvq_extend_attn(cache, torch.from_numpy(q).cuda(), b, L).cpu().numpy()
+    check_extend(got[0], q[0], k16[0], v16[0], L - T, T, D ** -0.5)
+    # one key at the end of fp16's range, all others small: scores stay finite
+    k[0, 5, 0, :] = np.linspace(0, 65504, D).astype(np.float16)  # code 255 decodes to 65535
+    K.kvq_append(cache, torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda(), z)
+    q[:] = 0
+    q[..., 0] = np.float16(1e-3)
+    k16, v16 = read_rows(cache, [L], L)
+    assert np.abs(k16[0, 5].astype(np.float64)).max() == 65504
+    got = K.kvq_extend_attn(cache, torch.from_numpy(q).cuda(), b, L, softmax_scale=0.01).cpu().numpy()
+    check_extend(got[0], q[0], k16[0], v16[0], L - T, T, 0.01)
+
+
 def test_large_scores_keep_the_softmax_exact():
     """Scores of several thousand: one key takes all the weight, whichever
     tile it is in, and earlier tiles' sums vanish without overflow."""
