@@ -74,6 +74,7 @@ struct Cfg {
   static constexpr int MAT = kKeys * D * 2;       // one fp16 tile
   static constexpr int STAGE = (LO ? 3 : 2) * MAT;
   static constexpr int STAGES = LO ? 3 : 4;
+  static constexpr int Q_STAGE = STAGES - (SOFT * 4096 + STAGE - 1) / STAGE;  // q passes through the stages from here on
   static constexpr int SEGS = D / 32;             // 32-channel segments of a row
   // A producer warp works on items: the whole rows of KPI keys of K or V, a
   // segment per lane.
@@ -388,7 +389,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
     const bool any_live = row0 < live_rows;
     // 32 rows of 128 bytes in the stages' memory, before they are first
     // filled and after the last product
-    uint8_t* scratch = smem + (warp - C::SOFT0) * 4096;
+    uint8_t* scratch = smem + C::Q_STAGE * C::STAGE + (warp - C::SOFT0) * 4096;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + C::COL_S + i * kKeys;
     const uint32_t to = tmem + lanes + C::COL_O + i * D;
@@ -405,22 +406,23 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
       // load: 7000 cycles for the tile)
       // (Set-up and writing out run once a block, their instructions fetched
       // anew: rolled loops.)
-#pragma unroll 1
-      for (int h = 0; h < D / 64; ++h) {
-        uint4 x[8];
+      uint4 x[D / 64][8];
 #pragma unroll
-        for (int it = 0; it < 8; ++it) {  // (all loads, then the stores)
-          const int row = min(row0 + it * 4 + (lane >> 3), (int)live_rows - 1), t2 = row / p.G;
-          const uint4* src = reinterpret_cast<const uint4*>(
-              p.q + (((long long)b * p.num_new + t2) * p.Hq + (long long)kvh * p.G + (row - t2 * p.G)) * D) + h * 8 +
-              (lane & 7);
-          x[it] = KVQ_IN(c, KVQ_ARRAY_Q, src, 16) ? __ldg(src) : make_uint4(0u, 0u, 0u, 0u);
-        }
+      for (int it = 0; it < 8; ++it) {  // (all loads, then the stores)
+        const int row = min(row0 + it * 4 + (lane >> 3), (int)live_rows - 1), t2 = row / p.G;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            p.q + (((long long)b * p.num_new + t2) * p.Hq + (long long)kvh * p.G + (row - t2 * p.G)) * D) + (lane & 7);
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h)
+          x[h][it] = KVQ_IN(c, KVQ_ARRAY_Q, src + h * 8, 16) ? __ldg(src + h * 8) : make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h) {
 #pragma unroll
         for (int it = 0; it < 8; ++it) {
           const int rr = it * 4 + (lane >> 3);
-          if (row0 + rr >= live_rows) x[it] = make_uint4(0u, 0u, 0u, 0u);
-          *reinterpret_cast<uint4*>(scratch + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4)) = x[it];
+          if (row0 + rr >= live_rows) x[h][it] = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(scratch + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4)) = x[h][it];
         }
         __syncwarp();
         uint32_t w[32];
@@ -573,7 +575,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
     }
     if (going && any_live && !(C::DUAL && i)) {
       const float inv = l != 0.f ? 1.f / l : 0.f;
-      scratch += C::DUAL ? 128 * D * 4 : 0;
+      scratch = smem + (C::DUAL ? 128 * D * 4 : 0) + (warp - C::SOFT0) * 4096;
 #pragma unroll 1
       for (int h = 0; h < D / 32; ++h) {
         uint32_t o[32];
@@ -639,9 +641,11 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
     // ------------------------------------------------------ producers
     const int tid = threadIdx.x - C::PROD0 * 32, pw = tid >> 5;
     bool ok = true;  // after a wait that ran out the loops go on without waiting
-    for (int k = 0; k < nq; ++k)  // (q passes through the stages' memory first)
-      if (C::DUAL ? k < tiles : tiles > 0) ok = ok && tc::mbar_wait(q_full(k), 0, stop);
-    ok = __all_sync(0xffffffffu, ok);
+    auto wait_q = [&] {  // before the stages are filled that q passes through
+      for (int k = 0; k < nq; ++k)
+        if (C::DUAL ? k < tiles : tiles > 0) ok = ok && tc::mbar_wait(q_full(k), 0, stop);
+      ok = __all_sync(0xffffffffu, ok);
+    };
     if constexpr (KIND != 2) {
       uint32_t lut[4] = {0u, 0u, 0u, 0u};
       if constexpr (KIND == 1) {
@@ -665,6 +669,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
         for (int j = 0; j < tiles; ++j) {
           if (ok) ok = tc::mbar_wait(raw_full(slot), rph, stop) && tc::mbar_wait(empty(st), ph, stop);
           ok = __all_sync(0xffffffffu, ok);
+          if (j == C::Q_STAGE) wait_q();
           uint8_t* base = smem + st * C::STAGE;
           const uint8_t* ring = smem + C::STAGES * C::STAGE + slot * C::RAW;
           const uint32_t ok0 = sh.raw_ok[slot][0], ok1 = sh.raw_ok[slot][1];
@@ -706,6 +711,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
         const int st = j % C::STAGES;
         if (ok) ok = tc::mbar_wait(empty(st), ((j / C::STAGES) & 1) ^ 1, stop);
         ok = __all_sync(0xffffffffu, ok);
+        if (j == C::Q_STAGE) wait_q();
         uint8_t* const stage = smem + st * C::STAGE;
         const uint32_t base = tc::smem_addr(stage) + (ch >> 3) * (kKeys * 128);
 #pragma unroll 4
