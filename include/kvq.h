@@ -464,9 +464,12 @@ KVQ_API size_t kvq_extend_workspace_size(const kvq_cache_desc* desc, int32_t bat
  *   max_seq_len      host upper bound on seq_lens_before[b] + new_lens[b]
  *   out              device fp16 like q; may not overlap it
  * num_splits, softmax_scale and workspace as for kvq_decode_attn, but any
- * number of query heads per KV head.  Scores and softmax in fp32; K and V
- * enter the products as the fp16 values that kvq_cache_read returns, the
- * probabilities as fp16 (relative to their row's maximum).  A sequence whose
+ * number of query heads per KV head.  Scores and softmax in fp32; K enters the
+ * products as x_hat = (q - z) s to 22 bits (two fp16 numbers), V as the fp16
+ * values that kvq_cache_read returns, the probabilities as fp16 (11 bits down
+ * to 2^-21 of the row's largest).  An infinity or NaN in a token's V row makes
+ * NaN or infinities of the rows that see the token, possibly in more channels
+ * than its own; rows that do not see it are untouched.  A sequence whose
  * length exceeds min(max_seq_len, cache capacity) flags KVQ_FLAG_SEQ_LEN and
  * yields zero rows; a token whose page is unmapped flags KVQ_FLAG_BLOCK_TABLE
  * and is left out; a row with nothing to attend to is zero.
@@ -530,7 +533,8 @@ KVQ_API kvq_status kvq_pages_reorder(const kvq_page_pool* pool, const int32_t* p
  *                       when new_lens is NULL); 0 for a skipped sequence
  * With too few free pages nothing changes for any sequence: KVQ_FLAG_POOL_EMPTY,
  * no copies, granted 0 throughout (pass granted as new_lens to the calls that
- * write and nothing is written).
+ * write and nothing is written).  A call whose sequences could touch 2^31
+ * blocks together: KVQ_ERR_UNSUPPORTED.
  */
 KVQ_API kvq_status kvq_pages_reserve(const kvq_page_pool* pool, const int32_t* seq_lens_before,
                              const int32_t* new_lens, int32_t num_new, int32_t* copy_src,

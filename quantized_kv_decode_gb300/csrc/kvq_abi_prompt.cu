@@ -410,6 +410,9 @@ kvq_status kvq_pages_reserve(const kvq_page_pool* pool, const int32_t* seq_lens_
   kvq_status st = check_pool(pool);
   if (st != KVQ_OK) return st;
   if (num_new < 0) return KVQ_ERR_INVALID_ARG;
+  // the blocks that all sequences touch are counted in 32 bits
+  const int64_t blocks = std::min<int64_t>(pool->max_blocks_per_seq, (int64_t)num_new / pool->page_size + 2);
+  if (blocks * pool->batch > INT32_MAX) return KVQ_ERR_UNSUPPORTED;
   if (pool->batch == 0) return KVQ_OK;
   if ((st = check_pool_arrays(pool)) != KVQ_OK) return st;
   if (!seq_lens_before || !copy_src || !copy_dst) return KVQ_ERR_INVALID_ARG;

@@ -9,6 +9,12 @@
 // units: m' = max(m, max_j s_j), l' = 2^(m - m') l + sum_j 2^(s_j - m'),
 // o' = 2^(m - m') o + sum_j 2^(s_j - m') v_j; splits over the context write
 // (m, l, o) and a merge joins them.
+//
+// The kernel here, on mma.sync, takes what the tensor-core kernel of
+// kvq_extend_tc.cuh does not: head_dim 256 and axis-aware caches.  As there, K
+// enters as hi + lo, V as hi alone, and the probabilities, rounded to fp16,
+// carry a factor (2^14: m is the exact maximum here) that keeps small ones in
+// fp16's normal range.
 #include "kvq_extend_tc.cuh"
 #include "kvq_host.cuh"
 #include "kvq_load.cuh"
@@ -25,11 +31,12 @@ using fast::smem_u32;
 
 constexpr int kRows = 64;  // 4 warps of 16 rows
 constexpr int kThreads = 128;
+constexpr float kLift = 14.f;  // log2 of the factor in the probabilities, l and o
 
-// Keys per tile: K and V rows as fp16 in shared memory
+// Keys per tile: K (hi and lo) and V rows as fp16 in shared memory
 __host__ __device__ constexpr int tile_keys(int D) { return D == 256 ? 32 : 64; }
 __host__ __device__ constexpr size_t extend_smem(int D) {
-  return (size_t)(kRows + 2 * tile_keys(D)) * D * 2 + 3 * tile_keys(D) * sizeof(int);
+  return (size_t)(kRows + 3 * tile_keys(D)) * D * 2 + 3 * tile_keys(D) * sizeof(int);
 }
 
 // Byte offset of 16-byte chunk c of row r in a [rows][D] fp16 tile; the
@@ -71,8 +78,8 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const __grid_constant_
   const long long live_rows = (long long)sp.n * p.G;
   if (r0 >= live_rows) return;
 
-  const uint32_t q_s = smem_u32(smem), k_s = q_s + kRows * D * 2, v_s = k_s + KEYS * D * 2;
-  int* ok_s = reinterpret_cast<int*>(smem + (kRows + 2 * KEYS) * D * 2);
+  const uint32_t q_s = smem_u32(smem), k_s = q_s + kRows * D * 2, v_s = k_s + 2 * KEYS * D * 2;
+  int* ok_s = reinterpret_cast<int*>(smem + (kRows + 3 * KEYS) * D * 2);
   int* bad_s = ok_s + KEYS;  // [2][KEYS], the tiles in turn: V held an infinity or NaN (set to zero)
   for (int i = threadIdx.x; i < 2 * KEYS; i += kThreads) bad_s[i] = 0;
 
@@ -112,7 +119,7 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const __grid_constant_
     __syncthreads();  // the tile before is used up (and q is in place)
     for (int i = threadIdx.x; i < KEYS * CH; i += kThreads) {
       const int j = i / CH, ch = i % CH, pos = ks + j;
-      uint4 kx = make_uint4(0u, 0u, 0u, 0u), vx = kx;
+      uint4 kx = make_uint4(0u, 0u, 0u, 0u), kl = kx, vx = kx;
       bool ok = pos < k1;
       if (ok) {
         const long long row = view_row(c, b, kvh, sp.L, pos);
@@ -120,7 +127,7 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const __grid_constant_
           ok = false;
           if (ch == 0 && p.status) atomicOr(p.status, KVQ_FLAG_BLOCK_TABLE);
         } else {
-          kx = load8<BITS>(p.v, 0, b, kvh, sp.L, pos, row, ch);
+          kx = load8<BITS>(p.v, 0, b, kvh, sp.L, pos, row, ch, &kl);
           vx = load8<BITS>(p.v, 1, b, kvh, sp.L, pos, row, ch);
           // In a tile that some row sees in part an infinite or NaN V must
           // not meet the zero weights of the rows that do not see it.
@@ -132,7 +139,8 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const __grid_constant_
         }
       }
       *reinterpret_cast<uint4*>(smem + kRows * D * 2 + at<D>(j, ch)) = kx;
-      *reinterpret_cast<uint4*>(smem + (kRows + KEYS) * D * 2 + at<D>(j, ch)) = vx;
+      if (BITS != 16) *reinterpret_cast<uint4*>(smem + (kRows + KEYS) * D * 2 + at<D>(j, ch)) = kl;
+      *reinterpret_cast<uint4*>(smem + (kRows + 2 * KEYS) * D * 2 + at<D>(j, ch)) = vx;
       if (ch == 0) ok_s[j] = ok;
     }
     __syncthreads();
@@ -147,10 +155,14 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const __grid_constant_
       ldsm_x4(q_s + at<D>(warp * 16 + (lane & 15), kb * 2 + (lane >> 4)), a[0], a[1], a[2], a[3]);
 #pragma unroll
       for (int n = 0; n < NT; n += 2) {
-        uint32_t b0, b1, b2, b3;  // keys n*8 .. n*8+15, channels 16 kb .. +15
-        ldsm_x4(k_s + at<D>(n * 8 + (lane & 7) + ((lane >> 4) << 3), kb * 2 + ((lane >> 3) & 1)), b0, b1, b2, b3);
-        mma16816(s[n], a[0], a[1], a[2], a[3], b0, b1);
-        mma16816(s[n + 1], a[0], a[1], a[2], a[3], b2, b3);
+#pragma unroll
+        for (int part = 0; part < (BITS == 16 ? 1 : 2); ++part) {  // hi, lo
+          uint32_t b0, b1, b2, b3;  // keys n*8 .. n*8+15, channels 16 kb .. +15
+          ldsm_x4(k_s + part * KEYS * D * 2 + at<D>(n * 8 + (lane & 7) + ((lane >> 4) << 3), kb * 2 + ((lane >> 3) & 1)),
+                  b0, b1, b2, b3);
+          mma16816(s[n], a[0], a[1], a[2], a[3], b0, b1);
+          mma16816(s[n + 1], a[0], a[1], a[2], a[3], b2, b3);
+        }
       }
     }
 
@@ -171,8 +183,8 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const __grid_constant_
       mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
       mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
       const float mn = fmaxf(m[e], mx[e]);
-      base[e] = mn == -INFINITY ? 0.f : mn;  // nothing seen yet: every weight is 2^-inf = 0
-      alpha[e] = ex2(m[e] - base[e]);
+      base[e] = mn == -INFINITY ? 0.f : mn - kLift;  // nothing seen yet: every weight is 2^-inf = 0
+      alpha[e] = mn == -INFINITY ? 0.f : ex2(m[e] - mn);
       m[e] = mn;
       l[e] *= alpha[e];
     }

@@ -32,8 +32,11 @@
 // share.  V enters as hi alone: its errors average out over the keys.  Scores,
 // sums and O are fp32.  fp16 caches are exact as they are.
 //
-// Reference maximum.  m moves only when a tile's maximum exceeds it by 2^8
-// (P is at most 256 then), so O in tensor memory is rescaled rarely.
+// Reference maximum.  m moves only when a tile's maximum exceeds it by 2^8,
+// so O in tensor memory is rescaled rarely.  P carries a factor 2^7 that the
+// division by the sum takes out: at most 2^15 it stays within fp16, and keys
+// 2^-21 of the largest still have all 11 bits (a long context can hold enough
+// of them to matter).
 //
 // Order of the MMAs.  One lane issues PV(j) and then QK(j + 1) of a tile,
 // and MMAs run in the order issued: S may be overwritten as soon as QK(j + 1)
@@ -57,6 +60,7 @@ struct Int {
   static constexpr int value = N;
 };
 constexpr float kLazy = 8.f;  // log2 units the maximum may lead the reference
+constexpr float kLift = 7.f;  // log2 of the factor in P, l and O
 
 // KIND: 0 uniform codes (asymmetric or symmetric), 1 NF4, 2 fp16
 template <int BITS, int KIND, int D, int NQ>
@@ -273,8 +277,7 @@ __device__ __forceinline__ void store_seg(const Seg<BITS>& x, bool is_k, int key
           a[e] = ((float)(c & ((1u << BITS) - 1u)) - __half2float(gc.z)) * __low2float(gc.s);
         }
         h[i] = pack_sat(a[0], a[1]);
-        const float2 v = __half22float2(as_h2(h[i]));
-        l[i] = pack_sat(fabsf(a[0]) > 65504.f ? 0.f : a[0] - v.x, fabsf(a[1]) > 65504.f ? 0.f : a[1] - v.y);
+        l[i] = pack_rest(a[0], a[1], h[i]);
       }
       const uint32_t at = base + ((turn ^ ch) << 4);
       *reinterpret_cast<uint4*>(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
@@ -509,7 +512,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
             }
           }
         }
-        const float base = m == -INFINITY ? 0.f : m;
+        const float base = m == -INFINITY ? 0.f : m - kLift;
         const float2 sl2 = make_float2(p.scale_log2, p.scale_log2), nb2 = make_float2(-base, -base);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll

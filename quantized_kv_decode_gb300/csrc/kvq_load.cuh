@@ -39,13 +39,21 @@ __device__ __forceinline__ uint32_t pack_sat(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// What pack_sat's rounding of a and b left (0 where it held them).
+__device__ __forceinline__ uint32_t pack_rest(float a, float b, uint32_t hi) {
+  const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  return pack_sat(fabsf(a) > 65504.f ? 0.f : a - v.x, fabsf(b) > 65504.f ? 0.f : b - v.y);
+}
+
 // Channels [8 ch, 8 ch + 8) of K (which = 0) or V (which = 1) at position
-// pos, cache row `row` >= 0, of a sequence of L tokens.
+// pos, cache row `row` >= 0, of a sequence of L tokens.  lo (may be null):
+// what the rounding to fp16 left, itself as fp16.
 template <int BITS>
 __device__ __forceinline__ uint4 load8(const CacheView& v, int which, int b, int kvh, int L,
-                                       int pos, long long row, int ch) {
+                                       int pos, long long row, int ch, uint4* lo = nullptr) {
   const CacheGeom& c = v.geom;
   uint4 o = make_uint4(0u, 0u, 0u, 0u);
+  if (lo) *lo = o;
   const int a_codes = which ? KVQ_ARRAY_V_CODES : KVQ_ARRAY_K_CODES;
   const uint8_t* src = v.codes[which] + row * c.row_bytes + ch * BITS;
   if constexpr (BITS == 16) {
@@ -110,6 +118,10 @@ __device__ __forceinline__ uint4 load8(const CacheView& v, int which, int b, int
     o.y = pack_sat(x[2], x[3]);
     o.z = pack_sat(x[4], x[5]);
     o.w = pack_sat(x[6], x[7]);
+    if (lo) {
+      *lo = make_uint4(pack_rest(x[0], x[1], o.x), pack_rest(x[2], x[3], o.y), pack_rest(x[4], x[5], o.z),
+                       pack_rest(x[6], x[7], o.w));
+    }
     return o;
   }
 }

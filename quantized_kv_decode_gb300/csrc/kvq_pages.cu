@@ -424,7 +424,7 @@ cudaError_t launch_pages_reserve(const PoolParams& p, cudaStream_t stream) {
                                        KVQ_MAX_POOL_BATCH * 8);
   if (e != cudaSuccess) return e;
   int lps = 4;
-  while (lps < 32 && lps < p.num_new / p.pool.page_size + 2) lps *= 2;
+  while (lps < 32 && lps - 2 < p.num_new / p.pool.page_size) lps *= 2;
   return launch_int(reserve_kernel, dim3(1), dim3(kOne), smem, stream, p, lps);
 }
 

@@ -3,7 +3,10 @@
 As in api.py, PyTorch provides device memory and streams only: each function
 checks dtypes, shapes and devices, passes raw pointers to libkvq.so and
 returns.  The tensors of a call live on one device; the call runs on that
-device, on its current stream unless `stream` is given.
+device, on its current stream unless `stream` is given.  Outputs and
+workspaces made here are made on the call's stream too: what fills them runs
+before the kernels, and their memory is not handed to other streams' work
+while the kernels may still run.
 """
 from __future__ import annotations
 
@@ -57,12 +60,26 @@ def _bytes(t, device, need, name):
     return t, size
 
 
+def _made_like(t, new_lens):
+    """An output of a call: rows behind new_lens[b], which no kernel writes, are zeros."""
+    return torch.empty_like(t) if new_lens is None else torch.zeros_like(t)
+
+
 class _on:
-    """Makes the tensors' device current for a call, where it is not already."""
+    """Makes a call's device and stream current, where they are not already."""
     __slots__ = ("guard",)
 
-    def __init__(self, device):
-        self.guard = None if device == torch.cuda.current_device() else torch.cuda.device(device)
+    def __init__(self, device, stream):
+        if stream is not None:
+            if not isinstance(stream, torch.cuda.Stream):
+                handle = getattr(stream, "cuda_stream", stream)
+                stream = (torch.cuda.ExternalStream(handle, device) if handle
+                          else torch.cuda.default_stream(device))
+            if stream.device.index != device:
+                raise ValueError(f"the stream is of {stream.device}, the tensors are on cuda:{device}")
+            self.guard = torch.cuda.stream(stream)
+        else:
+            self.guard = None if device == torch.cuda.current_device() else torch.cuda.device(device)
 
     def __enter__(self):
         if self.guard is not None:
@@ -73,10 +90,8 @@ class _on:
             self.guard.__exit__(*exc)
 
 
-def _stream_on(stream, device):
-    if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
-    return getattr(stream, "cuda_stream", stream)
+def _handle(device):
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _same_cache_device(cache: KVCache, device):
@@ -129,23 +144,20 @@ def kvq_rope_apply(rope: kvq_rope, q: torch.Tensor | None = None, k: torch.Tenso
     _optional(seq_lens_before, torch.int32, "seq_lens_before", (B,), dev)
     _optional(new_lens, torch.int32, "new_lens", (B,), dev)
     _status(dev_status, dev)
-    outs = []
     for t, o, name in ((q, q_out, "q"), (k, k_out, "k")):
-        if t is None:
+        if t is not None:
+            _check(t, torch.float16, name, (B, T, None, D), dev)
             if o is not None:
-                raise ValueError(f"{name}_out without {name}")
-            outs.append(None)
-            continue
-        _check(t, torch.float16, name, (B, T, None, D), dev)
-        if o is None:
-            o = torch.zeros_like(t) if new_lens is not None else torch.empty_like(t)
-        _check(o, torch.float16, name + "_out", t.shape, dev)
-        outs.append(o)
-    with _on(dev):
+                _check(o, torch.float16, name + "_out", t.shape, dev)
+        elif o is not None:
+            raise ValueError(f"{name}_out without {name}")
+    with _on(dev, stream):
+        outs = [o if t is None or o is not None else _made_like(t, new_lens)
+                for t, o in ((q, q_out), (k, k_out))]
         st = _lib.lib().kvq_rope_apply(
             byref(rope), D, B, T, 0 if q is None else q.shape[2], _ptr(q), _ptr(outs[0]),
             0 if k is None else k.shape[2], _ptr(k), _ptr(outs[1]), _ptr(positions),
-            _ptr(seq_lens_before), _ptr(new_lens), _ptr(dev_status), _stream_on(stream, dev))
+            _ptr(seq_lens_before), _ptr(new_lens), _ptr(dev_status), _handle(dev))
     _lib.check(st, "kvq_rope_apply")
     return outs[0], outs[1]
 
@@ -169,16 +181,17 @@ def kvq_rope_append(cache: KVCache, rope: kvq_rope, k_new: torch.Tensor, v_new: 
     _status(dev_status, dev)
     if q is not None:
         _check(q, torch.float16, "q", (B, T, None, D), dev)
-        if q_out is None:
-            q_out = torch.zeros_like(q) if new_lens is not None else torch.empty_like(q)
-        _check(q_out, torch.float16, "q_out", q.shape, dev)
+        if q_out is not None:
+            _check(q_out, torch.float16, "q_out", q.shape, dev)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    with _on(dev):
+    with _on(dev, stream):
+        if q is not None and q_out is None:
+            q_out = _made_like(q, new_lens)
         st = _lib.lib().kvq_rope_append(
             byref(d), byref(cache.ptrs), byref(rope), B, T, _ptr(k_new), _ptr(v_new),
             0 if q is None else q.shape[2], _ptr(q), _ptr(q_out), _ptr(seq_lens_before),
-            _ptr(new_lens), _ptr(dev_status), _stream_on(stream, dev))
+            _ptr(new_lens), _ptr(dev_status), _handle(dev))
     _lib.check(st, "kvq_rope_append")
     return q_out
 
@@ -203,10 +216,10 @@ def kvq_cache_read(cache: KVCache, seq_lens: torch.Tensor, start: torch.Tensor,
     _same_cache_device(cache, dev)
     _batch(cache, B)
     _status(dev_status, dev)
-    with _on(dev):
+    with _on(dev, stream):
         st = _lib.lib().kvq_cache_read(byref(d), byref(cache.ptrs), B, T, _ptr(seq_lens),
                                        _ptr(start), _ptr(k_out), _ptr(v_out), _ptr(dev_status),
-                                       _stream_on(stream, dev))
+                                       _handle(dev))
     _lib.check(st, "kvq_cache_read")
     return k_out, v_out
 
@@ -239,17 +252,18 @@ def kvq_extend_attn(cache: KVCache, q: torch.Tensor, seq_lens_before: torch.Tens
     _same_cache_device(cache, dev)
     _batch(cache, B)
     _status(dev_status, dev)
-    if out is None:
-        out = torch.zeros_like(q) if new_lens is not None else torch.empty_like(q)
-    _check(out, torch.float16, "out", q.shape, dev)
-    with _on(dev):
+    if out is not None:
+        _check(out, torch.float16, "out", q.shape, dev)
+    with _on(dev, stream):
+        if out is None:
+            out = _made_like(q, new_lens)
         need = 0 if workspace is not None else \
             kvq_extend_workspace_size(d, B, T, Hq, max_seq_len, num_splits)
         workspace, ws_bytes = _bytes(workspace, dev, need, "workspace")
         st = _lib.lib().kvq_extend_attn(
             byref(d), byref(cache.ptrs), B, T, Hq, _ptr(q), _ptr(seq_lens_before), _ptr(new_lens),
             int(max_seq_len), int(num_splits), float(softmax_scale), _ptr(out), _ptr(workspace),
-            ws_bytes, _ptr(dev_status), _stream_on(stream, dev))
+            ws_bytes, _ptr(dev_status), _handle(dev))
     _lib.check(st, "kvq_extend_attn")
     return out
 
@@ -293,9 +307,9 @@ def kvq_pages_reorder(pool: PagePool, parent: torch.Tensor, keep_lens: torch.Ten
     _check(parent, torch.int32, "parent", (B,), dev)
     _optional(keep_lens, torch.int32, "keep_lens", (B,), dev)
     _status(dev_status, dev)
-    with _on(dev):
+    with _on(dev, stream):
         st = _lib.lib().kvq_pages_reorder(byref(pool.struct), _ptr(parent), _ptr(keep_lens),
-                                          _ptr(dev_status), _stream_on(stream, dev))
+                                          _ptr(dev_status), _handle(dev))
     _lib.check(st, "kvq_pages_reorder")
 
 
@@ -315,13 +329,13 @@ def kvq_pages_reserve(pool: PagePool, seq_lens_before: torch.Tensor,
     _optional(granted, torch.int32, "granted", (B,), dev)
     _status(dev_status, dev)
     pl = pool.struct
-    with _on(dev):
+    with _on(dev, stream):
         need = int(_lib.lib().kvq_pages_workspace_size(byref(pl)))
         workspace, ws_bytes = _bytes(workspace, dev, need, "workspace")
         st = _lib.lib().kvq_pages_reserve(
             byref(pl), _ptr(seq_lens_before), _ptr(new_lens), int(max_new), _ptr(copy_src),
             _ptr(copy_dst), _ptr(granted), _ptr(workspace), ws_bytes, _ptr(dev_status),
-            _stream_on(stream, dev))
+            _handle(dev))
     _lib.check(st, "kvq_pages_reserve")
 
 
@@ -336,12 +350,12 @@ def kvq_pages_compact(pool: PagePool, move_src: torch.Tensor, move_dst: torch.Te
     _check(num_live, torch.int32, "num_live", (1,), dev)
     _status(dev_status, dev)
     pl = pool.struct
-    with _on(dev):
+    with _on(dev, stream):
         need = int(_lib.lib().kvq_pages_workspace_size(byref(pl)))
         workspace, ws_bytes = _bytes(workspace, dev, need, "workspace")
         st = _lib.lib().kvq_pages_compact(byref(pl), _ptr(move_src), _ptr(move_dst),
                                           _ptr(num_live), _ptr(workspace), ws_bytes,
-                                          _ptr(dev_status), _stream_on(stream, dev))
+                                          _ptr(dev_status), _handle(dev))
     _lib.check(st, "kvq_pages_compact")
 
 
@@ -377,9 +391,9 @@ def kvq_pages_copy(caches, copy_src: torch.Tensor, copy_dst: torch.Tensor,
     # the kvq_cache structures: their pointers one after the other
     structs = array("Q", flat)
     arrays = structs.buffer_info()[0]
-    with _on(dev):
+    with _on(dev, stream):
         st = _lib.lib().kvq_pages_copy(byref(caches[0].desc), arrays, len(caches), _ptr(copy_src),
                                        _ptr(copy_dst), copy_src.numel(), _ptr(dev_status),
-                                       _stream_on(stream, dev))
+                                       _handle(dev))
     _lib.check(st, "kvq_pages_copy")
 

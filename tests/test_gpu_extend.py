@@ -5,7 +5,8 @@ import numpy as np
 import pytest
 
 from tests._cases import Guarded, check_guards
-from tests._prompt import FORMATS, check_extend, new_cache, read_rows
+from oracle import prompt_oracle as P
+from tests._prompt import FORMATS, check_extend, expected_rows, new_cache, read_rows
 
 pytestmark = pytest.mark.gpu
 
@@ -328,6 +329,99 @@ def test_streams_and_graph_replay():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, eager[i])
+
+
+@pytest.mark.parametrize("T", [3, 140])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("fmt", ["int4", "int8", "int2", "sym8", "nf4"])
+def test_scores_follow_the_dequantized_keys(fmt, D, T):
+    """Large scores, against (q - z) s itself: keys rounded to 11 bits would be
+    off by up to 2^-11 of a score of 80.
+
+    Bound: a score takes K to 22 bits and its scaling in fp32 (2^-22 and four
+    roundings of 2^-24, relative to 80 log2(e)), felt by its own weight and by
+    the sum of weights; weights and V are rounded to fp16 (2^-11 each, or
+    2^-32 absolute for small weights), the sums take L terms in fp32, the
+    output is rounded to fp16."""
+    import torch
+    import quantized_kv_decode_gb300 as K
+    rng = np.random.default_rng(11)
+    before, Hq, Hkv, scale = 150, 2, 1, 0.1
+    L = before + T
+    cache = new_cache(fmt, Hkv, D, 1, L)
+    k = rng.standard_normal((1, L, Hkv, D)).astype(np.float16)
+    k[..., 5] = rng.uniform(-25, 25, (1, L, Hkv))
+    v = rng.standard_normal((1, L, Hkv, D)).astype(np.float16)
+    K.kvq_append(cache, torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda(),
+                 torch.zeros(1, dtype=torch.int32, device="cuda"))
+    q = np.zeros((1, T, Hq, D), dtype=np.float16)
+    q[..., 0, 5], q[..., 1, 5] = 32, -32
+    got = K.kvq_extend_attn(cache, torch.from_numpy(q).cuda(), torch.tensor([before], dtype=torch.int32, device="cuda"),
+                            L, softmax_scale=scale, num_splits=1).cpu().numpy()[0].astype(np.float64)
+    kx, vx = (expected_rows(fmt, x[0]).transpose(1, 0, 2) for x in (k, v))
+    want, mass = P.extend_attention(q[0].astype(np.float64), kx, vx, before, scale)
+    top = 32 * scale * np.abs(kx[..., 5]).max() * 1.4427
+    rel = 2 * 2.0 ** -11 + 2 * top * (2.0 ** -22 + 4 * 2.0 ** -24) + L * 2.0 ** -23
+    bound = mass * rel + 2.0 ** -11 * np.abs(want) + L * 2.0 ** -32 * np.abs(vx).max() + 2.0 ** -24
+    assert (np.abs(got - want) / bound).max() <= 1.0
+
+
+@pytest.mark.parametrize("splits", [1, 3])
+@pytest.mark.parametrize("T", [3, 140])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_many_small_weights(D, T, splits):
+    """One key whose value is zero, and thousands 2^-20.4 of its weight that
+    make up the output: each weight keeps its 11 bits (fp16's own steps at
+    2^-20 are an eighth of that).  Scores are exact up to fp32's roundings."""
+    import torch
+    import quantized_kv_decode_gb300 as K
+    rng = np.random.default_rng(12)
+    before, scale = 2500, 0.0625
+    L = before + T
+    cache = new_cache("fp16", 1, D, 1, L)
+    k = np.zeros((1, L, 1, D), dtype=np.float16)
+    k[:, 1:, :, 3] = -14.140625
+    v = rng.uniform(1, 2, (1, L, 1, D)).astype(np.float16)
+    v[:, 0] = 0
+    K.kvq_append(cache, torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda(),
+                 torch.zeros(1, dtype=torch.int32, device="cuda"))
+    q = np.zeros((1, T, 1, D), dtype=np.float16)
+    q[..., 3] = 16
+    got = K.kvq_extend_attn(cache, torch.from_numpy(q).cuda(), torch.tensor([before], dtype=torch.int32, device="cuda"),
+                            L, softmax_scale=scale, num_splits=splits).cpu().numpy()[0].astype(np.float64)
+    kx, vx = (x[0].astype(np.float64).transpose(1, 0, 2) for x in (k, v))
+    want, mass = P.extend_attention(q[0].astype(np.float64), kx, vx, before, scale)
+    rel = 2.0 ** -11 + 2 * 20.4 * 4 * 2.0 ** -24 + 2 * L * 2.0 ** -24
+    bound = mass * rel + 2.0 ** -11 * np.abs(want)
+    assert (np.abs(got - want) / bound).max() <= 1.0
+
+
+def test_outputs_made_on_the_calls_stream():
+    """Outputs and workspaces made by a call on another stream than the
+    current one are made on that stream: work queued on the current stream
+    neither comes in between nor afterwards."""
+    import torch
+    import quantized_kv_decode_gb300 as K
+    rng = np.random.default_rng(13)
+    B, T, Hq, Hkv, D, L = 2, 9, 8, 2, 128, 900
+    cache = new_cache("int4", Hkv, D, B, L)
+    _fill(K, cache, rng, [L] * B, Hkv, D, L)
+    before = torch.tensor([L - T, 100], dtype=torch.int32, device="cuda")
+    new = torch.tensor([T, 5], dtype=torch.int32, device="cuda")
+    q = torch.from_numpy(rng.standard_normal((B, T, Hq, D)).astype(np.float16)).cuda()
+    rope = K.make_rope(D)
+    want = K.kvq_extend_attn(cache, q, before, L, new_lens=new)
+    turned = K.kvq_rope_apply(rope, q, seq_lens_before=before, new_lens=new)[0]
+    assert want.abs().max() > 0 and (want[1, 5:] == 0).all() and (turned[1, 5:] == 0).all()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream):
+        torch.cuda._sleep(100_000_000)  # the current stream is busy meanwhile
+        out = K.kvq_extend_attn(cache, q, before, L, new_lens=new, stream=stream)
+        y = K.kvq_rope_apply(rope, q, seq_lens_before=before, new_lens=new, stream=stream)[0]
+        side.synchronize()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(y, turned)
 
 
 def test_workspace_refusal_and_device_checks():

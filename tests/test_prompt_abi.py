@@ -160,6 +160,17 @@ def test_pool_refusals(K):
     assert lib.kvq_pages_reorder(byref(pool(batch=0, table=None)), None, None, None, None) == K.KVQ_OK
 
 
+def test_reserve_refuses_more_blocks_than_32_bits_count(K):
+    """Pages are counted in 32 bits: a call that could ask for more is refused
+    before anything is launched."""
+    lib = K.lib()
+    ref, table, a, b, c, ws = _ptrs(6)
+    for num_new, blocks, want in ((8 * 200000, 200000, K.KVQ_ERR_UNSUPPORTED), (2 ** 31 - 1, 2 ** 17, K.KVQ_ERR_UNSUPPORTED),
+                                  (8 * 200000, 131071, K.KVQ_ERR_WORKSPACE), (8 * 100000, 200000, K.KVQ_ERR_WORKSPACE)):
+        p = K.kvq_page_pool(64, 8, 16384, blocks, ref, table)
+        assert lib.kvq_pages_reserve(byref(p), a, None, num_new, b, c, None, ws, 8, None, None) == want
+
+
 def test_page_copy_refusals(K):
     lib = K.lib()
     caches = (K.kvq_cache * 2)(_cache(K), _cache(K))
