@@ -12,9 +12,9 @@
 //
 // The kernel here, on mma.sync, takes what the tensor-core kernel of
 // kvq_extend_tc.cuh does not: head_dim 256 and axis-aware caches.  As there, K
-// enters as hi + lo, V as hi alone, and the probabilities, rounded to fp16,
-// carry a factor (2^14: m is the exact maximum here) that keeps small ones in
-// fp16's normal range.
+// and V enter as hi + lo, and the probabilities, rounded to fp16, carry a
+// factor (2^14: m is the exact maximum here) that keeps small ones in fp16's
+// normal range.
 #include "kvq_extend_tc.cuh"
 #include "kvq_host.cuh"
 #include "kvq_load.cuh"
@@ -33,10 +33,10 @@ constexpr int kRows = 64;  // 4 warps of 16 rows
 constexpr int kThreads = 128;
 constexpr float kLift = 14.f;  // log2 of the factor in the probabilities, l and o
 
-// Keys per tile: K (hi and lo) and V rows as fp16 in shared memory
+// Keys per tile: K and V rows, hi and lo, as fp16 in shared memory
 __host__ __device__ constexpr int tile_keys(int D) { return D == 256 ? 32 : 64; }
 __host__ __device__ constexpr size_t extend_smem(int D) {
-  return (size_t)(kRows + 3 * tile_keys(D)) * D * 2 + 3 * tile_keys(D) * sizeof(int);
+  return (size_t)(kRows + 4 * tile_keys(D)) * D * 2 + 3 * tile_keys(D) * sizeof(int);
 }
 
 // Byte offset of 16-byte chunk c of row r in a [rows][D] fp16 tile; the
@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const __grid_constant_
   if (r0 >= live_rows) return;
 
   const uint32_t q_s = smem_u32(smem), k_s = q_s + kRows * D * 2, v_s = k_s + 2 * KEYS * D * 2;
-  int* ok_s = reinterpret_cast<int*>(smem + (kRows + 3 * KEYS) * D * 2);
+  int* ok_s = reinterpret_cast<int*>(smem + (kRows + 4 * KEYS) * D * 2);
   int* bad_s = ok_s + KEYS;  // [2][KEYS], the tiles in turn: V held an infinity or NaN (set to zero)
   for (int i = threadIdx.x; i < 2 * KEYS; i += kThreads) bad_s[i] = 0;
 
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const __grid_constant_
     __syncthreads();  // the tile before is used up (and q is in place)
     for (int i = threadIdx.x; i < KEYS * CH; i += kThreads) {
       const int j = i / CH, ch = i % CH, pos = ks + j;
-      uint4 kx = make_uint4(0u, 0u, 0u, 0u), kl = kx, vx = kx;
+      uint4 kx = make_uint4(0u, 0u, 0u, 0u), kl = kx, vx = kx, vl = kx;
       bool ok = pos < k1;
       if (ok) {
         const long long row = view_row(c, b, kvh, sp.L, pos);
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const __grid_constant_
           if (ch == 0 && p.status) atomicOr(p.status, KVQ_FLAG_BLOCK_TABLE);
         } else {
           kx = load8<BITS>(p.v, 0, b, kvh, sp.L, pos, row, ch, &kl);
-          vx = load8<BITS>(p.v, 1, b, kvh, sp.L, pos, row, ch);
+          vx = load8<BITS>(p.v, 1, b, kvh, sp.L, pos, row, ch, &vl);
           // In a tile that some row sees in part an infinite or NaN V must
           // not meet the zero weights of the rows that do not see it.
           if (ks + KEYS - 1 > all_see && (ext::nonfinite2(vx.x) || ext::nonfinite2(vx.y) || ext::nonfinite2(vx.z) ||
@@ -139,7 +139,10 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const __grid_constant_
         }
       }
       *reinterpret_cast<uint4*>(smem + kRows * D * 2 + at<D>(j, ch)) = kx;
-      if (BITS != 16) *reinterpret_cast<uint4*>(smem + (kRows + KEYS) * D * 2 + at<D>(j, ch)) = kl;
+      if (BITS != 16) {
+        *reinterpret_cast<uint4*>(smem + (kRows + KEYS) * D * 2 + at<D>(j, ch)) = kl;
+        *reinterpret_cast<uint4*>(smem + (kRows + 3 * KEYS) * D * 2 + at<D>(j, ch)) = vl;
+      }
       *reinterpret_cast<uint4*>(smem + (kRows + 2 * KEYS) * D * 2 + at<D>(j, ch)) = vx;
       if (ch == 0) ok_s[j] = ok;
     }
@@ -211,10 +214,13 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const __grid_constant_
       const uint32_t a3 = fast::pack_h2(s[2 * kb + 1][2], s[2 * kb + 1][3]);
 #pragma unroll
       for (int n = 0; n < D / 8; n += 2) {
-        uint32_t b0, b1, b2, b3;  // keys 16 kb .. +15, channels n*8 .. +15
-        ldsm_x4_t(v_s + at<D>(kb * 16 + (lane & 15), n + (lane >> 4)), b0, b1, b2, b3);
-        mma16816(o[n], a0, a1, a2, a3, b0, b1);
-        mma16816(o[n + 1], a0, a1, a2, a3, b2, b3);
+#pragma unroll
+        for (int part = 0; part < (BITS == 16 ? 1 : 2); ++part) {  // hi, lo
+          uint32_t b0, b1, b2, b3;  // keys 16 kb .. +15, channels n*8 .. +15
+          ldsm_x4_t(v_s + part * KEYS * D * 2 + at<D>(kb * 16 + (lane & 15), n + (lane >> 4)), b0, b1, b2, b3);
+          mma16816(o[n], a0, a1, a2, a3, b0, b1);
+          mma16816(o[n + 1], a0, a1, a2, a3, b2, b3);
+        }
       }
     }
   }

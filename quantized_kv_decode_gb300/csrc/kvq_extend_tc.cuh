@@ -23,14 +23,14 @@
 // softmax runs under the other's products.
 //
 // Precision.  q - z is a whole number (exact in fp16 up to 2048) and s has
-// 11 bits, so x_hat = (q - z) s has up to 23: K enters as the sum of two fp16
+// 11 bits, so x_hat = (q - z) s has up to 23: K and V enter as sums of two fp16
 // numbers, hi = fp16(x_hat) and lo = fp16(x_hat - hi), two products into one
-// accumulator.  With hi alone the scores of keys with large channels are off
-// by 4e-4 (rms, INT4 groups of 32 with 10x channels) and the outputs by 1e-3,
-// five times what rounding the output costs; with both by 3e-4, which the
-// fp16 rounding of V and of the probabilities and the output's own rounding
-// share.  V enters as hi alone: its errors average out over the keys.  Scores,
-// sums and O are fp32.  fp16 caches are exact as they are.
+// accumulator.  With hi alone for both, the outputs of keys with large
+// channels (INT4 groups of 32, 10x channels) are off by 1.0e-3 to 1.3e-3
+// relative, five times what rounding the output costs (2.1e-4); with K's lo by
+// 3.2e-4, with both by 2.7e-4: the output's own rounding and that of the
+// probabilities to fp16, whose errors average out over the keys.  Scores, sums
+// and O are fp32.  fp16 caches are exact as they are.
 //
 // Reference maximum.  m moves only when a tile's maximum exceeds it by 2^8,
 // so O in tensor memory is rescaled rarely.  P carries a factor 2^7 that the
@@ -76,9 +76,15 @@ struct Cfg {
   static constexpr int SOFT0 = 4, PROD0 = SOFT0 + SOFT, WARPS = PROD0 + PROD;
   static constexpr int THREADS = WARPS * 32;
   static constexpr int MAT = kKeys * D * 2;       // one fp16 tile
-  static constexpr int STAGE = (LO ? 3 : 2) * MAT;
-  static constexpr int STAGES = LO ? 3 : 4;
-  static constexpr int Q_STAGE = STAGES - (SOFT * 4096 + STAGE - 1) / STAGE;  // q passes through the stages from here on
+  // A stage holds K and V of a key tile, hi and lo.  Quantized formats fill
+  // and free the two by themselves, so that K of a tile to come is converted
+  // under the softmax, and two stages do.
+  static constexpr int HALF = (LO ? 2 : 1) * MAT, STAGE = 2 * HALF;
+  static constexpr int STAGES = !LO ? 4 : D == 128 ? 2 : 3;
+  static constexpr int K_STEP = LO ? HALF : STAGE, V_AT = LO ? STAGES * HALF : HALF, V_STEP = K_STEP;
+  // q passes through the V tiles (fp16: the stages) from this one on
+  static constexpr int Q_STAGE = STAGES - (SOFT * 4096 + V_STEP - 1) / V_STEP;
+  static constexpr int Q_AT = (LO ? V_AT : 0) + Q_STAGE * V_STEP;
   static constexpr int SEGS = D / 32;             // 32-channel segments of a row
   // A producer warp works on items: the whole rows of KPI keys of K or V, a
   // segment per lane.
@@ -92,7 +98,7 @@ struct Cfg {
   static constexpr int HDR = kKeys * D / 4 + 16;  // most bytes of one header array, from a 16-byte boundary on
   static constexpr int RAW = LO ? 2 * CODES + 4 * HDR : 0;     // K codes, V codes, K scale, K zero, V scale, V zero
   // arrivals that fill a ring slot (fp16: a stage's copies and key masks), and a stage
-  static constexpr int RAW_FULL = LO ? LOAD : PROD * 32 + 1, FULL = LO ? PROD : 1;
+  static constexpr int RAW_FULL = LO ? LOAD : PROD * 32 + 1, FULL = LO ? PROD / 2 : 1;
   static constexpr int SLOTS = LO ? DEPTH : STAGES;
   // tensor memory columns: per tile S (64, P in its place), O (D), Q (D / 2)
   static constexpr uint32_t COL_S = 0, COL_O = 2 * kKeys, COL_Q = COL_O + 2 * D, COLS = 512;
@@ -112,10 +118,10 @@ template <int STAGES>
 struct Shared {
   unsigned long long raw_full[kMaxDepth], raw_empty[kMaxDepth];
   uint32_t raw_ok[kMaxDepth][2];
-  unsigned long long full[STAGES], empty[STAGES];
+  unsigned long long full[2][STAGES], empty[2][STAGES];  // K, V (fp16: full[0] and empty[1], both at once)
   unsigned long long q_full[2], s_full[2], p_full[2], o_full[2], turn[2], merge;
   float2 ml[128];           // the second stream's maximum and sum per row
-  uint32_t ok[STAGES][2];   // per key: mapped and before the end
+  uint32_t ok[2 * STAGES][2];  // per key: mapped and before the end (a K tile is freed before the softmax has read these)
   alignas(4) uint8_t bad[STAGES][kKeys];  // per key: V held an infinity or NaN (set to zero)
   uint32_t tmem;
   int stop;
@@ -229,12 +235,12 @@ __device__ __forceinline__ void codes8(const Seg<BITS>& x, int ch, const Group& 
   }
 }
 
-// One segment to fp16 (hi, and lo for K) at its places in the tile: blocks
+// One segment to fp16, hi and lo, at its places in the tile: blocks
 // of 64 channels, [key][128 bytes], 16-byte chunks XORed with the key.
 // NG: groups in the segment.  swap (0 or 2): x holds its chunks in that order.
 template <int BITS, int KIND, int NG>
-__device__ __forceinline__ void store_seg(const Seg<BITS>& x, bool is_k, int key, int seg, int sym, int swap,
-                                          uint8_t* hi, uint8_t* lo, const uint32_t (&lut)[4]) {
+__device__ __forceinline__ void store_seg(const Seg<BITS>& x, int key, int seg, int sym, int swap, uint8_t* hi,
+                                          uint8_t* lo, const uint32_t (&lut)[4]) {
   const uint32_t base = (uint32_t)((seg >> 1) * (kKeys * 128) + key * 128);
   const uint32_t turn = (uint32_t)(((seg & 1) * 4) ^ swap ^ (key & 7));
   Group g[NG];
@@ -254,11 +260,9 @@ __device__ __forceinline__ void store_seg(const Seg<BITS>& x, bool is_k, int key
       for (int i = 0; i < 4; ++i) v[i] = __hmul2_rn(d[i], gc.s);
       const uint32_t at = base + ((turn ^ ch) << 4);
       *reinterpret_cast<uint4*>(hi + at) = make_uint4(as_u32(v[0]), as_u32(v[1]), as_u32(v[2]), as_u32(v[3]));
-      if (is_k) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = __hfma2(d[i], gc.s, __hneg2(v[i]));  // exact inside: what hi left
-        *reinterpret_cast<uint4*>(lo + at) = make_uint4(as_u32(v[0]), as_u32(v[1]), as_u32(v[2]), as_u32(v[3]));
-      }
+      for (int i = 0; i < 4; ++i) v[i] = __hfma2(d[i], gc.s, __hneg2(v[i]));  // exact inside: what hi left
+      *reinterpret_cast<uint4*>(lo + at) = make_uint4(as_u32(v[0]), as_u32(v[1]), as_u32(v[2]), as_u32(v[3]));
     }
   } else {  // far zero-points and scales near fp16's end, in fp32
 #pragma unroll
@@ -281,7 +285,7 @@ __device__ __forceinline__ void store_seg(const Seg<BITS>& x, bool is_k, int key
       }
       const uint32_t at = base + ((turn ^ ch) << 4);
       *reinterpret_cast<uint4*>(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
-      if (is_k) *reinterpret_cast<uint4*>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
+      *reinterpret_cast<uint4*>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
     }
   }
 }
@@ -328,8 +332,8 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
 
   static_assert(sizeof(Shared<C::STAGES>) <= 2048, "room behind the stages");
   const uint32_t bars = tc::smem_addr(&sh);
-  auto full = [&](int s) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, full) + 8 * s; };
-  auto empty = [&](int s) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, empty) + 8 * s; };
+  auto full = [&](int v, int s) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, full) + 8 * (v * C::STAGES + s); };
+  auto empty = [&](int v, int s) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, empty) + 8 * (v * C::STAGES + s); };
   auto raw_full = [&](int s) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, raw_full) + 8 * s; };
   auto raw_empty = [&](int s) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, raw_empty) + 8 * s; };
   auto q_full = [&](int i) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, q_full) + 8 * i; };
@@ -341,9 +345,9 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
   volatile int* stop = &sh.stop;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::STAGES; ++s) {
-      tc::mbar_init(full(s), C::FULL);
-      tc::mbar_init(empty(s), C::DUAL ? 1 : nq);
+    for (int s = 0; s < 2 * C::STAGES; ++s) {
+      tc::mbar_init(full(0, s), C::FULL);
+      tc::mbar_init(empty(0, s), C::DUAL ? 1 : nq);
     }
     for (int s = 0; s < C::SLOTS; ++s) {
       tc::mbar_init(raw_full(s), C::RAW_FULL);
@@ -392,7 +396,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
     const bool any_live = row0 < live_rows;
     // 32 rows of 128 bytes in the stages' memory, before they are first
     // filled and after the last product
-    uint8_t* scratch = smem + C::Q_STAGE * C::STAGE + (warp - C::SOFT0) * 4096;
+    uint8_t* scratch = smem + C::Q_AT + (warp - C::SOFT0) * 4096;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + C::COL_S + i * kKeys;
     const uint32_t to = tmem + lanes + C::COL_O + i * D;
@@ -463,7 +467,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
         tc::ld32(ts, u[0]);
         tc::ld32(ts + 32, u[1]);
         const int ks = k0 + j * kKeys;
-        const uint32_t ok0 = sh.ok[st][0], ok1 = sh.ok[st][1];
+        const uint32_t ok0 = sh.ok[j % (2 * C::STAGES)][0], ok1 = sh.ok[j % (2 * C::STAGES)][1];
         const bool whole = __all_sync(0xffffffffu, (ok0 & ok1) == 0xFFFFFFFFu && ks + kKeys - 1 <= last);
         tc::wait_ld();
         if (!whole) {
@@ -659,7 +663,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
           lut[2 + (i >> 2)] |= (h >> 8) << (8 * (i & 3));
         }
       }
-      constexpr int KI = kKeys / C::KPI;  // items of K (and of V)
+      const int is_v = pw >= C::PROD / 2;  // half the warps turn K, half V
       const int seg = lane % C::SEGS, key_l = lane / C::SEGS;
       const int swap = seg >= 2 ? 2 : 0;
       const bool zeros = KIND == 0 && !c.sym;
@@ -670,31 +674,30 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
         int st = 0, ph = 1, slot = 0, rph = 0;
 #pragma unroll 1
         for (int j = 0; j < tiles; ++j) {
-          if (ok) ok = tc::mbar_wait(raw_full(slot), rph, stop) && tc::mbar_wait(empty(st), ph, stop);
-          ok = __all_sync(0xffffffffu, ok);
-          if (j == C::Q_STAGE) wait_q();
-          uint8_t* base = smem + st * C::STAGE;
+          if (ok) ok = tc::mbar_wait(raw_full(slot), rph, stop);
           const uint8_t* ring = smem + C::STAGES * C::STAGE + slot * C::RAW;
           const uint32_t ok0 = sh.raw_ok[slot][0], ok1 = sh.raw_ok[slot][1];
-          if (pw == 0 && lane == 0) sh.ok[st][0] = ok0, sh.ok[st][1] = ok1;
           const bool all = (ok0 & ok1) == 0xFFFFFFFFu;
+          if (ok) ok = tc::mbar_wait(empty(is_v, st), ph, stop);
+          ok = __all_sync(0xffffffffu, ok);
+          if (is_v && j == C::Q_STAGE) wait_q();
+          if (pw == 0 && lane == 0)
+            sh.ok[j % (2 * C::STAGES)][0] = ok0, sh.ok[j % (2 * C::STAGES)][1] = ok1;
+          uint8_t* const to = smem + (is_v ? C::V_AT + st * C::V_STEP : st * C::K_STEP);
 #pragma unroll 1
           for (int u = 0; u < C::MINE; ++u) {
-            const int item = u * C::PROD + pw, key0 = (item % KI) * C::KPI, key = key0 + key_l;
-            const bool is_k = item < KI;
-            const uint8_t* h = ring + 2 * C::CODES + (is_k ? 0 : 2 * C::HDR) + mis + key * hb + hseg;
+            const int key0 = (u * (C::PROD / 2) + (pw & (C::PROD / 2 - 1))) * C::KPI, key = key0 + key_l;
+            const uint8_t* h = ring + 2 * C::CODES + is_v * 2 * C::HDR + mis + key * hb + hseg;
             Seg<BITS> x;
-            take_item<BITS, KIND, NG>(ring + (is_k ? 0 : C::CODES) + key0 * (D * BITS / 8), h, h + C::HDR, zeros, lane,
-                                      swap, x);
+            take_item<BITS, KIND, NG>(ring + is_v * C::CODES + key0 * (D * BITS / 8), h, h + C::HDR, zeros, lane, swap, x);
             if (!all && !((key < 32 ? ok0 : ok1) >> (key & 31) & 1u))  // not a key: zeros, whatever the ring held
               x.s[0] = x.s[1] = x.z[0] = x.z[1] = 0;
-            store_seg<BITS, KIND, NG>(x, is_k, key, seg, c.sym, swap, base + (is_k ? 0 : 2 * C::MAT), base + C::MAT,
-                                      lut);
+            store_seg<BITS, KIND, NG>(x, key, seg, c.sym, swap, to, to + C::MAT, lut);
           }
           tc::fence_async_shared();
           __syncwarp();
           if (lane == 0) {
-            tc::mbar_arrive(full(st));
+            tc::mbar_arrive(full(is_v, st));
             tc::mbar_arrive(raw_empty(slot));
           }
           if (++st == C::STAGES) st = 0, ph ^= 1;
@@ -712,7 +715,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
 #pragma unroll 1
       for (int j = 0; j < tiles; ++j) {
         const int st = j % C::STAGES;
-        if (ok) ok = tc::mbar_wait(empty(st), ((j / C::STAGES) & 1) ^ 1, stop);
+        if (ok) ok = tc::mbar_wait(empty(1, st), ((j / C::STAGES) & 1) ^ 1, stop);
         ok = __all_sync(0xffffffffu, ok);
         if (j == C::Q_STAGE) wait_q();
         uint8_t* const stage = smem + st * C::STAGE;
@@ -727,7 +730,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
           fast::cp_async16(dst + C::MAT, p.v.codes[1] + o, row >= 0 && KVQ_IN(c, KVQ_ARRAY_V_CODES, p.v.codes[1] + o, 16));
         }
         if (pw == 0) {
-          note_keys(sh.ok[st], j);
+          note_keys(sh.ok[j % (2 * C::STAGES)], j);
           if (lane == 0) tc::mbar_arrive(raw_full(st));
         }
         if (k0 + (j + 1) * kKeys - 1 <= all_see) {
@@ -854,7 +857,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
         const int st = j % C::STAGES;
         ok = __all_sync(0xffffffffu, tc::mbar_wait(raw_full(st), (j / C::STAGES) & 1, stop));
         tc::fence_async_shared();
-        if (ok && lane == 0) tc::mbar_arrive(full(st));
+        if (ok && lane == 0) tc::mbar_arrive(full(0, st));
         __syncwarp();
       }
     }
@@ -868,10 +871,10 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
     const uint32_t data = tc::smem_addr(smem);
     constexpr uint32_t hi = tc::desc_hi(1024);
     const uint32_t k_lo = tc::desc_lo(data, 16);
-    const uint32_t v_lo = tc::desc_lo(data + (C::LO ? 2 : 1) * C::MAT, kKeys * 128);
+    const uint32_t v_lo = tc::desc_lo(data + C::V_AT, kKeys * 128);
     const uint32_t d_s = t0 + C::COL_S + i * kKeys, d_o = t0 + C::COL_O + i * D, a_q = t0 + C::COL_Q + i * (D / 2);
     auto qk = [&](int st) {
-      const uint32_t kd = k_lo + st * (C::STAGE / 16);
+      const uint32_t kd = k_lo + st * (C::K_STEP / 16);
       // hi, then lo: the tiles follow one another in 64-channel blocks
 #pragma unroll
       for (int n = 0; n < (C::LO ? 2 : 1) * (D / 64); ++n)
@@ -880,6 +883,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
           tc::mma_ts(d_s, a_q + ((n * 4) & (D / 16 - 1)) * 8 + kk * 8, kd + n * (kKeys * 128 / 16) + kk * 2, hi, id_qk,
                      n || kk);
       tc::commit(s_full(i));
+      if (C::LO) tc::commit(empty(0, st));
     };
     auto wait = [&](uint32_t bar, int parity) { return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, stop)); };
     // the warps take turns, so that one tile's softmax runs under the other
@@ -889,7 +893,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
       __syncwarp();
     };
     const int j0 = C::DUAL ? i : 0;  // this stream's first key tile
-    if (i < nq && j0 < tiles && wait(full(j0), 0) && wait(q_full(i), 0) && (C::DUAL || i == 0 || wait(turn(1), 0))) {
+    if (i < nq && j0 < tiles && wait(full(0, j0), 0) && wait(q_full(i), 0) && (C::DUAL || i == 0 || wait(turn(1), 0))) {
       tc::fence_after();
       qk(j0);
       pass();
@@ -899,22 +903,25 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
         const int next = j + STEP;
         const bool more = next < tiles;
         const int st1 = next % C::STAGES;
-        if (!C::DUAL && more && !wait(full(st1), (next / C::STAGES) & 1)) break;
+        if (!C::DUAL && more && !wait(full(0, st1), (next / C::STAGES) & 1)) break;
+        if (C::LO && !wait(full(1, st), (j / C::STAGES) & 1)) break;
         if (!wait(p_full(i), n & 1)) break;
         if (!C::DUAL && nq == 2 && !wait(turn(i), tp)) break;
         tp ^= 1;
         tc::fence_after();
-        const uint32_t vd = v_lo + st * (C::STAGE / 16);
+        const uint32_t vd = v_lo + st * (C::V_STEP / 16);
 #pragma unroll
-        for (int kk = 0; kk < kKeys / 16; ++kk)
-          tc::mma_ts(d_o, d_s + kk * 8, vd + kk * (2048 / 16), hi, id_pv, n || kk);
+        for (int part = 0; part < (C::LO ? 2 : 1); ++part)
+#pragma unroll
+          for (int kk = 0; kk < kKeys / 16; ++kk)
+            tc::mma_ts(d_o, d_s + kk * 8, vd + part * (C::MAT / 16) + kk * (2048 / 16), hi, id_pv, n || part || kk);
         if (!more) {
           tc::commit(o_full(i));
           pass();
           break;
         }
-        tc::commit(empty(st));
-        if (C::DUAL && !wait(full(st1), (next / C::STAGES) & 1)) break;
+        tc::commit(empty(1, st));
+        if (C::DUAL && !wait(full(0, st1), (next / C::STAGES) & 1)) break;
         qk(st1);
         pass();
         st = st1;
