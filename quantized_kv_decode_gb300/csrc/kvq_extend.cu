@@ -14,7 +14,10 @@
 // kvq_extend_tc.cuh does not: head_dim 256 and axis-aware caches.  As there, K
 // and V enter as hi + lo, and the probabilities, rounded to fp16, carry a
 // factor (2^14: m is the exact maximum here) that keeps small ones in fp16's
-// normal range.
+// normal range.  Bound by the conversion of a tile before its products, which
+// nothing overlaps: it is the form that is right for every cache, kept for the
+// shapes that tensor memory has no room for (D = 256: two tiles' O alone fill
+// it) or whose keys have a scale per channel.
 #include "kvq_extend_tc.cuh"
 #include "kvq_host.cuh"
 #include "kvq_load.cuh"

@@ -16,11 +16,21 @@
 // bytes a cycle from shared memory, half its bandwidth or less; with Q in
 // shared memory a 64-key step would be bound by fetching Q again.
 //
-// Warps.  0 and 3 issue the MMAs, a tile each; 1 and 2 copy codes and headers to a ring in
-// shared memory; from 4 on softmax, a row per thread (four warps a tile); the
-// producers behind turn the ring's codes into fp16 in the tensor core's
-// swizzled layout (eight warps; four for fp16).  One tile's (or stream's)
-// softmax runs under the other's products.
+// Warps.  0 and 3 issue the MMAs, a tile each; 1 and 2 copy codes and headers
+// to a ring in shared memory; from 4 on softmax, a row per thread (four warps a
+// tile); the eight producers behind turn the ring's codes into fp16 in the
+// tensor core's swizzled layout, four of them K's and four V's (fp16 caches:
+// they copy rows).  One tile's (or stream's) softmax runs under the other's
+// products.
+//
+// What bounds it.  256 rows: the chain scores - softmax - weighted V of a tile,
+// about 3000 cycles a 64-key step of which the products take 2048 (K and V each
+// in two parts; fp16 caches 1024 of 2400): INT4, 4096 tokens after 12288, 32 / 8
+// heads, 1.14 ms, 848 TFLOP/s of the formula's; fp16 1.00 ms, 963.  S of the
+// next step cannot be computed ahead: S, O and q of two tiles fill tensor
+// memory.  At most 128 rows: the conversion, about 1300 of 1900 cycles a step,
+// bound by its own latency with two warps a scheduler: 17 tokens over 32768
+// (INT8) 46 us.
 //
 // Precision.  q - z is a whole number (exact in fp16 up to 2048) and s has
 // 11 bits, so x_hat = (q - z) s has up to 23: K and V enter as sums of two fp16
@@ -69,7 +79,7 @@ struct Cfg {
   static constexpr bool DUAL = NQ == 1;           // one tile of rows, the key tiles shared between two streams
   static constexpr int ROWS = 128 * NQ;
   static constexpr int SOFT = 8;                  // softmax warps
-  static constexpr int PROD = LO ? 8 : 4;         // producer warps
+  static constexpr int PROD = 8;                  // producer warps
   static constexpr int LOAD = LO ? 2 : 1;         // loader warps, K and V (fp16: the warp that passes stages on)
   // warps 0 and 3 issue the MMAs, 1 .. LOAD load; softmax from 4 on (a warp reads
   // the tensor memory lanes of its number modulo 4), producers behind
@@ -238,7 +248,7 @@ __device__ __forceinline__ void codes8(const Seg<BITS>& x, int ch, const Group& 
 // One segment to fp16, hi and lo, at its places in the tile: blocks
 // of 64 channels, [key][128 bytes], 16-byte chunks XORed with the key.
 // NG: groups in the segment.  swap (0 or 2): x holds its chunks in that order.
-template <int BITS, int KIND, int NG>
+template <int BITS, int KIND, int NG, int UNROLL>
 __device__ __forceinline__ void store_seg(const Seg<BITS>& x, int key, int seg, int sym, int swap, uint8_t* hi,
                                           uint8_t* lo, const uint32_t (&lut)[4]) {
   const uint32_t base = (uint32_t)((seg >> 1) * (kKeys * 128) + key * 128);
@@ -251,11 +261,17 @@ __device__ __forceinline__ void store_seg(const Seg<BITS>& x, int key, int seg, 
     plain = plain && g[n].plain;
   }
   if (plain) {
-#pragma unroll
+    // A small loop, its words shifted on.  One chunk a turn where the softmax
+    // of 256 rows runs beside it, whose code shares the instruction caches
+    // (late prompt chunk: 1.135 ms, two a turn 1.163); two a turn where few
+    // rows wait for the conversion (16 x 5 tokens over ragged 8000: 98 us, one
+    // a turn 105).
+    Seg<BITS> y = x;
+    Group gc = g[0];
+#pragma unroll UNROLL
     for (int ch = 0; ch < 4; ++ch) {
-      const Group& gc = g[ch / (4 / NG)];
       __half2 d[4], v[4];
-      codes8<BITS, KIND>(x, ch, gc, lut, d);
+      codes8<BITS, KIND>(y, 0, gc, lut, d);
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = __hmul2_rn(d[i], gc.s);
       const uint32_t at = base + ((turn ^ ch) << 4);
@@ -263,6 +279,20 @@ __device__ __forceinline__ void store_seg(const Seg<BITS>& x, int key, int seg, 
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = __hfma2(d[i], gc.s, __hneg2(v[i]));  // exact inside: what hi left
       *reinterpret_cast<uint4*>(lo + at) = make_uint4(as_u32(v[0]), as_u32(v[1]), as_u32(v[2]), as_u32(v[3]));
+      if constexpr (BITS == 2) {
+        y.w[0] = __funnelshift_r(y.w[0], y.w[1], 16);
+        y.w[1] >>= 16;
+      } else {
+#pragma unroll
+        for (int i = 0; i + BITS / 4 < BITS; ++i) y.w[i] = y.w[i + BITS / 4];
+      }
+      if constexpr (NG > 1) {
+        if (NG == 4 || ch == 1) {
+          y.s[0] = __funnelshift_r(y.s[0], y.s[1], 16), y.s[1] >>= 16;
+          y.z[0] = __funnelshift_r(y.z[0], y.z[1], 16), y.z[1] >>= 16;
+          gc = group_of<BITS, KIND>(y.s[0], y.z[0], sym);
+        }
+      }
     }
   } else {  // far zero-points and scales near fp16's end, in fp32
 #pragma unroll
@@ -692,7 +722,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
             take_item<BITS, KIND, NG>(ring + is_v * C::CODES + key0 * (D * BITS / 8), h, h + C::HDR, zeros, lane, swap, x);
             if (!all && !((key < 32 ? ok0 : ok1) >> (key & 31) & 1u))  // not a key: zeros, whatever the ring held
               x.s[0] = x.s[1] = x.z[0] = x.z[1] = 0;
-            store_seg<BITS, KIND, NG>(x, key, seg, c.sym, swap, to, to + C::MAT, lut);
+            store_seg<BITS, KIND, NG, C::DUAL ? 2 : 1>(x, key, seg, c.sym, swap, to, to + C::MAT, lut);
           }
           tc::fence_async_shared();
           __syncwarp();
@@ -767,6 +797,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
       const bool zeros = KIND == 0 && !c.sym, paged = c.layout == KVQ_PAGED;
       const uint32_t hb = 2 * c.ngroups;
       constexpr uint32_t RB = D * BITS / 8;
+      const long long hdr_bytes = (long long)p.batch * c.Hkv * c.slots * hb;  // dense: of a header array, at least
       const uint8_t* const codes = p.v.codes[which];
       const uint8_t* const scale = reinterpret_cast<const uint8_t*>(p.v.scale[which]);
       const uint8_t* const zero = reinterpret_cast<const uint8_t*>(p.v.zero[which]);
@@ -790,10 +821,14 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
                KVQ_IN(c, which ? KVQ_ARRAY_V_SCALE : KVQ_ARRAY_K_SCALE, scale + row * hb, (long long)rows * hb) &&
                (!zeros || KVQ_IN(c, which ? KVQ_ARRAY_V_ZERO : KVQ_ARRAY_K_ZERO, zero + row * hb, (long long)rows * hb));
         // Whole 16-byte pieces: in a page, rows rounded up to 8 (the page has
-        // them); a dense header array starts mis bytes into one, and what its
-        // last piece holds is copied by hand.
+        // them); a dense header array starts mis bytes into one and is copied
+        // to the end of its last one, which holds the rows that follow.  Behind
+        // the last of all rows there may be nothing: that piece is copied by
+        // hand (its loads wait for memory: 900 cycles a tile when every tile
+        // did it).
         const uint32_t up = paged ? (rows + 7) & ~7 : rows;
-        const uint32_t hdr = paged ? up * hb : (mis + rows * hb) & ~15u;
+        const bool by_hand = !paged && row >= 0 && (row + rows) * hb + 15 > hdr_bytes;
+        const uint32_t hdr = paged ? up * hb : (mis + rows * hb + (by_hand ? 0 : 15)) & ~15u;
         const uint32_t total = __reduce_add_sync(0xffffffffu, live ? up * RB + (zeros ? 2 : 1) * hdr : 0u);
         ok = __all_sync(0xffffffffu, tc::mbar_wait(raw_empty(slot), ph, stop));
         if (!ok) break;
@@ -818,7 +853,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
         }
         uint32_t todo = __ballot_sync(0xffffffffu, live);
         const int n = mis + (p1 - p0) * (int)hb;
-        if (!paged && (n & 15) && todo) {
+        if (__any_sync(0xffffffffu, by_hand) && (n & 15) && todo) {
           const int x = (n & ~15) + 2 * lane;
           const long long from = (((long long)b * c.Hkv + kvh) * c.slots + p0) * hb - mis + x;
           if (x >= mis && x < n) {
