@@ -129,7 +129,7 @@ struct Shared {
   unsigned long long raw_full[kMaxDepth], raw_empty[kMaxDepth];
   uint32_t raw_ok[kMaxDepth][2];
   unsigned long long full[2][STAGES], empty[2][STAGES];  // K, V (fp16: full[0] and empty[1], both at once)
-  unsigned long long q_full[2], s_full[2], p_full[2], o_full[2], turn[2], merge;
+  unsigned long long q_full[2], s_full[2], p_half[2], p_full[2], o_full[2], turn[2], merge;
   float2 ml[128];           // the second stream's maximum and sum per row
   uint32_t ok[2 * STAGES][2];  // per key: mapped and before the end (a K tile is freed before the softmax has read these)
   alignas(4) uint8_t bad[STAGES][kKeys];  // per key: V held an infinity or NaN (set to zero)
@@ -368,6 +368,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
   auto raw_empty = [&](int s) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, raw_empty) + 8 * s; };
   auto q_full = [&](int i) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, q_full) + 8 * i; };
   auto s_full = [&](int i) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, s_full) + 8 * i; };
+  auto p_half = [&](int i) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, p_half) + 8 * i; };
   auto p_full = [&](int i) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, p_full) + 8 * i; };
   auto turn = [&](int i) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, turn) + 8 * i; };
   const uint32_t merge = bars + (uint32_t)offsetof(Shared<C::STAGES>, merge);
@@ -386,6 +387,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(q_full(i), 128);
       tc::mbar_init(s_full(i), 1);
+      tc::mbar_init(p_half(i), 4);
       tc::mbar_init(p_full(i), 4);
       tc::mbar_init(o_full(i), 1);
       tc::mbar_init(turn(i), 1);
@@ -563,10 +565,18 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
             w[e >> 1] = fast::pack_h2(x.x, x.y);
           }
           tc::st8(ts + 8 * h, w);
+          if (h == 1) {  // the first 32 keys' products may start
+            tc::wait_st();
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(p_half(i));
+          }
         }
         tc::wait_st();
         sum[0] = tc::add2(sum[0], sum[1]);
         l += sum[0].x + sum[0].y;
+      } else if (lane == 0) {
+        tc::mbar_arrive(p_half(i));
       }
       tc::fence_before();
       __syncwarp();
@@ -940,16 +950,24 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
         const int st1 = next % C::STAGES;
         if (!C::DUAL && more && !wait(full(0, st1), (next / C::STAGES) & 1)) break;
         if (C::LO && !wait(full(1, st), (j / C::STAGES) & 1)) break;
-        if (!wait(p_full(i), n & 1)) break;
+        if (!wait(p_half(i), n & 1)) break;
         if (!C::DUAL && nq == 2 && !wait(turn(i), tp)) break;
         tp ^= 1;
         tc::fence_after();
         const uint32_t vd = v_lo + st * (C::V_STEP / 16);
+        auto pv = [&](int half) {
 #pragma unroll
-        for (int part = 0; part < (C::LO ? 2 : 1); ++part)
+          for (int part = 0; part < (C::LO ? 2 : 1); ++part)
 #pragma unroll
-          for (int kk = 0; kk < kKeys / 16; ++kk)
-            tc::mma_ts(d_o, d_s + kk * 8, vd + part * (C::MAT / 16) + kk * (2048 / 16), hi, id_pv, n || part || kk);
+            for (int e = 0; e < kKeys / 32; ++e) {
+              const int kk = half * (kKeys / 32) + e;
+              tc::mma_ts(d_o, d_s + kk * 8, vd + part * (C::MAT / 16) + kk * (2048 / 16), hi, id_pv, n || part || kk);
+            }
+        };
+        pv(0);
+        if (!wait(p_full(i), n & 1)) break;
+        tc::fence_after();
+        pv(1);
         if (!more) {
           tc::commit(o_full(i));
           pass();
