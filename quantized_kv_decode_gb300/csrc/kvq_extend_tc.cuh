@@ -110,11 +110,17 @@ struct Cfg {
   // arrivals that fill a ring slot (fp16: a stage's copies and key masks), and a stage
   static constexpr int RAW_FULL = LO ? LOAD : PROD * 32 + 1, FULL = LO ? PROD / 2 : 1;
   static constexpr int SLOTS = LO ? DEPTH : STAGES;
-  // tensor memory columns: per tile S (64, P in its place), O (D), Q (D / 2)
-  static constexpr uint32_t COL_S = 0, COL_O = 2 * kKeys, COL_Q = COL_O + 2 * D, COLS = 512;
-  static constexpr size_t SMEM = (size_t)STAGES * STAGE + (size_t)DEPTH * RAW + 1024 + 2048;
+  // Two S per tile where tensor memory has room for them: at head_dim 64, and
+  // at 128 with q in shared memory, which only fp16 caches leave the room for.
+  static constexpr bool Q_SMEM = !LO && D == 128 && !DUAL;
+  static constexpr int SB = !DUAL && (D == 64 || Q_SMEM) ? 2 : 1;
+  // tensor memory columns: per tile S (64 each, P in its place), O (D), Q (D / 2)
+  static constexpr uint32_t COL_S = 0, COL_O = 2 * SB * kKeys, COL_Q = COL_O + 2 * D, COLS = 512;
+  static constexpr int Q_BYTES = Q_SMEM ? 2 * 128 * D * 2 : 0;  // behind the ring, on a 1024-byte boundary
+  static_assert(!Q_SMEM || DEPTH == 0, "q follows the stages");
+  static constexpr size_t SMEM = (size_t)STAGES * STAGE + (size_t)DEPTH * RAW + Q_BYTES + 1024 + 2048;
   static_assert(SMEM <= 227 * 1024, "shared memory");
-  static_assert(COL_Q + 2 * D / 2 <= COLS, "tensor memory");
+  static_assert(COL_Q + (Q_SMEM ? 0 : 2 * D / 2) <= COLS, "tensor memory");
   static_assert((size_t)STAGES * STAGE >= (DUAL ? (size_t)128 * D * 4 : 0) + SOFT * 4096, "scratch in the stages");
   // channel held at place i of an eight-channel chunk (the unpacking leaves
   // 4-bit and 2-bit codes as pairs (i, i + 4))
@@ -129,7 +135,7 @@ struct Shared {
   unsigned long long raw_full[kMaxDepth], raw_empty[kMaxDepth];
   uint32_t raw_ok[kMaxDepth][2];
   unsigned long long full[2][STAGES], empty[2][STAGES];  // K, V (fp16: full[0] and empty[1], both at once)
-  unsigned long long q_full[2], s_full[2], p_half[2], p_full[2], o_full[2], turn[2], merge;
+  unsigned long long q_full[2], s_full[4], p_half[4], p_full[4], o_full[2], o_step[2], turn[2], merge;  // s, p: [tile][S]
   float2 ml[128];           // the second stream's maximum and sum per row
   uint32_t ok[2 * STAGES][2];  // per key: mapped and before the end (a K tile is freed before the softmax has read these)
   alignas(4) uint8_t bad[STAGES][kKeys];  // per key: V held an infinity or NaN (set to zero)
@@ -334,7 +340,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
   pdl_launch_dependents();
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + ((1024 - (tc::smem_addr(raw) & 1023)) & 1023);
-  auto& sh = *reinterpret_cast<Shared<C::STAGES>*>(smem + C::STAGES * C::STAGE + C::DEPTH * C::RAW);
+  auto& sh = *reinterpret_cast<Shared<C::STAGES>*>(smem + C::STAGES * C::STAGE + C::DEPTH * C::RAW + C::Q_BYTES);
   const CacheGeom& c = p.v.geom;
   const int warp = tc::uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int kvh = blockIdx.y, b = blockIdx.z;
@@ -362,14 +368,18 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
 
   static_assert(sizeof(Shared<C::STAGES>) <= 2048, "room behind the stages");
   const uint32_t bars = tc::smem_addr(&sh);
+  // which S a tile's n-th step uses, and its barriers' phase
+  auto buf = [](int n) { return C::SB == 2 ? n & 1 : 0; };
+  auto phase = [](int n) { return C::SB == 2 ? n >> 1 & 1 : n & 1; };
   auto full = [&](int v, int s) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, full) + 8 * (v * C::STAGES + s); };
   auto empty = [&](int v, int s) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, empty) + 8 * (v * C::STAGES + s); };
   auto raw_full = [&](int s) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, raw_full) + 8 * s; };
   auto raw_empty = [&](int s) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, raw_empty) + 8 * s; };
   auto q_full = [&](int i) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, q_full) + 8 * i; };
-  auto s_full = [&](int i) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, s_full) + 8 * i; };
-  auto p_half = [&](int i) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, p_half) + 8 * i; };
-  auto p_full = [&](int i) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, p_full) + 8 * i; };
+  auto s_full = [&](int i, int n) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, s_full) + 8 * (2 * i + buf(n)); };
+  auto o_step = [&](int i) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, o_step) + 8 * i; };
+  auto p_half = [&](int i, int n) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, p_half) + 8 * (2 * i + buf(n)); };
+  auto p_full = [&](int i, int n) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, p_full) + 8 * (2 * i + buf(n)); };
   auto turn = [&](int i) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, turn) + 8 * i; };
   const uint32_t merge = bars + (uint32_t)offsetof(Shared<C::STAGES>, merge);
   auto o_full = [&](int i) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, o_full) + 8 * i; };
@@ -386,9 +396,12 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(q_full(i), 128);
-      tc::mbar_init(s_full(i), 1);
-      tc::mbar_init(p_half(i), 4);
-      tc::mbar_init(p_full(i), 4);
+      for (int n = 0; n < C::SB; ++n) {
+        tc::mbar_init(s_full(i, n), 1);
+        tc::mbar_init(p_half(i, n), 4);
+        tc::mbar_init(p_full(i, n), 4);
+      }
+      tc::mbar_init(o_step(i), 1);
       tc::mbar_init(o_full(i), 1);
       tc::mbar_init(turn(i), 1);
     }
@@ -430,7 +443,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
     // filled and after the last product
     uint8_t* scratch = smem + C::Q_AT + (warp - C::SOFT0) * 4096;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lanes + C::COL_S + i * kKeys;
+    const uint32_t ts0 = tmem + lanes + C::COL_S + i * C::SB * kKeys;
     const uint32_t to = tmem + lanes + C::COL_O + i * D;
     const uint32_t tq = tmem + lanes + C::COL_Q + i * (D / 2);
     const int t = live ? r / p.G : 0;
@@ -457,6 +470,16 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
       }
 #pragma unroll
       for (int h = 0; h < D / 64; ++h) {
+        if constexpr (C::Q_SMEM) {  // straight to its place, swizzled as K
+          uint8_t* const at = smem + C::STAGES * C::STAGE + ((i * 2 + h) * 128 + (warp & 3) * 32) * 128;
+#pragma unroll
+          for (int it = 0; it < 8; ++it) {
+            const int rr = it * 4 + (lane >> 3);
+            if (row0 + rr >= live_rows) x[h][it] = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4*>(at + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4)) = x[h][it];
+          }
+          continue;
+        }
 #pragma unroll
         for (int it = 0; it < 8; ++it) {
           const int rr = it * 4 + (lane >> 3);
@@ -480,7 +503,8 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
         tc::st32(tq + h * 32, w);
         __syncwarp();
       }
-      tc::wait_st();
+      if constexpr (C::Q_SMEM) tc::fence_async_shared();
+      else tc::wait_st();
       tc::fence_before();
       tc::mbar_arrive(q_full(i));
     }
@@ -489,9 +513,10 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
 #pragma unroll 1
     for (int n = 0; going && n < mine; ++n) {
       const int j = C::DUAL ? 2 * n + i : n, st = j % C::STAGES;
+      const uint32_t ts = ts0 + buf(n) * kKeys;
       // (S follows the stage's arrival, so its key masks are there too; they
       // stay until P is handed over)
-      going = __all_sync(0xffffffffu, tc::mbar_wait(s_full(i), n & 1, stop));
+      going = __all_sync(0xffffffffu, tc::mbar_wait(s_full(i, n), phase(n), stop));
       if (!going) break;
       tc::fence_after();
       if (any_live) {
@@ -536,6 +561,9 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
           const float alpha = moves ? ex2(m - mn) : 1.f;
           m = mn;
           l *= alpha;
+          // (with one S, its arrival says that the products before are done)
+          if (C::SB == 2 && n) going = __all_sync(0xffffffffu, tc::mbar_wait(o_step(i), (n - 1) & 1, stop));
+          if (C::SB == 2) tc::fence_after();
           if (n) {
 #pragma unroll 1
             for (int h = 0; h < D / 16; ++h) {  // rare: few registers
@@ -569,18 +597,18 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
             tc::wait_st();
             tc::fence_before();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(p_half(i));
+            if (lane == 0) tc::mbar_arrive(p_half(i, n));
           }
         }
         tc::wait_st();
         sum[0] = tc::add2(sum[0], sum[1]);
         l += sum[0].x + sum[0].y;
       } else if (lane == 0) {
-        tc::mbar_arrive(p_half(i));
+        tc::mbar_arrive(p_half(i, n));
       }
       tc::fence_before();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(p_full(i));
+      if (lane == 0) tc::mbar_arrive(p_full(i, n));
     }
     // both tiles' (streams') products are done with the stages
     for (int k = 0; k < nq && going; ++k)
@@ -917,17 +945,22 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
     constexpr uint32_t hi = tc::desc_hi(1024);
     const uint32_t k_lo = tc::desc_lo(data, 16);
     const uint32_t v_lo = tc::desc_lo(data + C::V_AT, kKeys * 128);
-    const uint32_t d_s = t0 + C::COL_S + i * kKeys, d_o = t0 + C::COL_O + i * D, a_q = t0 + C::COL_Q + i * (D / 2);
-    auto qk = [&](int st) {
+    const uint32_t s0 = t0 + C::COL_S + i * C::SB * kKeys, d_o = t0 + C::COL_O + i * D, a_q = t0 + C::COL_Q + i * (D / 2);
+    const uint32_t q_lo = tc::desc_lo(data + C::STAGES * C::STAGE + i * (128 * D * 2), 16);  // (Q_SMEM)
+    auto qk = [&](int st, int at) {  // the at-th step's scores
+      const uint32_t d_s = s0 + buf(at) * kKeys;
       const uint32_t kd = k_lo + st * (C::K_STEP / 16);
       // hi, then lo: the tiles follow one another in 64-channel blocks
 #pragma unroll
       for (int n = 0; n < (C::LO ? 2 : 1) * (D / 64); ++n)
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          tc::mma_ts(d_s, a_q + ((n * 4) & (D / 16 - 1)) * 8 + kk * 8, kd + n * (kKeys * 128 / 16) + kk * 2, hi, id_qk,
-                     n || kk);
-      tc::commit(s_full(i));
+          if constexpr (C::Q_SMEM)
+            tc::mma_ss(d_s, q_lo + n * (128 * 128 / 16) + kk * 2, kd + n * (kKeys * 128 / 16) + kk * 2, hi, id_qk, n || kk);
+          else
+            tc::mma_ts(d_s, a_q + ((n * 4) & (D / 16 - 1)) * 8 + kk * 8, kd + n * (kKeys * 128 / 16) + kk * 2, hi, id_qk,
+                       n || kk);
+      tc::commit(s_full(i, at));
       if (C::LO) tc::commit(empty(0, st));
     };
     auto wait = [&](uint32_t bar, int parity) { return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, stop)); };
@@ -940,17 +973,25 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
     const int j0 = C::DUAL ? i : 0;  // this stream's first key tile
     if (i < nq && j0 < tiles && wait(full(0, j0), 0) && wait(q_full(i), 0) && (C::DUAL || i == 0 || wait(turn(1), 0))) {
       tc::fence_after();
-      qk(j0);
+      qk(j0, 0);
+      bool ahead = C::SB == 2 && 1 < tiles;  // the second S filled too
+      if (ahead) ahead = wait(full(0, 1), 0);
+      if (ahead) {
+        tc::fence_after();
+        qk(1, 1);
+      }
       pass();
       int st = j0, tp = i;  // stage of key tile j; phase of the turn
 #pragma unroll 1
       for (int j = j0, n = 0;; j += STEP, ++n) {
-        const int next = j + STEP;
-        const bool more = next < tiles;
+        const int next = j + C::SB * STEP;  // the tile whose scores follow
+        const bool more = next < tiles, last_one = j + STEP >= tiles;
         const int st1 = next % C::STAGES;
+        const uint32_t d_s = s0 + buf(n) * kKeys;
+        if (C::SB == 2 && !last_one && n == 0 && !ahead) break;
         if (!C::DUAL && more && !wait(full(0, st1), (next / C::STAGES) & 1)) break;
         if (C::LO && !wait(full(1, st), (j / C::STAGES) & 1)) break;
-        if (!wait(p_half(i), n & 1)) break;
+        if (!wait(p_half(i, n), phase(n))) break;
         if (!C::DUAL && nq == 2 && !wait(turn(i), tp)) break;
         tp ^= 1;
         tc::fence_after();
@@ -965,19 +1006,20 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
             }
         };
         pv(0);
-        if (!wait(p_full(i), n & 1)) break;
+        if (!wait(p_full(i, n), phase(n))) break;
         tc::fence_after();
         pv(1);
-        if (!more) {
+        if (C::SB == 2) tc::commit(o_step(i));
+        if (last_one) {
           tc::commit(o_full(i));
           pass();
           break;
         }
         tc::commit(empty(1, st));
         if (C::DUAL && !wait(full(0, st1), (next / C::STAGES) & 1)) break;
-        qk(st1);
+        if (more) qk(st1, n + C::SB);
         pass();
-        st = st1;
+        st = (j + STEP) % C::STAGES;
       }
     }
   }

@@ -162,6 +162,16 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, ui
       "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"((uint32_t)acc)
       : "memory");
 }
+// The same with A in shared memory (its descriptor's low word; the high word
+// is B's).
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t ab_hi, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n.reg .pred p, e;\n.reg .b64 a, b;\nmov.b64 a, {%1, %3};\nmov.b64 b, {%2, %3};\nsetp.ne.u32 p, %5, 0;\n"
+      "elect.sync _|e, 0xffffffff;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n}\n" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(ab_hi), "r"(idesc), "r"((uint32_t)acc)
+      : "memory");
+}
 // all MMAs issued so far by the elected lane arrive on the barrier when done
 __device__ __forceinline__ void commit(uint32_t bar) {
   asm volatile(
