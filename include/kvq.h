@@ -464,10 +464,10 @@ KVQ_API size_t kvq_extend_workspace_size(const kvq_cache_desc* desc, int32_t bat
  *   max_seq_len      host upper bound on seq_lens_before[b] + new_lens[b]
  *   out              device fp16 like q; may not overlap it
  * num_splits, softmax_scale and workspace as for kvq_decode_attn, but any
- * number of query heads per KV head.  Scores and softmax in fp32; K enters the
- * products as x_hat = (q - z) s to 22 bits (two fp16 numbers), V as the fp16
- * values that kvq_cache_read returns, the probabilities as fp16 (11 bits down
- * to 2^-21 of the row's largest).  An infinity or NaN in a token's V row makes
+ * number of query heads per KV head.  Scores and softmax in fp32; K and V
+ * enter the products as x_hat = (q - z) s to 22 bits (two fp16 numbers, held at
+ * fp16's largest), the probabilities as fp16 (11 bits down to 2^-21 of the
+ * row's largest).  An infinity or NaN in a token's V row makes
  * NaN or infinities of the rows that see the token, possibly in more channels
  * than its own; rows that do not see it are untouched.  A sequence whose
  * length exceeds min(max_seq_len, cache capacity) flags KVQ_FLAG_SEQ_LEN and

@@ -23,14 +23,14 @@
 // they copy rows).  One tile's (or stream's) softmax runs under the other's
 // products.
 //
-// What bounds it.  256 rows: the chain scores - softmax - weighted V of a tile,
-// about 3000 cycles a 64-key step of which the products take 2048 (K and V each
-// in two parts; fp16 caches 1024 of 2400): INT4, 4096 tokens after 12288, 32 / 8
-// heads, 1.14 ms, 848 TFLOP/s of the formula's; fp16 1.00 ms, 963.  S of the
-// next step cannot be computed ahead: S, O and q of two tiles fill tensor
-// memory.  At most 128 rows: the conversion, about 1300 of 1900 cycles a step,
-// bound by its own latency with two warps a scheduler: 17 tokens over 32768
-// (INT8) 46 us.
+// What bounds it.  256 rows of 128 channels over codes: the tensor core, 2048
+// cycles a 64-key step of about 2600 (K and V each in two parts): INT4, 4096
+// tokens after 12288, 32 / 8 heads, 1.05 ms, 914 TFLOP/s of the formula's.  Over
+// fp16: the softmax, about 2000 cycles a step (512 of them a warp's exponentials
+// alone, and two warps share a scheduler's unit) where the products take 1280:
+// 0.88 ms, 1098 TFLOP/s.  At most 128 rows: the conversion, about 1300 of 1900
+// cycles a step, bound by its own latency with two warps a scheduler: 17 tokens
+// over 32768 (INT8) 46 us.
 //
 // Precision.  q - z is a whole number (exact in fp16 up to 2048) and s has
 // 11 bits, so x_hat = (q - z) s has up to 23: K and V enter as sums of two fp16
@@ -51,7 +51,10 @@
 // Order of the MMAs.  One lane issues PV(j) and then QK(j + 1) of a tile,
 // and MMAs run in the order issued: S may be overwritten as soon as QK(j + 1)
 // is issued, and when its completion is seen PV(j) is complete too, so the
-// softmax may rescale O until it hands over P(j + 1).
+// softmax may rescale O until it hands over P(j + 1).  PV(j) starts with the
+// first 32 keys' P (late chunk below: 1.14 -> 1.05 ms, fp16 1.00 -> 0.90).
+// Where tensor memory holds two S per tile (SB), QK(j + 2) follows PV(j)
+// instead, and a rescale waits for PV(j - 1) by itself.
 #pragma once
 
 #include "kvq_decode_fast.cuh"
@@ -114,6 +117,10 @@ struct Cfg {
   // at 128 with q in shared memory, which only fp16 caches leave the room for.
   static constexpr bool Q_SMEM = !LO && D == 128 && !DUAL;
   static constexpr int SB = !DUAL && (D == 64 || Q_SMEM) ? 2 : 1;
+  // Whether the tiles' MMA warps take turns: with one S per tile, which keeps
+  // the tiles a softmax apart; with two they only wait for one another (fp16
+  // 0.89 -> 0.88 ms, prompts of 2048 219 -> 211 us without).
+  static constexpr bool TURNS = !DUAL && SB == 1;
   // tensor memory columns: per tile S (64 each, P in its place), O (D), Q (D / 2)
   static constexpr uint32_t COL_S = 0, COL_O = 2 * SB * kKeys, COL_Q = COL_O + 2 * D, COLS = 512;
   static constexpr int Q_BYTES = Q_SMEM ? 2 * 128 * D * 2 : 0;  // behind the ring, on a 1024-byte boundary
@@ -470,38 +477,34 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
       }
 #pragma unroll
       for (int h = 0; h < D / 64; ++h) {
-        if constexpr (C::Q_SMEM) {  // straight to its place, swizzled as K
-          uint8_t* const at = smem + C::STAGES * C::STAGE + ((i * 2 + h) * 128 + (warp & 3) * 32) * 128;
-#pragma unroll
-          for (int it = 0; it < 8; ++it) {
-            const int rr = it * 4 + (lane >> 3);
-            if (row0 + rr >= live_rows) x[h][it] = make_uint4(0u, 0u, 0u, 0u);
-            *reinterpret_cast<uint4*>(at + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4)) = x[h][it];
-          }
-          continue;
-        }
+        // in shared memory for good (Q_SMEM, swizzled as K), or on its way
+        uint8_t* const at = C::Q_SMEM
+                                ? smem + C::STAGES * C::STAGE + ((i * 2 + h) * 128 + (warp & 3) * 32) * 128
+                                : scratch;
 #pragma unroll
         for (int it = 0; it < 8; ++it) {
           const int rr = it * 4 + (lane >> 3);
           if (row0 + rr >= live_rows) x[h][it] = make_uint4(0u, 0u, 0u, 0u);
-          *reinterpret_cast<uint4*>(scratch + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4)) = x[h][it];
+          *reinterpret_cast<uint4*>(at + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4)) = x[h][it];
         }
-        __syncwarp();
-        uint32_t w[32];
+        if constexpr (!C::Q_SMEM) {
+          __syncwarp();
+          uint32_t w[32];
 #pragma unroll
-        for (int ch = 0; ch < 8; ++ch) {
-          const uint4 y = *reinterpret_cast<const uint4*>(scratch + lane * 128 + ((ch ^ (lane & 7)) << 4));
-          if constexpr (C::PAIRED) {  // (0, 4), (1, 5), (2, 6), (3, 7)
-            w[4 * ch] = fast::prmt_b32(y.x, y.z, 0x5410u);
-            w[4 * ch + 1] = fast::prmt_b32(y.x, y.z, 0x7632u);
-            w[4 * ch + 2] = fast::prmt_b32(y.y, y.w, 0x5410u);
-            w[4 * ch + 3] = fast::prmt_b32(y.y, y.w, 0x7632u);
-          } else {
-            w[4 * ch] = y.x, w[4 * ch + 1] = y.y, w[4 * ch + 2] = y.z, w[4 * ch + 3] = y.w;
+          for (int ch = 0; ch < 8; ++ch) {
+            const uint4 y = *reinterpret_cast<const uint4*>(scratch + lane * 128 + ((ch ^ (lane & 7)) << 4));
+            if constexpr (C::PAIRED) {  // (0, 4), (1, 5), (2, 6), (3, 7)
+              w[4 * ch] = fast::prmt_b32(y.x, y.z, 0x5410u);
+              w[4 * ch + 1] = fast::prmt_b32(y.x, y.z, 0x7632u);
+              w[4 * ch + 2] = fast::prmt_b32(y.y, y.w, 0x5410u);
+              w[4 * ch + 3] = fast::prmt_b32(y.y, y.w, 0x7632u);
+            } else {
+              w[4 * ch] = y.x, w[4 * ch + 1] = y.y, w[4 * ch + 2] = y.z, w[4 * ch + 3] = y.w;
+            }
           }
+          tc::st32(tq + h * 32, w);
+          __syncwarp();
         }
-        tc::st32(tq + h * 32, w);
-        __syncwarp();
       }
       if constexpr (C::Q_SMEM) tc::fence_async_shared();
       else tc::wait_st();
@@ -964,14 +967,14 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
       if (C::LO) tc::commit(empty(0, st));
     };
     auto wait = [&](uint32_t bar, int parity) { return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, stop)); };
-    // the warps take turns, so that one tile's softmax runs under the other
-    // tile's products and not beside its softmax
+    // the warps take turns (TURNS), so that one tile's softmax runs under the
+    // other tile's products and not beside its softmax
     auto pass = [&] {
-      if (!C::DUAL && nq == 2 && lane == 0) tc::mbar_arrive(turn(1 - i));
+      if (C::TURNS && nq == 2 && lane == 0) tc::mbar_arrive(turn(1 - i));
       __syncwarp();
     };
     const int j0 = C::DUAL ? i : 0;  // this stream's first key tile
-    if (i < nq && j0 < tiles && wait(full(0, j0), 0) && wait(q_full(i), 0) && (C::DUAL || i == 0 || wait(turn(1), 0))) {
+    if (i < nq && j0 < tiles && wait(full(0, j0), 0) && wait(q_full(i), 0) && (!C::TURNS || i == 0 || wait(turn(1), 0))) {
       tc::fence_after();
       qk(j0, 0);
       bool ahead = C::SB == 2 && 1 < tiles;  // the second S filled too
@@ -992,7 +995,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
         if (!C::DUAL && more && !wait(full(0, st1), (next / C::STAGES) & 1)) break;
         if (C::LO && !wait(full(1, st), (j / C::STAGES) & 1)) break;
         if (!wait(p_half(i, n), phase(n))) break;
-        if (!C::DUAL && nq == 2 && !wait(turn(i), tp)) break;
+        if (C::TURNS && nq == 2 && !wait(turn(i), tp)) break;
         tp ^= 1;
         tc::fence_after();
         const uint32_t vd = v_lo + st * (C::V_STEP / 16);
