@@ -73,8 +73,8 @@ def read_rows(cache, lens, most):
     return [o.cpu().numpy() for o in out]
 
 
-def extend_bound(q, k, mass, out, scale):
-    """How far an output may be from the formula's on the same fp16 K and V.
+def extend_bound(q, k, mass, out, scale, rounded=False):
+    """How far an output may be from the formula's on the dequantized K and V.
 
     Per score: D products accumulated in fp32, error at most D 2^-24 of the
     sum of magnitudes S = sum |q_d k_d| (taken over the largest row of K and
@@ -82,14 +82,21 @@ def extend_bound(q, k, mass, out, scale):
     the exponentials and their reference.  Each probability is rounded to
     fp16: half a step is 2^-11 relative, or 2^-25 absolute below 2^-14.  The
     weighted sum and the sum of probabilities accumulate L terms in fp32, the
-    output is rounded to fp16 once more."""
+    output is rounded to fp16 once more.  K and V enter with 22 bits: 2^-22 of
+    S in a score, like four more of the D roundings, and of the mass.
+
+    rounded: k and v are what kvq_cache_read returns, each a rounding to fp16
+    (2^-11) from what the call uses: in V directly, in K by 2^-11 S a score,
+    felt in a weight and in the sum of weights."""
     D, L = q.shape[-1], k.shape[1]
     S = float((np.abs(q).max(axis=(0, 1)) * np.abs(k).max(axis=(0, 1))).sum())
-    rel = 2.0 ** -11 + 2 * 1.5 * scale * D * 2.0 ** -24 * S + 2.0 ** -19 + 2 * L * 2.0 ** -24
+    rel = 2.0 ** -11 + 2 * 1.5 * scale * (D + 4) * 2.0 ** -24 * S + 2.0 ** -19 + 2 * L * 2.0 ** -24
+    if rounded:
+        rel += 2.0 ** -11 + 2 * scale * 2.0 ** -11 * S
     return mass * rel + 2.0 ** -11 * np.abs(out) + L * 2.0 ** -25 * 8.0 + 2.0 ** -24
 
 
-def check_extend(got, q, k16, v16, before, n, scale, mapped=None):
+def check_extend(got, q, k16, v16, before, n, scale, mapped=None, rounded=False):
     """One sequence: got [n][Hq][D] against the oracle on K / V [L][Hkv][D]."""
     L = before + n
     k = k16[:L].astype(np.float64).transpose(1, 0, 2)
@@ -97,7 +104,7 @@ def check_extend(got, q, k16, v16, before, n, scale, mapped=None):
     q = q[:n].astype(np.float64)
     want, mass = P.extend_attention(q, k, v, before, scale, mapped)
     assert np.abs(v).max(initial=0) <= 8.0  # extend_bound's last term
-    bound = extend_bound(q, k, mass, want, scale)
+    bound = extend_bound(q, k, mass, want, scale, rounded)
     off = np.abs(got[:n].astype(np.float64) - want)
     assert np.isfinite(got[:n]).all()
     worst = (off / bound).max()

@@ -1,6 +1,6 @@
-"""GPU tests of kvq_extend_attn against the fp64 oracle on the cache's own
-rows (read back through kvq_cache_read, itself tested bit for bit), with the
-error bound of tests/_prompt.py; refusals and flags; splits, streams, graphs; and equality with the decode call for one new token."""
+"""GPU tests of kvq_extend_attn against the fp64 oracle on the rows that the
+cache holds, dequantized in fp64 (axis-aware caches: read back through
+kvq_cache_read, rounded to fp16), with the error bound of tests/_prompt.py; refusals and flags; splits, streams, graphs; and equality with the decode call for one new token."""
 import numpy as np
 import pytest
 
@@ -20,6 +20,7 @@ def _fill(K, cache, rng, lens, Hkv, D, most):
     v = rng.standard_normal((B, most, Hkv, D)).astype(np.float16)
     z = torch.zeros(B, dtype=torch.int32, device="cuda")
     K.kvq_append(cache, torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda(), z)
+    return k, v
 
 
 def _case(fmt, D, Hq, Hkv, T, before, new=None, page=0, splits=0, seed=0, scale=0.0, extra=2):
@@ -41,8 +42,8 @@ def _case(fmt, D, Hq, Hkv, T, before, new=None, page=0, splits=0, seed=0, scale=
         K.kvq_append(cache, torch.from_numpy(k[:, :lens[0]].copy()).cuda(),
                      torch.from_numpy(v[:, :lens[0]].copy()).cuda(), torch.from_numpy(at).cuda())
     else:
-        _fill(K, cache, rng, lens, Hkv, D, most)
-    k16, v16 = read_rows(cache, lens, most)
+        k, v = _fill(K, cache, rng, lens, Hkv, D, most)
+    kx, vx = read_rows(cache, lens, most) if kch else (expected_rows(fmt, k), expected_rows(fmt, v))
     q = rng.standard_normal((B, T, Hq, D)).astype(np.float16)
     dev = "cuda"
     tq = torch.from_numpy(q).to(dev)
@@ -64,7 +65,7 @@ def _case(fmt, D, Hq, Hkv, T, before, new=None, page=0, splits=0, seed=0, scale=
         for b in range(B):
             assert (got[b, new[b]:] == 9).all(), "rows behind the sequence"
             if new[b]:
-                check_extend(got[b], q[b], k16[b], v16[b], before[b], new[b], scale or D ** -0.5)
+                check_extend(got[b], q[b], kx[b], vx[b], before[b], new[b], scale or D ** -0.5, rounded=kch)
     return got
 
 
@@ -158,7 +159,7 @@ def test_flags_and_left_out_tokens():
         got = out.cpu().numpy()
         mapped = np.ones(25, dtype=bool)
         mapped[8:16] = False
-        check_extend(got[0], q[0], k16[0], v16[0], 20, T, D ** -0.5, mapped)
+        check_extend(got[0], q[0], k16[0], v16[0], 20, T, D ** -0.5, mapped, rounded=True)
         assert (got[1:] == 0).all()         # too long, negative, nothing mapped: zero rows
     # an unusable new_lens: that sequence is skipped
     out.fill_(9)
@@ -169,7 +170,7 @@ def test_flags_and_left_out_tokens():
     got = out.cpu().numpy()
     assert int(st.item()) & K._lib.KVQ_FLAG_SEQ_LEN
     assert (got[0] == 9).all() and (got[1] == 9).all() and (got[2, 1:] == 9).all() and (got[3] == 9).all()
-    check_extend(got[2], q[2], k16[2], v16[2], 0, 1, D ** -0.5)
+    check_extend(got[2], q[2], k16[2], v16[2], 0, 1, D ** -0.5, rounded=True)
 
 
 @pytest.mark.parametrize("T", [3, 200])
@@ -193,7 +194,7 @@ def test_rows_behind_the_sequence_do_not_count(fmt, value, T):
     q = rng.standard_normal((1, T, 4, D)).astype(np.float16)
     got = K.kvq_extend_attn(cache, torch.from_numpy(q).cuda(), torch.tensor([150], dtype=torch.int32, device="cuda"),
                             L + 100).cpu().numpy()
-    check_extend(got[0], q[0], k16[0], v16[0], 150, T, D ** -0.5)
+    check_extend(got[0], q[0], k16[0], v16[0], 150, T, D ** -0.5, rounded=True)
 
 
 @pytest.mark.parametrize("value", [float("nan"), float("inf")])
@@ -214,7 +215,7 @@ def test_a_later_token_does_not_reach_earlier_ones(T, D, value):
     q = rng.standard_normal((1, T, 4, D)).astype(np.float16)
     got = K.kvq_extend_attn(cache, torch.from_numpy(q).cuda(), torch.tensor([before], dtype=torch.int32, device="cuda"),
                             L).cpu().numpy()
-    check_extend(got[0], q[0], k16[0], v16[0], before, at, D ** -0.5)
+    check_extend(got[0], q[0], k16[0], v16[0], before, at, D ** -0.5, rounded=True)
     assert not np.isfinite(got[0, at:]).all(axis=-1).any()
 
 
@@ -239,7 +240,7 @@ def test_header_arrays_of_any_alignment(fmt, g_is_D, extra):
         got = K.kvq_extend_attn(cache, torch.from_numpy(q).cuda(), torch.tensor(before, dtype=torch.int32, device="cuda"),
                                 L, num_splits=splits).cpu().numpy()
         for b in range(B):
-            check_extend(got[b], q[b], k16[b], v16[b], before[b], T, D ** -0.5)
+            check_extend(got[b], q[b], k16[b], v16[b], before[b], T, D ** -0.5, rounded=True)
 
 
 def test_far_zero_points_and_large_scales():
@@ -260,7 +261,7 @@ def test_far_zero_points_and_large_scales():
     q = rng.standard_normal((1, T, 2, D)).astype(np.float16)
     b = torch.tensor([L - T], dtype=torch.int32, device="cuda")
     got = K.kvq_extend_attn(cache, torch.from_numpy(q).cuda(), b, L).cpu().numpy()
-    check_extend(got[0], q[0], k16[0], v16[0], L - T, T, D ** -0.5)
+    check_extend(got[0], q[0], k16[0], v16[0], L - T, T, D ** -0.5, rounded=True)
     # one key at the end of fp16's range, all others small: scores stay finite
     k[0, 5, 0, :] = np.linspace(0, 65504, D).astype(np.float16)  # code 255 decodes to 65535
     K.kvq_append(cache, torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda(), z)
@@ -269,7 +270,7 @@ def test_far_zero_points_and_large_scales():
     k16, v16 = read_rows(cache, [L], L)
     assert np.abs(k16[0, 5].astype(np.float64)).max() == 65504
     got = K.kvq_extend_attn(cache, torch.from_numpy(q).cuda(), b, L, softmax_scale=0.01).cpu().numpy()
-    check_extend(got[0], q[0], k16[0], v16[0], L - T, T, 0.01)
+    check_extend(got[0], q[0], k16[0], v16[0], L - T, T, 0.01, rounded=True)
 
 
 def test_large_scores_keep_the_softmax_exact():

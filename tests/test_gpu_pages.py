@@ -287,7 +287,7 @@ def test_a_served_run_of_all_calls():
                 hist[layer][b] = kept + [(k16[b, i], v16[b, i]) for i in range(lens[b], total[b])]
                 if new[b]:
                     check_extend(out[b].cpu().numpy(), q[b].cpu().numpy(), k16[b], v16[b], int(lens[b]),
-                                 int(new[b]), D ** -0.5)
+                                 int(new[b]), D ** -0.5, rounded=True)
         assert int(st.item()) == 0
         lens[:] = lens + new
 
