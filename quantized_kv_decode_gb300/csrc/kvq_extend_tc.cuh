@@ -528,13 +528,18 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
         tc::ld32(ts + 32, u[1]);
         const int ks = k0 + j * kKeys;
         const uint32_t ok0 = sh.ok[j % (2 * C::STAGES)][0], ok1 = sh.ok[j % (2 * C::STAGES)][1];
-        const bool whole = __all_sync(0xffffffffu, (ok0 & ok1) == 0xFFFFFFFFu && ks + kKeys - 1 <= last);
+        // (a tile that the block's first row sees in part may hold V rows set to
+        // zero, which count for every row that sees them)
+        const bool checked = KIND == 2 && ks + kKeys - 1 > all_see;
+        const bool spoilt = checked && reinterpret_cast<const unsigned short*>(sh.bad[st])[lane];
+        const bool whole =
+            __all_sync(0xffffffffu, (ok0 & ok1) == 0xFFFFFFFFu && ks + kKeys - 1 <= last && !spoilt);
         tc::wait_ld();
         if (!whole) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t bad = 0;
-            if (KIND == 2 && ks + kKeys - 1 > all_see) {  // (checked in these tiles alone)
+            if (checked) {
 #pragma unroll
               for (int g = 0; g < 8; ++g) {
                 const uint32_t v = reinterpret_cast<const uint32_t*>(sh.bad[st])[h * 8 + g];
