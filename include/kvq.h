@@ -668,6 +668,33 @@ typedef enum {
  */
 KVQ_API kvq_status kvq_debug_shrink_extent(int32_t array, int64_t bytes);
 
+/* The waits of kvq_extend_attn's tensor-core kernel (head_dim 64 and 128,
+ * per-token formats), by the warp that waits, named for kvq_debug_fail_wait. */
+typedef enum {
+  KVQ_WAIT_NONE = 0,
+  KVQ_WAIT_SOFTMAX = 1,     /* a softmax warp for a key tile's scores           */
+  KVQ_WAIT_K = 2,           /* a warp that turns K codes into fp16 (fp16 caches:
+                               that copies rows)                                */
+  KVQ_WAIT_V = 3,           /* the same for V (fp16 caches: never)              */
+  KVQ_WAIT_LOAD_K = 4,      /* the warp that copies K codes (fp16 caches: that
+                               passes stages on)                                */
+  KVQ_WAIT_LOAD_V = 5,      /* the same for V (fp16 caches: never)              */
+  KVQ_WAIT_SCORES = 6,      /* the first warp that issues products, for K       */
+  KVQ_WAIT_SUM = 7,         /* the same, between the halves of a weighted sum   */
+  KVQ_WAIT_COUNT = 8
+} kvq_debug_wait;
+
+/*
+ * Tests what happens when a wait runs out (debug builds only; a release build
+ * returns KVQ_ERR_UNSUPPORTED).  In every later launch of that kernel the wait
+ * `wait` (a kvq_debug_wait) for key tile `tile` of a thread block's share
+ * counts as run out at once: the block gives up, waits for its copies and
+ * products in flight, writes no more output and sets KVQ_FLAG_TIMEOUT.
+ * KVQ_WAIT_NONE ends that.  Process-wide host state, as above.  Returns
+ * KVQ_ERR_INVALID_ARG for an unknown wait or tile < 0.
+ */
+KVQ_API kvq_status kvq_debug_fail_wait(int32_t wait, int32_t tile);
+
 /* Static, human-readable name of a status code. */
 KVQ_API const char* kvq_status_string(kvq_status status);
 

@@ -36,6 +36,10 @@ ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "bands": 3, "yarn": 4}
 KVQ_ROPE_MAX_PAIRS = 128
 KVQ_MAX_POOL_BATCH = 16384
 
+# kvq_debug_wait: the waits a debug build can let run out
+(KVQ_WAIT_NONE, KVQ_WAIT_SOFTMAX, KVQ_WAIT_K, KVQ_WAIT_V, KVQ_WAIT_LOAD_K, KVQ_WAIT_LOAD_V,
+ KVQ_WAIT_SCORES, KVQ_WAIT_SUM, KVQ_WAIT_COUNT) = range(9)
+
 # kvq_array: the caller arrays a debug build checks
 (KVQ_ARRAY_K_CODES, KVQ_ARRAY_V_CODES, KVQ_ARRAY_K_SCALE, KVQ_ARRAY_K_ZERO, KVQ_ARRAY_V_SCALE,
  KVQ_ARRAY_V_ZERO, KVQ_ARRAY_K_WINDOW, KVQ_ARRAY_V_WINDOW, KVQ_ARRAY_BLOCK_TABLE, KVQ_ARRAY_Q,
@@ -168,6 +172,7 @@ SIGNATURES = {
                                  c_void_p, c_int32, c_void_p, c_void_p]),
     "kvq_debug_checks": (c_int32, []),
     "kvq_debug_shrink_extent": (c_int32, [c_int32, c_int64]),
+    "kvq_debug_fail_wait": (c_int32, [c_int32, c_int32]),
     "kvq_status_string": (ctypes.c_char_p, [c_int32]),
 }
 

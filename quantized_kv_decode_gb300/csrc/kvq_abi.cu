@@ -283,6 +283,8 @@ kvq_status make_plan(const kvq_cache_desc* desc, const CacheGeom& geom, int32_t 
 #ifdef KVQ_DEBUG
 // Bytes kvq_debug_shrink_extent takes off each array's extent.
 int64_t g_dbg_shrink[KVQ_ARRAY_COUNT] = {};
+// The wait that kvq_debug_fail_wait lets run out, and its key tile.
+int32_t g_dbg_fail_wait = KVQ_WAIT_NONE, g_dbg_fail_tile = 0;
 
 void dbg_set(DbgExtents& x, int a, const void* base, size_t bytes) {
   const unsigned long long lo = (unsigned long long)reinterpret_cast<uintptr_t>(base);
@@ -323,6 +325,8 @@ void dbg_fill(CacheGeom& g, const kvq_cache_desc* desc, const kvq_cache* cache, 
   dbg_set(x, KVQ_ARRAY_SEQ_LENS, lens, (size_t)batch * 4);
   dbg_set(x, KVQ_ARRAY_WORKSPACE, ws, ws_bytes);
   x.status = status;
+  x.fail_wait = g_dbg_fail_wait;
+  x.fail_tile = g_dbg_fail_tile;
 #else
   (void)g, (void)desc, (void)cache, (void)batch, (void)num_q_heads, (void)num_new, (void)q;
   (void)k_new, (void)v_new, (void)lens, (void)out, (void)ws, (void)ws_bytes, (void)status;
@@ -627,6 +631,18 @@ kvq_status kvq_debug_shrink_extent(int32_t array, int64_t bytes) {
   return KVQ_OK;
 #else
   (void)array, (void)bytes;
+  return KVQ_ERR_UNSUPPORTED;
+#endif
+}
+
+kvq_status kvq_debug_fail_wait(int32_t wait, int32_t tile) {
+#ifdef KVQ_DEBUG
+  if (wait < 0 || wait >= KVQ_WAIT_COUNT || tile < 0) return KVQ_ERR_INVALID_ARG;
+  g_dbg_fail_wait = wait;
+  g_dbg_fail_tile = tile;
+  return KVQ_OK;
+#else
+  (void)wait, (void)tile;
   return KVQ_ERR_UNSUPPORTED;
 #endif
 }

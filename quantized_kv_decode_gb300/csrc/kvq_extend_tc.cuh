@@ -143,6 +143,8 @@ struct Shared {
   uint32_t raw_ok[kMaxDepth][2];
   unsigned long long full[2][STAGES], empty[2][STAGES];  // K, V (fp16: full[0] and empty[1], both at once)
   unsigned long long q_full[2], s_full[4], p_half[4], p_full[4], o_full[2], o_step[2], turn[2], merge;  // s, p: [tile][S]
+  unsigned long long done[2];  // a tile's (stream's) products when its warp gives up
+  int loaded[2];               // key tiles whose K, V copies were issued
   float2 ml[128];           // the second stream's maximum and sum per row
   uint32_t ok[2 * STAGES][2];  // per key: mapped and before the end (a K tile is freed before the softmax has read these)
   alignas(4) uint8_t bad[STAGES][kKeys];  // per key: V held an infinity or NaN (set to zero)
@@ -390,7 +392,14 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
   auto turn = [&](int i) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, turn) + 8 * i; };
   const uint32_t merge = bars + (uint32_t)offsetof(Shared<C::STAGES>, merge);
   auto o_full = [&](int i) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, o_full) + 8 * i; };
+  auto done = [&](int i) { return bars + (uint32_t)offsetof(Shared<C::STAGES>, done) + 8 * i; };
   volatile int* stop = &sh.stop;
+  // (debug builds: a wait that is to run out)
+  auto runs_out = [&](int wait, int j) {
+    if (!KVQ_FAILS(c, wait, j)) return false;
+    *stop = 1;
+    return true;
+  };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2 * C::STAGES; ++s) {
@@ -411,6 +420,8 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
       tc::mbar_init(o_step(i), 1);
       tc::mbar_init(o_full(i), 1);
       tc::mbar_init(turn(i), 1);
+      tc::mbar_init(done(i), 1);
+      sh.loaded[i] = 0;
     }
     tc::mbar_init(merge, 4);
     sh.stop = 0;
@@ -519,7 +530,8 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
       const uint32_t ts = ts0 + buf(n) * kKeys;
       // (S follows the stage's arrival, so its key masks are there too; they
       // stay until P is handed over)
-      going = __all_sync(0xffffffffu, tc::mbar_wait(s_full(i, n), phase(n), stop));
+      going = __all_sync(0xffffffffu, !(warp == C::SOFT0 && runs_out(KVQ_WAIT_SOFTMAX, j)) &&
+                                           tc::mbar_wait(s_full(i, n), phase(n), stop));
       if (!going) break;
       tc::fence_after();
       if (any_live) {
@@ -723,7 +735,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
   } else if (warp >= C::PROD0) {
     // ------------------------------------------------------ producers
     const int tid = threadIdx.x - C::PROD0 * 32, pw = tid >> 5;
-    bool ok = true;  // after a wait that ran out the loops go on without waiting
+    bool ok = true;
     auto wait_q = [&] {  // before the stages are filled that q passes through
       for (int k = 0; k < nq; ++k)
         if (C::DUAL ? k < tiles : tiles > 0) ok = ok && tc::mbar_wait(q_full(k), 0, stop);
@@ -750,13 +762,15 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
         int st = 0, ph = 1, slot = 0, rph = 0;
 #pragma unroll 1
         for (int j = 0; j < tiles; ++j) {
-          if (ok) ok = tc::mbar_wait(raw_full(slot), rph, stop);
+          ok = !(pw == (is_v ? C::PROD / 2 : 0) && runs_out(is_v ? KVQ_WAIT_V : KVQ_WAIT_K, j)) &&
+               tc::mbar_wait(raw_full(slot), rph, stop);
           const uint8_t* ring = smem + C::STAGES * C::STAGE + slot * C::RAW;
           const uint32_t ok0 = sh.raw_ok[slot][0], ok1 = sh.raw_ok[slot][1];
           const bool all = (ok0 & ok1) == 0xFFFFFFFFu;
           if (ok) ok = tc::mbar_wait(empty(is_v, st), ph, stop);
           ok = __all_sync(0xffffffffu, ok);
-          if (is_v && j == C::Q_STAGE) wait_q();
+          if (ok && is_v && j == C::Q_STAGE) wait_q();
+          if (!ok) break;
           if (pw == 0 && lane == 0)
             sh.ok[j % (2 * C::STAGES)][0] = ok0, sh.ok[j % (2 * C::STAGES)][1] = ok1;
           uint8_t* const to = smem + (is_v ? C::V_AT + st * C::V_STEP : st * C::K_STEP);
@@ -791,9 +805,10 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
 #pragma unroll 1
       for (int j = 0; j < tiles; ++j) {
         const int st = j % C::STAGES;
-        if (ok) ok = tc::mbar_wait(empty(1, st), ((j / C::STAGES) & 1) ^ 1, stop);
-        ok = __all_sync(0xffffffffu, ok);
-        if (j == C::Q_STAGE) wait_q();
+        ok = __all_sync(0xffffffffu, !(pw == 0 && runs_out(KVQ_WAIT_K, j)) &&
+                                         tc::mbar_wait(empty(1, st), ((j / C::STAGES) & 1) ^ 1, stop));
+        if (ok && j == C::Q_STAGE) wait_q();
+        if (!ok) break;
         uint8_t* const stage = smem + st * C::STAGE;
         const uint32_t base = tc::smem_addr(stage) + (ch >> 3) * (kKeys * 128);
 #pragma unroll 4
@@ -876,7 +891,8 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
         const bool by_hand = !paged && row >= 0 && (row + rows) * hb + 15 > hdr_bytes;
         const uint32_t hdr = paged ? up * hb : (mis + rows * hb + (by_hand ? 0 : 15)) & ~15u;
         const uint32_t total = __reduce_add_sync(0xffffffffu, live ? up * RB + (zeros ? 2 : 1) * hdr : 0u);
-        ok = __all_sync(0xffffffffu, tc::mbar_wait(raw_empty(slot), ph, stop));
+        ok = __all_sync(0xffffffffu, !runs_out(which ? KVQ_WAIT_LOAD_V : KVQ_WAIT_LOAD_K, j) &&
+                                         tc::mbar_wait(raw_empty(slot), ph, stop));
         if (!ok) break;
         uint8_t* const at = smem + C::STAGES * C::STAGE + slot * C::RAW;
         uint8_t* const at_h = at + 2 * C::CODES + 2 * which * C::HDR;
@@ -926,9 +942,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
         }
         if (++slot == C::DEPTH) slot = 0, ph ^= 1;
       }
-      // after a wait that ran out: nothing in flight when the block ends
-      if (!ok)
-        for (int t = max(j - C::DEPTH, 0); t < j; ++t) tc::mbar_drain(raw_full(t % C::DEPTH), (t / C::DEPTH) & 1);
+      if (lane == 0) sh.loaded[which] = j;
     } else {
       // The rows of a stage have landed: make them visible to the tensor core
       // and pass the stage on.  (Not the producers' job: the fence would wait
@@ -936,7 +950,8 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
 #pragma unroll 1
       for (int j = 0; j < tiles && ok; ++j) {
         const int st = j % C::STAGES;
-        ok = __all_sync(0xffffffffu, tc::mbar_wait(raw_full(st), (j / C::STAGES) & 1, stop));
+        ok = __all_sync(0xffffffffu, !runs_out(KVQ_WAIT_LOAD_K, j) &&
+                                         tc::mbar_wait(raw_full(st), (j / C::STAGES) & 1, stop));
         tc::fence_async_shared();
         if (ok && lane == 0) tc::mbar_arrive(full(0, st));
         __syncwarp();
@@ -997,6 +1012,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
         const int st1 = next % C::STAGES;
         const uint32_t d_s = s0 + buf(n) * kKeys;
         if (C::SB == 2 && !last_one && n == 0 && !ahead) break;
+        if (i == 0 && more && runs_out(KVQ_WAIT_SCORES, next)) break;
         if (!C::DUAL && more && !wait(full(0, st1), (next / C::STAGES) & 1)) break;
         if (C::LO && !wait(full(1, st), (j / C::STAGES) & 1)) break;
         if (!wait(p_half(i, n), phase(n))) break;
@@ -1014,6 +1030,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
             }
         };
         pv(0);
+        if (i == 0 && runs_out(KVQ_WAIT_SUM, j)) break;
         if (!wait(p_full(i, n), phase(n))) break;
         tc::fence_after();
         pv(1);
@@ -1034,11 +1051,30 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
   __syncwarp();
   tc::fence_before();
   __syncthreads();
+  if (sh.stop) {
+    // Given up: no product may read shared or tensor memory, and no copy land,
+    // after the block has ended.  Copies of the last DEPTH tiles may be in
+    // flight (a tile before has been converted); where one loader got further
+    // than the other, the other's arrival is made up for.
+    if (warp == 0 || warp == 3) {
+      tc::commit(done(warp == 3));
+      tc::mbar_drain(done(warp == 3), 0);
+    }
+    if (C::LO && threadIdx.x == 32) {
+      const int most = max(sh.loaded[0], sh.loaded[1]), both = min(sh.loaded[0], sh.loaded[1]);
+      for (int t = max(most - C::SLOTS, 0); t < most; ++t) {
+        if (t >= both) tc::mbar_arrive(raw_full(t % C::SLOTS));
+        tc::mbar_drain(raw_full(t % C::SLOTS), (t / C::SLOTS) & 1);
+      }
+    }
+    if (threadIdx.x == 0 && p.status) atomicOr(p.status, KVQ_FLAG_TIMEOUT);
+    __syncwarp();
+    __syncthreads();
+  }
   if (warp == 0) {
     tc::fence_after();
     tc::tmem_dealloc(tmem, C::COLS);
   }
-  if (threadIdx.x == 0 && sh.stop && p.status) atomicOr(p.status, KVQ_FLAG_TIMEOUT);
 }
 
 template <int BITS, int KIND, int D, int NQ>

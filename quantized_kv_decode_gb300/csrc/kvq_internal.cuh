@@ -26,6 +26,7 @@ struct DbgExtents {
   unsigned long long lo[KVQ_ARRAY_COUNT];
   unsigned long long hi[KVQ_ARRAY_COUNT];
   uint32_t* status;
+  int32_t fail_wait, fail_tile;  // kvq_debug_fail_wait
 };
 
 // The kernels name K / V pairs and the prefetch regions by offset.
@@ -47,10 +48,13 @@ __device__ __forceinline__ bool dbg_in(const DbgExtents& x, int a, const void* p
 }
 // KVQ_IN(geometry, kvq_array, pointer, bytes): may the access go ahead?
 #define KVQ_IN(geo, a, ptr, n) (::kvq::dbg_in((geo).dbg, (a), (ptr), (n)))
+// KVQ_FAILS(geometry, kvq_debug_wait, key tile): is this wait to run out?
+#define KVQ_FAILS(geo, w, tile) ((geo).dbg.fail_wait == (w) && (geo).dbg.fail_tile == (tile))
 #else
 // (release: no check; the array id and pointer are only named, so that
 // variables kept for the check count as used)
 #define KVQ_IN(geo, a, ptr, n) ((void)(a), (void)(ptr), true)
+#define KVQ_FAILS(geo, w, tile) ((void)(w), (void)(tile), false)
 #endif
 
 // Geometry of one cache (K and V share it).
