@@ -560,7 +560,8 @@ KVQ_API kvq_status kvq_pages_compact(const kvq_page_pool* pool, int32_t* move_sr
  * arrays; pairs with a -1 are skipped).  No page may be the target of two
  * pairs, or source and target; then KVQ_FLAG_PAGE_LIST is set and the
  * contents of the targets concerned are unspecified.  An index outside the
- * pool flags KVQ_FLAG_BLOCK_TABLE and its pair is skipped.
+ * pool flags KVQ_FLAG_BLOCK_TABLE and its pair is skipped; skipped pairs do
+ * not count in the list.
  */
 KVQ_API kvq_status kvq_pages_copy(const kvq_cache_desc* desc, const kvq_cache* caches,
                           int32_t num_layers, const int32_t* copy_src, const int32_t* copy_dst,

@@ -484,7 +484,7 @@ kvq_status kvq_pages_copy(const kvq_cache_desc* desc, const kvq_cache* caches, i
   p.num_pairs = num_pairs;
   for (int32_t l0 = 0; l0 < num_layers; l0 += kCopyLayers) {
     p.layers = std::min(kCopyLayers, num_layers - l0);
-    p.report = l0 == 0;
+    p.report = l0 == 0 && dev_status != nullptr;
     for (int32_t l = 0; l < p.layers; ++l) {
       const kvq_cache& c = caches[l0 + l];
       void* const arrays[6] = {c.k_codes, c.v_codes, c.k_scale, c.k_zero, c.v_scale, c.v_zero};

@@ -344,6 +344,10 @@ __global__ void __launch_bounds__(kOne) compact_kernel(const __grid_constant__ P
 
 // Grid: x = pairs, y = layers.
 constexpr int kCopyThreads = 128, kCopyLoads = 8;
+constexpr int kListInline = 2048;  // pairs up to which the copying CTAs check the list
+__device__ __forceinline__ bool copied(const PageCopyParams& p, int s, int d) {
+  return s >= 0 && d >= 0 && s < p.num_pages && d < p.num_pages;
+}
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ PageCopyParams p) {
   pdl_launch_dependents();
   pdl_wait();
@@ -379,15 +383,63 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
     for (int u = 0; u < kCopyLoads; ++u)
       if (to[u]) *to[u] = v[u];
   }
-  if (report) {
+  if (report && p.num_pairs <= kListInline) {
     uint32_t flags = d == s ? KVQ_FLAG_PAGE_LIST : 0u;
     for (int j = threadIdx.x; j < p.num_pairs; j += blockDim.x) {
       if (j == i) continue;
       const int sj = __ldg(p.src + j), dj = __ldg(p.dst + j);
-      if (sj >= 0 && dj >= 0 && (sj == d || dj == d)) flags = KVQ_FLAG_PAGE_LIST;
+      if (copied(p, sj, dj) && (sj == d || dj == d)) flags = KVQ_FLAG_PAGE_LIST;
     }
     flag(p.status, flags);
   }
+}
+
+// The same check of a long list: a CTA per kListPages pages marks the targets
+// among them in a bitmap, then looks the sources up.  Sixteen pairs a thread
+// in flight: 500 000 pairs 90 us (each pair against every other, as in a
+// short list: 132 ms with 200 000 of them to copy).
+constexpr int kListThreads = 1024, kListPages = 1 << 20, kListLoads = 4;
+__global__ void __launch_bounds__(kListThreads) list_kernel(const __grid_constant__ PageCopyParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  extern __shared__ uint32_t targets[];  // a bit per page
+  const int first = blockIdx.x * kListPages;
+  const uint32_t pairs = (uint32_t)p.num_pairs;
+  for (int i = threadIdx.x; i < kListPages / 32; i += kListThreads) targets[i] = 0;
+  __syncthreads();
+  bool bad = false;
+  for (int look = 0; look < 2; ++look) {
+    for (uint32_t k0 = 4 * threadIdx.x; k0 < pairs; k0 += 4 * kListThreads * kListLoads) {
+      int4 s[kListLoads], d[kListLoads];
+#pragma unroll
+      for (int u = 0; u < kListLoads; ++u) {
+        const uint32_t k = k0 + 4 * kListThreads * u;
+        s[u] = d[u] = make_int4(-1, -1, -1, -1);
+        if (k + 4 <= pairs) {
+          s[u] = __ldg(reinterpret_cast<const int4*>(p.src + k));
+          d[u] = __ldg(reinterpret_cast<const int4*>(p.dst + k));
+        } else {
+          if (k < pairs) s[u].x = __ldg(p.src + k), d[u].x = __ldg(p.dst + k);
+          if (k + 1 < pairs) s[u].y = __ldg(p.src + k + 1), d[u].y = __ldg(p.dst + k + 1);
+          if (k + 2 < pairs) s[u].z = __ldg(p.src + k + 2), d[u].z = __ldg(p.dst + k + 2);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kListLoads; ++u) {
+        const int sv[4] = {s[u].x, s[u].y, s[u].z, s[u].w}, dv[4] = {d[u].x, d[u].y, d[u].z, d[u].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (!copied(p, sv[e], dv[e])) continue;
+          const uint32_t at = (uint32_t)((look ? sv[e] : dv[e]) - first);
+          if (at >= (uint32_t)kListPages) continue;  // another CTA's page
+          const uint32_t bit = 1u << (at & 31);
+          bad |= ((look ? targets[at >> 5] : atomicOr(&targets[at >> 5], bit)) & bit) != 0;
+        }
+      }
+    }
+    __syncthreads();
+  }
+  if (__syncthreads_or(bad) && threadIdx.x == 0) flag(p.status, KVQ_FLAG_PAGE_LIST);
 }
 
 }  // namespace
@@ -439,7 +491,12 @@ cudaError_t launch_pages_compact(const PoolParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_pages_copy(const PageCopyParams& p, cudaStream_t stream) {
-  return launch_pdl(copy_kernel, dim3(p.num_pairs, p.layers), dim3(kCopyThreads), 0, stream, p);
+  cudaError_t e = launch_pdl(copy_kernel, dim3(p.num_pairs, p.layers), dim3(kCopyThreads), 0, stream, p);
+  if (e != cudaSuccess || !p.report || p.num_pairs <= kListInline) return e;
+  e = cudaFuncSetAttribute(list_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kListPages / 8);
+  if (e != cudaSuccess) return e;
+  const unsigned grid = (unsigned)(((long long)p.num_pages + kListPages - 1) / kListPages);
+  return launch_pdl(list_kernel, dim3(grid), dim3(kListThreads), kListPages / 8, stream, p);
 }
 
 }  // namespace kvq
