@@ -523,12 +523,17 @@ KVQ_API kvq_status kvq_pages_reorder(const kvq_page_pool* pool, const int32_t* p
 /*
  * Makes positions [seq_lens_before[b], seq_lens_before[b] + new_lens[b])
  * writable for every sequence: blocks without a page get one, and a page
- * shared with another sequence is replaced by a fresh one (where all holders
- * of a shared page ask for it, the last of them keeps it).  A replaced page
- * that holds tokens before seq_lens_before[b] has to be copied:
+ * shared with another sequence is replaced by a fresh one:
+ *   - a page in which the sequence keeps tokens (the first block, when
+ *     seq_lens_before[b] lies inside it) has to be copied first; where all
+ *     holders of such a page ask for it in this way, the last of them keeps it;
+ *   - a page that is written from its start (sequences forked without a trim,
+ *     then rewound) is replaced without a copy for every holder that asks, the
+ *     last one included.
  *   copy_src, copy_dst  device int32 [batch]: the pair of sequence b, or -1;
  *                       pass them to kvq_pages_copy for every layer, before
- *                       the new tokens are appended
+ *                       the new tokens are appended and before pages are
+ *                       reserved again (a source may be free by now)
  *   granted             device int32 [batch] or NULL: new_lens[b] (num_new
  *                       when new_lens is NULL); 0 for a skipped sequence
  * With too few free pages nothing changes for any sequence: KVQ_FLAG_POOL_EMPTY,
