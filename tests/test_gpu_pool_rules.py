@@ -54,3 +54,49 @@ def test_which_shared_pages_are_replaced(before, new, needs, keeps):
             copies = part and b != keeps
             assert got[1][b] == (first if copies else -1)
             assert (got[5][b][first] == first) == (b == keeps or new[b] == 0)
+
+
+@pytest.mark.parametrize("B,limit_us", [(300, 500), (5000, 500), (16384, 500)])
+@pytest.mark.parametrize("others", [0, 1])
+def test_large_batches_of_forks(B, limit_us, others):
+    """Every row a fork of one of three sequences and writing into its partly
+    filled page; with `others`, somebody who does not write holds each of the
+    pages too.  The time is that of a few passes over the rows; a look at all
+    rows before each took 2580 us for 16384."""
+    import torch
+    import quantized_kv_decode_gb300 as K
+    rng = np.random.default_rng(B)
+    who = rng.integers(0, 3, size=B)
+    table = np.stack([who, np.full(B, -1)], 1).astype(np.int32)
+    ref = np.zeros(B + 40, dtype=np.int32)
+    ref[:3] = np.bincount(who, minlength=3) + others
+    pool = K.PagePool(_i32(ref), _i32(table), PAGE)
+    src, dst, granted = (_i32([7] * B) for _ in range(3))
+    before = _i32(np.full(B, 5))
+    ws = torch.empty(K.kvq_pages_workspace_size(pool), dtype=torch.uint8, device="cuda")
+    times = []
+    for _ in range(4):
+        pool.ref_count.copy_(torch.from_numpy(ref))
+        pool.block_table.copy_(torch.from_numpy(table))
+        ws.fill_(0xFF)
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        torch.cuda.synchronize()
+        a.record()
+        K.kvq_pages_reserve(pool, before, None, src, dst, granted, max_new=1, workspace=ws)
+        b.record()
+        torch.cuda.synchronize()
+        times.append(a.elapsed_time(b) * 1e3)
+    keep = np.zeros(B, dtype=bool)
+    if not others:
+        for w in range(3):
+            keep[np.flatnonzero(who == w)[-1]] = True
+    fresh = 3 + np.cumsum(~keep) - 1
+    assert src.tolist() == np.where(keep, -1, who).tolist()
+    assert dst.tolist() == np.where(keep, -1, fresh).tolist()
+    assert granted.tolist() == [1] * B
+    assert pool.block_table[:, 0].tolist() == np.where(keep, who, fresh).tolist()
+    left = ref.copy()
+    left[3:3 + (~keep).sum()] = 1
+    left[:3] = 1
+    assert pool.ref_count.tolist() == left.tolist()
+    assert min(times) < limit_us, times
