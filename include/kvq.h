@@ -123,7 +123,8 @@ typedef enum {
 #define KVQ_FLAG_PAGE_LIST    0x40u /* a copy list names a page twice as target,
                                        or one page as source and target       */
 #define KVQ_FLAG_TIMEOUT      0x80u /* a kernel's internal wait ran out (2 s):
-                                       the call's output is unusable          */
+                                       the call's output is unusable (only this
+                                       word tells; see kvq_extend_attn)       */
 
 typedef enum { KVQ_DENSE = 0, KVQ_PAGED = 1 } kvq_layout;
 
@@ -473,6 +474,10 @@ KVQ_API size_t kvq_extend_workspace_size(const kvq_cache_desc* desc, int32_t bat
  * length exceeds min(max_seq_len, cache capacity) flags KVQ_FLAG_SEQ_LEN and
  * yields zero rows; a token whose page is unmapped flags KVQ_FLAG_BLOCK_TABLE
  * and is left out; a row with nothing to attend to is zero.
+ * The kernel's warps hand tiles to one another; should such a wait last two
+ * seconds, which no input causes, the thread block gives up and its rows of
+ * `out` are not written (or joined from what the workspace held).  Only
+ * KVQ_FLAG_TIMEOUT in *dev_status tells, so pass it where that matters.
  */
 KVQ_API kvq_status kvq_extend_attn(const kvq_cache_desc* desc, const kvq_cache* cache,
                            int32_t batch, int32_t num_new, int32_t num_q_heads,

@@ -6,7 +6,7 @@ Build the library with ``python -m quantized_kv_decode_gb300.build``.
 """
 from ._lib import (KVQ_DENSE, KVQ_ERR_CUDA, KVQ_ERR_INVALID_ARG, KVQ_ERR_UNSUPPORTED,  # noqa: F401
                    KVQ_ERR_WORKSPACE, KVQ_FLAG_BLOCK_TABLE, KVQ_FLAG_NONFINITE, KVQ_FLAG_OOB,
-                   KVQ_FLAG_PAGE_LIST, KVQ_FLAG_POOL_EMPTY, KVQ_FLAG_SEQ_LEN,
+                   KVQ_FLAG_PAGE_LIST, KVQ_FLAG_POOL_EMPTY, KVQ_FLAG_SEQ_LEN, KVQ_FLAG_TIMEOUT,
                    KVQ_FLAG_ZERO_CLAMPED, KVQ_OK, KVQ_PAGED, KVQError, kvq_cache, kvq_cache_desc,
                    kvq_page_pool, kvq_rope, kvq_rope_desc, lib)
 
