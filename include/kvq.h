@@ -236,6 +236,14 @@ KVQ_API kvq_status kvq_cache_array_bytes(const kvq_cache_desc* desc, int32_t bat
  * to their slots.  One call is two kernel launches, in stream order.
  * Axis-aware caches take at most KVQ_MAX_BATCH sequences per call (larger:
  * KVQ_ERR_UNSUPPORTED before any launch).
+ * The window of an axis-aware sequence holds the newest tokens appended and no
+ * others.  So its length is what has been appended: all num_new rows of a
+ * padded batch count, and sequences of different numbers of new tokens take a
+ * call each (with the sequence's part of the arrays, batch 1).  Nor can a
+ * sequence of L tokens be cut back to any length: only to one of at most S
+ * tokens, to a block's border S + j g, or to one within its last, unfinished
+ * block.  Other lengths ask for window rows that have been replaced, which
+ * nothing can flag.
  */
 KVQ_API kvq_status kvq_append(const kvq_cache_desc* desc, const kvq_cache* cache,
                       int32_t batch, int32_t num_new,
@@ -434,7 +442,8 @@ KVQ_API kvq_status kvq_rope_append(const kvq_cache_desc* desc, const kvq_cache* 
  * Reads cached rows back: row t of sequence b is position start[b] + t, for
  * the t < num_rows with start[b] + t < seq_lens[b]; rows behind are left as
  * they were.
- *   seq_lens      device int32 [batch]: tokens cached
+ *   seq_lens      device int32 [batch]: tokens cached (axis-aware caches: all
+ *                 that have been appended, see kvq_append)
  *   start         device int32 [batch]
  *   k_out, v_out  device fp16 [batch][num_rows][num_kv_heads][head_dim]
  *                 (either may be NULL)
@@ -464,6 +473,8 @@ KVQ_API size_t kvq_extend_workspace_size(const kvq_cache_desc* desc, int32_t bat
  *                    token t attends to positions [0, seq_lens_before[b] + t].
  *   max_seq_len      host upper bound on seq_lens_before[b] + new_lens[b]
  *   out              device fp16 like q; may not overlap it
+ * Axis-aware caches: seq_lens_before[b] + new_lens[b] is all that has been
+ * appended to the sequence (see kvq_append).
  * num_splits, softmax_scale and workspace as for kvq_decode_attn, but any
  * number of query heads per KV head.  Scores and softmax in fp32; K and V
  * enter the products as x_hat = (q - z) s to 22 bits (two fp16 numbers, held at
@@ -493,7 +504,8 @@ KVQ_API kvq_status kvq_extend_attn(const kvq_cache_desc* desc, const kvq_cache* 
  * free, and pages are always taken lowest first, so the same calls give the
  * same tables.  All of it runs on the device, in stream order.
  * For an axis-aware cache the pool's positions are those after the sinks, and
- * the fp16 windows, which are per sequence, are the caller's to copy.
+ * the fp16 windows, which are per sequence, are the caller's to copy; which
+ * lengths a sequence can be trimmed to, kvq_append says.
  * ------------------------------------------------------------------------ */
 
 /* Largest batch of a pool (kvq_pages_reserve holds the batch on chip). */
