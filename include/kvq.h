@@ -477,9 +477,9 @@ KVQ_API size_t kvq_extend_workspace_size(const kvq_cache_desc* desc, int32_t bat
  * appended to the sequence (see kvq_append).
  * num_splits, softmax_scale and workspace as for kvq_decode_attn, but any
  * number of query heads per KV head.  Scores and softmax in fp32; K and V
- * enter the products as x_hat = (q - z) s to 22 bits (two fp16 numbers, held at
- * fp16's largest), the probabilities as fp16 (11 bits down to 2^-21 of the
- * row's largest).  An infinity or NaN in a token's V row makes
+ * enter the products as x_hat = (q - z) s, held at fp16's largest and otherwise
+ * exact (as the sum of two fp16 numbers; NF4 values to within 2^-25), the
+ * probabilities as fp16 (11 bits down to 2^-21 of the row's largest).  An infinity or NaN in a token's V row makes
  * NaN or infinities of the rows that see the token, possibly in more channels
  * than its own; rows that do not see it are untouched.  A sequence whose
  * length exceeds min(max_seq_len, cache capacity) flags KVQ_FLAG_SEQ_LEN and

@@ -32,10 +32,12 @@
 // cycles a step, bound by its own latency with two warps a scheduler: 17 tokens
 // over 32768 (INT8) 46 us.
 //
-// Precision.  q - z is a whole number (exact in fp16 up to 2048) and s has
-// 11 bits, so x_hat = (q - z) s has up to 23: K and V enter as sums of two fp16
-// numbers, hi = fp16(x_hat) and lo = fp16(x_hat - hi), two products into one
-// accumulator.  With hi alone for both, the outputs of keys with large
+// Precision.  q - z is a whole number of up to 12 bits (exact in fp16 up to
+// 2048) and s has 11, so x_hat = (q - z) s has up to 23 and is, like s, a whole
+// number of 2^-24: K and V enter as sums of two fp16 numbers, hi = fp16(x_hat)
+// and lo = x_hat - hi, which fp16 holds exactly (at most 2^11 units of s's last
+// bit); two products into one accumulator.  (NF4: a level times s has bits below
+// 2^-24 where s < 2; lo is off by up to 2^-25.)  With hi alone for both, the outputs of keys with large
 // channels (INT4 groups of 32, 10x channels) are off by 1.0e-3 to 1.3e-3
 // relative, five times what rounding the output costs (2.1e-4); with K's lo by
 // 3.2e-4, with both by 2.7e-4: the output's own rounding and that of the

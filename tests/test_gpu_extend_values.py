@@ -1,10 +1,11 @@
 """GPU tests of kvq_extend_attn on values that a softmax and its weighted sum
 must not lose: an infinity or NaN in V alone, seen by some of a tile's rows
-and not by others."""
+and not by others; K and V so small that fp16 has few bits for them."""
 import numpy as np
 import pytest
 
-from tests._prompt import check_extend, new_cache, read_rows
+from oracle import prompt_oracle as P
+from tests._prompt import check_extend, expected_rows, new_cache, read_rows
 
 pytestmark = pytest.mark.gpu
 
@@ -51,3 +52,51 @@ def test_every_row_that_sees_a_value_takes_part(T, before, Hq, D, splits, value)
         v[before - 1, 5] = value
         got = K.kvq_extend_attn(cache, tq, tb, before + T, num_splits=splits).cpu().numpy()
         assert not np.isfinite(got[0, :, :, 5]).any()
+
+
+def _small_bound(q, k, mass, out, scale, v, nf4):
+    """How far an output may be from the formula's where K and V enter exactly.
+
+    Per score: D products in fp32, error at most D 2^-24 of S = sum |q_d k_d|
+    (over the largest row of K and q), felt by its weight and by the sum of
+    weights, 1.5 in the exponent's base; 2^-19 for the exponentials and their
+    reference.  A weight is rounded to fp16: 2^-11 of itself, or 2^-25 in units
+    of 2^-7 of the row's largest.  The weighted sum and the sum of weights take
+    L terms in fp32.  The output is rounded to fp16: 2^-11 of itself, or half of
+    the smallest step, 2^-25.  NF4: K and V are each off by up to 2^-25."""
+    D, L = q.shape[-1], k.shape[1]
+    qs = np.abs(q).max(axis=(0, 1))
+    S = float((qs * np.abs(k).max(axis=(0, 1))).sum())
+    rel = 2.0 ** -11 + 2 * 1.5 * scale * D * 2.0 ** -24 * S + 2.0 ** -19 + 2 * L * 2.0 ** -24
+    low = 2.0 ** -25 + L * 2.0 ** -32 * np.abs(v).max()
+    if nf4:
+        rel += 2 * scale * 2.0 ** -25 * float(qs.sum())
+        low += 2.0 ** -25
+    return mass * rel + 2.0 ** -11 * np.abs(out) + low
+
+
+@pytest.mark.parametrize("size", [1e-2, 1e-4])
+@pytest.mark.parametrize("T", [5, 140])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("fmt", ["int4", "int8", "int2", "sym8", "nf4"])
+def test_small_values_enter_whole(fmt, D, T, size):
+    """K and V of 1e-2 and 1e-4, where a single fp16 number has few bits left
+    and the second one's steps are fp16's smallest: scores of several units (q
+    as much larger) and outputs against (q - z) s itself."""
+    import torch
+    import quantized_kv_decode_gb300 as K
+    rng = np.random.default_rng(17)
+    before, Hq, Hkv = 150, 2, 1
+    L = before + T
+    cache = new_cache(fmt, Hkv, D, 1, L)
+    k, v = ((size * rng.standard_normal((1, L, Hkv, D))).astype(np.float16) for _ in "kv")
+    K.kvq_append(cache, torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda(),
+                 torch.zeros(1, dtype=torch.int32, device="cuda"))
+    q = (rng.standard_normal((1, T, Hq, D)) / size).astype(np.float16)
+    scale = 2.0 * D ** -0.5
+    got = K.kvq_extend_attn(cache, torch.from_numpy(q).cuda(), torch.tensor([before], dtype=torch.int32, device="cuda"),
+                            L, softmax_scale=scale, num_splits=1).cpu().numpy()[0].astype(np.float64)
+    kx, vx = (expected_rows(fmt, x[0]).transpose(1, 0, 2) for x in (k, v))
+    want, mass = P.extend_attention(q[0].astype(np.float64), kx, vx, before, scale)
+    off = np.abs(got - want) / _small_bound(q[0].astype(np.float64), kx, mass, want, scale, vx, fmt == "nf4")
+    assert off.max() <= 1.0, off.max()
