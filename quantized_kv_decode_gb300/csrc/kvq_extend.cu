@@ -330,11 +330,15 @@ cudaError_t run(const ExtendParams* p, ExtendPlan* plan, cudaStream_t stream) {
   return launch_pdl(extend_kernel<BITS, D>, grid, dim3(kThreads), extend_smem(D), stream, *p);
 }
 
+// Axis-aware caches are INT4 or INT8; of the other formats only head_dim 256
+// comes here.
 template <int BITS>
 cudaError_t run_d(int D, const ExtendParams* p, ExtendPlan* plan, cudaStream_t stream) {
-  if (D == 64) return run<BITS, 64>(p, plan, stream);
-  if (D == 128) return run<BITS, 128>(p, plan, stream);
-  return run<BITS, 256>(p, plan, stream);
+  if constexpr (BITS == 4 || BITS == 8) {
+    if (D == 64) return run<BITS, 64>(p, plan, stream);
+    if (D == 128) return run<BITS, 128>(p, plan, stream);
+  }
+  return D == 256 ? run<BITS, 256>(p, plan, stream) : cudaErrorInvalidValue;
 }
 
 cudaError_t run_any(const CacheGeom& c, const ExtendParams* p, ExtendPlan* plan, cudaStream_t stream) {

@@ -63,3 +63,20 @@ def test_two_fp16_numbers_hold_an_nf4_value():
     assert off.max() <= 2.0 ** -25
     assert np.array_equal(lv * 2.0 ** 15, np.rint(lv * 2.0 ** 15))
     assert not off[s[:, 0] >= 2.0].any()
+
+
+def test_no_attention_instance_that_nothing_reaches():
+    """The mma.sync form of kvq_extend_attn is built for axis-aware caches (4
+    and 8 bits) at every head_dim, and for the other formats at 256 only."""
+    import os
+    import re
+    import shutil
+    import subprocess
+    from quantized_kv_decode_gb300 import build
+    build.build()
+    obj = os.path.join(build.BUILD, "kvq_extend.cu.o")
+    if shutil.which("nm") is None or not os.path.exists(obj):
+        pytest.skip("no nm, or no object files")
+    out = subprocess.run(["nm", "-C", obj], capture_output=True, text=True, check=True).stdout
+    got = {(int(b), int(d)) for b, d in re.findall(r"extend_kernel<(\d+), (\d+)>", out)}
+    assert got == {(2, 256), (16, 256)} | {(b, d) for b in (4, 8) for d in (64, 128, 256)}
