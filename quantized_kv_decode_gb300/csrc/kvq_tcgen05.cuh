@@ -75,8 +75,9 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
 }
 
 // Waits for copies or products in flight before the block gives up, whoever
-// else has (two seconds at most).
-__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
+// else has (two seconds at most).  (Out of line: inlined where it is called it
+// took 2 % of a late prompt chunk by the kernel's size.)
+static __device__ __noinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
   int none = 0;
   mbar_wait_slow(bar, parity, &none);
 }

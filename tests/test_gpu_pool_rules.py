@@ -56,7 +56,7 @@ def test_which_shared_pages_are_replaced(before, new, needs, keeps):
             assert (got[5][b][first] == first) == (b == keeps or new[b] == 0)
 
 
-@pytest.mark.parametrize("B,limit_us", [(300, 500), (5000, 500), (16384, 500)])
+@pytest.mark.parametrize("B,limit_us", [(300, 1000), (5000, 1000), (16384, 1000)])
 @pytest.mark.parametrize("others", [0, 1])
 def test_large_batches_of_forks(B, limit_us, others):
     """Every row a fork of one of three sequences and writing into its partly
