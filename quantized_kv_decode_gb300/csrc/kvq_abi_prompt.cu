@@ -86,8 +86,8 @@ struct ExtendChoice {
 // writing out), the partials their bytes written and read, 6800 a ns against
 // 13 ns a position with one tile of rows, 20 with two (the fp16 kernel's; the
 // quantized ones' are up to a quarter more).  16 sequences of 1390 to 6527
-// tokens, 5 new ones, INT4: 3 splits chosen, 98 us; 1 to 12 splits 98, 104, 98,
-// 96, 103, 105, 108, 113, 119, 123, 127, 132.
+// tokens, 5 new ones, INT4, calls in turn on one cache: 3 splits chosen, 98 us;
+// 1 to 12 splits 99, 105, 98, 97, 104, 107, 109, 114, 120, 124, 128, 133.
 constexpr int64_t kFixed = 384;
 int32_t choose_extend_splits(int64_t units, int64_t max_len, int64_t rows, int64_t D, bool several, int requested,
                              const ExtendPlan& plan) {

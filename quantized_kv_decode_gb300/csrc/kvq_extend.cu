@@ -16,8 +16,9 @@
 // factor (2^14: m is the exact maximum here) that keeps small ones in fp16's
 // normal range.  Bound by the conversion of a tile before its products, which
 // nothing overlaps: it is the form that is right for every cache, kept for the
-// shapes that tensor memory has no room for (D = 256: two tiles' O alone fill
-// it) or whose keys have a scale per channel.
+// shapes that the tensor-core kernel is not written for: D = 256 (the O of its
+// two tiles of rows alone would fill tensor memory; one tile would fit, 448 of
+// 512 columns) and keys that have a scale per channel.
 #include "kvq_extend_tc.cuh"
 #include "kvq_host.cuh"
 #include "kvq_load.cuh"

@@ -25,12 +25,16 @@
 //
 // What bounds it.  256 rows of 128 channels over codes: the tensor core, 2048
 // cycles a 64-key step of about 2600 (K and V each in two parts): INT4, 4096
-// tokens after 12288, 32 / 8 heads, 1.05 ms, 914 TFLOP/s of the formula's.  Over
+// tokens after 12288, 32 / 8 heads (the late chunk below), 1.03 ms by itself
+// (profiler), 937 TFLOP/s of the formula's; calls in turn, each with the merge
+// of its two splits (47 us), 1.07 to 1.13 ms by the inputs and the power.  Over
 // fp16: the softmax, about 2000 cycles a step (512 of them a warp's exponentials
 // alone, and two warps share a scheduler's unit) where the products take 1280:
-// 0.88 ms, 1098 TFLOP/s.  At most 128 rows: the conversion, about 1300 of 1900
-// cycles a step, bound by its own latency with two warps a scheduler: 17 tokens
-// over 32768 (INT8) 46 us.
+// 0.88 ms, 1088 TFLOP/s, calls in turn.  At most 128 rows: the conversion, about
+// 1300 of 1900 cycles a step, bound by its own latency with two warps a
+// scheduler: 17 tokens over 32768 (INT8) 42 us by itself, 44 in turn.
+// (Figures "a -> b" below are of the step that brought them: calls in turn, on
+// one set of inputs.)
 //
 // Precision.  q - z is a whole number of up to 12 bits (exact in fp16 up to
 // 2048) and s has 11, so x_hat = (q - z) s has up to 23 and is, like s, a whole
@@ -281,8 +285,8 @@ __device__ __forceinline__ void store_seg(const Seg<BITS>& x, int key, int seg, 
     // A small loop, its words shifted on.  One chunk a turn where the softmax
     // of 256 rows runs beside it, whose code shares the instruction caches
     // (late prompt chunk: 1.135 ms, two a turn 1.163); two a turn where few
-    // rows wait for the conversion (16 x 5 tokens over ragged 8000: 98 us, one
-    // a turn 105).
+    // rows wait for the conversion (16 x 5 tokens over ragged 8000, calls in turn
+    // on one cache: 98 us, one a turn 105).
     Seg<BITS> y = x;
     Group gc = g[0];
 #pragma unroll UNROLL

@@ -5,7 +5,7 @@
 // dependent passes over the table and counts (256 sequences of 190 blocks: 5 us
 // and, for the first two blocks of each, 11 us; reserve and compact are one
 // CTA, so that their prefix sums need no second launch).  copy:
-// memory, 0.97 of the rate of a plain copy (16 layers of a compaction, 684 us).
+// memory, the rate of a plain copy (16 layers of a compaction, 646 us).
 //
 // Reference counts change by integer atomics only, whose sums do not depend
 // on the order, and pages are handed out by prefix sums over the page index,
