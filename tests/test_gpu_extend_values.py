@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 
 from oracle import prompt_oracle as P
-from tests._prompt import check_extend, expected_rows, new_cache, read_rows
+from tests._prompt import FORMATS, check_extend, expected_rows, new_cache, read_rows
 
 pytestmark = pytest.mark.gpu
 
@@ -100,3 +100,36 @@ def test_small_values_enter_whole(fmt, D, T, size):
     want, mass = P.extend_attention(q[0].astype(np.float64), kx, vx, before, scale)
     off = np.abs(got - want) / _small_bound(q[0].astype(np.float64), kx, mass, want, scale, vx, fmt == "nf4")
     assert off.max() <= 1.0, off.max()
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("T,before", [(90, 0), (31, 59)])
+def test_values_of_an_axis_aware_window(T, before, D, value):
+    """The same for the rows that an axis-aware cache keeps in fp16: the sinks
+    and the unfinished block, V alone and K and V."""
+    import torch
+    import quantized_kv_decode_gb300 as K
+    rng = np.random.default_rng(23)
+    bits, g, kw = FORMATS["kch4"]
+    S, L, Hq = kw["sink_tokens"], before + T, 2
+    cache = new_cache("kch4", 1, D, 1, L)
+    k, v = (torch.from_numpy(rng.standard_normal((1, L, 1, D)).astype(np.float16)).cuda() for _ in "kv")
+    K.kvq_append(cache, k, v, torch.zeros(1, dtype=torch.int32, device="cuda"))
+    k16, v16 = read_rows(cache, [L], L)
+    q = rng.standard_normal((1, T, Hq, D)).astype(np.float16)
+    tb = torch.tensor([before], dtype=torch.int32, device="cuda")
+    r0 = S + (L - S) // g * g
+    assert r0 < L - 2
+    for pos, slot in ((1, 1), (r0, S), (L - 1, S + (L - 1 - S) % g)):
+        for windows in ((cache.v_window,), (cache.k_window, cache.v_window)):
+            held = [w[0, 0, slot, 3].item() for w in windows]
+            for w in windows:
+                w[0, 0, slot, 3] = value
+            got = K.kvq_extend_attn(cache, torch.from_numpy(q).cuda(), tb, L).cpu().numpy()
+            for w, x in zip(windows, held):
+                w[0, 0, slot, 3] = x
+            at = max(pos - before, 0)       # the first row that sees it
+            assert not np.isfinite(got[0, at:, :, 3]).any(), (pos, len(windows))
+            if at:
+                check_extend(got[0], q[0], k16[0], v16[0], before, at, D ** -0.5, rounded=True)
