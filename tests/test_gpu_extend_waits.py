@@ -76,7 +76,7 @@ def test_a_wait_that_runs_out(debug_lib, fmt, D, page, T):
             assert status == L.KVQ_FLAG_TIMEOUT, (wait, tile)
             # the waits that end a block for good found their copies and
             # products done: each of them has two seconds
-            assert took < 1.0, (wait, tile, took)
+            assert took < 1.8, (wait, tile, took)
             if tile >= 3:                       # these sequences have fewer key tiles
                 assert torch.equal(got[1], want[1]) and torch.equal(got[3], want[3]), (wait, tile)
             status, _, got = call()
