@@ -427,7 +427,7 @@ def _prepare_shared(st, gen, dev):
     if S:  # one pool: the prefixes' pages and the tails'
         blocks = [-(-n // S) for n in prefix] + [-(-(b + n) // S) for b, n in zip(before, new)]
         table = _tables(blocks, max(blocks), sum(blocks) + 3, gen, dev)
-        st["prefix_table"], st["tail_table"] = table[:N].contiguous(), table[N:].contiguous()
+        st["prefix_table"], st["tail_table"] = table[:N].clone(), table[N:].clone()  # (each on a 16-byte boundary)
         st["prefix"] = st["tail"] = _filled_cache(D, *fmt[0], (sum(blocks) + 3, Hkv, S), gen, dev)
     else:
         st["prefix_table"] = st["tail_table"] = None
