@@ -439,6 +439,60 @@ KVQ_API kvq_status kvq_rope_append(const kvq_cache_desc* desc, const kvq_cache* 
                            uint32_t* dev_status, void* stream);
 
 /*
+ * Rotary positions by several axes (images: rows and columns; video: time
+ * too).  A token has one position per axis, and every pair turns by the
+ * position of its axis.
+ *   pairs[a]    pairs of axis a; together rotary_dim / 2
+ *   cycled      0: the pairs of an axis follow one another, axis by axis;
+ *               1: the axes take turns, pair by pair, while they have pairs left
+ *   own_ladders 0: pair i turns by w_i, whatever its axis; 1: the j-th pair of
+ *               axis a turns as pair j of a rotation of 2 pairs[a] channels
+ * (scaling YARN with own_ladders: the amplitude is the same for every axis.)
+ */
+#define KVQ_ROPE_MAX_AXES 4
+
+typedef struct {
+  kvq_rope_desc rope;       /* rotary_dim = twice the pairs of all axes        */
+  int32_t num_axes;         /* 1 .. KVQ_ROPE_MAX_AXES                          */
+  int32_t pairs[KVQ_ROPE_MAX_AXES];  /* >= 1 for a < num_axes                  */
+  int32_t cycled;
+  int32_t own_ladders;
+} kvq_rope_axes_desc;
+
+typedef struct {
+  kvq_rope rope;
+  int32_t num_axes;
+  uint8_t axis[KVQ_ROPE_MAX_PAIRS];  /* of each pair, below num_axes           */
+} kvq_rope_axes;
+
+/* Fills *axes from *desc.  Host arithmetic only. */
+KVQ_API kvq_status kvq_rope_axes_init(const kvq_rope_axes_desc* desc, kvq_rope_axes* axes);
+
+/*
+ * kvq_rope_apply with a position per axis:
+ *   positions  device int32 [batch][num_new][num_axes], any value
+ * Angles, roundings and the rest as there.
+ */
+KVQ_API kvq_status kvq_rope_axes_apply(const kvq_rope_axes* axes, int32_t head_dim, int32_t batch,
+                               int32_t num_new, int32_t num_q_heads, const uint16_t* q,
+                               uint16_t* q_out, int32_t num_k_heads, const uint16_t* k,
+                               uint16_t* k_out, const int32_t* positions,
+                               const int32_t* new_lens, uint32_t* dev_status, void* stream);
+
+/*
+ * kvq_rope_append with a position per axis: the angles come from positions
+ * (as above), the cache rows from seq_lens_before[b] + t.  Bit for bit
+ * kvq_rope_axes_apply on q and k_new followed by the append of the result and
+ * v_new.  Axis-aware caches: KVQ_ERR_UNSUPPORTED, as there.
+ */
+KVQ_API kvq_status kvq_rope_axes_append(const kvq_cache_desc* desc, const kvq_cache* cache,
+                                const kvq_rope_axes* axes, int32_t batch, int32_t num_new,
+                                const uint16_t* k_new, const uint16_t* v_new,
+                                int32_t num_q_heads, const uint16_t* q, uint16_t* q_out,
+                                const int32_t* positions, const int32_t* seq_lens_before,
+                                const int32_t* new_lens, uint32_t* dev_status, void* stream);
+
+/*
  * Reads cached rows back: row t of sequence b is position start[b] + t, for
  * the t < num_rows with start[b] + t < seq_lens[b]; rows behind are left as
  * they were.
@@ -589,6 +643,117 @@ KVQ_API kvq_status kvq_pages_copy(const kvq_cache_desc* desc, const kvq_cache* c
                           int32_t num_layers, const int32_t* copy_src, const int32_t* copy_dst,
                           int32_t num_pairs, uint32_t* dev_status, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Shared prefixes: sequences whose first tokens are the same (a system prompt,
+ * a document or video with many questions about it, parallel samples of one
+ * prompt) attend to them together, and the prefix is read once for all of them.
+ * A prefix is a sequence of one cache, and every sequence's own tokens, its
+ * tail, are a sequence of another (or of the same pages through another block
+ * table, which kvq_prefix_find makes).  The two caches may differ in format,
+ * layout and size; num_kv_heads and head_dim are the same.
+ * ------------------------------------------------------------------------ */
+
+/* Most prefixes of a plan. */
+#define KVQ_MAX_PREFIXES 65535
+
+/* Bytes of a plan; 0 for sizes that cannot be. */
+KVQ_API size_t kvq_prefix_plan_size(int32_t batch, int32_t num_prefixes);
+
+/*
+ * Which sequence is on which prefix, once for all layers of a step.
+ *   prefix_of    device int32 [batch]: 0 .. num_prefixes - 1, or -1 (none)
+ *   prefix_lens  device int32 [num_prefixes]: tokens of each prefix; 0: empty
+ *   plan         device, kvq_prefix_plan_size() bytes, 16-byte aligned: read by
+ *                kvq_prefix_attn, which needs neither array again
+ * Another prefix_of flags KVQ_FLAG_BLOCK_TABLE and counts as none, a negative
+ * length KVQ_FLAG_SEQ_LEN and as empty.
+ */
+KVQ_API kvq_status kvq_prefix_plan(int32_t batch, int32_t num_prefixes, const int32_t* prefix_of,
+                           const int32_t* prefix_lens, void* plan, size_t plan_bytes,
+                           uint32_t* dev_status, void* stream);
+
+/* Device scratch of kvq_prefix_find. */
+KVQ_API size_t kvq_prefix_find_workspace_size(const kvq_page_pool* pool);
+
+/*
+ * The prefixes that a page pool's sequences share, from its block table alone.
+ * With S tokens a page, sequence b holds n_b = seq_lens_before[b] / S whole
+ * pages; k = max(1, ceil(min_tokens / S)):
+ *   - a sequence with n_b >= k and a page in block k - 1 belongs to the group
+ *     of the sequences with the same page there; its leader is the lowest one;
+ *   - its run is the number of leading blocks that hold the leader's pages, at
+ *     most min(n_b, n_leader); with a run below k it belongs to no group;
+ *   - a group's prefix is as many blocks as some member's run r for which
+ *     (members with a run >= r, less one) * r, the blocks not read again, is
+ *     largest (the longest of equal ones); with nothing saved it has none;
+ *   - members with a run of at least that are on the prefix.
+ * Prefixes are numbered by their leaders, ascending; of more than max_prefixes
+ * the first are kept.  The shared pages are whole, so tokens appended behind
+ * seq_lens_before change none of them.
+ *   prefix_of      device int32 [batch], -1: none
+ *   prefix_lens    device int32 [max_prefixes]; 0 behind the last
+ *   prefix_table   device int32 [max_prefixes][max_blocks_per_seq]; -1 behind
+ *   tail_table     device int32 [batch][max_blocks_per_seq]: each row of the
+ *                  pool's table without the prefix's blocks; -1 behind
+ *   tail_lens      device int32 [batch]: seq_lens_before less the prefix
+ *   num_prefixes   device int32 [1] or NULL: prefixes found, those beyond
+ *                  max_prefixes among them
+ * kvq_prefix_plan takes prefix_of and prefix_lens; kvq_prefix_attn the pool's
+ * caches with the two tables and tail_lens.  Appending goes through the pool's
+ * own table and lengths.  For per-token caches: an axis-aware sequence's sinks
+ * and window are not in the table.  A length that cannot be flags
+ * KVQ_FLAG_SEQ_LEN; that sequence has no prefix and keeps its length.  batch *
+ * max_blocks_per_seq^2 of 2^62 and above: KVQ_ERR_UNSUPPORTED.
+ */
+KVQ_API kvq_status kvq_prefix_find(const kvq_page_pool* pool, const int32_t* seq_lens_before,
+                           int32_t min_tokens, int32_t max_prefixes, int32_t* prefix_of,
+                           int32_t* prefix_lens, int32_t* prefix_table, int32_t* tail_table,
+                           int32_t* tail_lens, int32_t* num_prefixes, void* workspace,
+                           size_t workspace_bytes, uint32_t* dev_status, void* stream);
+
+/* Device scratch of kvq_prefix_attn (the splits as there). */
+KVQ_API size_t kvq_prefix_attn_workspace_size(const kvq_cache_desc* prefix_desc,
+                                      const kvq_cache_desc* desc, int32_t num_prefixes,
+                                      int32_t batch, int32_t num_new, int32_t num_q_heads,
+                                      int32_t max_prefix_len, int32_t max_seq_len,
+                                      int32_t prefix_splits, int32_t tail_splits);
+
+/*
+ * Attention of one or several new tokens per sequence over its prefix and its
+ * tail, the new tokens' own rows included (already appended to the tail): for
+ * num_new = 1 a decode step, else as kvq_extend_attn.
+ *   prefix_desc, prefix_cache  num_prefixes sequences (num_prefixes 0: NULL)
+ *   desc, cache                batch tails
+ *   q                device fp16 [batch][num_new][num_q_heads][head_dim]
+ *   seq_lens_before  device int32 [batch]: tokens of the tail before the new
+ *                    ones; token t attends to the whole prefix and to the
+ *                    tail's positions [0, seq_lens_before[b] + t]
+ *   new_lens         device int32 [batch] or NULL, as above
+ *   plan             of kvq_prefix_plan, for this batch and num_prefixes
+ *   max_prefix_len   host upper bound on the prefixes' lengths
+ *   max_seq_len      host upper bound on seq_lens_before[b] + new_lens[b]
+ *   prefix_splits, tail_splits  0: library choice, else as num_splits of
+ *                    kvq_decode_attn, for each of the two
+ *   out              device fp16 like q; may not overlap it
+ * Axis-aware caches: a prefix's length is all that has been appended to it.
+ * Precision: over the prefix as in kvq_extend_attn, over the tail as in
+ * kvq_decode_attn (one new token, shapes its tensor-core kernels take) or
+ * kvq_extend_attn; the partial results are joined in fp32.  A tail whose length
+ * exceeds min(max_seq_len, its cache's capacity) flags KVQ_FLAG_SEQ_LEN and
+ * yields zero rows.  A prefix longer than min(max_prefix_len, its cache's
+ * capacity) flags KVQ_FLAG_SEQ_LEN and is left out; so is a token whose page
+ * is unmapped (KVQ_FLAG_BLOCK_TABLE).  KVQ_FLAG_TIMEOUT as there.
+ */
+KVQ_API kvq_status kvq_prefix_attn(const kvq_cache_desc* prefix_desc, const kvq_cache* prefix_cache,
+                           int32_t num_prefixes, const kvq_cache_desc* desc,
+                           const kvq_cache* cache, int32_t batch, int32_t num_new,
+                           int32_t num_q_heads, const uint16_t* q,
+                           const int32_t* seq_lens_before, const int32_t* new_lens,
+                           const void* plan, size_t plan_bytes, int32_t max_prefix_len,
+                           int32_t max_seq_len, int32_t prefix_splits, int32_t tail_splits,
+                           float softmax_scale, uint16_t* out, void* workspace,
+                           size_t workspace_bytes, uint32_t* dev_status, void* stream);
+
 /* Size of the library's own split scratch used by kvq_decode_attn_static_ws. */
 #define KVQ_STATIC_WORKSPACE_BYTES ((size_t)8 << 20)
 
@@ -645,11 +810,12 @@ KVQ_API kvq_status kvq_decode_attn_static_ws(const kvq_cache_desc* desc, const k
  *   workspace      workspace_bytes (the static array for the
  *                  _static_ws call).
  *   kvq_cache_read: k_out and v_out as k_new and v_new with num_rows tokens;
- *   kvq_extend_attn: q and out batch * num_new rows; kvq_rope_append: k_new
- *   and v_new.  The other arrays of the prompt and pool calls (q of the
- *   rotations, positions, new_lens, start, the pool's and the copy lists) are
- *   read and written at indexes the kernels have checked against the sizes
- *   given, in every build, and carry no extents.
+ *   kvq_extend_attn: q and out batch * num_new rows; kvq_prefix_attn: the same,
+ *   its prefixes' cache with num_prefixes sequences; kvq_rope_append and
+ *   kvq_rope_axes_append: k_new and v_new.  The other arrays of the prompt, pool
+ *   and prefix calls (q of the rotations, positions, new_lens, start, the pool's,
+ *   the copy lists, plans) are read and written at indexes the kernels have
+ *   checked against the sizes given, in every build, and carry no extents.
  * Every global load and store of the arrays above first checks that its bytes
  * lie inside the extent of the array it addresses.  An access that does not is
  * skipped (a load yields zeros), and KVQ_FLAG_OOB is OR-ed into *dev_status

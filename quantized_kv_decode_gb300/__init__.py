@@ -8,7 +8,7 @@ from ._lib import (KVQ_DENSE, KVQ_ERR_CUDA, KVQ_ERR_INVALID_ARG, KVQ_ERR_UNSUPPO
                    KVQ_ERR_WORKSPACE, KVQ_FLAG_BLOCK_TABLE, KVQ_FLAG_NONFINITE, KVQ_FLAG_OOB,
                    KVQ_FLAG_PAGE_LIST, KVQ_FLAG_POOL_EMPTY, KVQ_FLAG_SEQ_LEN, KVQ_FLAG_TIMEOUT,
                    KVQ_FLAG_ZERO_CLAMPED, KVQ_OK, KVQ_PAGED, KVQError, kvq_cache, kvq_cache_desc,
-                   kvq_page_pool, kvq_rope, kvq_rope_desc, lib)
+                   kvq_page_pool, kvq_rope, kvq_rope_axes, kvq_rope_axes_desc, kvq_rope_desc, lib)
 
 __all__ = [
     "KVCache", "make_desc", "kvq_append", "kvq_decode_attn", "kvq_append_decode_attn",
@@ -18,6 +18,9 @@ __all__ = [
     "kvq_extend_num_splits", "kvq_extend_workspace_size",
     "PagePool", "kvq_pages_workspace_size", "kvq_pages_reorder", "kvq_pages_reserve",
     "kvq_pages_compact", "kvq_pages_copy",
+    "make_rope_axes", "kvq_rope_axes_apply", "kvq_rope_axes_append",
+    "PrefixPlan", "kvq_prefix_plan", "kvq_prefix_find", "kvq_prefix_find_workspace_size",
+    "kvq_prefix_attn", "kvq_prefix_attn_workspace_size",
     "kvq_status_string", "KVQError", "lib",
 ]
 
@@ -30,5 +33,8 @@ def __getattr__(name):
         if hasattr(api, name):
             return getattr(api, name)
         from . import prompt
-        return getattr(prompt, name)
+        if hasattr(prompt, name):
+            return getattr(prompt, name)
+        from . import prefix
+        return getattr(prefix, name)
     raise AttributeError(name)

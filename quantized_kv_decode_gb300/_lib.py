@@ -8,8 +8,8 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import (POINTER, Structure, byref, c_double, c_float, c_int32, c_int64, c_size_t, c_uint32,  # noqa: F401
-                    c_uint64, c_void_p)
+from ctypes import (POINTER, Structure, byref, c_double, c_float, c_int32, c_int64, c_size_t, c_uint8,  # noqa: F401
+                    c_uint32, c_uint64, c_void_p)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libkvq.so")
@@ -34,7 +34,9 @@ KVQ_FLAG_TIMEOUT = 0x80  # a bounded wait inside a kernel ran out
 # kvq_rope_scaling
 ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "bands": 3, "yarn": 4}
 KVQ_ROPE_MAX_PAIRS = 128
+KVQ_ROPE_MAX_AXES = 4
 KVQ_MAX_POOL_BATCH = 16384
+KVQ_MAX_PREFIXES = 65535
 
 # kvq_debug_wait: the waits a debug build can let run out
 (KVQ_WAIT_NONE, KVQ_WAIT_SOFTMAX, KVQ_WAIT_K, KVQ_WAIT_V, KVQ_WAIT_LOAD_K, KVQ_WAIT_LOAD_V,
@@ -104,6 +106,24 @@ class kvq_rope(Structure):
     ]
 
 
+class kvq_rope_axes_desc(Structure):
+    _fields_ = [
+        ("rope", kvq_rope_desc),
+        ("num_axes", c_int32),
+        ("pairs", c_int32 * KVQ_ROPE_MAX_AXES),
+        ("cycled", c_int32),
+        ("own_ladders", c_int32),
+    ]
+
+
+class kvq_rope_axes(Structure):
+    _fields_ = [
+        ("rope", kvq_rope),
+        ("num_axes", c_int32),
+        ("axis", c_uint8 * KVQ_ROPE_MAX_PAIRS),
+    ]
+
+
 class kvq_page_pool(Structure):
     _fields_ = [
         ("num_pages", c_int32),
@@ -152,6 +172,14 @@ SIGNATURES = {
     "kvq_rope_append": (c_int32, [POINTER(kvq_cache_desc), POINTER(kvq_cache), POINTER(kvq_rope),
                                   c_int32, c_int32, c_void_p, c_void_p, c_int32, c_void_p,
                                   c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+    "kvq_rope_axes_init": (c_int32, [POINTER(kvq_rope_axes_desc), POINTER(kvq_rope_axes)]),
+    "kvq_rope_axes_apply": (c_int32, [POINTER(kvq_rope_axes), c_int32, c_int32, c_int32, c_int32,
+                                      c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_void_p,
+                                      c_void_p, c_void_p, c_void_p]),
+    "kvq_rope_axes_append": (c_int32, [POINTER(kvq_cache_desc), POINTER(kvq_cache),
+                                       POINTER(kvq_rope_axes), c_int32, c_int32, c_void_p,
+                                       c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_void_p,
+                                       c_void_p, c_void_p, c_void_p]),
     "kvq_cache_read": (c_int32, [POINTER(kvq_cache_desc), POINTER(kvq_cache), c_int32, c_int32,
                                  c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
     "kvq_extend_num_splits": (c_int32, [POINTER(kvq_cache_desc), c_int32, c_int32, c_int32,
@@ -170,6 +198,21 @@ SIGNATURES = {
                                     c_void_p, c_size_t, c_void_p, c_void_p]),
     "kvq_pages_copy": (c_int32, [POINTER(kvq_cache_desc), c_void_p, c_int32, c_void_p,
                                  c_void_p, c_int32, c_void_p, c_void_p]),
+    "kvq_prefix_plan_size": (c_size_t, [c_int32, c_int32]),
+    "kvq_prefix_plan": (c_int32, [c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_size_t,
+                                  c_void_p, c_void_p]),
+    "kvq_prefix_find_workspace_size": (c_size_t, [POINTER(kvq_page_pool)]),
+    "kvq_prefix_find": (c_int32, [POINTER(kvq_page_pool), c_void_p, c_int32, c_int32, c_void_p,
+                                  c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                  c_size_t, c_void_p, c_void_p]),
+    "kvq_prefix_attn_workspace_size": (c_size_t, [POINTER(kvq_cache_desc), POINTER(kvq_cache_desc),
+                                                  c_int32, c_int32, c_int32, c_int32, c_int32,
+                                                  c_int32, c_int32, c_int32]),
+    "kvq_prefix_attn": (c_int32, [POINTER(kvq_cache_desc), POINTER(kvq_cache), c_int32,
+                                  POINTER(kvq_cache_desc), POINTER(kvq_cache), c_int32, c_int32,
+                                  c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t,
+                                  c_int32, c_int32, c_int32, c_int32, c_float, c_void_p, c_void_p,
+                                  c_size_t, c_void_p, c_void_p]),
     "kvq_debug_checks": (c_int32, []),
     "kvq_debug_shrink_extent": (c_int32, [c_int32, c_int64]),
     "kvq_debug_fail_wait": (c_int32, [c_int32, c_int32]),

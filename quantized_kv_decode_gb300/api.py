@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import math
 from ctypes import byref, c_size_t
-from dataclasses import dataclass
+from dataclasses import dataclass, replace
 
 import torch
 
@@ -117,6 +117,16 @@ class KVCache:
         return kvq_cache(_ptr(self.k_codes), _ptr(self.v_codes), _ptr(self.k_scale),
                          _ptr(self.k_zero), _ptr(self.v_scale), _ptr(self.v_zero),
                          _ptr(self.block_table), _ptr(self.k_window), _ptr(self.v_window))
+
+    def with_table(self, block_table: torch.Tensor) -> "KVCache":
+        """The pages of a paged cache as the sequences of another block table
+        [sequences][max_blocks_per_seq] see them; nothing is copied."""
+        if self.desc.layout != KVQ_PAGED or self.desc.k_per_channel:
+            raise ValueError("only paged per-token caches can be seen through another table")
+        _need(block_table, torch.int32, "block_table", 2)
+        if block_table.device != self.k_codes.device or block_table.shape[1] != self.desc.max_blocks_per_seq:
+            raise ValueError(f"block_table must have {self.desc.max_blocks_per_seq} columns, on {self.k_codes.device}")
+        return replace(self, batch=block_table.shape[0], block_table=block_table)
 
     def nbytes(self) -> int:
         return sum(t.numel() * t.element_size() for t in

@@ -333,6 +333,77 @@ void dbg_fill(CacheGeom& g, const kvq_cache_desc* desc, const kvq_cache* cache, 
 #endif
 }
 
+void dbg_extent(CacheGeom& g, int array, const void* base, size_t bytes) {
+#ifdef KVQ_DEBUG
+  dbg_set(g.dbg, array, base, bytes);
+#else
+  (void)g, (void)array, (void)base, (void)bytes;
+#endif
+}
+
+kvq_status tail_decode_plan(const kvq_cache_desc* desc, const CacheGeom& geom, int32_t batch, int32_t num_q_heads,
+                            int32_t max_len, int32_t requested, TailDecode* t) {
+  const int G = num_q_heads / desc->num_kv_heads;
+  *t = TailDecode{};
+  if (G > 8 || batch > KVQ_MAX_BATCH || geom.kch) return KVQ_OK;
+  while (t->gp < G) t->gp <<= 1;
+  if (desc->bits == 16) {
+    t->takes = desc->head_dim == 64 || desc->head_dim == 128;
+  } else if (fast_format(desc, G)) {
+    DecodeParams probe{};
+    probe.geom = geom;
+    probe.G = G;
+    const cudaError_t e = launch_decode_fast(probe, desc->bits, t->gp, nullptr, &t->takes, &t->occ);
+    if (t->takes && e != cudaSuccess) return from_cuda(e);
+  }
+  if (!t->takes) return KVQ_OK;
+  Plan plan;
+  const kvq_status st = make_plan(desc, geom, batch, num_q_heads, max_len, requested, &plan);
+  t->splits = plan.splits;
+  return st;
+}
+
+cudaError_t tail_decode(const kvq_cache_desc* desc, const kvq_cache* cache, const CacheGeom& geom, int32_t batch,
+                        int32_t num_q_heads, const uint16_t* q, const int32_t* before, const int32_t* new_lens,
+                        int32_t max_len, const TailDecode& t, float scale_log2, float* ws_o, float* ws_ml,
+                        const void* ws, size_t ws_bytes, uint32_t* status, cudaStream_t stream) {
+  DecodeParams p{};
+  p.geom = geom;
+  p.geom.block_table = cache->block_table;
+  p.codes[0] = reinterpret_cast<const uint8_t*>(cache->k_codes);
+  p.codes[1] = reinterpret_cast<const uint8_t*>(cache->v_codes);
+  p.scale[0] = reinterpret_cast<const __half*>(cache->k_scale);
+  p.scale[1] = reinterpret_cast<const __half*>(cache->v_scale);
+  p.zero[0] = reinterpret_cast<const __half*>(cache->k_zero);
+  p.zero[1] = reinterpret_cast<const __half*>(cache->v_zero);
+  if (geom.nf4) memcpy(p.nf4_level, nf4_table().level, sizeof(p.nf4_level));
+  p.q = reinterpret_cast<const __half*>(q);
+  p.seq_lens = before;
+  p.len_add = 1;
+  p.tail_new = new_lens;
+  p.ws_o = ws_o;
+  p.ws_ml = ws_ml;
+  p.status = status;
+  p.batch = batch;
+  p.Hq = num_q_heads;
+  p.G = num_q_heads / desc->num_kv_heads;
+  p.splits = t.splits;
+  p.chunk = split_chunk(max_len, t.splits);
+  const int64_t cap = (int64_t)desc->capacity * (desc->layout == KVQ_DENSE ? 1 : desc->max_blocks_per_seq);
+  p.len_limit = (int32_t)std::min<int64_t>(cap, max_len);
+  p.scale_log2 = scale_log2;
+  p.rows32 = desc->layout == KVQ_PAGED &&
+             (int64_t)desc->num_pages * desc->num_kv_heads * desc->capacity * geom.row_bytes < ((int64_t)1 << 31);
+  dbg_fill(p.geom, desc, cache, batch, num_q_heads, 0, q, nullptr, nullptr, before, nullptr, ws, ws_bytes, status);
+  if (desc->bits == 16) return launch_decode_generic(p, stream);  // (the fp16 tensor-core kernel)
+  // longest first where the grid has more than one wave, as in a decode call
+  p.longest_first = t.occ > 0 && batch > 1 && batch <= kLongestFirstMaxBatch &&
+                    (int64_t)t.splits * desc->num_kv_heads * batch > (int64_t)sm_count() * t.occ;
+  bool handled = false;
+  const cudaError_t e = launch_decode_fast(p, desc->bits, t.gp, stream, &handled, nullptr);
+  return handled ? e : cudaErrorInvalidValue;
+}
+
 size_t workspace_bytes(int64_t batch, int64_t Hq, int64_t D, int64_t splits) {
   if (splits <= 1) return 0;
   const size_t o = (size_t)(batch * Hq * splits * D) * sizeof(float);

@@ -1,0 +1,259 @@
+// Host side of the shared-prefix calls of include/kvq.h: argument validation,
+// planning and dispatch.  Nothing here allocates memory or synchronizes a
+// stream.
+#include <math.h>
+
+#include <algorithm>
+
+#include "kvq_prompt_host.cuh"
+
+using namespace kvq;
+
+namespace {
+
+size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// One pass's partials: sums of rows * splits, then (maximum, sum) pairs.
+size_t partial_bytes(int64_t rows, int64_t D, int64_t splits) {
+  return up256((size_t)(rows * splits * D) * sizeof(float)) + up256((size_t)(rows * splits) * 2 * sizeof(float));
+}
+void carve_partials(void* at, int64_t rows, int64_t D, int64_t splits, float** o, float** ml) {
+  *o = reinterpret_cast<float*>(at);
+  *ml = reinterpret_cast<float*>(reinterpret_cast<char*>(at) + up256((size_t)(rows * splits * D) * sizeof(float)));
+}
+
+// How a call runs: the prefix pass, then the tails by a decode kernel or by
+// extend attention, then the join.
+struct PrefixChoice {
+  CacheGeom pg, tg;
+  bool prefixes = false;  // there is a prefix pass
+  ExtendPlan pre, tail;
+  TailDecode decode;
+  int32_t prefix_splits = 0, tail_splits = 0;
+  size_t prefix_bytes = 0, tail_bytes = 0;
+};
+
+kvq_status choose(const kvq_cache_desc* pd, const kvq_cache_desc* d, int32_t N, int32_t B, int32_t T, int32_t Hq,
+                  int32_t max_prefix, int32_t max_len, int32_t want_prefix, int32_t want_tail, PrefixChoice* c) {
+  kvq_status st = check_desc(d, &c->tg);
+  if (st != KVQ_OK) return st;
+  if (N < 0 || B < 0 || T < 0 || Hq <= 0 || max_prefix < 0 || max_len < 0 || want_prefix < 0 || want_tail < 0)
+    return KVQ_ERR_INVALID_ARG;
+  if (Hq % d->num_kv_heads) return KVQ_ERR_INVALID_ARG;
+  if (N > 0) {
+    if ((st = check_desc(pd, &c->pg)) != KVQ_OK) return st;
+    if (pd->num_kv_heads != d->num_kv_heads || pd->head_dim != d->head_dim) return KVQ_ERR_INVALID_ARG;
+  }
+  if (N > KVQ_MAX_PREFIXES || B > KVQ_MAX_BATCH || d->num_kv_heads > 65535 || too_many_rows(B, T, Hq))
+    return KVQ_ERR_UNSUPPORTED;
+  if (B == 0 || T == 0) return KVQ_OK;
+  const int G = Hq / d->num_kv_heads;
+  const int64_t D = d->head_dim, rows = (int64_t)B * T * Hq, each = (int64_t)T * G;
+  if (T == 1 && (st = tail_decode_plan(d, c->tg, B, Hq, max_len, want_tail, &c->decode)) != KVQ_OK) return st;
+  c->tail_splits = c->decode.splits;
+  if (!c->decode.takes) {
+    const cudaError_t e = extend_plan(c->tg, T, G, &c->tail);
+    if (e != cudaSuccess) return from_cuda(e);
+    const int64_t tiles = ceil_div(each, c->tail.tile_rows);
+    c->tail_splits =
+        choose_extend_splits(tiles * d->num_kv_heads * B, max_len, rows, D, B > 1, want_tail, c->tail);
+    if (tiles * c->tail_splits > INT32_MAX) return KVQ_ERR_UNSUPPORTED;
+  }
+  if (c->tail_splits <= 0) return KVQ_ERR_CUDA;
+  c->tail_bytes = partial_bytes(rows, D, c->tail_splits);
+  c->prefixes = N > 0 && max_prefix > 0;
+  if (c->prefixes) {
+    const int32_t used = std::min(N, B);
+    const cudaError_t e = extend_prefix_plan(c->pg, ceil_div(B * each, used), &c->pre);
+    if (e != cudaSuccess) return from_cuda(e);
+    // (a prefix's members fill their tiles on average; the bound counts a part
+    // of a tile more for each prefix)
+    const int64_t tiles = std::max<int64_t>(used, ceil_div(B * each, c->pre.tile_rows));
+    c->prefix_splits =
+        choose_extend_splits(tiles * d->num_kv_heads, max_prefix, rows, D, false, want_prefix, c->pre);
+    if (c->prefix_splits <= 0) return KVQ_ERR_CUDA;
+    if (prefix_tiles_bound(B, N, each, c->pre.tile_rows) * c->prefix_splits > INT32_MAX) return KVQ_ERR_UNSUPPORTED;
+    c->prefix_bytes = partial_bytes(rows, D, c->prefix_splits);
+  }
+  return KVQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t kvq_prefix_plan_size(int32_t batch, int32_t num_prefixes) {
+  if (batch < 0 || num_prefixes < 0 || batch > KVQ_MAX_BATCH || num_prefixes > KVQ_MAX_PREFIXES) return 0;
+  return plan_words(batch, num_prefixes) * sizeof(int32_t);
+}
+
+kvq_status kvq_prefix_plan(int32_t batch, int32_t num_prefixes, const int32_t* prefix_of, const int32_t* prefix_lens,
+                           void* plan, size_t plan_bytes, uint32_t* dev_status, void* stream) {
+  if (batch < 0 || num_prefixes < 0) return KVQ_ERR_INVALID_ARG;
+  if (batch > KVQ_MAX_BATCH || num_prefixes > KVQ_MAX_PREFIXES) return KVQ_ERR_UNSUPPORTED;
+  if ((batch && !prefix_of) || (num_prefixes && !prefix_lens) || !aligned(prefix_of) || !aligned(prefix_lens))
+    return KVQ_ERR_INVALID_ARG;
+  if (!plan || !aligned(plan) || plan_bytes < kvq_prefix_plan_size(batch, num_prefixes)) return KVQ_ERR_WORKSPACE;
+  PrefixPlanParams p{};
+  p.of = prefix_of;
+  p.len = prefix_lens;
+  p.plan = reinterpret_cast<int32_t*>(plan);
+  p.status = dev_status;
+  p.B = batch;
+  p.N = num_prefixes;
+  return from_cuda(launch_prefix_plan(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t kvq_prefix_find_workspace_size(const kvq_page_pool* pool) {
+  if (check_pool(pool) != KVQ_OK) return 0;
+  return (size_t)std::max(pool->batch, 1) * 16;
+}
+
+kvq_status kvq_prefix_find(const kvq_page_pool* pool, const int32_t* seq_lens_before, int32_t min_tokens,
+                           int32_t max_prefixes, int32_t* prefix_of, int32_t* prefix_lens, int32_t* prefix_table,
+                           int32_t* tail_table, int32_t* tail_lens, int32_t* num_prefixes, void* workspace,
+                           size_t workspace_bytes, uint32_t* dev_status, void* stream) {
+  kvq_status st = check_pool(pool);
+  if (st != KVQ_OK) return st;
+  if (min_tokens < 0 || max_prefixes < 1) return KVQ_ERR_INVALID_ARG;
+  if (max_prefixes > KVQ_MAX_PREFIXES) return KVQ_ERR_UNSUPPORTED;
+  // a group's savings and run are compared as one 64-bit number
+  const double M = pool->max_blocks_per_seq;
+  if (pool->batch * M * (M + 1) >= 0x1p62) return KVQ_ERR_UNSUPPORTED;
+  if ((st = check_pool_arrays(pool)) != KVQ_OK) return st;
+  if (!prefix_lens || !prefix_table || !aligned(prefix_lens) || !aligned(prefix_table)) return KVQ_ERR_INVALID_ARG;
+  if (pool->batch && (!seq_lens_before || !prefix_of || !tail_table || !tail_lens)) return KVQ_ERR_INVALID_ARG;
+  if (!aligned(seq_lens_before) || !aligned(prefix_of) || !aligned(tail_table) || !aligned(tail_lens) ||
+      !aligned(num_prefixes))
+    return KVQ_ERR_INVALID_ARG;
+  const size_t table = (size_t)pool->batch * pool->max_blocks_per_seq * 4;
+  if (pool->batch && (tail_table == pool->block_table || partly_over(tail_table, pool->block_table, table) ||
+                      tail_lens == seq_lens_before))
+    return KVQ_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace) || workspace_bytes < kvq_prefix_find_workspace_size(pool))
+    return KVQ_ERR_WORKSPACE;
+  PrefixFindParams p{};
+  p.pool = *pool;
+  p.lens = seq_lens_before;
+  p.of = prefix_of;
+  p.len = prefix_lens;
+  p.prefix_table = prefix_table;
+  p.tail_table = tail_table;
+  p.tail_lens = tail_lens;
+  p.num = num_prefixes;
+  p.best = reinterpret_cast<unsigned long long*>(workspace);
+  p.status = dev_status;
+  p.most = max_prefixes;
+  p.depth = (int32_t)std::max<int64_t>(1, ceil_div(min_tokens, pool->page_size));
+  return from_cuda(launch_prefix_find(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t kvq_prefix_attn_workspace_size(const kvq_cache_desc* prefix_desc, const kvq_cache_desc* desc,
+                                      int32_t num_prefixes, int32_t batch, int32_t num_new, int32_t num_q_heads,
+                                      int32_t max_prefix_len, int32_t max_seq_len, int32_t prefix_splits,
+                                      int32_t tail_splits) {
+  PrefixChoice c;
+  if (choose(prefix_desc, desc, num_prefixes, batch, num_new, num_q_heads, max_prefix_len, max_seq_len, prefix_splits,
+             tail_splits, &c) != KVQ_OK)
+    return 0;
+  return c.prefix_bytes + c.tail_bytes;
+}
+
+kvq_status kvq_prefix_attn(const kvq_cache_desc* prefix_desc, const kvq_cache* prefix_cache, int32_t num_prefixes,
+                           const kvq_cache_desc* desc, const kvq_cache* cache, int32_t batch, int32_t num_new,
+                           int32_t num_q_heads, const uint16_t* q, const int32_t* seq_lens_before,
+                           const int32_t* new_lens, const void* plan, size_t plan_bytes, int32_t max_prefix_len,
+                           int32_t max_seq_len, int32_t prefix_splits, int32_t tail_splits, float softmax_scale,
+                           uint16_t* out, void* workspace, size_t workspace_size, uint32_t* dev_status, void* stream) {
+  PrefixChoice c;
+  kvq_status st = choose(prefix_desc, desc, num_prefixes, batch, num_new, num_q_heads, max_prefix_len, max_seq_len,
+                         prefix_splits, tail_splits, &c);
+  if (st != KVQ_OK) return st;
+  if (!(softmax_scale >= 0.f) || isinf(softmax_scale)) return KVQ_ERR_INVALID_ARG;
+  if ((st = check_cache(desc, cache)) != KVQ_OK) return st;
+  if (num_prefixes > 0 && (st = check_cache(prefix_desc, prefix_cache)) != KVQ_OK) return st;
+  if (batch == 0 || num_new == 0) return KVQ_OK;
+  if (!q || !out || !seq_lens_before || !plan) return KVQ_ERR_INVALID_ARG;
+  if (!aligned(q) || !aligned(out) || !aligned(seq_lens_before) || !aligned(new_lens) || !aligned(plan))
+    return KVQ_ERR_INVALID_ARG;
+  if (plan_bytes < kvq_prefix_plan_size(batch, num_prefixes)) return KVQ_ERR_INVALID_ARG;
+  const int64_t rows = (int64_t)batch * num_new * num_q_heads;
+  const size_t bytes = (size_t)rows * desc->head_dim * 2;
+  if (q == out || partly_over(q, out, bytes)) return KVQ_ERR_INVALID_ARG;
+  const size_t need = c.prefix_bytes + c.tail_bytes;
+  if (!workspace || workspace_size < need || !aligned(workspace)) return KVQ_ERR_WORKSPACE;
+
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int64_t D = desc->head_dim;
+  const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf((float)desc->head_dim);
+  const float scale_log2 = scale * 1.4426950408889634f;
+  float *po = nullptr, *pml = nullptr, *to, *tml;
+  if (c.prefixes) carve_partials(workspace, rows, D, c.prefix_splits, &po, &pml);
+  carve_partials(reinterpret_cast<char*>(workspace) + c.prefix_bytes, rows, D, c.tail_splits, &to, &tml);
+
+  ExtendParams p{};  // what both passes of extend attention share
+  p.q = reinterpret_cast<const __half*>(q);
+  p.status = dev_status;
+  p.num_new = num_new;
+  p.Hq = num_q_heads;
+  p.G = num_q_heads / desc->num_kv_heads;
+  p.scale_log2 = scale_log2;
+  const PrefixPlan pl = plan_of(plan, batch, num_prefixes);
+  cudaError_t e = cudaSuccess;
+  int32_t prefix_limit = 0;
+  if (c.prefixes) {
+    ExtendParams x = p;
+    x.v = view_of(c.pg, prefix_cache);
+    dbg_fill(x.v.geom, prefix_desc, prefix_cache, num_prefixes, 0, 0, nullptr, nullptr, nullptr, nullptr, nullptr,
+             workspace, workspace_size, dev_status);
+    dbg_extent(x.v.geom, KVQ_ARRAY_Q, q, bytes);
+    x.ws_o = po;
+    x.ws_ml = pml;
+    x.batch = num_prefixes;
+    x.splits = c.prefix_splits;
+    x.chunk = split_chunk(max_prefix_len, c.prefix_splits);
+    x.len_limit = prefix_limit = (int32_t)std::min<int64_t>(cache_capacity(c.pg), max_prefix_len);
+    x.plan = pl;
+    if ((e = launch_extend_prefix(x, c.pre, s)) != cudaSuccess) return from_cuda(e);
+  }
+  if (c.decode.takes) {
+    e = tail_decode(desc, cache, c.tg, batch, num_q_heads, q, seq_lens_before, new_lens, max_seq_len, c.decode,
+                    scale_log2, to, tml, workspace, workspace_size, dev_status, s);
+  } else {
+    ExtendParams x = p;
+    x.v = view_of(c.tg, cache);
+    dbg_fill(x.v.geom, desc, cache, batch, num_q_heads * num_new, 0, q, nullptr, nullptr, seq_lens_before, nullptr,
+             workspace, workspace_size, dev_status);
+    x.ws_o = to;
+    x.ws_ml = tml;
+    x.lens_before = seq_lens_before;
+    x.new_lens = new_lens;
+    x.batch = batch;
+    x.splits = c.tail_splits;
+    x.chunk = split_chunk(max_seq_len, c.tail_splits);
+    x.len_limit = (int32_t)std::min<int64_t>(cache_capacity(c.tg), max_seq_len);
+    e = launch_extend_partials(x, c.tail, s);
+  }
+  if (e != cudaSuccess) return from_cuda(e);
+
+  PrefixJoinParams j{};
+  j.geom = c.tg;
+  dbg_fill(j.geom, desc, cache, batch, num_q_heads * num_new, 0, nullptr, nullptr, nullptr, seq_lens_before, out,
+           workspace, workspace_size, dev_status);
+  j.plan = pl;
+  j.part[0] = {po, pml, std::max(c.prefix_splits, 1), split_chunk(max_prefix_len, std::max(c.prefix_splits, 1)),
+               c.pre.lift};
+  j.part[1] = {to, tml, c.tail_splits, split_chunk(max_seq_len, c.tail_splits), c.decode.takes ? 0.f : c.tail.lift};
+  j.out = reinterpret_cast<__half*>(out);
+  j.tail_before = seq_lens_before;
+  j.new_lens = new_lens;
+  j.T = num_new;
+  j.Hq = num_q_heads;
+  j.D = desc->head_dim;
+  j.prefix_limit = prefix_limit;
+  j.tail_limit = (int32_t)std::min<int64_t>(cache_capacity(c.tg), max_seq_len);
+  j.status = dev_status;
+  return from_cuda(launch_prefix_join(j, s));
+}
+
+}  // extern "C"

@@ -6,49 +6,15 @@
 
 #include <algorithm>
 
-#include "kvq_host.cuh"
-#include "kvq_load.cuh"
 #include "kvq_pages.cuh"
+#include "kvq_prompt_host.cuh"
 #include "kvq_rope.cuh"
 
-using namespace kvq;
+namespace kvq {
 
-namespace {
-
-kvq_status check_rope(const kvq_rope* r) {
-  if (!r || r->rotary_dim < 2 || r->rotary_dim > 2 * KVQ_ROPE_MAX_PAIRS || r->rotary_dim % 2)
-    return KVQ_ERR_INVALID_ARG;
-  if (r->interleaved != 0 && r->interleaved != 1) return KVQ_ERR_INVALID_ARG;
-  if (r->amplitude == 0 || r->amplitude >= (1ull << 63)) return KVQ_ERR_INVALID_ARG;
-  return KVQ_OK;
-}
-
-// [a, a + n) and [b, b + n) share a byte but are not the same array
 bool partly_over(const void* a, const void* b, size_t n) {
   const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
   return x != y && x < y + n && y < x + n;
-}
-
-AppendParams append_params(const CacheGeom& g, const kvq_cache* cache, int32_t batch,
-                           int32_t num_new, const uint16_t* k_new, const uint16_t* v_new,
-                           const int32_t* before, uint32_t* status) {
-  AppendParams a{};
-  a.geom = g;
-  a.geom.block_table = cache->block_table;
-  a.codes[0] = reinterpret_cast<uint8_t*>(cache->k_codes);
-  a.codes[1] = reinterpret_cast<uint8_t*>(cache->v_codes);
-  a.scale[0] = reinterpret_cast<__half*>(cache->k_scale);
-  a.scale[1] = reinterpret_cast<__half*>(cache->v_scale);
-  a.zero[0] = reinterpret_cast<__half*>(cache->k_zero);
-  a.zero[1] = reinterpret_cast<__half*>(cache->v_zero);
-  a.src[0] = reinterpret_cast<const __half*>(k_new);
-  a.src[1] = reinterpret_cast<const __half*>(v_new);
-  if (g.nf4) memcpy(a.nf4_mid, nf4_table().mid, sizeof(a.nf4_mid));
-  a.seq_lens_before = before;
-  a.status = status;
-  a.batch = batch;
-  a.num_new = num_new;
-  return a;
 }
 
 CacheView view_of(const CacheGeom& g, const kvq_cache* cache) {
@@ -67,15 +33,9 @@ CacheView view_of(const CacheGeom& g, const kvq_cache* cache) {
   return v;
 }
 
-// Rows of a padded batch are counted in 32 bits by the kernels' grids.
 bool too_many_rows(int64_t batch, int64_t num_new, int64_t heads) {
   return batch * num_new > INT32_MAX / 2 || batch * num_new * heads > INT32_MAX / 2;
 }
-
-struct ExtendChoice {
-  ExtendPlan plan;
-  int32_t splits = 0;
-};
 
 // Splits spread a call with few row tiles over the device, and even out
 // sequences of different lengths.  The automatic choice weighs, in positions
@@ -113,6 +73,165 @@ int32_t choose_extend_splits(int64_t units, int64_t max_len, int64_t rows, int64
   return (int32_t)best;
 }
 
+kvq_status check_pool(const kvq_page_pool* p) {
+  if (!p || p->num_pages <= 0 || p->page_size <= 0 || p->batch < 0 || p->max_blocks_per_seq <= 0)
+    return KVQ_ERR_INVALID_ARG;
+  if ((int64_t)p->page_size * p->max_blocks_per_seq > INT32_MAX) return KVQ_ERR_INVALID_ARG;
+  if (p->num_pages > INT32_MAX / 4) return KVQ_ERR_UNSUPPORTED;
+  if (p->batch > KVQ_MAX_POOL_BATCH) return KVQ_ERR_UNSUPPORTED;
+  return KVQ_OK;
+}
+
+kvq_status check_pool_arrays(const kvq_page_pool* p) {
+  if (!p->ref_count || (p->batch && !p->block_table)) return KVQ_ERR_INVALID_ARG;
+  if (!aligned(p->ref_count) || !aligned(p->block_table)) return KVQ_ERR_INVALID_ARG;
+  return KVQ_OK;
+}
+
+}  // namespace kvq
+
+using namespace kvq;
+
+namespace {
+
+kvq_status check_rope(const kvq_rope* r) {
+  if (!r || r->rotary_dim < 2 || r->rotary_dim > 2 * KVQ_ROPE_MAX_PAIRS || r->rotary_dim % 2)
+    return KVQ_ERR_INVALID_ARG;
+  if (r->interleaved != 0 && r->interleaved != 1) return KVQ_ERR_INVALID_ARG;
+  if (r->amplitude == 0 || r->amplitude >= (1ull << 63)) return KVQ_ERR_INVALID_ARG;
+  return KVQ_OK;
+}
+
+kvq_status check_axes(const kvq_rope_axes* x) {
+  const kvq_status st = check_rope(x ? &x->rope : nullptr);
+  if (st != KVQ_OK) return st;
+  if (x->num_axes < 1 || x->num_axes > KVQ_ROPE_MAX_AXES) return KVQ_ERR_INVALID_ARG;
+  for (int i = 0; i < x->rope.rotary_dim / 2; ++i)
+    if (x->axis[i] >= x->num_axes) return KVQ_ERR_INVALID_ARG;
+  return KVQ_OK;
+}
+
+AppendParams append_params(const CacheGeom& g, const kvq_cache* cache, int32_t batch,
+                           int32_t num_new, const uint16_t* k_new, const uint16_t* v_new,
+                           const int32_t* before, uint32_t* status) {
+  AppendParams a{};
+  a.geom = g;
+  a.geom.block_table = cache->block_table;
+  a.codes[0] = reinterpret_cast<uint8_t*>(cache->k_codes);
+  a.codes[1] = reinterpret_cast<uint8_t*>(cache->v_codes);
+  a.scale[0] = reinterpret_cast<__half*>(cache->k_scale);
+  a.scale[1] = reinterpret_cast<__half*>(cache->v_scale);
+  a.zero[0] = reinterpret_cast<__half*>(cache->k_zero);
+  a.zero[1] = reinterpret_cast<__half*>(cache->v_zero);
+  a.src[0] = reinterpret_cast<const __half*>(k_new);
+  a.src[1] = reinterpret_cast<const __half*>(v_new);
+  if (g.nf4) memcpy(a.nf4_mid, nf4_table().mid, sizeof(a.nf4_mid));
+  a.seq_lens_before = before;
+  a.status = status;
+  a.batch = batch;
+  a.num_new = num_new;
+  return a;
+}
+
+void axes_params(RopeAxesParams& p, const kvq_rope_axes* axes, const int32_t* positions) {
+  p.at = positions;
+  p.num_axes = axes->num_axes;
+  memcpy(p.axis, axes->axis, sizeof(p.axis));
+}
+
+// Validation and launch of a rotation; axes: one position per axis and token
+// (rope is &axes->rope), else null.
+kvq_status rope_apply_impl(const kvq_rope* rope, const kvq_rope_axes* axes, int32_t head_dim, int32_t batch,
+                           int32_t num_new, int32_t num_q_heads, const uint16_t* q, uint16_t* q_out,
+                           int32_t num_k_heads, const uint16_t* k, uint16_t* k_out, const int32_t* positions,
+                           const int32_t* seq_lens_before, const int32_t* new_lens, uint32_t* dev_status,
+                           void* stream) {
+  if (head_dim <= 0 || head_dim % 8 || rope->rotary_dim > head_dim) return KVQ_ERR_INVALID_ARG;
+  if (head_dim > 2 * KVQ_ROPE_MAX_PAIRS) return KVQ_ERR_UNSUPPORTED;
+  if (batch < 0 || num_new < 0 || num_q_heads < 0 || num_k_heads < 0) return KVQ_ERR_INVALID_ARG;
+  if (batch == 0 || num_new == 0 || (num_q_heads == 0 && num_k_heads == 0)) return KVQ_OK;
+  if (too_many_rows(batch, num_new, std::max(num_q_heads, num_k_heads))) return KVQ_ERR_UNSUPPORTED;
+  if (!positions && !seq_lens_before) return KVQ_ERR_INVALID_ARG;
+  if (num_q_heads && (!q || !q_out || !aligned(q) || !aligned(q_out))) return KVQ_ERR_INVALID_ARG;
+  if (num_k_heads && (!k || !k_out || !aligned(k) || !aligned(k_out))) return KVQ_ERR_INVALID_ARG;
+  if (!aligned(positions) || !aligned(seq_lens_before) || !aligned(new_lens)) return KVQ_ERR_INVALID_ARG;
+  const size_t row = (size_t)batch * num_new * head_dim * 2;
+  if (num_q_heads && partly_over(q, q_out, row * num_q_heads)) return KVQ_ERR_INVALID_ARG;
+  if (num_k_heads && partly_over(k, k_out, row * num_k_heads)) return KVQ_ERR_INVALID_ARG;
+  RopeAxesParams x{};
+  RopeParams& p = x.r;
+  p.rope = *rope;
+  p.q = reinterpret_cast<const __half*>(q);
+  p.q_out = reinterpret_cast<__half*>(q_out);
+  p.k = reinterpret_cast<const __half*>(k);
+  p.k_out = reinterpret_cast<__half*>(k_out);
+  p.positions = positions;
+  p.seq_lens_before = seq_lens_before;
+  p.new_lens = new_lens;
+  p.status = dev_status;
+  p.D = head_dim;
+  p.batch = batch;
+  p.num_new = num_new;
+  p.Hq = num_q_heads;
+  p.Hk = num_k_heads;
+  if (axes) {
+    axes_params(x, axes, positions);
+    return from_cuda(launch_rope_axes(x, reinterpret_cast<cudaStream_t>(stream)));
+  }
+  return from_cuda(launch_rope(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// The same for the rotation on the way into the cache.
+kvq_status rope_append_impl(const kvq_cache_desc* desc, const kvq_cache* cache, const kvq_rope* rope,
+                            const kvq_rope_axes* axes, int32_t batch, int32_t num_new, const uint16_t* k_new,
+                            const uint16_t* v_new, int32_t num_q_heads, const uint16_t* q, uint16_t* q_out,
+                            const int32_t* positions, const int32_t* seq_lens_before, const int32_t* new_lens,
+                            uint32_t* dev_status, void* stream) {
+  CacheGeom g;
+  kvq_status st = check_desc(desc, &g);
+  if (st != KVQ_OK) return st;
+  if ((st = check_cache(desc, cache)) != KVQ_OK) return st;
+  if ((st = axes ? check_axes(axes) : check_rope(rope)) != KVQ_OK) return st;
+  if (rope->rotary_dim > desc->head_dim) return KVQ_ERR_INVALID_ARG;
+  if (batch < 0 || num_new < 0 || num_q_heads < 0) return KVQ_ERR_INVALID_ARG;
+  if (desc->k_per_channel) return KVQ_ERR_UNSUPPORTED;
+  if (batch == 0 || num_new == 0) return KVQ_OK;
+  if (too_many_rows(batch, num_new, std::max(num_q_heads, 2 * desc->num_kv_heads)))
+    return KVQ_ERR_UNSUPPORTED;
+  if (!k_new || !v_new || !seq_lens_before || (axes && (!positions || !aligned(positions)))) return KVQ_ERR_INVALID_ARG;
+  if (!aligned(k_new) || !aligned(v_new) || !aligned(seq_lens_before) || !aligned(new_lens))
+    return KVQ_ERR_INVALID_ARG;
+  if (num_q_heads) {
+    if (!q || !q_out || !aligned(q) || !aligned(q_out)) return KVQ_ERR_INVALID_ARG;
+    if (partly_over(q, q_out, (size_t)batch * num_new * num_q_heads * desc->head_dim * 2))
+      return KVQ_ERR_INVALID_ARG;
+  }
+  RopeAxesParams p{};
+  p.a = append_params(g, cache, batch, num_new, k_new, v_new, seq_lens_before, dev_status);
+  dbg_fill(p.a.geom, desc, cache, batch, 0, num_new, nullptr, k_new, v_new, seq_lens_before,
+           nullptr, nullptr, 0, dev_status);
+  p.r.rope = *rope;
+  p.r.q = reinterpret_cast<const __half*>(q);
+  p.r.q_out = reinterpret_cast<__half*>(q_out);
+  p.r.seq_lens_before = seq_lens_before;
+  p.r.new_lens = new_lens;
+  p.r.status = dev_status;
+  p.r.D = desc->head_dim;
+  p.r.batch = batch;
+  p.r.num_new = num_new;
+  p.r.Hq = num_q_heads;
+  if (axes) {
+    axes_params(p, axes, positions);
+    return from_cuda(launch_rope_axes_append(p, reinterpret_cast<cudaStream_t>(stream)));
+  }
+  return from_cuda(launch_rope_append(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+struct ExtendChoice {
+  ExtendPlan plan;
+  int32_t splits = 0;
+};
+
 kvq_status choose_extend(const kvq_cache_desc* desc, const CacheGeom& g, int32_t batch,
                          int32_t num_new, int32_t num_q_heads, int32_t max_seq_len,
                          int32_t requested, ExtendChoice* out) {
@@ -129,21 +248,6 @@ kvq_status choose_extend(const kvq_cache_desc* desc, const CacheGeom& g, int32_t
 
 size_t extend_ws(int64_t rows, int64_t D, int64_t splits) {
   return workspace_bytes(rows, 1, D, splits);
-}
-
-kvq_status check_pool(const kvq_page_pool* p) {
-  if (!p || p->num_pages <= 0 || p->page_size <= 0 || p->batch < 0 || p->max_blocks_per_seq <= 0)
-    return KVQ_ERR_INVALID_ARG;
-  if ((int64_t)p->page_size * p->max_blocks_per_seq > INT32_MAX) return KVQ_ERR_INVALID_ARG;
-  if (p->num_pages > INT32_MAX / 4) return KVQ_ERR_UNSUPPORTED;
-  if (p->batch > KVQ_MAX_POOL_BATCH) return KVQ_ERR_UNSUPPORTED;
-  return KVQ_OK;
-}
-
-kvq_status check_pool_arrays(const kvq_page_pool* p) {
-  if (!p->ref_count || (p->batch && !p->block_table)) return KVQ_ERR_INVALID_ARG;
-  if (!aligned(p->ref_count) || !aligned(p->block_table)) return KVQ_ERR_INVALID_ARG;
-  return KVQ_OK;
 }
 
 }  // namespace
@@ -207,41 +311,57 @@ kvq_status kvq_rope_init(const kvq_rope_desc* d, kvq_rope* rope) {
   return KVQ_OK;
 }
 
+kvq_status kvq_rope_axes_init(const kvq_rope_axes_desc* d, kvq_rope_axes* axes) {
+  if (!d || !axes) return KVQ_ERR_INVALID_ARG;
+  if (d->num_axes < 1 || d->num_axes > KVQ_ROPE_MAX_AXES) return KVQ_ERR_INVALID_ARG;
+  if ((d->cycled != 0 && d->cycled != 1) || (d->own_ladders != 0 && d->own_ladders != 1)) return KVQ_ERR_INVALID_ARG;
+  int64_t all = 0;
+  for (int a = 0; a < d->num_axes; ++a) {
+    if (d->pairs[a] < 1 || d->pairs[a] > KVQ_ROPE_MAX_PAIRS) return KVQ_ERR_INVALID_ARG;
+    all += d->pairs[a];
+  }
+  if (2 * all != d->rope.rotary_dim) return KVQ_ERR_INVALID_ARG;
+  kvq_rope_axes out{};
+  kvq_status st = kvq_rope_init(&d->rope, &out.rope);
+  if (st != KVQ_OK) return st;
+  out.num_axes = d->num_axes;
+  kvq_rope ladder[KVQ_ROPE_MAX_AXES];
+  for (int a = 0; d->own_ladders && a < d->num_axes; ++a) {
+    kvq_rope_desc one = d->rope;
+    one.rotary_dim = 2 * d->pairs[a];
+    if ((st = kvq_rope_init(&one, &ladder[a])) != KVQ_OK) return st;
+  }
+  int used[KVQ_ROPE_MAX_AXES] = {}, a = 0;
+  for (int i = 0; i < all; ++i) {
+    while (used[a] == d->pairs[a]) a = (a + 1) % d->num_axes;  // (some axis has a pair left)
+    out.axis[i] = (uint8_t)a;
+    if (d->own_ladders) out.rope.turns[i] = ladder[a].turns[used[a]];
+    ++used[a];
+    if (d->cycled) a = (a + 1) % d->num_axes;
+  }
+  *axes = out;
+  return KVQ_OK;
+}
+
 kvq_status kvq_rope_apply(const kvq_rope* rope, int32_t head_dim, int32_t batch, int32_t num_new,
                           int32_t num_q_heads, const uint16_t* q, uint16_t* q_out,
                           int32_t num_k_heads, const uint16_t* k, uint16_t* k_out,
                           const int32_t* positions, const int32_t* seq_lens_before,
                           const int32_t* new_lens, uint32_t* dev_status, void* stream) {
-  kvq_status st = check_rope(rope);
+  const kvq_status st = check_rope(rope);
   if (st != KVQ_OK) return st;
-  if (head_dim <= 0 || head_dim % 8 || rope->rotary_dim > head_dim) return KVQ_ERR_INVALID_ARG;
-  if (head_dim > 2 * KVQ_ROPE_MAX_PAIRS) return KVQ_ERR_UNSUPPORTED;
-  if (batch < 0 || num_new < 0 || num_q_heads < 0 || num_k_heads < 0) return KVQ_ERR_INVALID_ARG;
-  if (batch == 0 || num_new == 0 || (num_q_heads == 0 && num_k_heads == 0)) return KVQ_OK;
-  if (too_many_rows(batch, num_new, std::max(num_q_heads, num_k_heads))) return KVQ_ERR_UNSUPPORTED;
-  if (!positions && !seq_lens_before) return KVQ_ERR_INVALID_ARG;
-  if (num_q_heads && (!q || !q_out || !aligned(q) || !aligned(q_out))) return KVQ_ERR_INVALID_ARG;
-  if (num_k_heads && (!k || !k_out || !aligned(k) || !aligned(k_out))) return KVQ_ERR_INVALID_ARG;
-  if (!aligned(positions) || !aligned(seq_lens_before) || !aligned(new_lens)) return KVQ_ERR_INVALID_ARG;
-  const size_t row = (size_t)batch * num_new * head_dim * 2;
-  if (num_q_heads && partly_over(q, q_out, row * num_q_heads)) return KVQ_ERR_INVALID_ARG;
-  if (num_k_heads && partly_over(k, k_out, row * num_k_heads)) return KVQ_ERR_INVALID_ARG;
-  RopeParams p{};
-  p.rope = *rope;
-  p.q = reinterpret_cast<const __half*>(q);
-  p.q_out = reinterpret_cast<__half*>(q_out);
-  p.k = reinterpret_cast<const __half*>(k);
-  p.k_out = reinterpret_cast<__half*>(k_out);
-  p.positions = positions;
-  p.seq_lens_before = seq_lens_before;
-  p.new_lens = new_lens;
-  p.status = dev_status;
-  p.D = head_dim;
-  p.batch = batch;
-  p.num_new = num_new;
-  p.Hq = num_q_heads;
-  p.Hk = num_k_heads;
-  return from_cuda(launch_rope(p, reinterpret_cast<cudaStream_t>(stream)));
+  return rope_apply_impl(rope, nullptr, head_dim, batch, num_new, num_q_heads, q, q_out, num_k_heads, k, k_out,
+                         positions, seq_lens_before, new_lens, dev_status, stream);
+}
+
+kvq_status kvq_rope_axes_apply(const kvq_rope_axes* axes, int32_t head_dim, int32_t batch, int32_t num_new,
+                               int32_t num_q_heads, const uint16_t* q, uint16_t* q_out, int32_t num_k_heads,
+                               const uint16_t* k, uint16_t* k_out, const int32_t* positions,
+                               const int32_t* new_lens, uint32_t* dev_status, void* stream) {
+  const kvq_status st = check_axes(axes);
+  if (st != KVQ_OK) return st;
+  return rope_apply_impl(&axes->rope, axes, head_dim, batch, num_new, num_q_heads, q, q_out, num_k_heads, k, k_out,
+                         positions, nullptr, new_lens, dev_status, stream);
 }
 
 kvq_status kvq_rope_append(const kvq_cache_desc* desc, const kvq_cache* cache, const kvq_rope* rope,
@@ -249,40 +369,18 @@ kvq_status kvq_rope_append(const kvq_cache_desc* desc, const kvq_cache* cache, c
                            const uint16_t* v_new, int32_t num_q_heads, const uint16_t* q,
                            uint16_t* q_out, const int32_t* seq_lens_before,
                            const int32_t* new_lens, uint32_t* dev_status, void* stream) {
-  CacheGeom g;
-  kvq_status st = check_desc(desc, &g);
-  if (st != KVQ_OK) return st;
-  if ((st = check_cache(desc, cache)) != KVQ_OK) return st;
-  if ((st = check_rope(rope)) != KVQ_OK) return st;
-  if (rope->rotary_dim > desc->head_dim) return KVQ_ERR_INVALID_ARG;
-  if (batch < 0 || num_new < 0 || num_q_heads < 0) return KVQ_ERR_INVALID_ARG;
-  if (desc->k_per_channel) return KVQ_ERR_UNSUPPORTED;
-  if (batch == 0 || num_new == 0) return KVQ_OK;
-  if (too_many_rows(batch, num_new, std::max(num_q_heads, 2 * desc->num_kv_heads)))
-    return KVQ_ERR_UNSUPPORTED;
-  if (!k_new || !v_new || !seq_lens_before) return KVQ_ERR_INVALID_ARG;
-  if (!aligned(k_new) || !aligned(v_new) || !aligned(seq_lens_before) || !aligned(new_lens))
-    return KVQ_ERR_INVALID_ARG;
-  if (num_q_heads) {
-    if (!q || !q_out || !aligned(q) || !aligned(q_out)) return KVQ_ERR_INVALID_ARG;
-    if (partly_over(q, q_out, (size_t)batch * num_new * num_q_heads * desc->head_dim * 2))
-      return KVQ_ERR_INVALID_ARG;
-  }
-  RopeAppendParams p{};
-  p.a = append_params(g, cache, batch, num_new, k_new, v_new, seq_lens_before, dev_status);
-  dbg_fill(p.a.geom, desc, cache, batch, 0, num_new, nullptr, k_new, v_new, seq_lens_before,
-           nullptr, nullptr, 0, dev_status);
-  p.r.rope = *rope;
-  p.r.q = reinterpret_cast<const __half*>(q);
-  p.r.q_out = reinterpret_cast<__half*>(q_out);
-  p.r.seq_lens_before = seq_lens_before;
-  p.r.new_lens = new_lens;
-  p.r.status = dev_status;
-  p.r.D = desc->head_dim;
-  p.r.batch = batch;
-  p.r.num_new = num_new;
-  p.r.Hq = num_q_heads;
-  return from_cuda(launch_rope_append(p, reinterpret_cast<cudaStream_t>(stream)));
+  return rope_append_impl(desc, cache, rope, nullptr, batch, num_new, k_new, v_new, num_q_heads, q, q_out, nullptr,
+                          seq_lens_before, new_lens, dev_status, stream);
+}
+
+kvq_status kvq_rope_axes_append(const kvq_cache_desc* desc, const kvq_cache* cache, const kvq_rope_axes* axes,
+                                int32_t batch, int32_t num_new, const uint16_t* k_new, const uint16_t* v_new,
+                                int32_t num_q_heads, const uint16_t* q, uint16_t* q_out, const int32_t* positions,
+                                const int32_t* seq_lens_before, const int32_t* new_lens, uint32_t* dev_status,
+                                void* stream) {
+  if (!axes) return KVQ_ERR_INVALID_ARG;
+  return rope_append_impl(desc, cache, &axes->rope, axes, batch, num_new, k_new, v_new, num_q_heads, q, q_out,
+                          positions, seq_lens_before, new_lens, dev_status, stream);
 }
 
 kvq_status kvq_cache_read(const kvq_cache_desc* desc, const kvq_cache* cache, int32_t batch,

@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_f16_kernel(const Decode
         den = fmaf(f, ml[(w2 * GP + h) * 2 + 1], den);
       }
     }
-    if (p.splits == 1) {
+    if (p.ws_o == nullptr) {
       if (KVQ_IN(geo, KVQ_ARRAY_OUT, p.out + hq0 * D + i, 2))
         p.out[hq0 * D + i] = __float2half_rn(den > 0.f ? num / den : 0.f);
     } else {

@@ -1655,7 +1655,7 @@ __global__ void __launch_bounds__(Cfg<BITS, D, NG, GP, KCH>::THREADS, Cfg<BITS, 
         den += f;
       }
     }
-    if (p.splits == 1) {
+    if (p.ws_o == nullptr) {
       if (KVQ_IN(geo, KVQ_ARRAY_OUT, p.out + hq0 * D + i, 2))
         p.out[hq0 * D + i] = __float2half_rn(den > 0.f ? num / den : 0.f);
     } else {

@@ -67,20 +67,42 @@ __device__ __forceinline__ Span span_of(const ExtendParams& p, int b, bool repor
   return s;
 }
 
-template <int BITS, int D>
-__global__ void __launch_bounds__(kThreads) extend_kernel(const __grid_constant__ ExtendParams p) {
+// PRE: over shared prefixes, as in kvq_extend_tc.cuh.
+template <int BITS, int D, bool PRE>
+__device__ __forceinline__ void attend(const ExtendParams& p) {
   constexpr int KEYS = tile_keys(D), CH = D / 8, KB = D / 16, NT = KEYS / 8;
   pdl_launch_dependents();
   pdl_wait();
   extern __shared__ __align__(128) uint8_t smem[];
   const CacheGeom& c = p.v.geom;
-  const int kvh = blockIdx.y, b = blockIdx.z;
-  const int split = blockIdx.x % p.splits, tile = blockIdx.x / p.splits;
+  const int kvh = blockIdx.y;
+  const int split = blockIdx.x % p.splits;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const Span sp = span_of(p, b, threadIdx.x == 0 && blockIdx.x == 0 && kvh == 0);
+  int b = blockIdx.z, tile = blockIdx.x / p.splits, first = 0;
+  long long live_rows;
+  Span sp;
+  if constexpr (PRE) {
+    const PrefixTile pt = prefix_tile(p.plan, tile, p.num_new * p.G, kRows);
+    if (pt.n < 0) return;
+    b = pt.n, tile = pt.tile, first = pt.first;
+    sp.L = prefix_len(p.plan, b, p.len_limit);
+    if (split * p.chunk >= sp.L) return;
+    live_rows = (long long)pt.count * p.num_new * p.G;
+  } else {
+    sp = span_of(p, b, threadIdx.x == 0 && blockIdx.x == 0 && kvh == 0);
+    live_rows = (long long)sp.n * p.G;
+  }
   const long long r0 = (long long)tile * kRows;
-  const long long live_rows = (long long)sp.n * p.G;
   if (r0 >= live_rows) return;
+  // row r in q, out and the partials
+  auto row_at = [&](long long r) -> long long {
+    if constexpr (PRE) {
+      const int each = p.num_new * p.G, m = (int)(r / each), x = (int)(r - (long long)m * each);
+      return ((long long)plan_member(p.plan, first + m) * p.num_new + x / p.G) * p.Hq + (long long)kvh * p.G + x % p.G;
+    } else {
+      return ((long long)b * p.num_new + r / p.G) * p.Hq + (long long)kvh * p.G + r % p.G;
+    }
+  };
 
   const uint32_t q_s = smem_u32(smem), k_s = q_s + kRows * D * 2, v_s = k_s + 2 * KEYS * D * 2;
   int* ok_s = reinterpret_cast<int*>(smem + (kRows + 4 * KEYS) * D * 2);
@@ -92,18 +114,19 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const __grid_constant_
     const int r = i / CH, ch = i % CH;
     uint4 x = make_uint4(0u, 0u, 0u, 0u);
     if (r0 + r < live_rows) {
-      const int t = (int)((r0 + r) / p.G), h = (int)((r0 + r) % p.G);
-      const uint4* src = reinterpret_cast<const uint4*>(
-          p.q + (((long long)b * p.num_new + t) * p.Hq + (long long)kvh * p.G + h) * D) + ch;
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + row_at(r0 + r) * D) + ch;
       if (KVQ_IN(c, KVQ_ARRAY_Q, src, 16)) x = *src;
     }
     *reinterpret_cast<uint4*>(smem + at<D>(r, ch)) = x;
   }
 
   // the tile's last row sees positions below `end`
-  const int all_see = sp.L ? sp.before + (int)(r0 / p.G) : -1;  // every row sees the positions up to here
-  const int t_last = (int)((min(r0 + kRows, live_rows) - 1) / p.G);
-  const int end = sp.L ? min(sp.L, sp.before + t_last + 1) : 0;
+  int all_see = 0x7fffffff, end = sp.L;  // every row sees the positions up to all_see
+  if constexpr (!PRE) {
+    const int t_last = (int)((min(r0 + kRows, live_rows) - 1) / p.G);
+    all_see = sp.L ? sp.before + (int)(r0 / p.G) : -1;
+    end = sp.L ? min(sp.L, sp.before + t_last + 1) : 0;
+  }
   const int k0 = split * p.chunk, k1 = min(end, k0 + p.chunk);
 
   float o[D / 8][4];
@@ -115,7 +138,7 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const __grid_constant_
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const long long r = r0 + warp * 16 + (lane >> 2) + 8 * e;
-    last[e] = r < live_rows ? sp.before + (int)(r / p.G) : -1;
+    last[e] = r >= live_rows ? -1 : PRE ? 0x7fffffff : sp.before + (int)(r / p.G);
   }
 
   int turn = 0;
@@ -235,9 +258,8 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const __grid_constant_
     l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
     const long long r = r0 + warp * 16 + (lane >> 2) + 8 * e;
     if (r >= live_rows) continue;
-    const int t = (int)(r / p.G), h = (int)(r % p.G);
-    const long long orow = ((long long)b * p.num_new + t) * p.Hq + (long long)kvh * p.G + h;
-    if (p.splits == 1) {
+    const long long orow = row_at(r);
+    if (!PRE && p.ws_o == nullptr) {
       const float inv = l[e] != 0.f ? 1.f / l[e] : 0.f;
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) {
@@ -255,6 +277,15 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const __grid_constant_
       if ((lane & 3) == 0 && KVQ_IN(c, KVQ_ARRAY_WORKSPACE, ml, 8)) *ml = make_float2(m[e], l[e]);
     }
   }
+}
+
+template <int BITS, int D>
+__global__ void __launch_bounds__(kThreads) extend_kernel(const __grid_constant__ ExtendParams p) {
+  attend<BITS, D, false>(p);
+}
+template <int BITS, int D>
+__global__ void __launch_bounds__(kThreads) prefix_kernel(const __grid_constant__ ExtendParams p) {
+  attend<BITS, D, true>(p);
 }
 
 // out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s of each live row
@@ -315,39 +346,43 @@ __global__ void __launch_bounds__(256) extend_merge_kernel(const __grid_constant
     *to = make_uint2(fast::pack_h2(num.x * inv, num.y * inv), fast::pack_h2(num.z * inv, num.w * inv));
 }
 
-template <int BITS, int D>
+template <int BITS, int D, bool PRE>
 cudaError_t run(const ExtendParams* p, ExtendPlan* plan, cudaStream_t stream) {
+  void (*const kernel)(ExtendParams) = PRE ? prefix_kernel<BITS, D> : extend_kernel<BITS, D>;
   static KernelSetup setup;
   int occ = 0;
-  cudaError_t e = setup_kernel(extend_kernel<BITS, D>, setup, kThreads, extend_smem(D), &occ);
+  cudaError_t e = setup_kernel(kernel, setup, kThreads, extend_smem(D), &occ);
   if (e != cudaSuccess) return e;
   if (plan) {
     plan->tile_rows = kRows;
     plan->occ = occ;
+    plan->lift = kLift;
     return cudaSuccess;
   }
-  const long long tiles = ((long long)p->num_new * p->G + kRows - 1) / kRows;
-  const dim3 grid((unsigned)(tiles * p->splits), p->v.geom.Hkv, p->batch);
-  return launch_pdl(extend_kernel<BITS, D>, grid, dim3(kThreads), extend_smem(D), stream, *p);
+  const long long each = (long long)p->num_new * p->G;
+  const long long tiles = PRE ? prefix_tiles_bound(p->plan.B, p->plan.N, each, kRows) : (each + kRows - 1) / kRows;
+  const dim3 grid((unsigned)(tiles * p->splits), p->v.geom.Hkv, PRE ? 1 : p->batch);
+  return launch_pdl(kernel, grid, dim3(kThreads), extend_smem(D), stream, *p);
 }
 
 // Axis-aware caches are INT4 or INT8; of the other formats only head_dim 256
 // comes here.
-template <int BITS>
+template <int BITS, bool PRE>
 cudaError_t run_d(int D, const ExtendParams* p, ExtendPlan* plan, cudaStream_t stream) {
   if constexpr (BITS == 4 || BITS == 8) {
-    if (D == 64) return run<BITS, 64>(p, plan, stream);
-    if (D == 128) return run<BITS, 128>(p, plan, stream);
+    if (D == 64) return run<BITS, 64, PRE>(p, plan, stream);
+    if (D == 128) return run<BITS, 128, PRE>(p, plan, stream);
   }
-  return D == 256 ? run<BITS, 256>(p, plan, stream) : cudaErrorInvalidValue;
+  return D == 256 ? run<BITS, 256, PRE>(p, plan, stream) : cudaErrorInvalidValue;
 }
 
+template <bool PRE>
 cudaError_t run_any(const CacheGeom& c, const ExtendParams* p, ExtendPlan* plan, cudaStream_t stream) {
   switch (c.bits) {
-    case 2: return run_d<2>(c.D, p, plan, stream);
-    case 4: return run_d<4>(c.D, p, plan, stream);
-    case 8: return run_d<8>(c.D, p, plan, stream);
-    default: return run_d<16>(c.D, p, plan, stream);
+    case 2: return run_d<2, PRE>(c.D, p, plan, stream);
+    case 4: return run_d<4, PRE>(c.D, p, plan, stream);
+    case 8: return run_d<8, PRE>(c.D, p, plan, stream);
+    default: return run_d<16, PRE>(c.D, p, plan, stream);
   }
 }
 
@@ -368,15 +403,40 @@ static cudaError_t run_tc_any(const CacheGeom& c, int nq, const ExtendParams* p,
   }
 }
 
+static cudaError_t run_prefix_any(const CacheGeom& c, int nq, const ExtendParams* p, ExtendPlan* plan, cudaStream_t s) {
+  if (c.nf4) return run_prefix_tc_nf4(c.D, nq, p, plan, s);
+  switch (c.bits) {
+    case 2: return run_prefix_tc_int2(c.D, nq, p, plan, s);
+    case 4: return run_prefix_tc_int4(c.D, nq, p, plan, s);
+    case 8: return run_prefix_tc_int8(c.D, nq, p, plan, s);
+    default: return run_prefix_tc_fp16(c.D, nq, p, plan, s);
+  }
+}
+
 cudaError_t extend_plan(const CacheGeom& c, int num_new, int G, ExtendPlan* plan) {
   plan->kind = !takes_tc(c) ? 0 : (long long)num_new * G <= 128 ? 1 : 2;
-  if (plan->kind == 0) return run_any(c, nullptr, plan, nullptr);
+  if (plan->kind == 0) return run_any<false>(c, nullptr, plan, nullptr);
   return run_tc_any(c, plan->kind, nullptr, plan, nullptr);
 }
 
+cudaError_t extend_prefix_plan(const CacheGeom& c, long long rows, ExtendPlan* plan) {
+  plan->kind = !takes_tc(c) ? 0 : rows <= 128 ? 1 : 2;
+  if (plan->kind == 0) return run_any<true>(c, nullptr, plan, nullptr);
+  return run_prefix_any(c, plan->kind, nullptr, plan, nullptr);
+}
+
+cudaError_t launch_extend_prefix(const ExtendParams& p, const ExtendPlan& plan, cudaStream_t stream) {
+  return plan.kind == 0 ? run_any<true>(p.v.geom, &p, nullptr, stream)
+                        : run_prefix_any(p.v.geom, plan.kind, &p, nullptr, stream);
+}
+
+cudaError_t launch_extend_partials(const ExtendParams& p, const ExtendPlan& plan, cudaStream_t stream) {
+  return plan.kind == 0 ? run_any<false>(p.v.geom, &p, nullptr, stream)
+                        : run_tc_any(p.v.geom, plan.kind, &p, nullptr, stream);
+}
+
 cudaError_t launch_extend(const ExtendParams& p, const ExtendPlan& plan, cudaStream_t stream) {
-  cudaError_t e = plan.kind == 0 ? run_any(p.v.geom, &p, nullptr, stream)
-                                 : run_tc_any(p.v.geom, plan.kind, &p, nullptr, stream);
+  cudaError_t e = launch_extend_partials(p, plan, stream);
   if (e == cudaSuccess && p.splits > 1) {
     const long long rows = (long long)p.batch * p.num_new * p.Hq;
     const int per = 256 / (p.v.geom.D / 4);

@@ -347,7 +347,9 @@ __device__ __forceinline__ bool nonfinite2(uint32_t w) {
 
 // ---- the kernel -------------------------------------------------------
 
-template <int BITS, int KIND, int D, int NQ>
+// PRE: over shared prefixes (rows of all members of a prefix, which see all of
+// its keys; partials only).
+template <int BITS, int KIND, int D, int NQ, bool PRE>
 __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
     extend_tc_kernel(const __grid_constant__ ExtendParams p) {
   using C = Cfg<BITS, KIND, D, NQ>;
@@ -358,27 +360,53 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
   auto& sh = *reinterpret_cast<Shared<C::STAGES>*>(smem + C::STAGES * C::STAGE + C::DEPTH * C::RAW + C::Q_BYTES);
   const CacheGeom& c = p.v.geom;
   const int warp = tc::uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int kvh = blockIdx.y, b = blockIdx.z;
+  const int kvh = blockIdx.y;
   const int split = blockIdx.x % p.splits;
-  // row tiles last first: with a causal mask they see the most keys
-  const int tile = gridDim.x / p.splits - 1 - blockIdx.x / p.splits;
   pdl_wait();
 
-  const int before = tc::uniform(checked_len(c, p.lens_before, b, -1));
-  const int n_raw = tc::uniform(new_rows_of(p.new_lens, b, p.num_new));
-  const int n = max(n_raw, 0);
-  const bool fits = before >= 0 && n_raw >= 0 && (long long)before + n <= p.len_limit;
-  if (!fits && threadIdx.x == 0 && blockIdx.x == 0 && kvh == 0 && p.status) atomicOr(p.status, KVQ_FLAG_SEQ_LEN);
-  const long long live_rows = (long long)n * p.G;
-  const long long r0 = (long long)tile * ROWS;
-  if (r0 >= live_rows) return;
-  const int L = fits ? before + n : 0;
-  const int t_first = (int)(r0 / p.G);
-  const int t_last = (int)((min(r0 + ROWS, live_rows) - 1) / p.G);
-  const int end = L ? before + t_last + 1 : 0;
+  int b, before, end, all_see;  // all_see: every row sees the positions up to here
+  int first = 0;                // (PRE) the prefix's first member
+  long long live_rows, r0;
+  if constexpr (PRE) {
+    const PrefixTile pt = prefix_tile(p.plan, blockIdx.x / p.splits, p.num_new * p.G, ROWS);
+    b = tc::uniform(pt.n);
+    if (b < 0) return;
+    end = tc::uniform(prefix_len(p.plan, b, p.len_limit));
+    if (split * p.chunk >= end) return;  // the join knows which splits hold keys
+    first = tc::uniform(pt.first);
+    live_rows = (long long)tc::uniform(pt.count) * p.num_new * p.G;
+    r0 = (long long)tc::uniform(pt.tile) * ROWS;
+    before = all_see = 0x7fffffff;
+  } else {
+    // row tiles last first: with a causal mask they see the most keys
+    const int tile = gridDim.x / p.splits - 1 - blockIdx.x / p.splits;
+    b = blockIdx.z;
+    before = tc::uniform(checked_len(c, p.lens_before, b, -1));
+    const int n_raw = tc::uniform(new_rows_of(p.new_lens, b, p.num_new));
+    const int n = max(n_raw, 0);
+    const bool fits = before >= 0 && n_raw >= 0 && (long long)before + n <= p.len_limit;
+    if (!fits && threadIdx.x == 0 && blockIdx.x == 0 && kvh == 0 && p.status) atomicOr(p.status, KVQ_FLAG_SEQ_LEN);
+    live_rows = (long long)n * p.G;
+    r0 = (long long)tile * ROWS;
+    if (r0 >= live_rows) return;
+    const int L = fits ? before + n : 0;
+    const int t_first = (int)(r0 / p.G);
+    const int t_last = (int)((min(r0 + ROWS, live_rows) - 1) / p.G);
+    end = L ? before + t_last + 1 : 0;
+    all_see = L ? before + t_first : -1;
+  }
   const int k0 = split * p.chunk, k1 = min(end, k0 + p.chunk);
   const int tiles = k1 > k0 ? (k1 - k0 + kKeys - 1) / kKeys : 0;
-  const int all_see = L ? before + t_first : -1;  // every row sees the positions up to here
+  // row r of the tile in q, out and the partials
+  auto row_at = [&](int r) -> long long {
+    if constexpr (PRE) {
+      const int each = p.num_new * p.G, m = r / each, x = r - m * each, t = x / p.G;
+      return ((long long)plan_member(p.plan, first + m) * p.num_new + t) * p.Hq + (long long)kvh * p.G + (x - t * p.G);
+    } else {
+      const int t = r / p.G;
+      return ((long long)b * p.num_new + t) * p.Hq + (long long)kvh * p.G + (r - t * p.G);
+    }
+  };
   const int nq = (!C::DUAL && live_rows - r0 <= 128) ? 1 : 2;  // tiles of rows, or streams
 
   static_assert(sizeof(Shared<C::STAGES>) <= 2048, "room behind the stages");
@@ -470,10 +498,9 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
     const uint32_t ts0 = tmem + lanes + C::COL_S + i * C::SB * kKeys;
     const uint32_t to = tmem + lanes + C::COL_O + i * D;
     const uint32_t tq = tmem + lanes + C::COL_Q + i * (D / 2);
-    const int t = live ? r / p.G : 0;
-    const long long orow = ((long long)b * p.num_new + t) * p.Hq + (long long)kvh * p.G + (live ? r % p.G : 0);
+    const long long orow = row_at(live ? r : 0);
     // (rows behind the last take part with q = 0 and are not written)
-    const int last = live ? before + t : 0x7fffffff;
+    const int last = live && !PRE ? before + r / p.G : 0x7fffffff;
     const int mine = C::DUAL ? (tiles + 1 - i) / 2 : tiles;  // this stream's key tiles
     if (i < nq && mine) {
       // q to tensor memory, channels in the order the keys are unpacked in: 64
@@ -485,9 +512,8 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
       uint4 x[D / 64][8];
 #pragma unroll
       for (int it = 0; it < 8; ++it) {  // (all loads, then the stores)
-        const int row = min(row0 + it * 4 + (lane >> 3), (int)live_rows - 1), t2 = row / p.G;
-        const uint4* src = reinterpret_cast<const uint4*>(
-            p.q + (((long long)b * p.num_new + t2) * p.Hq + (long long)kvh * p.G + (row - t2 * p.G)) * D) + (lane & 7);
+        const int row = min(row0 + it * 4 + (lane >> 3), (int)live_rows - 1);
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + row_at(row) * D) + (lane & 7);
 #pragma unroll
         for (int h = 0; h < D / 64; ++h)
           x[h][it] = KVQ_IN(c, KVQ_ARRAY_Q, src + h * 8, 16) ? __ldg(src + h * 8) : make_uint4(0u, 0u, 0u, 0u);
@@ -701,7 +727,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
 #pragma unroll
         for (int e = 0; e < 32; ++e) x[(e & ~7) + C::channel(e & 7)] = __uint_as_float(o[e]);
         // through the scratch, so that lanes write whole lines of a row
-        const bool halves = p.splits == 1;
+        const bool halves = !PRE && p.ws_o == nullptr;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           if (halves && e >= 4) continue;
@@ -733,7 +759,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
         }
         __syncwarp();
       }
-      if (p.splits > 1 && live) {
+      if ((PRE || p.ws_o != nullptr) && live) {
         float2* ml = reinterpret_cast<float2*>(p.ws_ml) + orow * p.splits + split;
         if (KVQ_IN(c, KVQ_ARRAY_WORKSPACE, ml, 8)) *ml = make_float2(m, l);
       }
@@ -1083,28 +1109,31 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
   }
 }
 
-template <int BITS, int KIND, int D, int NQ>
+template <int BITS, int KIND, int D, int NQ, bool PRE>
 cudaError_t run_nq(const ExtendParams* p, ExtendPlan* plan, cudaStream_t stream) {
   using C = Cfg<BITS, KIND, D, NQ>;
   static KernelSetup setup;
   int occ = 0;
-  const cudaError_t e = setup_kernel(extend_tc_kernel<BITS, KIND, D, NQ>, setup, C::THREADS, C::SMEM, &occ);
+  const cudaError_t e = setup_kernel(extend_tc_kernel<BITS, KIND, D, NQ, PRE>, setup, C::THREADS, C::SMEM, &occ);
   if (e != cudaSuccess) return e;
   if (plan) {
     plan->tile_rows = 128 * NQ;
     plan->occ = occ;
+    plan->lift = kLift;
     return cudaSuccess;
   }
-  const long long tiles = ((long long)p->num_new * p->G + 128 * NQ - 1) / (128 * NQ);
-  const dim3 grid((unsigned)(tiles * p->splits), p->v.geom.Hkv, p->batch);
-  return launch_pdl(extend_tc_kernel<BITS, KIND, D, NQ>, grid, dim3(C::THREADS), C::SMEM, stream, *p);
+  const long long each = (long long)p->num_new * p->G;
+  const long long tiles = PRE ? prefix_tiles_bound(p->plan.B, p->plan.N, each, 128 * NQ) : (each + 128 * NQ - 1) / (128 * NQ);
+  const dim3 grid((unsigned)(tiles * p->splits), p->v.geom.Hkv, PRE ? 1 : p->batch);
+  return launch_pdl(extend_tc_kernel<BITS, KIND, D, NQ, PRE>, grid, dim3(C::THREADS), C::SMEM, stream, *p);
 }
 
-// One instance file per format calls this for its BITS and KIND.
-template <int BITS, int KIND>
+// Two instance files per format call this for its BITS and KIND.
+template <int BITS, int KIND, bool PRE = false>
 cudaError_t run_tc(int D, int nq, const ExtendParams* p, ExtendPlan* plan, cudaStream_t stream) {
-  if (D == 64) return nq == 1 ? run_nq<BITS, KIND, 64, 1>(p, plan, stream) : run_nq<BITS, KIND, 64, 2>(p, plan, stream);
-  return nq == 1 ? run_nq<BITS, KIND, 128, 1>(p, plan, stream) : run_nq<BITS, KIND, 128, 2>(p, plan, stream);
+  if (D == 64)
+    return nq == 1 ? run_nq<BITS, KIND, 64, 1, PRE>(p, plan, stream) : run_nq<BITS, KIND, 64, 2, PRE>(p, plan, stream);
+  return nq == 1 ? run_nq<BITS, KIND, 128, 1, PRE>(p, plan, stream) : run_nq<BITS, KIND, 128, 2, PRE>(p, plan, stream);
 }
 
 }  // namespace ext
@@ -1114,5 +1143,10 @@ cudaError_t run_extend_tc_int4(int D, int nq, const ExtendParams* p, ExtendPlan*
 cudaError_t run_extend_tc_int8(int D, int nq, const ExtendParams* p, ExtendPlan* plan, cudaStream_t stream);
 cudaError_t run_extend_tc_nf4(int D, int nq, const ExtendParams* p, ExtendPlan* plan, cudaStream_t stream);
 cudaError_t run_extend_tc_fp16(int D, int nq, const ExtendParams* p, ExtendPlan* plan, cudaStream_t stream);
+cudaError_t run_prefix_tc_int2(int D, int nq, const ExtendParams* p, ExtendPlan* plan, cudaStream_t stream);
+cudaError_t run_prefix_tc_int4(int D, int nq, const ExtendParams* p, ExtendPlan* plan, cudaStream_t stream);
+cudaError_t run_prefix_tc_int8(int D, int nq, const ExtendParams* p, ExtendPlan* plan, cudaStream_t stream);
+cudaError_t run_prefix_tc_nf4(int D, int nq, const ExtendParams* p, ExtendPlan* plan, cudaStream_t stream);
+cudaError_t run_prefix_tc_fp16(int D, int nq, const ExtendParams* p, ExtendPlan* plan, cudaStream_t stream);
 
 }  // namespace kvq

@@ -164,8 +164,8 @@ struct DecodeParams {
   const __half* q;          // [batch][Hq][D]
   const int32_t* seq_lens;  // [batch]
   __half* out;              // [batch][Hq][D]
-  float* ws_o;              // [batch][Hq][splits][D]     (splits > 1)
-  float* ws_ml;             // [batch][Hq][splits][2]      (splits > 1)
+  float* ws_o;              // [batch][Hq][splits][D]  (null: one split, written to out)
+  float* ws_ml;             // [batch][Hq][splits][2]
   uint32_t* status;
   int32_t batch;
   int32_t Hq;
@@ -195,6 +195,11 @@ struct DecodeParams {
   // partial, a split past the sequence's end the marker m = -inf, so the
   // merge reads all splits without the lengths
   int32_t merge_all;
+  // The tails of sequences with a shared prefix: seq_lens counts the tokens
+  // before len_add new ones (1; 0: seq_lens is what is attended), or before
+  // tail_new[b] of them where tail_new is set
+  int32_t len_add;
+  const int32_t* tail_new;
 };
 
 // lens[b] (a length array of the call), or `bad` when a debug build finds the
@@ -209,7 +214,10 @@ __device__ __forceinline__ int seq_len_of(const DecodeParams& p, int b) {
     const int x = checked_len(p.geom, p.lens_before, b, -1);
     return (x < 0 || x == 0x7fffffff) ? -1 : x + 1;
   }
-  return checked_len(p.geom, p.seq_lens, b, -1);
+  const int x = checked_len(p.geom, p.seq_lens, b, -1);
+  if (p.len_add == 0) return x;
+  const int n = p.tail_new ? __ldg(p.tail_new + b) : p.len_add;
+  return (x < 0 || x == 0x7fffffff || n < 0 || n > p.len_add) ? -1 : x + n;
 }
 
 // The sequence of rank r in a longest-first order of the batch: sequences

@@ -7,6 +7,7 @@
 #pragma once
 
 #include "kvq_internal.cuh"
+#include "kvq_prefix.cuh"
 
 namespace kvq {
 
@@ -143,13 +144,17 @@ struct ExtendParams {
   __half* out;
   const int32_t* lens_before;
   const int32_t* new_lens;
-  float* ws_o;   // [batch * num_new * Hq][splits][D]  (splits > 1)
+  float* ws_o;   // [batch * num_new * Hq][splits][D]  (null: one split, written to out)
   float* ws_ml;  // [batch * num_new * Hq][splits][2]
   uint32_t* status;
   int32_t batch, num_new, Hq, G;
   int32_t splits, chunk;  // chunk: positions per split, a multiple of kChunkAlign
   int32_t len_limit;
   float scale_log2;
+  // Attention over shared prefixes (launch_extend_prefix): the cache's sequences
+  // are the plan's prefixes, and a row of the tile is a (member, new token, head)
+  // triple of one of them; lens_before, new_lens and out are not used.
+  PrefixPlan plan;
 };
 
 // Which kernel takes the call, the rows of a CTA's tile (query token x head
@@ -158,8 +163,14 @@ struct ExtendPlan {
   int tile_rows = 0;
   int occ = 0;
   int kind = 0;  // 0: mma.sync kernel, 1 / 2: tensor-core kernel with that many 128-row tiles a CTA
+  float lift = 0.f;  // log2 of the factor in the partials' sums
 };
 cudaError_t extend_plan(const CacheGeom& c, int num_new, int G, ExtendPlan* plan);
 cudaError_t launch_extend(const ExtendParams& p, const ExtendPlan& plan, cudaStream_t stream);
+// The same without the merge of its splits: partials are left in ws_o, ws_ml.
+cudaError_t launch_extend_partials(const ExtendParams& p, const ExtendPlan& plan, cudaStream_t stream);
+// Over shared prefixes; rows: of a prefix's members together, on average.
+cudaError_t extend_prefix_plan(const CacheGeom& c, long long rows, ExtendPlan* plan);
+cudaError_t launch_extend_prefix(const ExtendParams& p, const ExtendPlan& plan, cudaStream_t stream);
 
 }  // namespace kvq

@@ -1,0 +1,351 @@
+// Shared prefixes: the plan of a batch, the prefixes that a page pool's table
+// holds, and the join of prefix and tail attention.
+#include "kvq_decode_fast.cuh"
+#include "kvq_prefix.cuh"
+#include "kvq_rope.cuh"
+
+namespace kvq {
+namespace {
+
+__device__ __forceinline__ void flag(uint32_t* status, uint32_t f) {
+  if (f && status) atomicOr(status, f);
+}
+__device__ __forceinline__ unsigned lanes_below() { return (1u << (threadIdx.x & 31)) - 1u; }
+
+// ---- the plan ----------------------------------------------------------
+//
+// A warp per prefix (and one more for the sequences without): it counts the
+// sequences of the prefixes before its own, then writes its own in ascending
+// order.  Integer sums and one writer an entry, so the plan is determined by
+// the inputs.  Bound by latency: two passes over B entries from the L2 cache.
+constexpr int kPlanWarps = 8;
+__device__ __forceinline__ int prefix_of(const PrefixPlanParams& p, int b, uint32_t& flags) {
+  const int n = __ldg(p.of + b);
+  if (n >= -1 && n < p.N) return n;
+  flags |= KVQ_FLAG_BLOCK_TABLE;
+  return -1;
+}
+__global__ void __launch_bounds__(kPlanWarps * 32) prefix_plan_kernel(const __grid_constant__ PrefixPlanParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int n = blockIdx.x * kPlanWarps + (threadIdx.x >> 5);  // N: the sequences without a prefix
+  if (n > p.N) return;
+  int32_t* const of = p.plan;
+  int32_t* const order = of + plan_pad(p.B);
+  int32_t* const first = order + plan_pad(p.B);
+  int32_t* const len = first + plan_pad(p.N + 1);
+  uint32_t flags = 0;
+  int before = 0;
+#pragma unroll 4
+  for (int b = lane; b < p.B; b += 32) {
+    const int x = prefix_of(p, b, flags);
+    before += x >= 0 && x < n;
+  }
+  before = __reduce_add_sync(0xffffffffu, before);
+  if (lane == 0) {
+    first[n] = before;
+    if (n < p.N) {
+      int l = __ldg(p.len + n);
+      if (l < 0) flags |= KVQ_FLAG_SEQ_LEN, l = 0;
+      len[n] = l;
+    }
+  }
+  const int mine = n < p.N ? n : -1;
+#pragma unroll 4
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int b = b0 + lane;
+    uint32_t unused = 0;
+    const bool hit = b < p.B && prefix_of(p, b, unused) == mine;
+    const unsigned m = __ballot_sync(0xffffffffu, hit);
+    if (hit) {
+      order[before + __popc(m & lanes_below())] = b;
+      of[b] = mine;
+    }
+    before += __popc(m);
+  }
+  flag(p.status, flags);
+}
+
+// ---- prefixes in a page pool's table -------------------------------------
+
+constexpr int kFindWarps = 32;
+constexpr int kFindKeys = 4096;  // keys held in shared memory at a time
+
+__device__ __forceinline__ bool is_page(const kvq_page_pool& pl, int e) { return e >= 0 && e < pl.num_pages; }
+
+// Whole blocks of sequence b (0 for a length that cannot be), flagged.
+__device__ __forceinline__ int whole_blocks(const PrefixFindParams& p, int b, uint32_t& flags) {
+  const kvq_page_pool& pl = p.pool;
+  const int L = __ldg(p.lens + b);
+  if (L < 0 || (long long)L > (long long)pl.page_size * pl.max_blocks_per_seq) {
+    flags |= KVQ_FLAG_SEQ_LEN;
+    return 0;
+  }
+  return L / pl.page_size;
+}
+// What candidates share: the page in block depth - 1; -1: no candidate.
+__device__ __forceinline__ int key_of(const PrefixFindParams& p, int b) {
+  uint32_t unused = 0;
+  if (whole_blocks(p, b, unused) < p.depth) return -1;
+  const int e = __ldg(p.pool.block_table + (long long)b * p.pool.max_blocks_per_seq + p.depth - 1);
+  return is_page(p.pool, e) ? e : -1;
+}
+
+struct FindSpace {
+  unsigned long long* best;  // [B] of a leader: (blocks saved) (M + 1) + run
+  int32_t* leader;           // [B], -1: member of no group
+  int32_t* run;              // [B]
+};
+__device__ __forceinline__ FindSpace space_of(const PrefixFindParams& p) {
+  FindSpace s;
+  s.best = p.best;
+  s.leader = reinterpret_cast<int32_t*>(p.best + p.pool.batch);
+  s.run = s.leader + p.pool.batch;
+  return s;
+}
+
+// A warp per sequence: its leader (lowest sequence with the same key) and how
+// many leading blocks it shares with it.
+__global__ void __launch_bounds__(kFindWarps * 32) find_leaders_kernel(const __grid_constant__ PrefixFindParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  __shared__ int keys[kFindKeys];
+  const kvq_page_pool& pl = p.pool;
+  const int B = pl.batch, M = pl.max_blocks_per_seq;
+  const int lane = threadIdx.x & 31;
+  const int b = blockIdx.x * kFindWarps + (threadIdx.x >> 5);
+  const int last = min(B, (int)(blockIdx.x + 1) * kFindWarps);  // no leader lies behind its members
+  int own = -1, lead = b;
+  if (b < B) own = key_of(p, b);
+  bool found = false;
+  for (int base = 0; base < last; base += kFindKeys) {
+    const int n = min(kFindKeys, last - base);
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += blockDim.x) keys[i] = key_of(p, base + i);
+    __syncthreads();
+    for (int i = 0; own >= 0 && !found && i < n; i += 32) {
+      const unsigned m = __ballot_sync(0xffffffffu, i + lane < n && keys[i + lane] == own);
+      if (m) {
+        lead = base + i + __ffs(m) - 1;  // (at the latest the sequence itself)
+        found = true;
+      }
+    }
+  }
+  if (b >= B) return;
+  const FindSpace s = space_of(p);
+  uint32_t flags = 0, unused = 0;
+  const int whole = whole_blocks(p, b, flags);
+  int run = 0;
+  if (own >= 0) {
+    const int most = min(whole, whole_blocks(p, lead, unused));
+    const int32_t* x = pl.block_table + (long long)b * M;
+    const int32_t* y = pl.block_table + (long long)lead * M;
+    run = most;
+    for (int j0 = 0; j0 < most; j0 += 128) {  // four loads of each in flight
+      int e[4], f[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int j = j0 + 32 * u + lane;
+        e[u] = j < most ? __ldg(x + j) : 0;
+        f[u] = j < most ? __ldg(y + j) : 0;
+      }
+      int stop = most;
+#pragma unroll
+      for (int u = 3; u >= 0; --u) {
+        const int j = j0 + 32 * u + lane;
+        const unsigned m = __ballot_sync(0xffffffffu, j < most && (e[u] != f[u] || !is_page(pl, e[u])));
+        if (m) stop = j0 + 32 * u + __ffs(m) - 1;
+      }
+      if (stop < most) {
+        run = stop;
+        break;
+      }
+    }
+  }
+  if (lane == 0) {
+    s.leader[b] = run >= p.depth ? lead : -1;
+    s.run[b] = run;
+    s.best[b] = 0;
+    flag(p.status, flags);
+  }
+}
+
+// A warp per sequence: what its run would save as the group's prefix.
+__global__ void __launch_bounds__(kFindWarps * 32) find_savings_kernel(const __grid_constant__ PrefixFindParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int B = p.pool.batch;
+  const int lane = threadIdx.x & 31;
+  const int b = blockIdx.x * kFindWarps + (threadIdx.x >> 5);
+  if (b >= B) return;
+  const FindSpace s = space_of(p);
+  const int lead = s.leader[b], run = s.run[b];
+  if (lead < 0) return;
+  int with = 0;  // members with at least this run
+#pragma unroll 4
+  for (int i = lead + lane; i < B; i += 32) with += s.leader[i] == lead && s.run[i] >= run;
+  with = __reduce_add_sync(0xffffffffu, with);
+  if (lane == 0 && with > 1)
+    atomicMax(s.best + lead, (unsigned long long)(with - 1) * run * (unsigned)(p.pool.max_blocks_per_seq + 1u) + run);
+}
+
+// Copies n entries of a table row, -1 behind, by one warp.
+__device__ __forceinline__ void copy_row(const int32_t* from, int n, int32_t* to, int M, int lane) {
+  for (int j0 = 0; j0 < M; j0 += 128) {
+    int e[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int j = j0 + 32 * u + lane;
+      e[u] = j < n ? __ldg(from + j) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int j = j0 + 32 * u + lane;
+      if (j < M) to[j] = e[u];
+    }
+  }
+}
+
+// A warp per sequence (its prefix and its tail's row) and per prefix (its row).
+__global__ void __launch_bounds__(kFindWarps * 32) find_tables_kernel(const __grid_constant__ PrefixFindParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const kvq_page_pool& pl = p.pool;
+  const int B = pl.batch, M = pl.max_blocks_per_seq;
+  const int lane = threadIdx.x & 31;
+  const long long w = (long long)blockIdx.x * kFindWarps + (threadIdx.x >> 5);
+  const FindSpace s = space_of(p);
+  const unsigned base = (unsigned)M + 1u;
+  if (w < B) {
+    const int b = (int)w, lead = s.leader[b];
+    const int prefix = lead < 0 ? 0 : (int)(s.best[lead] % base);
+    int n = -1;
+    if (prefix > 0 && s.run[b] >= prefix) {
+      int before = 0;  // groups with a lower leader
+#pragma unroll 4
+      for (int i = lane; i < lead; i += 32) before += s.best[i] != 0;
+      before = __reduce_add_sync(0xffffffffu, before);
+      if (before < p.most) n = before;
+    }
+    const int shift = n >= 0 ? prefix : 0;
+    if (lane == 0) {
+      p.of[b] = n;
+      p.tail_lens[b] = __ldg(p.lens + b) - shift * pl.page_size;
+    }
+    copy_row(pl.block_table + (long long)b * M + shift, M - shift, p.tail_table + (long long)b * M, M, lane);
+  } else if (w < (long long)B + p.most) {
+    const int n = (int)(w - B);
+    int lead = -1, groups = 0;
+    for (int i0 = 0; i0 < B; i0 += 32) {
+      const unsigned m = __ballot_sync(0xffffffffu, i0 + lane < B && s.best[min(i0 + lane, B - 1)] != 0);
+      const int here = __popc(m);
+      if (lead < 0 && groups + here > n) lead = i0 + (int)__fns(m, 0, n - groups + 1);
+      groups += here;
+      if (lead >= 0 && !(n == 0 && p.num)) break;
+    }
+    const int prefix = lead < 0 ? 0 : (int)(s.best[lead] % base);
+    if (lane == 0) {
+      p.len[n] = prefix * pl.page_size;
+      if (n == 0 && p.num) *p.num = groups;
+    }
+    copy_row(pl.block_table + (long long)max(lead, 0) * M, prefix, p.prefix_table + (long long)n * M, M, lane);
+  }
+}
+
+// ---- the join -----------------------------------------------------------
+//
+// out = sum_i 2^(m_i - lift_i - X) o_i / sum_i 2^(m_i - lift_i - X) l_i over the
+// partials of a row, X their largest m - lift.  D / 4 threads a row, four
+// channels each, kJoin partials in flight.
+constexpr int kJoin = 4;
+__global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant__ PrefixJoinParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const CacheGeom& c = p.geom;
+  // prefixes that do not fit, whether a sequence is on them or not
+  for (long long n = (long long)blockIdx.x * 256 + threadIdx.x; n < p.plan.N; n += (long long)gridDim.x * 256)
+    if (__ldg(p.plan.len + n) > p.prefix_limit) flag(p.status, KVQ_FLAG_SEQ_LEN);
+  const int per = p.D / 4;  // 16, 32 or 64
+  const long long row = (long long)blockIdx.x * (256 / per) + threadIdx.x / per;
+  if (row >= (long long)p.plan.B * p.T * p.Hq) return;
+  const long long tok = row / p.Hq;
+  const int b = (int)(tok / p.T), t = (int)(tok - (long long)b * p.T);
+  const int n_new = new_rows_of(p.new_lens, b, p.T);
+  if (t >= n_new) return;
+  const int before = checked_len(c, p.tail_before, b, -1);
+  const bool fits = before >= 0 && (long long)before + n_new <= p.tail_limit;
+  int use[2] = {0, fits ? (before + n_new + p.part[1].chunk - 1) / p.part[1].chunk : 0};
+  const int n = __ldg(p.plan.of + b);
+  const int d = threadIdx.x % per * 4;
+  if (fits && n >= 0 && n < p.plan.N)
+    use[0] = (prefix_len(p.plan, n, p.prefix_limit) + p.part[0].chunk - 1) / p.part[0].chunk;
+  float M = -INFINITY, den = 0.f;
+  float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int total = use[0] + use[1];
+  for (int s0 = 0; s0 < total; s0 += kJoin) {
+    float2 v[kJoin];
+    float4 x[kJoin];
+    float Mn = M;
+#pragma unroll
+    for (int u = 0; u < kJoin; ++u) {
+      const int i = s0 + u, w = i >= use[0];
+      const PrefixPartials& part = p.part[w];
+      const long long at = row * part.splits + (w ? i - use[0] : i);
+      v[u] = make_float2(-INFINITY, 0.f);
+      x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < total && KVQ_IN(c, KVQ_ARRAY_WORKSPACE, part.ml + 2 * at, 8) &&
+          KVQ_IN(c, KVQ_ARRAY_WORKSPACE, part.o + at * p.D + d, 16)) {
+        v[u] = *reinterpret_cast<const float2*>(part.ml + 2 * at);
+        v[u].x -= part.lift;
+        x[u] = *reinterpret_cast<const float4*>(part.o + at * p.D + d);
+      }
+      Mn = fmaxf(Mn, v[u].x);
+    }
+    const float base = Mn == -INFINITY ? 0.f : Mn, a = fast::ex2(M - base);
+    num = make_float4(num.x * a, num.y * a, num.z * a, num.w * a);
+    den *= a;
+#pragma unroll
+    for (int u = 0; u < kJoin; ++u) {
+      if (v[u].x == -INFINITY && !(v[u].y != 0.f)) continue;  // nothing seen there
+      const float f = fast::ex2(v[u].x - base);
+      num.x = fmaf(f, x[u].x, num.x);
+      num.y = fmaf(f, x[u].y, num.y);
+      num.z = fmaf(f, x[u].z, num.z);
+      num.w = fmaf(f, x[u].w, num.w);
+      den = fmaf(f, v[u].y, den);
+    }
+    M = Mn;
+  }
+  const float inv = den != 0.f ? 1.f / den : 0.f;
+  uint2* to = reinterpret_cast<uint2*>(p.out + row * p.D + d);
+  if (KVQ_IN(c, KVQ_ARRAY_OUT, to, 8))
+    *to = make_uint2(fast::pack_h2(num.x * inv, num.y * inv), fast::pack_h2(num.z * inv, num.w * inv));
+}
+
+}  // namespace
+
+cudaError_t launch_prefix_plan(const PrefixPlanParams& p, cudaStream_t stream) {
+  const long long warps = (long long)p.N + 1;
+  return launch_pdl(prefix_plan_kernel, dim3((unsigned)((warps + kPlanWarps - 1) / kPlanWarps)), dim3(kPlanWarps * 32),
+                    0, stream, p);
+}
+
+cudaError_t launch_prefix_find(const PrefixFindParams& p, cudaStream_t stream) {
+  const auto grid = [](long long warps) { return dim3((unsigned)((warps + kFindWarps - 1) / kFindWarps)); };
+  const int B = p.pool.batch;
+  cudaError_t e = cudaSuccess;
+  if (B > 0) e = launch_pdl(find_leaders_kernel, grid(B), dim3(kFindWarps * 32), 0, stream, p);
+  if (e == cudaSuccess && B > 0) e = launch_pdl(find_savings_kernel, grid(B), dim3(kFindWarps * 32), 0, stream, p);
+  if (e == cudaSuccess)
+    e = launch_pdl(find_tables_kernel, grid((long long)B + p.most), dim3(kFindWarps * 32), 0, stream, p);
+  return e;
+}
+
+cudaError_t launch_prefix_join(const PrefixJoinParams& p, cudaStream_t stream) {
+  const long long rows = (long long)p.plan.B * p.T * p.Hq;
+  const int per = 256 / (p.D / 4);
+  return launch_pdl(prefix_join_kernel, dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0, stream, p);
+}
+
+}  // namespace kvq

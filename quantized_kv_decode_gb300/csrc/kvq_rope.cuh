@@ -236,7 +236,17 @@ struct RopeAppendParams {
   RopeParams r;  // q (Hq = 0: none); k unused
 };
 
+// Several axes: pair i turns by at[token][axis[i]]; the cache rows of an
+// append still follow r.seq_lens_before.
+struct RopeAxesParams : RopeAppendParams {
+  const int32_t* at;  // [batch][num_new][num_axes]
+  int32_t num_axes;
+  uint8_t axis[KVQ_ROPE_MAX_PAIRS];
+};
+
 cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream);
 cudaError_t launch_rope_append(const RopeAppendParams& p, cudaStream_t stream);
+cudaError_t launch_rope_axes(const RopeAxesParams& p, cudaStream_t stream);
+cudaError_t launch_rope_axes_append(const RopeAxesParams& p, cudaStream_t stream);
 
 }  // namespace kvq

@@ -18,7 +18,7 @@ from operator import attrgetter
 import torch
 
 from . import _lib
-from ._lib import ROPE_SCALING, kvq_page_pool, kvq_rope, kvq_rope_desc
+from ._lib import ROPE_SCALING, kvq_page_pool, kvq_rope, kvq_rope_axes, kvq_rope_axes_desc, kvq_rope_desc
 from .api import KVCache, _ptr
 
 
@@ -112,14 +112,39 @@ def make_rope(rotary_dim: int, base: float = 10000.0, interleaved: bool = False,
     """A rotation for kvq_rope_apply / kvq_rope_append.  scaling: "none",
     "linear", "ntk", "bands" or "yarn" (see kvq_rope_scaling in kvq.h); a 0
     for low_turns, high_turns or amplitude takes the scaling's default."""
-    if scaling not in ROPE_SCALING:
-        raise ValueError(f"scaling must be one of {', '.join(ROPE_SCALING)}")
-    desc = kvq_rope_desc(int(rotary_dim), int(bool(interleaved)), ROPE_SCALING[scaling],
-                         int(original_context), float(base), float(factor), float(low_turns),
-                         float(high_turns), float(amplitude))
+    desc = _rope_desc(rotary_dim, base, interleaved, scaling, factor, original_context, low_turns, high_turns,
+                      amplitude)
     rope = kvq_rope()
     _lib.check(_lib.lib().kvq_rope_init(byref(desc), byref(rope)), "kvq_rope_init")
     return rope
+
+
+def _rope_desc(rotary_dim, base, interleaved, scaling, factor, original_context, low_turns, high_turns, amplitude):
+    if scaling not in ROPE_SCALING:
+        raise ValueError(f"scaling must be one of {', '.join(ROPE_SCALING)}")
+    return kvq_rope_desc(int(rotary_dim), int(bool(interleaved)), ROPE_SCALING[scaling],
+                         int(original_context), float(base), float(factor), float(low_turns),
+                         float(high_turns), float(amplitude))
+
+
+def make_rope_axes(pairs, cycled: bool = False, own_ladders: bool = False, base: float = 10000.0,
+                   interleaved: bool = False, scaling: str = "none", factor: float = 1.0,
+                   original_context: int = 0, low_turns: float = 0.0, high_turns: float = 0.0,
+                   amplitude: float = 0.0) -> kvq_rope_axes:
+    """A rotation by len(pairs) axes (time, height and width, say), pairs[a] of
+    the channel pairs turning by the position on axis a: one axis after another
+    or, cycled, in turns; own_ladders restarts the frequencies for each axis
+    (see kvq_rope_axes_desc in kvq.h).  The rest as for make_rope."""
+    pairs = [int(n) for n in pairs]
+    if not 1 <= len(pairs) <= _lib.KVQ_ROPE_MAX_AXES:
+        raise ValueError(f"a rotation has 1 to {_lib.KVQ_ROPE_MAX_AXES} axes")
+    desc = kvq_rope_axes_desc(_rope_desc(2 * sum(pairs), base, interleaved, scaling, factor, original_context,
+                                         low_turns, high_turns, amplitude), len(pairs))
+    desc.pairs[:len(pairs)] = pairs
+    desc.cycled, desc.own_ladders = int(bool(cycled)), int(bool(own_ladders))
+    axes = kvq_rope_axes()
+    _lib.check(_lib.lib().kvq_rope_axes_init(byref(desc), byref(axes)), "kvq_rope_axes_init")
+    return axes
 
 
 def kvq_rope_apply(rope: kvq_rope, q: torch.Tensor | None = None, k: torch.Tensor | None = None,
@@ -193,6 +218,73 @@ def kvq_rope_append(cache: KVCache, rope: kvq_rope, k_new: torch.Tensor, v_new: 
             0 if q is None else q.shape[2], _ptr(q), _ptr(q_out), _ptr(seq_lens_before),
             _ptr(new_lens), _ptr(dev_status), _handle(dev))
     _lib.check(st, "kvq_rope_append")
+    return q_out
+
+
+def kvq_rope_axes_apply(axes: kvq_rope_axes, positions: torch.Tensor, q: torch.Tensor | None = None,
+                        k: torch.Tensor | None = None, new_lens: torch.Tensor | None = None,
+                        q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None,
+                        dev_status: torch.Tensor | None = None, stream=None):
+    """Rotate q [B][T][Hq][D] and / or k [B][T][Hk][D] fp16 by positions
+    [B][T][axes]; returns (q_out, k_out).  The rest as kvq_rope_apply."""
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("q or k must be given")
+    _check(x, torch.float16, "q" if q is not None else "k", (None,) * 4, None)
+    B, T, _, D = x.shape
+    dev = x.get_device()
+    _check(positions, torch.int32, "positions", (B, T, axes.num_axes), dev)
+    _optional(new_lens, torch.int32, "new_lens", (B,), dev)
+    _status(dev_status, dev)
+    for t, o, name in ((q, q_out, "q"), (k, k_out, "k")):
+        if t is not None:
+            _check(t, torch.float16, name, (B, T, None, D), dev)
+            if o is not None:
+                _check(o, torch.float16, name + "_out", t.shape, dev)
+        elif o is not None:
+            raise ValueError(f"{name}_out without {name}")
+    with _on(dev, stream):
+        outs = [o if t is None or o is not None else _made_like(t, new_lens)
+                for t, o in ((q, q_out), (k, k_out))]
+        st = _lib.lib().kvq_rope_axes_apply(
+            byref(axes), D, B, T, 0 if q is None else q.shape[2], _ptr(q), _ptr(outs[0]),
+            0 if k is None else k.shape[2], _ptr(k), _ptr(outs[1]), _ptr(positions), _ptr(new_lens),
+            _ptr(dev_status), _handle(dev))
+    _lib.check(st, "kvq_rope_axes_apply")
+    return outs[0], outs[1]
+
+
+def kvq_rope_axes_append(cache: KVCache, axes: kvq_rope_axes, positions: torch.Tensor, k_new: torch.Tensor,
+                         v_new: torch.Tensor, seq_lens_before: torch.Tensor, q: torch.Tensor | None = None,
+                         q_out: torch.Tensor | None = None, new_lens: torch.Tensor | None = None,
+                         dev_status: torch.Tensor | None = None, stream=None):
+    """kvq_rope_append with the angles of positions [B][T][axes]; the tokens go
+    to the cache's positions seq_lens_before[b] + t.  Returns q_out."""
+    d = cache.desc
+    _check(k_new, torch.float16, "k_new", (None, None, d.num_kv_heads, d.head_dim), None)
+    B, T, _, D = k_new.shape
+    dev = k_new.get_device()
+    _check(positions, torch.int32, "positions", (B, T, axes.num_axes), dev)
+    _check(v_new, torch.float16, "v_new", k_new.shape, dev)
+    _check(seq_lens_before, torch.int32, "seq_lens_before", (B,), dev)
+    _optional(new_lens, torch.int32, "new_lens", (B,), dev)
+    _same_cache_device(cache, dev)
+    _batch(cache, B)
+    _status(dev_status, dev)
+    if q is not None:
+        _check(q, torch.float16, "q", (B, T, None, D), dev)
+        if q_out is not None:
+            _check(q_out, torch.float16, "q_out", q.shape, dev)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    with _on(dev, stream):
+        if q is not None and q_out is None:
+            q_out = _made_like(q, new_lens)
+        st = _lib.lib().kvq_rope_axes_append(
+            byref(d), byref(cache.ptrs), byref(axes), B, T, _ptr(k_new), _ptr(v_new),
+            0 if q is None else q.shape[2], _ptr(q), _ptr(q_out), _ptr(positions), _ptr(seq_lens_before),
+            _ptr(new_lens), _ptr(dev_status), _handle(dev))
+    _lib.check(st, "kvq_rope_axes_append")
     return q_out
 
 
