@@ -29,12 +29,9 @@ def __getattr__(name):
     # the torch-facing API is imported lazily so that the input generators and
     # the ctypes layer can be used without importing torch
     if name in __all__:
-        from . import api
-        if hasattr(api, name):
-            return getattr(api, name)
-        from . import prompt
-        if hasattr(prompt, name):
-            return getattr(prompt, name)
-        from . import prefix
-        return getattr(prefix, name)
+        from . import api, prefix, prompt
+        for module in (api, prompt, prefix):
+            if hasattr(module, name):
+                # (found at once from now on: a call looks its function up by name)
+                return globals().setdefault(name, getattr(module, name))
     raise AttributeError(name)

@@ -341,6 +341,14 @@ void dbg_extent(CacheGeom& g, int array, const void* base, size_t bytes) {
 #endif
 }
 
+static cudaError_t launch_decode_one(const DecodeParams& p, int gp, cudaStream_t s, bool* handled, int* occ) {
+  if (p.geom.bits == 2) return launch_decode_one_int2(p, gp, s, handled, occ);
+  if (p.geom.nf4) return launch_decode_one_nf4(p, gp, s, handled, occ);
+  if (p.geom.bits == 4)
+    return p.geom.sym ? launch_decode_one_int4_sym(p, gp, s, handled, occ) : launch_decode_one_int4(p, gp, s, handled, occ);
+  return p.geom.sym ? launch_decode_one_int8_sym(p, gp, s, handled, occ) : launch_decode_one_int8(p, gp, s, handled, occ);
+}
+
 kvq_status tail_decode_plan(const kvq_cache_desc* desc, const CacheGeom& geom, int32_t batch, int32_t num_q_heads,
                             int32_t max_len, int32_t requested, TailDecode* t) {
   const int G = num_q_heads / desc->num_kv_heads;
@@ -358,15 +366,34 @@ kvq_status tail_decode_plan(const kvq_cache_desc* desc, const CacheGeom& geom, i
   }
   if (!t->takes) return KVQ_OK;
   Plan plan;
-  const kvq_status st = make_plan(desc, geom, batch, num_q_heads, max_len, requested, &plan);
+  plan.splits = 1;
+  // The tail kernel: contexts that need no splits.  Up to 2048 tokens that holds
+  // for any batch: 4 sequences, 8 KV heads, INT4, tails of 64, 512, 2048 tokens
+  // behind 1024 shared ones: 10.9, 10.9, 20.3 us against 17.3, 18.7, 21.3 with
+  // splits, partials and the join; 256 sequences 32, 56, 111 against 60, 81, 135.
+  const bool shorts = desc->bits != 16 && requested == 0 && max_len <= 2048;
+  if (!shorts) {
+    const kvq_status st = make_plan(desc, geom, batch, num_q_heads, max_len, requested, &plan);
+    if (st != KVQ_OK) return st;
+  }
   t->splits = plan.splits;
-  return st;
+  t->one = desc->bits != 16 && requested == 0 && plan.splits == 1;
+  // Its warps a (sequence, KV head): as many as have room at once (8 an SM), more
+  // where contexts are long enough to be worth a second turn.  256 sequences of 2
+  // KV heads (head_dim 64, INT8), 1, 2, 4 warps: tails of 256 tokens 16.6, 21.0,
+  // 20.6 us, of 2048 58, 45, 34; 256 of 8 KV heads (INT4): 41.6, 43.0, 53.3 and 126,
+  // 111, 121; 32 sequences of 8: 18.7, 17.5, 17.2 and 62, 41, 24.5.
+  const int64_t units = (int64_t)batch * desc->num_kv_heads, room = (int64_t)sm_count() * 8;
+  if (units * 4 <= room || (units * 2 <= room && max_len > 600)) t->wpu = 4;
+  else t->wpu = units * 2 <= room || max_len > (units <= room ? 384 : 768) ? 2 : 1;
+  return KVQ_OK;
 }
 
 cudaError_t tail_decode(const kvq_cache_desc* desc, const kvq_cache* cache, const CacheGeom& geom, int32_t batch,
                         int32_t num_q_heads, const uint16_t* q, const int32_t* before, const int32_t* new_lens,
                         int32_t max_len, const TailDecode& t, float scale_log2, float* ws_o, float* ws_ml,
-                        const void* ws, size_t ws_bytes, uint32_t* status, cudaStream_t stream) {
+                        const void* ws, size_t ws_bytes, uint32_t* status, cudaStream_t stream,
+                        const PrefixJoin& join, uint16_t* out) {
   DecodeParams p{};
   p.geom = geom;
   p.geom.block_table = cache->block_table;
@@ -394,7 +421,15 @@ cudaError_t tail_decode(const kvq_cache_desc* desc, const kvq_cache* cache, cons
   p.scale_log2 = scale_log2;
   p.rows32 = desc->layout == KVQ_PAGED &&
              (int64_t)desc->num_pages * desc->num_kv_heads * desc->capacity * geom.row_bytes < ((int64_t)1 << 31);
-  dbg_fill(p.geom, desc, cache, batch, num_q_heads, 0, q, nullptr, nullptr, before, nullptr, ws, ws_bytes, status);
+  dbg_fill(p.geom, desc, cache, batch, num_q_heads, 0, q, nullptr, nullptr, before, out, ws, ws_bytes, status);
+  if (t.one) {
+    p.join = join;
+    p.join.wpu = t.wpu;
+    p.out = reinterpret_cast<__half*>(out);
+    bool handled = false;
+    const cudaError_t e = launch_decode_one(p, t.gp, stream, &handled, nullptr);
+    return handled ? e : cudaErrorInvalidValue;
+  }
   if (desc->bits == 16) return launch_decode_generic(p, stream);  // (the fp16 tensor-core kernel)
   // longest first where the grid has more than one wave, as in a decode call
   p.longest_first = t.occ > 0 && batch > 1 && batch <= kLongestFirstMaxBatch &&

@@ -33,6 +33,43 @@ struct PrefixChoice {
   size_t prefix_bytes = 0, tail_bytes = 0;
 };
 
+// Splits of the prefix pass, and what the call then costs in ns.  A block takes
+// kFixed keys' time beside its own; blocks run in whole turns over the device;
+// the partials are written and read at 6800 bytes a ns.  The tail kernel
+// (tail_warps of them, eight an SM, with tail_keys each) runs beside the pass
+// where that leaves room, and behind it where not.  Fitted to sweeps of 8 to 256
+// rows over prefixes of 512 to 16384 tokens (head_dim 64 and 128, INT4, INT8).
+int32_t prefix_splits(const ExtendPlan& plan, int64_t units, int64_t max_len, int64_t rows, int64_t D, int requested,
+                      int64_t tail_warps, int64_t tail_keys, double* cost) {
+  static const double kNs[5] = {40, 16, 20, 24, 30};  // a key, by plan.kind
+  static const double kFixed[5] = {200, 550, 650, 128, 128};
+  const int64_t L = std::max<int64_t>(max_len, 1);
+  const int sms = sm_count(), occ = std::max(plan.occ, 1);
+  const int64_t slots = (int64_t)std::max(sms, 1) * occ, cap = std::min<int64_t>(ceil_div(L, 128), 64);
+  if (requested > 0) {
+    requested = choose_splits(units, L, requested, 0);
+  } else if (sms <= 0) {
+    return 0;
+  }
+  // an SM holds eight tail warps
+  const double turns = ceil((double)tail_warps / (8.0 * std::max(sms, 1)));
+  const double tail = tail_warps ? turns * (2000.0 + 30.0 * tail_keys) : 0.0;
+  int32_t best = 0;
+  *cost = 1e300;
+  for (int64_t s = requested > 0 ? requested : 1; s <= (requested > 0 ? requested : cap); ++s) {
+    const int64_t chunk = split_chunk(L, (int32_t)s), eff = ceil_div(L, chunk), n = std::max<int64_t>(units, 1) * eff;
+    const double pass = ceil((double)n / slots) * (chunk + kFixed[plan.kind]) * kNs[plan.kind];
+    // (SMs without a block of the pass: on the others the two would share it)
+    const double beside = n >= sms || tail_warps == 0 ? 0.0 : std::min(1.0, (sms - n) * 8.0 / tail_warps);
+    const double t = std::max(pass, tail) + (1.0 - beside) * std::min(pass, tail) + rows * D * 8.0 * eff / 6800.0;
+    if (t < *cost * 0.999) {
+      *cost = t;
+      best = (int32_t)eff;
+    }
+  }
+  return best;
+}
+
 kvq_status choose(const kvq_cache_desc* pd, const kvq_cache_desc* d, int32_t N, int32_t B, int32_t T, int32_t Hq,
                   int32_t max_prefix, int32_t max_len, int32_t want_prefix, int32_t want_tail, PrefixChoice* c) {
   kvq_status st = check_desc(d, &c->tg);
@@ -60,17 +97,28 @@ kvq_status choose(const kvq_cache_desc* pd, const kvq_cache_desc* d, int32_t N, 
     if (tiles * c->tail_splits > INT32_MAX) return KVQ_ERR_UNSUPPORTED;
   }
   if (c->tail_splits <= 0) return KVQ_ERR_CUDA;
-  c->tail_bytes = partial_bytes(rows, D, c->tail_splits);
+  c->tail_bytes = c->decode.one ? 0 : partial_bytes(rows, D, c->tail_splits);
   c->prefixes = N > 0 && max_prefix > 0;
   if (c->prefixes) {
     const int32_t used = std::min(N, B);
-    const cudaError_t e = extend_prefix_plan(c->pg, ceil_div(B * each, used), &c->pre);
-    if (e != cudaSuccess) return from_cuda(e);
-    // (a prefix's members fill their tiles on average; the bound counts a part
-    // of a tile more for each prefix)
-    const int64_t tiles = std::max<int64_t>(used, ceil_div(B * each, c->pre.tile_rows));
-    c->prefix_splits =
-        choose_extend_splits(tiles * d->num_kv_heads, max_prefix, rows, D, false, want_prefix, c->pre);
+    const int64_t per_prefix = ceil_div(B * each, used);
+    double best = 1e300;
+    for (int few = 0; few <= (extend_prefix_few(c->pg) ? 1 : 0); ++few) {
+      ExtendPlan plan;
+      const cudaError_t e = extend_prefix_plan(c->pg, per_prefix, few, &plan);
+      if (e != cudaSuccess) return from_cuda(e);
+      // (members are taken to be shared out evenly; the grid has room for any way)
+      const int64_t units = used * ceil_div(per_prefix, plan.tile_rows) * d->num_kv_heads;
+      const int64_t tail_warps = c->decode.one ? (int64_t)B * d->num_kv_heads * c->decode.wpu : 0;
+      double cost = 0;
+      const int32_t splits = prefix_splits(plan, units, max_prefix, rows, D, want_prefix, tail_warps,
+                                           c->decode.one ? max_len / c->decode.wpu : 0, &cost);
+      if (splits > 0 && cost < best) {
+        best = cost;
+        c->pre = plan;
+        c->prefix_splits = splits;
+      }
+    }
     if (c->prefix_splits <= 0) return KVQ_ERR_CUDA;
     if (prefix_tiles_bound(B, N, each, c->pre.tile_rows) * c->prefix_splits > INT32_MAX) return KVQ_ERR_UNSUPPORTED;
     c->prefix_bytes = partial_bytes(rows, D, c->prefix_splits);
@@ -181,15 +229,15 @@ kvq_status kvq_prefix_attn(const kvq_cache_desc* prefix_desc, const kvq_cache* p
   const size_t bytes = (size_t)rows * desc->head_dim * 2;
   if (q == out || partly_over(q, out, bytes)) return KVQ_ERR_INVALID_ARG;
   const size_t need = c.prefix_bytes + c.tail_bytes;
-  if (!workspace || workspace_size < need || !aligned(workspace)) return KVQ_ERR_WORKSPACE;
+  if (need && (!workspace || workspace_size < need || !aligned(workspace))) return KVQ_ERR_WORKSPACE;
 
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int64_t D = desc->head_dim;
   const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf((float)desc->head_dim);
   const float scale_log2 = scale * 1.4426950408889634f;
-  float *po = nullptr, *pml = nullptr, *to, *tml;
+  float *po = nullptr, *pml = nullptr, *to = nullptr, *tml = nullptr;
   if (c.prefixes) carve_partials(workspace, rows, D, c.prefix_splits, &po, &pml);
-  carve_partials(reinterpret_cast<char*>(workspace) + c.prefix_bytes, rows, D, c.tail_splits, &to, &tml);
+  if (c.tail_bytes) carve_partials(reinterpret_cast<char*>(workspace) + c.prefix_bytes, rows, D, c.tail_splits, &to, &tml);
 
   ExtendParams p{};  // what both passes of extend attention share
   p.q = reinterpret_cast<const __half*>(q);
@@ -213,12 +261,26 @@ kvq_status kvq_prefix_attn(const kvq_cache_desc* prefix_desc, const kvq_cache* p
     x.splits = c.prefix_splits;
     x.chunk = split_chunk(max_prefix_len, c.prefix_splits);
     x.len_limit = prefix_limit = (int32_t)std::min<int64_t>(cache_capacity(c.pg), max_prefix_len);
+    x.new_lens = new_lens;
     x.plan = pl;
     if ((e = launch_extend_prefix(x, c.pre, s)) != cudaSuccess) return from_cuda(e);
   }
+  const int32_t splits = std::max(c.prefix_splits, 1), chunk = split_chunk(max_prefix_len, splits);  // of the prefixes
   if (c.decode.takes) {
+    PrefixJoin j{};
+    j.o = po;
+    j.ml = pml;
+    j.of = pl.of;
+    j.len = pl.len;
+    j.N = num_prefixes;
+    j.splits = splits;
+    j.chunk = chunk;
+    j.limit = prefix_limit;
+    j.lift = c.pre.lift;
+    j.early = c.prefixes;
     e = tail_decode(desc, cache, c.tg, batch, num_q_heads, q, seq_lens_before, new_lens, max_seq_len, c.decode,
-                    scale_log2, to, tml, workspace, workspace_size, dev_status, s);
+                    scale_log2, to, tml, workspace, workspace_size, dev_status, s, j, out);
+    if (c.decode.one) return from_cuda(e);
   } else {
     ExtendParams x = p;
     x.v = view_of(c.tg, cache);
@@ -241,8 +303,7 @@ kvq_status kvq_prefix_attn(const kvq_cache_desc* prefix_desc, const kvq_cache* p
   dbg_fill(j.geom, desc, cache, batch, num_q_heads * num_new, 0, nullptr, nullptr, nullptr, seq_lens_before, out,
            workspace, workspace_size, dev_status);
   j.plan = pl;
-  j.part[0] = {po, pml, std::max(c.prefix_splits, 1), split_chunk(max_prefix_len, std::max(c.prefix_splits, 1)),
-               c.pre.lift};
+  j.part[0] = {po, pml, splits, chunk, c.pre.lift};
   j.part[1] = {to, tml, c.tail_splits, split_chunk(max_seq_len, c.tail_splits), c.decode.takes ? 0.f : c.tail.lift};
   j.out = reinterpret_cast<__half*>(out);
   j.tail_before = seq_lens_before;

@@ -31,6 +31,10 @@
 //    subtracted once at the end.
 //  * The warps' (m, l, o) are merged in shared memory; the CTA writes the
 //    final row (one split) or its partial for the merge kernel.
+//  * The tails of sequences with a shared prefix (ONE): one, two or four warps
+//    take a (sequence, KV head), as many as leave all of them room at once, so
+//    that short contexts do not queue for a CTA each; they join their rows with
+//    the prefix's partials and write them out.
 //  * Fused append (lens_before set): the CTA holding the new position
 //    quantizes the new K/V in one warp, stores them, and merges the token as
 //    one more partial; its tiles stop before that position.
@@ -301,9 +305,11 @@ __device__ __forceinline__ uint32_t pack_halves(__half lo, __half hi) {
 // the CTA merge), the tile masks and the appended token's partial; NF4
 // instances then hold their score-side level table (kNfLutBytes, 16-byte
 // aligned).
-template <int BITS, int D, int NG, int GP, bool KCH>
+template <int BITS, int D, int NG, int GP, bool KCH, bool ONE = false>
 __host__ __device__ constexpr size_t fast_smem_bytes() {
   using C = Cfg<BITS, D, NG, GP, KCH>;
+  if (ONE)  // every warp's q; nothing merged or appended
+    return (size_t)kWarps * (((GP * D * 2 + 127) / 128) * 128 + C::WARP_BYTES) + ((kWarps * C::STAGES * 4 + 15) / 16) * 16;
   const size_t pipe = (size_t)kWarps * C::WARP_BYTES;
   const size_t masks = ((kWarps * C::STAGES * 4 + 15) / 16) * 16;
   const size_t newtok = (D + GP) * sizeof(float);
@@ -317,9 +323,9 @@ __host__ __device__ constexpr size_t fast_smem_bytes() {
 // bank for the same byte value.
 constexpr int kNfLutCopies = 8;
 constexpr size_t kNfLutBytes = 256 * kNfLutCopies * 4;
-template <int BITS, int D, int NG, int GP, bool KCH>
+template <int BITS, int D, int NG, int GP, bool KCH, bool ONE = false>
 __host__ __device__ constexpr size_t nf_lut_offset() {
-  return (fast_smem_bytes<BITS, D, NG, GP, KCH>() + 15) / 16 * 16;
+  return (fast_smem_bytes<BITS, D, NG, GP, KCH, ONE>() + 15) / 16 * 16;
 }
 
 // NF4 codes of one 32-bit word to their fp16 levels through that table,
@@ -337,14 +343,81 @@ __device__ __forceinline__ void nib8_to_h2_nf4_table(uint32_t w, uint32_t (&o)[4
   }
 }
 
+// The rows of a unit's wpu warps (each: o [GP][D], then (m, l) [GP], STRIDE floats
+// apart) joined with one another and with the partials of the sequence's prefix,
+// and written out: four channels a lane, the partials of four splits in flight.
+// live: the sequence's length is one that can be (else zeros).
+template <int D, int GP, int STRIDE>
+__device__ __forceinline__ void join_and_write(const DecodeParams& p, int b, long long row0, bool live, const float* red,
+                                               int sub, int wpu) {
+  const int lane = threadIdx.x & 31;
+  constexpr int PER = D / 4, ROWS = 32 / PER;  // lanes of a row, rows a pass (D = 64: 2)
+  const int d = lane % PER * 4;
+  const PrefixJoin& x = p.join;
+  const int n = live && x.N ? __ldg(x.of + b) : -1;
+  int splits = 0;
+  if (n >= 0 && n < x.N) {
+    const int len = __ldg(x.len + n);
+    splits = len > x.limit ? 0 : (max(len, 0) + x.chunk - 1) / x.chunk;
+  }
+  if (x.early) pdl_wait();
+  for (int h = sub * ROWS + lane / PER; h < p.G; h += wpu * ROWS) {
+    const long long row = row0 + h;
+    float M = -INFINITY, den = 0.f;
+    float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int w = 0; w < wpu && live; ++w) M = fmaxf(M, red[w * STRIDE + GP * D + 2 * h]);
+    for (int w = 0; w < wpu && M != -INFINITY; ++w) {
+      const float* from = red + w * STRIDE;
+      const float f = ex2(from[GP * D + 2 * h] - M);
+      const float4 y = *reinterpret_cast<const float4*>(from + h * D + d);
+      num = make_float4(fmaf(f, y.x, num.x), fmaf(f, y.y, num.y), fmaf(f, y.z, num.z), fmaf(f, y.w, num.w));
+      den = fmaf(f, from[GP * D + 2 * h + 1], den);
+    }
+    for (int s0 = 0; s0 < splits; s0 += 4) {
+      float2 v[4];
+      float4 y[4];
+      float Mn = M;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const long long at = row * x.splits + s0 + u;
+        v[u] = make_float2(-INFINITY, 0.f);
+        y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (s0 + u < splits && KVQ_IN(p.geom, KVQ_ARRAY_WORKSPACE, x.ml + 2 * at, 8) &&
+            KVQ_IN(p.geom, KVQ_ARRAY_WORKSPACE, x.o + at * D + d, 16)) {
+          v[u] = *reinterpret_cast<const float2*>(x.ml + 2 * at);
+          v[u].x -= x.lift;
+          y[u] = *reinterpret_cast<const float4*>(x.o + at * D + d);
+        }
+        Mn = fmaxf(Mn, v[u].x);
+      }
+      const float base = Mn == -INFINITY ? 0.f : Mn, a = ex2(M - base);
+      num = make_float4(num.x * a, num.y * a, num.z * a, num.w * a);
+      den *= a;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (v[u].x == -INFINITY && v[u].y == 0.f) continue;  // nothing seen there
+        const float f = ex2(v[u].x - base);
+        num = make_float4(fmaf(f, y[u].x, num.x), fmaf(f, y[u].y, num.y), fmaf(f, y[u].z, num.z), fmaf(f, y[u].w, num.w));
+        den = fmaf(f, v[u].y, den);
+      }
+      M = Mn;
+    }
+    const float inv = den != 0.f ? 1.f / den : 0.f;
+    uint2* to = reinterpret_cast<uint2*>(p.out + row * D + d);
+    if (KVQ_IN(p.geom, KVQ_ARRAY_OUT, to, 8))
+      *to = make_uint2(pack_h2(num.x * inv, num.y * inv), pack_h2(num.z * inv, num.w * inv));
+  }
+}
+
 // Threshold (log2 units) by which a head's tile maximum may exceed the
 // reference maximum before the accumulators are rescaled; probabilities are
 // bounded by 2^kSlack.
 constexpr float kSlack = 4.f;
 
-template <int BITS, int D, int NG, int GP, bool SYM, bool KCH, bool NF = false, bool PG = false>
-__global__ void __launch_bounds__(Cfg<BITS, D, NG, GP, KCH>::THREADS, Cfg<BITS, D, NG, GP, KCH>::MIN_CTAS)
+template <int BITS, int D, int NG, int GP, bool SYM, bool KCH, bool NF = false, bool PG = false, bool ONE = false>
+__global__ void __launch_bounds__(ONE ? kWarps * 32 : Cfg<BITS, D, NG, GP, KCH>::THREADS, Cfg<BITS, D, NG, GP, KCH>::MIN_CTAS)
     decode_fast_kernel(const DecodeParams p) {
+  static_assert(!ONE || !KCH, "ONE: per-token caches");
   // SYM: symmetric caches, no zero arrays; every zero-point is 2^(BITS-1).
   // NF: NF4 codes (with SYM: scale only), which stand for normal-quantile
   // levels; no offset to remove and no zero-point.
@@ -381,7 +454,7 @@ __global__ void __launch_bounds__(Cfg<BITS, D, NG, GP, KCH>::THREADS, Cfg<BITS, 
   // staged publishes it
   uint32_t nf_lut_lane = 0u;
   if constexpr (NF) {
-    uint32_t* t = reinterpret_cast<uint32_t*>(smem + nf_lut_offset<BITS, D, NG, GP, KCH>());
+    uint32_t* t = reinterpret_cast<uint32_t*>(smem + nf_lut_offset<BITS, D, NG, GP, KCH, ONE>());
     for (int i = threadIdx.x; i < 256 * kNfLutCopies; i += blockDim.x) {
       const int v = i / kNfLutCopies;
       t[i] = pack_halves(__float2half_rn(p.nf4_level[v & 15]), __float2half_rn(p.nf4_level[v >> 4]));
@@ -401,10 +474,19 @@ __global__ void __launch_bounds__(Cfg<BITS, D, NG, GP, KCH>::THREADS, Cfg<BITS, 
   // the q n-tile of k-block kb's group (TQ2), else 0
   auto qtile = [](int kb) { return TQ2 ? ((kb * 16) / C::GSZ) / (8 / GP) : 0; };
   const CacheGeom& geo = p.geom;
-  const int split = blockIdx.x, kvh = blockIdx.y;
-  const int G = p.G;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // ONE: the warps of a unit, and which of them this is (heads first: a block's
+  // contexts are of one length)
+  const int wpu = ONE ? p.join.wpu : kWarps, sub = ONE ? warp & (wpu - 1) : warp;
+  const int unit = ONE ? ((int)blockIdx.x * kWarps + warp) / wpu : 0;
+  const int split = ONE ? 0 : blockIdx.x, kvh = ONE ? unit % geo.Hkv : blockIdx.y;
+  const int G = p.G;
   const int rho = lane >> 2, j = lane & 3;
+  // the warps that work on one range
+  auto sync = [&] {
+    if constexpr (ONE) asm volatile("bar.sync %0, %1;\n" ::"r"(1 + warp / wpu), "r"(32 * wpu) : "memory");
+    else __syncthreads();
+  };
 
   // Launched with programmatic stream serialization: the next kernel of the
   // stream may start launching now.  Until the previous kernel has completed
@@ -414,7 +496,7 @@ __global__ void __launch_bounds__(Cfg<BITS, D, NG, GP, KCH>::THREADS, Cfg<BITS, 
   // read again after the wait, so a previous kernel that wrote them is still
   // seen.
   pdl_launch_dependents();
-  if constexpr (!KCH) {
+  if constexpr (!KCH && !ONE) {
     if (!p.longest_first && geo.layout == KVQ_DENSE && warp < kWarps && lane < C::STAGES * 6) {
       const int b = blockIdx.z;
       const int it = lane / 6, region = lane % 6;
@@ -439,7 +521,7 @@ __global__ void __launch_bounds__(Cfg<BITS, D, NG, GP, KCH>::THREADS, Cfg<BITS, 
   }
   // the CTA's q rows, for the fused step the new token's K and V rows, and
   // for axis-aware caches the unit's fp16 rows (sinks and residual window)
-  if (!p.longest_first && warp == 1 && lane < 5) {
+  if (!ONE && !p.longest_first && warp == 1 && lane < 5) {
     const int b = blockIdx.z;
     const void* src = nullptr;
     uint32_t bytes = 0;
@@ -464,7 +546,7 @@ __global__ void __launch_bounds__(Cfg<BITS, D, NG, GP, KCH>::THREADS, Cfg<BITS, 
   // CTAs cannot warm their own rows: the first three CTAs warm L2 with the
   // whole q array and the new K and V rows instead, in 32 slices each
   // (GQA mix 66.48 -> 66.06 us per fused call)
-  if (p.longest_first && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z < 3 && warp == 1) {
+  if (!ONE && p.longest_first && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z < 3 && warp == 1) {
     const int z = blockIdx.z;
     const void* base = z == 0 ? (const void*)p.q
                      : (p.lens_before != nullptr ? (const void*)p.new_kv[z - 1] : nullptr);
@@ -478,13 +560,26 @@ __global__ void __launch_bounds__(Cfg<BITS, D, NG, GP, KCH>::THREADS, Cfg<BITS, 
         prefetch_l2(from, (uint32_t)n);
     }
   }
-  pdl_wait();
+  // (ONE: behind the pass over the prefixes it starts at once and waits for that
+  // pass's partials before it joins them)
+  if (!ONE || !p.join.early) pdl_wait();
 
-  const int b = p.longest_first ? longest_first_seq(p, blockIdx.z, reinterpret_cast<int*>(smem))
-                                : (int)blockIdx.z;
+  const int b = ONE ? unit / geo.Hkv
+                    : p.longest_first ? longest_first_seq(p, blockIdx.z, reinterpret_cast<int*>(smem))
+                                      : (int)blockIdx.z;
+  if constexpr (ONE) {
+    if constexpr (NF) __syncthreads();  // the level table
+    // prefixes that do not fit, whether a sequence is on them or not
+    for (long long n = (long long)blockIdx.x * (kWarps * 32) + threadIdx.x; n < p.join.N; n += (long long)gridDim.x * (kWarps * 32))
+      if (__ldg(p.join.len + n) > p.join.limit && p.status) atomicOr(p.status, KVQ_FLAG_SEQ_LEN);
+    if (b >= p.batch || (p.tail_new && __ldg(p.tail_new + b) == 0)) {  // (no new token: its row stays)
+      if (p.join.early) pdl_wait();
+      return;
+    }
+  }
   int L = seq_len_of(p, b);
   if (L < 0 || L > p.len_limit) {
-    if (threadIdx.x == 0 && split == 0 && kvh == 0 && p.status) atomicOr(p.status, KVQ_FLAG_SEQ_LEN);
+    if ((ONE ? lane + sub : threadIdx.x) == 0 && split == 0 && kvh == 0 && p.status) atomicOr(p.status, KVQ_FLAG_SEQ_LEN);
     L = 0;
   }
   const int t0 = split * p.chunk;
@@ -512,8 +607,10 @@ __global__ void __launch_bounds__(Cfg<BITS, D, NG, GP, KCH>::THREADS, Cfg<BITS, 
 
   // shared memory: [q fp16 GP x D][per warp: stages, header scratch][tile
   // masks][the appended token's partial: v_hat fp32 [D], scores fp32 [GP]]
-  __half* q_s = reinterpret_cast<__half*>(smem);
-  uint8_t* pipe = smem + ((GP * D * 2 + 127) / 128) * 128;
+  // (ONE: q of every warp)
+  constexpr int QB = ((GP * D * 2 + 127) / 128) * 128;
+  __half* q_s = reinterpret_cast<__half*>(smem + (ONE ? (warp - sub) * QB : 0));
+  uint8_t* pipe = smem + (ONE ? kWarps : 1) * QB;
   uint32_t* mask_s = reinterpret_cast<uint32_t*>(pipe + kWarps * C::WARP_BYTES);
   float* tok_v = reinterpret_cast<float*>(pipe + kWarps * C::WARP_BYTES +
                                          ((kWarps * C::STAGES * 4 + 15) / 16) * 16);
@@ -528,8 +625,18 @@ __global__ void __launch_bounds__(Cfg<BITS, D, NG, GP, KCH>::THREADS, Cfg<BITS, 
   auto madd_of = [&](int buf) { return reinterpret_cast<float*>(vzx_of(buf) + NG * C::VROW); };
 
   const __half* qg = p.q + ((long long)b * p.Hq + (long long)kvh * G) * D;
-  for (int i = threadIdx.x; i < GP * D; i += blockDim.x)
-    q_s[i] = (i < G * D && KVQ_IN(geo, KVQ_ARRAY_Q, qg + i, 2)) ? qg[i] : __float2half_rn(0.f);
+  if constexpr (ONE) {
+#pragma unroll
+    for (int i = sub * 32 + lane; i < GP * D / 8; i += wpu * 32) {
+      const uint4* from = reinterpret_cast<const uint4*>(qg) + i;
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (i < G * D / 8 && KVQ_IN(geo, KVQ_ARRAY_Q, from, 16)) v = __ldg(from);
+      reinterpret_cast<uint4*>(q_s)[i] = v;
+    }
+  } else {
+    for (int i = threadIdx.x; i < GP * D; i += blockDim.x)
+      q_s[i] = (i < G * D && KVQ_IN(geo, KVQ_ARRAY_Q, qg + i, 2)) ? qg[i] : __float2half_rn(0.f);
+  }
   // Fused step on an axis-aware cache, one split: this CTA appends its
   // unit's new token (position L - 1) with the append kernel's code, so that
   // it reads the cache as the two-call step leaves it.  A token that
@@ -561,7 +668,7 @@ __global__ void __launch_bounds__(Cfg<BITS, D, NG, GP, KCH>::THREADS, Cfg<BITS, 
     }
   }
 
-  __syncthreads();
+  sync();
 
   // Fused append: in the CTA whose range holds the new position, the tiles
   // stop short of it.  One warp quantizes the new K and V vectors (the
@@ -570,7 +677,7 @@ __global__ void __launch_bounds__(Cfg<BITS, D, NG, GP, KCH>::THREADS, Cfg<BITS, 
   // 1, value v_hat) that the CTA merge adds to the warps' partials.  No read
   // of this launch touches the new row, so the store needs no ordering.
   const int pos_new = L - 1;
-  const bool owner_cta = !KCH && p.lens_before != nullptr && L > 0 && pos_new >= t0 && pos_new < t1;
+  const bool owner_cta = !KCH && !ONE && p.lens_before != nullptr && L > 0 && pos_new >= t0 && pos_new < t1;
   const int t_end = owner_cta ? t1 - 1 : t1;  // tiles cover [t0, t_end)
 
   // ---- score-mma A fragments: row r <-> (group r / GP, head r % GP); for
@@ -712,12 +819,13 @@ __global__ void __launch_bounds__(Cfg<BITS, D, NG, GP, KCH>::THREADS, Cfg<BITS, 
   constexpr int kSpill = 12;
   const int spill = (owner_cta && !C::AW) ? min(kSpill, ntiles) : 0;
   const int nrr = ntiles - spill;  // tiles [0, nrr) round-robin over all streaming warps
-  int nmine = (warp < kWarps && nrr > warp) ? (nrr - warp + kWarps - 1) / kWarps : 0;
+  int nmine = ONE ? (ntiles > sub ? (ntiles - sub + wpu - 1) / wpu : 0) : (warp < kWarps && nrr > warp) ? (nrr - warp + kWarps - 1) / kWarps : 0;
   const int srank = warp - (warp > owner_warp ? 1 : 0);  // rank among the non-owner warps
   if (spill && warp < kWarps && warp != owner_warp)
     nmine += (spill - srank + kWarps - 2) / (kWarps - 1);
   // the CTA tile this warp takes as its it-th
   auto tile_of = [&](int it) {
+    if constexpr (ONE) return sub + it * wpu;
     const int r = nrr > warp ? (nrr - warp + kWarps - 1) / kWarps : 0;
     return it < r ? warp + it * kWarps : nrr + srank + (it - r) * (kWarps - 1);
   };
@@ -1464,10 +1572,11 @@ __global__ void __launch_bounds__(Cfg<BITS, D, NG, GP, KCH>::THREADS, Cfg<BITS, 
   if (bt_bad && p.status) atomicOr(p.status, KVQ_FLAG_BLOCK_TABLE);
   l_run += __shfl_xor_sync(0xffffffffu, l_run, 1);
   l_run += __shfl_xor_sync(0xffffffffu, l_run, 2);
-  __syncthreads();  // every warp is done with its pipeline: reuse it for the merge
+  sync();  // every warp is done with its pipeline: reuse it for the merge
 
-  float* red = reinterpret_cast<float*>(pipe);                 // [warps][GP][D] o
-  float* ml = red + kWarps * GP * D;                            // [warps][GP][2]
+  // [warps][GP][D] o (ONE: this warp's own, in its pipeline)
+  float* red = reinterpret_cast<float*>(pipe) + (ONE ? warp * (C::WARP_BYTES / 4 - GP * D) : 0);
+  float* ml = ONE ? red + (warp + 1) * GP * D - warp * GP * 2 : red + kWarps * GP * D;  // [warps][GP][2]
 #pragma unroll
   for (int m = 0; m < C::MT; ++m) {
     // rows rho / rho + 8 of m-tile m: channels d0 / d0 + d1, held in units
@@ -1619,9 +1728,14 @@ __global__ void __launch_bounds__(Cfg<BITS, D, NG, GP, KCH>::THREADS, Cfg<BITS, 
       }
     }
   }
-  __syncthreads();
+  sync();
 
   const long long hq0 = (long long)b * p.Hq + (long long)kvh * G;
+  if constexpr (ONE) {
+    const float* first = reinterpret_cast<const float*>(pipe + (warp - sub) * C::WARP_BYTES);  // of the unit
+    join_and_write<D, GP, C::WARP_BYTES / 4>(p, b, hq0, L > 0, first, sub, wpu);
+    return;
+  }
   for (int i = threadIdx.x; i < G * D; i += blockDim.x) {
     const int h = i / D, d = i - h * D;
     float M = -INFINITY;
@@ -1698,6 +1812,20 @@ cudaError_t launch_fast_inst(const DecodeParams& p, cudaStream_t stream, int* ct
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, decode_fast_kernel<BITS, D, NG, GP, SYM, KCH, NF, PG>, p);
+}
+
+// The same for ONE: p.join.wpu warps a (sequence, KV head), one split.
+template <int BITS, int D, int NG, int GP, bool SYM, bool NF = false>
+cudaError_t launch_one_inst(const DecodeParams& p, cudaStream_t stream, int* ctas_per_sm) {
+  constexpr size_t smem = NF ? nf_lut_offset<BITS, D, NG, GP, false, true>() + kNfLutBytes
+                             : fast_smem_bytes<BITS, D, NG, GP, false, true>();
+  static KernelSetup setup;
+  const cudaError_t e =
+      setup_kernel(decode_fast_kernel<BITS, D, NG, GP, SYM, false, NF, false, true>, setup, kWarps * 32, smem, ctas_per_sm);
+  if (e != cudaSuccess || ctas_per_sm) return e;
+  const long long warps = (long long)p.batch * p.geom.Hkv * p.join.wpu;
+  return launch_pdl(decode_fast_kernel<BITS, D, NG, GP, SYM, false, NF, false, true>,
+                    dim3((unsigned)((warps + kWarps - 1) / kWarps)), dim3(kWarps * 32), smem, stream, p);
 }
 
 }  // namespace fast

@@ -71,23 +71,28 @@ __device__ __forceinline__ Span span_of(const ExtendParams& p, int b, bool repor
 template <int BITS, int D, bool PRE>
 __device__ __forceinline__ void attend(const ExtendParams& p) {
   constexpr int KEYS = tile_keys(D), CH = D / 8, KB = D / 16, NT = KEYS / 8;
-  pdl_launch_dependents();
+  if (!PRE) pdl_launch_dependents();
   pdl_wait();
+  if (PRE) pdl_launch_dependents();  // (a tail kernel starts without waiting for what came before)
   extern __shared__ __align__(128) uint8_t smem[];
   const CacheGeom& c = p.v.geom;
   const int kvh = blockIdx.y;
   const int split = blockIdx.x % p.splits;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int b = blockIdx.z, tile = blockIdx.x / p.splits, first = 0;
+  int b = blockIdx.z, tile = blockIdx.x / p.splits;
   long long live_rows;
+  __shared__ int toks[PRE ? kRows : 1];  // the tile's rows' tokens
   Span sp;
   if constexpr (PRE) {
     const PrefixTile pt = prefix_tile(p.plan, tile, p.num_new * p.G, kRows);
     if (pt.n < 0) return;
-    b = pt.n, tile = pt.tile, first = pt.first;
+    b = pt.n, tile = pt.tile;
     sp.L = prefix_len(p.plan, b, p.len_limit);
     if (split * p.chunk >= sp.L) return;
-    live_rows = (long long)pt.count * p.num_new * p.G;
+    int tok;
+    live_rows = prefix_rows(p.plan, pt, p.new_lens, p.num_new, p.G, (long long)tile * kRows + (warp & 1) * 32 + lane, &tok);
+    if (warp < 2) toks[warp * 32 + lane] = tok;
+    __syncthreads();
   } else {
     sp = span_of(p, b, threadIdx.x == 0 && blockIdx.x == 0 && kvh == 0);
     live_rows = (long long)sp.n * p.G;
@@ -97,8 +102,7 @@ __device__ __forceinline__ void attend(const ExtendParams& p) {
   // row r in q, out and the partials
   auto row_at = [&](long long r) -> long long {
     if constexpr (PRE) {
-      const int each = p.num_new * p.G, m = (int)(r / each), x = (int)(r - (long long)m * each);
-      return ((long long)plan_member(p.plan, first + m) * p.num_new + x / p.G) * p.Hq + (long long)kvh * p.G + x % p.G;
+      return (long long)toks[r - r0] * p.Hq + (long long)kvh * p.G + r % p.G;
     } else {
       return ((long long)b * p.num_new + r / p.G) * p.Hq + (long long)kvh * p.G + r % p.G;
     }
@@ -403,7 +407,18 @@ static cudaError_t run_tc_any(const CacheGeom& c, int nq, const ExtendParams* p,
   }
 }
 
-static cudaError_t run_prefix_any(const CacheGeom& c, int nq, const ExtendParams* p, ExtendPlan* plan, cudaStream_t s) {
+// The kernel for few rows takes INT4, NF4 and INT8 groups of 32 channels or more,
+// two or four of them to a row (headers of 4 or 8 bytes).
+static bool takes_rows(const CacheGeom& c) {
+  if (!takes_tc(c) || (c.bits != 4 && c.bits != 8)) return false;
+  return (c.ngroups == 2 || c.ngroups == 4) && c.g >= 32;
+}
+
+static cudaError_t run_prefix_any(const CacheGeom& c, int kind, const ExtendParams* p, ExtendPlan* plan, cudaStream_t s) {
+  if (kind >= 3)
+    return c.nf4 ? run_rows_nf4(c.D, kind - 2, p, plan, s)
+                 : c.bits == 4 ? run_rows_int4(c.D, kind - 2, p, plan, s) : run_rows_int8(c.D, kind - 2, p, plan, s);
+  const int nq = kind;
   if (c.nf4) return run_prefix_tc_nf4(c.D, nq, p, plan, s);
   switch (c.bits) {
     case 2: return run_prefix_tc_int2(c.D, nq, p, plan, s);
@@ -419,11 +434,13 @@ cudaError_t extend_plan(const CacheGeom& c, int num_new, int G, ExtendPlan* plan
   return run_tc_any(c, plan->kind, nullptr, plan, nullptr);
 }
 
-cudaError_t extend_prefix_plan(const CacheGeom& c, long long rows, ExtendPlan* plan) {
-  plan->kind = !takes_tc(c) ? 0 : rows <= 128 ? 1 : 2;
+cudaError_t extend_prefix_plan(const CacheGeom& c, long long rows, bool few, ExtendPlan* plan) {
+  plan->kind = !takes_tc(c) ? 0 : few ? (rows <= 16 ? 3 : 4) : rows <= 128 ? 1 : 2;
   if (plan->kind == 0) return run_any<true>(c, nullptr, plan, nullptr);
   return run_prefix_any(c, plan->kind, nullptr, plan, nullptr);
 }
+
+bool extend_prefix_few(const CacheGeom& c) { return takes_rows(c); }
 
 cudaError_t launch_extend_prefix(const ExtendParams& p, const ExtendPlan& plan, cudaStream_t stream) {
   return plan.kind == 0 ? run_any<true>(p.v.geom, &p, nullptr, stream)

@@ -354,7 +354,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
     extend_tc_kernel(const __grid_constant__ ExtendParams p) {
   using C = Cfg<BITS, KIND, D, NQ>;
   constexpr int ROWS = C::ROWS, STEP = C::DUAL ? 2 : 1;  // key tiles from one of a stream's to its next
-  pdl_launch_dependents();
+  if (!PRE) pdl_launch_dependents();
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + ((1024 - (tc::smem_addr(raw) & 1023)) & 1023);
   auto& sh = *reinterpret_cast<Shared<C::STAGES>*>(smem + C::STAGES * C::STAGE + C::DEPTH * C::RAW + C::Q_BYTES);
@@ -363,19 +363,23 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
   const int kvh = blockIdx.y;
   const int split = blockIdx.x % p.splits;
   pdl_wait();
+  if (PRE) pdl_launch_dependents();  // (a tail kernel starts without waiting for what came before)
 
   int b, before, end, all_see;  // all_see: every row sees the positions up to here
-  int first = 0;                // (PRE) the prefix's first member
+  PrefixTile pt{};              // (PRE)
+  int own_tok = 0;              // (PRE) the token of this lane's row of the tile
   long long live_rows, r0;
   if constexpr (PRE) {
-    const PrefixTile pt = prefix_tile(p.plan, blockIdx.x / p.splits, p.num_new * p.G, ROWS);
+    pt = prefix_tile(p.plan, blockIdx.x / p.splits, p.num_new * p.G, ROWS);
     b = tc::uniform(pt.n);
     if (b < 0) return;
     end = tc::uniform(prefix_len(p.plan, b, p.len_limit));
     if (split * p.chunk >= end) return;  // the join knows which splits hold keys
-    first = tc::uniform(pt.first);
-    live_rows = (long long)tc::uniform(pt.count) * p.num_new * p.G;
     r0 = (long long)tc::uniform(pt.tile) * ROWS;
+    const int soft = max(warp - C::SOFT0, 0) & 7;  // a softmax warp's rows
+    const long long own = r0 + (C::DUAL ? (soft & 3) : soft) * 32 + lane;
+    live_rows = tc::uniform(prefix_rows(p.plan, pt, p.new_lens, p.num_new, p.G, own, &own_tok));
+    if (r0 >= live_rows) return;
     before = all_see = 0x7fffffff;
   } else {
     // row tiles last first: with a causal mask they see the most keys
@@ -397,16 +401,6 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
   }
   const int k0 = split * p.chunk, k1 = min(end, k0 + p.chunk);
   const int tiles = k1 > k0 ? (k1 - k0 + kKeys - 1) / kKeys : 0;
-  // row r of the tile in q, out and the partials
-  auto row_at = [&](int r) -> long long {
-    if constexpr (PRE) {
-      const int each = p.num_new * p.G, m = r / each, x = r - m * each, t = x / p.G;
-      return ((long long)plan_member(p.plan, first + m) * p.num_new + t) * p.Hq + (long long)kvh * p.G + (x - t * p.G);
-    } else {
-      const int t = r / p.G;
-      return ((long long)b * p.num_new + t) * p.Hq + (long long)kvh * p.G + (r - t * p.G);
-    }
-  };
   const int nq = (!C::DUAL && live_rows - r0 <= 128) ? 1 : 2;  // tiles of rows, or streams
 
   static_assert(sizeof(Shared<C::STAGES>) <= 2048, "room behind the stages");
@@ -498,9 +492,12 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
     const uint32_t ts0 = tmem + lanes + C::COL_S + i * C::SB * kKeys;
     const uint32_t to = tmem + lanes + C::COL_O + i * D;
     const uint32_t tq = tmem + lanes + C::COL_Q + i * (D / 2);
-    const long long orow = row_at(live ? r : 0);
+    // this lane's row in q, out and the partials
+    const int t = live ? r / p.G : 0;
+    const long long orow = (PRE ? (long long)own_tok : (long long)b * p.num_new + t) * p.Hq + (long long)kvh * p.G +
+                           (live ? r - t * p.G : 0);
     // (rows behind the last take part with q = 0 and are not written)
-    const int last = live && !PRE ? before + r / p.G : 0x7fffffff;
+    const int last = live && !PRE ? before + t : 0x7fffffff;
     const int mine = C::DUAL ? (tiles + 1 - i) / 2 : tiles;  // this stream's key tiles
     if (i < nq && mine) {
       // q to tensor memory, channels in the order the keys are unpacked in: 64
@@ -512,8 +509,8 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
       uint4 x[D / 64][8];
 #pragma unroll
       for (int it = 0; it < 8; ++it) {  // (all loads, then the stores)
-        const int row = min(row0 + it * 4 + (lane >> 3), (int)live_rows - 1);
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + row_at(row) * D) + (lane & 7);
+        const long long row = __shfl_sync(0xffffffffu, orow, it * 4 + (lane >> 3));
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + row * D) + (lane & 7);
 #pragma unroll
         for (int h = 0; h < D / 64; ++h)
           x[h][it] = KVQ_IN(c, KVQ_ARRAY_Q, src + h * 8, 16) ? __ldg(src + h * 8) : make_uint4(0u, 0u, 0u, 0u);

@@ -43,9 +43,11 @@ void dbg_extent(CacheGeom& g, int array, const void* base, size_t bytes);
 
 // The tails of sequences with a shared prefix, one new token each: whether a
 // tensor-core decode kernel takes them, and its launch, which leaves partials
-// ([batch][num_q_heads][splits]) for the join.
+// ([batch][num_q_heads][splits]) for the join or (t.one) writes `out`, joined.
 struct TailDecode {
   bool takes = false;
+  bool one = false;  // the tail kernel: joined with the prefixes and written out
+  int wpu = 0;       // its warps a (sequence, KV head)
   int gp = 1, occ = 0;
   int32_t splits = 0;
 };
@@ -54,6 +56,7 @@ kvq_status tail_decode_plan(const kvq_cache_desc* desc, const CacheGeom& geom, i
 cudaError_t tail_decode(const kvq_cache_desc* desc, const kvq_cache* cache, const CacheGeom& geom, int32_t batch,
                         int32_t num_q_heads, const uint16_t* q, const int32_t* before, const int32_t* new_lens,
                         int32_t max_len, const TailDecode& t, float scale_log2, float* ws_o, float* ws_ml,
-                        const void* ws, size_t ws_bytes, uint32_t* status, cudaStream_t stream);
+                        const void* ws, size_t ws_bytes, uint32_t* status, cudaStream_t stream,
+                        const PrefixJoin& join, uint16_t* out);
 
 }  // namespace kvq

@@ -156,6 +156,19 @@ struct AppendParams {
   int32_t num_new;
 };
 
+// What a tail kernel joins its rows with: the partials that the pass over shared
+// prefixes left, (m, l, o) times 2^lift of each row and split.
+struct PrefixJoin {
+  const float* o;     // [row][splits][D]
+  const float* ml;    // [row][splits][2]
+  const int32_t* of;  // prefix of each sequence, -1: none
+  const int32_t* len; // tokens of each prefix
+  int32_t N, splits, chunk, limit;  // longer prefixes than limit are left out
+  float lift;
+  int32_t early;      // the kernel before is that pass, whose start already waited for what came before
+  int32_t wpu;        // warps that work on a (sequence, KV head): 1, 2 or 4
+};
+
 struct DecodeParams {
   CacheGeom geom;
   const uint8_t* codes[2];  // K, V
@@ -200,12 +213,21 @@ struct DecodeParams {
   // tail_new[b] of them where tail_new is set
   int32_t len_add;
   const int32_t* tail_new;
+  PrefixJoin join;  // the tail kernel joins its rows with these and writes them out
 };
 
 // lens[b] (a length array of the call), or `bad` when a debug build finds the
 // read outside the array.
 __device__ __forceinline__ int checked_len(const CacheGeom& c, const int32_t* lens, int b, int bad) {
   return KVQ_IN(c, KVQ_ARRAY_SEQ_LENS, lens + b, 4) ? __ldg(lens + b) : bad;
+}
+
+// Which rows of a padded batch sequence b has: new_lens[b], or num_new
+// without the array; -1 for a value outside [0, num_new].
+__device__ __forceinline__ int new_rows_of(const int32_t* new_lens, int b, int num_new) {
+  if (!new_lens) return num_new;
+  const int n = __ldg(new_lens + b);
+  return (n < 0 || n > num_new) ? -1 : n;
 }
 
 // Tokens to attend over for sequence b (-1 for a length that cannot be formed).
@@ -400,6 +422,17 @@ cudaError_t launch_decode_fast_int8_kch_paged(const DecodeParams& p, int gp, cud
                                               bool* handled, int* occ);
 cudaError_t launch_decode_fast_int8(const DecodeParams& p, int gp, cudaStream_t s, bool* handled,
                                     int* occ);
+// The same kernel for tails: one, two or four warps a (sequence, KV head), joined
+// with the partials of shared prefixes (p.join); one split, per-token caches.
+#define KVQ_ONE(name) \
+  cudaError_t launch_decode_one_##name(const DecodeParams& p, int gp, cudaStream_t s, bool* handled, int* occ)
+KVQ_ONE(int2);
+KVQ_ONE(int4);
+KVQ_ONE(int4_sym);
+KVQ_ONE(int8);
+KVQ_ONE(int8_sym);
+KVQ_ONE(nf4);
+#undef KVQ_ONE
 int generic_ctas_per_sm(const DecodeParams& p);
 
 // Size of the workspace for `splits` splits (0 when splits == 1).

@@ -153,7 +153,7 @@ struct ExtendParams {
   float scale_log2;
   // Attention over shared prefixes (launch_extend_prefix): the cache's sequences
   // are the plan's prefixes, and a row of the tile is a (member, new token, head)
-  // triple of one of them; lens_before, new_lens and out are not used.
+  // triple of one of them; lens_before and out are not used.
   PrefixPlan plan;
 };
 
@@ -162,15 +162,23 @@ struct ExtendParams {
 struct ExtendPlan {
   int tile_rows = 0;
   int occ = 0;
-  int kind = 0;  // 0: mma.sync kernel, 1 / 2: tensor-core kernel with that many 128-row tiles a CTA
+  // 0: mma.sync kernel, 1 / 2: tensor-core kernel with that many 128-row tiles a
+  // CTA, 3 / 4: the kernel for few rows (kvq_rows.cuh), 16 or 32 of them
+  int kind = 0;
   float lift = 0.f;  // log2 of the factor in the partials' sums
 };
 cudaError_t extend_plan(const CacheGeom& c, int num_new, int G, ExtendPlan* plan);
 cudaError_t launch_extend(const ExtendParams& p, const ExtendPlan& plan, cudaStream_t stream);
 // The same without the merge of its splits: partials are left in ws_o, ws_ml.
 cudaError_t launch_extend_partials(const ExtendParams& p, const ExtendPlan& plan, cudaStream_t stream);
-// Over shared prefixes; rows: of a prefix's members together, on average.
-cudaError_t extend_prefix_plan(const CacheGeom& c, long long rows, ExtendPlan* plan);
+// Over shared prefixes; rows: of a prefix's members together, on average; few: by
+// the kernel for few rows, which takes the caches that extend_prefix_few says.
+cudaError_t extend_prefix_plan(const CacheGeom& c, long long rows, bool few, ExtendPlan* plan);
+bool extend_prefix_few(const CacheGeom& c);
 cudaError_t launch_extend_prefix(const ExtendParams& p, const ExtendPlan& plan, cudaStream_t stream);
+// The kernel for few rows over prefixes, 16 (mt 1) or 32 (mt 2).
+cudaError_t run_rows_int4(int D, int mt, const ExtendParams* p, ExtendPlan* plan, cudaStream_t stream);
+cudaError_t run_rows_int8(int D, int mt, const ExtendParams* p, ExtendPlan* plan, cudaStream_t stream);
+cudaError_t run_rows_nf4(int D, int mt, const ExtendParams* p, ExtendPlan* plan, cudaStream_t stream);
 
 }  // namespace kvq

@@ -86,6 +86,45 @@ __device__ __forceinline__ PrefixTile prefix_tile(const PrefixPlan& p, long long
   }
   return PrefixTile{-1, 0, 0, 0};
 }
+// The tokens of a prefix's members, as rows of `G` heads: row r of the prefix
+// (this lane's) is head r % G of token *tok, counted b T + t over the padded
+// batch (rows behind the last: some token of the first member).  Returns the
+// rows there are.  Of a padded batch only live tokens make rows, found by a
+// scan over the members, 32 a turn (24 sequences of 1 to 200 tokens: 442 us with
+// a row for each of the 200, half of them dead, 224 without); one new token a
+// sequence takes its place in any case.  Every lane of a warp calls it.
+__device__ __forceinline__ int prefix_rows(const PrefixPlan& p, const PrefixTile& pt, const int32_t* new_lens, int T,
+                                           int G, long long r, int* tok) {
+  const int lane = threadIdx.x & 31;
+  if (!new_lens || T == 1) {
+    const int live = pt.count * T * G;
+    const int x = (int)(r < live ? r : 0) / G, m = x / T;
+    *tok = plan_member(p, pt.first + m) * T + (x - m * T);
+    return live;
+  }
+  const int want = (int)(r / G);
+  int base = 0;
+  *tok = plan_member(p, pt.first) * T;
+  for (int i0 = 0; i0 < pt.count; i0 += 32) {
+    const bool in = i0 + lane < pt.count;
+    const int b = plan_member(p, pt.first + (in ? i0 + lane : 0));
+    const int n = in ? max(new_rows_of(new_lens, b, T), 0) : 0;
+    int upto = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    const int total = __shfl_sync(0xffffffffu, upto, 31), x = want - base;
+    int k = 0;  // the first lane with upto > x
+#pragma unroll
+    for (int o = 16; o; o >>= 1) k += __shfl_sync(0xffffffffu, upto, k + o - 1) <= x ? o : 0;
+    const int bk = __shfl_sync(0xffffffffu, b, k), before = __shfl_sync(0xffffffffu, upto - n, k);
+    if (x >= 0 && x < total) *tok = bk * T + (x - before);
+    base += total;
+  }
+  return base * G;
+}
 // At most so many tiles.
 inline long long prefix_tiles_bound(long long B, long long N, long long each, long long rows) {
   return B * each / rows + (B < N ? B : N);

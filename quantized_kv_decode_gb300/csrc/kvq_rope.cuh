@@ -210,14 +210,6 @@ __device__ __forceinline__ void rotate_chunk(const Turn* t, int stride, float e,
 
 }  // namespace rope
 
-// Which rows of a padded batch sequence b has: new_lens[b], or num_new
-// without the array; -1 for a value outside [0, num_new].
-__device__ __forceinline__ int new_rows_of(const int32_t* new_lens, int b, int num_new) {
-  if (!new_lens) return num_new;
-  const int n = __ldg(new_lens + b);
-  return (n < 0 || n > num_new) ? -1 : n;
-}
-
 struct RopeParams {
   kvq_rope rope;
   const __half* q;
