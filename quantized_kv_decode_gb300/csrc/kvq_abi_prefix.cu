@@ -154,7 +154,7 @@ kvq_status kvq_prefix_plan(int32_t batch, int32_t num_prefixes, const int32_t* p
 
 size_t kvq_prefix_find_workspace_size(const kvq_page_pool* pool) {
   if (check_pool(pool) != KVQ_OK) return 0;
-  return (size_t)std::max(pool->batch, 1) * 16;
+  return (size_t)pool->batch * 24 + 16;
 }
 
 kvq_status kvq_prefix_find(const kvq_page_pool* pool, const int32_t* seq_lens_before, int32_t min_tokens,
@@ -288,6 +288,7 @@ kvq_status kvq_prefix_attn(const kvq_cache_desc* prefix_desc, const kvq_cache* p
              workspace, workspace_size, dev_status);
     x.ws_o = to;
     x.ws_ml = tml;
+    x.early = c.prefixes;
     x.lens_before = seq_lens_before;
     x.new_lens = new_lens;
     x.batch = batch;

@@ -72,7 +72,7 @@ template <int BITS, int D, bool PRE>
 __device__ __forceinline__ void attend(const ExtendParams& p) {
   constexpr int KEYS = tile_keys(D), CH = D / 8, KB = D / 16, NT = KEYS / 8;
   if (!PRE) pdl_launch_dependents();
-  pdl_wait();
+  if (PRE || !p.early) pdl_wait();
   if (PRE) pdl_launch_dependents();  // (a tail kernel starts without waiting for what came before)
   extern __shared__ __align__(128) uint8_t smem[];
   const CacheGeom& c = p.v.geom;
@@ -98,7 +98,10 @@ __device__ __forceinline__ void attend(const ExtendParams& p) {
     live_rows = (long long)sp.n * p.G;
   }
   const long long r0 = (long long)tile * kRows;
-  if (r0 >= live_rows) return;
+  if (r0 >= live_rows) {
+    if (!PRE) ext::end_after_prefixes(p);
+    return;
+  }
   // row r in q, out and the partials
   auto row_at = [&](long long r) -> long long {
     if constexpr (PRE) {
@@ -281,6 +284,7 @@ __device__ __forceinline__ void attend(const ExtendParams& p) {
       if ((lane & 3) == 0 && KVQ_IN(c, KVQ_ARRAY_WORKSPACE, ml, 8)) *ml = make_float2(m[e], l[e]);
     }
   }
+  if (!PRE) ext::end_after_prefixes(p);
 }
 
 template <int BITS, int D>

@@ -117,7 +117,7 @@ struct Cfg {
   static constexpr int HDR = kKeys * D / 4 + 16;  // most bytes of one header array, from a 16-byte boundary on
   static constexpr int RAW = LO ? 2 * CODES + 4 * HDR : 0;     // K codes, V codes, K scale, K zero, V scale, V zero
   // arrivals that fill a ring slot (fp16: a stage's copies and key masks), and a stage
-  static constexpr int RAW_FULL = LO ? LOAD : PROD * 32 + 1, FULL = LO ? PROD / 2 : 1;
+  static constexpr int RAW_FULL = LO ? LOAD : PROD * 32, FULL = LO ? PROD / 2 : 1;
   static constexpr int SLOTS = LO ? DEPTH : STAGES;
   // Two S per tile where tensor memory has room for them: at head_dim 64, and
   // at 128 with q in shared memory, which only fp16 caches leave the room for.
@@ -347,6 +347,12 @@ __device__ __forceinline__ bool nonfinite2(uint32_t w) {
 
 // ---- the kernel -------------------------------------------------------
 
+// (ExtendParams::early)
+__device__ __forceinline__ void end_after_prefixes(const ExtendParams& p) {
+  if (p.early && threadIdx.x == 0 && blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1)
+    pdl_wait();
+}
+
 // PRE: over shared prefixes (rows of all members of a prefix, which see all of
 // its keys; partials only).
 template <int BITS, int KIND, int D, int NQ, bool PRE>
@@ -362,7 +368,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
   const int warp = tc::uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int kvh = blockIdx.y;
   const int split = blockIdx.x % p.splits;
-  pdl_wait();
+  if (PRE || !p.early) pdl_wait();
   if (PRE) pdl_launch_dependents();  // (a tail kernel starts without waiting for what came before)
 
   int b, before, end, all_see;  // all_see: every row sees the positions up to here
@@ -392,7 +398,10 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
     if (!fits && threadIdx.x == 0 && blockIdx.x == 0 && kvh == 0 && p.status) atomicOr(p.status, KVQ_FLAG_SEQ_LEN);
     live_rows = (long long)n * p.G;
     r0 = (long long)tile * ROWS;
-    if (r0 >= live_rows) return;
+    if (r0 >= live_rows) {
+      end_after_prefixes(p);
+      return;
+    }
     const int L = fits ? before + n : 0;
     const int t_first = (int)(r0 / p.G);
     const int t_last = (int)((min(r0 + ROWS, live_rows) - 1) / p.G);
@@ -831,9 +840,16 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
       // per lane took a tag per lane and copy: 2050 cycles of issue a tile).
       constexpr int CH = D / 8, RPP = C::PROD * 32 / CH;  // chunks of a row, rows a pass
       const int ch = tid % CH, sub = tid / CH;
+      // Where a warp's eight keys of a tile lie, a lane per key, looked up a tile
+      // ahead: a page takes a division and a load from the table.
+      constexpr int SPW = 32 / CH;  // rows a warp has in a pass
+      static_assert(SPW * (kKeys / RPP) == 8, "eight keys a warp and tile");
+      auto own_row = [&](int j) { return row_of(k0 + j * kKeys + (lane & 7) / SPW * RPP + pw * SPW + (lane & 7) % SPW); };
+      long long ahead = own_row(0);
 #pragma unroll 1
       for (int j = 0; j < tiles; ++j) {
         const int st = j % C::STAGES;
+        const long long rows8 = ahead;
         ok = __all_sync(0xffffffffu, !(pw == 0 && runs_out(KVQ_WAIT_K, j)) &&
                                          tc::mbar_wait(empty(1, st), ((j / C::STAGES) & 1) ^ 1, stop));
         if (ok && j == C::Q_STAGE) wait_q();
@@ -843,16 +859,13 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
 #pragma unroll 4
         for (int pass = 0; pass < kKeys / RPP; ++pass) {
           const int key = pass * RPP + sub;
-          const long long row = row_of(k0 + j * kKeys + key);
+          const long long row = __shfl_sync(0xffffffffu, rows8, pass * SPW + lane / CH);
           const uint32_t dst = base + key * 128 + (((ch & 7) ^ (key & 7)) << 4);
           const long long o = max(row, 0ll) * (2 * D) + ch * 16;
           fast::cp_async16(dst, p.v.codes[0] + o, row >= 0 && KVQ_IN(c, KVQ_ARRAY_K_CODES, p.v.codes[0] + o, 16));
           fast::cp_async16(dst + C::MAT, p.v.codes[1] + o, row >= 0 && KVQ_IN(c, KVQ_ARRAY_V_CODES, p.v.codes[1] + o, 16));
         }
-        if (pw == 0) {
-          note_keys(sh.ok[j % (2 * C::STAGES)], j);
-          if (lane == 0) tc::mbar_arrive(raw_full(st));
-        }
+        ahead = own_row(j + 1);  // (-1 behind the last tile)
         if (k0 + (j + 1) * kKeys - 1 <= all_see) {
           tc::mbar_arrive_copies(raw_full(st));
           continue;
@@ -979,6 +992,8 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
 #pragma unroll 1
       for (int j = 0; j < tiles && ok; ++j) {
         const int st = j % C::STAGES;
+        // (the softmax is at most STAGES tiles behind, so that the slot is free)
+        note_keys(sh.ok[j % (2 * C::STAGES)], j);
         ok = __all_sync(0xffffffffu, !runs_out(KVQ_WAIT_LOAD_K, j) &&
                                          tc::mbar_wait(raw_full(st), (j / C::STAGES) & 1, stop));
         tc::fence_async_shared();
@@ -1104,6 +1119,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
     tc::fence_after();
     tc::tmem_dealloc(tmem, C::COLS);
   }
+  if constexpr (!PRE) end_after_prefixes(p);
 }
 
 template <int BITS, int KIND, int D, int NQ, bool PRE>

@@ -68,9 +68,18 @@ __global__ void __launch_bounds__(kPlanWarps * 32) prefix_plan_kernel(const __gr
 }
 
 // ---- prefixes in a page pool's table -------------------------------------
-
-constexpr int kFindWarps = 32;
-constexpr int kFindKeys = 4096;  // keys held in shared memory at a time
+//
+// Three kernels: leaders and runs (a warp a sequence), savings and the numbers
+// of the groups (a warp a sequence, the last block numbers them), tables (a warp
+// a row).  Bound by memory latency: keys and (leader, run) pairs are brought to
+// shared memory by the block, rows are read and written 256 entries at a time.
+// 2048 sequences of up to 1012 blocks: 43 us when rows went 128 at a time and
+// every warp looked through the pairs and the groups' savings in global memory.
+// Integer sums and maxima only: the result does not depend on the order.
+constexpr int kFindWarps = 16;
+constexpr int kFindHeld = 4096;  // keys or pairs held in shared memory at a time
+constexpr int kRowLoads = 8;     // loads in flight a lane
+constexpr int kRanks = 4;        // sequences a thread numbers at a time
 
 __device__ __forceinline__ bool is_page(const kvq_page_pool& pl, int e) { return e >= 0 && e < pl.num_pages; }
 
@@ -94,14 +103,19 @@ __device__ __forceinline__ int key_of(const PrefixFindParams& p, int b) {
 
 struct FindSpace {
   unsigned long long* best;  // [B] of a leader: (blocks saved) (M + 1) + run
-  int32_t* leader;           // [B], -1: member of no group
-  int32_t* run;              // [B]
+  int2* pair;                // [B] leader (-1: member of no group), run
+  int32_t* rank;             // [B] of a leader whose group has a prefix
+  int32_t* lead;             // [B] the leaders by rank
+  int32_t* done;             // blocks of the second kernel that are through; prefixes
 };
 __device__ __forceinline__ FindSpace space_of(const PrefixFindParams& p) {
   FindSpace s;
+  const int B = p.pool.batch;
   s.best = p.best;
-  s.leader = reinterpret_cast<int32_t*>(p.best + p.pool.batch);
-  s.run = s.leader + p.pool.batch;
+  s.pair = reinterpret_cast<int2*>(p.best + B);
+  s.rank = reinterpret_cast<int32_t*>(s.pair + B);
+  s.lead = s.rank + B;
+  s.done = s.lead + B;
   return s;
 }
 
@@ -110,7 +124,7 @@ __device__ __forceinline__ FindSpace space_of(const PrefixFindParams& p) {
 __global__ void __launch_bounds__(kFindWarps * 32) find_leaders_kernel(const __grid_constant__ PrefixFindParams p) {
   pdl_launch_dependents();
   pdl_wait();
-  __shared__ int keys[kFindKeys];
+  __shared__ int keys[kFindHeld];
   const kvq_page_pool& pl = p.pool;
   const int B = pl.batch, M = pl.max_blocks_per_seq;
   const int lane = threadIdx.x & 31;
@@ -119,8 +133,8 @@ __global__ void __launch_bounds__(kFindWarps * 32) find_leaders_kernel(const __g
   int own = -1, lead = b;
   if (b < B) own = key_of(p, b);
   bool found = false;
-  for (int base = 0; base < last; base += kFindKeys) {
-    const int n = min(kFindKeys, last - base);
+  for (int base = 0; base < last; base += kFindHeld) {
+    const int n = min(kFindHeld, last - base);
     __syncthreads();
     for (int i = threadIdx.x; i < n; i += blockDim.x) keys[i] = key_of(p, base + i);
     __syncthreads();
@@ -132,8 +146,9 @@ __global__ void __launch_bounds__(kFindWarps * 32) find_leaders_kernel(const __g
       }
     }
   }
-  if (b >= B) return;
   const FindSpace s = space_of(p);
+  if (blockIdx.x == 0 && threadIdx.x == 0) s.done[0] = 0;
+  if (b >= B) return;
   uint32_t flags = 0, unused = 0;
   const int whole = whole_blocks(p, b, flags);
   int run = 0;
@@ -142,65 +157,113 @@ __global__ void __launch_bounds__(kFindWarps * 32) find_leaders_kernel(const __g
     const int32_t* x = pl.block_table + (long long)b * M;
     const int32_t* y = pl.block_table + (long long)lead * M;
     run = most;
-    for (int j0 = 0; j0 < most; j0 += 128) {  // four loads of each in flight
-      int e[4], f[4];
+    for (int j0 = 0; j0 < most && run == most; j0 += 32 * kRowLoads) {
+      int e[kRowLoads], f[kRowLoads];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < kRowLoads; ++u) {
         const int j = j0 + 32 * u + lane;
         e[u] = j < most ? __ldg(x + j) : 0;
         f[u] = j < most ? __ldg(y + j) : 0;
       }
-      int stop = most;
 #pragma unroll
-      for (int u = 3; u >= 0; --u) {
+      for (int u = kRowLoads - 1; u >= 0; --u) {
         const int j = j0 + 32 * u + lane;
         const unsigned m = __ballot_sync(0xffffffffu, j < most && (e[u] != f[u] || !is_page(pl, e[u])));
-        if (m) stop = j0 + 32 * u + __ffs(m) - 1;
-      }
-      if (stop < most) {
-        run = stop;
-        break;
+        if (m) run = j0 + 32 * u + __ffs(m) - 1;
       }
     }
   }
   if (lane == 0) {
-    s.leader[b] = run >= p.depth ? lead : -1;
-    s.run[b] = run;
+    s.pair[b] = make_int2(run >= p.depth ? lead : -1, run);
     s.best[b] = 0;
     flag(p.status, flags);
   }
 }
 
-// A warp per sequence: what its run would save as the group's prefix.
+// A warp per sequence: what its run would save as the group's prefix.  The last
+// block through numbers the groups that have one.
 __global__ void __launch_bounds__(kFindWarps * 32) find_savings_kernel(const __grid_constant__ PrefixFindParams p) {
   pdl_launch_dependents();
   pdl_wait();
+  __shared__ __align__(16) int2 pairs[kFindHeld];
+  __shared__ int sums[kFindWarps + 1], is_last;
   const int B = p.pool.batch;
-  const int lane = threadIdx.x & 31;
-  const int b = blockIdx.x * kFindWarps + (threadIdx.x >> 5);
-  if (b >= B) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int b = blockIdx.x * kFindWarps + warp;
   const FindSpace s = space_of(p);
-  const int lead = s.leader[b], run = s.run[b];
-  if (lead < 0) return;
+  const int2 own = b < B ? s.pair[b] : make_int2(-1, 0);
   int with = 0;  // members with at least this run
+  for (int base = 0; base < B; base += kFindHeld) {
+    const int n = min(kFindHeld, B - base);
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += blockDim.x) pairs[i] = s.pair[base + i];
+    __syncthreads();
+    if (own.x >= 0) {  // (two pairs a load)
+      const int4* const two = reinterpret_cast<const int4*>(pairs);
 #pragma unroll 4
-  for (int i = lead + lane; i < B; i += 32) with += s.leader[i] == lead && s.run[i] >= run;
+      for (int i = lane; i < n / 2; i += 32) {
+        const int4 v = two[i];
+        with += (v.x == own.x && v.y >= own.y) + (v.z == own.x && v.w >= own.y);
+      }
+      if ((n & 1) && lane == 0) with += pairs[n - 1].x == own.x && pairs[n - 1].y >= own.y;
+    }
+  }
   with = __reduce_add_sync(0xffffffffu, with);
-  if (lane == 0 && with > 1)
-    atomicMax(s.best + lead, (unsigned long long)(with - 1) * run * (unsigned)(p.pool.max_blocks_per_seq + 1u) + run);
+  if (lane == 0 && own.x >= 0 && with > 1)
+    atomicMax(s.best + own.x, (unsigned long long)(with - 1) * own.y * (unsigned)(p.pool.max_blocks_per_seq + 1u) + own.y);
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) is_last = atomicAdd(s.done, 1) == (int)gridDim.x - 1;
+  __syncthreads();
+  if (!is_last) return;
+  __threadfence();
+  int groups = 0;
+  for (int base = 0; base < B; base += kFindWarps * 32 * kRanks) {
+    // a warp takes 32 kRanks neighbours, so that one look at the warps' sums does
+    bool has[kRanks];
+    const int i0 = base + warp * (32 * kRanks) + lane;
+#pragma unroll
+    for (int u = 0; u < kRanks; ++u) has[u] = i0 + 32 * u < B && __ldcg(s.best + i0 + 32 * u) != 0;
+    int mine = 0;
+#pragma unroll
+    for (int u = 0; u < kRanks; ++u) mine += __popc(__ballot_sync(0xffffffffu, has[u]));
+    if (lane == 0) sums[warp] = mine;
+    __syncthreads();
+    int r = groups, all = 0;
+#pragma unroll
+    for (int w = 0; w < kFindWarps; ++w) {
+      r += w < warp ? sums[w] : 0;
+      all += sums[w];
+    }
+#pragma unroll
+    for (int u = 0; u < kRanks; ++u) {
+      const unsigned m = __ballot_sync(0xffffffffu, has[u]);
+      if (has[u]) {
+        s.rank[i0 + 32 * u] = r + __popc(m & lanes_below());
+        s.lead[r + __popc(m & lanes_below())] = i0 + 32 * u;
+      }
+      r += __popc(m);
+    }
+    groups += all;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    s.done[1] = groups;
+    if (p.num) *p.num = groups;
+  }
 }
 
 // Copies n entries of a table row, -1 behind, by one warp.
 __device__ __forceinline__ void copy_row(const int32_t* from, int n, int32_t* to, int M, int lane) {
-  for (int j0 = 0; j0 < M; j0 += 128) {
-    int e[4];
+  for (int j0 = 0; j0 < M; j0 += 32 * kRowLoads) {
+    int e[kRowLoads];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < kRowLoads; ++u) {
       const int j = j0 + 32 * u + lane;
       e[u] = j < n ? __ldg(from + j) : -1;
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < kRowLoads; ++u) {
       const int j = j0 + 32 * u + lane;
       if (j < M) to[j] = e[u];
     }
@@ -218,15 +281,13 @@ __global__ void __launch_bounds__(kFindWarps * 32) find_tables_kernel(const __gr
   const FindSpace s = space_of(p);
   const unsigned base = (unsigned)M + 1u;
   if (w < B) {
-    const int b = (int)w, lead = s.leader[b];
-    const int prefix = lead < 0 ? 0 : (int)(s.best[lead] % base);
+    const int b = (int)w;
+    const int2 own = s.pair[b];
+    const int prefix = own.x < 0 ? 0 : (int)(s.best[own.x] % base);
     int n = -1;
-    if (prefix > 0 && s.run[b] >= prefix) {
-      int before = 0;  // groups with a lower leader
-#pragma unroll 4
-      for (int i = lane; i < lead; i += 32) before += s.best[i] != 0;
-      before = __reduce_add_sync(0xffffffffu, before);
-      if (before < p.most) n = before;
+    if (prefix > 0 && own.y >= prefix) {
+      const int r = s.rank[own.x];
+      if (r < p.most) n = r;
     }
     const int shift = n >= 0 ? prefix : 0;
     if (lane == 0) {
@@ -236,18 +297,11 @@ __global__ void __launch_bounds__(kFindWarps * 32) find_tables_kernel(const __gr
     copy_row(pl.block_table + (long long)b * M + shift, M - shift, p.tail_table + (long long)b * M, M, lane);
   } else if (w < (long long)B + p.most) {
     const int n = (int)(w - B);
-    int lead = -1, groups = 0;
-    for (int i0 = 0; i0 < B; i0 += 32) {
-      const unsigned m = __ballot_sync(0xffffffffu, i0 + lane < B && s.best[min(i0 + lane, B - 1)] != 0);
-      const int here = __popc(m);
-      if (lead < 0 && groups + here > n) lead = i0 + (int)__fns(m, 0, n - groups + 1);
-      groups += here;
-      if (lead >= 0 && !(n == 0 && p.num)) break;
-    }
+    const int lead = B > 0 && n < s.done[1] ? s.lead[n] : -1;
     const int prefix = lead < 0 ? 0 : (int)(s.best[lead] % base);
     if (lane == 0) {
       p.len[n] = prefix * pl.page_size;
-      if (n == 0 && p.num) *p.num = groups;
+      if (B == 0 && n == 0 && p.num) *p.num = 0;
     }
     copy_row(pl.block_table + (long long)max(lead, 0) * M, prefix, p.prefix_table + (long long)n * M, M, lane);
   }

@@ -148,7 +148,7 @@ struct PrefixFindParams {
   int32_t* tail_table;    // [batch][max_blocks]
   int32_t* tail_lens;
   int32_t* num;           // may be null
-  unsigned long long* best;  // workspace: [batch]; then leader [batch], run [batch]
+  unsigned long long* best;  // workspace (see the kernels)
   uint32_t* status;
   int32_t most, depth;    // depth: blocks a prefix has at least
 };

@@ -22,24 +22,34 @@ from ._lib import ROPE_SCALING, kvq_page_pool, kvq_rope, kvq_rope_axes, kvq_rope
 from .api import KVCache, _ptr
 
 
+_Tensor = torch.Tensor
+_device_now = torch._C._cuda_getDevice
+
+
 def _check(t, dtype, name, shape, device):
     """A contiguous CUDA tensor of this dtype and shape (None in it: any size),
-    on `device` (an index; None: any)."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda:
+    on `device` (an index; None: any).  A call checks six to ten arrays, half a
+    microsecond each: what is right is seen to be so first."""
+    if isinstance(t, _Tensor) and t.dtype is dtype:
+        at = t.get_device()  # (-1: host memory)
+        if at >= 0 and (at == device or device is None) and t.is_contiguous():
+            got = t.shape
+            if got == shape:
+                return
+            if len(got) == len(shape):
+                for w, n in zip(shape, got):
+                    if w != n and w is not None:
+                        break
+                else:
+                    return
+    if not isinstance(t, _Tensor) or t.dtype != dtype or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor of dtype {dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    got = t.shape
-    if got != shape:
-        fits = len(got) == len(shape)
-        for w, n in zip(shape, got):
-            if w != n and w is not None:
-                fits = False
-        if not fits:
-            raise ValueError(f"{name} must have shape {tuple('*' if w is None else w for w in shape)}, "
-                             f"not {tuple(got)}")
-    if device is not None and t.get_device() != device:
-        raise ValueError(f"{name} is on {t.device}, not on cuda:{device}")
+    if len(t.shape) != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
+        raise ValueError(f"{name} must have shape {tuple('*' if w is None else w for w in shape)}, "
+                         f"not {tuple(t.shape)}")
+    raise ValueError(f"{name} is on {t.device}, not on cuda:{device}")
 
 
 def _optional(t, dtype, name, shape, device):
@@ -83,7 +93,7 @@ class _on:
                 raise ValueError(f"the stream is of {stream.device}, the tensors are on cuda:{device}")
             self.guard = torch.cuda.stream(stream)
         else:
-            self.guard = None if device == torch.cuda.current_device() else torch.cuda.device(device)
+            self.guard = None if device == _device_now() else torch.cuda.device(device)
 
     def __enter__(self):
         if self.guard is not None:
@@ -235,27 +245,37 @@ def kvq_rope_axes_apply(axes: kvq_rope_axes, positions: torch.Tensor, q: torch.T
     if x is None:
         raise ValueError("q or k must be given")
     _check(x, torch.float16, "q" if q is not None else "k", (None,) * 4, None)
-    B, T, _, D = x.shape
+    B, T, Hq, D = x.shape
+    Hk = 0
     dev = x.get_device()
     _check(positions, torch.int32, "positions", (B, T, axes.num_axes), dev)
-    _optional(new_lens, torch.int32, "new_lens", (B,), dev)
-    _status(dev_status, dev)
-    for t, o, name in ((q, q_out, "q"), (k, k_out, "k")):
-        if t is not None:
-            _check(t, torch.float16, name, (B, T, None, D), dev)
-            if o is not None:
-                _check(o, torch.float16, name + "_out", t.shape, dev)
-        elif o is not None:
-            raise ValueError(f"{name}_out without {name}")
+    if new_lens is not None:
+        _check(new_lens, torch.int32, "new_lens", (B,), dev)
+    if dev_status is not None:
+        _status(dev_status, dev)
+    if q is None:
+        Hq, Hk = 0, Hq
+    elif k is not None:
+        _check(k, torch.float16, "k", (B, T, None, D), dev)
+        Hk = k.shape[2]
+    if q_out is not None:
+        if q is None:
+            raise ValueError("q_out without q")
+        _check(q_out, torch.float16, "q_out", (B, T, Hq, D), dev)
+    if k_out is not None:
+        if k is None:
+            raise ValueError("k_out without k")
+        _check(k_out, torch.float16, "k_out", (B, T, Hk, D), dev)
     with _on(dev, stream):
-        outs = [o if t is None or o is not None else _made_like(t, new_lens)
-                for t, o in ((q, q_out), (k, k_out))]
-        st = _lib.lib().kvq_rope_axes_apply(
-            byref(axes), D, B, T, 0 if q is None else q.shape[2], _ptr(q), _ptr(outs[0]),
-            0 if k is None else k.shape[2], _ptr(k), _ptr(outs[1]), _ptr(positions), _ptr(new_lens),
-            _ptr(dev_status), _handle(dev))
-    _lib.check(st, "kvq_rope_axes_apply")
-    return outs[0], outs[1]
+        if q is not None and q_out is None:
+            q_out = _made_like(q, new_lens)
+        if k is not None and k_out is None:
+            k_out = _made_like(k, new_lens)
+        st = _lib.lib().kvq_rope_axes_apply(byref(axes), D, B, T, Hq, _ptr(q), _ptr(q_out), Hk, _ptr(k), _ptr(k_out),
+                                            positions.data_ptr(), _ptr(new_lens), _ptr(dev_status), _handle(dev))
+    if st:
+        _lib.check(st, "kvq_rope_axes_apply")
+    return q_out, k_out
 
 
 def kvq_rope_axes_append(cache: KVCache, axes: kvq_rope_axes, positions: torch.Tensor, k_new: torch.Tensor,

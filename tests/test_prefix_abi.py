@@ -126,8 +126,8 @@ def test_plan_and_find_refusals(K):
     for name in ("lens", "of", "plens", "ptab", "ttab", "tlens"):
         assert find(**{name: None}) == bad and find(**{name: a + 0x900004}) == bad, name
     assert find(ttab=table) == bad and find(ttab=table + 16) == bad and find(tlens=a) == bad and find(num=a + 4) == bad
-    assert find(ws=None) == ws_err and find(n=4 * 16 - 1) == ws_err and find(ws=ws + 8) == ws_err
-    assert lib.kvq_prefix_find_workspace_size(byref(pool())) == 64
+    need = lib.kvq_prefix_find_workspace_size(byref(pool()))
+    assert need > 0 and find(ws=None) == ws_err and find(n=need - 1) == ws_err and find(ws=ws + 8) == ws_err
     assert lib.kvq_prefix_find_workspace_size(byref(pool(page=0))) == 0
 
 
