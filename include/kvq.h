@@ -731,10 +731,16 @@ KVQ_API size_t kvq_prefix_attn_workspace_size(const kvq_cache_desc* prefix_desc,
  *   new_lens         device int32 [batch] or NULL, as above
  *   plan             of kvq_prefix_plan, for this batch and num_prefixes
  *   max_prefix_len   host upper bound on the prefixes' lengths
- *   max_seq_len      host upper bound on seq_lens_before[b] + new_lens[b]
+ *   max_seq_len      host upper bound on seq_lens_before[b] + new_lens[b]; the
+ *                    nearer the bounds, the better the choice of splits
  *   prefix_splits, tail_splits  0: library choice, else as num_splits of
  *                    kvq_decode_attn, for each of the two
  *   out              device fp16 like q; may not overlap it
+ *   workspace        kvq_prefix_attn_workspace_size() bytes for the same sizes
+ *                    and splits (may be NULL when that is 0); calls that can
+ *                    overlap on the GPU need one each
+ * (A row of q without a new token may be read, to no effect; its row of out is
+ * not written.)
  * Axis-aware caches: a prefix's length is all that has been appended to it.
  * Precision: over the prefix as in kvq_extend_attn, over the tail as in
  * kvq_decode_attn (one new token, shapes its tensor-core kernels take) or

@@ -114,9 +114,12 @@ class KVCache:
 
     @property
     def ptrs(self) -> kvq_cache:
-        return kvq_cache(_ptr(self.k_codes), _ptr(self.v_codes), _ptr(self.k_scale),
-                         _ptr(self.k_zero), _ptr(self.v_scale), _ptr(self.v_zero),
-                         _ptr(self.block_table), _ptr(self.k_window), _ptr(self.v_window))
+        ks, kz, vs, vz = self.k_scale, self.k_zero, self.v_scale, self.v_zero
+        bt, kw, vw = self.block_table, self.k_window, self.v_window
+        return kvq_cache(self.k_codes.data_ptr(), self.v_codes.data_ptr(), None if ks is None else ks.data_ptr(),
+                         None if kz is None else kz.data_ptr(), None if vs is None else vs.data_ptr(),
+                         None if vz is None else vz.data_ptr(), None if bt is None else bt.data_ptr(),
+                         None if kw is None else kw.data_ptr(), None if vw is None else vw.data_ptr())
 
     def with_table(self, block_table: torch.Tensor) -> "KVCache":
         """The pages of a paged cache as the sequences of another block table

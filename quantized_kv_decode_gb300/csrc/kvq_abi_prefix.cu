@@ -56,7 +56,8 @@ int32_t prefix_splits(const ExtendPlan& plan, int64_t units, int64_t max_len, in
   const double tail = tail_warps ? turns * (2000.0 + 30.0 * tail_keys) : 0.0;
   int32_t best = 0;
   *cost = 1e300;
-  for (int64_t s = requested > 0 ? requested : 1; s <= (requested > 0 ? requested : cap); ++s) {
+  for (int64_t s = requested > 0 ? requested : 1; s <= (requested > 0 ? requested : cap);
+       s += s < 24 ? 1 : 4) {
     const int64_t chunk = split_chunk(L, (int32_t)s), eff = ceil_div(L, chunk), n = std::max<int64_t>(units, 1) * eff;
     const double pass = ceil((double)n / slots) * (chunk + kFixed[plan.kind]) * kNs[plan.kind];
     // (SMs without a block of the pass: on the others the two would share it)

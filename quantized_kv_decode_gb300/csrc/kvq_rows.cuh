@@ -70,6 +70,14 @@ struct RowCfg {
   }
 };
 
+// How far (log2 units) a tile's maximum may lead the reference.  A probability,
+// at most 2^kSlackRows, times V's scale stays within fp16 for any V that fp16 holds:
+// INT4 scales reach 9358 (absmax 65504 over 7), times 4.  NF4 scales reach 65504:
+// there the probabilities carry 2^-kSlackRows (kHead).
+constexpr float kSlackRows = 2.f;
+template <int KIND>
+constexpr float kHead = KIND == 1 ? kSlackRows : 0.f;
+
 // A block takes a prefix, a KV head, a tile of rows and a split.
 template <int BITS, int KIND, int D, int MT>
 __global__ void __launch_bounds__(kWarps * 32, 2) rows_kernel(const __grid_constant__ ExtendParams p) {
@@ -396,20 +404,20 @@ __global__ void __launch_bounds__(kWarps * 32, 2) rows_kernel(const __grid_const
             }
       }
 
-      // softmax, the reference moved only where it is exceeded by kSlack
+      // softmax, the reference moved only where it is exceeded by kSlackRows
       uint32_t pa[MT][4];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         float top[2];
         top[0] = fmaxf(fmaxf(s[mt][0][0], s[mt][0][1]), fmaxf(s[mt][1][0], s[mt][1][1])) * p.scale_log2;
         top[1] = fmaxf(fmaxf(s[mt][0][2], s[mt][0][3]), fmaxf(s[mt][1][2], s[mt][1][3])) * p.scale_log2;
-        if (__any_sync(0xffffffffu, top[0] > m_ref[mt][0] + kSlack || top[1] > m_ref[mt][1] + kSlack)) {
+        if (__any_sync(0xffffffffu, top[0] > m_ref[mt][0] + kSlackRows || top[1] > m_ref[mt][1] + kSlackRows)) {
           float alpha[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
             top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
-            const bool moves = top[e] > m_ref[mt][e] + kSlack;
+            const bool moves = top[e] > m_ref[mt][e] + kSlackRows;
             alpha[e] = moves ? ex2(m_ref[mt][e] - top[e]) : 1.f;
             m_ref[mt][e] = moves ? top[e] : m_ref[mt][e];
             l_run[mt][e] *= alpha[e];
@@ -419,8 +427,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) rows_kernel(const __grid_const
           for (int n = 0; n < NT; ++n)
             o[mt][n][0] *= alpha[0], o[mt][n][1] *= alpha[0], o[mt][n][2] *= alpha[1], o[mt][n][3] *= alpha[1];
         }
-        const float ma = m_ref[mt][0] == -INFINITY ? 0.f : -m_ref[mt][0];
-        const float mb = m_ref[mt][1] == -INFINITY ? 0.f : -m_ref[mt][1];
+        const float ma = m_ref[mt][0] == -INFINITY ? 0.f : -m_ref[mt][0] - kHead<KIND>;
+        const float mb = m_ref[mt][1] == -INFINITY ? 0.f : -m_ref[mt][1] - kHead<KIND>;
         const float2 sl = make_float2(p.scale_log2, p.scale_log2);
         float2 sum[2];
 #pragma unroll
@@ -581,7 +589,7 @@ cudaError_t run(const ExtendParams* p, ExtendPlan* plan, cudaStream_t stream) {
   if (plan) {
     plan->tile_rows = C::ROWS;
     plan->occ = occ;
-    plan->lift = 0.f;
+    plan->lift = -kHead<KIND>;
     return cudaSuccess;
   }
   const long long each = (long long)p->num_new * p->G;

@@ -126,10 +126,12 @@ def kvq_prefix_attn(prefix: KVCache | None, cache: KVCache, plan: PrefixPlan, q:
         need = 0 if workspace is not None else \
             kvq_prefix_attn_workspace_size(pd, d, N, B, T, Hq, max_prefix_len, max_seq_len, prefix_splits, tail_splits)
         workspace, ws_bytes = _bytes(workspace, dev, need, "workspace")
+        words = plan.words
         st = _lib.lib().kvq_prefix_attn(
             None if pd is None else byref(pd), None if prefix is None else byref(prefix.ptrs), N, byref(d),
-            byref(cache.ptrs), B, T, Hq, _ptr(q), _ptr(seq_lens_before), _ptr(new_lens), _ptr(plan.words),
-            plan.words.numel() * 4, int(max_prefix_len), int(max_seq_len), int(prefix_splits), int(tail_splits),
-            float(softmax_scale), _ptr(out), _ptr(workspace), ws_bytes, _ptr(dev_status), _handle(dev))
-    _lib.check(st, "kvq_prefix_attn")
+            byref(cache.ptrs), B, T, Hq, q.data_ptr(), seq_lens_before.data_ptr(), _ptr(new_lens), words.data_ptr(),
+            words.numel() * 4, int(max_prefix_len), int(max_seq_len), int(prefix_splits), int(tail_splits),
+            float(softmax_scale), out.data_ptr(), _ptr(workspace), ws_bytes, _ptr(dev_status), _handle(dev))
+    if st:
+        _lib.check(st, "kvq_prefix_attn")
     return out
