@@ -665,6 +665,7 @@ KVQ_API size_t kvq_prefix_plan_size(int32_t batch, int32_t num_prefixes);
  *   prefix_lens  device int32 [num_prefixes]: tokens of each prefix; 0: empty
  *   plan         device, kvq_prefix_plan_size() bytes, 16-byte aligned: read by
  *                kvq_prefix_attn, which needs neither array again
+ *                (may not overlap either of them)
  * Another prefix_of flags KVQ_FLAG_BLOCK_TABLE and counts as none, a negative
  * length KVQ_FLAG_SEQ_LEN and as empty.
  */
@@ -698,6 +699,7 @@ KVQ_API size_t kvq_prefix_find_workspace_size(const kvq_page_pool* pool);
  *   tail_lens      device int32 [batch]: seq_lens_before less the prefix
  *   num_prefixes   device int32 [1] or NULL: prefixes found, those beyond
  *                  max_prefixes among them
+ * No array that is written may overlap another of the call.
  * kvq_prefix_plan takes prefix_of and prefix_lens; kvq_prefix_attn the pool's
  * caches with the two tables and tail_lens.  Appending goes through the pool's
  * own table and lengths.  For per-token caches: an axis-aware sequence's sinks

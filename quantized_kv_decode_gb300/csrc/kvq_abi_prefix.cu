@@ -11,6 +11,24 @@ using namespace kvq;
 
 namespace {
 
+// Arrays of a call: bytes, and whether the call writes it.  One that is written
+// shares no byte with another.
+struct Span {
+  const void* at;
+  size_t bytes;
+  bool out;
+};
+template <int N>
+bool apart(const Span (&spans)[N]) {
+  for (int i = 0; i < N; ++i)
+    for (int j = 0; j < i; ++j) {
+      const Span &a = spans[i], &b = spans[j];
+      const uintptr_t x = (uintptr_t)a.at, y = (uintptr_t)b.at;
+      if ((a.out || b.out) && a.bytes && b.bytes && x && y && x < y + b.bytes && y < x + a.bytes) return false;
+    }
+  return true;
+}
+
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 // One pass's partials: sums of rows * splits, then (maximum, sum) pairs.
@@ -143,6 +161,10 @@ kvq_status kvq_prefix_plan(int32_t batch, int32_t num_prefixes, const int32_t* p
   if ((batch && !prefix_of) || (num_prefixes && !prefix_lens) || !aligned(prefix_of) || !aligned(prefix_lens))
     return KVQ_ERR_INVALID_ARG;
   if (!plan || !aligned(plan) || plan_bytes < kvq_prefix_plan_size(batch, num_prefixes)) return KVQ_ERR_WORKSPACE;
+  const Span spans[] = {{plan, kvq_prefix_plan_size(batch, num_prefixes), true},
+                        {prefix_of, (size_t)batch * 4, false},
+                        {prefix_lens, (size_t)num_prefixes * 4, false}};
+  if (!apart(spans)) return KVQ_ERR_INVALID_ARG;
   PrefixPlanParams p{};
   p.of = prefix_of;
   p.len = prefix_lens;
@@ -175,12 +197,19 @@ kvq_status kvq_prefix_find(const kvq_page_pool* pool, const int32_t* seq_lens_be
   if (!aligned(seq_lens_before) || !aligned(prefix_of) || !aligned(tail_table) || !aligned(tail_lens) ||
       !aligned(num_prefixes))
     return KVQ_ERR_INVALID_ARG;
-  const size_t table = (size_t)pool->batch * pool->max_blocks_per_seq * 4;
-  if (pool->batch && (tail_table == pool->block_table || partly_over(tail_table, pool->block_table, table) ||
-                      tail_lens == seq_lens_before))
-    return KVQ_ERR_INVALID_ARG;
-  if (!workspace || !aligned(workspace) || workspace_bytes < kvq_prefix_find_workspace_size(pool))
-    return KVQ_ERR_WORKSPACE;
+  const size_t need = kvq_prefix_find_workspace_size(pool);
+  if (!workspace || !aligned(workspace) || workspace_bytes < need) return KVQ_ERR_WORKSPACE;
+  const size_t row = (size_t)pool->max_blocks_per_seq * 4, each = (size_t)pool->batch * 4, most = max_prefixes;
+  const Span spans[] = {{pool->block_table, pool->batch * row, false},
+                        {seq_lens_before, each, false},
+                        {prefix_of, each, true},
+                        {prefix_lens, most * 4, true},
+                        {prefix_table, most * row, true},
+                        {tail_table, pool->batch * row, true},
+                        {tail_lens, each, true},
+                        {num_prefixes, 4, true},
+                        {workspace, need, true}};
+  if (!apart(spans)) return KVQ_ERR_INVALID_ARG;
   PrefixFindParams p{};
   p.pool = *pool;
   p.lens = seq_lens_before;

@@ -51,20 +51,22 @@ __device__ __forceinline__ int plan_member(const PrefixPlan& p, int i) {
 // Tile `flat` of the tiles of `rows` rows that all prefixes' members make, one
 // prefix after another (a member is `each` rows): its prefix n (-1: no such
 // tile), its place among that prefix's tiles, and the prefix's members.  Every
-// lane of a warp calls it; 32 prefixes a turn.
+// lane of a warp calls it; 32 prefixes a turn, up to the last that has members.
 struct PrefixTile {
   int n, tile, first, count;
 };
 __device__ __forceinline__ PrefixTile prefix_tile(const PrefixPlan& p, long long flat, int each, int rows) {
   const int lane = threadIdx.x & 31;
+  const int all = __ldg(p.first + p.N);  // members of all prefixes
   for (int base = 0; base < p.N; base += 32) {
     const int n = base + lane;
     int f0 = 0, count = 0;
     if (n < p.N) {
       f0 = min(max(__ldg(p.first + n), 0), p.B);
       count = min(max(__ldg(p.first + n + 1), f0), p.B) - f0;
-      if (__ldg(p.len + n) <= 0) count = 0;
     }
+    const bool last = __any_sync(0xffffffffu, f0 + count >= all);
+    if (n < p.N && __ldg(p.len + n) <= 0) count = 0;
     const int tiles = (int)(((long long)count * each + rows - 1) / rows);
     int upto = tiles;
 #pragma unroll
@@ -82,6 +84,7 @@ __device__ __forceinline__ PrefixTile prefix_tile(const PrefixPlan& p, long long
       t.count = __shfl_sync(0xffffffffu, count, hit);
       return t;
     }
+    if (last) break;
     flat -= total;
   }
   return PrefixTile{-1, 0, 0, 0};

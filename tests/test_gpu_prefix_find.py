@@ -134,3 +134,34 @@ def test_plan_flags_and_refills():
     assert plan.words[:4].tolist() == [1, 1, 1, 1] and plan.words[12:14].tolist() == [0, 9]
     with pytest.raises(ValueError):
         K.kvq_prefix_plan(torch.zeros(5, dtype=torch.int32, device="cuda"), lens, plan=plan)
+
+
+def test_find_and_plan_captured_and_replayed():
+    """One graph of both calls over tables and lengths that change between replays."""
+    import torch
+    rng = np.random.default_rng(11)
+    B, M, page, N = 70, 12, 16, 9
+    tables = [rng.integers(0, 3, size=(B, M)).astype(np.int32) for _ in range(3)]
+    lens = [rng.integers(0, page * M + 1, size=B).astype(np.int32) for _ in range(3)]
+    table, ln = torch.from_numpy(tables[0]).cuda(), torch.from_numpy(lens[0]).cuda()
+    K = __import__("quantized_kv_decode_gb300")
+    pool = K.PagePool(torch.ones(64, dtype=torch.int32, device="cuda"), table, page)
+    i32 = lambda *n: torch.zeros(n, dtype=torch.int32, device="cuda")
+    of, plens, ptab, ttab, tlens, num = i32(B), i32(N), i32(N, M), i32(B, M), i32(B), i32(1)
+    ws = torch.empty(K.kvq_prefix_find_workspace_size(pool), dtype=torch.uint8, device="cuda")
+    plan = K.kvq_prefix_plan(of, plens)
+    run = lambda: (K.kvq_prefix_find(pool, ln, of, plens, ptab, ttab, tlens, num_prefixes=num, workspace=ws),
+                   K.kvq_prefix_plan(of, plens, plan))
+    run()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    for t, n in zip(tables, lens):
+        table.copy_(torch.from_numpy(t))
+        ln.copy_(torch.from_numpy(n))
+        g.replay()
+        got = [x.clone() for x in (of, plens, ptab, ttab, tlens, num, plan.words)]
+        of.fill_(7), plens.fill_(7), plan.words.fill_(7)
+        run()
+        for a, b in zip(got, (of, plens, ptab, ttab, tlens, num, plan.words)):
+            assert torch.equal(a, b)

@@ -72,6 +72,54 @@ def test_long_tails_are_split(fmt):
     s.check(_run(s))
 
 
+@pytest.mark.parametrize("fmt,D", [("int4", 128), ("fp16", 128), ("int2", 128), ("int8", 256)])
+def test_prefixes_far_apart(fmt, D):
+    """Few of many prefixes have members: in the first 32, at the edge of the next,
+    behind many without any; one of them is empty."""
+    plens = np.full(230, 12, dtype=np.int32)
+    plens[[0, 64, 229]] = 40, 0, 75
+    of = [0, 33, 64, 150, 229, 229, 0, -1, 63]
+    s = Shared(fmt, fmt, D, 1, 2, plens, of, [3] * 9, [1] * 9, 1, seed=D)
+    s.check(_run(s))
+    some = Shared(fmt, fmt, D, 1, 2, plens, [0, 31, 5], [3, 0, 9], [1, 2, 1], 2, seed=D)
+    some.check(_run(some))
+
+
+@pytest.mark.parametrize("fmt,members", [("int4", 3), ("int4", 40), ("nf4", 3), ("fp16", 3)])
+def test_pages_beyond_four_gigabytes(fmt, members):
+    """Codes more than 2^32 bytes behind the arrays' start: what the first pages
+    of the pool hold gives the same result to the bit."""
+    import torch
+    import quantized_kv_decode_gb300 as K
+    from tests._prompt import FORMATS
+    bits, g, kw = FORMATS[fmt]
+    D, G, page, P, own = 128, 4, 64, 200, 40
+    far = 2 ** 32 // (page * D * bits // 8) + 100
+    gen = torch.Generator(device="cuda").manual_seed(members)
+    rand = lambda *n: torch.randn(*n, generator=gen, dtype=torch.float16, device="cuda")
+    pkv, tkv, q = [rand(1, P, 1, D) for _ in "kv"], [rand(members, own, 1, D) for _ in "kv"], rand(members, 1, G, D)
+    axes = K.make_rope_axes((32, 32))
+    outs = []
+    for pages in (100, far):
+        desc = K.make_desc(bits, g, 1, D, K.KVQ_PAGED, page, pages, 4, **kw)
+        rows = pages - 1 - torch.arange(4 + members, dtype=torch.int32, device="cuda")
+        table = torch.full((members, 4), -1, dtype=torch.int32, device="cuda")
+        table[:, 0] = rows[4:]
+        tail = K.KVCache.allocate(desc, members, "cuda", table)
+        prefix = tail.with_table(rows[:4].reshape(1, 4).clone())
+        for c, (k, v) in ((prefix, pkv), (tail, tkv)):
+            n, t = k.shape[:2]
+            pos = torch.arange(2 * t, dtype=torch.int32, device="cuda").reshape(1, t, 2).repeat(n, 1, 1)
+            K.kvq_rope_axes_append(c, axes, pos, k, v, torch.zeros(n, dtype=torch.int32, device="cuda"))
+        of = torch.zeros(members, dtype=torch.int32, device="cuda")
+        plan = K.kvq_prefix_plan(of, torch.tensor([P], dtype=torch.int32, device="cuda"))
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        outs.append(K.kvq_prefix_attn(prefix, tail, plan, q, of + own - 1, P, own, dev_status=st).cpu())
+        assert int(st.item()) == 0
+        del tail, prefix
+    assert torch.isfinite(outs[0]).all() and outs[0].any() and torch.equal(*outs)
+
+
 def test_no_new_lens_and_no_prefix_len():
     """Every row live; empty prefixes and a bound of 0 on their lengths."""
     import torch

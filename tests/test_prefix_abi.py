@@ -111,6 +111,7 @@ def test_plan_and_find_refusals(K):
     assert plan(B=-1) == bad and plan(N=-1) == bad and plan(of=None) == bad and plan(lens=None) == bad
     assert plan(of=a + 4) == bad and plan(lens=b + 8) == bad
     assert plan(B=65536) == un and plan(N=65536) == un
+    assert plan(to=a) == bad and plan(to=b) == bad and plan(to=b - 16) == bad
     assert plan(to=None) == ws_err and plan(n=size(5, 2) - 1) == ws_err and plan(to=c + 4) == ws_err
 
     def pool(pages=64, page=16, batch=4, blocks=8, ref=ref, table=table):
@@ -126,6 +127,8 @@ def test_plan_and_find_refusals(K):
     for name in ("lens", "of", "plens", "ptab", "ttab", "tlens"):
         assert find(**{name: None}) == bad and find(**{name: a + 0x900004}) == bad, name
     assert find(ttab=table) == bad and find(ttab=table + 16) == bad and find(tlens=a) == bad and find(num=a + 4) == bad
+    assert find(ptab=table) == bad and find(ptab=table + 64) == bad and find(ptab=e) == bad and find(of=a) == bad
+    assert find(plens=a) == bad and find(num=ws) == bad and find(ws=table) == bad and find(of=c) == bad
     need = lib.kvq_prefix_find_workspace_size(byref(pool()))
     assert need > 0 and find(ws=None) == ws_err and find(n=need - 1) == ws_err and find(ws=ws + 8) == ws_err
     assert lib.kvq_prefix_find_workspace_size(byref(pool(page=0))) == 0
