@@ -51,6 +51,11 @@ __global__ void __launch_bounds__(kPlanWarps * 32) prefix_plan_kernel(const __gr
       len[n] = l;
     }
   }
+  if (n == p.N && lane < 3) {  // the words between the arrays: every word of a plan is its inputs'
+    if (p.B + lane < plan_pad(p.B)) of[p.B + lane] = order[p.B + lane] = 0;
+    if (p.N + 1 + lane < plan_pad(p.N + 1)) first[p.N + 1 + lane] = 0;
+    if (p.N + lane < plan_pad(p.N)) len[p.N + lane] = 0;
+  }
   const int mine = n < p.N ? n : -1;
 #pragma unroll 4
   for (int b0 = 0; b0 < p.B; b0 += 32) {
