@@ -59,8 +59,8 @@ struct PrefixChoice {
 // rows over prefixes of 512 to 16384 tokens (head_dim 64 and 128, INT4, INT8).
 int32_t prefix_splits(const ExtendPlan& plan, int64_t units, int64_t max_len, int64_t rows, int64_t D, int requested,
                       int64_t tail_warps, int64_t tail_keys, double* cost) {
-  static const double kNs[5] = {40, 16, 20, 24, 30};  // a key, by plan.kind
-  static const double kFixed[5] = {200, 550, 650, 128, 128};
+  static const double kNs[5] = {40, 16, 20, 25, 30};  // a key, by plan.kind
+  static const double kFixed[5] = {200, 550, 650, 128, 180};
   const int64_t L = std::max<int64_t>(max_len, 1);
   const int sms = sm_count(), occ = std::max(plan.occ, 1);
   const int64_t slots = (int64_t)std::max(sms, 1) * occ, cap = std::min<int64_t>(ceil_div(L, 128), 64);
@@ -122,7 +122,7 @@ kvq_status choose(const kvq_cache_desc* pd, const kvq_cache_desc* d, int32_t N, 
     const int32_t used = std::min(N, B);
     const int64_t per_prefix = ceil_div(B * each, used);
     double best = 1e300;
-    for (int few = 0; few <= (extend_prefix_few(c->pg) ? 1 : 0); ++few) {
+    for (int few = 0; few <= extend_prefix_few(c->pg, per_prefix); ++few) {
       ExtendPlan plan;
       const cudaError_t e = extend_prefix_plan(c->pg, per_prefix, few, &plan);
       if (e != cudaSuccess) return from_cuda(e);

@@ -438,13 +438,13 @@ cudaError_t extend_plan(const CacheGeom& c, int num_new, int G, ExtendPlan* plan
   return run_tc_any(c, plan->kind, nullptr, plan, nullptr);
 }
 
-cudaError_t extend_prefix_plan(const CacheGeom& c, long long rows, bool few, ExtendPlan* plan) {
-  plan->kind = !takes_tc(c) ? 0 : few ? (rows <= 16 ? 3 : 4) : rows <= 128 ? 1 : 2;
+cudaError_t extend_prefix_plan(const CacheGeom& c, long long rows, int few, ExtendPlan* plan) {
+  plan->kind = !takes_tc(c) ? 0 : few ? 2 + few : rows <= 128 ? 1 : 2;
   if (plan->kind == 0) return run_any<true>(c, nullptr, plan, nullptr);
   return run_prefix_any(c, plan->kind, nullptr, plan, nullptr);
 }
 
-bool extend_prefix_few(const CacheGeom& c) { return takes_rows(c); }
+int extend_prefix_few(const CacheGeom& c, long long rows) { return !takes_rows(c) ? 0 : rows <= 16 ? 1 : 2; }
 
 cudaError_t launch_extend_prefix(const ExtendParams& p, const ExtendPlan& plan, cudaStream_t stream) {
   return plan.kind == 0 ? run_any<true>(p.v.geom, &p, nullptr, stream)

@@ -175,10 +175,11 @@ cudaError_t extend_plan(const CacheGeom& c, int num_new, int G, ExtendPlan* plan
 cudaError_t launch_extend(const ExtendParams& p, const ExtendPlan& plan, cudaStream_t stream);
 // The same without the merge of its splits: partials are left in ws_o, ws_ml.
 cudaError_t launch_extend_partials(const ExtendParams& p, const ExtendPlan& plan, cudaStream_t stream);
-// Over shared prefixes; rows: of a prefix's members together, on average; few: by
-// the kernel for few rows, which takes the caches that extend_prefix_few says.
-cudaError_t extend_prefix_plan(const CacheGeom& c, long long rows, bool few, ExtendPlan* plan);
-bool extend_prefix_few(const CacheGeom& c);
+// Over shared prefixes; rows: of a prefix's members together, on average; few: 1,
+// 2: by the kernel for few rows in tiles of 16, 32, where extend_prefix_few (the
+// tiles worth a look: both, 16, or 0 for caches that it does not take) allows it.
+cudaError_t extend_prefix_plan(const CacheGeom& c, long long rows, int few, ExtendPlan* plan);
+int extend_prefix_few(const CacheGeom& c, long long rows);
 cudaError_t launch_extend_prefix(const ExtendParams& p, const ExtendPlan& plan, cudaStream_t stream);
 // The kernel for few rows over prefixes, 16 (mt 1) or 32 (mt 2).
 cudaError_t run_rows_int4(int D, int mt, const ExtendParams* p, ExtendPlan* plan, cudaStream_t stream);

@@ -1,5 +1,7 @@
 // Shared prefixes: the plan of a batch, the prefixes that a page pool's table
 // holds, and the join of prefix and tail attention.
+#include <algorithm>
+
 #include "kvq_decode_fast.cuh"
 #include "kvq_prefix.cuh"
 #include "kvq_rope.cuh"
@@ -315,71 +317,78 @@ __global__ void __launch_bounds__(kFindWarps * 32) find_tables_kernel(const __gr
 // ---- the join -----------------------------------------------------------
 //
 // out = sum_i 2^(m_i - lift_i - X) o_i / sum_i 2^(m_i - lift_i - X) l_i over the
-// partials of a row, X their largest m - lift.  D / 4 threads a row, four
-// channels each, kJoin partials in flight.
+// partials of a row, X their largest m - lift.  A block takes a token, or some of
+// its heads where tokens are few: D / 4 threads a row, four channels each, kJoin
+// partials in flight.  What a token needs (its sequence, lengths, how many
+// partials) is worked out once for all its heads.
 constexpr int kJoin = 4;
+constexpr int kJoinBlocks = 1216;  // eight an SM
 __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant__ PrefixJoinParams p) {
   pdl_launch_dependents();
   pdl_wait();
   const CacheGeom& c = p.geom;
   // prefixes that do not fit, whether a sequence is on them or not
-  for (long long n = (long long)blockIdx.x * 256 + threadIdx.x; n < p.plan.N; n += (long long)gridDim.x * 256)
-    if (__ldg(p.plan.len + n) > p.prefix_limit) flag(p.status, KVQ_FLAG_SEQ_LEN);
-  const int per = p.D / 4;  // 16, 32 or 64
-  const long long row = (long long)blockIdx.x * (256 / per) + threadIdx.x / per;
-  if (row >= (long long)p.plan.B * p.T * p.Hq) return;
-  const long long tok = row / p.Hq;
-  const int b = (int)(tok / p.T), t = (int)(tok - (long long)b * p.T);
+  if (blockIdx.y == 0)
+    for (long long n = (long long)blockIdx.x * 256 + threadIdx.x; n < p.plan.N; n += (long long)gridDim.x * 256)
+      if (__ldg(p.plan.len + n) > p.prefix_limit) flag(p.status, KVQ_FLAG_SEQ_LEN);
+  const unsigned tok = blockIdx.x;
+  const int b = (int)(tok / (unsigned)p.T), t = (int)(tok - (unsigned)b * p.T);
   const int n_new = new_rows_of(p.new_lens, b, p.T);
   if (t >= n_new) return;
   const int before = checked_len(c, p.tail_before, b, -1);
   const bool fits = before >= 0 && (long long)before + n_new <= p.tail_limit;
-  int use[2] = {0, fits ? (before + n_new + p.part[1].chunk - 1) / p.part[1].chunk : 0};
+  int use = 0, total = fits ? (before + n_new + p.part[1].chunk - 1) / p.part[1].chunk : 0;  // of the prefix, of both
   const int n = __ldg(p.plan.of + b);
-  const int d = threadIdx.x % per * 4;
   if (fits && n >= 0 && n < p.plan.N)
-    use[0] = (prefix_len(p.plan, n, p.prefix_limit) + p.part[0].chunk - 1) / p.part[0].chunk;
-  float M = -INFINITY, den = 0.f;
-  float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-  const int total = use[0] + use[1];
-  for (int s0 = 0; s0 < total; s0 += kJoin) {
-    float2 v[kJoin];
-    float4 x[kJoin];
-    float Mn = M;
+    use = (prefix_len(p.plan, n, p.prefix_limit) + p.part[0].chunk - 1) / p.part[0].chunk;
+  total += use;
+  const int per = p.D / 4, step = 256 / per;  // 16, 32 or 64 threads a row
+  const int d = threadIdx.x % per * 4;
+  for (int h = blockIdx.y * step + threadIdx.x / per; h < p.Hq; h += gridDim.y * step) {
+    const long long row = (long long)tok * p.Hq + h;
+    const long long at0 = row * p.part[0].splits, at1 = row * p.part[1].splits - use;
+    float M = -INFINITY, den = 0.f;
+    float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s0 = 0; s0 < total; s0 += kJoin) {
+      float2 v[kJoin];
+      float4 x[kJoin];
+      float Mn = M;
 #pragma unroll
-    for (int u = 0; u < kJoin; ++u) {
-      const int i = s0 + u, w = i >= use[0];
-      const PrefixPartials& part = p.part[w];
-      const long long at = row * part.splits + (w ? i - use[0] : i);
-      v[u] = make_float2(-INFINITY, 0.f);
-      x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (i < total && KVQ_IN(c, KVQ_ARRAY_WORKSPACE, part.ml + 2 * at, 8) &&
-          KVQ_IN(c, KVQ_ARRAY_WORKSPACE, part.o + at * p.D + d, 16)) {
-        v[u] = *reinterpret_cast<const float2*>(part.ml + 2 * at);
-        v[u].x -= part.lift;
-        x[u] = *reinterpret_cast<const float4*>(part.o + at * p.D + d);
+      for (int u = 0; u < kJoin; ++u) {
+        const int i = s0 + u;
+        const bool pre = i < use;
+        const long long at = (pre ? at0 : at1) + i;
+        const float* const ml = (pre ? p.part[0].ml : p.part[1].ml) + 2 * at;
+        const float* const o = (pre ? p.part[0].o : p.part[1].o) + at * p.D + d;
+        v[u] = make_float2(-INFINITY, 0.f);
+        x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < total && KVQ_IN(c, KVQ_ARRAY_WORKSPACE, ml, 8) && KVQ_IN(c, KVQ_ARRAY_WORKSPACE, o, 16)) {
+          v[u] = *reinterpret_cast<const float2*>(ml);
+          v[u].x -= pre ? p.part[0].lift : p.part[1].lift;
+          x[u] = *reinterpret_cast<const float4*>(o);
+        }
+        Mn = fmaxf(Mn, v[u].x);
       }
-      Mn = fmaxf(Mn, v[u].x);
-    }
-    const float base = Mn == -INFINITY ? 0.f : Mn, a = fast::ex2(M - base);
-    num = make_float4(num.x * a, num.y * a, num.z * a, num.w * a);
-    den *= a;
+      const float base = Mn == -INFINITY ? 0.f : Mn, a = fast::ex2(M - base);
+      num = make_float4(num.x * a, num.y * a, num.z * a, num.w * a);
+      den *= a;
 #pragma unroll
-    for (int u = 0; u < kJoin; ++u) {
-      if (v[u].x == -INFINITY && !(v[u].y != 0.f)) continue;  // nothing seen there
-      const float f = fast::ex2(v[u].x - base);
-      num.x = fmaf(f, x[u].x, num.x);
-      num.y = fmaf(f, x[u].y, num.y);
-      num.z = fmaf(f, x[u].z, num.z);
-      num.w = fmaf(f, x[u].w, num.w);
-      den = fmaf(f, v[u].y, den);
+      for (int u = 0; u < kJoin; ++u) {
+        if (v[u].x == -INFINITY && !(v[u].y != 0.f)) continue;  // nothing seen there
+        const float f = fast::ex2(v[u].x - base);
+        num.x = fmaf(f, x[u].x, num.x);
+        num.y = fmaf(f, x[u].y, num.y);
+        num.z = fmaf(f, x[u].z, num.z);
+        num.w = fmaf(f, x[u].w, num.w);
+        den = fmaf(f, v[u].y, den);
+      }
+      M = Mn;
     }
-    M = Mn;
+    const float inv = den != 0.f ? 1.f / den : 0.f;
+    uint2* to = reinterpret_cast<uint2*>(p.out + row * p.D + d);
+    if (KVQ_IN(c, KVQ_ARRAY_OUT, to, 8))
+      *to = make_uint2(fast::pack_h2(num.x * inv, num.y * inv), fast::pack_h2(num.z * inv, num.w * inv));
   }
-  const float inv = den != 0.f ? 1.f / den : 0.f;
-  uint2* to = reinterpret_cast<uint2*>(p.out + row * p.D + d);
-  if (KVQ_IN(c, KVQ_ARRAY_OUT, to, 8))
-    *to = make_uint2(fast::pack_h2(num.x * inv, num.y * inv), fast::pack_h2(num.z * inv, num.w * inv));
 }
 
 }  // namespace
@@ -402,9 +411,10 @@ cudaError_t launch_prefix_find(const PrefixFindParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_prefix_join(const PrefixJoinParams& p, cudaStream_t stream) {
-  const long long rows = (long long)p.plan.B * p.T * p.Hq;
-  const int per = 256 / (p.D / 4);
-  return launch_pdl(prefix_join_kernel, dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0, stream, p);
+  const long long tokens = (long long)p.plan.B * p.T;
+  const int step = 256 / (p.D / 4), most = (p.Hq + step - 1) / step;
+  const long long slices = std::min<long long>(std::min(most, 65535), (kJoinBlocks + tokens - 1) / tokens);
+  return launch_pdl(prefix_join_kernel, dim3((unsigned)tokens, (unsigned)slices), dim3(256), 0, stream, p);
 }
 
 }  // namespace kvq

@@ -56,7 +56,11 @@ struct RowCfg {
   static constexpr int Q_FRAG = MT * (KB + NZ) * 32 * 16, Q_SUM = MAXNG * ROWS * 4;
   static constexpr int Q_BYTES = Q_FRAG + Q_SUM + ROWS * 4;
   static constexpr int FIXED = Q_BYTES;
-  static constexpr int STAGES_FIT = ((112 * 1024 - FIXED) / kWarps - XHDR) / STAGE;
+  // Blocks an SM: the tile of 16 rows leaves registers for three where its stages
+  // fit (32 heads over 16384 keys, INT4: 49.6 -> 42.8 us with three, over 4096
+  // 20.7 -> 20.3; a block of 32 rows needs all of its 255 registers).
+  static constexpr int CTAS = MT == 1 && BITS == 4 && D == 128 ? 3 : 2;
+  static constexpr int STAGES_FIT = (((CTAS == 3 ? 75 : 112) * 1024 - FIXED) / kWarps - XHDR) / STAGE;
   static constexpr int STAGES = STAGES_FIT > 4 ? 4 : STAGES_FIT;
   static constexpr int WARP_BYTES = STAGES * STAGE + XHDR;
   static constexpr int RED = D + 4;              // floats of a row in the join
@@ -64,7 +68,7 @@ struct RowCfg {
   static constexpr int JOIN = kWarps * ROWS * (RED + 2) * 4;
   static constexpr int SMEM = FIXED + (PIPE > JOIN ? PIPE : JOIN);
   static_assert(STAGES >= 2, "a tile in flight beside the one in use");
-  static_assert(2 * SMEM <= 226 * 1024, "two blocks an SM");
+  static_assert(CTAS * (SMEM + 1024) <= 228 * 1024, "the blocks an SM is to hold");
   __device__ static __forceinline__ uint32_t at(int t, int c) {
     return (uint32_t)(t * ROWB + ((c ^ ((t / RPL) & (CHUNKS - 1))) << 4));
   }
@@ -80,7 +84,7 @@ constexpr float kHead = KIND == 1 ? kSlackRows : 0.f;
 
 // A block takes a prefix, a KV head, a tile of rows and a split.
 template <int BITS, int KIND, int D, int MT>
-__global__ void __launch_bounds__(kWarps * 32, 2) rows_kernel(const __grid_constant__ ExtendParams p) {
+__global__ void __launch_bounds__(kWarps * 32, RowCfg<BITS, KIND, D, MT>::CTAS) rows_kernel(const __grid_constant__ ExtendParams p) {
   using C = RowCfg<BITS, KIND, D, MT>;
   constexpr float kSub = KIND == 1 ? 1.f : 16777216.f;  // 2^24: codes enter as c 2^-24
   extern __shared__ __align__(128) uint8_t smem[];

@@ -23,6 +23,16 @@ def test_rows_of_one_prefix(fmt, D, members):
     s.check(_run(s, prefix_splits=2))
 
 
+@pytest.mark.parametrize("fmt", CODES)
+@pytest.mark.parametrize("D", [64, 128])
+def test_rows_of_many_prefixes(fmt, D):
+    """16 prefixes of 16 KV heads, 32 rows each on average: tiles of 32 rows are
+    one turn over the device, of 16 two."""
+    rng = np.random.default_rng(D)
+    s = _batch(fmt, fmt, D, 16, 4, 1, rng.integers(90, 300, size=16).tolist(), 128, most=20, none=False, seed=D)
+    s.check(_run(s, prefix_splits=1), only=range(0, 128, 5))
+
+
 @pytest.mark.parametrize("page", [8, 16, 24, 64])
 @pytest.mark.parametrize("fmt", CODES)
 def test_rows_over_pages(fmt, page):
