@@ -56,7 +56,9 @@ struct PrefixChoice {
 // the partials are written and read at 6800 bytes a ns.  The tail kernel
 // (tail_warps of them, eight an SM, with tail_keys each) runs beside the pass
 // where that leaves room, and behind it where not.  Fitted to sweeps of 8 to 256
-// rows over prefixes of 512 to 16384 tokens (head_dim 64 and 128, INT4, INT8).
+// rows over prefixes of 512 to 16384 tokens (head_dim 64 and 128, INT4, INT8; some
+// of them at the kernel for few rows): the choice is within 5 % of the best kernel
+// in most of them, 15 % at worst.
 int32_t prefix_splits(const ExtendPlan& plan, int64_t units, int64_t max_len, int64_t rows, int64_t D, int requested,
                       int64_t tail_warps, int64_t tail_keys, double* cost) {
   static const double kNs[5] = {40, 16, 20, 25, 30};  // a key, by plan.kind
@@ -270,6 +272,7 @@ kvq_status kvq_prefix_attn(const kvq_cache_desc* prefix_desc, const kvq_cache* p
   if (c.tail_bytes) carve_partials(reinterpret_cast<char*>(workspace) + c.prefix_bytes, rows, D, c.tail_splits, &to, &tml);
 
   ExtendParams p{};  // what both passes of extend attention share
+  p.partials = 1;
   p.q = reinterpret_cast<const __half*>(q);
   p.status = dev_status;
   p.num_new = num_new;

@@ -477,6 +477,7 @@ kvq_status kvq_extend_attn(const kvq_cache_desc* desc, const kvq_cache* cache, i
   p.Hq = num_q_heads;
   p.G = num_q_heads / desc->num_kv_heads;
   p.splits = choice.splits;
+  p.partials = choice.splits > 1;
   p.chunk = split_chunk(max_seq_len, choice.splits);
   p.len_limit = (int32_t)std::min<int64_t>(cache_capacity(g), max_seq_len);
   const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf((float)desc->head_dim);

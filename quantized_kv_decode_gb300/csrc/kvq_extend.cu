@@ -266,7 +266,7 @@ __device__ __forceinline__ void attend(const ExtendParams& p) {
     const long long r = r0 + warp * 16 + (lane >> 2) + 8 * e;
     if (r >= live_rows) continue;
     const long long orow = row_at(r);
-    if (!PRE && p.ws_o == nullptr) {
+    if (!PRE && !p.partials) {
       const float inv = l[e] != 0.f ? 1.f / l[e] : 0.f;
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) {

@@ -518,7 +518,13 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
       uint4 x[D / 64][8];
 #pragma unroll
       for (int it = 0; it < 8; ++it) {  // (all loads, then the stores)
-        const long long row = __shfl_sync(0xffffffffu, orow, it * 4 + (lane >> 3));
+        long long row;
+        if constexpr (PRE || !C::LO) {
+          row = __shfl_sync(0xffffffffu, orow, it * 4 + (lane >> 3));
+        } else {  // (late chunks over codes: 1094 us by shuffles, 1080 so)
+          const int own = min(row0 + it * 4 + (lane >> 3), (int)live_rows - 1), t2 = own / p.G;
+          row = ((long long)b * p.num_new + t2) * p.Hq + (long long)kvh * p.G + (own - t2 * p.G);
+        }
         const uint4* src = reinterpret_cast<const uint4*>(p.q + row * D) + (lane & 7);
 #pragma unroll
         for (int h = 0; h < D / 64; ++h)
@@ -733,7 +739,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
 #pragma unroll
         for (int e = 0; e < 32; ++e) x[(e & ~7) + C::channel(e & 7)] = __uint_as_float(o[e]);
         // through the scratch, so that lanes write whole lines of a row
-        const bool halves = !PRE && p.ws_o == nullptr;
+        const bool halves = !PRE && !p.partials;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           if (halves && e >= 4) continue;
@@ -765,7 +771,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
         }
         __syncwarp();
       }
-      if ((PRE || p.ws_o != nullptr) && live) {
+      if ((PRE || p.partials) && live) {
         float2* ml = reinterpret_cast<float2*>(p.ws_ml) + orow * p.splits + split;
         if (KVQ_IN(c, KVQ_ARRAY_WORKSPACE, ml, 8)) *ml = make_float2(m, l);
       }

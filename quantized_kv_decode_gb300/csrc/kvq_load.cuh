@@ -144,12 +144,13 @@ struct ExtendParams {
   __half* out;
   const int32_t* lens_before;
   const int32_t* new_lens;
-  float* ws_o;   // [batch * num_new * Hq][splits][D]  (null: one split, written to out)
+  float* ws_o;   // [batch * num_new * Hq][splits][D]  (partials)
   float* ws_ml;  // [batch * num_new * Hq][splits][2]
   uint32_t* status;
   int32_t batch, num_new, Hq, G;
   int32_t splits, chunk;  // chunk: positions per split, a multiple of kChunkAlign
   int32_t len_limit;
+  int32_t partials;  // rows are left in ws_o and ws_ml (0: one split, written to out)
   float scale_log2;
   // Attention over shared prefixes (launch_extend_prefix): the cache's sequences
   // are the plan's prefixes, and a row of the tile is a (member, new token, head)

@@ -19,7 +19,8 @@ __device__ __forceinline__ unsigned lanes_below() { return (1u << (threadIdx.x &
 // A warp per prefix (and one more for the sequences without): it counts the
 // sequences of the prefixes before its own, then writes its own in ascending
 // order.  Integer sums and one writer an entry, so the plan is determined by
-// the inputs.  Bound by latency: two passes over B entries from the L2 cache.
+// the inputs.  Bound by latency: two passes over B entries from the L2 cache (4.9
+// us by itself for 4 to 256 sequences).
 constexpr int kPlanWarps = 8;
 __device__ __forceinline__ int prefix_of(const PrefixPlanParams& p, int b, uint32_t& flags) {
   const int n = __ldg(p.of + b);
@@ -80,8 +81,10 @@ __global__ void __launch_bounds__(kPlanWarps * 32) prefix_plan_kernel(const __gr
 // of the groups (a warp a sequence, the last block numbers them), tables (a warp
 // a row).  Bound by memory latency: keys and (leader, run) pairs are brought to
 // shared memory by the block, rows are read and written 256 entries at a time.
-// 2048 sequences of up to 1012 blocks: 43 us when rows went 128 at a time and
-// every warp looked through the pairs and the groups' savings in global memory.
+// 2048 sequences of up to 1012 blocks: 27 us, of which 17, 9 and 8 by themselves
+// (43 when rows went 128 at a time and every warp looked through the pairs and the
+// groups' savings in global memory); 8 sequences 6.2.  The rows' first entries
+// fetched before the leaders are known: 17.7 -> 26 us of the first kernel.
 // Integer sums and maxima only: the result does not depend on the order.
 constexpr int kFindWarps = 16;
 constexpr int kFindHeld = 4096;  // keys or pairs held in shared memory at a time
@@ -318,11 +321,67 @@ __global__ void __launch_bounds__(kFindWarps * 32) find_tables_kernel(const __gr
 //
 // out = sum_i 2^(m_i - lift_i - X) o_i / sum_i 2^(m_i - lift_i - X) l_i over the
 // partials of a row, X their largest m - lift.  A block takes a token, or some of
-// its heads where tokens are few: D / 4 threads a row, four channels each, kJoin
-// partials in flight.  What a token needs (its sequence, lengths, how many
-// partials) is worked out once for all its heads.
-constexpr int kJoin = 4;
+// its heads where tokens are few: D / 4 threads a row, four channels each.  What a
+// token needs (its sequence, lengths, how many partials) is worked out once for all
+// its heads: with a block for eight rows wherever they lie, each thread dividing for
+// itself, 4800 tokens (half of them live) of 32 heads of 128 took 57 us, 37 so.
+// Bound by instructions (61 % of the issue slots) next to memory (2.5 TB/s).
 constexpr int kJoinBlocks = 1216;  // eight an SM
+
+// The heads of token `tok` that are this block's: partials 0 .. use - 1 are the
+// prefix's, those up to total the tail's; U of them in flight (two are all there
+// are where neither pass is split: XXX).
+template <int U>
+__device__ __forceinline__ void join_rows(const PrefixJoinParams& p, unsigned tok, int use, int total) {
+  const CacheGeom& c = p.geom;
+  const int per = p.D / 4, step = 256 / per;  // 16, 32 or 64 threads a row
+  const int d = threadIdx.x % per * 4;
+  for (int h = blockIdx.y * step + threadIdx.x / per; h < p.Hq; h += gridDim.y * step) {
+    const long long row = (long long)tok * p.Hq + h;
+    const long long at0 = row * p.part[0].splits, at1 = row * p.part[1].splits - use;
+    float M = -INFINITY, den = 0.f;
+    float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s0 = 0; s0 < total; s0 += U) {
+      float2 v[U];
+      float4 x[U];
+      float Mn = M;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = s0 + u;
+        const bool pre = i < use;
+        const long long at = (pre ? at0 : at1) + i;
+        const float* const ml = (pre ? p.part[0].ml : p.part[1].ml) + 2 * at;
+        const float* const o = (pre ? p.part[0].o : p.part[1].o) + at * p.D + d;
+        v[u] = make_float2(-INFINITY, 0.f);
+        x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < total && KVQ_IN(c, KVQ_ARRAY_WORKSPACE, ml, 8) && KVQ_IN(c, KVQ_ARRAY_WORKSPACE, o, 16)) {
+          v[u] = *reinterpret_cast<const float2*>(ml);
+          v[u].x -= pre ? p.part[0].lift : p.part[1].lift;
+          x[u] = *reinterpret_cast<const float4*>(o);
+        }
+        Mn = fmaxf(Mn, v[u].x);
+      }
+      const float base = Mn == -INFINITY ? 0.f : Mn, a = fast::ex2(M - base);
+      num = make_float4(num.x * a, num.y * a, num.z * a, num.w * a);
+      den *= a;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (v[u].x == -INFINITY && !(v[u].y != 0.f)) continue;  // nothing seen there
+        const float f = fast::ex2(v[u].x - base);
+        num.x = fmaf(f, x[u].x, num.x);
+        num.y = fmaf(f, x[u].y, num.y);
+        num.z = fmaf(f, x[u].z, num.z);
+        num.w = fmaf(f, x[u].w, num.w);
+        den = fmaf(f, v[u].y, den);
+      }
+      M = Mn;
+    }
+    const float inv = den != 0.f ? 1.f / den : 0.f;
+    uint2* to = reinterpret_cast<uint2*>(p.out + row * p.D + d);
+    if (KVQ_IN(c, KVQ_ARRAY_OUT, to, 8))
+      *to = make_uint2(fast::pack_h2(num.x * inv, num.y * inv), fast::pack_h2(num.z * inv, num.w * inv));
+  }
+}
 __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant__ PrefixJoinParams p) {
   pdl_launch_dependents();
   pdl_wait();
@@ -342,53 +401,8 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant_
   if (fits && n >= 0 && n < p.plan.N)
     use = (prefix_len(p.plan, n, p.prefix_limit) + p.part[0].chunk - 1) / p.part[0].chunk;
   total += use;
-  const int per = p.D / 4, step = 256 / per;  // 16, 32 or 64 threads a row
-  const int d = threadIdx.x % per * 4;
-  for (int h = blockIdx.y * step + threadIdx.x / per; h < p.Hq; h += gridDim.y * step) {
-    const long long row = (long long)tok * p.Hq + h;
-    const long long at0 = row * p.part[0].splits, at1 = row * p.part[1].splits - use;
-    float M = -INFINITY, den = 0.f;
-    float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s0 = 0; s0 < total; s0 += kJoin) {
-      float2 v[kJoin];
-      float4 x[kJoin];
-      float Mn = M;
-#pragma unroll
-      for (int u = 0; u < kJoin; ++u) {
-        const int i = s0 + u;
-        const bool pre = i < use;
-        const long long at = (pre ? at0 : at1) + i;
-        const float* const ml = (pre ? p.part[0].ml : p.part[1].ml) + 2 * at;
-        const float* const o = (pre ? p.part[0].o : p.part[1].o) + at * p.D + d;
-        v[u] = make_float2(-INFINITY, 0.f);
-        x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (i < total && KVQ_IN(c, KVQ_ARRAY_WORKSPACE, ml, 8) && KVQ_IN(c, KVQ_ARRAY_WORKSPACE, o, 16)) {
-          v[u] = *reinterpret_cast<const float2*>(ml);
-          v[u].x -= pre ? p.part[0].lift : p.part[1].lift;
-          x[u] = *reinterpret_cast<const float4*>(o);
-        }
-        Mn = fmaxf(Mn, v[u].x);
-      }
-      const float base = Mn == -INFINITY ? 0.f : Mn, a = fast::ex2(M - base);
-      num = make_float4(num.x * a, num.y * a, num.z * a, num.w * a);
-      den *= a;
-#pragma unroll
-      for (int u = 0; u < kJoin; ++u) {
-        if (v[u].x == -INFINITY && !(v[u].y != 0.f)) continue;  // nothing seen there
-        const float f = fast::ex2(v[u].x - base);
-        num.x = fmaf(f, x[u].x, num.x);
-        num.y = fmaf(f, x[u].y, num.y);
-        num.z = fmaf(f, x[u].z, num.z);
-        num.w = fmaf(f, x[u].w, num.w);
-        den = fmaf(f, v[u].y, den);
-      }
-      M = Mn;
-    }
-    const float inv = den != 0.f ? 1.f / den : 0.f;
-    uint2* to = reinterpret_cast<uint2*>(p.out + row * p.D + d);
-    if (KVQ_IN(c, KVQ_ARRAY_OUT, to, 8))
-      *to = make_uint2(fast::pack_h2(num.x * inv, num.y * inv), fast::pack_h2(num.z * inv, num.w * inv));
-  }
+  if (total <= 2) join_rows<2>(p, tok, use, total);
+  else join_rows<4>(p, tok, use, total);
 }
 
 }  // namespace

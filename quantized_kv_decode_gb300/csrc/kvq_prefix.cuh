@@ -94,7 +94,7 @@ __device__ __forceinline__ PrefixTile prefix_tile(const PrefixPlan& p, long long
 // batch (rows behind the last: some token of the first member).  Returns the
 // rows there are.  Of a padded batch only live tokens make rows, found by a
 // scan over the members, 32 a turn (24 sequences of 1 to 200 tokens: 442 us with
-// a row for each of the 200, half of them dead, 224 without); one new token a
+// a row for each of the 200, half of them dead, 224 without, when this came); one new token a
 // sequence takes its place in any case.  Every lane of a warp calls it.
 __device__ __forceinline__ int prefix_rows(const PrefixPlan& p, const PrefixTile& pt, const int32_t* new_lens, int T,
                                            int G, long long r, int* tok) {

@@ -1,6 +1,6 @@
 // Attention of 16 or 32 rows over codes that stay in registers (INT4, INT8 and
 // NF4 caches at head_dim 64 and 128): the members of a shared prefix where they
-// are few, and the tails of a few new tokens.
+// are few.
 //
 // Rows are (sequence, new token, head of the KV head's group) triples, as in
 // kvq_extend_tc.cuh.  There the codes pass through shared memory as fp16 sums
@@ -19,8 +19,16 @@
 // and sum per row; the four of a block are joined at the end, and the block
 // leaves a partial.
 //
-// What bounds it: 32 rows of 128 channels over INT4 codes, mma.sync (8 cycles
-// of a key's 16384 products an SM) next to memory (160 bytes, 7 cycles).
+// What bounds it: latency, of unpacking, products and softmax in turn with two or
+// three warps a scheduler (32 heads x 32 rows over 4096 keys, INT4: 43 % of the
+// issue slots, 18 % of the tensor pipe, 0.7 TB/s; 23 us by itself, cold).  Against
+// the kernel of kvq_extend_tc.cuh, the whole call with tails of 64 keys, 8 KV heads
+// of 128 over INT4: 8 rows over 512, 4096, 16384 keys 8.0, 12.7, 20.5 us (12.7,
+// 16.5, 31.0 there), 32 rows 9.4, 16.6, 26.9 (13.5, 20.5, 33.5), 64 rows 10.9, 20.4,
+// 37.7 (13.6, 22.0, 34.7).  Tiles of 16 rows against tiles of 32: 32 rows of 8 heads
+// over 512 keys 9.4 against 11.1 us (INT8: 10.3, 14.0), of 32 heads over 16384 72.9
+// against 67.4.  Sixteen keys are taken at a time: 32 held more registers than there
+// are (108 spilled accesses a tile).
 #pragma once
 
 #include "kvq_decode_fast.cuh"
