@@ -504,7 +504,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
     // this lane's row in q, out and the partials
     const int t = live ? r / p.G : 0;
     const long long orow = (PRE ? (long long)own_tok : (long long)b * p.num_new + t) * p.Hq + (long long)kvh * p.G +
-                           (live ? r - t * p.G : 0);
+                           (live ? r % p.G : 0);
     // (rows behind the last take part with q = 0 and are not written)
     const int last = live && !PRE ? before + t : 0x7fffffff;
     const int mine = C::DUAL ? (tiles + 1 - i) / 2 : tiles;  // this stream's key tiles
@@ -521,7 +521,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
         long long row;
         if constexpr (PRE || !C::LO) {
           row = __shfl_sync(0xffffffffu, orow, it * 4 + (lane >> 3));
-        } else {  // (late chunks over codes: 1094 us by shuffles, 1080 so)
+        } else {  // (late chunks over codes: 1095 us by shuffles, 1070 so)
           const int own = min(row0 + it * 4 + (lane >> 3), (int)live_rows - 1), t2 = own / p.G;
           row = ((long long)b * p.num_new + t2) * p.Hq + (long long)kvh * p.G + (own - t2 * p.G);
         }

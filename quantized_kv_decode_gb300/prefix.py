@@ -86,7 +86,7 @@ def kvq_prefix_attn_workspace_size(prefix_desc, desc, num_prefixes, batch, num_n
                                    max_seq_len, prefix_splits=0, tail_splits=0) -> int:
     return int(_lib.lib().kvq_prefix_attn_workspace_size(
         None if prefix_desc is None else byref(prefix_desc), byref(desc), num_prefixes, batch, num_new, num_q_heads,
-        max_prefix_len, max_seq_len, prefix_splits, tail_splits))
+        int(max_prefix_len), int(max_seq_len), int(prefix_splits), int(tail_splits)))
 
 
 def kvq_prefix_attn(prefix: KVCache | None, cache: KVCache, plan: PrefixPlan, q: torch.Tensor,
