@@ -324,13 +324,14 @@ __global__ void __launch_bounds__(kFindWarps * 32) find_tables_kernel(const __gr
 // its heads where tokens are few: D / 4 threads a row, four channels each.  What a
 // token needs (its sequence, lengths, how many partials) is worked out once for all
 // its heads: with a block for eight rows wherever they lie, each thread dividing for
-// itself, 4800 tokens (half of them live) of 32 heads of 128 took 57 us, 37 so.
-// Bound by instructions (61 % of the issue slots) next to memory (2.5 TB/s).
+// itself, 4800 tokens (half of them live) of 32 heads of 128 took 57 us by itself
+// and cold, 37 so, 29 with the pairs of unsplit passes joined without a loop.  Bound
+// by instructions and latency (53 % of the issue slots at 3.2 TB/s).
 constexpr int kJoinBlocks = 1216;  // eight an SM
 
 // The heads of token `tok` that are this block's: partials 0 .. use - 1 are the
 // prefix's, those up to total the tail's; U of them in flight (two are all there
-// are where neither pass is split: XXX).
+// are where neither pass is split: 195 -> 188 us of the call with those tokens).
 template <int U>
 __device__ __forceinline__ void join_rows(const PrefixJoinParams& p, unsigned tok, int use, int total) {
   const CacheGeom& c = p.geom;
