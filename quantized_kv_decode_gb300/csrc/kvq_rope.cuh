@@ -130,43 +130,26 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
       : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
   return d;
 }
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("add.rn.f32x2 %0, %1, %2;\n"
-      : "=l"(*reinterpret_cast<unsigned long long*>(&d))
-      : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
-  return d;
-}
 __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 // y0 in the low half, y1 in the high one.  e: 1.0625 2^-24 max(amplitude, 1).
 // sure: whether the rounding is settled; if not, rotate_long tells.
-// PAIRS: the bounds in two-wide arithmetic (the same roundings).  In the append of
-// the half layout it pays (2 x 4095 tokens, INT8: 49.3 -> 43.9 us with the
-// read-back); the rotation by itself and the interleaved append take more moves
-// for it (4 x 8191 tokens: 75.3 -> 78.4; 256 x 1, INT4: 9.4 -> 11.1).
-template <bool PAIRS>
+// (The bounds in two-wide arithmetic too take more moves than they save: 4 x 8191
+// tokens 75.3 -> 78.4 us, appends of 4 x 8192 264 -> 276, of 256 x 1 9.4 -> 11.1; only
+// where few tokens are live do they pay, 1684 of 8190 24.9 -> 22.4.)
 __device__ __forceinline__ uint32_t rotate_pair(const Turn& t, float e, float x0, float x1, bool& sure) {
   const float2 x = make_float2(x0, x1), o = make_float2(-x1, x0);
   float2 r = mul2(x, make_float2(t.cl, t.cl));
   r = fma2(o, make_float2(t.sl, t.sl), r);
   r = fma2(o, make_float2(t.sh, t.sh), r);
   r = fma2(x, make_float2(t.ch, t.ch), r);
-  const float2 a = make_float2(fabsf(x1) + fabsf(r.x), fabsf(x0) + fabsf(r.y));
-  float2 above, below;
-  if constexpr (PAIRS) {
-    const float2 d = mul2(a, make_float2(e, e));
-    above = add2(r, d), below = fma2(d, make_float2(-1.f, -1.f), r);
-  } else {
-    const float d0 = __fmul_rn(a.x, e), d1 = __fmul_rn(a.y, e);
-    above = make_float2(r.x + d0, r.y + d1), below = make_float2(r.x - d0, r.y - d1);
-  }
-  const uint32_t up = half2_bits(above.x, above.y);
+  const float d0 = __fmul_rn(fabsf(x1) + fabsf(r.x), e), d1 = __fmul_rn(fabsf(x0) + fabsf(r.y), e);
+  const uint32_t up = half2_bits(r.x + d0, r.y + d1);
   // (an infinity among the inputs makes a NaN of x lo: the long way tells)
   const __half2 u = *reinterpret_cast<const __half2*>(&up);
-  sure = up == half2_bits(below.x, below.y) && __hbeq2(u, u);
+  sure = up == half2_bits(r.x - d0, r.y - d1) && __hbeq2(u, u);
   return up;
 }
 __device__ __forceinline__ uint32_t rotate_long(const Turn& t, float x0, float x1) {
@@ -184,7 +167,7 @@ __device__ __forceinline__ uint32_t pick(const uint4& v, int i) {
 // is x0[i]) turned by t[i * stride]: y0 and y1 laid out as x0 and x1.  The
 // pairs that plain arithmetic leaves open are gone over one at a time, so
 // that the long way is there once.
-template <int N, bool INTER, bool PAIRS>
+template <int N, bool INTER>
 __device__ __forceinline__ void rotate_chunk(const Turn* t, int stride, float e, const uint4& x0v, const uint4& x1v,
                                              uint4& y0v, uint4& y1v) {
   const uint32_t x0[4] = {x0v.x, x0v.y, x0v.z, x0v.w}, x1[4] = {x1v.x, x1v.y, x1v.z, x1v.w};
@@ -196,7 +179,7 @@ __device__ __forceinline__ void rotate_chunk(const Turn* t, int stride, float e,
     const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&a));
     const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&b));
     bool sure;
-    const uint32_t r = rotate_pair<PAIRS>(t[i * stride], e, (!INTER && (i & 1)) ? fa.y : fa.x,
+    const uint32_t r = rotate_pair(t[i * stride], e, (!INTER && (i & 1)) ? fa.y : fa.x,
                                    INTER ? fa.y : (i & 1) ? fb.y : fb.x, sure);
     if (!sure) open |= 1u << i;
     if (INTER) {

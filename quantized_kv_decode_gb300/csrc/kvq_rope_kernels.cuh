@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kWarps * 32)
             if (KVQ_IN(c, KVQ_ARRAY_K_NEW, oth, 16)) u = __ldg(oth);
           }
           const uint4 x0 = upper ? u : v, x1 = upper ? v : u;
-          rope::rotate_chunk<P, INTER, BITS != 0 && !INTER>(turn + item, rot, e, x0, x1, o0, o1);
+          rope::rotate_chunk<P, INTER>(turn + item, rot, e, x0, x1, o0, o1);
           v = upper ? o1 : o0;
         }
       }
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(kWarps * 32)
         continue;
       }
       uint4 y0, y1;
-      rope::rotate_chunk<P, INTER, BITS != 0 && !INTER>(turn + item, rot, e, x0[u], x1[u], y0, y1);
+      rope::rotate_chunk<P, INTER>(turn + item, rot, e, x0[u], x1[u], y0, y1);
       *reinterpret_cast<uint4*>(dst) = y0;
       if (!INTER) *reinterpret_cast<uint4*>(dst + pairs) = y1;
     }
@@ -443,9 +443,8 @@ cudaError_t launch_warp(const Params& p, cudaStream_t stream) {
   while (slices < passes && total * slices < 1216) slices *= 2;
   // An append's tokens take about as much beside the turns (the quantizer), and
   // padded batches hold fewer tokens than they have room for: two warps a token up
-  // to 12288 (2 x 4095 tokens all live, INT8: 102.8 us with one, 103.5 with two;
-  // 1685 of them live 44.4 and 32.3, 4 x 2000 with 4379 live 69 and 64; 4 x 8191
-  // 352 and 379).
+  // to 12288 (INT8, 2 x 4095 tokens all live 76.9 us with one, 78.4 with two; 1684
+  // of them live 40.3 and 24.9, 4 x 2000 with 4380 live 52.1 and 47.7).
   if (BITS && slices == 1 && passes > 1 && total <= 12288) slices = 2;
   const long long warps = total * slices;
   const dim3 grid((unsigned)((warps + kWarps - 1) / kWarps));
