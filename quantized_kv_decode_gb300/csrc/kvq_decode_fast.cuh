@@ -572,7 +572,7 @@ __global__ void __launch_bounds__(ONE ? kWarps * 32 : Cfg<BITS, D, NG, GP, KCH>:
     // prefixes that do not fit, whether a sequence is on them or not
     for (long long n = (long long)blockIdx.x * (kWarps * 32) + threadIdx.x; n < p.join.N; n += (long long)gridDim.x * (kWarps * 32))
       if (__ldg(p.join.len + n) > p.join.limit && p.status) atomicOr(p.status, KVQ_FLAG_SEQ_LEN);
-    if (b >= p.batch || (p.tail_new && __ldg(p.tail_new + b) == 0)) {  // (no new token: its row stays)
+    if (b >= p.batch) {
       if (p.join.early) pdl_wait();
       return;
     }
@@ -581,6 +581,12 @@ __global__ void __launch_bounds__(ONE ? kWarps * 32 : Cfg<BITS, D, NG, GP, KCH>:
   if (L < 0 || L > p.len_limit) {
     if ((ONE ? lane + sub : threadIdx.x) == 0 && split == 0 && kvh == 0 && p.status) atomicOr(p.status, KVQ_FLAG_SEQ_LEN);
     L = 0;
+  }
+  if constexpr (ONE) {
+    if (new_rows_of(p.tail_new, b, 1) != 1) {  // no new token, or a count that cannot be: its row stays
+      if (p.join.early) pdl_wait();
+      return;
+    }
   }
   const int t0 = split * p.chunk;
   const int t1 = min(L, t0 + p.chunk);

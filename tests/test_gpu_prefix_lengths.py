@@ -1,0 +1,42 @@
+"""GPU tests of kvq_prefix_attn on lengths and counts that cannot be, one new
+token a sequence: whichever kernel takes the tails, the call flags them and
+leaves or zeroes the rows that kvq.h names."""
+import numpy as np
+import pytest
+
+from tests.test_gpu_prefix_attn import _batch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("tail_splits", [0, 2])
+@pytest.mark.parametrize("fmt,D", [("int4", 64), ("int4", 128), ("int8", 64), ("int8", 128), ("int2", 128), ("sym4", 128),
+                                   ("sym8", 128), ("nf4", 64), ("nf4", 128), ("fp16", 128)])
+def test_counts_and_lengths_of_one_new_token(fmt, D, tail_splits):
+    """A count outside {0, 1}: flagged, the row left.  No new token: the row left,
+    a length that cannot be flagged all the same.  One new token behind a length
+    that does not fit: flagged, a zero row."""
+    import torch
+    s = _batch(fmt, fmt, D, 2, 2, 1, [50, 20], 7, none=False)
+    K, st = s.K, torch.zeros(1, dtype=torch.int32, device="cuda")
+    s.dev["new"].fill_(1)
+    s.new[:] = 1
+    s.before[:] = np.minimum(s.before, s.L - 1)
+    s.dev["before"].copy_(torch.from_numpy(s.before))
+    for new, before, flagged, row in ((2, None, True, "left"), (-1, None, True, "left"), (1 << 30, None, True, "left"),
+                                      (0, None, False, "left"), (0, -1, True, "left"), (0, s.L + 1, True, "left"),
+                                      (1, -1, True, "zero"), (1, s.L, True, "zero"), (1, 0x7fffffff, True, "zero")):
+        for b in (0, 6):
+            lens, counts = s.dev["before"].clone(), s.dev["new"].clone()
+            counts[b] = new
+            if before is not None:
+                lens[b] = before
+            st.zero_()
+            out = torch.full(s.q.shape, 7.0, dtype=torch.float16, device="cuda")
+            K.kvq_prefix_attn(s.prefix, s.tail, s.plan, s.dev["q"], lens, s.P, s.L, new_lens=counts, out=out,
+                              dev_status=st, tail_splits=tail_splits)
+            o = out.cpu().numpy()
+            what = (new, before, b)
+            assert int(st.item()) == (K.KVQ_FLAG_SEQ_LEN if flagged else 0), what
+            assert (o[b] == (7.0 if row == "left" else 0.0)).all(), what
+            s.check(o, only=[x for x in range(s.B) if x != b])
