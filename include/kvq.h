@@ -744,7 +744,11 @@ KVQ_API size_t kvq_prefix_attn_workspace_size(const kvq_cache_desc* prefix_desc,
  * (A row of q without a new token may be read, to no effect; its row of out is
  * not written.)
  * Axis-aware caches: a prefix's length is all that has been appended to it.
- * Precision: over the prefix as in kvq_extend_attn, over the tail as in
+ * Precision: over the prefix as in kvq_extend_attn; INT4, INT8 and NF4 caches
+ * may, where rows are few, take codes, scales and zero-points apart: a weight
+ * times V's scale is then rounded to fp16 once more (11 bits, down to 2^-25 of
+ * the row's largest weight times the group's largest scale), and the sums of
+ * codes and of zero-points in fp32 are subtracted.  Over the tail as in
  * kvq_decode_attn (one new token, shapes its tensor-core kernels take) or
  * kvq_extend_attn; the partial results are joined in fp32.  A tail whose length
  * exceeds min(max_seq_len, its cache's capacity) flags KVQ_FLAG_SEQ_LEN and

@@ -82,19 +82,33 @@ struct RowCfg {
   }
 };
 
-// How far (log2 units) a tile's maximum may lead the reference.  A probability,
-// at most 2^kSlackRows, times V's scale stays within fp16 for any V that fp16 holds:
-// INT4 scales reach 9358 (absmax 65504 over 7), times 4.  NF4 scales reach 65504:
-// there the probabilities carry 2^-kSlackRows (kHead).
+// How far (log2 units) a tile's maximum may lead the reference, and the factor that
+// the probabilities carry, so that they keep fp16's 11 bits down to 2^-21 of the
+// row's reference.
 constexpr float kSlackRows = 2.f;
-template <int KIND>
-constexpr float kHead = KIND == 1 ? kSlackRows : 0.f;
+constexpr float kLiftRows = 7.f;
+
+// A probability enters times V's scale, as fp16.  V's scales may be of any size, so
+// a warp takes those of a group times a power of two, exactly: the largest seen
+// comes to 2^4 .. 2^6.  A product is then at most 2^(2 + 7 + 6), and that of the
+// reference with the largest scale is 2^11 at least: the bits of smaller ones last
+// to 2^-25 of it (without the power, INT8 groups at 0.02 lost theirs from 2^-8 of the
+// row's largest on, 1.8e-2 of the result where one heavy key's V was small).  A
+// group's power, as the fp16 exponent that its scales stay within: it only rises,
+// and the group's sums come down with it.
+struct ScalePower {
+  // the exponent of a scale, and the one to allow for it: a binade more
+  __device__ static __forceinline__ uint32_t field(uint32_t bits) { return (bits & 0x7FFFu) >> 10; }
+  __device__ static __forceinline__ float factor(uint32_t allowed) { return __uint_as_float((147u - allowed) << 23); }    // 2^(20 - allowed)
+  __device__ static __forceinline__ float inverse(uint32_t allowed) { return __uint_as_float((107u + allowed) << 23); }
+};
 
 // A block takes a prefix, a KV head, a tile of rows and a split.
 template <int BITS, int KIND, int D, int MT>
 __global__ void __launch_bounds__(kWarps * 32, RowCfg<BITS, KIND, D, MT>::CTAS) rows_kernel(const __grid_constant__ ExtendParams p) {
   using C = RowCfg<BITS, KIND, D, MT>;
   constexpr float kSub = KIND == 1 ? 1.f : 16777216.f;  // 2^24: codes enter as c 2^-24
+  constexpr int NT = C::CHUNKS * C::FPC;                // n-tiles of V: D / 8
   extern __shared__ __align__(128) uint8_t smem[];
   const CacheGeom& geo = p.v.geom;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -278,7 +292,13 @@ __global__ void __launch_bounds__(kWarps * 32, RowCfg<BITS, KIND, D, MT>::CTAS) 
   __syncthreads();
 
   // ---- running state ----
-  constexpr int NT = C::CHUNKS * C::FPC;  // n-tiles of V: D / 8
+  uint32_t power = 0;  // of each group, a byte (ScalePower)
+  // Group g's entry of four (registers: the index is a constant but for the rows of
+  // two groups in a kernel for four).
+  auto of_chunk = [&](const float (&x)[C::MAXNG], int chunk) {
+    const int full = chunk * C::MAXNG / C::CHUNKS, half = chunk * 2 / C::CHUNKS;
+    return NG == C::MAXNG ? x[full] : x[half];
+  };
   float o[MT][NT][4], cz[MT][4], m_ref[MT][2], l_run[MT][2];
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
@@ -302,13 +322,41 @@ __global__ void __launch_bounds__(kWarps * 32, RowCfg<BITS, KIND, D, MT>::CTAS) 
     // headers: a lane its key's, to [group][key]
     {
       const uint16_t* h = reinterpret_cast<const uint16_t*>(st + 2 * C::CODE_TILE) + lane * NG;
+      uint32_t allowed = power;
+#pragma unroll
+      for (int g = 0; g < C::MAXNG; ++g) {
+        if (g >= NG) break;
+        const uint32_t top = ScalePower::field(__reduce_max_sync(0xffffffffu, h[C::HDR_TILE + g] & 0x7FFFu));
+        if (top > (power >> (8 * g) & 255u)) allowed = (allowed & ~(255u << (8 * g))) | (top + 1) << (8 * g);
+      }
+      if (allowed != power) {  // the sums so far come down with their groups' powers
+        float down[C::MAXNG];
+#pragma unroll
+        for (int g = 0; g < C::MAXNG; ++g)
+          down[g] = ScalePower::factor(allowed >> (8 * g) & 255u) * ScalePower::inverse(power >> (8 * g) & 255u);
+        power = allowed;
+        // (cz: group g's column, of lanes j = g / 2)
+        const float c0 = C::MAXNG == 4 && j == 1 ? down[C::MAXNG - 2] : down[0];
+        const float c1 = C::MAXNG == 4 && j == 1 ? down[C::MAXNG - 1] : down[1];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          cz[mt][0] *= c0, cz[mt][1] *= c1, cz[mt][2] *= c0, cz[mt][3] *= c1;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const float f = of_chunk(down, n / C::FPC);
+            o[mt][n][0] *= f, o[mt][n][1] *= f, o[mt][n][2] *= f, o[mt][n][3] *= f;
+          }
+        }
+      }
       constexpr uint16_t half_range = BITS == 4 ? 0x4800u : 0x5800u;  // 8, 128
 #pragma unroll
       for (int g = 0; g < C::MAXNG; ++g) {
         if (g >= NG) break;
         const float s = __half2float(__ushort_as_half(h[g]));
         ksc[g * C::KROW + lane] = s * kSub;
-        vs[g * C::VROW + lane] = h[C::HDR_TILE + g];
+        vs[g * C::VROW + lane] =
+            __half_as_ushort(__float2half_rn(__half2float(__ushort_as_half(h[C::HDR_TILE + g])) *
+                                             ScalePower::factor(power >> (8 * g) & 255u)));
         if constexpr (KIND == 0) {
           const float sz = s * __half2float(__ushort_as_half(zeros ? h[C::HDR_TILE / 2 + g] : half_range));
           const __half hi = __float2half_rn(fminf(fmaxf(sz, -65504.f), 65504.f));
@@ -439,8 +487,8 @@ __global__ void __launch_bounds__(kWarps * 32, RowCfg<BITS, KIND, D, MT>::CTAS) 
           for (int n = 0; n < NT; ++n)
             o[mt][n][0] *= alpha[0], o[mt][n][1] *= alpha[0], o[mt][n][2] *= alpha[1], o[mt][n][3] *= alpha[1];
         }
-        const float ma = m_ref[mt][0] == -INFINITY ? 0.f : -m_ref[mt][0] - kHead<KIND>;
-        const float mb = m_ref[mt][1] == -INFINITY ? 0.f : -m_ref[mt][1] - kHead<KIND>;
+        const float ma = m_ref[mt][0] == -INFINITY ? 0.f : -m_ref[mt][0] + kLiftRows;
+        const float mb = m_ref[mt][1] == -INFINITY ? 0.f : -m_ref[mt][1] + kLiftRows;
         const float2 sl = make_float2(p.scale_log2, p.scale_log2);
         float2 sum[2];
 #pragma unroll
@@ -516,6 +564,9 @@ __global__ void __launch_bounds__(kWarps * 32, RowCfg<BITS, KIND, D, MT>::CTAS) 
 
   // ---- the sums, zero-points taken off: in place, four (INT8: two) channels of
   // a row side by side ----
+  float up[C::MAXNG];
+#pragma unroll
+  for (int g = 0; g < C::MAXNG; ++g) up[g] = ScalePower::inverse(power >> (8 * g) & 255u);
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
@@ -526,14 +577,14 @@ __global__ void __launch_bounds__(kWarps * 32, RowCfg<BITS, KIND, D, MT>::CTAS) 
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int f = n % C::FPC, g = (n / C::FPC) >> lcpg;
-      const float fac = kSub * (BITS == 4 && KIND == 0 && (f & 1) ? 0.0625f : 1.f);
+      const float back = of_chunk(up, n / C::FPC), fac = back * (kSub * (BITS == 4 && KIND == 0 && (f & 1) ? 0.0625f : 1.f));
 #pragma unroll
       for (int e = 0; e < 2; ++e) {  // group g's sum lies in column g: lane g / 2, one of its two
         float corr = 0.f;
         if constexpr (KIND == 0) {
           const float c0 = __shfl_sync(0xffffffffu, cz[mt][2 * e], (rho << 2) | (g >> 1));
           const float c1 = __shfl_sync(0xffffffffu, cz[mt][2 * e + 1], (rho << 2) | (g >> 1));
-          corr = (g & 1) ? c1 : c0;
+          corr = ((g & 1) ? c1 : c0) * back;
         }
         o[mt][n][2 * e] = o[mt][n][2 * e] * fac - corr;
         o[mt][n][2 * e + 1] = o[mt][n][2 * e + 1] * fac - corr;
@@ -601,7 +652,7 @@ cudaError_t run(const ExtendParams* p, ExtendPlan* plan, cudaStream_t stream) {
   if (plan) {
     plan->tile_rows = C::ROWS;
     plan->occ = occ;
-    plan->lift = -kHead<KIND>;
+    plan->lift = kLiftRows;
     return cudaSuccess;
   }
   const long long each = (long long)p->num_new * p->G;
