@@ -200,44 +200,92 @@ __global__ void __launch_bounds__(kWarps * 32, RowCfg<BITS, KIND, D, MT>::CTAS) 
   for (int s = 0; s < C::STAGES; ++s) mask_of[s] = issue(s, s);
 
   // ---- q as fragments, its channels in the order the codes are unpacked in ----
+  //
+  // Integer codes: a row of q enters times a power of two, which the softmax takes
+  // back, so that its largest channel comes to 2^7 .. 2^8.  The sums over groups then
+  // fit fp16's range (as q stood, 32 channels above 2047 did not), and q / 16 is exact
+  // but for channels below 2^-17 of the largest.
   if (warp == 0 && lane < C::ROWS) toks[lane] = own_tok;
+  constexpr int QI = (MT * C::CHUNKS + kWarps - 1) / kWarps;  // chunks of rows rho and rho + 8 that a warp takes
+  uint32_t qx[QI][2][4];
+  uint16_t* const tops = reinterpret_cast<uint16_t*>(q_sum);  // [chunk][row]: the largest finite channel
+  static_assert(C::CHUNKS * 2 <= C::MAXNG * 4, "they fit where the sums come to lie");
 #pragma unroll
-  for (int i = 0; i < MT * C::CHUNKS; ++i) {  // a chunk of channels of rows rho and rho + 8
-    if (i % kWarps != warp) continue;
-    const int mt = i / C::CHUNKS, c = i % C::CHUNKS;
-    uint32_t x[2][4] = {};
+  for (int n = 0; n < QI; ++n) {
+    const int i = n * kWarps + warp, mt = i / C::CHUNKS, c = i % C::CHUNKS;
+    if (i >= MT * C::CHUNKS) break;
 #pragma unroll
     for (int hh = 0; hh < 2; ++hh) {
+      qx[n][hh][0] = qx[n][hh][1] = qx[n][hh][2] = qx[n][hh][3] = 0u;
       const int r = mt * 16 + rho + 8 * hh;
       const int tok = __shfl_sync(0xffffffffu, own_tok, r);
-      if (r0 + r >= live_rows) continue;
-      const __half* from = p.q + ((long long)tok * p.Hq + (long long)kvh * p.G + (r0 + r) % p.G) * D + c * C::DPC + j * (C::DPC / 4);
-      if constexpr (BITS == 4) {
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (KVQ_IN(geo, KVQ_ARRAY_Q, from, 16)) v = __ldg(reinterpret_cast<const uint4*>(from));
-        x[hh][0] = v.x, x[hh][1] = v.y, x[hh][2] = v.z, x[hh][3] = v.w;
-      } else {
-        uint2 v = make_uint2(0u, 0u);
-        if (KVQ_IN(geo, KVQ_ARRAY_Q, from, 8)) v = __ldg(reinterpret_cast<const uint2*>(from));
-        x[hh][0] = v.x, x[hh][1] = v.y;
+      if (r0 + r < live_rows) {
+        const __half* from = p.q + ((long long)tok * p.Hq + (long long)kvh * p.G + (r0 + r) % p.G) * D + c * C::DPC + j * (C::DPC / 4);
+        if constexpr (BITS == 4) {
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (KVQ_IN(geo, KVQ_ARRAY_Q, from, 16)) v = __ldg(reinterpret_cast<const uint4*>(from));
+          qx[n][hh][0] = v.x, qx[n][hh][1] = v.y, qx[n][hh][2] = v.z, qx[n][hh][3] = v.w;
+        } else {
+          uint2 v = make_uint2(0u, 0u);
+          if (KVQ_IN(geo, KVQ_ARRAY_Q, from, 8)) v = __ldg(reinterpret_cast<const uint2*>(from));
+          qx[n][hh][0] = v.x, qx[n][hh][1] = v.y;
+        }
+      }
+      if constexpr (KIND == 0) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int e = 0; e < 2 * (C::DPC / 8); ++e) {
+          const uint32_t h = qx[n][hh][e >> 1] >> (16 * (e & 1)) & 0x7FFFu;
+          top = max(top, h < 0x7C00u ? h : 0u);
+        }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        if (j == 0) tops[c * C::ROWS + r] = (uint16_t)top;
       }
     }
+  }
+  if constexpr (KIND == 0) __syncthreads();
+  float unit[MT][2];                      // scores to log2 units
+  uint32_t lift[MT][2], lift_odd[MT][2];  // the row's power (fp16, twice), and where channels meet 16 c
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+      unit[mt][hh] = p.scale_log2;
+      lift[mt][hh] = lift_odd[mt][hh] = 0x3C003C00u;  // 1
+      if constexpr (KIND == 0) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int c = 0; c < C::CHUNKS; ++c) top = max(top, (uint32_t)tops[c * C::ROWS + mt * 16 + rho + 8 * hh]);
+        const int a = min(22 - (int)(top >> 10), 15);  // -8 .. 15
+        unit[mt][hh] *= __int_as_float((127 - a) << 23);
+        lift[mt][hh] = (uint32_t)(15 + a) * 0x04000400u;
+        lift_odd[mt][hh] = (uint32_t)(11 + a) * 0x04000400u;
+      }
+    }
+#pragma unroll
+  for (int n = 0; n < QI; ++n) {
+    const int i = n * kWarps + warp, mt = i / C::CHUNKS, c = i % C::CHUNKS;
+    if (i >= MT * C::CHUNKS) break;
+    const __half2 f0 = u32_as_h2(mt ? lift[MT - 1][0] : lift[0][0]), f1 = u32_as_h2(mt ? lift[MT - 1][1] : lift[0][1]);
     uint4* const to = q_frag + (mt * C::KB + c * C::KPC) * 32 + lane;
     if constexpr (BITS == 4) {
       // channels 8j + (0, 4, 1, 5), then + (2, 6, 3, 7); the odd ones meet
       // nibbles held as 16 c
-      const __half2 odd = u32_as_h2(KIND == 0 ? kH1_16 : 0x3C003C00u);
+      const __half2 g0 = u32_as_h2(mt ? lift_odd[MT - 1][0] : lift_odd[0][0]);
+      const __half2 g1 = u32_as_h2(mt ? lift_odd[MT - 1][1] : lift_odd[0][1]);
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk) {
         uint4 f;
-        f.x = prmt_b32(x[0][kk], x[0][2 + kk], 0x5410u);
-        f.y = prmt_b32(x[1][kk], x[1][2 + kk], 0x5410u);
-        f.z = h2_as_u32(__hmul2(u32_as_h2(prmt_b32(x[0][kk], x[0][2 + kk], 0x7632u)), odd));
-        f.w = h2_as_u32(__hmul2(u32_as_h2(prmt_b32(x[1][kk], x[1][2 + kk], 0x7632u)), odd));
+        f.x = h2_as_u32(__hmul2(u32_as_h2(prmt_b32(qx[n][0][kk], qx[n][0][2 + kk], 0x5410u)), f0));
+        f.y = h2_as_u32(__hmul2(u32_as_h2(prmt_b32(qx[n][1][kk], qx[n][1][2 + kk], 0x5410u)), f1));
+        f.z = h2_as_u32(__hmul2(u32_as_h2(prmt_b32(qx[n][0][kk], qx[n][0][2 + kk], 0x7632u)), g0));
+        f.w = h2_as_u32(__hmul2(u32_as_h2(prmt_b32(qx[n][1][kk], qx[n][1][2 + kk], 0x7632u)), g1));
         to[32 * kk] = f;
       }
     } else {
-      to[0] = make_uint4(x[0][0], x[1][0], x[0][1], x[1][1]);
+      to[0] = make_uint4(h2_as_u32(__hmul2(u32_as_h2(qx[n][0][0]), f0)), h2_as_u32(__hmul2(u32_as_h2(qx[n][1][0]), f1)),
+                         h2_as_u32(__hmul2(u32_as_h2(qx[n][0][1]), f0)), h2_as_u32(__hmul2(u32_as_h2(qx[n][1][1]), f1)));
     }
   }
   __syncthreads();
@@ -293,6 +341,11 @@ __global__ void __launch_bounds__(kWarps * 32, RowCfg<BITS, KIND, D, MT>::CTAS) 
 
   // ---- running state ----
   uint32_t power = 0;  // of each group, a byte (ScalePower)
+  // K's scales enter times a power of two as well, so that the largest s z seen comes
+  // to 2^12 .. 2^14 and both of its parts keep their bits (keys of 1e-4: the second
+  // part was gone); `unit` takes it back.  Its exponent field, 0: all zero so far.
+  uint32_t power_k = 0;
+  float lift_k = 1.f;
   // Group g's entry of four (registers: the index is a constant but for the rows of
   // two groups in a kernel for four).
   auto of_chunk = [&](const float (&x)[C::MAXNG], int chunk) {
@@ -322,14 +375,31 @@ __global__ void __launch_bounds__(kWarps * 32, RowCfg<BITS, KIND, D, MT>::CTAS) 
     // headers: a lane its key's, to [group][key]
     {
       const uint16_t* h = reinterpret_cast<const uint16_t*>(st + 2 * C::CODE_TILE) + lane * NG;
-      uint32_t allowed = power;
+      constexpr uint16_t half_range = BITS == 4 ? 0x4800u : 0x5800u;  // 8, 128
+      float sz[C::MAXNG];
+      uint32_t top_k = 0;
+      bool over = false;  // a scale, or K's scale times zero-point, beyond what its power allows
 #pragma unroll
       for (int g = 0; g < C::MAXNG; ++g) {
+        sz[g] = 0.f;
         if (g >= NG) break;
-        const uint32_t top = ScalePower::field(__reduce_max_sync(0xffffffffu, h[C::HDR_TILE + g] & 0x7FFFu));
-        if (top > (power >> (8 * g) & 255u)) allowed = (allowed & ~(255u << (8 * g))) | (top + 1) << (8 * g);
+        over |= ScalePower::field(h[C::HDR_TILE + g]) > (power >> (8 * g) & 255u);
+        if constexpr (KIND == 0) {
+          sz[g] = __half2float(__ushort_as_half(h[g])) * __half2float(__ushort_as_half(zeros ? h[C::HDR_TILE / 2 + g] : half_range));
+          const uint32_t bits = __float_as_uint(fabsf(sz[g]));
+          top_k = max(top_k, bits < 0x7F800000u ? bits : 0u);
+        }
       }
-      if (allowed != power) {  // the sums so far come down with their groups' powers
+      over |= top_k >> 23 > power_k;
+      if (__any_sync(0xffffffffu, over)) {
+        uint32_t allowed = power;
+#pragma unroll
+        for (int g = 0; g < C::MAXNG; ++g) {
+          if (g >= NG) break;
+          const uint32_t top = ScalePower::field(__reduce_max_sync(0xffffffffu, h[C::HDR_TILE + g] & 0x7FFFu));
+          if (top > (power >> (8 * g) & 255u)) allowed = (allowed & ~(255u << (8 * g))) | (top + 1) << (8 * g);
+        }
+        // the sums so far come down with their groups' powers
         float down[C::MAXNG];
 #pragma unroll
         for (int g = 0; g < C::MAXNG; ++g)
@@ -347,22 +417,30 @@ __global__ void __launch_bounds__(kWarps * 32, RowCfg<BITS, KIND, D, MT>::CTAS) 
             o[mt][n][0] *= f, o[mt][n][1] *= f, o[mt][n][2] *= f, o[mt][n][3] *= f;
           }
         }
+        if constexpr (KIND == 0) {
+          const uint32_t top = __reduce_max_sync(0xffffffffu, top_k) >> 23;  // at most 159
+          if (top > power_k) {
+            const float f = __uint_as_float((top + 1 - (power_k ? power_k : 140u) + 127u) << 23);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) unit[mt][0] *= f, unit[mt][1] *= f;
+            power_k = top + 1;
+            lift_k = __uint_as_float((267u - power_k) << 23);
+          }
+        }
       }
-      constexpr uint16_t half_range = BITS == 4 ? 0x4800u : 0x5800u;  // 8, 128
 #pragma unroll
       for (int g = 0; g < C::MAXNG; ++g) {
         if (g >= NG) break;
-        const float s = __half2float(__ushort_as_half(h[g]));
-        ksc[g * C::KROW + lane] = s * kSub;
+        ksc[g * C::KROW + lane] = __half2float(__ushort_as_half(h[g])) * (kSub * lift_k);
         vs[g * C::VROW + lane] =
             __half_as_ushort(__float2half_rn(__half2float(__ushort_as_half(h[C::HDR_TILE + g])) *
                                              ScalePower::factor(power >> (8 * g) & 255u)));
         if constexpr (KIND == 0) {
-          const float sz = s * __half2float(__ushort_as_half(zeros ? h[C::HDR_TILE / 2 + g] : half_range));
-          const __half hi = __float2half_rn(fminf(fmaxf(sz, -65504.f), 65504.f));
+          const float y = sz[g] * lift_k;
+          const __half hi = __float2half_rn(y);
           uint16_t* const to = kz + lane * C::ZROW + g;
           to[0] = to[2 * C::MAXNG] = __half_as_ushort(hi);
-          to[C::MAXNG] = __half_as_ushort(__float2half_rn(sz - __half2float(hi)));
+          to[C::MAXNG] = __half_as_ushort(__float2half_rn(y - __half2float(hi)));
           vz[g * C::VROW + lane] = zeros ? h[3 * C::HDR_TILE / 2 + g] : half_range;
         }
       }
@@ -469,8 +547,8 @@ __global__ void __launch_bounds__(kWarps * 32, RowCfg<BITS, KIND, D, MT>::CTAS) 
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         float top[2];
-        top[0] = fmaxf(fmaxf(s[mt][0][0], s[mt][0][1]), fmaxf(s[mt][1][0], s[mt][1][1])) * p.scale_log2;
-        top[1] = fmaxf(fmaxf(s[mt][0][2], s[mt][0][3]), fmaxf(s[mt][1][2], s[mt][1][3])) * p.scale_log2;
+        top[0] = fmaxf(fmaxf(s[mt][0][0], s[mt][0][1]), fmaxf(s[mt][1][0], s[mt][1][1])) * unit[mt][0];
+        top[1] = fmaxf(fmaxf(s[mt][0][2], s[mt][0][3]), fmaxf(s[mt][1][2], s[mt][1][3])) * unit[mt][1];
         if (__any_sync(0xffffffffu, top[0] > m_ref[mt][0] + kSlackRows || top[1] > m_ref[mt][1] + kSlackRows)) {
           float alpha[2];
 #pragma unroll
@@ -489,12 +567,11 @@ __global__ void __launch_bounds__(kWarps * 32, RowCfg<BITS, KIND, D, MT>::CTAS) 
         }
         const float ma = m_ref[mt][0] == -INFINITY ? 0.f : -m_ref[mt][0] + kLiftRows;
         const float mb = m_ref[mt][1] == -INFINITY ? 0.f : -m_ref[mt][1] + kLiftRows;
-        const float2 sl = make_float2(p.scale_log2, p.scale_log2);
         float2 sum[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          float2 a = tc::fma2(make_float2(s[mt][u][0], s[mt][u][1]), sl, make_float2(ma, ma));
-          float2 d = tc::fma2(make_float2(s[mt][u][2], s[mt][u][3]), sl, make_float2(mb, mb));
+          float2 a = tc::fma2(make_float2(s[mt][u][0], s[mt][u][1]), make_float2(unit[mt][0], unit[mt][0]), make_float2(ma, ma));
+          float2 d = tc::fma2(make_float2(s[mt][u][2], s[mt][u][3]), make_float2(unit[mt][1], unit[mt][1]), make_float2(mb, mb));
           a = make_float2(ex2(a.x), ex2(a.y));
           d = make_float2(ex2(d.x), ex2(d.y));
           pa[mt][2 * u] = pack_h2(a.x, a.y);

@@ -1,5 +1,6 @@
 """GPU tests of kvq_prefix_attn over few rows (codes in registers) on values that
-fp16 has few bits for: small V, and rows where one key has most of the weight."""
+fp16 has few bits for, or no room: small V, rows where one key has most of the
+weight, q and K far from one."""
 import numpy as np
 import pytest
 
@@ -140,3 +141,35 @@ def test_scales_that_grow_along_the_prefix(fmt):
     r = Rows(fmt, k, v, rng.standard_normal((3, 1, 4, D)).astype(np.float16))
     for splits in (1, 2):
         assert r.worst(D ** -0.5, splits) <= 1.0
+
+
+@pytest.mark.parametrize("size_q,size_k,shift", [(1e4, 1e-4, 0.0), (100.0, 1e-2, 0.0), (3000.0, 1.0, 1.0), (8000.0, 1.0, 0.0),
+                                                 (1e-3, 1e3, 0.0), (1e-5, 1e4, 0.0), (60000.0, 1e-5, 0.0)])
+@pytest.mark.parametrize("fmt", list(FEW))
+def test_scores_of_any_size(fmt, size_q, size_k, shift):
+    """q far from one, K as far or not at all: scores of a few units by the softmax
+    scale.  shift: channels of one sign, whose sum fp16 does not hold."""
+    rng = np.random.default_rng(9)
+    D, P = 128, 500
+    q = np.clip(size_q * (shift + rng.standard_normal((3, 1, 4, D)) * (0.2 if shift else 1.0)), -65504, 65504).astype(np.float16)
+    k = np.clip(size_k * rng.standard_normal((P, D)), -65504, 65504).astype(np.float16)
+    r = Rows(fmt, k, (0.5 + rng.standard_normal((P, D))).astype(np.float16), q)
+    scale = 2.0 / float(np.std(q.astype(np.float64)[0, 0] @ r.k.T))
+    for splits in (1, 2):
+        assert r.worst(scale, splits) <= 1.0
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("nan"), 65504.0, 1e-7])
+@pytest.mark.parametrize("fmt", ["int4", "int8"])
+def test_a_row_does_not_change_another(fmt, value):
+    """Rows of one tile whose q has an infinity, a NaN, fp16's largest or nearly
+    nothing: the others are to the bit what they are beside ordinary rows."""
+    r = _rows_of(fmt, 128, 1, 1.0, 1.0)
+    call = lambda: r.K.kvq_prefix_attn(r.prefix, r.tail, r.plan, r.dev_q, r.before, r.P, r.T, prefix_splits=2)  # noqa: E731
+    want = call()
+    r.dev_q[1, 0, 2, 5] = value
+    if value == 1e-7:
+        r.dev_q[1, 0, 2] = value
+    got = call()
+    same = (want == got).all(-1)
+    assert [bool(x) for x in same.flatten()] == [i != 6 for i in range(12)]
