@@ -737,10 +737,11 @@ KVQ_API size_t kvq_prefix_attn_workspace_size(const kvq_cache_desc* prefix_desc,
  *                    nearer the bounds, the better the choice of splits
  *   prefix_splits, tail_splits  0: library choice, else as num_splits of
  *                    kvq_decode_attn, for each of the two
- *   out              device fp16 like q; may not overlap it
+ *   out              device fp16 like q
  *   workspace        kvq_prefix_attn_workspace_size() bytes for the same sizes
  *                    and splits (may be NULL when that is 0); calls that can
  *                    overlap on the GPU need one each
+ * Neither out nor the workspace may overlap the other, q, the lengths or the plan.
  * (A row of q without a new token may be read, to no effect; its row of out is
  * not written.)
  * Axis-aware caches: a prefix's length is all that has been appended to it.

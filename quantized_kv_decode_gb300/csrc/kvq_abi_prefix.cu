@@ -91,8 +91,9 @@ int32_t prefix_splits(const ExtendPlan& plan, int64_t units, int64_t max_len, in
   return best;
 }
 
-kvq_status choose(const kvq_cache_desc* pd, const kvq_cache_desc* d, int32_t N, int32_t B, int32_t T, int32_t Hq,
-                  int32_t max_prefix, int32_t max_len, int32_t want_prefix, int32_t want_tail, PrefixChoice* c) {
+// The checks of a call's numbers, which need no device.
+kvq_status check_sizes(const kvq_cache_desc* pd, const kvq_cache_desc* d, int32_t N, int32_t B, int32_t T, int32_t Hq,
+                       int32_t max_prefix, int32_t max_len, int32_t want_prefix, int32_t want_tail, PrefixChoice* c) {
   kvq_status st = check_desc(d, &c->tg);
   if (st != KVQ_OK) return st;
   if (N < 0 || B < 0 || T < 0 || Hq <= 0 || max_prefix < 0 || max_len < 0 || want_prefix < 0 || want_tail < 0)
@@ -104,6 +105,13 @@ kvq_status choose(const kvq_cache_desc* pd, const kvq_cache_desc* d, int32_t N, 
   }
   if (N > KVQ_MAX_PREFIXES || B > KVQ_MAX_BATCH || d->num_kv_heads > 65535 || too_many_rows(B, T, Hq))
     return KVQ_ERR_UNSUPPORTED;
+  return KVQ_OK;
+}
+
+// Kernels, splits and workspace of a call whose numbers are right.
+kvq_status choose(const kvq_cache_desc* d, int32_t N, int32_t B, int32_t T, int32_t Hq, int32_t max_prefix,
+                  int32_t max_len, int32_t want_prefix, int32_t want_tail, PrefixChoice* c) {
+  kvq_status st = KVQ_OK;
   if (B == 0 || T == 0) return KVQ_OK;
   const int G = Hq / d->num_kv_heads;
   const int64_t D = d->head_dim, rows = (int64_t)B * T * Hq, each = (int64_t)T * G;
@@ -233,8 +241,10 @@ size_t kvq_prefix_attn_workspace_size(const kvq_cache_desc* prefix_desc, const k
                                       int32_t max_prefix_len, int32_t max_seq_len, int32_t prefix_splits,
                                       int32_t tail_splits) {
   PrefixChoice c;
-  if (choose(prefix_desc, desc, num_prefixes, batch, num_new, num_q_heads, max_prefix_len, max_seq_len, prefix_splits,
-             tail_splits, &c) != KVQ_OK)
+  if (check_sizes(prefix_desc, desc, num_prefixes, batch, num_new, num_q_heads, max_prefix_len, max_seq_len,
+                  prefix_splits, tail_splits, &c) != KVQ_OK ||
+      choose(desc, num_prefixes, batch, num_new, num_q_heads, max_prefix_len, max_seq_len, prefix_splits, tail_splits,
+             &c) != KVQ_OK)
     return 0;
   return c.prefix_bytes + c.tail_bytes;
 }
@@ -246,8 +256,8 @@ kvq_status kvq_prefix_attn(const kvq_cache_desc* prefix_desc, const kvq_cache* p
                            int32_t max_seq_len, int32_t prefix_splits, int32_t tail_splits, float softmax_scale,
                            uint16_t* out, void* workspace, size_t workspace_size, uint32_t* dev_status, void* stream) {
   PrefixChoice c;
-  kvq_status st = choose(prefix_desc, desc, num_prefixes, batch, num_new, num_q_heads, max_prefix_len, max_seq_len,
-                         prefix_splits, tail_splits, &c);
+  kvq_status st = check_sizes(prefix_desc, desc, num_prefixes, batch, num_new, num_q_heads, max_prefix_len,
+                              max_seq_len, prefix_splits, tail_splits, &c);
   if (st != KVQ_OK) return st;
   if (!(softmax_scale >= 0.f) || isinf(softmax_scale)) return KVQ_ERR_INVALID_ARG;
   if ((st = check_cache(desc, cache)) != KVQ_OK) return st;
@@ -258,10 +268,21 @@ kvq_status kvq_prefix_attn(const kvq_cache_desc* prefix_desc, const kvq_cache* p
     return KVQ_ERR_INVALID_ARG;
   if (plan_bytes < kvq_prefix_plan_size(batch, num_prefixes)) return KVQ_ERR_INVALID_ARG;
   const int64_t rows = (int64_t)batch * num_new * num_q_heads;
-  const size_t bytes = (size_t)rows * desc->head_dim * 2;
-  if (q == out || partly_over(q, out, bytes)) return KVQ_ERR_INVALID_ARG;
+  const size_t bytes = (size_t)rows * desc->head_dim * 2, each = (size_t)batch * 4;
+  Span spans[] = {{q, bytes, false},
+                  {seq_lens_before, each, false},
+                  {new_lens, each, false},
+                  {plan, kvq_prefix_plan_size(batch, num_prefixes), false},
+                  {out, bytes, true},
+                  {workspace, 0, true}};
+  if (!apart(spans)) return KVQ_ERR_INVALID_ARG;
+  if ((st = choose(desc, num_prefixes, batch, num_new, num_q_heads, max_prefix_len, max_seq_len, prefix_splits,
+                   tail_splits, &c)) != KVQ_OK)
+    return st;
   const size_t need = c.prefix_bytes + c.tail_bytes;
   if (need && (!workspace || workspace_size < need || !aligned(workspace))) return KVQ_ERR_WORKSPACE;
+  spans[5].bytes = need;
+  if (!apart(spans)) return KVQ_ERR_INVALID_ARG;
 
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int64_t D = desc->head_dim;

@@ -1,6 +1,6 @@
 """GPU tests of kvq_prefix_attn on lengths and counts that cannot be, one new
-token a sequence: whichever kernel takes the tails, the call flags them and
-leaves or zeroes the rows that kvq.h names."""
+token a sequence (whichever kernel takes the tails, the call flags them and
+leaves or zeroes the rows that kvq.h names), and of what it refuses."""
 import numpy as np
 import pytest
 
@@ -40,3 +40,35 @@ def test_counts_and_lengths_of_one_new_token(fmt, D, tail_splits):
             assert int(st.item()) == (K.KVQ_FLAG_SEQ_LEN if flagged else 0), what
             assert (o[b] == (7.0 if row == "left" else 0.0)).all(), what
             s.check(o, only=[x for x in range(s.B) if x != b])
+
+
+def test_a_workspace_over_another_array_is_refused():
+    """The workspace shares no byte with q, the lengths, the plan or out: refused
+    before anything is launched."""
+    import torch
+    s = _batch("int4", "int4", 64, 1, 2, 1, [50, 20], 6, none=False)
+    K = s.K
+    n = K.kvq_prefix_attn_workspace_size(s.prefix.desc, s.tail.desc, s.N, s.B, 1, 2, s.P, s.L)
+    size = s.q.size * 2
+    room = torch.full((n + 4096,), 7, dtype=torch.uint8, device="cuda")
+    ws = room[2048:2048 + n]
+    for at in (0, 2048 - size + 16, 2048, 2048 + n - 16):
+        if at % 16:
+            at -= at % 16
+        over = room[at:at + size]
+        for name in ("q", "out"):
+            part = over.view(torch.float16).view(s.q.shape)
+            args = dict(q=s.dev["q"], out=None)
+            args[name] = part
+            clash = at + size > 2048
+            try:
+                K.kvq_prefix_attn(s.prefix, s.tail, s.plan, args["q"], s.dev["before"], s.P, s.L, out=args["out"], workspace=ws)
+                assert not clash
+            except K.KVQError as e:
+                assert clash and e.status == K.KVQ_ERR_INVALID_ARG
+    lens = room[2048 + n - 32:2048 + n - 32 + 4 * s.B].view(torch.int32)
+    for kw in (dict(new_lens=lens), dict(before=lens)):
+        with pytest.raises(K.KVQError) as e:
+            K.kvq_prefix_attn(s.prefix, s.tail, s.plan, s.dev["q"], kw.get("before", s.dev["before"]), s.P, s.L,
+                              new_lens=kw.get("new_lens"), workspace=ws)
+        assert e.value.status == K.KVQ_ERR_INVALID_ARG

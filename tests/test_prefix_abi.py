@@ -179,3 +179,24 @@ def test_binding_checks(K):
 def test_structs_match_the_header(K):
     assert ctypes.sizeof(K.kvq_rope_axes_desc) == ctypes.sizeof(K.kvq_rope_desc) + 4 + 4 * 4 + 8 + 4
     assert ctypes.sizeof(K.kvq_rope_axes) == ctypes.sizeof(K.kvq_rope) + 4 + 128 + 4
+
+
+def test_prefix_attn_arrays_apart(K):
+    """out shares no byte with what the call reads (q, the lengths, the plan); what
+    it reads may be one array."""
+    lib = K.lib()
+    pc, c = _cache(K), _cache(K)
+    d = K.make_desc(4, 32, 2, 64, K.KVQ_DENSE, 64)
+    base = 0x70000000
+    q, lens, new, plan, out = [base + i * 0x10000 for i in range(5)]
+    n = 2 * 4 * 64 * 2  # bytes of q and out: 2 sequences, 4 heads of 64
+    words = int(lib.kvq_prefix_plan_size(2, 1))
+
+    def call(q=q, lens=lens, new=new, plan=plan, out=out):
+        return lib.kvq_prefix_attn(byref(d), byref(pc), 1, byref(d), byref(c), 2, 1, 4, q, lens, new, plan, 1 << 16, 64,
+                                   64, 1, 1, 0.0, out, None, 0, None, None)
+    for at in (q, q + n - 16, q - n + 16, lens, lens - n + 16, new, new - n + 16, plan, plan + words - 16, plan - n + 16):
+        assert call(out=at) == K.KVQ_ERR_INVALID_ARG, hex(at)
+    # (without a device, or a workspace, the next step refuses with another status)
+    for ok in (call(), call(out=q + n), call(out=plan - n), call(new=None), call(new=lens)):
+        assert ok in (K.KVQ_ERR_CUDA, K.KVQ_ERR_WORKSPACE)
