@@ -23,7 +23,10 @@ from .api import KVCache, _ptr
 
 
 _Tensor = torch.Tensor
-_device_now = torch._C._cuda_getDevice
+# the current device, and the handle of its current stream without an object for it
+# (1 us of a call of 10); a torch that lacks either has the public functions
+_device_now = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_handle = getattr(torch._C, "_cuda_getCurrentRawStream", lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _check(t, dtype, name, shape, device):
@@ -102,10 +105,6 @@ class _on:
     def __exit__(self, *exc):
         if self.guard is not None:
             self.guard.__exit__(*exc)
-
-
-# the current stream's handle without an object for it (1 us of a call of 10)
-_handle = torch._C._cuda_getCurrentRawStream
 
 
 def _same_cache_device(cache: KVCache, device):

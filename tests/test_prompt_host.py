@@ -80,3 +80,27 @@ def test_no_attention_instance_that_nothing_reaches():
     out = subprocess.run(["nm", "-C", obj], capture_output=True, text=True, check=True).stdout
     got = {(int(b), int(d)) for b, d in re.findall(r"extend_kernel<(\d+), (\d+)>", out)}
     assert got == {(2, 256), (16, 256)} | {(b, d) for b in (4, 8) for d in (64, 128, 256)}
+
+
+def test_the_package_needs_no_private_names_of_torch(K):
+    """Without torch's own fast ways to the current device and stream the package is
+    imported all the same, and takes the public functions."""
+    import subprocess
+    import sys
+    from tests.conftest import ROOT
+    code = """
+import torch
+for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+import quantized_kv_decode_gb300 as K
+from quantized_kv_decode_gb300 import prompt
+assert K.KVCache and K.make_rope(64).rotary_dim == 64
+torch.cuda.current_device = lambda: 3
+class Stream:
+    cuda_stream = 17
+torch.cuda.current_stream = lambda device: Stream if device == 3 else None
+assert prompt._handle(3) == 17 and callable(prompt._device_now)
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
