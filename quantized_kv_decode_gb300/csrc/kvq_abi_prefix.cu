@@ -48,7 +48,8 @@ struct PrefixChoice {
   ExtendPlan pre, tail;
   TailDecode decode;
   int32_t prefix_splits = 0, tail_splits = 0;
-  size_t prefix_bytes = 0, tail_bytes = 0;
+  size_t prefix_bytes = 0, tail_bytes = 0, word_bytes = 0;  // (a word: start_beside)
+  size_t workspace() const { return prefix_bytes + tail_bytes + word_bytes; }
 };
 
 // Splits of the prefix pass, and what the call then costs in ns.  A block takes
@@ -151,6 +152,8 @@ kvq_status choose(const kvq_cache_desc* d, int32_t N, int32_t B, int32_t T, int3
     if (c->prefix_splits <= 0) return KVQ_ERR_CUDA;
     if (prefix_tiles_bound(B, N, each, c->pre.tile_rows) * c->prefix_splits > INT32_MAX) return KVQ_ERR_UNSUPPORTED;
     c->prefix_bytes = partial_bytes(rows, D, c->prefix_splits);
+    // tails that start beside the pass: all but those of the decode kernels with splits
+    if (c->decode.one || !c->decode.takes) c->word_bytes = up256(sizeof(unsigned long long));
   }
   return KVQ_OK;
 }
@@ -246,7 +249,7 @@ size_t kvq_prefix_attn_workspace_size(const kvq_cache_desc* prefix_desc, const k
       choose(desc, num_prefixes, batch, num_new, num_q_heads, max_prefix_len, max_seq_len, prefix_splits, tail_splits,
              &c) != KVQ_OK)
     return 0;
-  return c.prefix_bytes + c.tail_bytes;
+  return c.workspace();
 }
 
 kvq_status kvq_prefix_attn(const kvq_cache_desc* prefix_desc, const kvq_cache* prefix_cache, int32_t num_prefixes,
@@ -279,7 +282,7 @@ kvq_status kvq_prefix_attn(const kvq_cache_desc* prefix_desc, const kvq_cache* p
   if ((st = choose(desc, num_prefixes, batch, num_new, num_q_heads, max_prefix_len, max_seq_len, prefix_splits,
                    tail_splits, &c)) != KVQ_OK)
     return st;
-  const size_t need = c.prefix_bytes + c.tail_bytes;
+  const size_t need = c.workspace();
   if (need && (!workspace || workspace_size < need || !aligned(workspace))) return KVQ_ERR_WORKSPACE;
   spans[5].bytes = need;
   if (!apart(spans)) return KVQ_ERR_INVALID_ARG;
@@ -292,7 +295,12 @@ kvq_status kvq_prefix_attn(const kvq_cache_desc* prefix_desc, const kvq_cache* p
   if (c.prefixes) carve_partials(workspace, rows, D, c.prefix_splits, &po, &pml);
   if (c.tail_bytes) carve_partials(reinterpret_cast<char*>(workspace) + c.prefix_bytes, rows, D, c.tail_splits, &to, &tml);
 
+  unsigned long long* const started =
+      c.word_bytes ? reinterpret_cast<unsigned long long*>(reinterpret_cast<char*>(workspace) + c.prefix_bytes + c.tail_bytes)
+                   : nullptr;
+
   ExtendParams p{};  // what both passes of extend attention share
+  p.started = started;
   p.partials = 1;
   p.q = reinterpret_cast<const __half*>(q);
   p.status = dev_status;
@@ -331,7 +339,7 @@ kvq_status kvq_prefix_attn(const kvq_cache_desc* prefix_desc, const kvq_cache* p
     j.chunk = chunk;
     j.limit = prefix_limit;
     j.lift = c.pre.lift;
-    j.early = c.prefixes;
+    j.started = started;
     e = tail_decode(desc, cache, c.tg, batch, num_q_heads, q, seq_lens_before, new_lens, max_seq_len, c.decode,
                     scale_log2, to, tml, workspace, workspace_size, dev_status, s, j, out);
     if (c.decode.one) return from_cuda(e);
@@ -342,7 +350,6 @@ kvq_status kvq_prefix_attn(const kvq_cache_desc* prefix_desc, const kvq_cache* p
              workspace, workspace_size, dev_status);
     x.ws_o = to;
     x.ws_ml = tml;
-    x.early = c.prefixes;
     x.lens_before = seq_lens_before;
     x.new_lens = new_lens;
     x.batch = batch;

@@ -360,7 +360,7 @@ __device__ __forceinline__ void join_and_write(const DecodeParams& p, int b, lon
     const int len = __ldg(x.len + n);
     splits = len > x.limit ? 0 : (max(len, 0) + x.chunk - 1) / x.chunk;
   }
-  if (x.early) pdl_wait();
+  wait_beside(x.started, blockIdx.x == 0 && threadIdx.x == 0);
   for (int h = sub * ROWS + lane / PER; h < p.G; h += wpu * ROWS) {
     const long long row = row0 + h;
     float M = -INFINITY, den = 0.f;
@@ -562,7 +562,8 @@ __global__ void __launch_bounds__(ONE ? kWarps * 32 : Cfg<BITS, D, NG, GP, KCH>:
   }
   // (ONE: behind the pass over the prefixes it starts at once and waits for that
   // pass's partials before it joins them)
-  if (!ONE || !p.join.early) pdl_wait();
+  if constexpr (ONE) start_beside(p.join.started);
+  else pdl_wait();
 
   const int b = ONE ? unit / geo.Hkv
                     : p.longest_first ? longest_first_seq(p, blockIdx.z, reinterpret_cast<int*>(smem))
@@ -573,7 +574,7 @@ __global__ void __launch_bounds__(ONE ? kWarps * 32 : Cfg<BITS, D, NG, GP, KCH>:
     for (long long n = (long long)blockIdx.x * (kWarps * 32) + threadIdx.x; n < p.join.N; n += (long long)gridDim.x * (kWarps * 32))
       if (__ldg(p.join.len + n) > p.join.limit && p.status) atomicOr(p.status, KVQ_FLAG_SEQ_LEN);
     if (b >= p.batch) {
-      if (p.join.early) pdl_wait();
+      wait_beside(p.join.started, blockIdx.x == 0 && threadIdx.x == 0);
       return;
     }
   }
@@ -584,7 +585,7 @@ __global__ void __launch_bounds__(ONE ? kWarps * 32 : Cfg<BITS, D, NG, GP, KCH>:
   }
   if constexpr (ONE) {
     if (new_rows_of(p.tail_new, b, 1) != 1) {  // no new token, or a count that cannot be: its row stays
-      if (p.join.early) pdl_wait();
+      wait_beside(p.join.started, blockIdx.x == 0 && threadIdx.x == 0);
       return;
     }
   }

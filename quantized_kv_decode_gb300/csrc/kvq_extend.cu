@@ -72,8 +72,12 @@ template <int BITS, int D, bool PRE>
 __device__ __forceinline__ void attend(const ExtendParams& p) {
   constexpr int KEYS = tile_keys(D), CH = D / 8, KB = D / 16, NT = KEYS / 8;
   if (!PRE) pdl_launch_dependents();
-  if (PRE || !p.early) pdl_wait();
-  if (PRE) pdl_launch_dependents();  // (a tail kernel starts without waiting for what came before)
+  if constexpr (PRE) {
+    pdl_wait();
+    say_started(p.started);
+  } else {
+    start_beside(p.started);
+  }
   extern __shared__ __align__(128) uint8_t smem[];
   const CacheGeom& c = p.v.geom;
   const int kvh = blockIdx.y;

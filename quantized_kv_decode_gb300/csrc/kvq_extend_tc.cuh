@@ -347,10 +347,10 @@ __device__ __forceinline__ bool nonfinite2(uint32_t w) {
 
 // ---- the kernel -------------------------------------------------------
 
-// (ExtendParams::early)
+// (ExtendParams::started)
 __device__ __forceinline__ void end_after_prefixes(const ExtendParams& p) {
-  if (p.early && threadIdx.x == 0 && blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1)
-    pdl_wait();
+  if (threadIdx.x == 0 && blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1)
+    wait_beside(p.started, true);
 }
 
 // PRE: over shared prefixes (rows of all members of a prefix, which see all of
@@ -368,8 +368,12 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
   const int warp = tc::uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int kvh = blockIdx.y;
   const int split = blockIdx.x % p.splits;
-  if (PRE || !p.early) pdl_wait();
-  if (PRE) pdl_launch_dependents();  // (a tail kernel starts without waiting for what came before)
+  if constexpr (PRE) {
+    pdl_wait();
+    say_started(p.started);
+  } else {
+    start_beside(p.started);
+  }
 
   int b, before, end, all_see;  // all_see: every row sees the positions up to here
   PrefixTile pt{};              // (PRE)
@@ -900,6 +904,7 @@ __global__ void __launch_bounds__((Cfg<BITS, KIND, D, NQ>::THREADS), 1)
     // ------------------------------------------------------ loaders
     bool ok = true;
     if constexpr (KIND != 2) {
+      if (p.started) tc::fence_async();  // (start_beside, for the bulk copies too)
       // A tile's rows come in runs of consecutive rows: one in a dense cache,
       // one per page (or part of one) in a paged one; lane r finds run r.
       const int which = warp - 1;

@@ -165,7 +165,7 @@ struct PrefixJoin {
   const int32_t* len; // tokens of each prefix
   int32_t N, splits, chunk, limit;  // longer prefixes than limit are left out
   float lift;
-  int32_t early;      // the kernel before is that pass, whose start already waited for what came before
+  unsigned long long* started;  // the kernel before is that pass, and says there when it has started (start_beside)
   int32_t wpu;        // warps that work on a (sequence, KV head): 1, 2 or 4
 };
 
@@ -323,6 +323,36 @@ __device__ __forceinline__ void pdl_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+
+// A kernel that works beside the one before it (the tails of sequences with shared
+// prefixes, beside the pass over the prefixes) reads what kernels before both wrote,
+// and must not wait for its neighbour.  The neighbour has waited for them: it says so
+// in a word of the call's workspace (a release), and what sees the word (an acquire)
+// sees what they wrote, through the neighbour's wait.  What does not see it waits as
+// any other kernel does.  The word is cleared at the end, so that no call finds
+// another's; a workspace comes with any bits but hardly these.
+constexpr unsigned long long kStarted = 0x6b76715f70726573ull;
+// By every thread of the neighbour, behind its pdl_wait: the word, then the next kernel
+// may start.
+__device__ __forceinline__ void say_started(unsigned long long* word) {
+  if (threadIdx.x != 0) return;
+  if (word && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
+    asm volatile("st.release.gpu.global.u64 [%0], %1;\n" ::"l"(word), "l"(kStarted) : "memory");
+  pdl_launch_dependents();
+}
+// By every thread, in the place of pdl_wait (without a word: pdl_wait).
+__device__ __forceinline__ void start_beside(const unsigned long long* word) {
+  unsigned long long x = 0;
+  if (word) asm volatile("ld.acquire.gpu.global.u64 %0, [%1];\n" : "=l"(x) : "l"(word) : "memory");
+  if (x != kStarted) pdl_wait();
+}
+// Before what the neighbour left is read, or at the end; `last`: one thread, which clears
+// the word.
+__device__ __forceinline__ void wait_beside(unsigned long long* word, bool last) {
+  if (!word) return;
+  pdl_wait();
+  if (last) *word = 0;
+}
 
 template <typename Params>
 cudaError_t launch_pdl(void (*kernel)(Params), dim3 grid, dim3 block, size_t smem,

@@ -156,10 +156,10 @@ struct ExtendParams {
   // are the plan's prefixes, and a row of the tile is a (member, new token, head)
   // triple of one of them; lens_before and out are not used.
   PrefixPlan plan;
-  // The kernel before is the pass over shared prefixes, whose start already waited
-  // for what came before: this one starts beside it, and its last block ends after
-  // it, so that what waits for this kernel waits for both.
-  int32_t early;
+  // The pass over shared prefixes says there that it has started; tails behind it
+  // start beside it (start_beside), and their last block ends after it, so that what
+  // waits for this kernel waits for both.  Null: each waits for the kernel before.
+  unsigned long long* started;
 };
 
 // Which kernel takes the call, the rows of a CTA's tile (query token x head

@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kWarps * 32, RowCfg<BITS, KIND, D, MT>::CTAS) 
     }
   }
   pdl_wait();
-  pdl_launch_dependents();  // (a tail kernel starts without waiting for what came before)
+  say_started(p.started);
 
   // ---- which rows, which keys ----
   const int kvh = blockIdx.y, split = blockIdx.x % p.splits;
