@@ -44,6 +44,7 @@ void carve_partials(void* at, int64_t rows, int64_t D, int64_t splits, float** o
 // extend attention, then the join.
 struct PrefixChoice {
   CacheGeom pg, tg;
+  int32_t max_prefix = 0, max_len = 0;  // the call's bounds, at most what the caches hold
   bool prefixes = false;  // there is a prefix pass
   ExtendPlan pre, tail;
   TailDecode decode;
@@ -106,13 +107,16 @@ kvq_status check_sizes(const kvq_cache_desc* pd, const kvq_cache_desc* d, int32_
   }
   if (N > KVQ_MAX_PREFIXES || B > KVQ_MAX_BATCH || d->num_kv_heads > 65535 || too_many_rows(B, T, Hq))
     return KVQ_ERR_UNSUPPORTED;
+  c->max_len = (int32_t)std::min<int64_t>(cache_capacity(c->tg), max_len);
+  if (N > 0) c->max_prefix = (int32_t)std::min<int64_t>(cache_capacity(c->pg), max_prefix);
   return KVQ_OK;
 }
 
 // Kernels, splits and workspace of a call whose numbers are right.
-kvq_status choose(const kvq_cache_desc* d, int32_t N, int32_t B, int32_t T, int32_t Hq, int32_t max_prefix,
-                  int32_t max_len, int32_t want_prefix, int32_t want_tail, PrefixChoice* c) {
+kvq_status choose(const kvq_cache_desc* d, int32_t N, int32_t B, int32_t T, int32_t Hq, int32_t want_prefix,
+                  int32_t want_tail, PrefixChoice* c) {
   kvq_status st = KVQ_OK;
+  const int32_t max_prefix = c->max_prefix, max_len = c->max_len;
   if (B == 0 || T == 0) return KVQ_OK;
   const int G = Hq / d->num_kv_heads;
   const int64_t D = d->head_dim, rows = (int64_t)B * T * Hq, each = (int64_t)T * G;
@@ -128,7 +132,7 @@ kvq_status choose(const kvq_cache_desc* d, int32_t N, int32_t B, int32_t T, int3
   }
   if (c->tail_splits <= 0) return KVQ_ERR_CUDA;
   c->tail_bytes = c->decode.one ? 0 : partial_bytes(rows, D, c->tail_splits);
-  c->prefixes = N > 0 && max_prefix > 0;
+  c->prefixes = max_prefix > 0;
   if (c->prefixes) {
     const int32_t used = std::min(N, B);
     const int64_t per_prefix = ceil_div(B * each, used);
@@ -246,8 +250,7 @@ size_t kvq_prefix_attn_workspace_size(const kvq_cache_desc* prefix_desc, const k
   PrefixChoice c;
   if (check_sizes(prefix_desc, desc, num_prefixes, batch, num_new, num_q_heads, max_prefix_len, max_seq_len,
                   prefix_splits, tail_splits, &c) != KVQ_OK ||
-      choose(desc, num_prefixes, batch, num_new, num_q_heads, max_prefix_len, max_seq_len, prefix_splits, tail_splits,
-             &c) != KVQ_OK)
+      choose(desc, num_prefixes, batch, num_new, num_q_heads, prefix_splits, tail_splits, &c) != KVQ_OK)
     return 0;
   return c.workspace();
 }
@@ -279,8 +282,7 @@ kvq_status kvq_prefix_attn(const kvq_cache_desc* prefix_desc, const kvq_cache* p
                   {out, bytes, true},
                   {workspace, 0, true}};
   if (!apart(spans)) return KVQ_ERR_INVALID_ARG;
-  if ((st = choose(desc, num_prefixes, batch, num_new, num_q_heads, max_prefix_len, max_seq_len, prefix_splits,
-                   tail_splits, &c)) != KVQ_OK)
+  if ((st = choose(desc, num_prefixes, batch, num_new, num_q_heads, prefix_splits, tail_splits, &c)) != KVQ_OK)
     return st;
   const size_t need = c.workspace();
   if (need && (!workspace || workspace_size < need || !aligned(workspace))) return KVQ_ERR_WORKSPACE;
@@ -321,13 +323,13 @@ kvq_status kvq_prefix_attn(const kvq_cache_desc* prefix_desc, const kvq_cache* p
     x.ws_ml = pml;
     x.batch = num_prefixes;
     x.splits = c.prefix_splits;
-    x.chunk = split_chunk(max_prefix_len, c.prefix_splits);
-    x.len_limit = prefix_limit = (int32_t)std::min<int64_t>(cache_capacity(c.pg), max_prefix_len);
+    x.chunk = split_chunk(c.max_prefix, c.prefix_splits);
+    x.len_limit = prefix_limit = c.max_prefix;
     x.new_lens = new_lens;
     x.plan = pl;
     if ((e = launch_extend_prefix(x, c.pre, s)) != cudaSuccess) return from_cuda(e);
   }
-  const int32_t splits = std::max(c.prefix_splits, 1), chunk = split_chunk(max_prefix_len, splits);  // of the prefixes
+  const int32_t splits = std::max(c.prefix_splits, 1), chunk = split_chunk(c.max_prefix, splits);  // of the prefixes
   if (c.decode.takes) {
     PrefixJoin j{};
     j.o = po;
@@ -340,7 +342,7 @@ kvq_status kvq_prefix_attn(const kvq_cache_desc* prefix_desc, const kvq_cache* p
     j.limit = prefix_limit;
     j.lift = c.pre.lift;
     j.started = started;
-    e = tail_decode(desc, cache, c.tg, batch, num_q_heads, q, seq_lens_before, new_lens, max_seq_len, c.decode,
+    e = tail_decode(desc, cache, c.tg, batch, num_q_heads, q, seq_lens_before, new_lens, c.max_len, c.decode,
                     scale_log2, to, tml, workspace, workspace_size, dev_status, s, j, out);
     if (c.decode.one) return from_cuda(e);
   } else {
@@ -354,8 +356,8 @@ kvq_status kvq_prefix_attn(const kvq_cache_desc* prefix_desc, const kvq_cache* p
     x.new_lens = new_lens;
     x.batch = batch;
     x.splits = c.tail_splits;
-    x.chunk = split_chunk(max_seq_len, c.tail_splits);
-    x.len_limit = (int32_t)std::min<int64_t>(cache_capacity(c.tg), max_seq_len);
+    x.chunk = split_chunk(c.max_len, c.tail_splits);
+    x.len_limit = c.max_len;
     e = launch_extend_partials(x, c.tail, s);
   }
   if (e != cudaSuccess) return from_cuda(e);
@@ -366,7 +368,7 @@ kvq_status kvq_prefix_attn(const kvq_cache_desc* prefix_desc, const kvq_cache* p
            workspace, workspace_size, dev_status);
   j.plan = pl;
   j.part[0] = {po, pml, splits, chunk, c.pre.lift};
-  j.part[1] = {to, tml, c.tail_splits, split_chunk(max_seq_len, c.tail_splits), c.decode.takes ? 0.f : c.tail.lift};
+  j.part[1] = {to, tml, c.tail_splits, split_chunk(c.max_len, c.tail_splits), c.decode.takes ? 0.f : c.tail.lift};
   j.out = reinterpret_cast<__half*>(out);
   j.tail_before = seq_lens_before;
   j.new_lens = new_lens;
@@ -374,7 +376,7 @@ kvq_status kvq_prefix_attn(const kvq_cache_desc* prefix_desc, const kvq_cache* p
   j.Hq = num_q_heads;
   j.D = desc->head_dim;
   j.prefix_limit = prefix_limit;
-  j.tail_limit = (int32_t)std::min<int64_t>(cache_capacity(c.tg), max_seq_len);
+  j.tail_limit = c.max_len;
   j.status = dev_status;
   return from_cuda(launch_prefix_join(j, s));
 }

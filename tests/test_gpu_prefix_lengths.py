@@ -72,3 +72,23 @@ def test_a_workspace_over_another_array_is_refused():
             K.kvq_prefix_attn(s.prefix, s.tail, s.plan, s.dev["q"], kw.get("before", s.dev["before"]), s.P, s.L,
                               new_lens=kw.get("new_lens"), workspace=ws)
         assert e.value.status == K.KVQ_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("splits", [0, 1, 3])
+@pytest.mark.parametrize("fmt,T", [("int4", 1), ("fp16", 1), ("int8", 3), ("kch4", 2)])
+def test_bounds_beyond_the_caches(fmt, T, splits):
+    """Bounds of any size, for a program that knows none: what the caches hold is bound
+    enough."""
+    import torch
+    s = _batch(fmt, fmt, 128, 1, 2, T, [150, 40], 5)
+    for bound in (2 ** 31 - 1, 2 ** 31 - 128, 2 ** 30):
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = s.K.kvq_prefix_attn(s.prefix, s.tail, s.plan, s.dev["q"], s.dev["before"], bound, bound,
+                                  new_lens=s.dev["new"], prefix_splits=splits, tail_splits=splits, dev_status=st)
+        s.check(out.cpu().numpy())
+        assert int(st.item()) == 0
+    size = s.K.kvq_prefix_attn_workspace_size
+    sizes = (s.N, s.B, T, 2)
+    most = [int(c.desc.capacity) + int(c.desc.sink_tokens) for c in (s.prefix, s.tail)]
+    assert size(s.prefix.desc, s.tail.desc, *sizes, bound, bound, splits, splits) == \
+        size(s.prefix.desc, s.tail.desc, *sizes, *most, splits, splits)
