@@ -355,6 +355,7 @@ kvq_status tail_decode_plan(const kvq_cache_desc* desc, const CacheGeom& geom, i
   *t = TailDecode{};
   if (G > 8 || batch > KVQ_MAX_BATCH || geom.kch) return KVQ_OK;
   while (t->gp < G) t->gp <<= 1;
+  bool has_one = false;  // the tail kernel is built for the format
   if (desc->bits == 16) {
     t->takes = desc->head_dim == 64 || desc->head_dim == 128;
   } else if (fast_format(desc, G)) {
@@ -363,6 +364,10 @@ kvq_status tail_decode_plan(const kvq_cache_desc* desc, const CacheGeom& geom, i
     probe.G = G;
     const cudaError_t e = launch_decode_fast(probe, desc->bits, t->gp, nullptr, &t->takes, &t->occ);
     if (t->takes && e != cudaSuccess) return from_cuda(e);
+    int occ = 0;
+    const cudaError_t e_one = t->takes ? launch_decode_one(probe, t->gp, nullptr, &has_one, &occ) : cudaSuccess;
+    if (has_one && e_one != cudaSuccess) return from_cuda(e_one);
+    has_one = has_one && requested == 0;
   }
   if (!t->takes) return KVQ_OK;
   Plan plan;
@@ -371,13 +376,12 @@ kvq_status tail_decode_plan(const kvq_cache_desc* desc, const CacheGeom& geom, i
   // for any batch: 4 sequences, 8 KV heads, INT4, tails of 64, 512, 2048 tokens
   // behind 1024 shared ones: 10.9, 10.9, 20.3 us against 17.3, 18.7, 21.3 with
   // splits, partials and the join; 256 sequences 32, 56, 111 against 60, 81, 135.
-  const bool shorts = desc->bits != 16 && requested == 0 && max_len <= 2048;
-  if (!shorts) {
+  if (!has_one || max_len > 2048) {
     const kvq_status st = make_plan(desc, geom, batch, num_q_heads, max_len, requested, &plan);
     if (st != KVQ_OK) return st;
   }
   t->splits = plan.splits;
-  t->one = desc->bits != 16 && requested == 0 && plan.splits == 1;
+  t->one = has_one && plan.splits == 1;
   // Its warps a (sequence, KV head): as many as have room at once (8 an SM), more
   // where contexts are long enough to be worth a second turn.  256 sequences of 2
   // KV heads (head_dim 64, INT8), 1, 2, 4 warps: tails of 256 tokens 16.6, 21.0,

@@ -178,3 +178,31 @@ def test_values_at_the_ends_of_fp16(fmt):
         off = np.abs(out[b] - want)
         assert np.isfinite(out[b]).all()
         assert (off <= mass * rel + np.abs(want) * 2.0 ** -11 + 1.0).all(), (off / mass).max()
+
+
+@pytest.mark.parametrize("bits,kw", [(2, {}), (4, {}), (8, {}), (2, dict(symmetric=True)), (4, dict(symmetric=True)),
+                                     (8, dict(symmetric=True)), (4, dict(nf4=True)), (16, {})])
+def test_one_new_token_in_every_format(bits, kw):
+    """Group sizes, head sizes and heads per KV head of every width: whichever kernel
+    the tails come to, one that is built for them takes the call, and without prefixes
+    the result is what kvq_decode_attn gives."""
+    import torch
+    import quantized_kv_decode_gb300 as K
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    B, L = 3, 90
+    plan = K.kvq_prefix_plan(i32([-1] * B), i32([]))
+    gen = torch.Generator(device="cuda").manual_seed(bits)
+    rand = lambda *s: torch.randn(*s, generator=gen, dtype=torch.float16, device="cuda")  # noqa: E731
+    for D in (64, 128, 256):
+        for g in (8, 16, 32, 64, 128) if bits != 16 else (0,):
+            if g > D:
+                continue
+            cache = K.KVCache.allocate(K.make_desc(bits, g, 2, D, K.KVQ_DENSE, 96, **kw), B, "cuda")
+            K.kvq_append(cache, rand(B, L, 2, D), rand(B, L, 2, D), i32([0] * B))
+            for G in (1, 2, 3, 4, 8, 9):
+                q = rand(B, 1, 2 * G, D)
+                want = K.kvq_decode_attn(cache, q[:, 0].contiguous(), i32([L, 1, 33]), L).float()
+                for splits in (0, 2):
+                    got = K.kvq_prefix_attn(None, cache, plan, q, i32([L - 1, 0, 32]), 0, L, tail_splits=splits)
+                    # two sums in different orders: each 2^-9 (weights and result to 11 bits) of up to 4
+                    assert (got[:, 0].float() - want).abs().max() <= 2 * 2.0 ** -9 * 4, (D, g, G, splits)
