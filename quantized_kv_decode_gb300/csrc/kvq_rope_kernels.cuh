@@ -441,11 +441,13 @@ cudaError_t launch_warp(const Params& p, cudaStream_t stream) {
   }
   long long slices = 1;
   while (slices < passes && total * slices < 1216) slices *= 2;
-  // An append's tokens take about as much beside the turns (the quantizer), and
-  // padded batches hold fewer tokens than they have room for: two warps a token up
-  // to 12288 (INT8, 2 x 4095 tokens all live 76.9 us with one, 78.4 with two; 1684
-  // of them live 40.3 and 24.9, 4 x 2000 with 4380 live 52.1 and 47.7).
-  if (BITS && slices == 1 && passes > 1 && total <= 12288) slices = 2;
+  // An append's tokens take about as much beside the turns (the quantizer): two warps
+  // a token where one leaves the SMs half empty (INT8, all of 1300, 2000 tokens 30.6,
+  // 27.1 us with one, 21.3, 21.9 with two; 4096, 8190, 12288 39.7, 74.1, 107.3 and
+  // 41.3, 76.4, 112.3), and up to 12288 for padded batches, which hold fewer tokens
+  // than they have room for (a fifth of 4096, 8190, 12288: 35.5, 38.1, 38.8 and 20.4,
+  // 23.3, 32.5; half of them 34.2, 40.4, 63.9 and 22.1, 41.8, 61.2).
+  if (BITS && slices == 1 && passes > 1 && total <= (p.r.new_lens ? 12288 : 2432)) slices = 2;
   const long long warps = total * slices;
   const dim3 grid((unsigned)((warps + kWarps - 1) / kWarps));
   return inter ? launch2(rope_warp_kernel<BITS, KIND, true, Params>, grid, kWarps * 32, 0, stream, p, (int)slices)
