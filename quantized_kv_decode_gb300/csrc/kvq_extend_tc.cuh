@@ -349,7 +349,7 @@ __device__ __forceinline__ bool nonfinite2(uint32_t w) {
 
 // (ExtendParams::started)
 __device__ __forceinline__ void end_after_prefixes(const ExtendParams& p) {
-  if (threadIdx.x == 0 && blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1)
+  if (p.started && threadIdx.x == 0 && blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1)
     wait_beside(p.started, true);
 }
 

@@ -342,9 +342,12 @@ __device__ __forceinline__ void say_started(unsigned long long* word) {
 }
 // By every thread, in the place of pdl_wait (without a word: pdl_wait).
 __device__ __forceinline__ void start_beside(const unsigned long long* word) {
-  unsigned long long x = 0;
-  if (word) asm volatile("ld.acquire.gpu.global.u64 %0, [%1];\n" : "=l"(x) : "l"(word) : "memory");
-  if (x != kStarted) pdl_wait();
+  if (word) {
+    unsigned long long x;
+    asm volatile("ld.acquire.gpu.global.u64 %0, [%1];\n" : "=l"(x) : "l"(word) : "memory");
+    if (x == kStarted) return;
+  }
+  pdl_wait();
 }
 // Before what the neighbour left is read, or at the end; `last`: one thread, which clears
 // the word.
