@@ -251,7 +251,9 @@ __global__ void __launch_bounds__(kWarps * 32, RowCfg<BITS, KIND, D, MT>::CTAS) 
   for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
     for (int hh = 0; hh < 2; ++hh) {
-      unit[mt][hh] = p.scale_log2;
+      // (2^-60: scores reach 2^41, so that below it all weights are alike; with the powers
+      // `unit` is then 2^-115 at least, and not 0 times a masked key's infinity)
+      unit[mt][hh] = fmaxf(p.scale_log2, 0x1p-60f);
       lift[mt][hh] = lift_odd[mt][hh] = 0x3C003C00u;  // 1
       if constexpr (KIND == 0) {
         uint32_t top = 0;
@@ -420,10 +422,11 @@ __global__ void __launch_bounds__(kWarps * 32, RowCfg<BITS, KIND, D, MT>::CTAS) 
         if constexpr (KIND == 0) {
           const uint32_t top = __reduce_max_sync(0xffffffffu, top_k) >> 23;  // at most 159
           if (top > power_k) {
-            const float f = __uint_as_float((top + 1 - (power_k ? power_k : 140u) + 127u) << 23);
+            const uint32_t next = max(top + 1u, 100u);  // (of less than 2^-27 a few bits go)
+            const float f = __uint_as_float((next - (power_k ? power_k : 140u) + 127u) << 23);
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) unit[mt][0] *= f, unit[mt][1] *= f;
-            power_k = top + 1;
+            power_k = next;
             lift_k = __uint_as_float((267u - power_k) << 23);
           }
         }

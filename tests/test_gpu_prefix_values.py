@@ -173,3 +173,14 @@ def test_a_row_does_not_change_another(fmt, value):
     got = call()
     same = (want == got).all(-1)
     assert [bool(x) for x in same.flatten()] == [i != 6 for i in range(12)]
+
+
+@pytest.mark.parametrize("scale", [1e-12, 1e-20, 1e-37])
+@pytest.mark.parametrize("size", [1.0, 1e-6])
+@pytest.mark.parametrize("fmt", ["int4", "int8", "nf4"])
+def test_a_softmax_scale_of_nearly_nothing(fmt, size, scale):
+    """All weights alike, and keys that do not count (the last tile is not full)
+    count for nothing."""
+    rng = np.random.default_rng(4)
+    x = [(s * rng.standard_normal(n)).astype(np.float16) for s, n in ((size, (333, 128)), (1.0, (333, 128)), (size, (2, 1, 4, 128)))]
+    assert Rows(fmt, *x).worst(scale, 1) <= 1.0
