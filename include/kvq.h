@@ -733,8 +733,13 @@ KVQ_API size_t kvq_prefix_attn_workspace_size(const kvq_cache_desc* prefix_desc,
  *   new_lens         device int32 [batch] or NULL, as above
  *   plan             of kvq_prefix_plan, for this batch and num_prefixes
  *   max_prefix_len   host upper bound on the prefixes' lengths
- *   max_seq_len      host upper bound on seq_lens_before[b] + new_lens[b]; the
- *                    nearer the bounds, the better the choice of splits
+ *   max_seq_len      host upper bound on seq_lens_before[b] + new_lens[b]
+ * Kernels and splits are chosen by the host from these numbers, as if the batch
+ * were shared out evenly over min(num_prefixes, batch) prefixes of
+ * max_prefix_len tokens, with tails of max_seq_len: the nearer the truth, the
+ * better the choice, and slots that kvq_prefix_find left empty are far from it
+ * (give it few max_prefixes, or read its num_prefixes where a search serves
+ * many steps).  What the caches hold is bound enough for any length.
  *   prefix_splits, tail_splits  0: library choice, else as num_splits of
  *                    kvq_decode_attn, for each of the two
  *   out              device fp16 like q
@@ -745,6 +750,9 @@ KVQ_API size_t kvq_prefix_attn_workspace_size(const kvq_cache_desc* prefix_desc,
  * (A row of q without a new token may be read, to no effect; its row of out is
  * not written.)
  * Axis-aware caches: a prefix's length is all that has been appended to it.
+ * (Where sharing does not pay: axis-aware caches with one new token a sequence,
+ * which kvq_decode_attn reads faster, and new tokens by the hundred over codes,
+ * which are bound by their products.)
  * Precision: over the prefix as in kvq_extend_attn; INT4, INT8 and NF4 caches
  * may, where rows are few, take codes, scales and zero-points apart: a weight
  * times V's scale is then rounded to fp16 once more (11 bits, down to 2^-25 of

@@ -57,10 +57,12 @@ struct PrefixChoice {
 // kFixed keys' time beside its own; blocks run in whole turns over the device;
 // the partials are written and read at 6800 bytes a ns.  The tail kernel
 // (tail_warps of them, eight an SM, with tail_keys each) runs beside the pass
-// where that leaves room, and behind it where not.  Fitted to sweeps of 8 to 256
-// rows over prefixes of 512 to 16384 tokens (head_dim 64 and 128, INT4, INT8; some
-// of them at the kernel for few rows): the choice is within 5 % of the best kernel
-// in most of them, 15 % at worst.
+// where that leaves room, and behind it where not.  The constants fit head_dim 128
+// best.  Of 384 cases (8 to 256 rows over one prefix of 512 to 16384 tokens, tails of
+// 64, 8 and 32 KV heads, head_dim 64 and 128; INT4, INT8, NF4, fp16) the choice is
+// within 5 % of the best kernel and splits in 78 %, within 15 % in 96 %, and 29 % off
+// at worst (NF4 at head_dim 64).  Members are taken to be shared out evenly over the
+// prefixes that there is room for: the host does not know better.
 int32_t prefix_splits(const ExtendPlan& plan, int64_t units, int64_t max_len, int64_t rows, int64_t D, int requested,
                       int64_t tail_warps, int64_t tail_keys, double* cost) {
   static const double kNs[5] = {40, 16, 20, 25, 30};  // a key, by plan.kind

@@ -15,20 +15,22 @@
 //                V's codes with the keys in pairs (ldmatrix.trans); sum p s z of
 //                each group by one more product against its zero-points, taken
 //                off at the end
+// q, K's scales and V's scales enter times powers of two that keep them where fp16
+// has its bits, whatever their size; they are taken back in fp32.
 // A warp has a pipeline of 32-key tiles to itself and its own running maximum
 // and sum per row; the four of a block are joined at the end, and the block
 // leaves a partial.
 //
 // What bounds it: latency, of unpacking, products and softmax in turn with two or
-// three warps a scheduler (32 heads x 32 rows over 4096 keys, INT4: 43 % of the
+// three warps a scheduler (32 heads x 32 rows over 4096 keys, INT4: 46 % of the
 // issue slots, 18 % of the tensor pipe, 0.7 TB/s; 23 us by itself, cold).  Against
 // the kernel of kvq_extend_tc.cuh, the whole call with tails of 64 keys, 8 KV heads
-// of 128 over INT4: 8 rows over 512, 4096, 16384 keys 8.0, 12.7, 20.5 us (12.7,
-// 16.5, 31.0 there), 32 rows 9.4, 16.6, 26.9 (13.5, 20.5, 33.5), 64 rows 10.9, 20.4,
-// 37.7 (13.6, 22.0, 34.7).  Tiles of 16 rows against tiles of 32: 32 rows of 8 heads
-// over 512 keys 9.4 against 11.1 us (INT8: 10.3, 14.0), of 32 heads over 16384 72.9
-// against 67.4.  Sixteen keys are taken at a time: 32 held more registers than there
-// are (108 spilled accesses a tile).
+// of 128 over INT4, each with its best splits: 8 rows over 512, 4096, 16384 keys 8.2,
+// 11.5, 20.7 us (12.1, 15.9, 25.3 there), 32 rows 9.7, 16.0, 27.2 (12.7, 17.7, 28.6),
+// 64 rows 11.3, 19.1, 37.1 (12.9, 17.9, 29.4).  Tiles of 16 rows against tiles of 32:
+// 32 rows of 8 heads over 512 keys 9.7 against 12.1 us (INT8: 9.9, 14.8), of 32 heads
+// over 16384 78.6 against 69.3.  Sixteen keys are taken at a time: 32 held more
+// registers than there are (108 spilled accesses a tile).
 #pragma once
 
 #include "kvq_decode_fast.cuh"
@@ -93,9 +95,11 @@ constexpr float kLiftRows = 7.f;
 // comes to 2^4 .. 2^6.  A product is then at most 2^(2 + 7 + 6), and that of the
 // reference with the largest scale is 2^11 at least: the bits of smaller ones last
 // to 2^-25 of it (without the power, INT8 groups at 0.02 lost theirs from 2^-8 of the
-// row's largest on, 1.8e-2 of the result where one heavy key's V was small).  A
-// group's power, as the fp16 exponent that its scales stay within: it only rises,
-// and the group's sums come down with it.
+// row's largest on: 14 times the bound where one heavy key's V was small).  A group's
+// power, as the fp16 exponent that its scales stay within: it only rises, and the
+// group's sums come down with it.  All the powers together cost 2 % (32 heads over
+// 4096 keys, the whole call 36.5 -> 37.1 us; 37.8 with the maxima worked out in each
+// tile instead of a vote).
 struct ScalePower {
   // the exponent of a scale, and the one to allow for it: a binade more
   __device__ static __forceinline__ uint32_t field(uint32_t bits) { return (bits & 0x7FFFu) >> 10; }
